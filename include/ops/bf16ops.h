@@ -1,0 +1,154 @@
+/*
+ * bf16ops.h -- C ABI of libbf16ops: the operators on either side of the weight sync.
+ *
+ * libbf16delta (bf16delta.h) moves a trainer's new BF16 weights to the rollout workers.  This
+ * library holds what makes those weights and what answers with them:
+ *
+ *   AdamW over many tensors at once (bo_adamw_*): the optimizer step whose result the compress
+ *   encodes, with first and second moments in 32 or in 8 bits, an FP32 master copy or BF16
+ *   weights alone, the global gradient norm, and clipping by it.
+ *
+ *   Low-rank adapters of many requests (bo_adapter_*): forward and backward beside a projection
+ *   that all requests share.  The factors are read where they lie, so a delta applied to them
+ *   (bd_decompress) takes effect with the next call.
+ *
+ * Conventions are those of bf16delta.h: "d_" pointers are device memory and "h_" pointers host
+ * memory, all owned by the caller; nothing is allocated; calls are asynchronous on `stream` and
+ * never wait for the GPU; the return value (a bd_status) reports argument and launch errors
+ * only, and nothing has been enqueued when it is BD_ERR_INVALID_ARG.  Every call may be captured
+ * in a CUDA graph.  Handles (bo_adamw, bo_adapter_set) are plain structs in host memory: the
+ * caller owns them and may copy or drop them; their fields are the library's.
+ */
+#ifndef BF16OPS_H
+#define BF16OPS_H
+
+#include <stdint.h>
+
+#include "bf16delta.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Device status beside those of bd_status: the step was skipped because the gradient norm was
+ * not finite; weights, master, moments and the step count are as before the call. */
+#define BO_SKIPPED_NONFINITE 16
+
+/* ------------------------------------------------------------------------------- AdamW
+ *
+ * For every element, with t the number of this step (1 for the first):
+ *   c = min(1, max_norm / (norm + 1e-6)) when clipping, else 1;   g' = c g
+ *   m = beta1 m + (1 - beta1) g'          v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr wd) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * computed in FP32 (the quotient is 0 where m is 0, whatever eps).  norm = sqrt(sum of g^2 over all tensors), summed in a fixed order.
+ *
+ * State arenas.  The elements of item i take the blocks of 256 from first_block on (the last
+ * one padded); m, v and master of all items lie in one arena each, indexed by
+ * 256 * block + element.  Padding is never read into a result and stays as it is (8-bit codes
+ * of padding are written as 0).
+ *
+ * 8-bit moments: per block an FP32 scale (sm = max |m|, sv = max v) and codes
+ *   m: int8 c, value sign(c) (c/127)^2 sm, c = rint(127 sqrt(|m| / sm)) with m's sign;
+ *   v: uint8 c, value (c/255)^4 sv; of the two codes whose values enclose v the upper one with
+ *      the probability (v - lower) / (upper - lower), and never 0 for v > 0.
+ * The codes are spaced so that small values keep relative precision.  v is rounded
+ * stochastically because beta2 moves it by less than half a code step: rounded to nearest it
+ * would stay where it is.  A block that holds a value that is not finite gets a NaN scale and
+ * reads as NaN throughout (pass max_norm, if only INFINITY, to skip such steps).
+ *
+ * Random bits: R_j = mix64(mix64(seed ^ t G) + (j + 1) G) with SplitMix64's mix64 and G
+ * (bf16delta.h) and j = e >> 1 for arena element e, whose 32 bits are R_j >> 32 * (e & 1); the
+ * upper 16 round v's code, the lower 16 a BF16 weight.  A step is a function of its inputs,
+ * the seed and t. */
+
+typedef enum bo_weight_kind {
+  BO_WEIGHT_MASTER = 0, /* FP32 master in the arena; d_out gets its BF16 rounding */
+  BO_WEIGHT_BF16 = 1,   /* BF16 weights alone: d_weight is read, d_out written */
+  BO_WEIGHT_FP32 = 2    /* FP32 weights: d_weight is read, d_out written */
+} bo_weight_kind;
+
+typedef enum bo_dtype { BO_BF16 = 0, BO_FP32 = 1 } bo_dtype;
+
+#define BO_BLOCK_ELEMS 256u
+#define BO_ADAMW_STOCHASTIC 1u /* flag: BF16 weights alone are rounded stochastically */
+
+/* One tensor of a step.  Pointers 16-byte aligned. */
+typedef struct bo_adamw_item {
+  const void* d_weight;  /* weights before the step (not read, may be NULL, with a master) */
+  void* d_out;           /* weights after the step; == d_weight for a step in place */
+  const void* d_grad;    /* gradients */
+  uint64_t n;            /* elements */
+  uint64_t first_block;  /* first block of 256 in the arenas */
+  float weight_decay;
+  uint32_t reserved;     /* 0 */
+} bo_adamw_item;
+
+/* The arenas (256-byte aligned), of `blocks` blocks each. */
+typedef struct bo_adamw_state {
+  void* d_m;            /* float, or int8 codes */
+  void* d_v;            /* float, or uint8 codes */
+  float* d_m_scale;     /* 8 bits only: one per block */
+  float* d_v_scale;
+  float* d_master;      /* BO_WEIGHT_MASTER only */
+  uint64_t blocks;
+} bo_adamw_state;
+
+/* Results of a step on the device. */
+typedef struct bo_adamw_control {
+  int64_t step;         /* steps taken */
+  float norm;           /* gradient norm of the last step (when max_norm was given) */
+  float coef;           /* its clipping factor */
+  int32_t status;       /* BD_OK or BO_SKIPPED_NONFINITE */
+  uint32_t ticket[3];   /* the library's */
+} bo_adamw_control;
+
+typedef struct bo_adamw {
+  bo_adamw_state state;
+  bo_adamw_control* d_control;
+  void* d_chunks;
+  double* d_partials;
+  uint64_t chunks;
+  uint32_t weight_kind, grad_dtype, state_bits, flags;
+} bo_adamw;
+
+/* Arguments of one step. */
+typedef struct bo_adamw_step_args {
+  float lr;
+  const float* d_lr;    /* when not NULL, the rate is read from here instead */
+  double beta1, beta2;
+  float eps;
+  float max_norm;       /* > 0: clip, and skip a step whose norm is not finite; 0: neither */
+  uint64_t seed;
+} bo_adamw_step_args;
+
+/* Bytes of device memory (256-byte aligned) that a plan over k tensors takes; 0 on bad
+ * arguments. */
+BD_API uint64_t bo_adamw_plan_size(const bo_adamw_item* h_items, uint32_t k);
+
+/* Lays the tensor table out in d_plan and fills *h_out.  h_items is read during the call only.
+ * step: steps taken so far.  The tensors, the arenas and d_plan must stay where they are while
+ * the handle is used.  Arenas of different items may not overlap. */
+BD_API int bo_adamw_plan(const bo_adamw_item* h_items, uint32_t k, const bo_adamw_state* state,
+                         uint32_t weight_kind, uint32_t grad_dtype, uint32_t state_bits,
+                         uint32_t flags, int64_t step, void* d_plan, uint64_t plan_bytes,
+                         bo_adamw* h_out, void* stream);
+
+/* One step over all tensors of the plan. */
+BD_API int bo_adamw_step(const bo_adamw* h, const bo_adamw_step_args* args, void* stream);
+
+/* The global gradient norm alone: control.norm, and control.coef for max_norm (1 for 0). */
+BD_API int bo_adamw_norm(const bo_adamw* h, float max_norm, void* stream);
+
+/* Both moments of an 8-bit state as values of `dtype`, in the arenas' layout (256 * blocks
+ * elements each; 16-byte aligned).  Either output may be NULL. */
+BD_API int bo_adamw_moments(const bo_adamw* h, uint32_t dtype, void* d_m, void* d_v,
+                            void* stream);
+
+/* Library utility: static description of a status, bd_status included. */
+BD_API const char* bo_status_string(int code);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* BF16OPS_H */

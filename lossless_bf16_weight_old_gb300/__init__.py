@@ -19,6 +19,7 @@ from typing import Sequence
 import torch
 
 from . import _lib
+from .ops import AdamWBatch, SKIPPED_NONFINITE, OpsError, ops_status_name
 
 OK, ERR_INVALID_ARG, ERR_CAPACITY, ERR_FORMAT, ERR_CHECKSUM, ERR_CUDA, ERR_BASE = range(7)
 FORMAT_NAME = "bf16_xor_v1"
@@ -31,6 +32,7 @@ __all__ = [
     "decompress_batch", "decompress_incremental", "IncrementalBatch", "checksum",
     "compress_bound", "compress_workspace_size", "decompress_workspace_size", "payload_info",
     "DeltaError", "status_name", "MappedHostBuffer", "StreamedDecompressBatch",
+    "AdamWBatch", "SKIPPED_NONFINITE", "OpsError", "ops_status_name",
 ]
 
 

@@ -1,0 +1,786 @@
+// bo_adamw.cu -- AdamW over many tensors at once, with 32-bit or 8-bit moments, and the global
+// gradient norm (include/ops/bf16ops.h has the formulas and the layout of the state).
+//
+// One table entry per 2048 elements carries everything a block needs, so a launch covers any
+// number of tensors and a block's work is one 48-byte load away.  All kernels are bound by HBM:
+// the step moves 28 bytes per element (BF16 gradients, FP32 master, 32-bit moments; 16 with
+// 8-bit moments), the norm 2.
+#include <cmath>
+#include <cstring>
+#include <memory>
+#include <new>
+#include <vector>
+
+#include "bo_internal.cuh"
+
+namespace bo {
+namespace {
+
+constexpr uint32_t kThreads = 256;
+constexpr uint32_t kChunkElems = 2048;   // eight elements a thread; eight 8-bit blocks
+constexpr uint32_t kMaxGrid = 152 * 8;   // most blocks of the norm (its partial sums)
+constexpr uint64_t kGamma = 0x9E3779B97F4A7C15ull;
+
+struct alignas(16) Chunk {
+  const void* w;    // weights of the chunk's first element (nullptr with a master)
+  void* out;
+  const void* g;
+  uint64_t e0;      // its element in the arenas
+  float wd;
+  uint32_t count;   // elements, at most kChunkElems
+  uint64_t pad;
+};
+static_assert(sizeof(Chunk) == 48, "three 16-byte words");
+
+__device__ __forceinline__ Chunk load_chunk(const Chunk* p) {
+  Chunk c;
+  const uint4* s = reinterpret_cast<const uint4*>(p);
+  uint4* d = reinterpret_cast<uint4*>(&c);
+  d[0] = __ldg(s);
+  d[1] = __ldg(s + 1);
+  d[2] = __ldg(s + 2);
+  return c;
+}
+
+// ------------------------------------------------------------------------------- the table
+struct alignas(16) DevItem {
+  const uint8_t* w;
+  uint8_t* out;
+  const uint8_t* g;
+  uint64_t n;
+  uint64_t first_block;
+  uint64_t chunk0;   // chunks before this item
+  float wd;
+  uint32_t pad;
+  uint64_t pad2;
+};
+static_assert(sizeof(DevItem) % 16 == 0, "uploaded in 16-byte words");
+
+__global__ void k_build_chunks(const DevItem* __restrict__ items, uint32_t k, uint64_t chunks,
+                               Chunk* __restrict__ table, uint32_t wsize, uint32_t gsize,
+                               uint32_t osize) {
+  const uint64_t c = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (c >= chunks) return;
+  uint32_t lo = 0, hi = k;   // the last item whose chunk0 <= c
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) / 2;
+    if (items[mid].chunk0 <= c) lo = mid; else hi = mid;
+  }
+  const DevItem it = items[lo];
+  const uint64_t at = (c - it.chunk0) * kChunkElems;
+  Chunk ch;
+  ch.w = it.w ? it.w + at * wsize : nullptr;
+  ch.out = it.out + at * osize;
+  ch.g = it.g + at * gsize;
+  ch.e0 = it.first_block * BO_BLOCK_ELEMS + at;
+  ch.wd = it.wd;
+  const uint64_t left = it.n - at;
+  ch.count = left < kChunkElems ? (uint32_t)left : kChunkElems;
+  ch.pad = 0;
+  table[c] = ch;
+}
+
+__global__ void k_init_control(bo_adamw_control* ctl, int64_t step) {
+  ctl->step = step;
+  ctl->norm = 0.f;
+  ctl->coef = 1.f;
+  ctl->status = BD_OK;
+  ctl->ticket[0] = ctl->ticket[1] = ctl->ticket[2] = 0;
+}
+
+// ------------------------------------------------------------------- eight elements of a kind
+template <bool F32>
+__device__ __forceinline__ void load8(const void* p, uint32_t i, float (&x)[8]) {
+  if (F32) {
+    const uint4 a = ld16(static_cast<const float*>(p) + i);
+    const uint4 b = ld16(static_cast<const float*>(p) + i + 4);
+    x[0] = __uint_as_float(a.x); x[1] = __uint_as_float(a.y);
+    x[2] = __uint_as_float(a.z); x[3] = __uint_as_float(a.w);
+    x[4] = __uint_as_float(b.x); x[5] = __uint_as_float(b.y);
+    x[6] = __uint_as_float(b.z); x[7] = __uint_as_float(b.w);
+  } else {
+    const uint4 a = ld16(static_cast<const uint16_t*>(p) + i);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      x[2 * j] = bf16_lo(w[j]);
+      x[2 * j + 1] = bf16_hi(w[j]);
+    }
+  }
+}
+template <bool F32>
+__device__ __forceinline__ float load1(const void* p, uint32_t i) {
+  return F32 ? static_cast<const float*>(p)[i]
+             : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
+}
+
+// ------------------------------------------------------------------------------ random bits
+__device__ __forceinline__ uint64_t mix64(uint64_t z) {   // SplitMix64 (Steele, Lea & Flood 2014)
+  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+  return z ^ (z >> 31);
+}
+// the 32 bits of each of the eight elements from e0 on (e0 a multiple of 8)
+__device__ __forceinline__ void noise8(uint64_t key, uint64_t e0, uint32_t (&r)[8]) {
+  uint64_t z = key + ((e0 >> 1) + 1) * kGamma;
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    const uint64_t h = mix64(z);
+    r[2 * j] = (uint32_t)h;
+    r[2 * j + 1] = (uint32_t)(h >> 32);
+    z += kGamma;
+  }
+}
+// BF16 bits of x: away from zero when the cut-off part plus 16 random bits carries
+__device__ __forceinline__ uint32_t bf16_stochastic(float x, uint32_t r) {
+  const uint32_t b = __float_as_uint(x);
+  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0x7FFFu;   // NaN: no carry into the sign
+  return (b + (r & 0xFFFFu)) >> 16;
+}
+
+// ----------------------------------------------------------------------------- the formula
+struct Rates {      // per launch
+  float b1, c1, b2, c2;      // beta and 1 - beta
+  float inv_bc1, inv_bc2;    // 1 / (1 - beta^t)
+  float lr, eps, coef;
+};
+
+struct StepParams {
+  const Chunk* table;
+  uint64_t chunks;
+  bo_adamw_state st;
+  bo_adamw_control* ctl;
+  const float* d_lr;
+  float lr, b1, c1, b2, c2, log_b1, log_b2, eps;
+  uint32_t clip;
+  uint32_t stochastic;
+  uint64_t seed;
+};
+
+// Reads what the step depends on, once per block; false: the step is skipped.  The step count
+// is written only after every block has passed here (finish_step).
+__device__ __forceinline__ bool begin_step(const StepParams& P, Rates& R, uint64_t& key) {
+  __shared__ float sh[4];
+  __shared__ unsigned long long sh_key;
+  if (threadIdx.x == 0) {
+    const int64_t t = *reinterpret_cast<volatile int64_t*>(&P.ctl->step) + 1;
+    // 1 - beta^t without cancellation (beta = 0: log is -inf and the factor 1)
+    sh[0] = 1.f / -expm1f((float)t * P.log_b1);
+    sh[1] = 1.f / -expm1f((float)t * P.log_b2);
+    sh[2] = P.d_lr ? *P.d_lr : P.lr;
+    float coef = 1.f;
+    if (P.clip) {
+      const float norm = P.ctl->norm;
+      coef = isfinite(norm) ? P.ctl->coef : -1.f;
+    }
+    sh[3] = coef;
+    sh_key = mix64(P.seed ^ ((uint64_t)t * kGamma));
+  }
+  __syncthreads();
+  R.b1 = P.b1; R.c1 = P.c1; R.b2 = P.b2; R.c2 = P.c2; R.eps = P.eps;
+  R.inv_bc1 = sh[0];
+  R.inv_bc2 = sh[1];
+  R.lr = sh[2];
+  R.coef = sh[3];
+  key = sh_key;
+  return sh[3] >= 0.f;
+}
+
+// The last block to finish counts the step.
+__device__ __forceinline__ void finish_step(const StepParams& P, bool taken) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if (atomicInc(&P.ctl->ticket[1], gridDim.x - 1) == gridDim.x - 1) {
+      if (taken) P.ctl->step = P.ctl->step + 1;
+      P.ctl->status = taken ? BD_OK : BO_SKIPPED_NONFINITE;
+    }
+  }
+}
+
+__device__ __forceinline__ float sqrt_fast(float x) {   // within 2^-22 or so of the root
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// One element: updates m, v and p.  The root and the quotient are the hardware's approximations,
+// a few units in the last place of a term that lr scales down before it meets p.
+__device__ __forceinline__ void update(const Rates& R, float keep, float g, float& m, float& v,
+                                       float& p) {
+  g *= R.coef;
+  m = fmaf(R.b1, m, R.c1 * g);
+  v = fmaf(R.b2, v, R.c2 * g * g);
+  const float den = sqrt_fast(v * R.inv_bc2) + R.eps;
+  const float q = m == 0.f ? 0.f : __fdividef(m * R.inv_bc1, den);   // (eps = 0: 0 / 0 is 0)
+  p = fmaf(p, keep, -R.lr * q);
+}
+
+// Eight new weights from p: the master and its rounding, or the weights alone.
+template <int WK>
+__device__ __forceinline__ void store_weights(const Chunk& c, uint32_t i, float* master,
+                                              const float (&p)[8], bool stochastic,
+                                              const uint32_t (&r)[8]) {
+  if (WK == BO_WEIGHT_FP32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(c.out) + i);
+    o[0] = make_float4(p[0], p[1], p[2], p[3]);
+    o[1] = make_float4(p[4], p[5], p[6], p[7]);
+    return;
+  }
+  if (WK == BO_WEIGHT_MASTER) {
+    Float8 q;
+#pragma unroll
+    for (int j = 0; j < 8; j++) q.v[j] = p[j];
+    st8(master, q);
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; j++)
+    w[j] = (WK == BO_WEIGHT_BF16 && stochastic)
+               ? (bf16_stochastic(p[2 * j], r[2 * j]) |
+                  bf16_stochastic(p[2 * j + 1], r[2 * j + 1]) << 16)
+               : pack_bf16(p[2 * j], p[2 * j + 1]);
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.out) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int WK>
+__device__ __forceinline__ void store_weight1(const Chunk& c, uint32_t i, float* master, float p,
+                                              bool stochastic, uint32_t r) {
+  if (WK == BO_WEIGHT_FP32) {
+    static_cast<float*>(c.out)[i] = p;
+    return;
+  }
+  if (WK == BO_WEIGHT_MASTER) *master = p;
+  static_cast<uint16_t*>(c.out)[i] =
+      (uint16_t)((WK == BO_WEIGHT_BF16 && stochastic) ? bf16_stochastic(p, r)
+                                                       : pack_bf16(p, 0.f) & 0xFFFFu);
+}
+
+// ------------------------------------------------------------------------ 32-bit moments
+template <int WK, bool GF32>
+__global__ void __launch_bounds__(kThreads, 4) k_step32(const StepParams P) {
+  Rates R;
+  uint64_t key;
+  const bool taken = begin_step(P, R, key);
+  if (taken) {
+    float* const am = static_cast<float*>(P.st.d_m);
+    float* const av = static_cast<float*>(P.st.d_v);
+    Chunk next = load_chunk(P.table + blockIdx.x);
+    for (uint64_t ci = blockIdx.x; ci < P.chunks; ci += gridDim.x) {
+      const Chunk c = next;
+      if (ci + gridDim.x < P.chunks) next = load_chunk(P.table + ci + gridDim.x);
+      const uint32_t i = threadIdx.x * 8;
+      const float keep = 1.f - R.lr * c.wd;
+      const uint64_t e = c.e0 + i;
+      float* const pm = WK == BO_WEIGHT_MASTER ? P.st.d_master + e : nullptr;
+      if (i + 8 <= c.count) {
+        float g[8], p[8];
+        load8<GF32>(c.g, i, g);
+        Float8 m = ld8(am + e), v = ld8(av + e);
+        if (WK == BO_WEIGHT_MASTER) {
+          const Float8 q = ld8(pm);
+#pragma unroll
+          for (int j = 0; j < 8; j++) p[j] = q.v[j];
+        } else {
+          load8<WK == BO_WEIGHT_FP32>(c.w, i, p);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++) update(R, keep, g[j], m.v[j], v.v[j], p[j]);
+        st8(am + e, m);
+        st8(av + e, v);
+        uint32_t r[8] = {};
+        if (WK == BO_WEIGHT_BF16 && P.stochastic) noise8(key, e, r);
+        store_weights<WK>(c, i, pm, p, P.stochastic, r);
+      } else if (i < c.count) {   // a tensor's last elements
+        uint32_t r[8] = {};
+        if (WK == BO_WEIGHT_BF16 && P.stochastic) noise8(key, e, r);
+#pragma unroll
+        for (uint32_t j = 0; j < 8; j++) {
+          if (i + j >= c.count) break;
+          const float g = load1<GF32>(c.g, i + j);
+          float m = am[e + j], v = av[e + j];
+          float p = WK == BO_WEIGHT_MASTER ? pm[j] : load1<WK == BO_WEIGHT_FP32>(c.w, i + j);
+          update(R, keep, g, m, v, p);
+          am[e + j] = m;
+          av[e + j] = v;
+          store_weight1<WK>(c, i + j, pm + (WK == BO_WEIGHT_MASTER ? j : 0), p, P.stochastic, r[j]);
+        }
+      }
+    }
+  }
+  finish_step(P, taken);
+}
+
+// ------------------------------------------------------------------------- 8-bit moments
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) x = max_nan(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
+  return x;
+}
+// An infinite scale would read as infinity or NaN by the code: NaN throughout marks the block.
+__device__ __forceinline__ float finite_or_nan(float x) {
+  return isfinite(x) ? x : __int_as_float(0x7FFFFFFF);
+}
+// 1 / scale, taken at a power of two that keeps it a normal number: x / scale = x * pre * inv.
+__device__ __forceinline__ void inverse_scale(float scale, float& pre, float& inv) {
+  pre = scale < 0x1p-60f ? 0x1p80f : scale > 0x1p60f ? 0x1p-60f : 1.f;
+  inv = scale > 0.f ? 1.f / (scale * pre) : 0.f;   // (a NaN scale: codes 0, read as 0 * NaN)
+}
+__device__ __forceinline__ float m_value(float c) { return c * fabsf(c) * (1.f / 16129.f); }
+__device__ __forceinline__ float v_value(float c) {   // (c / 255)^4; c^2 is exact
+  const float c2 = c * c;
+  return c2 * c2 * (float)(1.0 / (65025.0 * 65025.0));
+}
+__device__ __forceinline__ int32_t m_code(float m, float pre, float inv) {
+  const float c = sqrt_fast(fabsf(m) * pre * inv) * 127.f;
+  const int32_t k = __float2int_rn(c);
+  return m < 0.f ? -k : k;
+}
+// Of the two codes whose values enclose v / scale, the upper one with the chance that makes the
+// expected value v / scale; never 0 for v > 0 (a root of 0 under a moment that is not 0 would
+// make a step without bound).
+__device__ __forceinline__ uint32_t v_code(float v, float pre, float inv, uint32_t r) {
+  const float x = v * pre * inv;
+  const float low = fminf(floorf(sqrt_fast(sqrt_fast(x)) * 255.f), 254.f);
+  const float a = v_value(low), b = v_value(low + 1.f);
+  const float u = (float)(r >> 16) * (1.f / 65536.f);
+  const float c = low + (u * (b - a) < x - a ? 1.f : 0.f);
+  return v > 0.f ? max((uint32_t)c, 1u) : 0u;
+}
+
+// One warp per block of 256: its eight elements a lane stay in registers while the block's
+// maxima are found, so each byte is read and written once.
+template <int WK, bool GF32>
+__global__ void __launch_bounds__(kThreads, 4) k_step8(const StepParams P) {
+  Rates R;
+  uint64_t key;
+  const bool taken = begin_step(P, R, key);
+  if (taken) {
+    uint8_t* const am = static_cast<uint8_t*>(P.st.d_m);
+    uint8_t* const av = static_cast<uint8_t*>(P.st.d_v);
+    const uint32_t lane = threadIdx.x & 31;
+    Chunk next = load_chunk(P.table + blockIdx.x);
+    for (uint64_t ci = blockIdx.x; ci < P.chunks; ci += gridDim.x) {
+      const Chunk c = next;
+      if (ci + gridDim.x < P.chunks) next = load_chunk(P.table + ci + gridDim.x);
+      const uint32_t i = threadIdx.x * 8;
+      if ((threadIdx.x & ~31u) * 8 >= c.count) continue;   // (the whole warp)
+      const float keep = 1.f - R.lr * c.wd;
+      const uint64_t e = c.e0 + i, blk = e / BO_BLOCK_ELEMS;
+      float* const pm = WK == BO_WEIGHT_MASTER ? P.st.d_master + e : nullptr;
+      const uint32_t cnt = c.count > i ? min(c.count - i, 8u) : 0u;
+      float g[8] = {}, p[8] = {}, m[8], v[8];
+      const uint2 cm = *reinterpret_cast<const uint2*>(am + e);
+      const uint2 cv = *reinterpret_cast<const uint2*>(av + e);
+      const float sm = P.st.d_m_scale[blk], sv = P.st.d_v_scale[blk];
+      if (cnt == 8) {
+        load8<GF32>(c.g, i, g);
+        if (WK == BO_WEIGHT_MASTER) {
+          const Float8 q = ld8(pm);
+#pragma unroll
+          for (int j = 0; j < 8; j++) p[j] = q.v[j];
+        } else {
+          load8<WK == BO_WEIGHT_FP32>(c.w, i, p);
+        }
+      } else {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; j++)
+          if (j < cnt) {
+            g[j] = load1<GF32>(c.g, i + j);
+            p[j] = WK == BO_WEIGHT_MASTER ? pm[j] : load1<WK == BO_WEIGHT_FP32>(c.w, i + j);
+          }
+      }
+      float mm = 0.f, mv = 0.f;
+#pragma unroll
+      for (uint32_t j = 0; j < 8; j++) {
+        const uint32_t wm = j < 4 ? cm.x : cm.y, wv = j < 4 ? cv.x : cv.y;
+        m[j] = m_value((float)(int8_t)(wm >> (8 * (j & 3)))) * sm;
+        v[j] = v_value((float)(uint8_t)(wv >> (8 * (j & 3)))) * sv;
+        if (j >= cnt) m[j] = v[j] = 0.f;   // padding behind the tensor's end
+        update(R, keep, g[j], m[j], v[j], p[j]);
+        mm = max_nan(mm, fabsf(m[j]));
+        mv = max_nan(mv, v[j]);
+      }
+      mm = finite_or_nan(warp_max(mm));
+      mv = finite_or_nan(warp_max(mv));
+      float mpre, minv, vpre, vinv;
+      inverse_scale(mm, mpre, minv);
+      inverse_scale(mv, vpre, vinv);
+      uint32_t r[8];
+      noise8(key, e, r);
+      uint2 qm = make_uint2(0, 0), qv = make_uint2(0, 0);
+#pragma unroll
+      for (uint32_t j = 0; j < 8; j++) {
+        const uint32_t a = ((uint32_t)m_code(m[j], mpre, minv) & 0xFFu) << (8 * (j & 3));
+        const uint32_t b = v_code(v[j], vpre, vinv, r[j]) << (8 * (j & 3));
+        if (j < 4) { qm.x |= a; qv.x |= b; } else { qm.y |= a; qv.y |= b; }
+      }
+      *reinterpret_cast<uint2*>(am + e) = qm;
+      *reinterpret_cast<uint2*>(av + e) = qv;
+      if (lane == 0) {
+        P.st.d_m_scale[blk] = mm;
+        P.st.d_v_scale[blk] = mv;
+      }
+      if (cnt == 8) {
+        store_weights<WK>(c, i, pm, p, P.stochastic, r);
+      } else {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; j++)
+          if (j < cnt)
+            store_weight1<WK>(c, i + j, pm + (WK == BO_WEIGHT_MASTER ? j : 0), p[j], P.stochastic,
+                              r[j]);
+      }
+    }
+  }
+  finish_step(P, taken);
+}
+
+// Codes to values, one lane per eight elements of the arenas.
+template <bool F32, bool V>
+__global__ void __launch_bounds__(kThreads) k_moments(const uint8_t* __restrict__ codes,
+                                                       const float* __restrict__ scales,
+                                                       uint64_t blocks, void* __restrict__ out) {
+  const uint64_t stride = (uint64_t)gridDim.x * blockDim.x;
+  for (uint64_t t = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; t < blocks * 32; t += stride) {
+    const uint2 c = reinterpret_cast<const uint2*>(codes)[t];
+    const float s = scales[t >> 5];
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      const uint32_t w = (j < 4 ? c.x : c.y) >> (8 * (j & 3));
+      x[j] = (V ? v_value((float)(uint8_t)w) : m_value((float)(int8_t)w)) * s;
+    }
+    if (F32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + 8 * t);
+      o[0] = make_float4(x[0], x[1], x[2], x[3]);
+      o[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+      reinterpret_cast<uint4*>(out)[t] =
+          make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                     pack_bf16(x[6], x[7]));
+    }
+  }
+}
+
+// --------------------------------------------------------------------------- gradient norm
+// Sums in a fixed order: eight FP32 sums a thread over its elements, joined in FP64 over the
+// block, and the blocks' sums by the last block to finish.
+template <bool GF32>
+__global__ void __launch_bounds__(kThreads, 8) k_norm(const Chunk* __restrict__ table,
+                                                      uint64_t chunks, double* __restrict__ part,
+                                                      bo_adamw_control* ctl, float max_norm) {
+  float s[8] = {};
+  if (blockIdx.x < chunks) {
+    Chunk next = load_chunk(table + blockIdx.x);
+    for (uint64_t ci = blockIdx.x; ci < chunks; ci += gridDim.x) {
+      const Chunk c = next;
+      if (ci + gridDim.x < chunks) next = load_chunk(table + ci + gridDim.x);
+      const uint32_t i = threadIdx.x * 8;
+      if (i + 8 <= c.count) {
+        float g[8];
+        load8<GF32>(c.g, i, g);
+#pragma unroll
+        for (int j = 0; j < 8; j++) s[j] = fmaf(g[j], g[j], s[j]);
+      } else {
+        for (uint32_t j = i; j < c.count; j++) {
+          const float g = load1<GF32>(c.g, j);
+          s[0] = fmaf(g, g, s[0]);
+        }
+      }
+    }
+  }
+  __shared__ double sh[kThreads];
+  __shared__ bool last;
+  sh[threadIdx.x] = (double)(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
+  __syncthreads();
+  for (uint32_t d = kThreads / 2; d; d >>= 1) {
+    if (threadIdx.x < d) sh[threadIdx.x] += sh[threadIdx.x + d];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    part[blockIdx.x] = sh[0];
+    __threadfence();
+    last = atomicInc(&ctl->ticket[0], gridDim.x - 1) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double t = 0;
+  for (uint32_t b = threadIdx.x; b < gridDim.x; b += kThreads) t += __ldcg(part + b);
+  sh[threadIdx.x] = t;
+  __syncthreads();
+  for (uint32_t d = kThreads / 2; d; d >>= 1) {
+    if (threadIdx.x < d) sh[threadIdx.x] += sh[threadIdx.x + d];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    const float norm = (float)sqrt(sh[0]);
+    ctl->norm = norm;
+    ctl->coef = max_norm > 0.f ? fminf(1.f, max_norm / (norm + 1e-6f)) : 1.f;
+  }
+}
+
+// ------------------------------------------------------------------------------- host side
+struct PlanLayout {
+  uint64_t control, partials, items, table, total, chunks;
+};
+
+bool plan_layout(const bo_adamw_item* items, uint32_t k, PlanLayout& L) {
+  if (k > 0 && !items) return false;
+  L.chunks = 0;
+  for (uint32_t i = 0; i < k; i++) {
+    if (items[i].n > BD_MAX_ELEMS) return false;
+    L.chunks += (items[i].n + kChunkElems - 1) / kChunkElems;
+  }
+  if (L.chunks > (1ull << 36)) return false;
+  L.control = 0;
+  L.partials = up(sizeof(bo_adamw_control), 256);
+  L.items = L.partials + up((uint64_t)kMaxGrid * sizeof(double), 256);
+  L.table = L.items + up((uint64_t)k * sizeof(DevItem), 256);
+  L.total = L.table + up(L.chunks * sizeof(Chunk), 256);
+  return true;
+}
+
+bool valid(const bo_adamw* h) {
+  return h && h->d_control && h->d_chunks && h->d_partials && h->weight_kind <= BO_WEIGHT_FP32 &&
+         h->grad_dtype <= BO_FP32 && (h->state_bits == 8 || h->state_bits == 32);
+}
+
+int launch_norm(const bo_adamw* h, float max_norm, int sms, cudaStream_t s) {
+  const uint64_t want = h->chunks < 1 ? 1 : h->chunks;
+  const uint32_t most = (uint32_t)sms * 8 < kMaxGrid ? (uint32_t)sms * 8 : kMaxGrid;
+  const uint32_t grid = (uint32_t)(want < most ? want : most);
+  const Chunk* table = static_cast<const Chunk*>(h->d_chunks);
+  if (h->grad_dtype == BO_FP32)
+    k_norm<true><<<grid, kThreads, 0, s>>>(table, h->chunks, h->d_partials, h->d_control, max_norm);
+  else
+    k_norm<false><<<grid, kThreads, 0, s>>>(table, h->chunks, h->d_partials, h->d_control, max_norm);
+  return check(cudaGetLastError());
+}
+
+template <int WK, bool GF32>
+void launch_step(bool bits8, uint32_t grid, const StepParams& P, cudaStream_t s) {
+  if (bits8)
+    k_step8<WK, GF32><<<grid, kThreads, 0, s>>>(P);
+  else
+    k_step32<WK, GF32><<<grid, kThreads, 0, s>>>(P);
+}
+
+}  // namespace
+
+constexpr uint32_t kBlobWords = 30 * 1024 / 16;
+struct Blob {
+  uint32_t words;
+  uint32_t pad[3];
+  uint4 data[kBlobWords];
+};
+static_assert(sizeof(Blob) <= 32000, "kernel parameter limit");
+
+__global__ void k_put(const __grid_constant__ Blob b, uint4* __restrict__ dst) {
+  const uint32_t i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < b.words) dst[i] = b.data[i];
+}
+
+cudaError_t upload(const void* host, uint64_t bytes, void* dst, cudaStream_t s) {
+  const uint64_t words = bytes / 16;
+  std::unique_ptr<Blob> b(new (std::nothrow) Blob);
+  if (!b) return cudaErrorMemoryAllocation;
+  for (uint64_t w0 = 0; w0 < words; w0 += kBlobWords) {
+    const uint32_t cnt = (uint32_t)(words - w0 < kBlobWords ? words - w0 : kBlobWords);
+    b->words = cnt;
+    std::memcpy(b->data, static_cast<const uint8_t*>(host) + w0 * 16, (size_t)cnt * 16);
+    k_put<<<(cnt + 127) / 128, 128, 0, s>>>(*b, static_cast<uint4*>(dst) + w0);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace bo
+
+using namespace bo;
+
+extern "C" {
+
+uint64_t bo_adamw_plan_size(const bo_adamw_item* h_items, uint32_t k) {
+  PlanLayout L;
+  return plan_layout(h_items, k, L) ? L.total : 0;
+}
+
+int bo_adamw_plan(const bo_adamw_item* h_items, uint32_t k, const bo_adamw_state* state,
+                  uint32_t weight_kind, uint32_t grad_dtype, uint32_t state_bits, uint32_t flags,
+                  int64_t step, void* d_plan, uint64_t plan_bytes, bo_adamw* h_out,
+                  void* stream) {
+  PlanLayout L;
+  if (!state || !h_out || !plan_layout(h_items, k, L)) return BD_ERR_INVALID_ARG;
+  if (weight_kind > BO_WEIGHT_FP32 || grad_dtype > BO_FP32 || (state_bits != 8 && state_bits != 32) ||
+      (flags & ~BO_ADAMW_STOCHASTIC) || step < 0)
+    return BD_ERR_INVALID_ARG;
+  if ((flags & BO_ADAMW_STOCHASTIC) && weight_kind != BO_WEIGHT_BF16) return BD_ERR_INVALID_ARG;
+  if (!d_plan || !aligned(d_plan, 256) || plan_bytes < L.total) return BD_ERR_INVALID_ARG;
+  const bool master = weight_kind == BO_WEIGHT_MASTER;
+  if (state->blocks > BD_MAX_ELEMS / BO_BLOCK_ELEMS) return BD_ERR_INVALID_ARG;
+  if (state->blocks > 0) {
+    if (!state->d_m || !state->d_v || !aligned(state->d_m, 256) || !aligned(state->d_v, 256) ||
+        (master && (!state->d_master || !aligned(state->d_master, 256))) ||
+        (state_bits == 8 && (!state->d_m_scale || !state->d_v_scale ||
+                             !aligned(state->d_m_scale, 256) || !aligned(state->d_v_scale, 256))))
+      return BD_ERR_INVALID_ARG;
+  }
+  const uint64_t wsize = weight_kind == BO_WEIGHT_FP32 ? 4 : 2, gsize = grad_dtype == BO_FP32 ? 4 : 2;
+  const uint64_t elems = state->blocks * BO_BLOCK_ELEMS, msize = state_bits == 8 ? 1 : 4;
+  std::unique_ptr<DevItem[]> dev(new (std::nothrow) DevItem[k ? k : 1]);
+  if (!dev) return BD_ERR_INVALID_ARG;
+  uint64_t chunk0 = 0;
+  for (uint32_t i = 0; i < k; i++) {
+    const bo_adamw_item& it = h_items[i];
+    const uint64_t blocks = (it.n + BO_BLOCK_ELEMS - 1) / BO_BLOCK_ELEMS;
+    if (it.reserved != 0 || it.first_block > state->blocks ||
+        blocks > state->blocks - it.first_block)
+      return BD_ERR_INVALID_ARG;
+    if (it.n > 0) {
+      if (!it.d_out || !it.d_grad || !aligned(it.d_out, 16) || !aligned(it.d_grad, 16))
+        return BD_ERR_INVALID_ARG;
+      if (!master && (!it.d_weight || !aligned(it.d_weight, 16))) return BD_ERR_INVALID_ARG;
+      const uint64_t ob = it.n * wsize;
+      if (!master && it.d_out != it.d_weight && overlaps(it.d_out, ob, it.d_weight, ob))
+        return BD_ERR_INVALID_ARG;
+      if (overlaps(it.d_out, ob, it.d_grad, it.n * gsize) ||
+          overlaps(it.d_out, ob, d_plan, L.total) ||
+          overlaps(it.d_out, ob, state->d_m, elems * msize) ||
+          overlaps(it.d_out, ob, state->d_v, elems * msize) ||
+          (master && overlaps(it.d_out, ob, state->d_master, elems * 4)))
+        return BD_ERR_INVALID_ARG;
+    }
+    DevItem& d = dev[i];
+    std::memset(&d, 0, sizeof(d));
+    d.w = master ? nullptr : static_cast<const uint8_t*>(it.d_weight);
+    d.out = static_cast<uint8_t*>(it.d_out);
+    d.g = static_cast<const uint8_t*>(it.d_grad);
+    d.n = it.n;
+    d.first_block = it.first_block;
+    d.chunk0 = chunk0;
+    d.wd = it.weight_decay;
+    chunk0 += (it.n + kChunkElems - 1) / kChunkElems;
+  }
+  uint8_t* p = static_cast<uint8_t*>(d_plan);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bo_adamw h;
+  std::memset(&h, 0, sizeof(h));
+  h.state = *state;
+  h.d_control = reinterpret_cast<bo_adamw_control*>(p + L.control);
+  h.d_partials = reinterpret_cast<double*>(p + L.partials);
+  h.d_chunks = p + L.table;
+  h.chunks = L.chunks;
+  h.weight_kind = weight_kind;
+  h.grad_dtype = grad_dtype;
+  h.state_bits = state_bits;
+  h.flags = flags;
+  int rc;
+  k_init_control<<<1, 1, 0, s>>>(h.d_control, step);
+  if ((rc = check(cudaGetLastError()))) return rc;
+  if (L.chunks > 0) {
+    if ((rc = check(upload(dev.get(), (uint64_t)k * sizeof(DevItem), p + L.items, s)))) return rc;
+    k_build_chunks<<<(uint32_t)((L.chunks + 255) / 256), 256, 0, s>>>(
+        reinterpret_cast<const DevItem*>(p + L.items), k, L.chunks,
+        reinterpret_cast<Chunk*>(p + L.table), (uint32_t)wsize, (uint32_t)gsize, (uint32_t)wsize);
+    if ((rc = check(cudaGetLastError()))) return rc;
+  }
+  *h_out = h;
+  return BD_OK;
+}
+
+int bo_adamw_norm(const bo_adamw* h, float max_norm, void* stream) {
+  if (!valid(h) || !(max_norm >= 0.f)) return BD_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  if (sms <= 0) return BD_ERR_CUDA;
+  return launch_norm(h, max_norm, sms, static_cast<cudaStream_t>(stream));
+}
+
+int bo_adamw_step(const bo_adamw* h, const bo_adamw_step_args* a, void* stream) {
+  if (!valid(h) || !a) return BD_ERR_INVALID_ARG;
+  if (!(a->beta1 >= 0 && a->beta1 < 1 && a->beta2 >= 0 && a->beta2 < 1) || !(a->eps >= 0.f) ||
+      !(a->max_norm >= 0.f) || (a->d_lr && !aligned(a->d_lr, 4)) ||
+      (!a->d_lr && !std::isfinite(a->lr)))
+    return BD_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  if (sms <= 0) return BD_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a->max_norm > 0.f) {
+    const int rc = launch_norm(h, a->max_norm, sms, s);
+    if (rc) return rc;
+  }
+  StepParams P;
+  P.table = static_cast<const Chunk*>(h->d_chunks);
+  P.chunks = h->chunks;
+  P.st = h->state;
+  P.ctl = h->d_control;
+  P.d_lr = a->d_lr;
+  P.lr = a->lr;
+  P.b1 = (float)a->beta1;
+  P.c1 = (float)(1.0 - a->beta1);
+  P.b2 = (float)a->beta2;
+  P.c2 = (float)(1.0 - a->beta2);
+  P.log_b1 = (float)std::log(a->beta1);
+  P.log_b2 = (float)std::log(a->beta2);
+  P.eps = a->eps;
+  P.clip = a->max_norm > 0.f;
+  P.stochastic = (h->flags & BO_ADAMW_STOCHASTIC) != 0;
+  P.seed = a->seed;
+  const uint64_t want = h->chunks < 1 ? 1 : h->chunks;
+  const uint32_t most = (uint32_t)sms * 4;
+  const uint32_t grid = (uint32_t)(want < most ? want : most);
+  const bool b8 = h->state_bits == 8;
+  switch (h->weight_kind * 2 + h->grad_dtype) {
+    case BO_WEIGHT_MASTER * 2 + BO_BF16: launch_step<BO_WEIGHT_MASTER, false>(b8, grid, P, s); break;
+    case BO_WEIGHT_MASTER * 2 + BO_FP32: launch_step<BO_WEIGHT_MASTER, true>(b8, grid, P, s); break;
+    case BO_WEIGHT_BF16 * 2 + BO_BF16: launch_step<BO_WEIGHT_BF16, false>(b8, grid, P, s); break;
+    case BO_WEIGHT_BF16 * 2 + BO_FP32: launch_step<BO_WEIGHT_BF16, true>(b8, grid, P, s); break;
+    case BO_WEIGHT_FP32 * 2 + BO_BF16: launch_step<BO_WEIGHT_FP32, false>(b8, grid, P, s); break;
+    default: launch_step<BO_WEIGHT_FP32, true>(b8, grid, P, s); break;
+  }
+  return check(cudaGetLastError());
+}
+
+int bo_adamw_moments(const bo_adamw* h, uint32_t dtype, void* d_m, void* d_v, void* stream) {
+  if (!valid(h) || h->state_bits != 8 || dtype > BO_FP32 || !aligned(d_m, 16) || !aligned(d_v, 16))
+    return BD_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  if (sms <= 0) return BD_ERR_CUDA;
+  const uint64_t blocks = h->state.blocks;
+  if (blocks == 0) return BD_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const uint64_t want = (blocks * 32 + kThreads - 1) / kThreads;
+  const uint32_t grid = (uint32_t)(want < (uint64_t)sms * 8 ? want : (uint64_t)sms * 8);
+  for (int v = 0; v < 2; v++) {
+    void* out = v ? d_v : d_m;
+    if (!out) continue;
+    const uint8_t* codes = static_cast<const uint8_t*>(v ? h->state.d_v : h->state.d_m);
+    const float* sc = v ? h->state.d_v_scale : h->state.d_m_scale;
+    if (dtype == BO_FP32) {
+      if (v) k_moments<true, true><<<grid, kThreads, 0, s>>>(codes, sc, blocks, out);
+      else k_moments<true, false><<<grid, kThreads, 0, s>>>(codes, sc, blocks, out);
+    } else {
+      if (v) k_moments<false, true><<<grid, kThreads, 0, s>>>(codes, sc, blocks, out);
+      else k_moments<false, false><<<grid, kThreads, 0, s>>>(codes, sc, blocks, out);
+    }
+    const int rc = check(cudaGetLastError());
+    if (rc) return rc;
+  }
+  return BD_OK;
+}
+
+const char* bo_status_string(int code) {
+  switch (code) {
+    case BD_OK: return "ok";
+    case BD_ERR_INVALID_ARG: return "invalid argument";
+    case BD_ERR_CUDA: return "CUDA error";
+    case BO_SKIPPED_NONFINITE: return "step skipped: the gradient norm is not finite";
+    default: return "unknown status";
+  }
+}
+
+}  // extern "C"

@@ -1,0 +1,214 @@
+"""The operators on either side of the weight sync (binding over include/ops/bf16ops.h).
+
+    AdamWBatch        one AdamW step over many tensors, moments in 32 or in 8 bits: what makes
+                      the new weights that CompressBatch encodes
+
+Every computation runs in libbf16ops' CUDA kernels; this module checks and marshals arguments
+and allocates device buffers with PyTorch.  The names are re-exported by the package.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Sequence
+
+import torch
+
+from . import _ops_lib
+
+OK, ERR_INVALID_ARG = 0, 1
+SKIPPED_NONFINITE = 16
+BLOCK_ELEMS = 256
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+_U64 = (1 << 64) - 1
+
+__all__ = ["AdamWBatch", "SKIPPED_NONFINITE", "OpsError", "ops_status_name"]
+
+
+class OpsError(RuntimeError):
+    def __init__(self, code: int, what: str):
+        self.code = int(code)
+        super().__init__(f"{what}: {ops_status_name(code)} ({code})")
+
+
+def ops_status_name(code: int) -> str:
+    """Description of a status of these operators."""
+    return _ops_lib.load().bo_status_string(int(code)).decode()
+
+
+def _check(rc: int, what: str) -> None:
+    if rc != OK:
+        raise OpsError(rc, what)
+
+
+def _stream(stream) -> int:
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _arena(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int, device) -> torch.Tensor:
+    if t.dtype != dtype or t.numel() != numel or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"state[{name!r}] must be a contiguous {dtype} tensor of {numel} "
+                         f"elements on {device}")
+    return t
+
+
+class AdamWBatch:
+    """One AdamW step over fixed tensors: the tensor table, the state and the step count.
+
+    weights       tensors to update: bfloat16, or float32 for 32-bit weights
+    grads         their gradients, all bfloat16 or all float32
+    news          (optional) where the new weights go instead, the old ones staying as they are:
+                  CompressBatch(weights, news) then encodes the step
+    master        keep an FP32 master copy of bfloat16 weights (default); without one the
+                  bfloat16 weights are all there is, best rounded with stochastic=True
+    state_bits    32, or 8 for moments coded per block of 256 elements
+    weight_decay  one number, or one per tensor
+    max_norm      clip by the global gradient norm and skip a step whose norm is not finite
+                  (math.inf: only skip); None: neither
+    stochastic    round bfloat16 weights without a master stochastically
+    seed          of the random bits that this and 8-bit moments use
+    step          steps taken so far
+    state         (optional) dict of tensors to hold the state, as in `state` of another batch:
+                  "m", "v", with 8 bits "m_scale" and "v_scale", with a master "master"; those
+                  that are missing are made here (moments 0, master = weights)
+
+    The arenas in `state` hold the tensors one after the other, each from a new block of 256 on;
+    `view(name, i)` is tensor i's part.  Results on the device after `run`: the new weights, the
+    state, `norm` (float32[1], with max_norm), `status` (int32[1]: OK or SKIPPED_NONFINITE) and
+    `steps` (int64[1]).  Tensors must stay where they are for the life of the batch."""
+
+    def __init__(self, weights: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], *,
+                 news: Sequence[torch.Tensor] | None = None, master: bool | None = None,
+                 state_bits: int = 32, lr: float = 1e-3, betas: tuple[float, float] = (0.9, 0.999),
+                 eps: float = 1e-8, weight_decay: float | Sequence[float] = 0.0,
+                 max_norm: float | None = None, stochastic: bool = False, seed: int = 0,
+                 step: int = 0, state: dict | None = None, stream=None):
+        k = len(weights)
+        if k == 0:
+            raise ValueError("no tensors")
+        outs = list(news) if news is not None else list(weights)
+        if len(grads) != k or len(outs) != k:
+            raise ValueError("weights, grads and news differ in length")
+        dev, wtype, gtype = weights[0].device, weights[0].dtype, grads[0].dtype
+        if wtype not in _DTYPES or gtype not in _DTYPES:
+            raise TypeError(f"weights and grads must be bfloat16 or float32, got {wtype} and {gtype}")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        if master is None:
+            master = wtype == torch.bfloat16
+        if master and wtype != torch.bfloat16:
+            raise ValueError("a master copy goes with bfloat16 weights")
+        if stochastic and (master or wtype != torch.bfloat16):
+            raise ValueError("stochastic rounding goes with bfloat16 weights without a master")
+        decay = [float(weight_decay)] * k if isinstance(weight_decay, (int, float)) else \
+            [float(d) for d in weight_decay]
+        if len(decay) != k:
+            raise ValueError("weight_decay must be one number or one per tensor")
+        if max_norm is not None and not max_norm > 0:
+            raise ValueError("max_norm must be positive")
+        if not (0 <= betas[0] < 1 and 0 <= betas[1] < 1) or not eps >= 0:
+            raise ValueError("betas must lie in [0, 1) and eps must not be negative")
+        if step < 0:
+            raise ValueError("step must not be negative")
+        for name, ts, dt in (("weights", weights, wtype), ("grads", grads, gtype), ("news", outs, wtype)):
+            for i, t in enumerate(ts):
+                if t.dtype != dt or not t.is_cuda or t.device != dev or not t.is_contiguous():
+                    raise ValueError(f"{name}[{i}] must be a contiguous {dt} tensor on {dev}")
+                if t.numel() != weights[i].numel():
+                    raise ValueError(f"{name}[{i}] has {t.numel()} elements, its weights "
+                                     f"{weights[i].numel()}")
+        self.shapes = [w.shape for w in weights]
+        self.ns = [w.numel() for w in weights]
+        self.first_blocks, blocks = [], 0
+        for n in self.ns:
+            self.first_blocks.append(blocks)
+            blocks += -(-n // BLOCK_ELEMS)
+        self.blocks, self.state_bits = blocks, state_bits
+        self.lr, self.betas, self.eps = lr, (float(betas[0]), float(betas[1])), float(eps)
+        self.max_norm = max_norm
+
+        given, elems = dict(state or {}), blocks * BLOCK_ELEMS
+        want = {"m": torch.float32, "v": torch.float32} if state_bits == 32 else \
+            {"m": torch.int8, "v": torch.uint8, "m_scale": torch.float32, "v_scale": torch.float32}
+        if master:
+            want["master"] = torch.float32
+        if set(given) - set(want):
+            raise ValueError(f"state has no place for {sorted(set(given) - set(want))}")
+        self.state: dict[str, torch.Tensor] = {}
+        for name, dt in want.items():
+            numel = blocks if name.endswith("_scale") else elems
+            self.state[name] = _arena(given[name], name, dt, numel, dev) if name in given else \
+                torch.zeros(numel, dtype=dt, device=dev)
+        if master and "master" not in given:
+            for i, w in enumerate(weights):
+                self.view("master", i).copy_(w)
+
+        items = (_ops_lib.AdamWItem * k)()
+        for i in range(k):
+            items[i].d_weight = weights[i].data_ptr()
+            items[i].d_out = outs[i].data_ptr()
+            items[i].d_grad = grads[i].data_ptr()
+            items[i].n = self.ns[i]
+            items[i].first_block = self.first_blocks[i]
+            items[i].weight_decay = decay[i]
+        ptr = {n: t.data_ptr() if blocks else None for n, t in self.state.items()}
+        st = _ops_lib.AdamWState(ptr["m"], ptr["v"], ptr.get("m_scale"), ptr.get("v_scale"),
+                                 ptr.get("master"), blocks)
+        lib = _ops_lib.load()
+        self.plan = torch.empty(int(lib.bo_adamw_plan_size(items, k)), dtype=torch.uint8, device=dev)
+        self.handle = _ops_lib.AdamW()
+        kind = 2 if wtype == torch.float32 else 0 if master else 1
+        _check(lib.bo_adamw_plan(items, k, ctypes.byref(st), kind, _DTYPES[gtype], state_bits,
+                                 int(bool(stochastic)), int(step), self.plan.data_ptr(),
+                                 self.plan.numel(), ctypes.byref(self.handle), _stream(stream)),
+               "bo_adamw_plan")
+        self.steps = self.plan[:8].view(torch.int64)
+        self.norm = self.plan[8:12].view(torch.float32)
+        self.status = self.plan[16:20].view(torch.int32)
+        self._args = _ops_lib.AdamWStepArgs(float(lr), None, self.betas[0], self.betas[1], self.eps,
+                                            0.0 if max_norm is None else float(max_norm),
+                                            int(seed) & _U64)
+        self._refs = ctypes.byref(self.handle), ctypes.byref(self._args)
+        self._step = lib.bo_adamw_step
+        self._keep = (list(weights), list(grads), outs)
+
+    def run(self, lr: float | torch.Tensor | None = None, stream=None) -> None:
+        """Takes one step, with this learning rate (a number, or a float32[1] device tensor that
+        the step reads when it runs) or the batch's own."""
+        if lr is not None:
+            if isinstance(lr, torch.Tensor):
+                if lr.dtype != torch.float32 or lr.numel() != 1 or not lr.is_cuda:
+                    raise ValueError("lr must be a number or a float32[1] CUDA tensor")
+                self._lr = lr
+                self._args.d_lr = lr.data_ptr()
+            else:
+                self.lr = float(lr)
+                self._args.lr, self._args.d_lr = self.lr, None
+        rc = self._step(*self._refs, _stream(stream))
+        if rc != OK:
+            raise OpsError(rc, "bo_adamw_step")
+
+    def grad_norm(self, stream=None) -> torch.Tensor:
+        """The global norm of the gradients as they are now (`norm`), without a step."""
+        _check(_ops_lib.load().bo_adamw_norm(self._refs[0], self._args.max_norm, _stream(stream)),
+               "bo_adamw_norm")
+        return self.norm
+
+    def view(self, name: str, i: int) -> torch.Tensor:
+        """Tensor i's part of a state arena, in its shape (scales: one per block)."""
+        b = self.first_blocks[i]
+        if name.endswith("_scale"):
+            return self.state[name][b:b + -(-self.ns[i] // BLOCK_ELEMS)]
+        return self.state[name][b * BLOCK_ELEMS:b * BLOCK_ELEMS + self.ns[i]].view(self.shapes[i])
+
+    def moments(self, dtype: torch.dtype = torch.float32, stream=None):
+        """Both moments as values of `dtype`, laid out as the arenas.  With 32-bit states these
+        are the arenas themselves (dtype float32) or copies."""
+        if dtype not in _DTYPES:
+            raise TypeError("dtype must be bfloat16 or float32")
+        if self.state_bits == 32:
+            return self.state["m"].to(dtype), self.state["v"].to(dtype)
+        m = torch.empty(self.state["m"].numel(), dtype=dtype, device=self.plan.device)
+        v = torch.empty_like(m)
+        _check(_ops_lib.load().bo_adamw_moments(self._refs[0], _DTYPES[dtype], m.data_ptr(),
+                                                v.data_ptr(), _stream(stream)), "bo_adamw_moments")
+        return m, v

@@ -144,6 +144,99 @@ BD_API int bo_adamw_norm(const bo_adamw* h, float max_norm, void* stream);
 BD_API int bo_adamw_moments(const bo_adamw* h, uint32_t dtype, void* d_m, void* d_v,
                             void* stream);
 
+/* ------------------------------------------------------------------- low-rank adapters
+ *
+ * Row t of a batch belongs to adapter a(t), or to none.  With the adapter's factors
+ * A (rank x hidden) and B (out x rank) and its scale s:
+ *   forward    low[t] = s A x[t]            y[t] += B low[t]
+ *   backward   dlow[t] = s B^T dy[t]        dx[t] += A^T dlow[t]
+ *              dA = sum over its rows of dlow[t] x[t]^T
+ *              dB = sum over its rows of dy[t] low[t]^T
+ * y is the output of the projection that all rows share (and dx that projection's part of the
+ * gradient): both are updated in place, so adapter rows cost one read and one write of them.
+ * Rows without an adapter are neither read nor written.  Sums are held in FP32; low and dlow
+ * are rounded to BF16, the type of the tensor cores' operands, once per row and rank (an error
+ * of at most 2^-8 of each term, that of a model that stores its low-rank activations); every output is
+ * rounded once.  Results do not depend on which other rows are in the batch's tiles, and the
+ * order of every sum is fixed for given sizes.
+ *
+ * x, y, dy, dx: rows of BF16 with a row stride in elements; any sizes and strides (16-byte
+ * aligned rows, with hidden, out and ranks multiples of 8, take wide accesses). */
+
+#define BO_ADAPTER_MAX_RANK 128u
+#define BO_ADAPTER_MAX_COUNT 65535u   /* adapters of a set */
+#define BO_ADAPTER_MAX_WIDTH (1u << 24)
+#define BO_ADAPTER_MAX_ROWS (1u << 30)
+
+/* One adapter.  Row strides in elements: at least hidden for down, at least rank for up.  The
+ * gradients may be NULL where no backward pass is made. */
+typedef struct bo_adapter {
+  const uint16_t* d_down;  /* A: rank x hidden */
+  const uint16_t* d_up;    /* B: out x rank */
+  uint64_t ld_down, ld_up;
+  void* d_grad_down;       /* dA, dB: as A and B, of grad_dtype */
+  void* d_grad_up;
+  uint64_t ld_grad_down, ld_grad_up;
+  uint32_t rank;           /* 1 to BO_ADAPTER_MAX_RANK */
+  float scale;
+} bo_adapter;
+
+/* A set of adapters of one projection, laid out by bo_adapter_set_init. */
+typedef struct bo_adapter_set {
+  const void* d_table;
+  uint32_t k, hidden, out;
+  uint32_t rank;           /* columns of low: the largest rank, as 16, 32, 64 or 128 */
+  uint32_t grad_dtype, has_grads;
+} bo_adapter_set;
+
+/* The rows of a batch grouped by adapter, laid out by bo_adapter_rows_init. */
+typedef struct bo_adapter_rows {
+  const int32_t* d_perm;     /* rows, grouped */
+  const int32_t* d_offsets;  /* adapter a has d_perm[d_offsets[a] .. d_offsets[a + 1]) */
+  const void* d_tiles[2];    /* tiles of at most 16 and 64 rows of one adapter */
+  const int32_t* d_ntiles;   /* how many of each */
+  uint32_t rows, k;
+} bo_adapter_rows;
+
+/* Bytes of device memory (256-byte aligned) for a set of k adapters. */
+BD_API uint64_t bo_adapter_set_size(uint32_t k);
+
+/* Lays out the table of k adapters (read during the call only).  The factors and gradients
+ * must stay where they are; their values may change between calls. */
+BD_API int bo_adapter_set_init(const bo_adapter* h_items, uint32_t k, uint32_t hidden,
+                               uint32_t out, uint32_t grad_dtype, void* d_set,
+                               uint64_t set_bytes, bo_adapter_set* h_out, void* stream);
+
+/* Bytes of device memory (256-byte aligned) to group `rows` rows over k adapters. */
+BD_API uint64_t bo_adapter_rows_size(uint32_t rows, uint32_t k);
+
+/* Groups rows by adapter on the device: d_index[t] is row t's adapter, -1 for none.  An index
+ * outside -1 .. k - 1 sets *d_status (optional) to BD_ERR_INVALID_ARG, else BD_OK, and counts
+ * as none.  One grouping serves every projection of a model step.  The call reads d_index in
+ * stream order; calling it again on the same memory regroups for new values. */
+BD_API int bo_adapter_rows_init(const int32_t* d_index, uint32_t rows, uint32_t k, void* d_rows,
+                                uint64_t rows_bytes, bo_adapter_rows* h_out, int32_t* d_status,
+                                void* stream);
+
+/* y += the adapters' products, in place.  d_low (optional): low for the backward pass, `rows`
+ * rows of set->rank columns, 16-byte aligned; columns past an adapter's rank are written as 0,
+ * rows without an adapter not at all. */
+BD_API int bo_adapter_forward(const bo_adapter_set* set, const bo_adapter_rows* rows,
+                              const uint16_t* d_x, uint64_t ldx, uint16_t* d_y, uint64_t ldy,
+                              uint16_t* d_low, void* stream);
+
+/* Bytes of workspace (256-byte aligned) that bo_adapter_backward takes. */
+BD_API uint64_t bo_adapter_backward_workspace_size(const bo_adapter_set* set, uint32_t rows);
+
+/* dx += (in place; d_dx may be NULL) and, when the set has gradients, dA and dB of every
+ * adapter (0 for one without rows), written over what is there or, with accumulate, added to
+ * it.  d_low is the forward pass's. */
+BD_API int bo_adapter_backward(const bo_adapter_set* set, const bo_adapter_rows* rows,
+                               const uint16_t* d_x, uint64_t ldx, const uint16_t* d_dy,
+                               uint64_t lddy, const uint16_t* d_low, uint16_t* d_dx,
+                               uint64_t lddx, int32_t accumulate, void* d_ws, uint64_t ws_bytes,
+                               void* stream);
+
 /* Library utility: static description of a status, bd_status included. */
 BD_API const char* bo_status_string(int code);
 

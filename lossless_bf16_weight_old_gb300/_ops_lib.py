@@ -34,6 +34,22 @@ class AdamWStepArgs(ctypes.Structure):
                 ("max_norm", c_f), ("seed", c_u64)]
 
 
+class Adapter(ctypes.Structure):
+    _fields_ = [("d_down", c_p), ("d_up", c_p), ("ld_down", c_u64), ("ld_up", c_u64),
+                ("d_grad_down", c_p), ("d_grad_up", c_p), ("ld_grad_down", c_u64),
+                ("ld_grad_up", c_u64), ("rank", c_u32), ("scale", c_f)]
+
+
+class AdapterSet(ctypes.Structure):
+    _fields_ = [("d_table", c_p), ("k", c_u32), ("hidden", c_u32), ("out", c_u32),
+                ("rank", c_u32), ("grad_dtype", c_u32), ("has_grads", c_u32)]
+
+
+class AdapterRows(ctypes.Structure):
+    _fields_ = [("d_perm", c_p), ("d_offsets", c_p), ("d_tiles", c_p * 2), ("d_ntiles", c_p),
+                ("rows", c_u32), ("k", c_u32)]
+
+
 # name -> (restype, argtypes); must match include/ops/bf16ops.h
 SIGNATURES = {
     "bo_adamw_plan_size": (c_u64, [c_p, c_u32]),
@@ -42,6 +58,14 @@ SIGNATURES = {
     "bo_adamw_step": (c_int, [c_p, c_p, c_p]),
     "bo_adamw_norm": (c_int, [c_p, c_f, c_p]),
     "bo_adamw_moments": (c_int, [c_p, c_u32, c_p, c_p, c_p]),
+    "bo_adapter_set_size": (c_u64, [c_u32]),
+    "bo_adapter_set_init": (c_int, [c_p, c_u32, c_u32, c_u32, c_u32, c_p, c_u64, c_p, c_p]),
+    "bo_adapter_rows_size": (c_u64, [c_u32, c_u32]),
+    "bo_adapter_rows_init": (c_int, [c_p, c_u32, c_u32, c_p, c_u64, c_p, c_p, c_p]),
+    "bo_adapter_forward": (c_int, [c_p, c_p, c_p, c_u64, c_p, c_u64, c_p, c_p]),
+    "bo_adapter_backward_workspace_size": (c_u64, [c_p, c_u32]),
+    "bo_adapter_backward": (c_int, [c_p, c_p, c_p, c_u64, c_p, c_u64, c_p, c_p, c_u64, c_int, c_p,
+                                    c_u64, c_p]),
     "bo_status_string": (ctypes.c_char_p, [c_int]),
 }
 

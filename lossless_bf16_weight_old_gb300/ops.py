@@ -2,6 +2,8 @@
 
     AdamWBatch        one AdamW step over many tensors, moments in 32 or in 8 bits: what makes
                       the new weights that CompressBatch encodes
+    AdapterSet, AdapterRows, adapter_forward, adapter_backward
+                      low-rank adapters of many requests beside a shared projection
 
 Every computation runs in libbf16ops' CUDA kernels; this module checks and marshals arguments
 and allocates device buffers with PyTorch.  The names are re-exported by the package.
@@ -21,7 +23,7 @@ BLOCK_ELEMS = 256
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 _U64 = (1 << 64) - 1
 
-__all__ = ["AdamWBatch", "SKIPPED_NONFINITE", "OpsError", "ops_status_name"]
+__all__ = ["AdamWBatch", "AdapterSet", "AdapterRows", "adapter_forward", "adapter_backward", "SKIPPED_NONFINITE", "OpsError", "ops_status_name"]
 
 
 class OpsError(RuntimeError):
@@ -212,3 +214,170 @@ class AdamWBatch:
         _check(_ops_lib.load().bo_adamw_moments(self._refs[0], _DTYPES[dtype], m.data_ptr(),
                                                 v.data_ptr(), _stream(stream)), "bo_adamw_moments")
         return m, v
+
+
+def _matrix(t: torch.Tensor, name: str, rows: int | None, width: int, device,
+            dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """Checks a matrix whose rows are contiguous (any row stride)."""
+    if t.dim() != 2 or t.dtype != dtype or not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a 2-dimensional {dtype} tensor on {device}")
+    if t.shape[1] != width or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"({'any' if rows is None else rows}, {width})")
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < width):
+        raise ValueError(f"{name}'s rows must be contiguous and may not overlap")
+    return t
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride in elements (of a single row: its width)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+class AdapterSet:
+    """The adapters of one projection, read where they lie.
+
+    downs, ups   factors: downs[i] is [rank_i, hidden], ups[i] is [out, rank_i], bfloat16, rows
+                 contiguous; ranks from 1 to 128 may differ
+    scales       one number per adapter (usually alpha / rank), or one for all
+    d_downs, d_ups   (for a backward pass) their gradients, all bfloat16 or all float32
+
+    The tensors must stay where they are for the life of the set; their values may change at any
+    time (an optimizer step, a delta applied in place)."""
+
+    def __init__(self, downs: Sequence[torch.Tensor], ups: Sequence[torch.Tensor],
+                 scales: float | Sequence[float] = 1.0, *,
+                 d_downs: Sequence[torch.Tensor] | None = None,
+                 d_ups: Sequence[torch.Tensor] | None = None, stream=None):
+        k = len(downs)
+        if k == 0 or len(ups) != k:
+            raise ValueError("downs and ups must hold the same number of adapters, at least one")
+        scales = [float(scales)] * k if isinstance(scales, (int, float)) else [float(s) for s in scales]
+        if len(scales) != k:
+            raise ValueError("scales must be one number or one per adapter")
+        if (d_downs is None) != (d_ups is None):
+            raise ValueError("d_downs and d_ups come together")
+        dev, hidden, out = downs[0].device, downs[0].shape[-1], ups[0].shape[0]
+        gtype = torch.bfloat16
+        if d_downs is not None:
+            if len(d_downs) != k or len(d_ups) != k:
+                raise ValueError("one gradient per factor")
+            gtype = d_downs[0].dtype
+            if gtype not in _DTYPES:
+                raise TypeError(f"gradients must be bfloat16 or float32, got {gtype}")
+        items = (_ops_lib.Adapter * k)()
+        for i in range(k):
+            r = downs[i].shape[0]
+            if not 1 <= r <= 128:
+                raise ValueError(f"adapter {i} has rank {r}; ranks are 1 to 128")
+            _matrix(downs[i], f"downs[{i}]", r, hidden, dev)
+            _matrix(ups[i], f"ups[{i}]", out, r, dev)
+            it = items[i]
+            it.d_down, it.ld_down = downs[i].data_ptr(), _ld(downs[i])
+            it.d_up, it.ld_up = ups[i].data_ptr(), _ld(ups[i])
+            it.rank, it.scale = r, scales[i]
+            if d_downs is not None:
+                _matrix(d_downs[i], f"d_downs[{i}]", r, hidden, dev, gtype)
+                _matrix(d_ups[i], f"d_ups[{i}]", out, r, dev, gtype)
+                it.d_grad_down, it.ld_grad_down = d_downs[i].data_ptr(), _ld(d_downs[i])
+                it.d_grad_up, it.ld_grad_up = d_ups[i].data_ptr(), _ld(d_ups[i])
+        lib = _ops_lib.load()
+        self.table = torch.empty(max(256, int(lib.bo_adapter_set_size(k))), dtype=torch.uint8, device=dev)
+        self.handle = _ops_lib.AdapterSet()
+        _check(lib.bo_adapter_set_init(items, k, hidden, out, _DTYPES[gtype], self.table.data_ptr(),
+                                       self.table.numel(), ctypes.byref(self.handle), _stream(stream)),
+               "bo_adapter_set_init")
+        self.k, self.hidden, self.out, self.device = k, hidden, out, dev
+        #: columns of `low`, the activations that the forward pass keeps for the backward
+        self.rank = int(self.handle.rank)
+        self._ref = ctypes.byref(self.handle)
+        self._keep = (list(downs), list(ups), d_downs, d_ups)
+
+
+class AdapterRows:
+    """The rows of a batch grouped by adapter, on the device: index[t] (int32) is the adapter of
+    row t, -1 for none.  One grouping serves every projection of a model step; `update` regroups
+    for new values of as many rows.  `status` (int32[1]) is ERR_INVALID_ARG when an index lies
+    outside -1 .. k - 1 (such rows count as rows without an adapter)."""
+
+    def __init__(self, index: torch.Tensor, k: int, *, stream=None):
+        if index.dtype != torch.int32 or index.dim() != 1 or not index.is_cuda:
+            raise ValueError("index must be a 1-dimensional int32 CUDA tensor")
+        lib = _ops_lib.load()
+        self.rows, self.k, self.device = index.numel(), int(k), index.device
+        need = int(lib.bo_adapter_rows_size(self.rows, self.k)) if self.k > 0 else 0
+        if need == 0:
+            raise ValueError("k must lie in 1 .. 65535 and the rows be fewer than 2**30")
+        self.memory = torch.empty(need, dtype=torch.uint8, device=index.device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=index.device)
+        self.handle = _ops_lib.AdapterRows()
+        self._ref = ctypes.byref(self.handle)
+        self.update(index, stream)
+
+    def update(self, index: torch.Tensor, stream=None) -> None:
+        if index.dtype != torch.int32 or index.numel() != self.rows or index.device != self.device \
+                or not index.is_contiguous():
+            raise ValueError(f"index must be a contiguous int32 tensor of {self.rows} elements on "
+                             f"{self.device}")
+        self.index = index
+        _check(_ops_lib.load().bo_adapter_rows_init(
+            index.data_ptr(), self.rows, self.k, self.memory.data_ptr(), self.memory.numel(),
+            self._ref, self.status.data_ptr(), _stream(stream)), "bo_adapter_rows_init")
+
+
+def _pair(adapters: AdapterSet, rows: AdapterRows) -> None:
+    if rows.k != adapters.k:
+        raise ValueError(f"rows are grouped over {rows.k} adapters, the set has {adapters.k}")
+
+
+def _low(low: torch.Tensor, adapters: AdapterSet, rows: AdapterRows) -> int:
+    if low.shape != (rows.rows, adapters.rank) or low.dtype != torch.bfloat16 or \
+            not low.is_contiguous() or low.device != adapters.device:
+        raise ValueError(f"low must be a contiguous bfloat16 tensor of shape "
+                         f"({rows.rows}, {adapters.rank}) on {adapters.device}")
+    return low.data_ptr()
+
+
+def adapter_forward(x: torch.Tensor, y: torch.Tensor, adapters: AdapterSet, rows: AdapterRows, *,
+                    low: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[t] += scale * up @ (down @ x[t]) with the adapter of row t, in place; y is the shared
+    projection's output.  x [rows, hidden] and y [rows, out] are bfloat16 with contiguous rows.
+    low (optional, bfloat16 [rows, adapters.rank]) receives what adapter_backward needs.  Rows
+    without an adapter are left alone.  Returns y."""
+    _pair(adapters, rows)
+    _matrix(x, "x", rows.rows, adapters.hidden, adapters.device)
+    _matrix(y, "y", rows.rows, adapters.out, adapters.device)
+    rc = _ops_lib.load().bo_adapter_forward(
+        adapters._ref, rows._ref, x.data_ptr(), _ld(x), y.data_ptr(), _ld(y),
+        None if low is None else _low(low, adapters, rows), _stream(stream))
+    if rc != OK:
+        raise OpsError(rc, "bo_adapter_forward")
+    return y
+
+
+def adapter_backward(x: torch.Tensor, dy: torch.Tensor, low: torch.Tensor,
+                     dx: torch.Tensor | None, adapters: AdapterSet, rows: AdapterRows, *,
+                     accumulate: bool = False, workspace: torch.Tensor | None = None,
+                     stream=None) -> None:
+    """The backward pass of adapter_forward: dx[t] += the adapter's part (dx holds the shared
+    projection's part; None: not wanted), in place, and the gradients given to the set are
+    written, or with accumulate=True added to.  low is the forward pass's."""
+    _pair(adapters, rows)
+    _matrix(x, "x", rows.rows, adapters.hidden, adapters.device)
+    _matrix(dy, "dy", rows.rows, adapters.out, adapters.device)
+    if dx is not None:
+        _matrix(dx, "dx", rows.rows, adapters.hidden, adapters.device)
+    lib = _ops_lib.load()
+    need = int(lib.bo_adapter_backward_workspace_size(adapters._ref, rows.rows))
+    ws = workspace
+    if ws is None:
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=adapters.device)
+        if stream is not None:
+            ws.record_stream(stream)   # (the allocator may not hand it out while it is in use)
+    rc = lib.bo_adapter_backward(
+        adapters._ref, rows._ref, x.data_ptr(), _ld(x), dy.data_ptr(), _ld(dy),
+        _low(low, adapters, rows), None if dx is None else dx.data_ptr(),
+        0 if dx is None else _ld(dx), int(accumulate), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _stream(stream))
+    if rc != OK:
+        raise OpsError(rc, "bo_adapter_backward")

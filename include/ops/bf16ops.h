@@ -186,15 +186,17 @@ typedef struct bo_adapter_set {
   const void* d_table;
   uint32_t k, hidden, out;
   uint32_t rank;           /* columns of low: the largest rank, as 16, 32, 64 or 128 */
-  uint32_t grad_dtype, has_grads;
+  uint32_t grad_dtype, has_grads, wide;
 } bo_adapter_set;
 
 /* The rows of a batch grouped by adapter, laid out by bo_adapter_rows_init. */
 typedef struct bo_adapter_rows {
   const int32_t* d_perm;     /* rows, grouped */
   const int32_t* d_offsets;  /* adapter a has d_perm[d_offsets[a] .. d_offsets[a + 1]) */
-  const void* d_tiles[2];    /* tiles of at most 16 and 64 rows of one adapter */
+  const int32_t* d_blocks;   /* blocks of 64 rows (at least one) of the adapters before */
+  const void* d_tiles[3];    /* tiles of at most 16, 64 and 128 rows of one adapter */
   const int32_t* d_ntiles;   /* how many of each */
+  int32_t* d_status;         /* as given; also BD_ERR_CUDA from a call whose waits ran out */
   uint32_t rows, k;
 } bo_adapter_rows;
 
@@ -218,12 +220,16 @@ BD_API int bo_adapter_rows_init(const int32_t* d_index, uint32_t rows, uint32_t 
                                 uint64_t rows_bytes, bo_adapter_rows* h_out, int32_t* d_status,
                                 void* stream);
 
-/* y += the adapters' products, in place.  d_low (optional): low for the backward pass, `rows`
- * rows of set->rank columns, 16-byte aligned; columns past an adapter's rank are written as 0,
- * rows without an adapter not at all. */
+/* y += the adapters' products, in place.  d_low receives low, which the backward pass takes:
+ * `rows` rows of set->rank columns, 16-byte aligned; columns past an adapter's rank are written
+ * as 0, rows without an adapter not at all.  It may be NULL below bo_adapter_low_rows(set) rows;
+ * from there on the call needs it as its workspace. */
 BD_API int bo_adapter_forward(const bo_adapter_set* set, const bo_adapter_rows* rows,
                               const uint16_t* d_x, uint64_t ldx, uint16_t* d_y, uint64_t ldy,
                               uint16_t* d_low, void* stream);
+
+/* The number of rows from which bo_adapter_forward needs d_low (0: not a set). */
+BD_API uint32_t bo_adapter_low_rows(const bo_adapter_set* set);
 
 /* Bytes of workspace (256-byte aligned) that bo_adapter_backward takes. */
 BD_API uint64_t bo_adapter_backward_workspace_size(const bo_adapter_set* set, uint32_t rows);

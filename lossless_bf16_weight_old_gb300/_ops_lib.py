@@ -42,11 +42,13 @@ class Adapter(ctypes.Structure):
 
 class AdapterSet(ctypes.Structure):
     _fields_ = [("d_table", c_p), ("k", c_u32), ("hidden", c_u32), ("out", c_u32),
-                ("rank", c_u32), ("grad_dtype", c_u32), ("has_grads", c_u32)]
+                ("rank", c_u32), ("grad_dtype", c_u32), ("has_grads", c_u32),
+                ("wide", c_u32)]
 
 
 class AdapterRows(ctypes.Structure):
-    _fields_ = [("d_perm", c_p), ("d_offsets", c_p), ("d_tiles", c_p * 2), ("d_ntiles", c_p),
+    _fields_ = [("d_perm", c_p), ("d_offsets", c_p), ("d_blocks", c_p), ("d_tiles", c_p * 3), ("d_ntiles", c_p),
+                ("d_status", c_p),
                 ("rows", c_u32), ("k", c_u32)]
 
 
@@ -63,6 +65,7 @@ SIGNATURES = {
     "bo_adapter_rows_size": (c_u64, [c_u32, c_u32]),
     "bo_adapter_rows_init": (c_int, [c_p, c_u32, c_u32, c_p, c_u64, c_p, c_p, c_p]),
     "bo_adapter_forward": (c_int, [c_p, c_p, c_p, c_u64, c_p, c_u64, c_p, c_p]),
+    "bo_adapter_low_rows": (c_u32, [c_p]),
     "bo_adapter_backward_workspace_size": (c_u64, [c_p, c_u32]),
     "bo_adapter_backward": (c_int, [c_p, c_p, c_p, c_u64, c_p, c_u64, c_p, c_p, c_u64, c_int, c_p,
                                     c_u64, c_p]),

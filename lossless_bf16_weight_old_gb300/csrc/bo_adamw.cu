@@ -143,6 +143,7 @@ struct Rates {      // per launch
   float b1, c1, b2, c2;      // beta and 1 - beta
   float inv_bc1, inv_bc2;    // 1 / (1 - beta^t)
   float lr, eps, coef;
+  float rate;                // -lr / (1 - beta1^t)
 };
 
 struct StepParams {
@@ -182,6 +183,7 @@ __device__ __forceinline__ bool begin_step(const StepParams& P, Rates& R, uint64
   R.inv_bc2 = sh[1];
   R.lr = sh[2];
   R.coef = sh[3];
+  R.rate = -(R.lr * sh[0]);
   key = sh_key;
   return sh[3] >= 0.f;
 }
@@ -197,9 +199,16 @@ __device__ __forceinline__ void finish_step(const StepParams& P, bool taken) {
   }
 }
 
-__device__ __forceinline__ float sqrt_fast(float x) {   // within 2^-22 or so of the root
+// Within 2^-22 or so of the root and the reciprocal; denormal numbers count as 0, which a root
+// beside eps and a ratio of two moments do not notice.
+__device__ __forceinline__ float sqrt_fast(float x) {
   float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -211,8 +220,8 @@ __device__ __forceinline__ void update(const Rates& R, float keep, float g, floa
   m = fmaf(R.b1, m, R.c1 * g);
   v = fmaf(R.b2, v, R.c2 * g * g);
   const float den = sqrt_fast(v * R.inv_bc2) + R.eps;
-  const float q = m == 0.f ? 0.f : __fdividef(m * R.inv_bc1, den);   // (eps = 0: 0 / 0 is 0)
-  p = fmaf(p, keep, -R.lr * q);
+  const float q = m == 0.f ? 0.f : m * rcp_fast(den);   // (eps = 0: 0 / 0 is 0)
+  p = fmaf(p, keep, R.rate * q);
 }
 
 // Eight new weights from p: the master and its rounding, or the weights alone.
@@ -257,16 +266,22 @@ __device__ __forceinline__ void store_weight1(const Chunk& c, uint32_t i, float*
 // ------------------------------------------------------------------------ 32-bit moments
 template <int WK, bool GF32>
 __global__ void __launch_bounds__(kThreads, 4) k_step32(const StepParams P) {
+  after_previous();
   Rates R;
   uint64_t key;
+  // Backwards after a norm: it has left the last gradients in L2.
+  const Chunk* const table = P.clip ? P.table + P.chunks - 1 : P.table;
+  const int64_t dir = P.clip ? -1 : 1;
+  Chunk next;
+  if (blockIdx.x < P.chunks) next = load_chunk(table + dir * (int64_t)blockIdx.x);
   const bool taken = begin_step(P, R, key);
   if (taken) {
     float* const am = static_cast<float*>(P.st.d_m);
     float* const av = static_cast<float*>(P.st.d_v);
-    Chunk next = load_chunk(P.table + blockIdx.x);
     for (uint64_t ci = blockIdx.x; ci < P.chunks; ci += gridDim.x) {
       const Chunk c = next;
-      if (ci + gridDim.x < P.chunks) next = load_chunk(P.table + ci + gridDim.x);
+      if (ci + gridDim.x < P.chunks)
+        next = load_chunk(table + dir * (int64_t)(ci + gridDim.x));
       const uint32_t i = threadIdx.x * 8;
       const float keep = 1.f - R.lr * c.wd;
       const uint64_t e = c.e0 + i;
@@ -310,62 +325,81 @@ __global__ void __launch_bounds__(kThreads, 4) k_step32(const StepParams P) {
 }
 
 // ------------------------------------------------------------------------- 8-bit moments
+// Integers and floats meet in the low bits of a float near 2^23 or 1.5 2^23: the converting
+// instructions run at an eighth of the rate of an addition, and there would be five an element.
+__device__ __forceinline__ float byte_u(uint32_t w, uint32_t j) {   // byte j as a float
+  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650 | j)) - 8388608.f;
+}
+__device__ __forceinline__ float byte_s(uint32_t w80, uint32_t j) {   // signed; w80 = w ^ 0x80808080
+  return __uint_as_float(__byte_perm(w80, 0x4B000000u, 0x7650 | j)) - 8388736.f;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) x = max_nan(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
-  return x;
+  float r;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 // An infinite scale would read as infinity or NaN by the code: NaN throughout marks the block.
 __device__ __forceinline__ float finite_or_nan(float x) {
   return isfinite(x) ? x : __int_as_float(0x7FFFFFFF);
 }
-// 1 / scale, taken at a power of two that keeps it a normal number: x / scale = x * pre * inv.
-__device__ __forceinline__ void inverse_scale(float scale, float& pre, float& inv) {
-  pre = scale < 0x1p-60f ? 0x1p80f : scale > 0x1p60f ? 0x1p-60f : 1.f;
-  inv = scale > 0.f ? 1.f / (scale * pre) : 0.f;   // (a NaN scale: codes 0, read as 0 * NaN)
+// 1 / scale; a scale next to the ends of the FP32 range comes with a power of two `pre` that
+// brings it and its block's values into the middle.
+__device__ __forceinline__ float inverse_scale(float scale, float& pre) {
+  pre = scale < 0x1p-100f ? 0x1p80f : scale > 0x1p100f ? 0x1p-80f : 1.f;
+  return scale > 0.f ? 1.f / (scale * pre) : 0.f;   // (under a NaN scale every code reads NaN)
 }
-__device__ __forceinline__ float m_value(float c) { return c * fabsf(c) * (1.f / 16129.f); }
-__device__ __forceinline__ float v_value(float c) {   // (c / 255)^4; c^2 is exact
+constexpr float kMUnit = 1.f / 16129.f;                        // 127^-2
+constexpr float kVUnit = (float)(1.0 / (65025.0 * 65025.0));   // 255^-4
+__device__ __forceinline__ float v_units(float c) {   // c^4; c^2 is exact
   const float c2 = c * c;
-  return c2 * c2 * (float)(1.0 / (65025.0 * 65025.0));
+  return c2 * c2;
 }
-__device__ __forceinline__ int32_t m_code(float m, float pre, float inv) {
-  const float c = sqrt_fast(fabsf(m) * pre * inv) * 127.f;
-  const int32_t k = __float2int_rn(c);
-  return m < 0.f ? -k : k;
+__device__ __forceinline__ float m_value(float c) { return c * fabsf(c) * kMUnit; }
+__device__ __forceinline__ float v_value(float c) { return v_units(c) * kVUnit; }
+// the code in the low byte
+__device__ __forceinline__ uint32_t m_code(float m, float inv) {
+  const float c = sqrt_fast(fabsf(m) * inv);
+  return __float_as_uint(fmaf(copysignf(c, m), 127.f, 12582912.f));
 }
 // Of the two codes whose values enclose v / scale, the upper one with the chance that makes the
 // expected value v / scale; never 0 for v > 0 (a root of 0 under a moment that is not 0 would
-// make a step without bound).
-__device__ __forceinline__ uint32_t v_code(float v, float pre, float inv, uint32_t r) {
-  const float x = v * pre * inv;
-  const float low = fminf(floorf(sqrt_fast(sqrt_fast(x)) * 255.f), 254.f);
-  const float a = v_value(low), b = v_value(low + 1.f);
-  const float u = (float)(r >> 16) * (1.f / 65536.f);
-  const float c = low + (u * (b - a) < x - a ? 1.f : 0.f);
-  return v > 0.f ? max((uint32_t)c, 1u) : 0u;
+// make a step without bound).  inv_units: 255^4 / scale.
+__device__ __forceinline__ uint32_t v_code(float v, float inv_units, uint32_t r) {
+  const float x = v * inv_units;
+  // floor of x's fourth root, by rounding down at 2^23
+  const float low = fminf(__fadd_rd(sqrt_fast(sqrt_fast(x)), 8388608.f) - 8388608.f, 254.f);
+  const float a = v_units(low), d = v_units(low + 1.f) - a;
+  const float u1 = __uint_as_float(0x3F800000u | (r >> 16) << 7);   // 1 + u
+  const float c = fmaf(u1, d, -d) < x - a ? low + 1.f : low;
+  return __float_as_uint((v > 0.f ? fmaxf(c, 1.f) : 0.f) + 8388608.f);
 }
 
 // One warp per block of 256: its eight elements a lane stay in registers while the block's
 // maxima are found, so each byte is read and written once.
 template <int WK, bool GF32>
 __global__ void __launch_bounds__(kThreads, 4) k_step8(const StepParams P) {
+  after_previous();
   Rates R;
   uint64_t key;
+  // Backwards after a norm: it has left the last gradients in L2.
+  const Chunk* const table = P.clip ? P.table + P.chunks - 1 : P.table;
+  const int64_t dir = P.clip ? -1 : 1;
+  Chunk next;
+  if (blockIdx.x < P.chunks) next = load_chunk(table + dir * (int64_t)blockIdx.x);
   const bool taken = begin_step(P, R, key);
   if (taken) {
     uint8_t* const am = static_cast<uint8_t*>(P.st.d_m);
     uint8_t* const av = static_cast<uint8_t*>(P.st.d_v);
     const uint32_t lane = threadIdx.x & 31;
-    Chunk next = load_chunk(P.table + blockIdx.x);
     for (uint64_t ci = blockIdx.x; ci < P.chunks; ci += gridDim.x) {
       const Chunk c = next;
-      if (ci + gridDim.x < P.chunks) next = load_chunk(P.table + ci + gridDim.x);
+      if (ci + gridDim.x < P.chunks)
+        next = load_chunk(table + dir * (int64_t)(ci + gridDim.x));
       const uint32_t i = threadIdx.x * 8;
       if ((threadIdx.x & ~31u) * 8 >= c.count) continue;   // (the whole warp)
       const float keep = 1.f - R.lr * c.wd;
@@ -396,9 +430,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_step8(const StepParams P) {
       float mm = 0.f, mv = 0.f;
 #pragma unroll
       for (uint32_t j = 0; j < 8; j++) {
-        const uint32_t wm = j < 4 ? cm.x : cm.y, wv = j < 4 ? cv.x : cv.y;
-        m[j] = m_value((float)(int8_t)(wm >> (8 * (j & 3)))) * sm;
-        v[j] = v_value((float)(uint8_t)(wv >> (8 * (j & 3)))) * sv;
+        m[j] = m_value(byte_s((j < 4 ? cm.x : cm.y) ^ 0x80808080u, j & 3)) * sm;
+        v[j] = v_value(byte_u(j < 4 ? cv.x : cv.y, j & 3)) * sv;
         if (j >= cnt) m[j] = v[j] = 0.f;   // padding behind the tensor's end
         update(R, keep, g[j], m[j], v[j], p[j]);
         mm = max_nan(mm, fabsf(m[j]));
@@ -406,18 +439,28 @@ __global__ void __launch_bounds__(kThreads, 4) k_step8(const StepParams P) {
       }
       mm = finite_or_nan(warp_max(mm));
       mv = finite_or_nan(warp_max(mv));
-      float mpre, minv, vpre, vinv;
-      inverse_scale(mm, mpre, minv);
-      inverse_scale(mv, vpre, vinv);
+      float mpre, vpre;
+      const float minv = inverse_scale(mm, mpre), vinv = inverse_scale(mv, vpre) * 4228250625.f;
+      if (mpre != 1.f || vpre != 1.f) {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; j++) {
+          m[j] *= mpre;
+          v[j] *= vpre;
+        }
+      }
       uint32_t r[8];
       noise8(key, e, r);
-      uint2 qm = make_uint2(0, 0), qv = make_uint2(0, 0);
+      uint32_t a[8], b[8];
 #pragma unroll
       for (uint32_t j = 0; j < 8; j++) {
-        const uint32_t a = ((uint32_t)m_code(m[j], mpre, minv) & 0xFFu) << (8 * (j & 3));
-        const uint32_t b = v_code(v[j], vpre, vinv, r[j]) << (8 * (j & 3));
-        if (j < 4) { qm.x |= a; qv.x |= b; } else { qm.y |= a; qv.y |= b; }
+        a[j] = m_code(m[j], minv);
+        b[j] = v_code(v[j], vinv, r[j]);
       }
+      auto low_bytes = [](const uint32_t* w) {
+        return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+      };
+      const uint2 qm = make_uint2(low_bytes(a), low_bytes(a + 4));
+      const uint2 qv = make_uint2(low_bytes(b), low_bytes(b + 4));
       *reinterpret_cast<uint2*>(am + e) = qm;
       *reinterpret_cast<uint2*>(av + e) = qv;
       if (lane == 0) {
@@ -438,29 +481,41 @@ __global__ void __launch_bounds__(kThreads, 4) k_step8(const StepParams P) {
   finish_step(P, taken);
 }
 
-// Codes to values, one lane per eight elements of the arenas.
-template <bool F32, bool V>
-__global__ void __launch_bounds__(kThreads) k_moments(const uint8_t* __restrict__ codes,
-                                                       const float* __restrict__ scales,
-                                                       uint64_t blocks, void* __restrict__ out) {
+// Codes to values, one lane per eight elements of the arenas; either output may be missing.
+template <bool F32>
+__device__ __forceinline__ void put8(void* out, uint64_t t, const float (&x)[8]) {
+  if (F32) {
+    float4* o = static_cast<float4*>(out) + 2 * t;
+    o[0] = make_float4(x[0], x[1], x[2], x[3]);
+    o[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    static_cast<uint4*>(out)[t] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                             pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  }
+}
+template <bool F32>
+__global__ void __launch_bounds__(kThreads) k_moments(const bo_adamw_state st,
+                                                       void* __restrict__ out_m,
+                                                       void* __restrict__ out_v) {
+  after_previous();
   const uint64_t stride = (uint64_t)gridDim.x * blockDim.x;
-  for (uint64_t t = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; t < blocks * 32; t += stride) {
-    const uint2 c = reinterpret_cast<const uint2*>(codes)[t];
-    const float s = scales[t >> 5];
+  for (uint64_t t = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; t < st.blocks * 32;
+       t += stride) {
     float x[8];
+    if (out_m) {
+      const uint2 c = static_cast<const uint2*>(st.d_m)[t];
+      const float s = st.d_m_scale[t >> 5];
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-      const uint32_t w = (j < 4 ? c.x : c.y) >> (8 * (j & 3));
-      x[j] = (V ? v_value((float)(uint8_t)w) : m_value((float)(int8_t)w)) * s;
+      for (int j = 0; j < 8; j++)
+        x[j] = m_value(byte_s((j < 4 ? c.x : c.y) ^ 0x80808080u, j & 3)) * s;
+      put8<F32>(out_m, t, x);
     }
-    if (F32) {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + 8 * t);
-      o[0] = make_float4(x[0], x[1], x[2], x[3]);
-      o[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-      reinterpret_cast<uint4*>(out)[t] =
-          make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                     pack_bf16(x[6], x[7]));
+    if (out_v) {
+      const uint2 c = static_cast<const uint2*>(st.d_v)[t];
+      const float s = st.d_v_scale[t >> 5];
+#pragma unroll
+      for (int j = 0; j < 8; j++) x[j] = v_value(byte_u(j < 4 ? c.x : c.y, j & 3)) * s;
+      put8<F32>(out_v, t, x);
     }
   }
 }
@@ -472,6 +527,7 @@ template <bool GF32>
 __global__ void __launch_bounds__(kThreads, 8) k_norm(const Chunk* __restrict__ table,
                                                       uint64_t chunks, double* __restrict__ part,
                                                       bo_adamw_control* ctl, float max_norm) {
+  after_previous();
   float s[8] = {};
   if (blockIdx.x < chunks) {
     Chunk next = load_chunk(table + blockIdx.x);
@@ -554,19 +610,13 @@ int launch_norm(const bo_adamw* h, float max_norm, int sms, cudaStream_t s) {
   const uint32_t most = (uint32_t)sms * 8 < kMaxGrid ? (uint32_t)sms * 8 : kMaxGrid;
   const uint32_t grid = (uint32_t)(want < most ? want : most);
   const Chunk* table = static_cast<const Chunk*>(h->d_chunks);
-  if (h->grad_dtype == BO_FP32)
-    k_norm<true><<<grid, kThreads, 0, s>>>(table, h->chunks, h->d_partials, h->d_control, max_norm);
-  else
-    k_norm<false><<<grid, kThreads, 0, s>>>(table, h->chunks, h->d_partials, h->d_control, max_norm);
-  return check(cudaGetLastError());
+  return check(launch(h->grad_dtype == BO_FP32 ? k_norm<true> : k_norm<false>, dim3(grid), kThreads,
+                      0, 1, s, table, h->chunks, h->d_partials, h->d_control, max_norm));
 }
 
 template <int WK, bool GF32>
-void launch_step(bool bits8, uint32_t grid, const StepParams& P, cudaStream_t s) {
-  if (bits8)
-    k_step8<WK, GF32><<<grid, kThreads, 0, s>>>(P);
-  else
-    k_step32<WK, GF32><<<grid, kThreads, 0, s>>>(P);
+cudaError_t launch_step(bool bits8, uint32_t grid, const StepParams& P, cudaStream_t s) {
+  return launch(bits8 ? k_step8<WK, GF32> : k_step32<WK, GF32>, dim3(grid), kThreads, 0, 1, s, P);
 }
 
 }  // namespace
@@ -734,15 +784,16 @@ int bo_adamw_step(const bo_adamw* h, const bo_adamw_step_args* a, void* stream) 
   const uint32_t most = (uint32_t)sms * 4;
   const uint32_t grid = (uint32_t)(want < most ? want : most);
   const bool b8 = h->state_bits == 8;
+  cudaError_t e;
   switch (h->weight_kind * 2 + h->grad_dtype) {
-    case BO_WEIGHT_MASTER * 2 + BO_BF16: launch_step<BO_WEIGHT_MASTER, false>(b8, grid, P, s); break;
-    case BO_WEIGHT_MASTER * 2 + BO_FP32: launch_step<BO_WEIGHT_MASTER, true>(b8, grid, P, s); break;
-    case BO_WEIGHT_BF16 * 2 + BO_BF16: launch_step<BO_WEIGHT_BF16, false>(b8, grid, P, s); break;
-    case BO_WEIGHT_BF16 * 2 + BO_FP32: launch_step<BO_WEIGHT_BF16, true>(b8, grid, P, s); break;
-    case BO_WEIGHT_FP32 * 2 + BO_BF16: launch_step<BO_WEIGHT_FP32, false>(b8, grid, P, s); break;
-    default: launch_step<BO_WEIGHT_FP32, true>(b8, grid, P, s); break;
+    case BO_WEIGHT_MASTER * 2 + BO_BF16: e = launch_step<BO_WEIGHT_MASTER, false>(b8, grid, P, s); break;
+    case BO_WEIGHT_MASTER * 2 + BO_FP32: e = launch_step<BO_WEIGHT_MASTER, true>(b8, grid, P, s); break;
+    case BO_WEIGHT_BF16 * 2 + BO_BF16: e = launch_step<BO_WEIGHT_BF16, false>(b8, grid, P, s); break;
+    case BO_WEIGHT_BF16 * 2 + BO_FP32: e = launch_step<BO_WEIGHT_BF16, true>(b8, grid, P, s); break;
+    case BO_WEIGHT_FP32 * 2 + BO_BF16: e = launch_step<BO_WEIGHT_FP32, false>(b8, grid, P, s); break;
+    default: e = launch_step<BO_WEIGHT_FP32, true>(b8, grid, P, s); break;
   }
-  return check(cudaGetLastError());
+  return check(e);
 }
 
 int bo_adamw_moments(const bo_adamw* h, uint32_t dtype, void* d_m, void* d_v, void* stream) {
@@ -755,22 +806,8 @@ int bo_adamw_moments(const bo_adamw* h, uint32_t dtype, void* d_m, void* d_v, vo
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const uint64_t want = (blocks * 32 + kThreads - 1) / kThreads;
   const uint32_t grid = (uint32_t)(want < (uint64_t)sms * 8 ? want : (uint64_t)sms * 8);
-  for (int v = 0; v < 2; v++) {
-    void* out = v ? d_v : d_m;
-    if (!out) continue;
-    const uint8_t* codes = static_cast<const uint8_t*>(v ? h->state.d_v : h->state.d_m);
-    const float* sc = v ? h->state.d_v_scale : h->state.d_m_scale;
-    if (dtype == BO_FP32) {
-      if (v) k_moments<true, true><<<grid, kThreads, 0, s>>>(codes, sc, blocks, out);
-      else k_moments<true, false><<<grid, kThreads, 0, s>>>(codes, sc, blocks, out);
-    } else {
-      if (v) k_moments<false, true><<<grid, kThreads, 0, s>>>(codes, sc, blocks, out);
-      else k_moments<false, false><<<grid, kThreads, 0, s>>>(codes, sc, blocks, out);
-    }
-    const int rc = check(cudaGetLastError());
-    if (rc) return rc;
-  }
-  return BD_OK;
+  return check(launch(dtype == BO_FP32 ? k_moments<true> : k_moments<false>, dim3(grid), kThreads, 0,
+                      1, s, h->state, d_m, d_v));
 }
 
 const char* bo_status_string(int code) {

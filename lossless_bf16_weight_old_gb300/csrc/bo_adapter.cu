@@ -3,16 +3,18 @@
 //
 // At ranks up to 128 a row's products take 2 r (hidden + out) operations for 2 hidden + 4 out
 // bytes: below 100 operations a byte against the 280 that the tensor cores and HBM balance at,
-// so every kernel here is built to stream x, y and the gradients once, through registers or a
-// ring of shared-memory tiles, with mma.sync on BF16 tiles beside it.
+// so every kernel here is built to stream x, y and the gradients once.
 //
 //   k_rows_*      group the rows of a batch by adapter (once per model step)
 //   k_apply16     one launch for low = s A x and y += B low over tiles of 16 rows: the serving
 //                 form, factors straight from global memory into the fragments
 //   k_apply64     the same over tiles of 64 rows, factors and x through shared memory
-//   k_transpose   the factors' transposes, with which the backward pass is the forward kernel:
+//   k_low         low alone (bo_adapter_tc.cu), and
+//   k_expand      y += B low alone: the two for many rows
+//   k_transpose   the factors' transposes, with which the backward pass is the forward kernels:
 //                 dlow = s B^T dy, dx += A^T dlow
-//   k_wgrad       dA and dB, sums over the rows of an adapter
+//   k_wgrad_tc    dA and dB, sums over the rows of an adapter (bo_adapter_tc.cu); k_wgrad the same
+//                 for rows and strides off the 16-byte boundary
 //
 // A tile of rows belongs to one adapter.  The thread blocks of a cluster share a tile: each takes
 // a slice of the first product's long sum, the slices' sums meet through distributed shared
@@ -22,7 +24,7 @@
 #include <memory>
 #include <new>
 
-#include "bo_internal.cuh"
+#include "bo_adapter.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -32,23 +34,6 @@ namespace {
 constexpr uint32_t kThreads = 256;   // eight warps
 constexpr uint32_t kMaxCluster = 8;
 
-struct alignas(16) DevAdapter {
-  const uint16_t* down;
-  const uint16_t* up;
-  uint64_t ld_down, ld_up;
-  void* gdown;
-  void* gup;
-  uint64_t ld_gdown, ld_gup;
-  uint32_t rank;
-  float scale;
-  uint32_t vec_down, vec_up;   // rows may be read 16 bytes at a time
-};
-static_assert(sizeof(DevAdapter) % 16 == 0, "uploaded in 16-byte words");
-
-struct Tile {
-  int32_t adapter, start, count, pad;
-};
-
 // ------------------------------------------------------------------------ grouping the rows
 // One block per adapter counts its rows, then one block per adapter places them in order: the
 // grouping is stable, so every later sum over an adapter's rows has one order.
@@ -56,6 +41,7 @@ __global__ void __launch_bounds__(kThreads) k_rows_count(const int32_t* __restri
                                                          uint32_t rows, uint32_t k,
                                                          int32_t* __restrict__ counts,
                                                          int32_t* __restrict__ status) {
+  after_previous();
   const int32_t a = (int32_t)blockIdx.x;
   int32_t c = 0, bad = 0;
   for (uint32_t t = threadIdx.x; t < rows; t += kThreads) {
@@ -92,33 +78,44 @@ __device__ __forceinline__ int32_t block_sum(int32_t v, int32_t* sh) {   // sh: 
 __global__ void __launch_bounds__(kThreads) k_rows_place(
     const int32_t* __restrict__ index, uint32_t rows, uint32_t k,
     const int32_t* __restrict__ counts, int32_t* __restrict__ perm, int32_t* __restrict__ offsets,
-    Tile* __restrict__ tiles16, Tile* __restrict__ tiles64, int32_t* __restrict__ ntiles) {
+    Tile* __restrict__ tiles16, Tile* __restrict__ tiles64, Tile* __restrict__ tiles128,
+    int32_t* __restrict__ ntiles, int32_t* __restrict__ blocks) {
+  after_previous();
   __shared__ int32_t sh[kThreads / 32];
   const uint32_t a = blockIdx.x;
-  int32_t c0 = 0, c16 = 0, c64 = 0;
+  int32_t c0 = 0, c16 = 0, c64 = 0, c128 = 0, cb = 0;
   for (uint32_t b = threadIdx.x; b < a; b += kThreads) {
     const int32_t c = counts[b];
     c0 += c;
     c16 += (c + 15) / 16;
     c64 += (c + 63) / 64;
+    c128 += (c + 127) / 128;
+    cb += c > 64 ? (c + 63) / 64 : 1;
   }
   c0 = block_sum(c0, sh);
   c16 = block_sum(c16, sh);
   c64 = block_sum(c64, sh);
+  c128 = block_sum(c128, sh);
+  cb = block_sum(cb, sh);
   const int32_t mine = counts[a];
-  const int32_t n16 = (mine + 15) / 16, n64 = (mine + 63) / 64;
+  const int32_t n16 = (mine + 15) / 16, n64 = (mine + 63) / 64, n128 = (mine + 127) / 128;
   if (threadIdx.x == 0) {
     offsets[a] = c0;
+    blocks[a] = cb;
     if (a == k - 1) {
       offsets[k] = c0 + mine;
+      blocks[k] = cb + (n64 > 1 ? n64 : 1);
       ntiles[0] = c16 + n16;
       ntiles[1] = c64 + n64;
+      ntiles[2] = c128 + n128;
     }
   }
   for (int32_t i = threadIdx.x; i < n16; i += kThreads)
-    tiles16[c16 + i] = Tile{(int32_t)a, c0 + 16 * i, min(16, mine - 16 * i), 0};
+    tiles16[c16 + i] = Tile{(int32_t)a, c0 + 16 * i, min(16, mine - 16 * i), c16 + n16};
   for (int32_t i = threadIdx.x; i < n64; i += kThreads)
-    tiles64[c64 + i] = Tile{(int32_t)a, c0 + 64 * i, min(64, mine - 64 * i), 0};
+    tiles64[c64 + i] = Tile{(int32_t)a, c0 + 64 * i, min(64, mine - 64 * i), c64 + n64};
+  for (int32_t i = threadIdx.x; i < n128; i += kThreads)
+    tiles128[c128 + i] = Tile{(int32_t)a, c0 + 128 * i, min(128, mine - 128 * i), c128 + n128};
   if (mine == 0) return;
   // four consecutive rows a thread, in order
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -162,9 +159,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -176,9 +170,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
-}
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -223,15 +214,6 @@ __device__ __forceinline__ void store8(uint16_t* p, uint4 v, int32_t n, bool vec
   for (int j = 0; j < 8; j++)
     if (j < n) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
 }
-// y + acc, rounded once, for a packed pair
-__device__ __forceinline__ uint32_t add_pair(uint32_t y, float a, float b) {
-  return pack_bf16(bf16_lo(y) + a, bf16_hi(y) + b);
-}
-
-// Byte address in a tile of rows that fill 128-byte lines: the 16-byte slots of a line are
-// permuted by the line's number, so that eight consecutive rows at one column (ldmatrix) fall
-// into different banks.
-__device__ __forceinline__ uint32_t swz(uint32_t byte) { return byte ^ (((byte >> 7) & 7) << 4); }
 
 // Columns of the second product are dealt out so that a thread ends with eight neighbours: of a
 // group of 32 columns, column 8 (i / 2) + 2 j + i % 2 is column i of the j-th mma tile, and the
@@ -249,46 +231,74 @@ __device__ __forceinline__ uint32_t swz_dealt(uint32_t row, uint32_t chunk) {
   return byte ^ (x << 4);
 }
 
-struct ApplyArgs {
-  const DevAdapter* table;
-  const Tile* tiles;
-  const int32_t* ntiles;
-  const int32_t* perm;
-  const uint16_t* x;      // rows of K values
-  uint64_t ldx;
-  uint16_t* y;            // rows of N values, may be NULL
-  uint64_t ldy;
-  uint16_t* low;          // may be NULL
-  uint32_t K, N;
-  uint32_t vec_x, vec_y;
-};
-
 // ---------------------------------------------------------------------- tiles of 16 rows
 // The sum's index may be dealt to the threads in any order as long as both factors agree, so a
 // thread reads 16 bytes (eight consecutive values) of each row and feeds them to two mma steps:
 // the fragments come straight from global memory, every load of a warp independent of the
-// others.
+// others.  low enters the second product as two BF16 numbers, its rounding and what that cut
+// off: with few rows the rounding errors of low would not average out in y, and the products
+// cost nothing beside the latency of the loads.
+template <int RP>
+struct Apply16 {
+  static constexpr uint32_t kULd = RP + 8;
+  static constexpr uint32_t kSmem = 9 * 16 * RP * 4 + 2 * 16 * kULd * 2;
+};
+
 template <int RP>
 __global__ void __launch_bounds__(kThreads) k_apply16(const ApplyArgs P) {
+  using L = Apply16<RP>;
   extern __shared__ __align__(1024) uint8_t smem[];
   float* const red = reinterpret_cast<float*>(smem);                 // [8][16][RP]
   float* const part = red + 8 * 16 * RP;                             // [16][RP]
-  uint16_t* const us = reinterpret_cast<uint16_t*>(part + 16 * RP);  // [16][RP + 8]
+  uint16_t* const us = reinterpret_cast<uint16_t*>(part + 16 * RP);  // [2][16][kULd]
   const cg::cluster_group cluster = cg::this_cluster();
   const uint32_t C = cluster.num_blocks(), c = cluster.block_rank();
   const uint32_t tile = blockIdx.x / C;
+  after_previous();
+  const Tile T = P.tiles[tile];              // (of the table's capacity, so within it)
   if (tile >= (uint32_t)*P.ntiles) return;   // (the whole cluster)
-  const Tile T = P.tiles[tile];
-  const DevAdapter A = P.table[T.adapter];
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   const int32_t r0 = (int32_t)g < T.count ? P.perm[T.start + g] : -1;
   const int32_t r1 = (int32_t)g + 8 < T.count ? P.perm[T.start + g + 8] : -1;
+  const DevAdapter A = P.table[T.adapter];
   const int32_t rank = (int32_t)A.rank;
+  const uint32_t first = c * 8 + warp, step = C * 8;
+
+  // a group of 32 columns of y, and (of a small rank) its rows of B: loaded ahead of the sum
+  constexpr int KS = RP >= 32 ? 32 : 16;
+  constexpr bool kAhead = RP <= 32;
+  uint4 y0, y1, w[4];
+  auto load_w = [&](uint32_t gc, int ks, int j) {
+    const uint32_t o = gc * 32 + dealt(g, j);
+    const int32_t k = KS == 32 ? ks * 32 + 8 * (int32_t)q : 4 * (int32_t)q;
+    const uint16_t* src = A.up + (uint64_t)o * A.ld_up + k;
+    const int32_t n = o < P.N ? rank - k : 0;
+    if (KS == 32) return load8w(src, n, A.vec_up);
+    uint2 t = make_uint2(0, 0);   // rank at most 16: four values a thread make one mma step
+    if (A.vec_up) {
+      if (n > 0) t = __ldg(reinterpret_cast<const uint2*>(src));
+    } else {
+      const uint4 f = gather8(src, min(n, 4));
+      t = make_uint2(f.x, f.y);
+    }
+    return make_uint4(t.x, t.y, 0, 0);
+  };
+  auto load_group = [&](uint32_t gc) {
+    const uint32_t col = gc * 32 + 8 * q;
+    const int32_t n = (int32_t)P.N - (int32_t)col;
+    y0 = load8(P.y + (int64_t)r0 * P.ldy + col, r0 >= 0 ? n : 0, P.vec_y);
+    y1 = load8(P.y + (int64_t)r1 * P.ldy + col, r1 >= 0 ? n : 0, P.vec_y);
+    if (kAhead) {
+#pragma unroll
+      for (int j = 0; j < 4; j++) w[j] = load_w(gc, 0, j);
+    }
+  };
+  const bool any = P.y && first * 32 < P.N;
+  if (any) load_group(first);
 
   float acc[RP / 8][4];
 #pragma unroll
   for (int j = 0; j < RP / 8; j++) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-  const uint32_t first = c * 8 + warp, step = C * 8;
 #pragma unroll(RP <= 32 ? 4 : 1)
   for (uint32_t kc = first; kc * 32 < P.K; kc += step) {
     const uint32_t k = kc * 32 + 8 * q;
@@ -313,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) k_apply16(const ApplyArgs P) {
   for (uint32_t e = threadIdx.x; e < 16 * RP; e += kThreads) {
     float s = 0.f;
 #pragma unroll
-    for (uint32_t w = 0; w < 8; w++) s += red[w * 16 * RP + e];
+    for (uint32_t v = 0; v < 8; v++) s += red[v * 16 * RP + e];
     part[e] = s;
   }
   cluster.sync();
@@ -322,64 +332,68 @@ __global__ void __launch_bounds__(kThreads) k_apply16(const ApplyArgs P) {
     for (uint32_t b = 0; b < C; b++) s += cluster.map_shared_rank(part, b)[e];
     const int32_t row = e / RP, col = e % RP;
     // columns past the rank are 0 whatever x holds (an infinity times a padded 0 is not)
-    const uint16_t u = col < rank ? (uint16_t)pack_bf16(s * A.scale, 0.f) : 0;
-    us[row * (RP + 8) + col] = u;
+    s = col < rank ? s * A.scale : 0.f;
+    const uint32_t hi = pack_bf16(s, 0.f);
+    const float rest = isfinite(s) ? s - bf16_lo(hi) : 0.f;
+    us[row * L::kULd + col] = (uint16_t)hi;
+    us[(16 + row) * L::kULd + col] = (uint16_t)pack_bf16(rest, 0.f);
     if (P.low && c == 0 && row < T.count)
-      P.low[(int64_t)P.perm[T.start + row] * RP + col] = u;
+      P.low[(int64_t)P.perm[T.start + row] * RP + col] = (uint16_t)hi;
   }
   __syncthreads();
   cg::cluster_group::arrival_token token = cluster.barrier_arrive();
 
-  if (P.y) {
+  if (any) {
     for (uint32_t gc = first; gc * 32 < P.N; gc += step) {
       const uint32_t col = gc * 32 + 8 * q;
       const int32_t n = (int32_t)P.N - (int32_t)col;
-      uint16_t* const p0 = P.y + (int64_t)r0 * P.ldy + col;
-      uint16_t* const p1 = P.y + (int64_t)r1 * P.ldy + col;
-      const uint4 y0 = load8(p0, r0 >= 0 ? n : 0, P.vec_y);
-      const uint4 y1 = load8(p1, r1 >= 0 ? n : 0, P.vec_y);
-      float d[4][4];
+      const uint32_t ya[4] = {y0.x, y0.y, y0.z, y0.w}, yb[4] = {y1.x, y1.y, y1.z, y1.w};
+      uint4 wc[4];
+      float d[4][4];   // y is the sum's first term
 #pragma unroll
-      for (int j = 0; j < 4; j++) d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
-      constexpr int KS = RP >= 32 ? 32 : 16;
+      for (int j = 0; j < 4; j++) {
+        d[j][0] = bf16_lo(ya[j]);
+        d[j][1] = bf16_hi(ya[j]);
+        d[j][2] = bf16_lo(yb[j]);
+        d[j][3] = bf16_hi(yb[j]);
+        if (kAhead) wc[j] = w[j];
+      }
+      if ((gc + step) * 32 < P.N) load_group(gc + step);
 #pragma unroll
       for (int ks = 0; ks < RP / KS; ks++) {
         if (ks * KS >= rank) break;
+        if (!kAhead) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          const uint32_t o = gc * 32 + dealt(g, j);
+          for (int j = 0; j < 4; j++) wc[j] = load_w(gc, ks, j);
+        }
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+          const uint16_t* u = us + (16 * half + g) * L::kULd;
           if (KS == 32) {
-            const int32_t k = ks * 32 + 8 * q;
-            const uint4 a = *reinterpret_cast<const uint4*>(us + g * (RP + 8) + k);
-            const uint4 b = *reinterpret_cast<const uint4*>(us + (g + 8) * (RP + 8) + k);
-            const uint4 w = load8w(A.up + (uint64_t)o * A.ld_up + k, o < P.N ? rank - k : 0, A.vec_up);
-            mma16816(d[j], a.x, b.x, a.y, b.y, w.x, w.y);
-            mma16816(d[j], a.z, b.z, a.w, b.w, w.z, w.w);
-          } else {
-            const int32_t k = 4 * q;   // four values a thread: one mma step
-            const uint2 a = *reinterpret_cast<const uint2*>(us + g * (RP + 8) + k);
-            const uint2 b = *reinterpret_cast<const uint2*>(us + (g + 8) * (RP + 8) + k);
-            uint2 w = make_uint2(0, 0);
-            const uint16_t* src = A.up + (uint64_t)o * A.ld_up + k;
-            if (o < P.N && k < rank) {
-              if (A.vec_up) {
-                w = __ldg(reinterpret_cast<const uint2*>(src));
-              } else {
-                const uint4 t = gather8(src, min(rank - k, 4));
-                w = make_uint2(t.x, t.y);
-              }
+            const uint4 a = *reinterpret_cast<const uint4*>(u + ks * 32 + 8 * q);
+            const uint4 b = *reinterpret_cast<const uint4*>(u + 8 * L::kULd + ks * 32 + 8 * q);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+              mma16816(d[j], a.x, b.x, a.y, b.y, wc[j].x, wc[j].y);
+              mma16816(d[j], a.z, b.z, a.w, b.w, wc[j].z, wc[j].w);
             }
-            mma16816(d[j], a.x, b.x, a.y, b.y, w.x, w.y);
+          } else {
+            const uint2 a = *reinterpret_cast<const uint2*>(u + 4 * q);
+            const uint2 b = *reinterpret_cast<const uint2*>(u + 8 * L::kULd + 4 * q);
+#pragma unroll
+            for (int j = 0; j < 4; j++) mma16816(d[j], a.x, b.x, a.y, b.y, wc[j].x, wc[j].y);
           }
         }
       }
       if (r0 >= 0)
-        store8(p0, make_uint4(add_pair(y0.x, d[0][0], d[0][1]), add_pair(y0.y, d[1][0], d[1][1]),
-                              add_pair(y0.z, d[2][0], d[2][1]), add_pair(y0.w, d[3][0], d[3][1])),
+        store8(P.y + (int64_t)r0 * P.ldy + col,
+               make_uint4(pack_bf16(d[0][0], d[0][1]), pack_bf16(d[1][0], d[1][1]),
+                          pack_bf16(d[2][0], d[2][1]), pack_bf16(d[3][0], d[3][1])),
                n, P.vec_y);
       if (r1 >= 0)
-        store8(p1, make_uint4(add_pair(y1.x, d[0][2], d[0][3]), add_pair(y1.y, d[1][2], d[1][3]),
-                              add_pair(y1.z, d[2][2], d[2][3]), add_pair(y1.w, d[3][2], d[3][3])),
+        store8(P.y + (int64_t)r1 * P.ldy + col,
+               make_uint4(pack_bf16(d[0][2], d[0][3]), pack_bf16(d[1][2], d[1][3]),
+                          pack_bf16(d[2][2], d[2][3]), pack_bf16(d[3][2], d[3][3])),
                n, P.vec_y);
     }
   }
@@ -402,99 +416,167 @@ struct Apply64 {
   static constexpr uint32_t kU = 64 * kULd * 2;
   static constexpr uint32_t kFirst = kRing > kPart + 2 * kUp ? kRing : kPart + 2 * kUp;
   static constexpr uint32_t kSmem = kFirst + kU + 64 * 4;
+  // Of the sum a warp takes 32 rows and a quarter of a stage, so that a fragment of A serves two
+  // tiles of rows; of rank 128, whose sums fill the registers, 16 rows and a half.
+  static constexpr int kMR = RP <= 64 ? 2 : 1;
 };
 
-template <int RP>
-__global__ void __launch_bounds__(kThreads) k_apply64(const ApplyArgs P) {
+// VEC: every row of x, y and of the factors can be read 16 bytes at a time.
+template <int RP, bool VEC>
+__global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const ApplyArgs P) {
   using L = Apply64<RP>;
   extern __shared__ __align__(1024) uint8_t smem[];
   float* const part = reinterpret_cast<float*>(smem);
-  uint8_t* const upt = smem + L::kPart;
   uint16_t* const us = reinterpret_cast<uint16_t*>(smem + L::kFirst);
   int32_t* const srow = reinterpret_cast<int32_t*>(smem + L::kFirst + L::kU);
   const cg::cluster_group cluster = cg::this_cluster();
   const uint32_t C = cluster.num_blocks(), c = cluster.block_rank();
   const uint32_t tile = blockIdx.x / C;
+  after_previous();
+  const Tile T = P.tiles[tile];              // (of the table's capacity, so within it)
   if (tile >= (uint32_t)*P.ntiles) return;   // (the whole cluster)
-  const Tile T = P.tiles[tile];
-  const DevAdapter A = P.table[T.adapter];
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const uint32_t wr = warp & 3, wh = warp >> 2;   // 16 rows; half of a stage, of a step's columns
-  const int32_t rank = (int32_t)A.rank;
+  // rows past the tile's end take its first row's place in loads and are never stored
+  const int32_t row_a = P.perm[T.start];
   if (tid < 64) srow[tid] = (int32_t)tid < T.count ? P.perm[T.start + tid] : -1;
+  const DevAdapter A = P.table[T.adapter];
+  const int32_t rank = (int32_t)A.rank;
   __syncthreads();
 
   // ---- low = s A x: this block's stages of the sum
   const uint32_t stages = (P.K + kBK - 1) / kBK;
   const uint32_t mine = stages > c ? (stages - c + C - 1) / C : 0;
-  const uint32_t xrow = tid >> 3, xch = tid & 7;   // rows xrow and xrow + 32, one 16-byte slot
-  const int32_t s0 = srow[xrow], s1 = srow[xrow + 32];
   const uint32_t ring = smem_addr(smem);
-  auto load_stage = [&](uint32_t i) {
-    const uint32_t k = (c + i * C) * kBK + xch * 8, at = ring + (i % kStages) * L::kStage;
-    const int32_t n = (int32_t)P.K - (int32_t)k;
-    fill8(at + swz(xrow * 128 + xch * 16), P.x + (int64_t)s0 * P.ldx + k, s0 >= 0 ? n : 0, P.vec_x);
-    fill8(at + swz((xrow + 32) * 128 + xch * 16), P.x + (int64_t)s1 * P.ldx + k, s1 >= 0 ? n : 0,
-          P.vec_x);
+  {
+    const uint32_t xrow = tid >> 3, xch = tid & 7;   // rows xrow and xrow + 32, one 16-byte slot
+    const int32_t s0 = srow[xrow], s1 = srow[xrow + 32];
+    const uint16_t* const xp0 = P.x + (int64_t)(s0 >= 0 ? s0 : row_a) * P.ldx + xch * 8;
+    const uint16_t* const xp1 = P.x + (int64_t)(s1 >= 0 ? s1 : row_a) * P.ldx + xch * 8;
+    const uint16_t* const wp = A.down + xch * 8;
+    const uint32_t sx = swz(xrow * 128 + xch * 16);   // (32 rows on: the same slot, 4096 bytes on)
+    auto load_stage = [&](uint32_t i) {
+      const uint32_t k0 = (c + i * C) * kBK, at = ring + (i % kStages) * L::kStage + sx;
+      const int32_t n = (int32_t)P.K - (int32_t)(k0 + xch * 8);
+      const uint32_t k = n > 0 ? k0 : 0;   // (nothing is read past a row's end)
+      if (VEC) {
+        cp16z(at, xp0 + k, s0 >= 0 && n > 0);
+        cp16z(at + 4096, xp1 + k, s1 >= 0 && n > 0);
+      } else {
+        fill8(at, xp0 + k, s0 >= 0 ? n : 0, P.vec_x);
+        fill8(at + 4096, xp1 + k, s1 >= 0 ? n : 0, P.vec_x);
+      }
 #pragma unroll
-    for (uint32_t r = 0; r < RP; r += 32) {
-      const uint32_t row = r + xrow;
-      if (RP >= 32 || row < RP)
-        fill8(at + L::kXBytes + swz(row * 128 + xch * 16), A.down + (uint64_t)row * A.ld_down + k,
-              (int32_t)row < rank ? n : 0, A.vec_down);
+      for (uint32_t r = 0; r < RP; r += 32) {
+        const uint32_t row = r + xrow;
+        if (RP < 32 && row >= RP) break;
+        const bool there = (int32_t)row < rank;
+        const uint16_t* src = wp + (there ? (uint64_t)row * A.ld_down : 0) + k;
+        if (VEC) cp16z(at + L::kXBytes + r * 128, src, there && n > 0);
+        else fill8(at + L::kXBytes + r * 128, src, there ? n : 0, A.vec_down);
+      }
+    };
+    constexpr int MR = L::kMR;
+    const uint32_t rg = warp % (4 / MR), kq = warp / (4 / MR);   // rows 16 MR rg ..; part of a stage
+    float acc[MR][RP / 8][4];
+#pragma unroll
+    for (int m = 0; m < MR; m++)
+#pragma unroll
+      for (int j = 0; j < RP / 8; j++)
+        acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.f;
+    for (uint32_t i = 0; i < kStages - 1; i++) {
+      if (i < mine) load_stage(i);
+      cp_commit();
     }
-  };
-  float acc[RP / 8][4];
+    for (uint32_t i = 0; i < mine; i++) {
+      cp_wait<kStages - 2>();
+      __syncthreads();
+      if (i + kStages - 1 < mine) load_stage(i + kStages - 1);
+      cp_commit();
+      const uint32_t xs = ring + (i % kStages) * L::kStage, ws = xs + L::kXBytes;
 #pragma unroll
-  for (int j = 0; j < RP / 8; j++) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-  for (uint32_t i = 0; i < kStages - 1; i++) {
-    if (i < mine) load_stage(i);
-    cp_commit();
-  }
-  for (uint32_t i = 0; i < mine; i++) {
-    cp_wait<kStages - 2>();
-    __syncthreads();
-    if (i + kStages - 1 < mine) load_stage(i + kStages - 1);
-    cp_commit();
-    const uint32_t xs = ring + (i % kStages) * L::kStage, ws = xs + L::kXBytes;
+      for (uint32_t kk = 0; kk < 2 / MR; kk++) {
+        const uint32_t kb = (kq * (2 / MR) + kk) * 32;   // byte of the 16-value step in a row
+        uint32_t a[MR][4];
 #pragma unroll
-    for (uint32_t kk = 0; kk < 2; kk++) {
-      const uint32_t kb = wh * 64 + kk * 32;   // byte of the 16-value step in a row
-      uint32_t a[4];
-      ldsm4(a, xs + swz((wr * 16 + (lane & 15)) * 128 + kb + (lane >> 4) * 16));
+        for (int m = 0; m < MR; m++)
+          ldsm4(a[m], xs + swz(((rg * MR + m) * 16 + (lane & 15)) * 128 + kb + (lane >> 4) * 16));
 #pragma unroll
-      for (int j = 0; j < RP / 16; j++) {
-        uint32_t b[4];
-        ldsm4(b, ws + swz((j * 16 + (lane >> 4) * 8 + (lane & 7)) * 128 + kb + ((lane >> 3) & 1) * 16));
-        mma16816(acc[2 * j], a[0], a[1], a[2], a[3], b[0], b[1]);
-        mma16816(acc[2 * j + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
+        for (int j = 0; j < RP / 16; j++) {
+          uint32_t b[4];
+          ldsm4(b, ws + swz(((lane >> 4) * 8 + (lane & 7)) * 128 + kb + ((lane >> 3) & 1) * 16) +
+                       j * 2048);
+#pragma unroll
+          for (int m = 0; m < MR; m++) {
+            mma16816(acc[m][2 * j], a[m][0], a[m][1], a[m][2], a[m][3], b[0], b[1]);
+            mma16816(acc[m][2 * j + 1], a[m][0], a[m][1], a[m][2], a[m][3], b[2], b[3]);
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+    // join the parts of every stage, in one order
+#pragma unroll
+    for (uint32_t pass = 0; pass < 2 * MR; pass++) {
+      __syncthreads();
+      if (kq == pass) {
+#pragma unroll
+        for (int m = 0; m < MR; m++)
+#pragma unroll
+          for (int j = 0; j < RP / 8; j++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              float2* d = reinterpret_cast<float2*>(
+                  part + ((rg * MR + m) * 16 + h * 8 + g) * RP + j * 8 + 2 * q);
+              const float2 v = make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+              *d = pass == 0 ? v : make_float2(d->x + v.x, d->y + v.y);
+            }
       }
     }
   }
-  cp_wait<0>();
-  __syncthreads();
-  // join the two halves of every stage, then the blocks of the cluster
-  if (wh == 1) {
+
+  // ---- y += B low: this block's steps of the columns, the first one's loads ahead of the join
+  const uint32_t steps = P.y ? (P.N + kBN - 1) / kBN : 0;
+  const uint32_t todo = steps > c ? (steps - c + C - 1) / C : 0;
+  constexpr uint32_t per = RP / 8, span = kThreads / per;   // 16-byte slots in a row; rows at once
+  const uint32_t urow = tid / per, uch = tid % per;
+  const uint32_t up0 = ring + L::kPart;
+  const uint16_t* const upp = A.up + (uint64_t)urow * A.ld_up + uch * 8;
+  const int32_t un = rank - (int32_t)uch * 8;
+  auto load_up = [&](uint32_t i) {
+    const uint32_t o0 = (c + i * C) * kBN, at = up0 + (i & 1) * L::kUp;
 #pragma unroll
-    for (int j = 0; j < RP / 8; j++) {
-      float* d = part + (wr * 16 + g) * RP + j * 8 + 2 * q;
-      *reinterpret_cast<float2*>(d) = make_float2(acc[j][0], acc[j][1]);
-      *reinterpret_cast<float2*>(d + 8 * RP) = make_float2(acc[j][2], acc[j][3]);
+    for (uint32_t r = 0; r < kBN; r += span) {
+      const bool there = o0 + r + urow < P.N;
+      const uint32_t dst = at + swz_dealt<RP>(r + urow, uch);
+      if (VEC) cp16z(dst, there && un > 0 ? upp + (uint64_t)(o0 + r) * A.ld_up : A.up, there && un > 0);
+      else fill8(dst, upp + (uint64_t)(o0 + r) * A.ld_up, there ? un : 0, A.vec_up);
     }
-  }
-  __syncthreads();
-  if (wh == 0) {
+  };
+  const int32_t r0 = srow[wr * 16 + g], r1 = srow[wr * 16 + g + 8];
+  uint16_t* const yp0 = P.y + (int64_t)(r0 >= 0 ? r0 : row_a) * P.ldy + wh * 64 + 8 * q;
+  uint16_t* const yp1 = P.y + (int64_t)(r1 >= 0 ? r1 : row_a) * P.ldy + wh * 64 + 8 * q;
+  const int32_t left = (int32_t)P.N - (int32_t)(wh * 64 + 8 * q);
+  uint4 y0[2], y1[2];
+  auto load_y = [&](uint32_t i) {
 #pragma unroll
-    for (int j = 0; j < RP / 8; j++) {
-      float2* d = reinterpret_cast<float2*>(part + (wr * 16 + g) * RP + j * 8 + 2 * q);
-      float2* e = reinterpret_cast<float2*>(part + (wr * 16 + g + 8) * RP + j * 8 + 2 * q);
-      *d = make_float2(d->x + acc[j][0], d->y + acc[j][1]);
-      *e = make_float2(e->x + acc[j][2], e->y + acc[j][3]);
+    for (uint32_t h = 0; h < 2; h++) {
+      const uint32_t at = (c + i * C) * kBN + h * 32;
+      const int32_t n = left - (int32_t)at;
+      y0[h] = load8(yp0 + at, n, VEC || P.vec_y);
+      y1[h] = load8(yp1 + at, n, VEC || P.vec_y);
     }
+  };
+  if (todo > 0) {
+    load_up(0);
+    load_y(0);
   }
+  cp_commit();
+
+  // join the sums of the cluster's blocks: each joins some of the rows and hands them to all
   cluster.sync();
   {
-    const uint32_t rows = 64 / C;   // this block joins these rows and hands them to all
+    const uint32_t rows = 64 / C;
     for (uint32_t e = tid * 2; e < rows * RP; e += kThreads * 2) {
       const uint32_t row = c * rows + e / RP, col = e % RP;
       float2 s = make_float2(0.f, 0.f);
@@ -514,51 +596,27 @@ __global__ void __launch_bounds__(kThreads) k_apply64(const ApplyArgs P) {
     }
   }
   cluster.sync();   // low is complete, and nobody reads another block's memory after this
-  if (!P.y) return;
 
-  // ---- y += B low: this block's steps of the columns
-  const uint32_t steps = (P.N + kBN - 1) / kBN;
-  const uint32_t todo = steps > c ? (steps - c + C - 1) / C : 0;
-  const uint32_t up0 = smem_addr(upt);
-  auto load_up = [&](uint32_t i) {
-    const uint32_t o0 = (c + i * C) * kBN, at = up0 + (i & 1) * L::kUp;
-    constexpr uint32_t per = RP / 8;   // 16-byte slots in a row
-#pragma unroll
-    for (uint32_t s = tid; s < kBN * per; s += kThreads) {
-      const uint32_t row = s / per, ch = s % per, o = o0 + row;
-      fill8(at + swz_dealt<RP>(row, ch), A.up + (uint64_t)o * A.ld_up + ch * 8,
-            o < P.N ? rank - (int32_t)ch * 8 : 0, A.vec_up);
-    }
-  };
-  const int32_t r0 = srow[wr * 16 + g], r1 = srow[wr * 16 + g + 8];
-  uint4 y0[2], y1[2];
-  auto load_y = [&](uint32_t i) {
-#pragma unroll
-    for (uint32_t h = 0; h < 2; h++) {
-      const uint32_t col = (c + i * C) * kBN + wh * 64 + h * 32 + 8 * q;
-      const int32_t n = (int32_t)P.N - (int32_t)col;
-      y0[h] = load8(P.y + (int64_t)r0 * P.ldy + col, r0 >= 0 ? n : 0, P.vec_y);
-      y1[h] = load8(P.y + (int64_t)r1 * P.ldy + col, r1 >= 0 ? n : 0, P.vec_y);
-    }
-  };
-  if (todo > 0) {
-    load_up(0);
-    cp_commit();
-    load_y(0);
-  }
   for (uint32_t i = 0; i < todo; i++) {
     cp_wait<0>();
     __syncthreads();
     if (i + 1 < todo) load_up(i + 1);
     cp_commit();
-    uint4 c0[2] = {y0[0], y0[1]}, c1[2] = {y1[0], y1[1]};
+    float d[2][4][4];   // y is the sum's first term
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const uint32_t a[4] = {y0[h].x, y0[h].y, y0[h].z, y0[h].w};
+      const uint32_t b[4] = {y1[h].x, y1[h].y, y1[h].z, y1[h].w};
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        d[h][j][0] = bf16_lo(a[j]);
+        d[h][j][1] = bf16_hi(a[j]);
+        d[h][j][2] = bf16_lo(b[j]);
+        d[h][j][3] = bf16_hi(b[j]);
+      }
+    }
     if (i + 1 < todo) load_y(i + 1);
     const uint32_t at = up0 + (i & 1) * L::kUp;
-    float d[2][4][4];
-#pragma unroll
-    for (int h = 0; h < 2; h++)
-#pragma unroll
-      for (int j = 0; j < 4; j++) d[h][j][0] = d[h][j][1] = d[h][j][2] = d[h][j][3] = 0.f;
 #pragma unroll
     for (int ks = 0; ks < RP / 16; ks++) {
       if (ks * 16 >= rank) break;
@@ -577,39 +635,222 @@ __global__ void __launch_bounds__(kThreads) k_apply64(const ApplyArgs P) {
     }
 #pragma unroll
     for (uint32_t h = 0; h < 2; h++) {
-      const uint32_t col = (c + i * C) * kBN + wh * 64 + h * 32 + 8 * q;
-      const int32_t n = (int32_t)P.N - (int32_t)col;
+      const uint32_t col = (c + i * C) * kBN + h * 32;
+      const int32_t n = left - (int32_t)col;
       if (r0 >= 0)
-        store8(P.y + (int64_t)r0 * P.ldy + col,
-               make_uint4(add_pair(c0[h].x, d[h][0][0], d[h][0][1]),
-                          add_pair(c0[h].y, d[h][1][0], d[h][1][1]),
-                          add_pair(c0[h].z, d[h][2][0], d[h][2][1]),
-                          add_pair(c0[h].w, d[h][3][0], d[h][3][1])),
-               n, P.vec_y);
+        store8(yp0 + col, make_uint4(pack_bf16(d[h][0][0], d[h][0][1]), pack_bf16(d[h][1][0], d[h][1][1]),
+                                     pack_bf16(d[h][2][0], d[h][2][1]), pack_bf16(d[h][3][0], d[h][3][1])),
+               n, VEC || P.vec_y);
       if (r1 >= 0)
-        store8(P.y + (int64_t)r1 * P.ldy + col,
-               make_uint4(add_pair(c1[h].x, d[h][0][2], d[h][0][3]),
-                          add_pair(c1[h].y, d[h][1][2], d[h][1][3]),
-                          add_pair(c1[h].z, d[h][2][2], d[h][2][3]),
-                          add_pair(c1[h].w, d[h][3][2], d[h][3][3])),
-               n, P.vec_y);
+        store8(yp1 + col, make_uint4(pack_bf16(d[h][0][2], d[h][0][3]), pack_bf16(d[h][1][2], d[h][1][3]),
+                                     pack_bf16(d[h][2][2], d[h][2][3]), pack_bf16(d[h][3][2], d[h][3][3])),
+               n, VEC || P.vec_y);
     }
+  }
+}
+
+// ------------------------------------------------------- y += B low, for many rows of an adapter
+// With low known, the blocks take equal shares of (columns, rows): a block keeps 256 columns' rows
+// of B in shared memory and runs down the adapter's rows, each warp by itself over 32 rows at a
+// time and 32 columns a step, so that B is read once per block and nothing waits for another
+// warp.  A thread's own pieces of y come through a ring of asynchronous copies four steps deep.
+template <int RP>
+struct Expand {
+  static constexpr uint32_t kN = RP <= 64 ? 256 : 128;   // columns of a block
+  static constexpr uint32_t kB = kN * RP * 2;
+  static constexpr uint32_t kDepth = 4;
+  static constexpr uint32_t kSlot = 4 * kThreads * 16;   // 64 bytes a thread
+  static constexpr uint32_t kSmem = kB + kDepth * kSlot;
+  // byte address of a factor row's 16-byte slot: the rows that a quarter warp reads together
+  // (two neighbours; of rank 16 also those 8 further on) fall into different banks
+  static __device__ __forceinline__ uint32_t at(uint32_t row, uint32_t byte) {
+    const uint32_t a = row * (RP * 2) + byte;
+    return RP >= 64 ? a ^ (row & 1) << 6 : RP == 16 ? a ^ (row >> 3 & 1) << 6 : a;
+  }
+};
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+template <int RP>
+__global__ void __launch_bounds__(kThreads, 2) k_expand(const ApplyArgs P) {
+  using L = Expand<RP>;
+  constexpr int KS = RP >= 32 ? RP / 32 : 1;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  after_previous();
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  const uint32_t nt = (uint32_t)*P.ntiles, chunks = (P.N + L::kN - 1) / L::kN;
+  const uint64_t all = (uint64_t)nt * chunks;
+  uint64_t at = all * blockIdx.x / gridDim.x;
+  const uint64_t end = all * (blockIdx.x + 1) / gridDim.x;
+  const uint32_t bs = smem_addr(smem), ring = bs + L::kB + tid * 16;
+  while (at < end) {
+    // the block's tiles of one adapter and one piece of the columns
+    const uint32_t t0 = (uint32_t)(at % nt), n0 = (uint32_t)(at / nt) * L::kN;
+    const Tile T = P.tiles[t0];
+    const uint64_t left = end - at;
+    const uint32_t t1 = left < (uint32_t)T.end - t0 ? t0 + (uint32_t)left : (uint32_t)T.end;
+    const Tile Z = P.tiles[t1 - 1];
+    at += t1 - t0;
+    const DevAdapter A = P.table[T.adapter];
+    const int32_t rank = (int32_t)A.rank, r_end = Z.start + Z.count;
+    __syncthreads();   // every warp is done with the B before
+    for (uint32_t s = tid; s < L::kN * (RP / 8); s += kThreads) {
+      const uint32_t row = s / (RP / 8), ch = s % (RP / 8);
+      const int32_t n = n0 + row < P.N ? rank - (int32_t)ch * 8 : 0;
+      const uint16_t* src = n > 0 ? A.up + (uint64_t)(n0 + row) * A.ld_up + ch * 8 : A.up;
+      cp16z(bs + L::at(row, ch * 16), src, n > 0);
+    }
+    cp_commit();
+    cp_wait<0>();
+    __syncthreads();
+
+    const int32_t n_left = (int32_t)(P.N - n0);
+    const uint32_t groups = (uint32_t)((n_left < (int32_t)L::kN ? n_left : (int32_t)L::kN) + 31) / 32;
+    const int32_t units = (r_end - T.start + 31) / 32;
+    const int32_t mine = units > (int32_t)warp ? (units - (int32_t)warp + 7) / 8 : 0;
+    if (mine == 0) continue;
+    auto row_of = [&](int32_t u, int i) {   // the thread's i-th row of its u-th unit, or -1
+      const int32_t r = T.start + ((int32_t)warp + u * 8) * 32 + (int32_t)g + 8 * i;
+      return u < mine && r < r_end ? P.perm[r] : -1;
+    };
+    const int64_t base = (int64_t)n0 + 8 * q;
+    // the copies run ahead: their unit, step and rows
+    int32_t pu = 0;
+    uint32_t pg = 0;
+    int32_t prow[4], pnext[4], row[4], next[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      row[i] = prow[i] = row_of(0, i);
+      next[i] = pnext[i] = row_of(1, i);
+    }
+    uint32_t issued = 0, total = (uint32_t)mine * groups;
+    auto issue = [&]() {
+      if (issued < total) {
+        const uint32_t dst = ring + (issued % L::kDepth) * L::kSlot;
+        const bool there = (int32_t)(pg * 32 + 8 * q) < n_left;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          if (prow[i] >= 0 && there)
+            cp16(dst + i * kThreads * 16, P.y + (int64_t)prow[i] * P.ldy + base + pg * 32);
+        if (++pg == groups) {
+          pg = 0;
+          pu++;
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            prow[i] = pnext[i];
+            pnext[i] = row_of(pu + 1, i);
+          }
+        }
+        issued++;
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (uint32_t i = 0; i < L::kDepth - 1; i++) issue();
+    uint32_t step = 0;
+    for (int32_t u = 0; u < mine; u++) {
+      uint4 a[4][KS];   // low: rows g, g + 8, g + 16, g + 24
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const uint16_t* src = P.low + (int64_t)(row[i] >= 0 ? row[i] : 0) * RP;
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++) {
+          if (RP >= 32) {
+            a[i][ks] = ld16(src + ks * 32 + 8 * q);
+          } else {
+            const uint2 t = *reinterpret_cast<const uint2*>(src + 4 * q);
+            a[i][ks] = make_uint4(t.x, t.y, 0, 0);
+          }
+        }
+      }
+      for (uint32_t gi = 0; gi < groups; gi++, step++) {
+        issue();
+        cp_wait<L::kDepth - 1>();
+        const int32_t n = n_left - (int32_t)(gi * 32 + 8 * q);
+        float d[2][4][4];   // y is the sum's first term
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const uint4 y = lds16(ring + (step % L::kDepth) * L::kSlot + i * kThreads * 16);
+          const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            d[i >> 1][j][2 * (i & 1)] = bf16_lo(w[j]);
+            d[i >> 1][j][2 * (i & 1) + 1] = bf16_hi(w[j]);
+          }
+        }
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const uint32_t o = gi * 32 + dealt(g, j);
+            if (RP >= 32) {
+              const uint4 b = lds16(bs + L::at(o, ks * 64 + q * 16));
+#pragma unroll
+              for (int m = 0; m < 2; m++) {
+                const uint4 &lo = a[2 * m][ks], &hi = a[2 * m + 1][ks];
+                mma16816(d[m][j], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+                mma16816(d[m][j], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+              }
+            } else {
+              const uint2 b = lds8(bs + L::at(o, q * 8));
+#pragma unroll
+              for (int m = 0; m < 2; m++)
+                mma16816(d[m][j], a[2 * m][0].x, a[2 * m + 1][0].x, a[2 * m][0].y,
+                         a[2 * m + 1][0].y, b.x, b.y);
+            }
+          }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int m = i >> 1, h = 2 * (i & 1);
+          if (row[i] >= 0)
+            store8(P.y + (int64_t)row[i] * P.ldy + base + gi * 32,
+                   make_uint4(pack_bf16(d[m][0][h], d[m][0][h + 1]),
+                              pack_bf16(d[m][1][h], d[m][1][h + 1]),
+                              pack_bf16(d[m][2][h], d[m][2][h + 1]),
+                              pack_bf16(d[m][3][h], d[m][3][h + 1])),
+                   n, true);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        row[i] = next[i];
+        next[i] = row_of(u + 2, i);
+      }
+    }
+    cp_wait<0>();
   }
 }
 
 // ---------------------------------------------------------------- transposes of the factors
 // down (rank x hidden) to hidden x RP and up (out x rank) to RP x out8, both zero-padded, and a
 // table entry that has them in the other's place.
+constexpr uint32_t kTF = 64;   // features a block turns at a time
+template <int RP>
 __global__ void __launch_bounds__(kThreads) k_transpose(const DevAdapter* __restrict__ table,
-                                                        uint32_t hidden, uint32_t out, uint32_t RP,
+                                                        uint32_t hidden, uint32_t out,
                                                         uint32_t out8, uint16_t* __restrict__ buf,
-                                                        DevAdapter* __restrict__ swapped) {
-  __shared__ uint16_t sh[32][33];
+                                                        DevAdapter* __restrict__ swapped,
+                                                        uint32_t* __restrict__ counters,
+                                                        uint32_t slices) {
+  constexpr uint32_t kLd = RP + 2;
+  __shared__ uint16_t sh[kTF * kLd];   // [feature][rank]
+  after_previous();
   const DevAdapter A = table[blockIdx.y];
   uint16_t* const at = buf + (uint64_t)blockIdx.y * RP * ((uint64_t)hidden + out8);
   uint16_t* const bt = at + (uint64_t)hidden * RP;
-  const uint32_t tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const uint32_t ht = (hidden + 31) / 32, ot = (out8 + 31) / 32;
+  const uint32_t ht = (hidden + kTF - 1) / kTF;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     DevAdapter S = A;
     S.down = bt;
@@ -619,220 +860,311 @@ __global__ void __launch_bounds__(kThreads) k_transpose(const DevAdapter* __rest
     S.vec_down = S.vec_up = 1;
     swapped[blockIdx.y] = S;
   }
-  for (uint32_t b = blockIdx.x; b < ht + ot; b += gridDim.x) {
-    const bool first = b < ht;
-    const uint32_t f0 = (first ? b : b - ht) * 32;
-    for (uint32_t r0 = 0; r0 < RP; r0 += 32) {
-      __syncthreads();
-      for (uint32_t i = ty; i < 32; i += 8) {
-        uint16_t v = 0;
-        if (first) {   // rows r0 + i, columns f0 + tx
-          if (r0 + i < A.rank && f0 + tx < hidden) v = A.down[(uint64_t)(r0 + i) * A.ld_down + f0 + tx];
-        } else {       // rows f0 + i, columns r0 + tx
-          if (f0 + i < out && r0 + tx < A.rank) v = A.up[(uint64_t)(f0 + i) * A.ld_up + r0 + tx];
-        }
-        sh[i][tx] = v;
-      }
-      __syncthreads();
-      for (uint32_t i = ty; i < 32; i += 8) {
-        const uint16_t v = sh[tx][i];
-        if (first) {
-          if (f0 + i < hidden && r0 + tx < RP) at[(uint64_t)(f0 + i) * RP + r0 + tx] = v;
-        } else {
-          if (r0 + i < RP && f0 + tx < out8) bt[(uint64_t)(r0 + i) * out8 + f0 + tx] = v;
-        }
-      }
+  for (uint32_t i = blockIdx.x * kThreads + threadIdx.x; i < slices; i += gridDim.x * kThreads)
+    counters[(uint64_t)blockIdx.y * slices + i] = 0;   // of k_wgrad
+  const bool first = blockIdx.x < ht;
+  const uint32_t f0 = (first ? blockIdx.x : blockIdx.x - ht) * kTF;
+  const int32_t rank = (int32_t)A.rank;
+  for (uint32_t s = threadIdx.x; s < kTF * RP / 8; s += kThreads) {
+    if (first) {   // eight features of a row of A
+      const uint32_t r = s / (kTF / 8), f = s % (kTF / 8) * 8;
+      const uint4 v = load8w(A.down + (uint64_t)r * A.ld_down + f0 + f,
+                             (int32_t)r < rank ? (int32_t)hidden - (int32_t)(f0 + f) : 0, A.vec_down);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 8; j++) sh[(f + j) * kLd + r] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+    } else {       // eight columns of a row of B
+      const uint32_t f = s / (RP / 8), r = s % (RP / 8) * 8;
+      const uint4 v = load8w(A.up + (uint64_t)(f0 + f) * A.ld_up + r,
+                             f0 + f < out ? rank - (int32_t)r : 0, A.vec_up);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; j++) *reinterpret_cast<uint32_t*>(sh + f * kLd + r + 2 * j) = w[j];
+    }
+  }
+  __syncthreads();
+  for (uint32_t s = threadIdx.x; s < kTF * RP / 8; s += kThreads) {
+    uint32_t w[4];
+    if (first) {
+      const uint32_t f = s / (RP / 8), r = s % (RP / 8) * 8;
+#pragma unroll
+      for (int j = 0; j < 4; j++) w[j] = *reinterpret_cast<const uint32_t*>(sh + f * kLd + r + 2 * j);
+      if (f0 + f < hidden)
+        *reinterpret_cast<uint4*>(at + (uint64_t)(f0 + f) * RP + r) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      const uint32_t r = s / (kTF / 8), f = s % (kTF / 8) * 8;
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+        w[j] = sh[(f + 2 * j) * kLd + r] | (uint32_t)sh[(f + 2 * j + 1) * kLd + r] << 16;
+      if (f0 + f < out8)
+        *reinterpret_cast<uint4*>(bt + (uint64_t)r * out8 + f0 + f) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
 
 // ------------------------------------------------------------------------ weight gradients
-// A block takes 128 features of x (for dA) or dy (for dB) of one adapter; the blocks of a
-// cluster split the adapter's rows in tiles of 64 and join their sums in a fixed order.
-struct WgradArgs {
-  const DevAdapter* table;
-  const int32_t* perm;
-  const int32_t* offsets;
-  const uint16_t* x;
-  uint64_t ldx;
-  const uint16_t* dy;
-  uint64_t lddy;
-  const uint16_t* low;
-  const uint16_t* dlow;
-  uint32_t hidden, out, vec_x, vec_dy;
-  uint32_t grad_f32, accumulate;
-};
-
-constexpr uint32_t kFeat = 128;
+// A piece is 128 features of x (for dA) or dy (for dB) of one adapter, a sum over the adapter's
+// rows in stages of 64.  The blocks take equal shares of all stages of all pieces, so none waits
+// while another works; a piece that several blocks share is joined by the one that ends last, in
+// the order of the blocks, from their sums in the workspace.
 constexpr uint32_t kWStages = 3;
 template <int RP>
 struct Wgrad {
   static constexpr uint32_t kQ = 64 * kFeat * 2, kPb = 64 * RP * 2, kStage = kQ + kPb;
-  static constexpr uint32_t kRing = kWStages * kStage, kPart = kFeat * RP * 4;
+  static constexpr uint32_t kLd = RP + 2;   // of the sums in shared memory, read along both ways
+  static constexpr uint32_t kRing = kWStages * kStage, kPart = kFeat * kLd * 4;
   static constexpr uint32_t kSmem = kRing > kPart ? kRing : kPart;
+  // 32 features a warp, so that a fragment of low serves two tiles; the warps' other half then
+  // takes the other half of the rows (of rank 128 the sums alone fill the registers: 16)
+  static constexpr int kMF = RP <= 64 ? 2 : 1;
 };
 
-__device__ __forceinline__ void put_grad(void* base, uint64_t at, float v, bool f32, bool acc) {
-  if (f32) {
-    float* p = static_cast<float*>(base) + at;
-    *p = acc ? *p + v : v;
-  } else {
-    uint16_t* p = static_cast<uint16_t*>(base) + at;
-    const float s = acc ? __uint_as_float((uint32_t)*p << 16) + v : v;
-    *p = (uint16_t)pack_bf16(s, 0.f);
-  }
-}
-
 template <int RP>
-__global__ void __launch_bounds__(kThreads) k_wgrad(const WgradArgs P) {
+__global__ void __launch_bounds__(kThreads, 2) k_wgrad(const WgradArgs P) {
   using L = Wgrad<RP>;
+  constexpr int MF = L::kMF;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const cg::cluster_group cluster = cg::this_cluster();
-  const uint32_t C = cluster.num_blocks(), c = cluster.block_rank();
-  const uint32_t slice = blockIdx.x / C, hs = (P.hidden + kFeat - 1) / kFeat;
-  const bool down = slice < hs;
-  const uint32_t f0 = (down ? slice : slice - hs) * kFeat, F = down ? P.hidden : P.out;
-  const uint16_t* const src = down ? P.x : P.dy;
-  const uint64_t lds = down ? P.ldx : P.lddy;
-  const bool vec = down ? P.vec_x : P.vec_dy;
-  const uint16_t* const pr = down ? P.dlow : P.low;
-  const int32_t start = P.offsets[blockIdx.y], end = P.offsets[blockIdx.y + 1];
+  float* const part = reinterpret_cast<float*>(smem);   // [feature][kLd], after a piece's stages
+  __shared__ uint32_t sh_last;
+  after_previous();
+  const uint32_t hs = (P.hidden + kFeat - 1) / kFeat, slices = hs + (P.out + kFeat - 1) / kFeat;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-  const uint32_t tiles = (uint32_t)(end - start + 63) / 64;
-  const uint32_t mine = tiles > c ? (tiles - c + C - 1) / C : 0;
+  const uint32_t fw = MF == 2 ? warp & 3 : warp, th = MF == 2 ? warp >> 2 : 0;
   const uint32_t ring = smem_addr(smem);
-  auto load_stage = [&](uint32_t i) {
-    const int32_t t0 = start + (int32_t)((c + i * C) * 64);
-    const uint32_t at = ring + (i % kWStages) * L::kStage;
+  const uint32_t qch = tid & 15, qrow = tid >> 4;
+  constexpr uint32_t per = RP / 8, span = kThreads / per, PN = (64 + span - 1) / span;
+  const uint32_t pch = tid % per, prow = tid / per;
+
+  Shares sh;
+  sh.all = (uint64_t)P.blocks[P.k] * slices;
+  sh.G = gridDim.x < sh.all ? gridDim.x : (uint32_t)sh.all;
+  if (blockIdx.x >= sh.G) return;
+  const uint64_t s_begin = sh.begin(blockIdx.x);
+  for (Piece Q(P, slices, s_begin, sh.begin(blockIdx.x + 1)); !Q.over(); Q.next(P, slices)) {
+    const uint32_t mine = Q.mine;
+    const DevAdapter A = P.table[Q.adapter];
+    const bool down = Q.slice < hs;
+    const uint32_t f0 = (down ? Q.slice : Q.slice - hs) * kFeat, F = down ? P.hidden : P.out;
+    const uint64_t lds = down ? P.ldx : P.lddy;
+    const bool vec = down ? P.vec_x : P.vec_dy;
+    const uint16_t* const pr = down ? P.dlow : P.low;
+    const int32_t start = Q.row0 + (int32_t)Q.first * 64, end = Q.row1;
+    const int32_t qn = (int32_t)F - (int32_t)(f0 + qch * 8);
+    const uint16_t* const qsrc = (down ? P.x : P.dy) + (qn > 0 ? f0 + qch * 8 : 0);
+
+    // A thread's slots of a stage: four rows of x or dy, up to four of low; their row numbers
+    // are read one stage ahead of the rows.
+    int32_t tq[4], tp[PN];
+    auto load_rows = [&](uint32_t i) {
+      const int32_t t0 = start + (int32_t)i * 64;
 #pragma unroll
-    for (uint32_t s = tid; s < 64 * 16; s += kThreads) {
-      const uint32_t row = s >> 4, ch = s & 15, f = f0 + ch * 8;
-      const int32_t t = t0 + (int32_t)row < end ? P.perm[t0 + row] : -1;
-      fill8(at + (ch >> 3) * 8192 + swz(row * 128 + (ch & 7) * 16), src + (int64_t)t * lds + f,
-            t >= 0 ? (int32_t)F - (int32_t)f : 0, vec);
+      for (uint32_t j = 0; j < 4; j++) {
+        const int32_t t = t0 + (int32_t)(qrow + 16 * j);
+        tq[j] = t < end ? P.perm[t] : -1;
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < PN; j++) {
+        const uint32_t r = prow + span * j;
+        const int32_t t = t0 + (int32_t)r;
+        tp[j] = r < 64 && t < end ? P.perm[t] : -1;
+      }
+    };
+    auto load_stage = [&](uint32_t i) {
+      const uint32_t to = ring + (i % kWStages) * L::kStage;
+#pragma unroll
+      for (uint32_t j = 0; j < 4; j++) {
+        const uint32_t dst = to + (qch >> 3) * 8192 + swz((qrow + 16 * j) * 128 + (qch & 7) * 16);
+        const uint16_t* p = qsrc + (int64_t)(tq[j] >= 0 ? tq[j] : 0) * lds;
+        fill8(dst, p, tq[j] >= 0 ? qn : 0, vec);
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < PN; j++) {
+        const uint32_t r = prow + span * j;
+        if (r < 64)
+          cp16z(to + L::kQ + swz(r * (RP * 2) + pch * 16),
+                pr + (int64_t)(tp[j] >= 0 ? tp[j] : 0) * RP + pch * 8, tp[j] >= 0);
+      }
+    };
+    float acc[MF][RP / 8][4];
+#pragma unroll
+    for (int m = 0; m < MF; m++)
+#pragma unroll
+      for (int j = 0; j < RP / 8; j++)
+        acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.f;
+    __syncthreads();   // the piece before is done with the ring
+    load_rows(0);
+    for (uint32_t i = 0; i < kWStages - 1; i++) {
+      if (i < mine) load_stage(i);
+      if (i + 1 < mine) load_rows(i + 1);
+      cp_commit();
     }
-    constexpr uint32_t per = RP / 8;
+    for (uint32_t i = 0; i < mine; i++) {
+      cp_wait<kWStages - 2>();
+      __syncthreads();
+      if (i + kWStages - 1 < mine) load_stage(i + kWStages - 1);
+      if (i + kWStages < mine) load_rows(i + kWStages);
+      cp_commit();
+      const uint32_t qs = ring + (i % kWStages) * L::kStage, ps = qs + L::kQ;
 #pragma unroll
-    for (uint32_t s = tid; s < 64 * per; s += kThreads) {
-      const uint32_t row = s / per, ch = s % per;
-      const int32_t t = t0 + (int32_t)row < end ? P.perm[t0 + row] : -1;
-      fill8(at + L::kQ + swz(row * (RP * 2) + ch * 16), pr + (int64_t)t * RP + ch * 8,
-            t >= 0 ? 8 : 0, true);
+      for (uint32_t kk = 0; kk < 4 / MF; kk++) {   // 16 rows of the batch
+        const uint32_t kt = th * 2 + kk;
+        uint32_t a[MF][4];
+#pragma unroll
+        for (int m = 0; m < MF; m++) {
+          const uint32_t f = (fw * MF + m) * 16;
+          ldsm4t(a[m], qs + (f >> 6) * 8192 +
+                           swz((kt * 16 + (lane >> 4) * 8 + (lane & 7)) * 128 + (f & 63) * 2 +
+                               ((lane >> 3) & 1) * 16));
+        }
+#pragma unroll
+        for (int j = 0; j < RP / 16; j++) {
+          uint32_t b[4];
+          ldsm4t(b, ps + swz((kt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * (RP * 2) + j * 32 +
+                             (lane >> 4) * 16));
+#pragma unroll
+          for (int m = 0; m < MF; m++) {
+            mma16816(acc[m][2 * j], a[m][0], a[m][1], a[m][2], a[m][3], b[0], b[1]);
+            mma16816(acc[m][2 * j + 1], a[m][0], a[m][1], a[m][2], a[m][3], b[2], b[3]);
+          }
+        }
+      }
     }
-  };
-  float acc[RP / 8][4];
+    cp_wait<0>();
 #pragma unroll
-  for (int j = 0; j < RP / 8; j++) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-  for (uint32_t i = 0; i < kWStages - 1; i++) {
-    if (i < mine) load_stage(i);
-    cp_commit();
-  }
-  for (uint32_t i = 0; i < mine; i++) {
-    cp_wait<kWStages - 2>();
+    for (int pass = 0; pass < MF; pass++) {   // join the two halves of every stage
+      __syncthreads();
+      if ((int)th == pass) {
+#pragma unroll
+        for (int m = 0; m < MF; m++)
+#pragma unroll
+          for (int j = 0; j < RP / 8; j++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              float2* d = reinterpret_cast<float2*>(
+                  part + ((fw * MF + m) * 16 + h * 8 + g) * L::kLd + j * 8 + 2 * q);
+              const float2 v = make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+              *d = pass == 0 ? v : make_float2(d->x + v.x, d->y + v.y);
+            }
+      }
+    }
     __syncthreads();
-    if (i + kWStages - 1 < mine) load_stage(i + kWStages - 1);
-    cp_commit();
-    const uint32_t qs = ring + (i % kWStages) * L::kStage + (warp >> 2) * 8192;
-    const uint32_t ps = ring + (i % kWStages) * L::kStage + L::kQ;
-#pragma unroll
-    for (uint32_t kt = 0; kt < 4; kt++) {   // 16 rows of the batch
-      uint32_t a[4];
-      ldsm4t(a, qs + swz((kt * 16 + (lane >> 4) * 8 + (lane & 7)) * 128 + (warp & 3) * 32 +
-                         ((lane >> 3) & 1) * 16));
-#pragma unroll
-      for (int j = 0; j < RP / 16; j++) {
-        uint32_t b[4];
-        ldsm4t(b, ps + swz((kt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * (RP * 2) + j * 32 +
-                           (lane >> 4) * 16));
-        mma16816(acc[2 * j], a[0], a[1], a[2], a[3], b[0], b[1]);
-        mma16816(acc[2 * j + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
+    bool write = true;
+    uint32_t b0 = 0, b1 = 0;   // the blocks that share the piece, when several do
+    if (mine < Q.stages) {
+      float* const to = P.sums + (2 * (uint64_t)blockIdx.x + (Q.at != s_begin)) * (kFeat * RP);
+      for (uint32_t e = tid * 2; e < kFeat * RP; e += kThreads * 2)
+        __stcg(reinterpret_cast<float2*>(to + e),
+               *reinterpret_cast<const float2*>(part + e / RP * L::kLd + e % RP));
+      // the blocks of the piece's first and last stage
+      const uint64_t p_last = Q.begin + Q.stages - 1;
+      b0 = (uint32_t)(Q.begin * sh.G / sh.all);
+      while (sh.begin(b0 + 1) <= Q.begin) b0++;
+      b1 = (uint32_t)(p_last * sh.G / sh.all);
+      while (sh.begin(b1 + 1) <= p_last) b1++;
+      __threadfence();
+      __syncthreads();
+      if (tid == 0)
+        sh_last = atomicInc(P.counters + (uint64_t)Q.adapter * slices + Q.slice, b1 - b0) == b1 - b0;
+      __syncthreads();
+      write = sh_last != 0;
+      __threadfence();
+    }
+    if (write) {
+      for (uint32_t e = tid; e < kFeat * RP; e += kThreads) {
+        // neighbours in memory to neighbouring threads: along the features for dA, the rank for dB
+        const uint32_t fl = down ? e % kFeat : e / RP, r = down ? e / kFeat : e % RP;
+        if (f0 + fl >= F || r >= A.rank) continue;
+        float v = 0.f;
+        if (mine == Q.stages) {
+          v = part[fl * L::kLd + r];
+        } else {
+          for (uint32_t b = b0; b <= b1; b++)   // a block's first piece, or its last
+            v += __ldcg(P.sums + (2 * (uint64_t)b + (sh.begin(b) < Q.begin)) * (kFeat * RP) + fl * RP + r);
+        }
+        if (down)
+          put_grad(A.gdown, (uint64_t)r * A.ld_gdown + f0 + fl, v, P.grad_f32, P.accumulate);
+        else
+          put_grad(A.gup, (uint64_t)(f0 + fl) * A.ld_gup + r, v, P.grad_f32, P.accumulate);
       }
     }
   }
-  cp_wait<0>();
-  __syncthreads();
-  float* const part = reinterpret_cast<float*>(smem);   // [feature][RP]
-#pragma unroll
-  for (int j = 0; j < RP / 8; j++) {
-    float* d = part + (warp * 16 + g) * RP + j * 8 + 2 * q;
-    *reinterpret_cast<float2*>(d) = make_float2(acc[j][0], acc[j][1]);
-    *reinterpret_cast<float2*>(d + 8 * RP) = make_float2(acc[j][2], acc[j][3]);
-  }
-  cluster.sync();
-  const DevAdapter A = P.table[blockIdx.y];
-  const uint32_t feats = kFeat / C;
-  for (uint32_t e = tid; e < feats * RP; e += kThreads) {
-    // neighbours in memory to neighbouring threads: along the features for dA, the rank for dB
-    const uint32_t fl = c * feats + (down ? e % feats : e / RP), r = down ? e / feats : e % RP;
-    if (f0 + fl >= F || r >= A.rank) continue;
-    float s = 0.f;
-    for (uint32_t b = 0; b < C; b++) s += cluster.map_shared_rank(part, b)[fl * RP + r];
-    if (down)
-      put_grad(A.gdown, (uint64_t)r * A.ld_gdown + f0 + fl, s, P.grad_f32, P.accumulate);
-    else
-      put_grad(A.gup, (uint64_t)(f0 + fl) * A.ld_gup + r, s, P.grad_f32, P.accumulate);
-  }
-  cluster.sync();   // the others may still read `part`
 }
 
 // ------------------------------------------------------------------------------- host side
-template <class F, class Args>
-int launch_clusters(F* kernel, uint32_t grid_x, uint32_t grid_y, uint32_t cluster, uint32_t smem,
-                    const Args& args, cudaStream_t s) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return BD_ERR_CUDA;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid_x * cluster, grid_y, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return check(cudaLaunchKernelEx(&cfg, kernel, args));
-}
-
 template <int RP>
-int launch_apply(bool small, uint32_t tiles, uint32_t cluster, const ApplyArgs& P, cudaStream_t s) {
-  if (small)
-    return launch_clusters(k_apply16<RP>, tiles, 1, cluster,
-                           (9 * 16 * RP) * 4 + 16 * (RP + 8) * 2, P, s);
-  return launch_clusters(k_apply64<RP>, tiles, 1, cluster, Apply64<RP>::kSmem, P, s);
+cudaError_t launch_apply(bool small, bool vec, uint32_t tiles, uint32_t C, const ApplyArgs& P,
+                         cudaStream_t s) {
+  if (small) return launch(k_apply16<RP>, dim3(tiles * C), kThreads, Apply16<RP>::kSmem, C, s, P);
+  return launch(vec ? k_apply64<RP, true> : k_apply64<RP, false>, dim3(tiles * C), kThreads,
+                Apply64<RP>::kSmem, C, s, P);
+}
+template <int RP>
+cudaError_t launch_expand(uint32_t grid, const ApplyArgs& P, cudaStream_t s) {
+  return launch(k_expand<RP>, dim3(grid), kThreads, Expand<RP>::kSmem, 1, s, P);
+}
+template <int RP>
+cudaError_t launch_wgrad(uint32_t grid, const WgradArgs& P, cudaStream_t s) {
+  return launch(k_wgrad<RP>, dim3(grid), kThreads, Wgrad<RP>::kSmem, 1, s, P);
 }
 
-// Blocks of a cluster that share a piece of work: enough for about two blocks per SM.
-uint32_t cluster_for(uint64_t pieces, int sms) {
+// Blocks of a cluster that share a tile: as many as keep all blocks on the SMs at once (`slots`).
+// Above that a second round waits for the first: 64 tiles of 64 rows with 4 blocks each take 25 us,
+// with 8 each 29 us (4096 x 4096, rank 16).
+uint32_t cluster_for(uint64_t tiles, uint64_t slots) {
   uint32_t c = 1;
-  while (c < kMaxCluster && pieces * c < 2 * (uint64_t)sms) c *= 2;
+  while (c < kMaxCluster && tiles * c * 2 <= slots) c *= 2;
   return c;
 }
 
-int apply(uint32_t RP, uint32_t rows, uint32_t k, const void* const* tiles, const int32_t* ntiles,
-          ApplyArgs& P, int sms, cudaStream_t s) {
+// Low and the second product are two launches from this many bytes of rows on.  One launch keeps
+// low on the SM and is ahead below (1024 rows of 4096 x 4096, rank 16: 10.7 us against 14.9 us);
+// two have better kernels for each half (16384 rows: 84 us against 75 us; of rank 64 and 4096 x
+// 11008: 193 us against 171 us).
+constexpr uint64_t kSplitBytes = 200000000;
+uint64_t row_bytes(uint32_t K, uint32_t N) { return 2 * ((uint64_t)K + 2 * (uint64_t)N); }
+
+uint32_t tile_bound(uint32_t rows, uint32_t k, uint32_t high) {
+  const uint64_t b = (uint64_t)rows / high + k;
+  return (uint32_t)(b < rows ? b : rows);
+}
+
+int apply(uint32_t RP, const bo_adapter_rows* R, ApplyArgs& P, int sms, cudaStream_t s) {
+  const uint32_t rows = R->rows, k = R->k;
+  P.perm = R->d_perm;
+  P.status = R->d_status;
+  const bool vec = P.vec_x && P.vec_factors && (!P.y || P.vec_y);
+  if (vec && P.low && rows * row_bytes(P.K, P.N) >= kSplitBytes) {
+    const uint32_t tiles = tile_bound(rows, k, 128);
+    P.tiles = static_cast<const Tile*>(R->d_tiles[2]);
+    P.ntiles = R->d_ntiles + 2;
+    const int rc = check(tc_low(RP, tiles, cluster_for(tiles, sms), P, s));
+    if (rc || !P.y) return rc;
+    P.tiles = static_cast<const Tile*>(R->d_tiles[1]);
+    P.ntiles = R->d_ntiles + 1;
+    const uint32_t grid = 2 * sms;
+    switch (RP) {
+      case 16: return check(launch_expand<16>(grid, P, s));
+      case 32: return check(launch_expand<32>(grid, P, s));
+      case 64: return check(launch_expand<64>(grid, P, s));
+      default: return check(launch_expand<128>(grid, P, s));
+    }
+  }
   // Tiles of 16 rows while the adapters have few rows each: a tile of 64 would be mostly empty.
   const bool small = rows <= 128 || rows / k < 24;
-  const uint64_t bound0 = (uint64_t)rows / (small ? 16 : 64) + k;
-  const uint32_t bound = (uint32_t)(bound0 < rows ? bound0 : rows);
-  P.tiles = static_cast<const Tile*>(tiles[small ? 0 : 1]);
-  P.ntiles = ntiles + (small ? 0 : 1);
-  const uint32_t cluster = cluster_for(bound, sms);
+  const uint32_t tiles = tile_bound(rows, k, small ? 16 : 64);
+  P.tiles = static_cast<const Tile*>(R->d_tiles[small ? 0 : 1]);
+  P.ntiles = R->d_ntiles + (small ? 0 : 1);
+  const uint32_t C = cluster_for(tiles, (uint64_t)sms * (small ? 4 : RP == 128 ? 1 : 2));
   switch (RP) {
-    case 16: return launch_apply<16>(small, bound, cluster, P, s);
-    case 32: return launch_apply<32>(small, bound, cluster, P, s);
-    case 64: return launch_apply<64>(small, bound, cluster, P, s);
-    default: return launch_apply<128>(small, bound, cluster, P, s);
+    case 16: return check(launch_apply<16>(small, vec, tiles, C, P, s));
+    case 32: return check(launch_apply<32>(small, vec, tiles, C, P, s));
+    case 64: return check(launch_apply<64>(small, vec, tiles, C, P, s));
+    default: return check(launch_apply<128>(small, vec, tiles, C, P, s));
   }
 }
 
 struct RowsLayout {
-  uint64_t counts, offsets, ntiles, perm, tiles16, tiles64, total;
+  uint64_t counts, offsets, blocks, ntiles, perm, tiles16, tiles64, tiles128, total;
 };
 bool rows_layout(uint32_t rows, uint32_t k, RowsLayout& L) {
   if (k == 0 || k > BO_ADAPTER_MAX_COUNT || rows > BO_ADAPTER_MAX_ROWS) return false;
@@ -844,10 +1176,12 @@ bool rows_layout(uint32_t rows, uint32_t k, RowsLayout& L) {
   };
   L.counts = take((uint64_t)k * 4);
   L.offsets = take(((uint64_t)k + 1) * 4);
-  L.ntiles = take(8);
+  L.blocks = take(((uint64_t)k + 1) * 4);
+  L.ntiles = take(12);
   L.perm = take((uint64_t)rows * 4);
   L.tiles16 = take(((uint64_t)rows / 16 + k) * sizeof(Tile));
   L.tiles64 = take(((uint64_t)rows / 64 + k) * sizeof(Tile));
+  L.tiles128 = take(((uint64_t)rows / 128 + k) * sizeof(Tile));
   L.total = off;
   return true;
 }
@@ -857,7 +1191,7 @@ bool valid(const bo_adapter_set* s) {
          (s->rank == 16 || s->rank == 32 || s->rank == 64 || s->rank == 128);
 }
 bool valid(const bo_adapter_rows* r) {
-  return r && r->d_perm && r->d_offsets && r->d_tiles[0] && r->d_tiles[1] && r->d_ntiles;
+  return r && r->d_perm && r->d_offsets && r->d_blocks && r->d_tiles[0] && r->d_tiles[1] && r->d_tiles[2] && r->d_ntiles;
 }
 bool wide(const void* p, uint64_t ld, uint64_t width) {
   return aligned(p, 16) && ld % 8 == 0 && width % 8 == 0;
@@ -868,14 +1202,20 @@ uint64_t extent(uint64_t rows, uint64_t ld, uint64_t width) {
 }
 uint64_t up8(uint64_t x) { return (x + 7) / 8 * 8; }
 
+uint32_t wgrad_slices(const bo_adapter_set* set) {
+  return (set->hidden + kFeat - 1) / kFeat + (set->out + kFeat - 1) / kFeat;
+}
+constexpr uint32_t kMaxSms = 256;   // (that a workspace is sized for)
 struct BackwardLayout {
-  uint64_t dlow, table, buf, total;
+  uint64_t dlow, table, counters, sums, buf, total;
 };
 BackwardLayout backward_layout(const bo_adapter_set* set, uint32_t rows) {
   BackwardLayout L;
   L.dlow = 0;
   L.table = up((uint64_t)rows * set->rank * 2, 256);
-  L.buf = L.table + up((uint64_t)set->k * sizeof(DevAdapter), 256);
+  L.counters = L.table + up((uint64_t)set->k * sizeof(DevAdapter), 256);
+  L.sums = L.counters + up((uint64_t)set->k * wgrad_slices(set) * 4, 256);
+  L.buf = L.sums + (uint64_t)2 * 2 * kMaxSms * kFeat * set->rank * 4;
   L.total = L.buf + up((uint64_t)set->k * set->rank * ((uint64_t)set->hidden + up8(set->out)) * 2, 256);
   return L;
 }
@@ -903,7 +1243,7 @@ int bo_adapter_set_init(const bo_adapter* h_items, uint32_t k, uint32_t hidden, 
   if (!dev) return BD_ERR_INVALID_ARG;
   const uintptr_t gsize = grad_dtype == BO_FP32 ? 4 : 2;
   uint32_t most = 1;
-  bool grads = true;
+  bool grads = true, all_wide = true;
   for (uint32_t i = 0; i < k; i++) {
     const bo_adapter& a = h_items[i];
     if (!a.d_down || !a.d_up || !aligned(a.d_down, 2) || !aligned(a.d_up, 2) || a.rank < 1 ||
@@ -929,18 +1269,22 @@ int bo_adapter_set_init(const bo_adapter* h_items, uint32_t k, uint32_t hidden, 
     d.scale = a.scale;
     d.vec_down = wide(a.d_down, a.ld_down, hidden);
     d.vec_up = wide(a.d_up, a.ld_up, a.rank);
+    d.vec_gup = a.d_grad_up && wide(a.d_grad_up, a.ld_grad_up, a.rank);
+    d.pad[0] = d.pad[1] = d.pad[2] = 0;
+    if (!d.vec_down || !d.vec_up) all_wide = false;
     if (a.rank > most) most = a.rank;
   }
   const int rc = check(upload(dev.get(), (uint64_t)k * sizeof(DevAdapter), d_set,
                               static_cast<cudaStream_t>(stream)));
   if (rc) return rc;
+  h_out->rank = most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 ? 64 : 128;
   h_out->d_table = d_set;
   h_out->k = k;
   h_out->hidden = hidden;
   h_out->out = out;
-  h_out->rank = most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 ? 64 : 128;
   h_out->grad_dtype = grad_dtype;
   h_out->has_grads = grads;
+  h_out->wide = all_wide;
   return BD_OK;
 }
 
@@ -960,20 +1304,25 @@ int bo_adapter_rows_init(const int32_t* d_index, uint32_t rows, uint32_t k, void
   uint8_t* p = static_cast<uint8_t*>(d_rows);
   int32_t* counts = reinterpret_cast<int32_t*>(p + L.counts);
   int32_t* offsets = reinterpret_cast<int32_t*>(p + L.offsets);
+  int32_t* blocks = reinterpret_cast<int32_t*>(p + L.blocks);
   int32_t* ntiles = reinterpret_cast<int32_t*>(p + L.ntiles);
   int32_t* perm = reinterpret_cast<int32_t*>(p + L.perm);
   Tile* t16 = reinterpret_cast<Tile*>(p + L.tiles16);
   Tile* t64 = reinterpret_cast<Tile*>(p + L.tiles64);
+  Tile* t128 = reinterpret_cast<Tile*>(p + L.tiles128);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  k_rows_count<<<k, kThreads, 0, s>>>(d_index, rows, k, counts, d_status);
-  int rc = check(cudaGetLastError());
+  int rc = check(launch(k_rows_count, dim3(k), kThreads, 0, 1, s, d_index, rows, k, counts, d_status));
   if (rc) return rc;
-  k_rows_place<<<k, kThreads, 0, s>>>(d_index, rows, k, counts, perm, offsets, t16, t64, ntiles);
-  if ((rc = check(cudaGetLastError()))) return rc;
+  rc = check(launch(k_rows_place, dim3(k), kThreads, 0, 1, s, d_index, rows, k, counts, perm, offsets,
+                    t16, t64, t128, ntiles, blocks));
+  if (rc) return rc;
   h_out->d_perm = perm;
   h_out->d_offsets = offsets;
+  h_out->d_blocks = blocks;
   h_out->d_tiles[0] = t16;
   h_out->d_tiles[1] = t64;
+  h_out->d_tiles[2] = t128;
+  h_out->d_status = d_status;
   h_out->d_ntiles = ntiles;
   h_out->rows = rows;
   h_out->k = k;
@@ -985,7 +1334,8 @@ int bo_adapter_forward(const bo_adapter_set* set, const bo_adapter_rows* rows, c
   if (!valid(set) || !valid(rows) || rows->k != set->k) return BD_ERR_INVALID_ARG;
   if (rows->rows == 0) return BD_OK;
   if (!d_x || !d_y || !aligned(d_x, 2) || !aligned(d_y, 2) || ldx < set->hidden ||
-      ldy < set->out || ldx > (1ull << 40) || ldy > (1ull << 40) || !aligned(d_low, 16))
+      ldy < set->out || ldx > (1ull << 40) || ldy > (1ull << 40) || !aligned(d_low, 16) ||
+      (!d_low && rows->rows >= bo_adapter_low_rows(set)))
     return BD_ERR_INVALID_ARG;
   const uint64_t yb = extent(rows->rows, ldy, set->out);
   const uint64_t lb = d_low ? (uint64_t)rows->rows * set->rank * 2 : 0;
@@ -996,7 +1346,6 @@ int bo_adapter_forward(const bo_adapter_set* set, const bo_adapter_rows* rows, c
   if (sms <= 0) return BD_ERR_CUDA;
   ApplyArgs P = {};
   P.table = static_cast<const DevAdapter*>(set->d_table);
-  P.perm = rows->d_perm;
   P.x = d_x;
   P.ldx = ldx;
   P.y = d_y;
@@ -1006,8 +1355,8 @@ int bo_adapter_forward(const bo_adapter_set* set, const bo_adapter_rows* rows, c
   P.N = set->out;
   P.vec_x = wide(d_x, ldx, set->hidden);
   P.vec_y = wide(d_y, ldy, set->out);
-  return apply(set->rank, rows->rows, set->k, rows->d_tiles, rows->d_ntiles, P, sms,
-               static_cast<cudaStream_t>(stream));
+  P.vec_factors = set->wide;
+  return apply(set->rank, rows, P, sms, static_cast<cudaStream_t>(stream));
 }
 
 uint64_t bo_adapter_backward_workspace_size(const bo_adapter_set* set, uint32_t rows) {
@@ -1042,17 +1391,17 @@ int bo_adapter_backward(const bo_adapter_set* set, const bo_adapter_rows* rows,
   DevAdapter* swapped = reinterpret_cast<DevAdapter*>(w + L.table);
   uint16_t* buf = reinterpret_cast<uint16_t*>(w + L.buf);
   const uint32_t out8 = (uint32_t)up8(set->out);
-  int rc;
+  uint32_t* counters = reinterpret_cast<uint32_t*>(w + L.counters);
+  const uint32_t slices = wgrad_slices(set);
+  const dim3 turn_grid((set->hidden + kTF - 1) / kTF + (out8 + kTF - 1) / kTF, set->k);
+  auto* turn = set->rank == 16 ? k_transpose<16> : set->rank == 32 ? k_transpose<32>
+               : set->rank == 64 ? k_transpose<64> : k_transpose<128>;
+  int rc = check(launch(turn, turn_grid, kThreads, 0, 1, s, static_cast<const DevAdapter*>(set->d_table),
+                        set->hidden, set->out, out8, buf, swapped, counters, slices));
+  if (rc) return rc;
   if (rows->rows > 0) {
-    const uint32_t pieces = (set->hidden + 31) / 32 + (out8 + 31) / 32;
-    const uint32_t most = (uint32_t)((uint64_t)sms * 8 / set->k + 1);
-    k_transpose<<<dim3(pieces < most ? pieces : most, set->k), kThreads, 0, s>>>(
-        static_cast<const DevAdapter*>(set->d_table), set->hidden, set->out, set->rank, out8, buf,
-        swapped);
-    if ((rc = check(cudaGetLastError()))) return rc;
     ApplyArgs P = {};
     P.table = swapped;
-    P.perm = rows->d_perm;
     P.x = d_dy;
     P.ldx = lddy;
     P.y = d_dx;
@@ -1062,8 +1411,8 @@ int bo_adapter_backward(const bo_adapter_set* set, const bo_adapter_rows* rows,
     P.N = set->hidden;
     P.vec_x = wide(d_dy, lddy, set->out);
     P.vec_y = d_dx && wide(d_dx, lddx, set->hidden);
-    if ((rc = apply(set->rank, rows->rows, set->k, rows->d_tiles, rows->d_ntiles, P, sms, s)))
-      return rc;
+    P.vec_factors = 1;
+    if ((rc = apply(set->rank, rows, P, sms, s))) return rc;
   }
   if (!set->has_grads) return BD_OK;
   WgradArgs G = {};
@@ -1076,20 +1425,37 @@ int bo_adapter_backward(const bo_adapter_set* set, const bo_adapter_rows* rows,
   G.lddy = lddy;
   G.low = d_low;
   G.dlow = dlow;
+  if (rows->rows == 0) G.x = G.dy = G.low = dlow;   // (nothing is read, but pointers are formed)
   G.hidden = set->hidden;
   G.out = set->out;
   G.vec_x = wide(d_x, ldx, set->hidden);
   G.vec_dy = wide(d_dy, lddy, set->out);
   G.grad_f32 = set->grad_dtype == BO_FP32;
   G.accumulate = accumulate != 0;
-  const uint32_t slices = (set->hidden + kFeat - 1) / kFeat + (set->out + kFeat - 1) / kFeat;
-  const uint32_t cluster = cluster_for((uint64_t)slices * set->k, sms);
+  G.blocks = rows->d_blocks;
+  G.sums = reinterpret_cast<float*>(w + L.sums);
+  G.counters = counters;
+  G.k = set->k;
+  const bool vec = G.vec_x && G.vec_dy;
+  G.status = rows->d_status;
+  const uint64_t stages = ((uint64_t)rows->rows / 64 + set->k) * slices;   // at most
+  const uint64_t slots = sms < (int)kMaxSms ? sms : (int)kMaxSms;
+  if (vec && rows->rows > 0)   // a block an SM
+    return check(tc_wgrad(set->rank, (uint32_t)(stages < slots ? stages : slots), G, s));
+  const uint32_t grid = (uint32_t)(stages < 2 * slots ? stages : 2 * slots);
   switch (set->rank) {
-    case 16: return launch_clusters(k_wgrad<16>, slices, set->k, cluster, Wgrad<16>::kSmem, G, s);
-    case 32: return launch_clusters(k_wgrad<32>, slices, set->k, cluster, Wgrad<32>::kSmem, G, s);
-    case 64: return launch_clusters(k_wgrad<64>, slices, set->k, cluster, Wgrad<64>::kSmem, G, s);
-    default: return launch_clusters(k_wgrad<128>, slices, set->k, cluster, Wgrad<128>::kSmem, G, s);
+    case 16: return check(launch_wgrad<16>(grid, G, s));
+    case 32: return check(launch_wgrad<32>(grid, G, s));
+    case 64: return check(launch_wgrad<64>(grid, G, s));
+    default: return check(launch_wgrad<128>(grid, G, s));
   }
+}
+
+uint32_t bo_adapter_low_rows(const bo_adapter_set* set) {
+  if (!valid(set)) return 0;
+  const uint64_t b = row_bytes(set->hidden, set->out);
+  const uint64_t n = (kSplitBytes + b - 1) / b;
+  return (uint32_t)(n < BO_ADAPTER_MAX_ROWS ? n : BO_ADAPTER_MAX_ROWS);
 }
 
 }  // extern "C"

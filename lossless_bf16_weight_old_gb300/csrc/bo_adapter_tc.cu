@@ -1,0 +1,612 @@
+// bo_adapter_tc.cu -- the adapters' long sums on the fifth-generation tensor cores: low = s A x
+// over 128 rows at a time, and the weight gradients' sums over an adapter's rows.
+//
+// Both are sums of thousands of terms into a narrow result, and what they cost is reading x (or
+// dy) once.  With mma.sync the warps spend that time on fragments and barriers: 300 instructions
+// a warp and stage, two thirds of the time waiting for one another.  Here eight warps do nothing
+// but copy rows into a ring of stages (cp.async: 16 bytes of any row, so that rows need not be
+// neighbours in the batch), laid out as the tensor cores read them, and one thread issues the
+// products (tcgen05.mma, the sums in tensor memory).  No warp waits for another but through the
+// stages' barriers: with one barrier for the block, what the copies, the products and the waits
+// cost adds up (0.4 us a stage instead of 0.25).
+//
+// Every wait is bounded (about two seconds); past its bound a block sets the status, lets its own
+// copies land and ends.
+#include <cooperative_groups.h>
+
+#include "bo_adapter.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace bo {
+namespace {
+
+
+// ------------------------------------------------------------------------------------ barriers
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Waits until the barrier's phase of this parity is over; false: it was not within two seconds.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; i++) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((i & 127) == 0) {
+      uint64_t now;
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > 2000000000ull) return false;
+    }
+  }
+}
+// The same for a warp: one lane looks (each lane's look is an access of its own).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  int32_t ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = bar_wait(bar, parity);
+  return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// ... and makes what this thread copied visible to the tensor cores
+__device__ __forceinline__ void copies_to_tensor() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// ------------------------------------------------------------------------------- tensor cores
+__device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst),
+               "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+               : "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// 16 columns of this warp's 32 lanes, there after tmem_wait()
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Shared-memory matrix descriptors: address, the two strides between 8-row (or 8-step) groups and
+// between swizzle-wide blocks, and the swizzle (2: 128 bytes, 4: 64, 6: 32).
+__device__ __forceinline__ uint64_t matrix(uint32_t addr, uint32_t lead, uint32_t stride,
+                                           uint32_t swizzle) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)((lead >> 4) & 0x3FFF) << 16 |
+         (uint64_t)((stride >> 4) & 0x3FFF) << 32 | 1ull << 46 | (uint64_t)swizzle << 61;
+}
+// BF16 x BF16 into FP32, M = 128; mn: both operands run along their rows / columns (not the sum)
+__host__ __device__ constexpr uint32_t instruction(uint32_t n, bool mn) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (mn ? 3u << 15 : 0u) | (n >> 3) << 17 | (128u >> 4) << 24;
+}
+
+constexpr uint32_t kMaxStages = 8;
+constexpr uint32_t kRingBudget = 200 * 1024;   // one block an SM
+constexpr uint32_t kCopyWarps = 8;
+
+struct alignas(8) Control {
+  uint64_t full[kMaxStages], freed[kMaxStages], done[2], drained[2];
+  uint32_t tmem, last, pad[2];
+};
+
+// A product waits for the one before it into the same sums (about 180 cycles, whatever its width),
+// so the steps of a stage have sums of their own, as far as `sets` of them fit in tensor memory.
+template <int RP, int SETS>
+struct Sums {
+  static constexpr uint32_t kN = 4 * RP * SETS <= 512 ? 4 : 2;
+  static constexpr uint32_t kCols = RP * kN;
+  static constexpr uint32_t kAlloc = kCols * SETS;
+  // sixteen columns, joined
+  static __device__ __forceinline__ void load(uint32_t from, uint32_t col, float (&v)[16]) {
+    uint32_t w[kN][16];
+#pragma unroll
+    for (uint32_t z = 0; z < kN; z++) tmem_ld16(from + z * RP + col, w[z]);
+    tmem_wait();
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      v[i] = __uint_as_float(w[0][i]);
+#pragma unroll
+      for (uint32_t z = 1; z < kN; z++) v[i] += __uint_as_float(w[z][i]);
+    }
+  }
+};
+
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+  return p + ((1024 - (smem_addr(p) & 1023)) & 1023);
+}
+
+// Barriers and tensor memory of a block; every thread calls it.
+__device__ __forceinline__ uint32_t begin_block(Control* ctl, uint32_t stages, uint32_t cols) {
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < stages; s++) {
+      bar_init(smem_addr(&ctl->full[s]), kCopyWarps);
+      bar_init(smem_addr(&ctl->freed[s]), 1);
+    }
+    for (uint32_t b = 0; b < 2; b++) {
+      bar_init(smem_addr(&ctl->done[b]), 1);
+      bar_init(smem_addr(&ctl->drained[b]), 128);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (threadIdx.x < 32) tmem_alloc(smem_addr(&ctl->tmem), cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  return ctl->tmem;
+}
+__device__ __forceinline__ void end_block(uint32_t tmem, uint32_t cols) {
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x < 32) tmem_free(tmem, cols);
+}
+
+// A copying warp's turn at stage i: waits for its place (of the ring's S) to be free ...
+template <uint32_t S>
+__device__ __forceinline__ bool stage_free(Control* ctl, uint32_t i) {
+  return i < S || warp_wait(smem_addr(&ctl->freed[i % S]), (i / S + 1) & 1);
+}
+// ... and, with the copies of stage i issued (or none left), hands on the one D - 1 before.
+template <uint32_t S, uint32_t D>
+__device__ __forceinline__ void stage_issued(Control* ctl, uint32_t i) {
+  copies_commit();
+  if (i + 1 >= D) {
+    copies_wait<D - 1>();
+    copies_to_tensor();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) bar_arrive(smem_addr(&ctl->full[(i + 1 - D) % S]));
+  }
+}
+
+// ---------------------------------------------------------------------- low = s A x, 128 rows
+// A stage is 64 values of the sum: 128 rows of x (16 KB) and the factor's rows.  The blocks of a
+// cluster split the sum and join through distributed shared memory in a fixed order.
+template <int RP>
+struct Low {
+  static constexpr uint32_t kThreads = 288;
+  static constexpr uint32_t kX = 128 * 128, kStage = kX + RP * 128;
+  static constexpr uint32_t kS = kRingBudget / kStage < kMaxStages ? kRingBudget / kStage : kMaxStages;
+  static constexpr uint32_t kLd = RP + 4;                            // of the sums in shared memory
+  static constexpr uint32_t kPart = 128 * kLd * 4;                   // over the ring
+  static constexpr uint32_t kRing = kS * kStage > kPart ? kS * kStage : kPart;
+  static constexpr uint32_t kSmem = kRing + sizeof(Control) + 1024;
+};
+
+template <int RP>
+__global__ void __launch_bounds__(288, 1) k_low(const ApplyArgs P) {
+  using L = Low<RP>;
+  using M = Sums<RP, 1>;
+  constexpr uint32_t S = L::kS, D = S - 2;   // stages, and how many are on their way
+  extern __shared__ uint8_t raw[];
+  uint8_t* const smem = align1024(raw);
+  const uint32_t ring = smem_addr(smem);
+  float* const part = reinterpret_cast<float*>(smem);
+  Control* const ctl = reinterpret_cast<Control*>(smem + L::kRing);
+  const cg::cluster_group cluster = cg::this_cluster();
+  const uint32_t C = cluster.num_blocks(), c = cluster.block_rank();
+  const uint32_t tile = blockIdx.x / C, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  after_previous();
+  const Tile T = P.tiles[tile];              // (of the table's capacity, so within it)
+  if (tile >= (uint32_t)*P.ntiles) return;   // (the whole cluster)
+  const DevAdapter A = P.table[T.adapter];
+  const int32_t rank = (int32_t)A.rank;
+  const uint32_t all = (P.K + 63) / 64;
+  const uint32_t mine = all > c ? (all - c + C - 1) / C : 0;
+  const uint32_t tmem = begin_block(ctl, S, M::kAlloc);
+  bool ok = true;
+
+  if (warp < kCopyWarps) {
+    // a thread's 16-byte slots of a stage: four rows of x, and of the factor's rows
+    const uint32_t ch = tid & 7, row0 = tid >> 3;
+    const uint16_t* xp[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {   // (past the tile's end: its first row, whose sum is not used)
+      const int32_t t = (int32_t)row0 + 32 * j;
+      xp[j] = P.x + (int64_t)P.perm[T.start + (t < T.count ? t : 0)] * P.ldx + ch * 8;
+    }
+    const uint32_t at = swz(row0 * 128 + ch * 16);
+    for (uint32_t i = 0; i < mine + D - 1; i++) {
+      if (i < mine) {
+        if (!(ok = stage_free<S>(ctl, i))) break;
+        const uint32_t k = (c + i * C) * 64, to = ring + i % S * L::kStage + at;
+        const bool there = k + ch * 8 < P.K;
+#pragma unroll
+        for (int j = 0; j < 4; j++) cp16z(to + j * 4096, xp[j] + (there ? k : 0), there);
+#pragma unroll
+        for (uint32_t j = 0; j < RP; j += 32) {
+          const uint32_t row = row0 + j;
+          if (RP < 32 && row >= RP) break;
+          const bool w = there && (int32_t)row < rank;
+          cp16z(to + L::kX + j * 128, A.down + (w ? (uint64_t)row * A.ld_down + k + ch * 8 : 0), w);
+        }
+      }
+      stage_issued<S, D>(ctl, i);
+    }
+    copies_wait<0>();
+  } else {
+    if (lane == 0) {
+      for (uint32_t i = 0; i < mine; i++) {
+        const uint32_t s = i % S;
+        if (!(ok = bar_wait(smem_addr(&ctl->full[s]), (i / S) & 1))) break;
+        tc_fence_after();
+        const uint64_t a = matrix(ring + s * L::kStage, 16, 1024, 2);
+        const uint64_t b = matrix(ring + s * L::kStage + L::kX, 16, 1024, 2);
+#pragma unroll
+        for (uint32_t k = 0; k < 4; k++)   // 16 values, 32 bytes, a step
+          tc_mma(tmem + k % M::kN * RP, a + 2 * k, b + 2 * k, instruction(RP, false),
+                 i > 0 || k >= M::kN);
+        tc_commit(smem_addr(&ctl->freed[s]));
+      }
+      tc_commit(smem_addr(&ctl->done[0]));
+    }
+    __syncwarp();
+  }
+  if (warp < kCopyWarps) {   // a warp: 32 rows, half the columns
+    ok = warp_wait(smem_addr(&ctl->done[0]), 0) && ok;
+    tc_fence_after();
+    const uint32_t quarter = warp & 3, row = quarter * 32 + lane;   // tensor memory's lanes
+    const uint32_t from = tmem + (quarter << 21);                   // lane in the upper half
+    const bool real = (int32_t)row < T.count;
+    uint16_t* const to = P.low + (real ? (int64_t)P.perm[T.start + row] * RP : 0);
+    for (uint32_t col = (warp >> 2) * 16; col < RP; col += 32) {
+      float v[16];
+      M::load(from, col, v);
+      if (mine == 0) {
+#pragma unroll
+        for (int i = 0; i < 16; i++) v[i] = 0.f;
+      }
+      if (C > 1) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<float4*>(part + row * L::kLd + col + i) =
+              make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      } else if (real) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++)   // past the rank 0, whatever x holds
+          w[i] = pack_bf16((int32_t)col + 2 * i < rank ? v[2 * i] * A.scale : 0.f,
+                           (int32_t)col + 2 * i + 1 < rank ? v[2 * i + 1] * A.scale : 0.f);
+        *reinterpret_cast<uint4*>(to + col) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(to + col + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+  }
+  if (!ok && P.status) *P.status = BD_ERR_CUDA;
+  if (C > 1) {
+    cluster.sync();
+    const uint32_t rows = 128 / C;
+    for (uint32_t e = tid * 4; e < rows * RP; e += L::kThreads * 4) {
+      const uint32_t row = c * rows + e / RP, col = e % RP;
+      if ((int32_t)row >= T.count) continue;
+      float v[4] = {};
+      for (uint32_t b = 0; b < C; b++) {
+        const float4 w = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, b) +
+                                                          row * L::kLd + col);
+        v[0] += w.x;
+        v[1] += w.y;
+        v[2] += w.z;
+        v[3] += w.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; i++) v[i] = (int32_t)col + i < rank ? v[i] * A.scale : 0.f;
+      *reinterpret_cast<uint2*>(P.low + (int64_t)P.perm[T.start + row] * RP + col) =
+          make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    }
+    cluster.sync();   // the others may still read `part`
+  }
+  end_block(tmem, M::kAlloc);
+}
+
+// ------------------------------------------------------------------------ weight gradients
+// A piece is 128 features of x (for dA) or dy (for dB) of one adapter, a sum over the adapter's
+// rows in stages of 64.  The blocks take equal shares of all stages of all pieces, so none waits
+// while another works; a piece that several blocks share is joined by the one that ends last, in
+// the order of the blocks, from their sums in the workspace.  Four warps carry a piece out while
+// the next one's stages arrive and are multiplied into the other set of sums.
+template <int RP>
+struct WgradTc {
+  static constexpr uint32_t kThreads = 32 * (kCopyWarps + 1 + 4);
+  static constexpr uint32_t kQ = 64 * kFeat * 2, kStage = kQ + 64 * RP * 2;
+  static constexpr uint32_t kBox = RP < 64 ? RP : 64;          // columns of low in a swizzled row
+  static constexpr uint32_t kLine = kBox * 2;                  // its bytes
+  static constexpr uint32_t kSwizzle = RP == 16 ? 6 : RP == 32 ? 4 : 2;
+  static constexpr uint32_t kS = kRingBudget / kStage < kMaxStages ? kRingBudget / kStage : kMaxStages;
+  static constexpr uint32_t kSmem = kS * kStage + sizeof(Control) + 1024;
+  // address of a 16-byte slot of low's rows
+  static __device__ __forceinline__ uint32_t at(uint32_t row, uint32_t slot) {
+    const uint32_t byte = slot / 8 * 8192 + row * kLine + slot % 8 * 16;
+    const uint32_t x = (byte >> 7) & (RP >= 64 ? 7 : RP == 32 ? 3 : 1);
+    return byte ^ x << 4;
+  }
+};
+
+template <int RP>
+__global__ void __launch_bounds__(32 * (kCopyWarps + 5), 1) k_wgrad_tc(const WgradArgs P) {
+  using L = WgradTc<RP>;
+  using M = Sums<RP, 2>;
+  constexpr uint32_t S = L::kS, D = S - 2;
+  extern __shared__ uint8_t raw[];
+  uint8_t* const smem = align1024(raw);
+  const uint32_t ring = smem_addr(smem);
+  Control* const ctl = reinterpret_cast<Control*>(smem + S * L::kStage);
+  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  after_previous();
+  const uint32_t hs = (P.hidden + kFeat - 1) / kFeat, slices = hs + (P.out + kFeat - 1) / kFeat;
+  Shares sh;
+  sh.all = (uint64_t)P.blocks[P.k] * slices;
+  sh.G = gridDim.x < sh.all ? gridDim.x : (uint32_t)sh.all;
+  if (blockIdx.x >= sh.G) return;
+  const uint64_t s_begin = sh.begin(blockIdx.x), s_end = sh.begin(blockIdx.x + 1);
+  const uint32_t tmem = begin_block(ctl, S, M::kAlloc);
+  bool ok = true;
+
+  if (warp < kCopyWarps) {
+    // a warp copies eight rows of a stage; a lane's 16-byte slots are four of x or dy, and of low
+    const uint32_t qch = lane & 15, qrow = lane >> 4;
+    constexpr uint32_t per = RP / 8, span = 32 / per > 8 ? 8 : 32 / per, PN = 8 / span;
+    const uint32_t pch = lane % per, prow = lane / per;
+    uint32_t i = 0;
+    for (Piece Q(P, slices, s_begin, s_end); !Q.over() && ok; Q.next(P, slices)) {
+      const bool down = Q.slice < hs;
+      const uint32_t f = (down ? Q.slice : Q.slice - hs) * kFeat + qch * 8;
+      const bool there = f < (down ? P.hidden : P.out);
+      const uint16_t* const qsrc = (down ? P.x : P.dy) + (there ? f : 0);
+      const uint16_t* const psrc = (down ? P.dlow : P.low) + pch * 8;
+      const uint64_t ld = down ? P.ldx : P.lddy;
+      // row numbers of four stages at once, a lane each, read four stages ahead
+      const int32_t start = Q.row0 + (int32_t)(Q.first * 64 + warp * 8), stop = Q.row1;
+      auto look = [&](uint32_t j) {   // of stages j .. j + 3
+        const int32_t t = start + (int32_t)((j + (lane >> 3)) * 64 + (lane & 7));
+        return t < stop ? P.perm[t] : -1;
+      };
+      int32_t rows = look(0), next = look(4);
+      for (uint32_t j = 0; j < Q.mine; j++, i++) {
+        if (j > 0 && j % 4 == 0) {
+          rows = next;
+          next = look(j + 4);
+        }
+        if (!(ok = stage_free<S>(ctl, i))) break;
+        const uint32_t to = ring + i % S * L::kStage;
+#pragma unroll
+        for (uint32_t u = 0; u < 4; u++) {
+          const uint32_t r = qrow + 2 * u;
+          const int32_t t = __shfl_sync(0xFFFFFFFFu, rows, (j % 4) * 8 + r);
+          cp16z(to + (qch >> 3) * 8192 + swz((warp * 8 + r) * 128 + (qch & 7) * 16),
+                qsrc + (t >= 0 ? t : 0) * ld, t >= 0 && there);
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < PN; u++) {
+          const uint32_t r = prow + span * u;
+          const int32_t t = __shfl_sync(0xFFFFFFFFu, rows, (j % 4) * 8 + (r & 7));
+          if (r < 8)
+            cp16z(to + L::kQ + L::at(warp * 8 + r, pch), psrc + (int64_t)(t >= 0 ? t : 0) * RP, t >= 0);
+        }
+        stage_issued<S, D>(ctl, i);
+      }
+    }
+    for (uint32_t e = 0; e < D - 1 && ok; e++, i++) stage_issued<S, D>(ctl, i);   // the last stages
+    copies_wait<0>();
+  } else if (warp == kCopyWarps) {   // issues the products
+    if (lane == 0) {
+      uint32_t i = 0, piece = 0;
+      for (Piece Q(P, slices, s_begin, s_end); !Q.over() && ok; Q.next(P, slices), piece++) {
+        const uint32_t b = piece & 1, d = tmem + b * M::kCols;
+        if (piece >= 2 && !(ok = bar_wait(smem_addr(&ctl->drained[b]), (piece / 2 + 1) & 1))) break;
+        tc_fence_after();
+        for (uint32_t j = 0; j < Q.mine; j++, i++) {
+          const uint32_t s = i % S;
+          if (!(ok = bar_wait(smem_addr(&ctl->full[s]), (i / S) & 1))) break;
+          tc_fence_after();
+          const uint64_t a = matrix(ring + s * L::kStage, 8192, 1024, 2);
+          const uint64_t l = matrix(ring + s * L::kStage + L::kQ, 8192, 8 * L::kLine, L::kSwizzle);
+#pragma unroll
+          for (uint32_t k = 0; k < 4; k++)   // 16 rows of the batch a step
+            tc_mma(d + k % M::kN * RP, a + k * (2048 >> 4), l + k * ((16 * L::kLine) >> 4),
+                   instruction(RP, true), j > 0 || k >= M::kN);
+          tc_commit(smem_addr(&ctl->freed[s]));
+        }
+        tc_commit(smem_addr(&ctl->done[b]));
+      }
+    }
+    __syncwarp();
+  } else {   // carries the sums out: a thread has a feature
+    const uint32_t quarter = warp & 3, fl = quarter * 32 + lane, t = tid - 32 * (kCopyWarps + 1);
+    auto meet = [](bool yes) {   // of the four warps: whether all say yes
+      uint32_t r;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+          "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(r)
+          : "r"((uint32_t)yes)
+          : "memory");
+      return r != 0;
+    };
+    uint32_t piece = 0;
+    DevAdapter A;
+    uint32_t known = 0xFFFFFFFFu;
+    for (Piece Q(P, slices, s_begin, s_end); !Q.over(); Q.next(P, slices), piece++) {
+      const uint32_t b = piece & 1;
+      if (Q.adapter != known) A = P.table[known = Q.adapter];
+      if (!(ok = meet(warp_wait(smem_addr(&ctl->done[b]), (piece / 2) & 1)))) break;   // (all or none)
+      tc_fence_after();
+      const uint32_t from = tmem + b * M::kCols + (quarter << 21);
+      const bool down = Q.slice < hs, whole = Q.mine == Q.stages;
+      const uint32_t f = (down ? Q.slice : Q.slice - hs) * kFeat + fl;
+      const bool real = f < (down ? P.hidden : P.out);
+      uint32_t b0 = blockIdx.x, b1 = blockIdx.x;   // the blocks of its first and last stage
+      bool write = true, kept = true;              // kept: this block's part stays in tensor memory
+      if (!whole) {
+        const uint64_t p_last = Q.begin + Q.stages - 1;
+        b0 = (uint32_t)(Q.begin * sh.G / sh.all);
+        while (sh.begin(b0 + 1) <= Q.begin) b0++;
+        b1 = (uint32_t)(p_last * sh.G / sh.all);
+        while (sh.begin(b1 + 1) <= p_last) b1++;
+        uint32_t* const count = P.counters + (uint64_t)Q.adapter * slices + Q.slice;
+        // The other parts are there already, as a rule: a block comes to a piece's end when the
+        // next block has long done the rest.
+        if (t == 0) {
+          uint32_t seen;
+          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(count) : "memory");
+          ctl->last = seen == b1 - b0;
+          if (ctl->last) *count = 0;
+        }
+        meet(true);
+        kept = ctl->last != 0;
+        __threadfence();
+        if (!kept) {   // this part to the workspace; the last block to do so joins
+          float* const to = P.sums + (2 * (uint64_t)blockIdx.x + (Q.at != s_begin)) * (kFeat * RP) + fl;
+#pragma unroll 1
+          for (uint32_t col = 0; col < RP; col += 16) {
+            float v[16];
+            M::load(from, col, v);
+#pragma unroll
+            for (int j = 0; j < 16; j++) __stcg(to + (col + j) * kFeat, v[j]);
+          }
+          __threadfence();
+          meet(true);
+          if (t == 0) ctl->last = atomicInc(count, b1 - b0) == b1 - b0;
+          meet(true);
+          write = ctl->last != 0;
+          __threadfence();
+        }
+      }
+      if (write) {
+        constexpr uint32_t W = RP < 32 ? RP : 32;   // columns read at once
+#pragma unroll 1
+        for (uint32_t wide = 0; wide < RP; wide += W) {
+          float sum[W];
+#pragma unroll
+          for (uint32_t j = 0; j < W; j++) sum[j] = 0.f;
+          for (uint32_t q = b0; q <= b1; q++) {
+            if (q == blockIdx.x && kept) {
+#pragma unroll
+              for (uint32_t part = 0; part < W; part += 16) {
+                float v[16];
+                M::load(from, wide + part, v);
+#pragma unroll
+                for (uint32_t j = 0; j < 16; j++) sum[part + j] += v[j];
+              }
+            } else {   // a block's first piece, or its last
+              const float* p =
+                  P.sums + (2 * (uint64_t)q + (sh.begin(q) < Q.begin)) * (kFeat * RP) + wide * kFeat + fl;
+#pragma unroll
+              for (uint32_t j = 0; j < W; j++) sum[j] += __ldcg(p + j * kFeat);
+            }
+          }
+#pragma unroll
+          for (uint32_t part = 0; part < W; part += 16) {
+            const uint32_t col = wide + part;
+            const float(&v)[16] = reinterpret_cast<const float(&)[16]>(sum[part]);
+            if (!real || col >= A.rank) continue;
+            if (P.accumulate || P.grad_f32) {
+#pragma unroll
+              for (uint32_t j = 0; j < 16; j++) {
+                if (col + j >= A.rank) break;
+                const uint64_t o = down ? (uint64_t)(col + j) * A.ld_gdown + f
+                                        : (uint64_t)f * A.ld_gup + col + j;
+                put_grad(down ? A.gdown : A.gup, o, v[j], P.grad_f32, P.accumulate);
+              }
+            } else if (down) {   // neighbouring features in neighbouring lanes
+              uint16_t* p = static_cast<uint16_t*>(A.gdown) + (uint64_t)col * A.ld_gdown + f;
+#pragma unroll
+              for (uint32_t j = 0; j < 16; j++, p += A.ld_gdown)
+                if (col + j < A.rank) *p = (uint16_t)pack_bf16(v[j], 0.f);
+            } else if (A.vec_gup) {   // (the rank is a multiple of 8 then)
+              uint16_t* const p = static_cast<uint16_t*>(A.gup) + (uint64_t)f * A.ld_gup + col;
+#pragma unroll
+              for (uint32_t j = 0; j < 16; j += 8)
+                if (col + j < A.rank)
+                  *reinterpret_cast<uint4*>(p + j) =
+                      make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]),
+                                 pack_bf16(v[j + 4], v[j + 5]), pack_bf16(v[j + 6], v[j + 7]));
+            } else {
+              uint16_t* const p = static_cast<uint16_t*>(A.gup) + (uint64_t)f * A.ld_gup + col;
+#pragma unroll
+              for (uint32_t j = 0; j < 16; j++)
+                if (col + j < A.rank) p[j] = (uint16_t)pack_bf16(v[j], 0.f);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      bar_arrive(smem_addr(&ctl->drained[b]));
+    }
+  }
+  if (!ok && P.status) *P.status = BD_ERR_CUDA;
+  end_block(tmem, M::kAlloc);
+}
+
+// ------------------------------------------------------------------------------- host side
+template <int RP>
+cudaError_t low(uint32_t blocks, uint32_t C, const ApplyArgs& P, cudaStream_t s) {
+  return launch(k_low<RP>, dim3(blocks), Low<RP>::kThreads, Low<RP>::kSmem, C, s, P);
+}
+template <int RP>
+cudaError_t wgrad(uint32_t grid, const WgradArgs& P, cudaStream_t s) {
+  return launch(k_wgrad_tc<RP>, dim3(grid), WgradTc<RP>::kThreads, WgradTc<RP>::kSmem, 1, s, P);
+}
+
+}  // namespace
+
+cudaError_t tc_low(uint32_t rp, uint32_t tiles, uint32_t C, const ApplyArgs& P, cudaStream_t s) {
+  switch (rp) {
+    case 16: return low<16>(tiles * C, C, P, s);
+    case 32: return low<32>(tiles * C, C, P, s);
+    case 64: return low<64>(tiles * C, C, P, s);
+    default: return low<128>(tiles * C, C, P, s);
+  }
+}
+
+cudaError_t tc_wgrad(uint32_t rp, uint32_t grid, const WgradArgs& P, cudaStream_t s) {
+  switch (rp) {
+    case 16: return wgrad<16>(grid, P, s);
+    case 32: return wgrad<32>(grid, P, s);
+    case 64: return wgrad<64>(grid, P, s);
+    default: return wgrad<128>(grid, P, s);
+  }
+}
+
+}  // namespace bo

@@ -31,6 +31,39 @@ inline int sm_count() {
 // may go as soon as the call returns, and the call works during stream capture.
 cudaError_t upload(const void* host, uint64_t bytes, void* dst, cudaStream_t s);
 
+// Launches a kernel so that its blocks may be placed while the kernel before it on the stream
+// still runs: every kernel launched this way first waits (after_previous) until all work before
+// it is done and visible, so only the launch itself overlaps.  cluster > 1: thread-block clusters.
+template <class... P, class... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, uint32_t threads, uint32_t smem,
+                   uint32_t cluster, cudaStream_t s, const A&... args) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+// First in every kernel that launch() starts, in every thread; then lets the next one be placed.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---- wide global memory accesses: each byte of a step or an adapter's rows is used once, so
 // none of them takes a line of L1.
 struct alignas(32) Float8 {

@@ -42,8 +42,11 @@ def _check(rc: int, what: str) -> None:
         raise OpsError(rc, what)
 
 
-def _stream(stream) -> int:
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+def _stream(stream, device: torch.device) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    # (the handle alone: a torch.cuda.Stream object would cost more than the launch)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _arena(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int, device) -> torch.Tensor:
@@ -161,7 +164,7 @@ class AdamWBatch:
         kind = 2 if wtype == torch.float32 else 0 if master else 1
         _check(lib.bo_adamw_plan(items, k, ctypes.byref(st), kind, _DTYPES[gtype], state_bits,
                                  int(bool(stochastic)), int(step), self.plan.data_ptr(),
-                                 self.plan.numel(), ctypes.byref(self.handle), _stream(stream)),
+                                 self.plan.numel(), ctypes.byref(self.handle), _stream(stream, dev)),
                "bo_adamw_plan")
         self.steps = self.plan[:8].view(torch.int64)
         self.norm = self.plan[8:12].view(torch.float32)
@@ -171,6 +174,7 @@ class AdamWBatch:
                                             int(seed) & _U64)
         self._refs = ctypes.byref(self.handle), ctypes.byref(self._args)
         self._step = lib.bo_adamw_step
+        self._device = dev
         self._keep = (list(weights), list(grads), outs)
 
     def run(self, lr: float | torch.Tensor | None = None, stream=None) -> None:
@@ -185,13 +189,14 @@ class AdamWBatch:
             else:
                 self.lr = float(lr)
                 self._args.lr, self._args.d_lr = self.lr, None
-        rc = self._step(*self._refs, _stream(stream))
+        rc = self._step(*self._refs, _stream(stream, self._device))
         if rc != OK:
             raise OpsError(rc, "bo_adamw_step")
 
     def grad_norm(self, stream=None) -> torch.Tensor:
         """The global norm of the gradients as they are now (`norm`), without a step."""
-        _check(_ops_lib.load().bo_adamw_norm(self._refs[0], self._args.max_norm, _stream(stream)),
+        _check(_ops_lib.load().bo_adamw_norm(self._refs[0], self._args.max_norm,
+                                               _stream(stream, self._device)),
                "bo_adamw_norm")
         return self.norm
 
@@ -212,7 +217,8 @@ class AdamWBatch:
         m = torch.empty(self.state["m"].numel(), dtype=dtype, device=self.plan.device)
         v = torch.empty_like(m)
         _check(_ops_lib.load().bo_adamw_moments(self._refs[0], _DTYPES[dtype], m.data_ptr(),
-                                                v.data_ptr(), _stream(stream)), "bo_adamw_moments")
+                                                v.data_ptr(), _stream(stream, self._device)),
+               "bo_adamw_moments")
         return m, v
 
 
@@ -285,12 +291,14 @@ class AdapterSet:
         self.table = torch.empty(max(256, int(lib.bo_adapter_set_size(k))), dtype=torch.uint8, device=dev)
         self.handle = _ops_lib.AdapterSet()
         _check(lib.bo_adapter_set_init(items, k, hidden, out, _DTYPES[gtype], self.table.data_ptr(),
-                                       self.table.numel(), ctypes.byref(self.handle), _stream(stream)),
+                                       self.table.numel(), ctypes.byref(self.handle), _stream(stream, dev)),
                "bo_adapter_set_init")
         self.k, self.hidden, self.out, self.device = k, hidden, out, dev
         #: columns of `low`, the activations that the forward pass keeps for the backward
         self.rank = int(self.handle.rank)
         self._ref = ctypes.byref(self.handle)
+        self._low_rows = int(lib.bo_adapter_low_rows(self._ref))
+        self._forward = lib.bo_adapter_forward
         self._keep = (list(downs), list(ups), d_downs, d_ups)
 
 
@@ -322,12 +330,22 @@ class AdapterRows:
         self.index = index
         _check(_ops_lib.load().bo_adapter_rows_init(
             index.data_ptr(), self.rows, self.k, self.memory.data_ptr(), self.memory.numel(),
-            self._ref, self.status.data_ptr(), _stream(stream)), "bo_adapter_rows_init")
+            self._ref, self.status.data_ptr(), _stream(stream, self.device)), "bo_adapter_rows_init")
 
 
 def _pair(adapters: AdapterSet, rows: AdapterRows) -> None:
     if rows.k != adapters.k:
         raise ValueError(f"rows are grouped over {rows.k} adapters, the set has {adapters.k}")
+
+
+def _rows_of(t: torch.Tensor, name: str, shape: tuple, device) -> int:
+    """Checks an activation matrix; returns its row stride."""
+    ld, one = t.stride() if t.dim() == 2 else (0, 0)
+    if t.shape != shape or t.dtype is not torch.bfloat16 or t.device != device or one != 1 or \
+            ld < shape[1]:
+        _matrix(t, name, *shape, device)     # says what is wrong, or that strides do not matter
+        return _ld(t)
+    return ld
 
 
 def _low(low: torch.Tensor, adapters: AdapterSet, rows: AdapterRows) -> int:
@@ -345,11 +363,15 @@ def adapter_forward(x: torch.Tensor, y: torch.Tensor, adapters: AdapterSet, rows
     low (optional, bfloat16 [rows, adapters.rank]) receives what adapter_backward needs.  Rows
     without an adapter are left alone.  Returns y."""
     _pair(adapters, rows)
-    _matrix(x, "x", rows.rows, adapters.hidden, adapters.device)
-    _matrix(y, "y", rows.rows, adapters.out, adapters.device)
-    rc = _ops_lib.load().bo_adapter_forward(
-        adapters._ref, rows._ref, x.data_ptr(), _ld(x), y.data_ptr(), _ld(y),
-        None if low is None else _low(low, adapters, rows), _stream(stream))
+    dev = adapters.device
+    ldx = _rows_of(x, "x", (rows.rows, adapters.hidden), dev)
+    ldy = _rows_of(y, "y", (rows.rows, adapters.out), dev)
+    if low is None and rows.rows >= adapters._low_rows:   # (workspace, for many rows)
+        low = torch.empty(rows.rows, adapters.rank, dtype=torch.bfloat16, device=dev)
+        if stream is not None:
+            low.record_stream(stream)
+    rc = adapters._forward(adapters._ref, rows._ref, x.data_ptr(), ldx, y.data_ptr(), ldy,
+                           None if low is None else _low(low, adapters, rows), _stream(stream, dev))
     if rc != OK:
         raise OpsError(rc, "bo_adapter_forward")
     return y
@@ -363,21 +385,20 @@ def adapter_backward(x: torch.Tensor, dy: torch.Tensor, low: torch.Tensor,
     projection's part; None: not wanted), in place, and the gradients given to the set are
     written, or with accumulate=True added to.  low is the forward pass's."""
     _pair(adapters, rows)
-    _matrix(x, "x", rows.rows, adapters.hidden, adapters.device)
-    _matrix(dy, "dy", rows.rows, adapters.out, adapters.device)
-    if dx is not None:
-        _matrix(dx, "dx", rows.rows, adapters.hidden, adapters.device)
+    dev = adapters.device
+    ldx = _rows_of(x, "x", (rows.rows, adapters.hidden), dev)
+    lddy = _rows_of(dy, "dy", (rows.rows, adapters.out), dev)
+    lddx = 0 if dx is None else _rows_of(dx, "dx", (rows.rows, adapters.hidden), dev)
     lib = _ops_lib.load()
-    need = int(lib.bo_adapter_backward_workspace_size(adapters._ref, rows.rows))
     ws = workspace
     if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=adapters.device)
+        need = int(lib.bo_adapter_backward_workspace_size(adapters._ref, rows.rows))
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
         if stream is not None:
             ws.record_stream(stream)   # (the allocator may not hand it out while it is in use)
     rc = lib.bo_adapter_backward(
-        adapters._ref, rows._ref, x.data_ptr(), _ld(x), dy.data_ptr(), _ld(dy),
-        _low(low, adapters, rows), None if dx is None else dx.data_ptr(),
-        0 if dx is None else _ld(dx), int(accumulate), ws.data_ptr(),
-        ws.numel() * ws.element_size(), _stream(stream))
+        adapters._ref, rows._ref, x.data_ptr(), ldx, dy.data_ptr(), lddy,
+        _low(low, adapters, rows), None if dx is None else dx.data_ptr(), lddx, int(accumulate),
+        ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream, dev))
     if rc != OK:
         raise OpsError(rc, "bo_adapter_backward")

@@ -131,11 +131,20 @@ __device__ __forceinline__ void noise8(uint64_t key, uint64_t e0, uint32_t (&r)[
     z += kGamma;
   }
 }
-// BF16 bits of x: away from zero when the cut-off part plus 16 random bits carries
+// BF16 bits of x in the upper half: away from zero when the cut-off part plus 16 random bits
+// carries.  (Of a NaN the carry may reach the sign: see nan_of.)
+__device__ __forceinline__ uint32_t bf16_carry(float x, uint32_t r) {
+  return __float_as_uint(x) + (r & 0xFFFFu);
+}
 __device__ __forceinline__ uint32_t bf16_stochastic(float x, uint32_t r) {
-  const uint32_t b = __float_as_uint(x);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0x7FFFu;   // NaN: no carry into the sign
-  return (b + (r & 0xFFFFu)) >> 16;
+  return isnan(x) ? 0x7FFFu : bf16_carry(x, r) >> 16;
+}
+// NaN if one of the eight is not finite, else 0: one instruction each
+__device__ __forceinline__ float nan_of(const float (&p)[8]) {
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; j++) s = fmaf(p[j], 0.f, s);
+  return s;
 }
 
 // ----------------------------------------------------------------------------- the formula
@@ -219,9 +228,9 @@ __device__ __forceinline__ void update(const Rates& R, float keep, float g, floa
   g *= R.coef;
   m = fmaf(R.b1, m, R.c1 * g);
   v = fmaf(R.b2, v, R.c2 * g * g);
-  const float den = sqrt_fast(v * R.inv_bc2) + R.eps;
-  const float q = m == 0.f ? 0.f : m * rcp_fast(den);   // (eps = 0: 0 / 0 is 0)
-  p = fmaf(p, keep, R.rate * q);
+  // (a denominator of 0, with eps = 0, counts as the least normal number: 0 / 0 is 0)
+  const float den = fmaxf(sqrt_fast(v * R.inv_bc2) + R.eps, 0x1p-126f);
+  p = fmaf(p, keep, R.rate * (m * rcp_fast(den)));
 }
 
 // Eight new weights from p: the master and its rounding, or the weights alone.
@@ -242,12 +251,19 @@ __device__ __forceinline__ void store_weights(const Chunk& c, uint32_t i, float*
     st8(master, q);
   }
   uint32_t w[4];
+  if (WK == BO_WEIGHT_BF16 && stochastic) {
 #pragma unroll
-  for (int j = 0; j < 4; j++)
-    w[j] = (WK == BO_WEIGHT_BF16 && stochastic)
-               ? (bf16_stochastic(p[2 * j], r[2 * j]) |
-                  bf16_stochastic(p[2 * j + 1], r[2 * j + 1]) << 16)
-               : pack_bf16(p[2 * j], p[2 * j + 1]);
+    for (int j = 0; j < 4; j++)
+      w[j] = __byte_perm(bf16_carry(p[2 * j], r[2 * j]), bf16_carry(p[2 * j + 1], r[2 * j + 1]), 0x7632);
+    if (isnan(nan_of(p))) {
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+        w[j] = bf16_stochastic(p[2 * j], r[2 * j]) | bf16_stochastic(p[2 * j + 1], r[2 * j + 1]) << 16;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; j++) w[j] = pack_bf16(p[2 * j], p[2 * j + 1]);
+  }
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.out) + i) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <int WK>
@@ -265,6 +281,25 @@ __device__ __forceinline__ void store_weight1(const Chunk& c, uint32_t i, float*
 
 // ------------------------------------------------------------------------ 32-bit moments
 template <int WK, bool GF32>
+struct Eight {   // a thread's elements
+  float g[8], p[8];
+  Float8 m, v;
+  __device__ __forceinline__ void load(const StepParams& P, const Chunk& c, uint32_t i) {
+    const uint64_t e = c.e0 + i;
+    load8<GF32>(c.g, i, g);
+    m = ld8(static_cast<float*>(P.st.d_m) + e);
+    v = ld8(static_cast<float*>(P.st.d_v) + e);
+    if (WK == BO_WEIGHT_MASTER) {
+      const Float8 q = ld8(P.st.d_master + e);
+#pragma unroll
+      for (int j = 0; j < 8; j++) p[j] = q.v[j];
+    } else {
+      load8<WK == BO_WEIGHT_FP32>(c.w, i, p);
+    }
+  }
+};
+
+template <int WK, bool GF32>
 __global__ void __launch_bounds__(kThreads, 4) k_step32(const StepParams P) {
   after_previous();
   Rates R;
@@ -272,8 +307,14 @@ __global__ void __launch_bounds__(kThreads, 4) k_step32(const StepParams P) {
   // Backwards after a norm: it has left the last gradients in L2.
   const Chunk* const table = P.clip ? P.table + P.chunks - 1 : P.table;
   const int64_t dir = P.clip ? -1 : 1;
+  const uint32_t i = threadIdx.x * 8;
   Chunk next;
+  next.count = 0;
   if (blockIdx.x < P.chunks) next = load_chunk(table + dir * (int64_t)blockIdx.x);
+  // the first elements are on their way while the rates are worked out
+  Eight<WK, GF32> x;
+  bool loaded = i + 8 <= next.count;
+  if (loaded) x.load(P, next, i);
   const bool taken = begin_step(P, R, key);
   if (taken) {
     float* const am = static_cast<float*>(P.st.d_m);
@@ -282,28 +323,19 @@ __global__ void __launch_bounds__(kThreads, 4) k_step32(const StepParams P) {
       const Chunk c = next;
       if (ci + gridDim.x < P.chunks)
         next = load_chunk(table + dir * (int64_t)(ci + gridDim.x));
-      const uint32_t i = threadIdx.x * 8;
       const float keep = 1.f - R.lr * c.wd;
       const uint64_t e = c.e0 + i;
       float* const pm = WK == BO_WEIGHT_MASTER ? P.st.d_master + e : nullptr;
       if (i + 8 <= c.count) {
-        float g[8], p[8];
-        load8<GF32>(c.g, i, g);
-        Float8 m = ld8(am + e), v = ld8(av + e);
-        if (WK == BO_WEIGHT_MASTER) {
-          const Float8 q = ld8(pm);
+        if (!loaded) x.load(P, c, i);
+        loaded = false;
 #pragma unroll
-          for (int j = 0; j < 8; j++) p[j] = q.v[j];
-        } else {
-          load8<WK == BO_WEIGHT_FP32>(c.w, i, p);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; j++) update(R, keep, g[j], m.v[j], v.v[j], p[j]);
-        st8(am + e, m);
-        st8(av + e, v);
+        for (int j = 0; j < 8; j++) update(R, keep, x.g[j], x.m.v[j], x.v.v[j], x.p[j]);
+        st8(am + e, x.m);
+        st8(av + e, x.v);
         uint32_t r[8] = {};
         if (WK == BO_WEIGHT_BF16 && P.stochastic) noise8(key, e, r);
-        store_weights<WK>(c, i, pm, p, P.stochastic, r);
+        store_weights<WK>(c, i, pm, x.p, P.stochastic, r);
       } else if (i < c.count) {   // a tensor's last elements
         uint32_t r[8] = {};
         if (WK == BO_WEIGHT_BF16 && P.stochastic) noise8(key, e, r);
@@ -325,13 +357,14 @@ __global__ void __launch_bounds__(kThreads, 4) k_step32(const StepParams P) {
 }
 
 // ------------------------------------------------------------------------- 8-bit moments
-// Integers and floats meet in the low bits of a float near 2^23 or 1.5 2^23: the converting
+// Integers and floats meet in the low bits of a float near a power of two: the converting
 // instructions run at an eighth of the rate of an addition, and there would be five an element.
-__device__ __forceinline__ float byte_u(uint32_t w, uint32_t j) {   // byte j as a float
-  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650 | j)) - 8388608.f;
+// Byte j, by 2^-8, and as a signed number (w80 = w ^ 0x80808080), by 2^-7:
+__device__ __forceinline__ float byte_u(uint32_t w, uint32_t j) {
+  return __uint_as_float(__byte_perm(w, 0x47000000u, 0x7650 | j)) - 32768.f;
 }
-__device__ __forceinline__ float byte_s(uint32_t w80, uint32_t j) {   // signed; w80 = w ^ 0x80808080
-  return __uint_as_float(__byte_perm(w80, 0x4B000000u, 0x7650 | j)) - 8388736.f;
+__device__ __forceinline__ float byte_s(uint32_t w80, uint32_t j) {
+  return __uint_as_float(__byte_perm(w80, 0x47800000u, 0x7650 | j)) - 65537.f;
 }
 __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
   float r;
@@ -353,14 +386,14 @@ __device__ __forceinline__ float inverse_scale(float scale, float& pre) {
   pre = scale < 0x1p-100f ? 0x1p80f : scale > 0x1p100f ? 0x1p-80f : 1.f;
   return scale > 0.f ? 1.f / (scale * pre) : 0.f;   // (under a NaN scale every code reads NaN)
 }
-constexpr float kMUnit = 1.f / 16129.f;                        // 127^-2
-constexpr float kVUnit = (float)(1.0 / (65025.0 * 65025.0));   // 255^-4
-__device__ __forceinline__ float v_units(float c) {   // c^4; c^2 is exact
+// A code's value is a power of (code / 2^k), exact but for one rounding, times the scale and
+constexpr float kMScale = (float)(16384.0 / 16129.0);                     // (128 / 127)^2
+constexpr float kVScale = (float)(4294967296.0 / (65025.0 * 65025.0));    // (256 / 255)^4
+__device__ __forceinline__ float m_power(float c) { return c * fabsf(c); }
+__device__ __forceinline__ float v_power(float c) {
   const float c2 = c * c;
   return c2 * c2;
 }
-__device__ __forceinline__ float m_value(float c) { return c * fabsf(c) * kMUnit; }
-__device__ __forceinline__ float v_value(float c) { return v_units(c) * kVUnit; }
 // the code in the low byte
 __device__ __forceinline__ uint32_t m_code(float m, float inv) {
   const float c = sqrt_fast(fabsf(m) * inv);
@@ -371,12 +404,13 @@ __device__ __forceinline__ uint32_t m_code(float m, float inv) {
 // make a step without bound).  inv_units: 255^4 / scale.
 __device__ __forceinline__ uint32_t v_code(float v, float inv_units, uint32_t r) {
   const float x = v * inv_units;
-  // floor of x's fourth root, by rounding down at 2^23
-  const float low = fminf(__fadd_rd(sqrt_fast(sqrt_fast(x)), 8388608.f) - 8388608.f, 254.f);
-  const float a = v_units(low), d = v_units(low + 1.f) - a;
-  const float u1 = __uint_as_float(0x3F800000u | (r >> 16) << 7);   // 1 + u
-  const float c = fmaf(u1, d, -d) < x - a ? low + 1.f : low;
-  return __float_as_uint((v > 0.f ? fmaxf(c, 1.f) : 0.f) + 8388608.f);
+  // floor of x's fourth root, by rounding down at 2^23, where the code stays in the low byte
+  const float at = fminf(__fadd_rd(sqrt_fast(sqrt_fast(x)), 8388608.f), 8388862.f);
+  const float low = at - 8388608.f, low2 = low * low;
+  const float d = fmaf(fmaf(fmaf(4.f, low, 6.f), low, 4.f), low, 1.f);   // (low + 1)^4 - low^4
+  const float u1 = __uint_as_float(0x3F800000u | (r >> 16) << 7);        // 1 + u
+  const float up = fmaf(u1, d, -d) < fmaf(-low2, low2, x) ? at + 1.f : at;
+  return __float_as_uint(fmaxf(up, v > 0.f ? 8388609.f : 8388608.f));
 }
 
 // One warp per block of 256: its eight elements a lane stay in registers while the block's
@@ -407,9 +441,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_step8(const StepParams P) {
       float* const pm = WK == BO_WEIGHT_MASTER ? P.st.d_master + e : nullptr;
       const uint32_t cnt = c.count > i ? min(c.count - i, 8u) : 0u;
       float g[8] = {}, p[8] = {}, m[8], v[8];
-      const uint2 cm = *reinterpret_cast<const uint2*>(am + e);
+      uint2 cm = *reinterpret_cast<const uint2*>(am + e);
+      cm = make_uint2(cm.x ^ 0x80808080u, cm.y ^ 0x80808080u);
       const uint2 cv = *reinterpret_cast<const uint2*>(av + e);
-      const float sm = P.st.d_m_scale[blk], sv = P.st.d_v_scale[blk];
+      const float sm = P.st.d_m_scale[blk] * kMScale, sv = P.st.d_v_scale[blk] * kVScale;
       if (cnt == 8) {
         load8<GF32>(c.g, i, g);
         if (WK == BO_WEIGHT_MASTER) {
@@ -430,10 +465,17 @@ __global__ void __launch_bounds__(kThreads, 4) k_step8(const StepParams P) {
       float mm = 0.f, mv = 0.f;
 #pragma unroll
       for (uint32_t j = 0; j < 8; j++) {
-        m[j] = m_value(byte_s((j < 4 ? cm.x : cm.y) ^ 0x80808080u, j & 3)) * sm;
-        v[j] = v_value(byte_u(j < 4 ? cv.x : cv.y, j & 3)) * sv;
-        if (j >= cnt) m[j] = v[j] = 0.f;   // padding behind the tensor's end
+        m[j] = m_power(byte_s(j < 4 ? cm.x : cm.y, j & 3)) * sm;
+        v[j] = v_power(byte_u(j < 4 ? cv.x : cv.y, j & 3)) * sv;
         update(R, keep, g[j], m[j], v[j], p[j]);
+      }
+      if (cnt < 8) {   // padding behind the tensor's end
+#pragma unroll
+        for (uint32_t j = 0; j < 8; j++)
+          if (j >= cnt) m[j] = v[j] = 0.f;
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < 8; j++) {
         mm = max_nan(mm, fabsf(m[j]));
         mv = max_nan(mv, v[j]);
       }
@@ -504,17 +546,17 @@ __global__ void __launch_bounds__(kThreads) k_moments(const bo_adamw_state st,
     float x[8];
     if (out_m) {
       const uint2 c = static_cast<const uint2*>(st.d_m)[t];
-      const float s = st.d_m_scale[t >> 5];
+      const float s = st.d_m_scale[t >> 5] * kMScale;
 #pragma unroll
       for (int j = 0; j < 8; j++)
-        x[j] = m_value(byte_s((j < 4 ? c.x : c.y) ^ 0x80808080u, j & 3)) * s;
+        x[j] = m_power(byte_s((j < 4 ? c.x : c.y) ^ 0x80808080u, j & 3)) * s;
       put8<F32>(out_m, t, x);
     }
     if (out_v) {
       const uint2 c = static_cast<const uint2*>(st.d_v)[t];
-      const float s = st.d_v_scale[t >> 5];
+      const float s = st.d_v_scale[t >> 5] * kVScale;
 #pragma unroll
-      for (int j = 0; j < 8; j++) x[j] = v_value(byte_u(j < 4 ? c.x : c.y, j & 3)) * s;
+      for (int j = 0; j < 8; j++) x[j] = v_power(byte_u(j < 4 ? c.x : c.y, j & 3)) * s;
       put8<F32>(out_v, t, x);
     }
   }
@@ -781,9 +823,9 @@ int bo_adamw_step(const bo_adamw* h, const bo_adamw_step_args* a, void* stream) 
   P.stochastic = (h->flags & BO_ADAMW_STOCHASTIC) != 0;
   P.seed = a->seed;
   const uint64_t want = h->chunks < 1 ? 1 : h->chunks;
+  const bool b8 = h->state_bits == 8;
   const uint32_t most = (uint32_t)sms * 4;
   const uint32_t grid = (uint32_t)(want < most ? want : most);
-  const bool b8 = h->state_bits == 8;
   cudaError_t e;
   switch (h->weight_kind * 2 + h->grad_dtype) {
     case BO_WEIGHT_MASTER * 2 + BO_BF16: e = launch_step<BO_WEIGHT_MASTER, false>(b8, grid, P, s); break;

@@ -194,15 +194,16 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p, int32_t n, bool vec) {
   if (vec) return n > 0 ? ld16(p) : make_uint4(0, 0, 0, 0);   // (n is a multiple of 8)
   return gather8(p, n);
 }
-// The same for the factors, which other blocks read too.
+// The same for the factors, which other blocks read too (n may be anything).
 __device__ __forceinline__ uint4 load8w(const uint16_t* p, int32_t n, bool vec) {
-  if (vec) return n > 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+  if (vec && (n >= 8 || n <= 0))
+    return n > 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
   return gather8(p, n);
 }
 // ... into shared memory
 __device__ __forceinline__ void fill8(uint32_t dst, const uint16_t* p, int32_t n, bool vec) {
-  if (vec && n > 0) cp16(dst, p);
-  else sts16(dst, vec ? make_uint4(0, 0, 0, 0) : gather8(p, n));
+  if (vec) cp16n(dst, p, n);
+  else sts16(dst, gather8(p, n));
 }
 __device__ __forceinline__ void store8(uint16_t* p, uint4 v, int32_t n, bool vec) {
   if (vec) {
@@ -276,8 +277,9 @@ __global__ void __launch_bounds__(kThreads) k_apply16(const ApplyArgs P) {
     if (KS == 32) return load8w(src, n, A.vec_up);
     uint2 t = make_uint2(0, 0);   // rank at most 16: four values a thread make one mma step
     if (A.vec_up) {
-      if (n > 0) t = __ldg(reinterpret_cast<const uint2*>(src));
-    } else {
+      if (n >= 4) t = __ldg(reinterpret_cast<const uint2*>(src));
+    }
+    if (!A.vec_up || (n > 0 && n < 4)) {
       const uint4 f = gather8(src, min(n, 4));
       t = make_uint2(f.x, f.y);
     }
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const Ap
     for (uint32_t r = 0; r < kBN; r += span) {
       const bool there = o0 + r + urow < P.N;
       const uint32_t dst = at + swz_dealt<RP>(r + urow, uch);
-      if (VEC) cp16z(dst, there && un > 0 ? upp + (uint64_t)(o0 + r) * A.ld_up : A.up, there && un > 0);
+      if (VEC) cp16n(dst, there && un > 0 ? upp + (uint64_t)(o0 + r) * A.ld_up : A.up, there ? un : 0);
       else fill8(dst, upp + (uint64_t)(o0 + r) * A.ld_up, there ? un : 0, A.vec_up);
     }
   };
@@ -710,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_expand(const ApplyArgs P) {
       const uint32_t row = s / (RP / 8), ch = s % (RP / 8);
       const int32_t n = n0 + row < P.N ? rank - (int32_t)ch * 8 : 0;
       const uint16_t* src = n > 0 ? A.up + (uint64_t)(n0 + row) * A.ld_up + ch * 8 : A.up;
-      cp16z(bs + L::at(row, ch * 16), src, n > 0);
+      cp16n(bs + L::at(row, ch * 16), src, n);
     }
     cp_commit();
     cp_wait<0>();
@@ -1268,7 +1270,7 @@ int bo_adapter_set_init(const bo_adapter* h_items, uint32_t k, uint32_t hidden, 
     d.rank = a.rank;
     d.scale = a.scale;
     d.vec_down = wide(a.d_down, a.ld_down, hidden);
-    d.vec_up = wide(a.d_up, a.ld_up, a.rank);
+    d.vec_up = wide(a.d_up, a.ld_up, 8);   // (a rank's last 16 bytes are read in part)
     d.vec_gup = a.d_grad_up && wide(a.d_grad_up, a.ld_grad_up, a.rank);
     d.pad[0] = d.pad[1] = d.pad[2] = 0;
     if (!d.vec_down || !d.vec_up) all_wide = false;

@@ -36,6 +36,12 @@ __device__ __forceinline__ void cp16z(uint32_t dst, const void* src, bool there)
                "r"(there ? 16 : 0)
                : "memory");
 }
+// The first n of eight values (none for n <= 0), and zeros in place of the others.
+__device__ __forceinline__ void cp16n(uint32_t dst, const void* src, int32_t n) {
+  const int32_t bytes = n >= 8 ? 16 : n > 0 ? 2 * n : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
 // Byte address in a tile of rows that fill 128-byte lines: the 16-byte slots of a line are
 // permuted by the line's number, so that eight consecutive rows at one column fall into
 // different banks (the 128-byte swizzle of the tensor cores' and the copy engine's tiles).

@@ -32,7 +32,6 @@ namespace bo {
 namespace {
 
 constexpr uint32_t kThreads = 256;   // eight warps
-constexpr uint32_t kMaxCluster = 8;
 
 // ------------------------------------------------------------------------ grouping the rows
 // One block per adapter counts its rows, then one block per adapter places them in order: the
@@ -330,8 +329,11 @@ __global__ void __launch_bounds__(kThreads) k_apply16(const ApplyArgs P) {
   }
   cluster.sync();
   for (uint32_t e = threadIdx.x; e < 16 * RP; e += kThreads) {
-    float s = 0.f;
-    for (uint32_t b = 0; b < C; b++) s += cluster.map_shared_rank(part, b)[e];
+    float v[kMaxCluster], s = 0.f;   // (all blocks' at once: each is a trip across the cluster)
+#pragma unroll
+    for (uint32_t b = 0; b < kMaxCluster; b++) v[b] = b < C ? cluster.map_shared_rank(part, b)[e] : 0.f;
+#pragma unroll
+    for (uint32_t b = 0; b < kMaxCluster; b++) s += v[b];
     const int32_t row = e / RP, col = e % RP;
     // columns past the rank are 0 whatever x holds (an infinity times a padded 0 is not)
     s = col < rank ? s * A.scale : 0.f;
@@ -581,18 +583,22 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const Ap
     const uint32_t rows = 64 / C;
     for (uint32_t e = tid * 2; e < rows * RP; e += kThreads * 2) {
       const uint32_t row = c * rows + e / RP, col = e % RP;
-      float2 s = make_float2(0.f, 0.f);
-      for (uint32_t b = 0; b < C; b++) {
-        const float2 v =
-            *reinterpret_cast<const float2*>(cluster.map_shared_rank(part, b) + row * RP + col);
-        s.x += v.x;
-        s.y += v.y;
+      float2 v[kMaxCluster], s = make_float2(0.f, 0.f);   // (all blocks' at once)
+#pragma unroll
+      for (uint32_t b = 0; b < kMaxCluster; b++)
+        v[b] = b < C ? *reinterpret_cast<const float2*>(cluster.map_shared_rank(part, b) + row * RP + col)
+                     : make_float2(0.f, 0.f);
+#pragma unroll
+      for (uint32_t b = 0; b < kMaxCluster; b++) {
+        s.x += v[b].x;
+        s.y += v[b].y;
       }
       // columns past the rank are 0 whatever x holds (an infinity times a padded 0 is not)
       const uint32_t u = pack_bf16((int32_t)col < rank ? s.x * A.scale : 0.f,
                                    (int32_t)col + 1 < rank ? s.y * A.scale : 0.f);
-      for (uint32_t b = 0; b < C; b++)
-        *reinterpret_cast<uint32_t*>(cluster.map_shared_rank(us, b) + row * L::kULd + col) = u;
+#pragma unroll
+      for (uint32_t b = 0; b < kMaxCluster; b++)
+        if (b < C) *reinterpret_cast<uint32_t*>(cluster.map_shared_rank(us, b) + row * L::kULd + col) = u;
       if (P.low && srow[row] >= 0)
         *reinterpret_cast<uint32_t*>(P.low + (int64_t)srow[row] * RP + col) = u;
     }

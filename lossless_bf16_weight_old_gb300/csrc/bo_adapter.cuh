@@ -5,6 +5,8 @@
 
 namespace bo {
 
+constexpr uint32_t kMaxCluster = 8;
+
 struct alignas(16) DevAdapter {
   const uint16_t* down;
   const uint16_t* up;

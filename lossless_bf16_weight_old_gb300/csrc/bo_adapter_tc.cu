@@ -321,14 +321,19 @@ __global__ void __launch_bounds__(288, 1) k_low(const ApplyArgs P) {
     for (uint32_t e = tid * 4; e < rows * RP; e += L::kThreads * 4) {
       const uint32_t row = c * rows + e / RP, col = e % RP;
       if ((int32_t)row >= T.count) continue;
+      float4 w[kMaxCluster];   // (all blocks' at once: each is a trip across the cluster)
+#pragma unroll
+      for (uint32_t b = 0; b < kMaxCluster; b++)
+        w[b] = b < C ? *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, b) +
+                                                        row * L::kLd + col)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
       float v[4] = {};
-      for (uint32_t b = 0; b < C; b++) {
-        const float4 w = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, b) +
-                                                          row * L::kLd + col);
-        v[0] += w.x;
-        v[1] += w.y;
-        v[2] += w.z;
-        v[3] += w.w;
+#pragma unroll
+      for (uint32_t b = 0; b < kMaxCluster; b++) {
+        v[0] += w[b].x;
+        v[1] += w[b].y;
+        v[2] += w[b].z;
+        v[3] += w[b].w;
       }
 #pragma unroll
       for (int i = 0; i < 4; i++) v[i] = (int32_t)col + i < rank ? v[i] * A.scale : 0.f;
@@ -470,32 +475,55 @@ __global__ void __launch_bounds__(32 * (kCopyWarps + 5), 1) k_wgrad_tc(const Wgr
     for (Piece Q(P, slices, s_begin, s_end); !Q.over(); Q.next(P, slices), piece++) {
       const uint32_t b = piece & 1;
       if (Q.adapter != known) A = P.table[known = Q.adapter];
-      if (!(ok = meet(warp_wait(smem_addr(&ctl->done[b]), (piece / 2) & 1)))) break;   // (all or none)
-      tc_fence_after();
-      const uint32_t from = tmem + b * M::kCols + (quarter << 21);
       const bool down = Q.slice < hs, whole = Q.mine == Q.stages;
       const uint32_t f = (down ? Q.slice : Q.slice - hs) * kFeat + fl;
       const bool real = f < (down ? P.hidden : P.out);
-      uint32_t b0 = blockIdx.x, b1 = blockIdx.x;   // the blocks of its first and last stage
-      bool write = true, kept = true;              // kept: this block's part stays in tensor memory
+      // The parts of a piece are joined from the last block's to the first's.  As a rule the first
+      // block ends last, by a long way: then it finds the others' parts while its own stages are
+      // still being multiplied, and its own part never leaves the SM.
+      uint32_t b0 = blockIdx.x, b1 = blockIdx.x;   // the blocks of the piece's first and last stage
+      uint32_t* const count = P.counters + (uint64_t)Q.adapter * slices + Q.slice;
       if (!whole) {
         const uint64_t p_last = Q.begin + Q.stages - 1;
         b0 = (uint32_t)(Q.begin * sh.G / sh.all);
         while (sh.begin(b0 + 1) <= Q.begin) b0++;
         b1 = (uint32_t)(p_last * sh.G / sh.all);
         while (sh.begin(b1 + 1) <= p_last) b1++;
-        uint32_t* const count = P.counters + (uint64_t)Q.adapter * slices + Q.slice;
-        // The other parts are there already, as a rule: a block comes to a piece's end when the
-        // next block has long done the rest.
+      }
+      bool kept = whole;                           // this block's part stays in tensor memory
+      auto look = [&]() {                          // whether the other parts are there
+        meet(true);                                // (every warp has read `last` as it was)
         if (t == 0) {
           uint32_t seen;
           asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(count) : "memory");
           ctl->last = seen == b1 - b0;
-          if (ctl->last) *count = 0;
         }
         meet(true);
-        kept = ctl->last != 0;
+        const bool r = ctl->last != 0;
         __threadfence();
+        return r;
+      };
+      constexpr uint32_t W = RP < 64 ? RP : 64;    // columns joined at once
+      auto join = [&](uint32_t wide, uint32_t q, float (&sum)[W]) {   // block q's first piece, or its last
+        const float* p =
+            P.sums + (2 * (uint64_t)q + (sh.begin(q) < Q.begin)) * (kFeat * RP) + wide * kFeat + fl;
+#pragma unroll
+        for (uint32_t j = 0; j < W; j++) sum[j] += __ldcg(p + j * kFeat);
+      };
+      float sum[W];
+#pragma unroll
+      for (uint32_t j = 0; j < W; j++) sum[j] = 0.f;
+      const bool early = !whole && b0 == blockIdx.x && look();
+      if (early) {
+        kept = true;
+        for (uint32_t q = b1; q > b0; q--) join(0, q, sum);
+      }
+      if (!(ok = meet(warp_wait(smem_addr(&ctl->done[b]), (piece / 2) & 1)))) break;   // (all or none)
+      tc_fence_after();
+      const uint32_t from = tmem + b * M::kCols + (quarter << 21);
+      bool write = true;
+      if (!whole && !early) {
+        kept = look();
         if (!kept) {   // this part to the workspace; the last block to do so joins
           float* const to = P.sums + (2 * (uint64_t)blockIdx.x + (Q.at != s_begin)) * (kFeat * RP) + fl;
 #pragma unroll 1
@@ -507,33 +535,31 @@ __global__ void __launch_bounds__(32 * (kCopyWarps + 5), 1) k_wgrad_tc(const Wgr
           }
           __threadfence();
           meet(true);
-          if (t == 0) ctl->last = atomicInc(count, b1 - b0) == b1 - b0;
+          if (t == 0) ctl->last = atomicAdd(count, 1) == b1 - b0;
           meet(true);
           write = ctl->last != 0;
           __threadfence();
         }
       }
       if (write) {
-        constexpr uint32_t W = RP < 32 ? RP : 32;   // columns read at once
+        if (!whole && t == 0) *count = 0;
 #pragma unroll 1
         for (uint32_t wide = 0; wide < RP; wide += W) {
-          float sum[W];
+          if (wide > 0) {
 #pragma unroll
-          for (uint32_t j = 0; j < W; j++) sum[j] = 0.f;
-          for (uint32_t q = b0; q <= b1; q++) {
-            if (q == blockIdx.x && kept) {
+            for (uint32_t j = 0; j < W; j++) sum[j] = 0.f;
+          }
+          for (uint32_t q = b1 + 1; q-- > b0;) {
+            if (q != blockIdx.x || !kept) {
+              if (!early || wide > 0) join(wide, q, sum);
+              continue;
+            }
 #pragma unroll
-              for (uint32_t part = 0; part < W; part += 16) {
-                float v[16];
-                M::load(from, wide + part, v);
+            for (uint32_t part = 0; part < W; part += 16) {
+              float v[16];
+              M::load(from, wide + part, v);
 #pragma unroll
-                for (uint32_t j = 0; j < 16; j++) sum[part + j] += v[j];
-              }
-            } else {   // a block's first piece, or its last
-              const float* p =
-                  P.sums + (2 * (uint64_t)q + (sh.begin(q) < Q.begin)) * (kFeat * RP) + wide * kFeat + fl;
-#pragma unroll
-              for (uint32_t j = 0; j < W; j++) sum[j] += __ldcg(p + j * kFeat);
+              for (uint32_t j = 0; j < 16; j++) sum[part + j] += v[j];
             }
           }
 #pragma unroll

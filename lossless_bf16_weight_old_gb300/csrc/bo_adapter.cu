@@ -215,6 +215,13 @@ __device__ __forceinline__ void store8(uint16_t* p, uint4 v, int32_t n, bool vec
     if (j < n) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
 }
 
+// ... of rows that will not be read again soon
+__device__ __forceinline__ void store8_stream(uint16_t* p, uint4 v) {
+  asm volatile("st.global.cs.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
 // Columns of the second product are dealt out so that a thread ends with eight neighbours: of a
 // group of 32 columns, column 8 (i / 2) + 2 j + i % 2 is column i of the j-th mma tile, and the
 // fragment's columns 2 q, 2 q + 1 over the four tiles are 8 q .. 8 q + 7.
@@ -720,15 +727,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_expand(const ApplyArgs P) {
       const uint16_t* src = n > 0 ? A.up + (uint64_t)(n0 + row) * A.ld_up + ch * 8 : A.up;
       cp16n(bs + L::at(row, ch * 16), src, n);
     }
-    cp_commit();
-    cp_wait<0>();
-    __syncthreads();
+    cp_commit();   // (waited for below, with the first pieces of y on their way too)
 
     const int32_t n_left = (int32_t)(P.N - n0);
     const uint32_t groups = (uint32_t)((n_left < (int32_t)L::kN ? n_left : (int32_t)L::kN) + 31) / 32;
     const int32_t units = (r_end - T.start + 31) / 32;
-    const int32_t mine = units > (int32_t)warp ? (units - (int32_t)warp + 7) / 8 : 0;
-    if (mine == 0) continue;
+    const int32_t mine = units > (int32_t)warp ? (units - (int32_t)warp + 7) / 8 : 0;   // (may be 0)
     auto row_of = [&](int32_t u, int i) {   // the thread's i-th row of its u-th unit, or -1
       const int32_t r = T.start + ((int32_t)warp + u * 8) * 32 + (int32_t)g + 8 * i;
       return u < mine && r < r_end ? P.perm[r] : -1;
@@ -751,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_expand(const ApplyArgs P) {
 #pragma unroll
         for (int i = 0; i < 4; i++)
           if (prow[i] >= 0 && there)
-            cp16(dst + i * kThreads * 16, P.y + (int64_t)prow[i] * P.ldy + base + pg * 32);
+            cp16_ahead(dst + i * kThreads * 16, P.y + (int64_t)prow[i] * P.ldy + base + pg * 32);
         if (++pg == groups) {
           pg = 0;
           pu++;
@@ -767,6 +771,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_expand(const ApplyArgs P) {
     };
 #pragma unroll
     for (uint32_t i = 0; i < L::kDepth - 1; i++) issue();
+    cp_wait<L::kDepth - 1>();
+    __syncthreads();   // B is there
     uint32_t step = 0;
     for (int32_t u = 0; u < mine; u++) {
       uint4 a[4][KS];   // low: rows g, g + 8, g + 16, g + 24
@@ -822,13 +828,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_expand(const ApplyArgs P) {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
           const int m = i >> 1, h = 2 * (i & 1);
-          if (row[i] >= 0)
-            store8(P.y + (int64_t)row[i] * P.ldy + base + gi * 32,
-                   make_uint4(pack_bf16(d[m][0][h], d[m][0][h + 1]),
-                              pack_bf16(d[m][1][h], d[m][1][h + 1]),
-                              pack_bf16(d[m][2][h], d[m][2][h + 1]),
-                              pack_bf16(d[m][3][h], d[m][3][h + 1])),
-                   n, true);
+          if (row[i] >= 0 && n > 0)
+            store8_stream(P.y + (int64_t)row[i] * P.ldy + base + gi * 32,
+                          make_uint4(pack_bf16(d[m][0][h], d[m][0][h + 1]),
+                                     pack_bf16(d[m][1][h], d[m][1][h + 1]),
+                                     pack_bf16(d[m][2][h], d[m][2][h + 1]),
+                                     pack_bf16(d[m][3][h], d[m][3][h + 1])));
         }
       }
 #pragma unroll

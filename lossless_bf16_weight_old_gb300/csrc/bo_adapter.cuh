@@ -29,8 +29,9 @@ struct Tile {
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// (rows that are read from end to end, a piece at a time: HBM may as well send the piece after)
+__device__ __forceinline__ void cp16_ahead(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 // 16 bytes, or zeros in their place (src is not read then, but points at memory of the caller's)
 __device__ __forceinline__ void cp16z(uint32_t dst, const void* src, bool there) {

@@ -235,18 +235,18 @@ __global__ void __launch_bounds__(288, 1) k_low(const ApplyArgs P) {
   const int32_t rank = (int32_t)A.rank;
   const uint32_t all = (P.K + 63) / 64;
   const uint32_t mine = all > c ? (all - c + C - 1) / C : 0;
+  // a copying thread's 16-byte slots of a stage: four rows of x, and of the factor's rows
+  const uint32_t ch = tid & 7, row0 = tid >> 3;
+  const uint16_t* xp[4];
+#pragma unroll
+  for (int j = 0; j < 4; j++) {   // (past the tile's end: its first row, whose sum is not used)
+    const int32_t t = (int32_t)row0 + 32 * j;
+    xp[j] = P.x + (int64_t)P.perm[T.start + (t < T.count ? t : 0)] * P.ldx + ch * 8;
+  }
   const uint32_t tmem = begin_block(ctl, S, M::kAlloc);
   bool ok = true;
 
   if (warp < kCopyWarps) {
-    // a thread's 16-byte slots of a stage: four rows of x, and of the factor's rows
-    const uint32_t ch = tid & 7, row0 = tid >> 3;
-    const uint16_t* xp[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {   // (past the tile's end: its first row, whose sum is not used)
-      const int32_t t = (int32_t)row0 + 32 * j;
-      xp[j] = P.x + (int64_t)P.perm[T.start + (t < T.count ? t : 0)] * P.ldx + ch * 8;
-    }
     const uint32_t at = swz(row0 * 128 + ch * 16);
     for (uint32_t i = 0; i < mine + D - 1; i++) {
       if (i < mine) {

@@ -120,11 +120,12 @@ __device__ __forceinline__ uint64_t mix64(uint64_t z) {   // SplitMix64 (Steele,
   z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
   return z ^ (z >> 31);
 }
-// the 32 bits of each of the eight elements from e0 on (e0 a multiple of 8)
-__device__ __forceinline__ void noise8(uint64_t key, uint64_t e0, uint32_t (&r)[8]) {
+// the 32 bits of each of the N elements from e0 on (both even)
+template <int N>
+__device__ __forceinline__ void noise(uint64_t key, uint64_t e0, uint32_t (&r)[N]) {
   uint64_t z = key + ((e0 >> 1) + 1) * kGamma;
 #pragma unroll
-  for (int j = 0; j < 4; j++) {
+  for (int j = 0; j < N / 2; j++) {
     const uint64_t h = mix64(z);
     r[2 * j] = (uint32_t)h;
     r[2 * j + 1] = (uint32_t)(h >> 32);
@@ -139,11 +140,12 @@ __device__ __forceinline__ uint32_t bf16_carry(float x, uint32_t r) {
 __device__ __forceinline__ uint32_t bf16_stochastic(float x, uint32_t r) {
   return isnan(x) ? 0x7FFFu : bf16_carry(x, r) >> 16;
 }
-// NaN if one of the eight is not finite, else 0: one instruction each
-__device__ __forceinline__ float nan_of(const float (&p)[8]) {
+// NaN if one of them is not finite, else 0: one instruction each
+template <int N>
+__device__ __forceinline__ float nan_of(const float (&p)[N]) {
   float s = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; j++) s = fmaf(p[j], 0.f, s);
+  for (int j = 0; j < N; j++) s = fmaf(p[j], 0.f, s);
   return s;
 }
 
@@ -215,6 +217,11 @@ __device__ __forceinline__ float sqrt_fast(float x) {
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float rsqrt_fast(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ float rcp_fast(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -233,11 +240,26 @@ __device__ __forceinline__ void update(const Rates& R, float keep, float g, floa
   p = fmaf(p, keep, R.rate * (m * rcp_fast(den)));
 }
 
-// Eight new weights from p: the master and its rounding, or the weights alone.
+// BF16 words of weights p, rounded to nearest or by the random bits
+template <int N>
+__device__ __forceinline__ void weight_words(const float (&p)[N], bool stochastic,
+                                             const uint32_t (&r)[N], uint32_t* w) {
+#pragma unroll
+  for (int j = 0; j < N / 2; j++)
+    w[j] = stochastic ? __byte_perm(bf16_carry(p[2 * j], r[2 * j]),
+                                    bf16_carry(p[2 * j + 1], r[2 * j + 1]), 0x7632)
+                      : pack_bf16(p[2 * j], p[2 * j + 1]);
+  if (stochastic && isnan(nan_of(p))) {
+#pragma unroll
+    for (int j = 0; j < N / 2; j++)
+      w[j] = bf16_stochastic(p[2 * j], r[2 * j]) | bf16_stochastic(p[2 * j + 1], r[2 * j + 1]) << 16;
+  }
+}
+// Eight new weights from p: the FP32 ones, or the master and the words of its rounding, or the
+// words alone.
 template <int WK>
 __device__ __forceinline__ void store_weights(const Chunk& c, uint32_t i, float* master,
-                                              const float (&p)[8], bool stochastic,
-                                              const uint32_t (&r)[8]) {
+                                              const float (&p)[8], const uint32_t (&w)[4]) {
   if (WK == BO_WEIGHT_FP32) {
     float4* o = reinterpret_cast<float4*>(static_cast<float*>(c.out) + i);
     o[0] = make_float4(p[0], p[1], p[2], p[3]);
@@ -249,20 +271,6 @@ __device__ __forceinline__ void store_weights(const Chunk& c, uint32_t i, float*
 #pragma unroll
     for (int j = 0; j < 8; j++) q.v[j] = p[j];
     st8(master, q);
-  }
-  uint32_t w[4];
-  if (WK == BO_WEIGHT_BF16 && stochastic) {
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-      w[j] = __byte_perm(bf16_carry(p[2 * j], r[2 * j]), bf16_carry(p[2 * j + 1], r[2 * j + 1]), 0x7632);
-    if (isnan(nan_of(p))) {
-#pragma unroll
-      for (int j = 0; j < 4; j++)
-        w[j] = bf16_stochastic(p[2 * j], r[2 * j]) | bf16_stochastic(p[2 * j + 1], r[2 * j + 1]) << 16;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; j++) w[j] = pack_bf16(p[2 * j], p[2 * j + 1]);
   }
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.out) + i) = make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -333,12 +341,14 @@ __global__ void __launch_bounds__(kThreads, 4) k_step32(const StepParams P) {
         for (int j = 0; j < 8; j++) update(R, keep, x.g[j], x.m.v[j], x.v.v[j], x.p[j]);
         st8(am + e, x.m);
         st8(av + e, x.v);
-        uint32_t r[8] = {};
-        if (WK == BO_WEIGHT_BF16 && P.stochastic) noise8(key, e, r);
-        store_weights<WK>(c, i, pm, x.p, P.stochastic, r);
+        uint32_t r[8] = {}, w[4] = {};
+        if (WK == BO_WEIGHT_BF16 && P.stochastic) noise(key, e, r);
+        if (WK != BO_WEIGHT_FP32)
+          weight_words(x.p, WK == BO_WEIGHT_BF16 && P.stochastic, r, w);
+        store_weights<WK>(c, i, pm, x.p, w);
       } else if (i < c.count) {   // a tensor's last elements
         uint32_t r[8] = {};
-        if (WK == BO_WEIGHT_BF16 && P.stochastic) noise8(key, e, r);
+        if (WK == BO_WEIGHT_BF16 && P.stochastic) noise(key, e, r);
 #pragma unroll
         for (uint32_t j = 0; j < 8; j++) {
           if (i + j >= c.count) break;
@@ -357,14 +367,31 @@ __global__ void __launch_bounds__(kThreads, 4) k_step32(const StepParams P) {
 }
 
 // ------------------------------------------------------------------------- 8-bit moments
+// Here arithmetic counts as much as HBM: about eighty instructions an element, a tenth of them for
+// the random bits, against the eighty-five that 16 bytes an element leave time for.  So additions,
+// products and their sums are taken two elements at a time (the packed FP32 instructions).
+//
+// A code feeds the next step, so where a moment lies next to the bound between two codes, the last
+// bit of its arithmetic decides between states that differ by a whole code.  Everything between
+// the old code and the new one is therefore the correctly rounded FP32 operation, one for each
+// operation of the formula and in its order: a step has one right result.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
 // Integers and floats meet in the low bits of a float near a power of two: the converting
 // instructions run at an eighth of the rate of an addition, and there would be five an element.
-// Byte j, by 2^-8, and as a signed number (w80 = w ^ 0x80808080), by 2^-7:
-__device__ __forceinline__ float byte_u(uint32_t w, uint32_t j) {
-  return __uint_as_float(__byte_perm(w, 0x47000000u, 0x7650 | j)) - 32768.f;
+// Bytes j and j + 1, by 2^-8, and as signed numbers (w80 = w ^ 0x80808080), by 2^-7:
+__device__ __forceinline__ float2 bytes_u(uint32_t w, uint32_t j) {
+  return add2(make_float2(__uint_as_float(__byte_perm(w, 0x47000000u, 0x7650 | j)),
+                          __uint_as_float(__byte_perm(w, 0x47000000u, 0x7651 | j))),
+              both(-32768.f));
 }
-__device__ __forceinline__ float byte_s(uint32_t w80, uint32_t j) {
-  return __uint_as_float(__byte_perm(w80, 0x47800000u, 0x7650 | j)) - 65537.f;
+__device__ __forceinline__ float2 bytes_s(uint32_t w80, uint32_t j) {
+  return add2(make_float2(__uint_as_float(__byte_perm(w80, 0x47800000u, 0x7650 | j)),
+                          __uint_as_float(__byte_perm(w80, 0x47800000u, 0x7651 | j))),
+              both(-65537.f));
 }
 __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
   float r;
@@ -386,31 +413,73 @@ __device__ __forceinline__ float inverse_scale(float scale, float& pre) {
   pre = scale < 0x1p-100f ? 0x1p80f : scale > 0x1p100f ? 0x1p-80f : 1.f;
   return scale > 0.f ? 1.f / (scale * pre) : 0.f;   // (under a NaN scale every code reads NaN)
 }
-// A code's value is a power of (code / 2^k), exact but for one rounding, times the scale and
-constexpr float kMScale = (float)(16384.0 / 16129.0);                     // (128 / 127)^2
-constexpr float kVScale = (float)(4294967296.0 / (65025.0 * 65025.0));    // (256 / 255)^4
-__device__ __forceinline__ float m_power(float c) { return c * fabsf(c); }
-__device__ __forceinline__ float v_power(float c) {
-  const float c2 = c * c;
-  return c2 * c2;
+// A code's value is m: (c |c| / 127^2) scale and v: (c / 255)^4 scale; the codes come divided by
+// 128 and 256, which the factors make good without another rounding.
+constexpr float kMUnit = (1.f / 16129.f) * 16384.f;
+constexpr float kVUnit = (1.f / 255.f) * 256.f;
+__device__ __forceinline__ float2 m_values(float2 c) {
+  return mul2(make_float2(c.x * fabsf(c.x), c.y * fabsf(c.y)), both(kMUnit));
 }
-// the code in the low byte
-__device__ __forceinline__ uint32_t m_code(float m, float inv) {
-  const float c = sqrt_fast(fabsf(m) * inv);
-  return __float_as_uint(fmaf(copysignf(c, m), 127.f, 12582912.f));
+__device__ __forceinline__ float2 v_values(float2 c) {
+  const float2 y = mul2(c, both(kVUnit)), y2 = mul2(y, y);
+  return mul2(y2, y2);
+}
+// (The compiler joins a packed product and a packed sum into one operation with one rounding.)
+__device__ __forceinline__ float2 sum2(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+// Two elements' update (the formula of `update`; the moments as said above).
+__device__ __forceinline__ void update2(const Rates& R, float keep, float2 g, float2& m, float2& v,
+                                        float2& p) {
+  g = mul2(g, both(R.coef));
+  m = sum2(mul2(m, both(R.b1)), mul2(g, both(R.c1)));
+  v = sum2(mul2(v, both(R.b2)), mul2(mul2(g, g), both(R.c2)));
+  const float2 t = mul2(v, both(R.inv_bc2));
+  const float2 den = add2(make_float2(sqrt_fast(t.x), sqrt_fast(t.y)), both(R.eps));
+  const float2 q = mul2(m, make_float2(rcp_fast(fmaxf(den.x, 0x1p-126f)),
+                                       rcp_fast(fmaxf(den.y, 0x1p-126f))));
+  p = fma2(p, both(keep), mul2(both(R.rate), q));
+}
+// x / scale, rounded once: the product with the reciprocal, put right by its remainder
+__device__ __forceinline__ float2 ratio2(float2 x, float scale, float inv) {
+  const float2 q = mul2(x, both(inv));
+  return fma2(fma2(q, both(-scale), x), both(inv), q);
+}
+// the codes in the low bytes
+__device__ __forceinline__ float2 m_codes(float2 m, float scale, float inv) {
+  const float2 q = ratio2(m, scale, inv);
+  const float2 x = make_float2(fmaxf(fabsf(q.x), 0x1p-100f), fmaxf(fabsf(q.y), 0x1p-100f));
+  // the root, rounded once: x / sqrt(x), put right by its remainder
+  const float2 h = make_float2(rsqrt_fast(x.x), rsqrt_fast(x.y)), y = mul2(x, h);
+  const float2 e = fma2(mul2(y, both(-1.f)), y, x);
+  const float2 r = mul2(fma2(e, mul2(h, both(0.5f)), y), both(127.f));
+  return add2(make_float2(copysignf(r.x, m.x), copysignf(r.y, m.y)), both(12582912.f));
 }
 // Of the two codes whose values enclose v / scale, the upper one with the chance that makes the
 // expected value v / scale; never 0 for v > 0 (a root of 0 under a moment that is not 0 would
-// make a step without bound).  inv_units: 255^4 / scale.
-__device__ __forceinline__ uint32_t v_code(float v, float inv_units, uint32_t r) {
-  const float x = v * inv_units;
-  // floor of x's fourth root, by rounding down at 2^23, where the code stays in the low byte
-  const float at = fminf(__fadd_rd(sqrt_fast(sqrt_fast(x)), 8388608.f), 8388862.f);
-  const float low = at - 8388608.f, low2 = low * low;
-  const float d = fmaf(fmaf(fmaf(4.f, low, 6.f), low, 4.f), low, 1.f);   // (low + 1)^4 - low^4
-  const float u1 = __uint_as_float(0x3F800000u | (r >> 16) << 7);        // 1 + u
-  const float up = fmaf(u1, d, -d) < fmaf(-low2, low2, x) ? at + 1.f : at;
-  return __float_as_uint(fmaxf(up, v > 0.f ? 8388609.f : 8388608.f));
+// make a step without bound).
+__device__ __forceinline__ float2 v_codes(float2 v, float scale, float inv, uint32_t r0, uint32_t r1) {
+  const float2 x = ratio2(v, scale, inv);
+  // floor of 255 times x's fourth root, by rounding down at 2^23, where the code stays in the low
+  // byte.  (One more or less next to a whole number makes the same code: its chance is 1 or 0.)
+  float2 at = __ffma2_rd(make_float2(sqrt_fast(sqrt_fast(x.x)), sqrt_fast(sqrt_fast(x.y))), both(255.f),
+                         both(8388608.f));
+  at = make_float2(fminf(at.x, 8388862.f), fminf(at.y, 8388862.f));
+  const float2 up = add2(at, both(1.f)), low = add2(at, both(-8388608.f));
+  const float2 ya = mul2(low, both(1.f / 255.f)), yb = mul2(add2(low, both(1.f)), both(1.f / 255.f));
+  const float2 a2 = mul2(ya, ya), b2 = mul2(yb, yb), a = mul2(a2, a2), b = mul2(b2, b2);
+  const float2 u = add2(make_float2(__uint_as_float(0x3F800000u | (r0 >> 16) << 7),
+                                    __uint_as_float(0x3F800000u | (r1 >> 16) << 7)),
+                        both(-1.f));
+  // u (upper - lower) < v / scale - lower
+  const float2 l = mul2(u, fma2(a, both(-1.f), b)), h = fma2(a, both(-1.f), x);
+  return make_float2(fmaxf(l.x < h.x ? up.x : at.x, v.x > 0.f ? 8388609.f : 8388608.f),
+                     fmaxf(l.y < h.y ? up.y : at.y, v.y > 0.f ? 8388609.f : 8388608.f));
+}
+// the low bytes of four
+__device__ __forceinline__ uint32_t low_bytes(float2 a, float2 b) {
+  return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                     __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
 }
 
 // One warp per block of 256: its eight elements a lane stay in registers while the block's
@@ -423,28 +492,24 @@ __global__ void __launch_bounds__(kThreads, 4) k_step8(const StepParams P) {
   // Backwards after a norm: it has left the last gradients in L2.
   const Chunk* const table = P.clip ? P.table + P.chunks - 1 : P.table;
   const int64_t dir = P.clip ? -1 : 1;
-  Chunk next;
-  if (blockIdx.x < P.chunks) next = load_chunk(table + dir * (int64_t)blockIdx.x);
   const bool taken = begin_step(P, R, key);
   if (taken) {
     uint8_t* const am = static_cast<uint8_t*>(P.st.d_m);
     uint8_t* const av = static_cast<uint8_t*>(P.st.d_v);
     const uint32_t lane = threadIdx.x & 31;
     for (uint64_t ci = blockIdx.x; ci < P.chunks; ci += gridDim.x) {
-      const Chunk c = next;
-      if (ci + gridDim.x < P.chunks)
-        next = load_chunk(table + dir * (int64_t)(ci + gridDim.x));
+      const Chunk c = load_chunk(table + dir * (int64_t)ci);   // (no registers for the one after)
       const uint32_t i = threadIdx.x * 8;
       if ((threadIdx.x & ~31u) * 8 >= c.count) continue;   // (the whole warp)
       const float keep = 1.f - R.lr * c.wd;
       const uint64_t e = c.e0 + i, blk = e / BO_BLOCK_ELEMS;
       float* const pm = WK == BO_WEIGHT_MASTER ? P.st.d_master + e : nullptr;
       const uint32_t cnt = c.count > i ? min(c.count - i, 8u) : 0u;
-      float g[8] = {}, p[8] = {}, m[8], v[8];
+      float g[8] = {}, p[8] = {};
       uint2 cm = *reinterpret_cast<const uint2*>(am + e);
       cm = make_uint2(cm.x ^ 0x80808080u, cm.y ^ 0x80808080u);
       const uint2 cv = *reinterpret_cast<const uint2*>(av + e);
-      const float sm = P.st.d_m_scale[blk] * kMScale, sv = P.st.d_v_scale[blk] * kVScale;
+      const float sm = P.st.d_m_scale[blk], sv = P.st.d_v_scale[blk];
       if (cnt == 8) {
         load8<GF32>(c.g, i, g);
         if (WK == BO_WEIGHT_MASTER) {
@@ -462,55 +527,58 @@ __global__ void __launch_bounds__(kThreads, 4) k_step8(const StepParams P) {
             p[j] = WK == BO_WEIGHT_MASTER ? pm[j] : load1<WK == BO_WEIGHT_FP32>(c.w, i + j);
           }
       }
+      float2 m[4], v[4];
       float mm = 0.f, mv = 0.f;
 #pragma unroll
-      for (uint32_t j = 0; j < 8; j++) {
-        m[j] = m_power(byte_s(j < 4 ? cm.x : cm.y, j & 3)) * sm;
-        v[j] = v_power(byte_u(j < 4 ? cv.x : cv.y, j & 3)) * sv;
-        update(R, keep, g[j], m[j], v[j], p[j]);
+      for (uint32_t j = 0; j < 4; j++) {
+        m[j] = mul2(m_values(bytes_s(j < 2 ? cm.x : cm.y, 2 * j & 3)), both(sm));
+        v[j] = mul2(v_values(bytes_u(j < 2 ? cv.x : cv.y, 2 * j & 3)), both(sv));
+        float2 q = make_float2(p[2 * j], p[2 * j + 1]);
+        update2(R, keep, make_float2(g[2 * j], g[2 * j + 1]), m[j], v[j], q);
+        p[2 * j] = q.x;
+        p[2 * j + 1] = q.y;
       }
       if (cnt < 8) {   // padding behind the tensor's end
 #pragma unroll
-        for (uint32_t j = 0; j < 8; j++)
-          if (j >= cnt) m[j] = v[j] = 0.f;
+        for (uint32_t j = 0; j < 4; j++) {
+          if (2 * j >= cnt) m[j].x = v[j].x = 0.f;
+          if (2 * j + 1 >= cnt) m[j].y = v[j].y = 0.f;
+        }
       }
 #pragma unroll
-      for (uint32_t j = 0; j < 8; j++) {
-        mm = max_nan(mm, fabsf(m[j]));
-        mv = max_nan(mv, v[j]);
+      for (uint32_t j = 0; j < 4; j++) {
+        mm = max_nan(max_nan(mm, fabsf(m[j].x)), fabsf(m[j].y));
+        mv = max_nan(max_nan(mv, v[j].x), v[j].y);
       }
       mm = finite_or_nan(warp_max(mm));
       mv = finite_or_nan(warp_max(mv));
       float mpre, vpre;
-      const float minv = inverse_scale(mm, mpre), vinv = inverse_scale(mv, vpre) * 4228250625.f;
+      const float minv = inverse_scale(mm, mpre), vinv = inverse_scale(mv, vpre);
       if (mpre != 1.f || vpre != 1.f) {
 #pragma unroll
-        for (uint32_t j = 0; j < 8; j++) {
-          m[j] *= mpre;
-          v[j] *= vpre;
+        for (uint32_t j = 0; j < 4; j++) {
+          m[j] = mul2(m[j], both(mpre));
+          v[j] = mul2(v[j], both(vpre));
         }
       }
-      uint32_t r[8];
-      noise8(key, e, r);
-      uint32_t a[8], b[8];
+      uint32_t r[8], w[4] = {};
+      noise(key, e, r);
+      float2 a[4], b[4];
 #pragma unroll
-      for (uint32_t j = 0; j < 8; j++) {
-        a[j] = m_code(m[j], minv);
-        b[j] = v_code(v[j], vinv, r[j]);
+      for (uint32_t j = 0; j < 4; j++) {
+        a[j] = m_codes(m[j], mm * mpre, minv);
+        b[j] = v_codes(v[j], mv * vpre, vinv, r[2 * j], r[2 * j + 1]);
       }
-      auto low_bytes = [](const uint32_t* w) {
-        return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
-      };
-      const uint2 qm = make_uint2(low_bytes(a), low_bytes(a + 4));
-      const uint2 qv = make_uint2(low_bytes(b), low_bytes(b + 4));
-      *reinterpret_cast<uint2*>(am + e) = qm;
-      *reinterpret_cast<uint2*>(av + e) = qv;
+      *reinterpret_cast<uint2*>(am + e) = make_uint2(low_bytes(a[0], a[1]), low_bytes(a[2], a[3]));
+      *reinterpret_cast<uint2*>(av + e) = make_uint2(low_bytes(b[0], b[1]), low_bytes(b[2], b[3]));
       if (lane == 0) {
         P.st.d_m_scale[blk] = mm;
         P.st.d_v_scale[blk] = mv;
       }
       if (cnt == 8) {
-        store_weights<WK>(c, i, pm, p, P.stochastic, r);
+        if (WK != BO_WEIGHT_FP32)
+          weight_words(p, WK == BO_WEIGHT_BF16 && P.stochastic, r, w);
+        store_weights<WK>(c, i, pm, p, w);
       } else {
 #pragma unroll
         for (uint32_t j = 0; j < 8; j++)
@@ -546,17 +614,26 @@ __global__ void __launch_bounds__(kThreads) k_moments(const bo_adamw_state st,
     float x[8];
     if (out_m) {
       const uint2 c = static_cast<const uint2*>(st.d_m)[t];
-      const float s = st.d_m_scale[t >> 5] * kMScale;
+      const float s = st.d_m_scale[t >> 5];
 #pragma unroll
-      for (int j = 0; j < 8; j++)
-        x[j] = m_power(byte_s((j < 4 ? c.x : c.y) ^ 0x80808080u, j & 3)) * s;
+      for (int j = 0; j < 8; j += 2) {
+        const float2 y = mul2(m_values(bytes_s((j < 4 ? c.x : c.y) ^ 0x80808080u, j & 3)), both(s));
+        x[j] = y.x;
+        x[j + 1] = y.y;
+      }
       put8<F32>(out_m, t, x);
     }
     if (out_v) {
       const uint2 c = static_cast<const uint2*>(st.d_v)[t];
-      const float s = st.d_v_scale[t >> 5] * kVScale;
+      const float s = st.d_v_scale[t >> 5];
 #pragma unroll
-      for (int j = 0; j < 8; j++) x[j] = v_power(byte_u(j < 4 ? c.x : c.y, j & 3)) * s;
+      for (int j = 0; j < 8; j += 2) {
+        // fewer roundings than the step's: (c / 256)^2 is exact
+        const float2 a = bytes_u(j < 4 ? c.x : c.y, j & 3), b = mul2(a, a);
+        const float2 y = mul2(mul2(mul2(b, b), both(4294967296.f / 4228250625.f)), both(s));
+        x[j] = y.x;
+        x[j + 1] = y.y;
+      }
       put8<F32>(out_v, t, x);
     }
   }
@@ -824,7 +901,10 @@ int bo_adamw_step(const bo_adamw* h, const bo_adamw_step_args* a, void* stream) 
   P.seed = a->seed;
   const uint64_t want = h->chunks < 1 ? 1 : h->chunks;
   const bool b8 = h->state_bits == 8;
-  const uint32_t most = (uint32_t)sms * 4;
+  // A block of the 32-bit step takes a few chunks only: blocks that start in order keep the arenas'
+  // pages open (625M parameters: 2.75 ms with 4 blocks an SM taking all chunks in turn, 2.54 ms
+  // with 64; 8-bit moments, which arithmetic bounds, do not care).
+  const uint32_t most = (uint32_t)sms * (b8 ? 4 : 64);
   const uint32_t grid = (uint32_t)(want < most ? want : most);
   cudaError_t e;
   switch (h->weight_kind * 2 + h->grad_dtype) {

@@ -181,6 +181,20 @@ __device__ __forceinline__ void sts16(uint32_t dst, uint4 v) {
                : "memory");
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
 // Eight values from p, of which the first n exist (n <= 0: none); the others are 0.
 __device__ __forceinline__ uint4 gather8(const uint16_t* p, int32_t n) {
   uint32_t w[4] = {0, 0, 0, 0};
@@ -422,11 +436,17 @@ struct Apply64 {
   static constexpr uint32_t kStage = kXBytes + kWBytes;
   static constexpr uint32_t kRing = kStages * kStage;
   static constexpr uint32_t kPart = 64 * RP * 4;               // over the ring, after the sum
-  static constexpr uint32_t kUp = kBN * RP * 2;                // two of them
+  // steps of B's rows (as many as fit over the ring) and of y that are there or on their way
+  static constexpr uint32_t kUp = kBN * RP * 2, kUps = RP <= 32 ? 4 : RP == 64 ? 3 : 2;
+  static constexpr uint32_t kY = 64 * kBN * 2, kYs = RP == 32 ? 3 : RP == 64 ? 2 : 4;
+  // groups of copies that may be on their way at a step: those after its B, and after its y
+  static constexpr int kAfterUp = 2 * (int)kUps - 3, kAfterY = 2 * (int)kYs - 2;
+  static constexpr int kPending = kAfterUp < kAfterY ? kAfterUp : kAfterY;
   static constexpr uint32_t kULd = RP + 8;
   static constexpr uint32_t kU = 64 * kULd * 2;
-  static constexpr uint32_t kFirst = kRing > kPart + 2 * kUp ? kRing : kPart + 2 * kUp;
-  static constexpr uint32_t kSmem = kFirst + kU + 64 * 4;
+  static constexpr uint32_t kFirst = kRing > kPart + kUps * kUp ? kRing : kPart + kUps * kUp;
+  static constexpr uint32_t kRows = kFirst + kU, kYRing = kRows + 64 * 4;
+  static constexpr uint32_t kSmem = kYRing + kYs * kY;
   // Of the sum a warp takes 32 rows and a quarter of a stage, so that a fragment of A serves two
   // tiles of rows; of rank 128, whose sums fill the registers, 16 rows and a half.
   static constexpr int kMR = RP <= 64 ? 2 : 1;
@@ -439,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const Ap
   extern __shared__ __align__(1024) uint8_t smem[];
   float* const part = reinterpret_cast<float*>(smem);
   uint16_t* const us = reinterpret_cast<uint16_t*>(smem + L::kFirst);
-  int32_t* const srow = reinterpret_cast<int32_t*>(smem + L::kFirst + L::kU);
+  int32_t* const srow = reinterpret_cast<int32_t*>(smem + L::kRows);
   const cg::cluster_group cluster = cg::this_cluster();
   const uint32_t C = cluster.num_blocks(), c = cluster.block_rank();
   const uint32_t tile = blockIdx.x / C;
@@ -454,6 +474,33 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const Ap
   const DevAdapter A = P.table[T.adapter];
   const int32_t rank = (int32_t)A.rank;
   __syncthreads();
+
+  // ---- this block's steps of the columns of y.  A thread fetches the pieces that it will add to
+  // by itself, ahead of the sum's end; (of rows off the 16-byte boundary one step ahead, into
+  // registers).
+  const uint32_t steps = P.y ? (P.N + kBN - 1) / kBN : 0;
+  const uint32_t todo = steps > c ? (steps - c + C - 1) / C : 0;
+  const int32_t r0 = srow[wr * 16 + g], r1 = srow[wr * 16 + g + 8];
+  uint16_t* const yp0 = P.y + (int64_t)(r0 >= 0 ? r0 : row_a) * P.ldy + wh * 64 + 8 * q;
+  uint16_t* const yp1 = P.y + (int64_t)(r1 >= 0 ? r1 : row_a) * P.ldy + wh * 64 + 8 * q;
+  const int32_t left = (int32_t)P.N - (int32_t)(wh * 64 + 8 * q);
+  uint4 y0[2], y1[2];
+  const uint32_t yring = smem_addr(smem + L::kYRing) + tid * 16;
+  auto load_y = [&](uint32_t i) {
+#pragma unroll
+    for (uint32_t h = 0; h < 2; h++) {
+      const uint32_t at = (c + i * C) * kBN + h * 32;
+      const int32_t n = left - (int32_t)at;
+      if (VEC) {
+        const uint32_t dst = yring + i % L::kYs * L::kY + h * 2 * kThreads * 16;
+        if (r0 >= 0 && n > 0) cp16_ahead(dst, yp0 + at);
+        if (r1 >= 0 && n > 0) cp16_ahead(dst + kThreads * 16, yp1 + at);
+      } else {
+        y0[h] = load8(yp0 + at, n, P.vec_y);
+        y1[h] = load8(yp1 + at, n, P.vec_y);
+      }
+    }
+  };
 
   // ---- low = s A x: this block's stages of the sum
   const uint32_t stages = (P.K + kBK - 1) / kBK;
@@ -499,10 +546,15 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const Ap
       if (i < mine) load_stage(i);
       cp_commit();
     }
+    // behind the last stage, which iteration `tail` no longer finds to fetch, come the first y
+    const uint32_t y_steps = todo < L::kYs ? todo : L::kYs;
+    const uint32_t tail = mine > kStages - 1 ? mine - (kStages - 1) : 0;
     for (uint32_t i = 0; i < mine; i++) {
       cp_wait<kStages - 2>();
       __syncthreads();
-      if (i + kStages - 1 < mine) load_stage(i + kStages - 1);
+      const uint32_t ahead = i + kStages - 1;
+      if (ahead < mine) load_stage(ahead);
+      else if (VEC && i - tail < y_steps) load_y(i - tail);
       cp_commit();
       const uint32_t xs = ring + (i % kStages) * L::kStage, ws = xs + L::kXBytes;
 #pragma unroll
@@ -525,37 +577,44 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const Ap
         }
       }
     }
-    cp_wait<0>();
-    // join the parts of every stage, in one order
-#pragma unroll
-    for (uint32_t pass = 0; pass < 2 * MR; pass++) {
-      __syncthreads();
-      if (kq == pass) {
-#pragma unroll
-        for (int m = 0; m < MR; m++)
-#pragma unroll
-          for (int j = 0; j < RP / 8; j++)
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-              float2* d = reinterpret_cast<float2*>(
-                  part + ((rg * MR + m) * 16 + h * 8 + g) * RP + j * 8 + 2 * q);
-              const float2 v = make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
-              *d = pass == 0 ? v : make_float2(d->x + v.x, d->y + v.y);
-            }
+    // (the last stage was waited for with everything before it; on their way are pieces of y)
+    if (VEC)
+      for (uint32_t i = mine - tail; i < y_steps; i++) {
+        load_y(i);
+        cp_commit();
       }
+    // join the parts of every stage, in one order
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < MR; m++)
+#pragma unroll
+      for (int j = 0; j < RP / 8; j++)
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+          *reinterpret_cast<float2*>(part + kq * 64 * RP + ((rg * MR + m) * 16 + h * 8 + g) * RP +
+                                     j * 8 + 2 * q) =
+              make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+    __syncthreads();
+    for (uint32_t e = tid * 2; e < 64 * RP; e += kThreads * 2) {
+      float2 s = *reinterpret_cast<const float2*>(part + e);
+#pragma unroll
+      for (uint32_t z = 1; z < 2 * MR; z++) {
+        const float2 v = *reinterpret_cast<const float2*>(part + z * 64 * RP + e);
+        s.x += v.x;
+        s.y += v.y;
+      }
+      *reinterpret_cast<float2*>(part + e) = s;
     }
   }
 
   // ---- y += B low: this block's steps of the columns, the first one's loads ahead of the join
-  const uint32_t steps = P.y ? (P.N + kBN - 1) / kBN : 0;
-  const uint32_t todo = steps > c ? (steps - c + C - 1) / C : 0;
   constexpr uint32_t per = RP / 8, span = kThreads / per;   // 16-byte slots in a row; rows at once
   const uint32_t urow = tid / per, uch = tid % per;
   const uint32_t up0 = ring + L::kPart;
   const uint16_t* const upp = A.up + (uint64_t)urow * A.ld_up + uch * 8;
   const int32_t un = rank - (int32_t)uch * 8;
   auto load_up = [&](uint32_t i) {
-    const uint32_t o0 = (c + i * C) * kBN, at = up0 + (i & 1) * L::kUp;
+    const uint32_t o0 = (c + i * C) * kBN, at = up0 + i % L::kUps * L::kUp;
 #pragma unroll
     for (uint32_t r = 0; r < kBN; r += span) {
       const bool there = o0 + r + urow < P.N;
@@ -564,28 +623,15 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const Ap
       else fill8(dst, upp + (uint64_t)(o0 + r) * A.ld_up, there ? un : 0, A.vec_up);
     }
   };
-  const int32_t r0 = srow[wr * 16 + g], r1 = srow[wr * 16 + g + 8];
-  uint16_t* const yp0 = P.y + (int64_t)(r0 >= 0 ? r0 : row_a) * P.ldy + wh * 64 + 8 * q;
-  uint16_t* const yp1 = P.y + (int64_t)(r1 >= 0 ? r1 : row_a) * P.ldy + wh * 64 + 8 * q;
-  const int32_t left = (int32_t)P.N - (int32_t)(wh * 64 + 8 * q);
-  uint4 y0[2], y1[2];
-  auto load_y = [&](uint32_t i) {
-#pragma unroll
-    for (uint32_t h = 0; h < 2; h++) {
-      const uint32_t at = (c + i * C) * kBN + h * 32;
-      const int32_t n = left - (int32_t)at;
-      y0[h] = load8(yp0 + at, n, VEC || P.vec_y);
-      y1[h] = load8(yp1 + at, n, VEC || P.vec_y);
-    }
-  };
-  if (todo > 0) {
-    load_up(0);
-    load_y(0);
-  }
-  cp_commit();
-
   // join the sums of the cluster's blocks: each joins some of the rows and hands them to all
   cluster.sync();
+  if (!VEC && todo > 0) load_y(0);
+#pragma unroll
+  for (uint32_t i = 0; i + 1 < L::kUps; i++) {
+    if (i < todo) load_up(i);
+    cp_commit();
+    cp_commit();   // (in the place of a y: every step has two groups)
+  }
   {
     const uint32_t rows = 64 / C;
     for (uint32_t e = tid * 2; e < rows * RP; e += kThreads * 2) {
@@ -613,10 +659,18 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const Ap
   cluster.sync();   // low is complete, and nobody reads another block's memory after this
 
   for (uint32_t i = 0; i < todo; i++) {
-    cp_wait<0>();
+    cp_wait<L::kPending>();
     __syncthreads();
-    if (i + 1 < todo) load_up(i + 1);
+    if (i + L::kUps - 1 < todo) load_up(i + L::kUps - 1);
     cp_commit();
+    if (VEC) {
+#pragma unroll
+      for (uint32_t h = 0; h < 2; h++) {
+        const uint32_t src = yring + i % L::kYs * L::kY + h * 2 * kThreads * 16;
+        y0[h] = lds16(src);
+        y1[h] = lds16(src + kThreads * 16);
+      }
+    }
     float d[2][4][4];   // y is the sum's first term
 #pragma unroll
     for (int h = 0; h < 2; h++) {
@@ -630,8 +684,9 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const Ap
         d[h][j][3] = bf16_hi(b[j]);
       }
     }
-    if (i + 1 < todo) load_y(i + 1);
-    const uint32_t at = up0 + (i & 1) * L::kUp;
+    if (VEC ? i + L::kYs < todo : i + 1 < todo) load_y(VEC ? i + L::kYs : i + 1);
+    cp_commit();
+    const uint32_t at = up0 + i % L::kUps * L::kUp;
 #pragma unroll
     for (int ks = 0; ks < RP / 16; ks++) {
       if (ks * 16 >= rank) break;
@@ -684,22 +739,10 @@ struct Expand {
   }
 };
 
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds8(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
-}
-
+// (At rank 128 low takes 64 registers: two blocks an SM spill, 130 us at 16384 rows of 4096 x 4096,
+// one does not, 119 us.)
 template <int RP>
-__global__ void __launch_bounds__(kThreads, 2) k_expand(const ApplyArgs P) {
+__global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_expand(const ApplyArgs P) {
   using L = Expand<RP>;
   constexpr int KS = RP >= 32 ? RP / 32 : 1;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -1107,7 +1150,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_wgrad(const WgradArgs P) {
 template <int RP>
 cudaError_t launch_apply(bool small, bool vec, uint32_t tiles, uint32_t C, const ApplyArgs& P,
                          cudaStream_t s) {
-  if (small) return launch(k_apply16<RP>, dim3(tiles * C), kThreads, Apply16<RP>::kSmem, C, s, P);
+  if constexpr (RP <= 64) {
+    if (small) return launch(k_apply16<RP>, dim3(tiles * C), kThreads, Apply16<RP>::kSmem, C, s, P);
+  }
   return launch(vec ? k_apply64<RP, true> : k_apply64<RP, false>, dim3(tiles * C), kThreads,
                 Apply64<RP>::kSmem, C, s, P);
 }
@@ -1120,12 +1165,11 @@ cudaError_t launch_wgrad(uint32_t grid, const WgradArgs& P, cudaStream_t s) {
   return launch(k_wgrad<RP>, dim3(grid), kThreads, Wgrad<RP>::kSmem, 1, s, P);
 }
 
-// Blocks of a cluster that share a tile: as many as keep all blocks on the SMs at once (`slots`).
-// Above that a second round waits for the first: 64 tiles of 64 rows with 4 blocks each take 25 us,
-// with 8 each 29 us (4096 x 4096, rank 16).
-uint32_t cluster_for(uint64_t tiles, uint64_t slots) {
+// Blocks of a cluster that share a tile: as many as the SMs hold at once, `slots` of them (`slots8`
+// of clusters of 8, which not every corner of the GPU takes).
+uint32_t cluster_for(uint64_t tiles, uint64_t slots, uint64_t slots8) {
   uint32_t c = 1;
-  while (c < kMaxCluster && tiles * c * 2 <= slots) c *= 2;
+  while (c < kMaxCluster && tiles * c * 2 <= (c == 4 ? slots8 : slots)) c *= 2;
   return c;
 }
 
@@ -1140,6 +1184,8 @@ uint32_t tile_bound(uint32_t rows, uint32_t k, uint32_t high) {
   const uint64_t b = (uint64_t)rows / high + k;
   return (uint32_t)(b < rows ? b : rows);
 }
+// ... as many as to expect: an adapter's last tile is there in two cases of three.
+uint32_t tile_guess(uint32_t rows, uint32_t k, uint32_t high) { return tile_bound(rows, 2 * k / 3 + 1, high); }
 
 int apply(uint32_t RP, const bo_adapter_rows* R, ApplyArgs& P, int sms, cudaStream_t s) {
   const uint32_t rows = R->rows, k = R->k;
@@ -1150,11 +1196,11 @@ int apply(uint32_t RP, const bo_adapter_rows* R, ApplyArgs& P, int sms, cudaStre
     const uint32_t tiles = tile_bound(rows, k, 128);
     P.tiles = static_cast<const Tile*>(R->d_tiles[2]);
     P.ntiles = R->d_ntiles + 2;
-    const int rc = check(tc_low(RP, tiles, cluster_for(tiles, sms), P, s));
+    const int rc = check(tc_low(RP, tiles, cluster_for(tiles, sms, sms), P, s));
     if (rc || !P.y) return rc;
     P.tiles = static_cast<const Tile*>(R->d_tiles[1]);
     P.ntiles = R->d_ntiles + 1;
-    const uint32_t grid = 2 * sms;
+    const uint32_t grid = (RP <= 64 ? 2 : 1) * sms;
     switch (RP) {
       case 16: return check(launch_expand<16>(grid, P, s));
       case 32: return check(launch_expand<32>(grid, P, s));
@@ -1162,12 +1208,25 @@ int apply(uint32_t RP, const bo_adapter_rows* R, ApplyArgs& P, int sms, cudaStre
       default: return check(launch_expand<128>(grid, P, s));
     }
   }
-  // Tiles of 16 rows while the adapters have few rows each: a tile of 64 would be mostly empty.
-  const bool small = rows <= 128 || rows / k < 24;
-  const uint32_t tiles = tile_bound(rows, k, small ? 16 : 64);
+  // Tiles of 16 rows have the shorter way to a result, tiles of 64 read the factors less often and
+  // carry less in registers (us, tiles of 16 / of 64):
+  //   rank 16, 4096 x 4096:   1 row 5.2 / 6.6, 512 rows of 8 adapters 6.6 / 7.6, 1024 of 32 10.5 / 9.8,
+  //                           1024 of 64 11.1 / 17.1, 2048 of 64 25 / 20
+  //   rank 64, 4096 x 11008:  1 row 15.7 / 16.8, 128 of 1 16.0 / 19.1, 64 of 64 47 / 41, 256 of 8 20 / 18
+  //   rank 128, 4096 x 4096:  1 row 18.6 / 16.0, 64 of 64 114 / 48
+  const bool small = RP <= 32   ? rows <= 512 || rows / k < 24
+                     : RP == 64 ? tile_guess(rows, k, 16) <= 16
+                                : false;
+  const uint32_t tiles = tile_bound(rows, k, small ? 16 : 64), guess = tile_guess(rows, k, small ? 16 : 64);
   P.tiles = static_cast<const Tile*>(R->d_tiles[small ? 0 : 1]);
   P.ntiles = R->d_ntiles + (small ? 0 : 1);
-  const uint32_t C = cluster_for(tiles, (uint64_t)sms * (small ? 4 : RP == 128 ? 1 : 2));
+  // Blocks of 64 rows fit twice on an SM (of rank 128 once), of 16 rows three times.  Past that a
+  // second round waits for the first: 64 tiles of 16 rows with 4 / 8 blocks each take 8.5 / 12.3 us,
+  // 32 of them 8.0 / 6.6 us; 64 tiles of 64 rows with 2 / 4 / 8 28.5 / 20.2 / 25.1 us (rank 16).
+  const uint64_t n = (uint64_t)sms;
+  const uint32_t C = small       ? cluster_for(guess, 3 * n, n * 12 / 5)
+                     : RP == 128 ? cluster_for(guess, n, n * 2 / 3)
+                                 : cluster_for(guess, 2 * n, 2 * n);
   switch (RP) {
     case 16: return check(launch_apply<16>(small, vec, tiles, C, P, s));
     case 32: return check(launch_apply<32>(small, vec, tiles, C, P, s));

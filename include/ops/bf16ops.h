@@ -161,7 +161,7 @@ BD_API int bo_adamw_moments(const bo_adamw* h, uint32_t dtype, void* d_m, void* 
  * order of every sum is fixed for given sizes.
  *
  * x, y, dy, dx: rows of BF16 with a row stride in elements; any sizes and strides (16-byte
- * aligned rows, with hidden, out and ranks multiples of 8, take wide accesses). */
+ * aligned rows, with hidden and out multiples of 8, take wide accesses). */
 
 #define BO_ADAPTER_MAX_RANK 128u
 #define BO_ADAPTER_MAX_COUNT 65535u   /* adapters of a set */

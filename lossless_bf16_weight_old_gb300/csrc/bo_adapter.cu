@@ -195,12 +195,24 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
   return v;
 }
 
-// Eight values from p, of which the first n exist (n <= 0: none); the others are 0.
+// Eight values from p, of which the first n exist (n <= 0: none); the others are 0.  Off the
+// 16-byte boundary they come as the 4-byte words that they fill, and the ends.
+__device__ __forceinline__ uint32_t ld4(const uint16_t* p) {
+  return *reinterpret_cast<const uint32_t*>(p);
+}
 __device__ __forceinline__ uint4 gather8(const uint16_t* p, int32_t n) {
   uint32_t w[4] = {0, 0, 0, 0};
+  if (n >= 8) {   // (one way for both: neighbouring rows may differ)
+    const uint32_t odd = (uint32_t)reinterpret_cast<uintptr_t>(p) >> 1 & 1;
+    const uint32_t t[5] = {odd ? (uint32_t)p[0] << 16 : ld4(p), ld4(p + 2 - odd), ld4(p + 4 - odd),
+                           ld4(p + 6 - odd), odd ? p[7] : 0u};
 #pragma unroll
-  for (int j = 0; j < 8; j++)
-    if (j < n) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+    for (int j = 0; j < 4; j++) w[j] = __funnelshift_r(t[j], t[j + 1], 16 * odd);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+      if (j < n) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ uint4 load8(const uint16_t* p, int32_t n, bool vec) {
@@ -224,6 +236,19 @@ __device__ __forceinline__ void store8(uint16_t* p, uint4 v, int32_t n, bool vec
     return;
   }
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (n >= 8) {
+    const uint32_t odd = (uint32_t)reinterpret_cast<uintptr_t>(p) >> 1 & 1;
+#pragma unroll
+    for (int j = 0; j < 3; j++)
+      *reinterpret_cast<uint32_t*>(p + odd + 2 * j) = __funnelshift_r(w[j], w[j + 1], 16 * odd);
+    if (odd) {
+      p[0] = (uint16_t)w[0];
+      p[7] = (uint16_t)(w[3] >> 16);
+    } else {
+      *reinterpret_cast<uint32_t*>(p + 6) = w[3];
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 8; j++)
     if (j < n) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
@@ -452,7 +477,8 @@ struct Apply64 {
   static constexpr int kMR = RP <= 64 ? 2 : 1;
 };
 
-// VEC: every row of x, y and of the factors can be read 16 bytes at a time.
+// VEC: every row of x, y and of the first factors can be read 16 bytes at a time.  (Rows of the
+// second, of any rank, are read as they lie.)
 template <int RP, bool VEC>
 __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const ApplyArgs P) {
   using L = Apply64<RP>;
@@ -619,8 +645,8 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const Ap
     for (uint32_t r = 0; r < kBN; r += span) {
       const bool there = o0 + r + urow < P.N;
       const uint32_t dst = at + swz_dealt<RP>(r + urow, uch);
-      if (VEC) cp16n(dst, there && un > 0 ? upp + (uint64_t)(o0 + r) * A.ld_up : A.up, there ? un : 0);
-      else fill8(dst, upp + (uint64_t)(o0 + r) * A.ld_up, there ? un : 0, A.vec_up);
+      if (A.vec_up) cp16n(dst, there && un > 0 ? upp + (uint64_t)(o0 + r) * A.ld_up : A.up, there ? un : 0);
+      else sts16(dst, gather8(upp + (uint64_t)(o0 + r) * A.ld_up, there ? un : 0));
     }
   };
   // join the sums of the cluster's blocks: each joins some of the rows and hands them to all
@@ -768,7 +794,8 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_expand(const App
       const uint32_t row = s / (RP / 8), ch = s % (RP / 8);
       const int32_t n = n0 + row < P.N ? rank - (int32_t)ch * 8 : 0;
       const uint16_t* src = n > 0 ? A.up + (uint64_t)(n0 + row) * A.ld_up + ch * 8 : A.up;
-      cp16n(bs + L::at(row, ch * 16), src, n);
+      if (A.vec_up) cp16n(bs + L::at(row, ch * 16), src, n);
+      else sts16(bs + L::at(row, ch * 16), gather8(src, n));
     }
     cp_commit();   // (waited for below, with the first pieces of y on their way too)
 
@@ -1343,7 +1370,7 @@ int bo_adapter_set_init(const bo_adapter* h_items, uint32_t k, uint32_t hidden, 
     d.vec_up = wide(a.d_up, a.ld_up, 8);   // (a rank's last 16 bytes are read in part)
     d.vec_gup = a.d_grad_up && wide(a.d_grad_up, a.ld_grad_up, a.rank);
     d.pad[0] = d.pad[1] = d.pad[2] = 0;
-    if (!d.vec_down || !d.vec_up) all_wide = false;
+    if (!d.vec_down) all_wide = false;
     if (a.rank > most) most = a.rank;
   }
   const int rc = check(upload(dev.get(), (uint64_t)k * sizeof(DevAdapter), d_set,

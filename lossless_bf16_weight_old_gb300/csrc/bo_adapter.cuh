@@ -62,7 +62,7 @@ struct ApplyArgs {
   uint16_t* low;          // may be NULL
   uint32_t K, N;
   uint32_t vec_x, vec_y;  // rows may be read 16 bytes at a time
-  uint32_t vec_factors;   // ... of every adapter's factors
+  uint32_t vec_factors;   // ... of every adapter's first factor
   int32_t* status;        // BD_ERR_CUDA when a wait inside a kernel ran out; may be NULL
 };
 

@@ -127,6 +127,7 @@ constexpr uint32_t kHalves = 2;   // of a stage, each a swizzled line (64 values
 struct alignas(8) Control {
   uint64_t full[kMaxStages], freed[kMaxStages], done[2], drained[2];
   uint32_t tmem, last, pad[2];
+  float turn[4][32][17];   // 16 columns of dB of the four warps that write gradients
 };
 
 // A product waits for the one before it into the same sums (about 180 cycles, whatever its width),
@@ -472,6 +473,7 @@ __global__ void __launch_bounds__(32 * (kCopyWarps + 5), 1) k_wgrad_tc(const Wgr
     __syncwarp();
   } else {   // carries the sums out: a thread has a feature
     const uint32_t quarter = warp & 3, fl = quarter * 32 + lane, t = tid - 32 * (kCopyWarps + 1);
+    float(&turn)[32][17] = ctl->turn[quarter];
     auto meet = [](bool yes) {   // of the four warps: whether all say yes
       uint32_t r;
       asm volatile(
@@ -579,21 +581,34 @@ __global__ void __launch_bounds__(32 * (kCopyWarps + 5), 1) k_wgrad_tc(const Wgr
           for (uint32_t part = 0; part < W; part += 16) {
             const uint32_t col = wide + part;
             const float(&v)[16] = reinterpret_cast<const float(&)[16]>(sum[part]);
-            if (!real || col >= A.rank) continue;
+            if (col >= A.rank) continue;
+            if (!down && (P.accumulate || P.grad_f32 || !A.vec_gup)) {
+              // a row's values lie in one thread: handed out, so that sixteen lanes write a row
+#pragma unroll
+              for (uint32_t j = 0; j < 16; j++) turn[lane][j] = v[j];
+              __syncwarp();
+              const uint32_t j = lane & 15, row = f - lane + (lane >> 4);   // and every other one
+              uint64_t o = (uint64_t)row * A.ld_gup + col + j;
+              const uint32_t n = col + j < A.rank && row < P.out ? (P.out - row + 1) / 2 : 0;
+#pragma unroll 2
+              for (uint32_t r = 0; r < 16 && r < n; r++, o += 2 * (uint64_t)A.ld_gup)
+                put_grad(A.gup, o, turn[(lane >> 4) + 2 * r][j], P.grad_f32, P.accumulate);
+              __syncwarp();
+              continue;
+            }
+            if (!real) continue;
             if (P.accumulate || P.grad_f32) {
 #pragma unroll
               for (uint32_t j = 0; j < 16; j++) {
                 if (col + j >= A.rank) break;
-                const uint64_t o = down ? (uint64_t)(col + j) * A.ld_gdown + f
-                                        : (uint64_t)f * A.ld_gup + col + j;
-                put_grad(down ? A.gdown : A.gup, o, v[j], P.grad_f32, P.accumulate);
+                put_grad(A.gdown, (uint64_t)(col + j) * A.ld_gdown + f, v[j], P.grad_f32, P.accumulate);
               }
             } else if (down) {   // neighbouring features in neighbouring lanes
               uint16_t* p = static_cast<uint16_t*>(A.gdown) + (uint64_t)col * A.ld_gdown + f;
 #pragma unroll
               for (uint32_t j = 0; j < 16; j++, p += A.ld_gdown)
                 if (col + j < A.rank) *p = (uint16_t)pack_bf16(v[j], 0.f);
-            } else if (A.vec_gup) {   // (the rank is a multiple of 8 then)
+            } else {   // (the rank is a multiple of 8 here)
               uint16_t* const p = static_cast<uint16_t*>(A.gup) + (uint64_t)f * A.ld_gup + col;
 #pragma unroll
               for (uint32_t j = 0; j < 16; j += 8)
@@ -601,11 +616,6 @@ __global__ void __launch_bounds__(32 * (kCopyWarps + 5), 1) k_wgrad_tc(const Wgr
                   *reinterpret_cast<uint4*>(p + j) =
                       make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]),
                                  pack_bf16(v[j + 4], v[j + 5]), pack_bf16(v[j + 6], v[j + 7]));
-            } else {
-              uint16_t* const p = static_cast<uint16_t*>(A.gup) + (uint64_t)f * A.ld_gup + col;
-#pragma unroll
-              for (uint32_t j = 0; j < 16; j++)
-                if (col + j < A.rank) p[j] = (uint16_t)pack_bf16(v[j], 0.f);
             }
           }
         }

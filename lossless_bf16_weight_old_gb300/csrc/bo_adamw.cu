@@ -2,9 +2,10 @@
 // gradient norm (include/ops/bf16ops.h has the formulas and the layout of the state).
 //
 // One table entry per 2048 elements carries everything a block needs, so a launch covers any
-// number of tensors and a block's work is one 48-byte load away.  All kernels are bound by HBM:
-// the step moves 28 bytes per element (BF16 gradients, FP32 master, 32-bit moments; 16 with
-// 8-bit moments), the norm 2.
+// number of tensors and a block's work is one 48-byte load away.  The step moves 28 bytes per
+// element (BF16 gradients, FP32 master, 32-bit moments; 16 with 8-bit moments), the norm 2.  HBM
+// bounds all but the step with 8-bit moments, which arithmetic bounds.  Measured rates stand at
+// the kernels, beside the 6.77 TB/s of a copy.
 #include <cmath>
 #include <cstring>
 #include <memory>
@@ -307,6 +308,9 @@ struct Eight {   // a thread's elements
   }
 };
 
+// Eight elements a thread, all loads of a chunk in flight at once: 625M elements (BF16 gradients,
+// FP32 master) in 2542 us, 6.9 TB/s; the smallest step, fourteen tensors, 4.2 us a call.  The
+// moments and p are rounded to FP32 once an operation, a BF16 weight once from FP32.
 template <int WK, bool GF32>
 __global__ void __launch_bounds__(kThreads, 4) k_step32(const StepParams P) {
   after_previous();
@@ -483,7 +487,11 @@ __device__ __forceinline__ uint32_t low_bytes(float2 a, float2 b) {
 }
 
 // One warp per block of 256: its eight elements a lane stay in registers while the block's
-// maxima are found, so each byte is read and written once.
+// maxima are found, so each byte is read and written once.  202M elements (BF16 gradients, FP32
+// master) take 605 us, 5.3 TB/s: 84 instructions an element keep the FP32 pipes busy, and HBM is
+// not the bound.  Four blocks an SM at 64 registers: three have room for more and take 775 us.
+// Fetching the next chunk ahead through shared memory does not help either (711 us, of BF16
+// weights 134 us for 40M elements with and without).
 template <int WK, bool GF32>
 __global__ void __launch_bounds__(kThreads, 4) k_step8(const StepParams P) {
   after_previous();
@@ -603,6 +611,7 @@ __device__ __forceinline__ void put8(void* out, uint64_t t, const float (&x)[8])
                                              pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
   }
 }
+// 6 bytes an element with BF16 values: 202M elements in 190 us, 6.4 TB/s.
 template <bool F32>
 __global__ void __launch_bounds__(kThreads) k_moments(const bo_adamw_state st,
                                                        void* __restrict__ out_m,
@@ -641,7 +650,8 @@ __global__ void __launch_bounds__(kThreads) k_moments(const bo_adamw_state st,
 
 // --------------------------------------------------------------------------- gradient norm
 // Sums in a fixed order: eight FP32 sums a thread over its elements, joined in FP64 over the
-// block, and the blocks' sums by the last block to finish.
+// block, and the blocks' sums by the last block to finish.  202M BF16 gradients in 74 us, 5.5 TB/s
+// (reads alone, and the join at the end; with twice the blocks it is slower).
 template <bool GF32>
 __global__ void __launch_bounds__(kThreads, 8) k_norm(const Chunk* __restrict__ table,
                                                       uint64_t chunks, double* __restrict__ part,

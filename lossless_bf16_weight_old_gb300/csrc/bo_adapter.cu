@@ -35,7 +35,9 @@ constexpr uint32_t kThreads = 256;   // eight warps
 
 // ------------------------------------------------------------------------ grouping the rows
 // One block per adapter counts its rows, then one block per adapter places them in order: the
-// grouping is stable, so every later sum over an adapter's rows has one order.
+// grouping is stable, so every later sum over an adapter's rows has one order.  Latency and the
+// number of adapters bound it, since each reads the whole index: 64 rows of 64 adapters 1.8 + 2.7
+// us, 16384 of 8 3.3 + 8.9 us, 131072 of 16 18 + 58 us.  A model step groups once for all layers.
 __global__ void __launch_bounds__(kThreads) k_rows_count(const int32_t* __restrict__ index,
                                                          uint32_t rows, uint32_t k,
                                                          int32_t* __restrict__ counts,
@@ -283,7 +285,9 @@ __device__ __forceinline__ uint32_t swz_dealt(uint32_t row, uint32_t chunk) {
 // the fragments come straight from global memory, every load of a warp independent of the
 // others.  low enters the second product as two BF16 numbers, its rounding and what that cut
 // off: with few rows the rounding errors of low would not average out in y, and the products
-// cost nothing beside the latency of the loads.
+// cost nothing beside the latency of the loads.  What bounds it is the chain from the row's number
+// to the stores, five trips to memory and one across the cluster: one row of rank 16 takes 4.8 us
+// (4096 x 4096), 64 rows of 48 adapters 8.6 us (4096 x 11008, whose bytes take 3.9 us).
 template <int RP>
 struct Apply16 {
   static constexpr uint32_t kULd = RP + 8;
@@ -451,6 +455,11 @@ __global__ void __launch_bounds__(kThreads) k_apply16(const ApplyArgs P) {
 }
 
 // ---------------------------------------------------------------------- tiles of 64 rows
+// x and the factors through a ring of stages, two blocks an SM.  2048 rows of rank 16 (4096 x 4096)
+// take 14.2 us for 50 MB: 1.1 us until the rows are known, 5.3 us of reading (at 6.3 TB/s, y
+// included), 2.5 us for the sums to meet, 2.9 us of storing; with all tiles on the SMs at once
+// nothing overlaps the middle.  A third block an SM would need 80 registers: the loads then sink
+// to their uses (16384 rows, rank 64: 246 us became 378).
 constexpr uint32_t kBK = 64;     // values of the first sum per stage
 constexpr uint32_t kBN = 128;    // columns of the second product per step
 constexpr uint32_t kStages = 4;
@@ -749,7 +758,10 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const Ap
 // With low known, the blocks take equal shares of (columns, rows): a block keeps 256 columns' rows
 // of B in shared memory and runs down the adapter's rows, each warp by itself over 32 rows at a
 // time and 32 columns a step, so that B is read once per block and nothing waits for another
-// warp.  A thread's own pieces of y come through a ring of asynchronous copies four steps deep.
+// warp.  A thread's own pieces of y come through a ring of asynchronous copies four steps deep,
+// which fetch 256 bytes of L2 at once; the stores are streamed (186, 176 and 172 us without, with
+// the one and with both).  16384 rows of rank 64 and 14336 columns: 172 us for 940 MB, 5.5 TB/s;
+// issue is active half of the time, and reads and writes of the same pages take turns.
 template <int RP>
 struct Expand {
   static constexpr uint32_t kN = RP <= 64 ? 256 : 128;   // columns of a block
@@ -918,7 +930,9 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_expand(const App
 
 // ---------------------------------------------------------------- transposes of the factors
 // down (rank x hidden) to hidden x RP and up (out x rank) to RP x out8, both zero-padded, and a
-// table entry that has them in the other's place.
+// table entry that has them in the other's place.  4.8 us for four adapters of rank 64 (4096 and
+// 11008 features, 15 MB), mostly latency; the factors change with every step of training, so the
+// transposes are made in every call.
 constexpr uint32_t kTF = 64;   // features a block turns at a time
 template <int RP>
 __global__ void __launch_bounds__(kThreads) k_transpose(const DevAdapter* __restrict__ table,
@@ -990,6 +1004,8 @@ __global__ void __launch_bounds__(kThreads) k_transpose(const DevAdapter* __rest
 // rows in stages of 64.  The blocks take equal shares of all stages of all pieces, so none waits
 // while another works; a piece that several blocks share is joined by the one that ends last, in
 // the order of the blocks, from their sums in the workspace.
+// This form, on mma.sync, takes what the other's 16-byte copies cannot: 8192 rows of 4095 and 4097
+// features, rank 64, take 157 us; of 4096, there, 38 us.
 constexpr uint32_t kWStages = 3;
 template <int RP>
 struct Wgrad {

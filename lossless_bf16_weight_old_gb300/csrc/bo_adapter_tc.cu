@@ -200,8 +200,10 @@ __device__ __forceinline__ void stage_issued(Control* ctl, uint32_t i) {
 }
 
 // ---------------------------------------------------------------------- low = s A x, 128 rows
-// A stage is 64 values of the sum: 128 rows of x (16 KB) and the factor's rows.  The blocks of a
-// cluster split the sum and join through distributed shared memory in a fixed order.
+// Half a stage is 64 values of the sum: 128 rows of x (16 KB) and the factor's rows.  The blocks of
+// a cluster split the sum and join through distributed shared memory in a fixed order.  16384 rows
+// of 4096, rank 64: 32 us for 134 MB, 4.2 TB/s.  Without the copies of x it is 17 us, without the
+// products 31: reading bounds it, on 128 SMs (one tile each).
 template <int RP>
 struct Low {
   static constexpr uint32_t kThreads = 288;
@@ -354,7 +356,9 @@ __global__ void __launch_bounds__(288, 1) k_low(const ApplyArgs P) {
 // rows in stages of 64.  The blocks take equal shares of all stages of all pieces, so none waits
 // while another works; a piece that several blocks share is joined by the one that ends last, in
 // the order of the blocks, from their sums in the workspace.  Four warps carry a piece out while
-// the next one's stages arrive and are multiplied into the other set of sums.
+// the next one's stages arrive and are multiplied into the other set of sums.  8191 rows of 4
+// adapters, 4096 and 11008 features, rank 64: 61 us for 247 MB, 4.0 TB/s, of which 53 us are the
+// reading and the rest its start and the last piece's join; 2048 rows of 4096 + 4096: 14.5 us.
 template <int RP>
 struct WgradTc {
   static constexpr uint32_t kThreads = 32 * (kCopyWarps + 1 + 4);

@@ -229,8 +229,18 @@ __device__ __forceinline__ uint4 load8w(const uint16_t* p, int32_t n, bool vec) 
 }
 // ... into shared memory
 __device__ __forceinline__ void fill8(uint32_t dst, const uint16_t* p, int32_t n, bool vec) {
-  if (vec) cp16n(dst, p, n);
-  else sts16(dst, gather8(p, n));
+  if (vec) {
+    cp16n(dst, p, n);
+  } else if (n >= 8 && !(reinterpret_cast<uintptr_t>(p) & 2)) {
+    // rows of even widths: not waited for either (8192 rows of 4094 and 4098, rank 16: forward 110
+    // us, with loads and stores 128)
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + 4 * j), "l"(p + 2 * j)
+                   : "memory");
+  } else {
+    sts16(dst, gather8(p, n));
+  }
 }
 __device__ __forceinline__ void store8(uint16_t* p, uint4 v, int32_t n, bool vec) {
   if (vec) {
@@ -1034,9 +1044,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_wgrad(const WgradArgs P) {
   constexpr uint32_t per = RP / 8, span = kThreads / per, PN = (64 + span - 1) / span;
   const uint32_t pch = tid % per, prow = tid / per;
 
-  Shares sh;
-  sh.all = (uint64_t)P.blocks[P.k] * slices;
-  sh.G = gridDim.x < sh.all ? gridDim.x : (uint32_t)sh.all;
+  const Shares sh((uint64_t)P.blocks[P.k] * slices, gridDim.x);
   if (blockIdx.x >= sh.G) return;
   const uint64_t s_begin = sh.begin(blockIdx.x);
   for (Piece Q(P, slices, s_begin, sh.begin(blockIdx.x + 1)); !Q.over(); Q.next(P, slices)) {
@@ -1156,10 +1164,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_wgrad(const WgradArgs P) {
                *reinterpret_cast<const float2*>(part + e / RP * L::kLd + e % RP));
       // the blocks of the piece's first and last stage
       const uint64_t p_last = Q.begin + Q.stages - 1;
-      b0 = (uint32_t)(Q.begin * sh.G / sh.all);
-      while (sh.begin(b0 + 1) <= Q.begin) b0++;
-      b1 = (uint32_t)(p_last * sh.G / sh.all);
-      while (sh.begin(b1 + 1) <= p_last) b1++;
+      b0 = sh.owner(Q.begin);
+      b1 = sh.owner(p_last);
       __threadfence();
       __syncthreads();
       if (tid == 0)

@@ -99,9 +99,20 @@ __device__ __forceinline__ void put_grad(void* base, uint64_t at, float v, bool 
 
 // A block's share of all stages of all pieces, and the piece that a stage belongs to.
 struct Shares {
-  uint64_t all;
-  uint32_t G;   // blocks that have a share (none is empty, so those of a piece are consecutive)
-  __device__ __forceinline__ uint64_t begin(uint64_t b) const { return all * b / G; }
+  uint64_t all, each;
+  uint32_t G, rest;   // blocks that have a share (none is empty, so those of a piece are consecutive)
+  __device__ __forceinline__ Shares(uint64_t stages, uint32_t grid)
+      : all(stages), G(grid < stages ? grid : (uint32_t)stages) {
+    each = G ? all / G : 0;
+    rest = (uint32_t)(all - each * G);
+  }
+  // all b / G (a grid has a few hundred blocks)
+  __device__ __forceinline__ uint64_t begin(uint32_t b) const { return each * b + rest * b / G; }
+  __device__ __forceinline__ uint32_t owner(uint64_t stage) const {
+    uint32_t b = (uint32_t)(stage * G / all);
+    while (begin(b + 1) <= stage) b++;
+    return b;
+  }
 };
 // Walks over the pieces of a block's share; only a new adapter is looked up.
 struct Piece {

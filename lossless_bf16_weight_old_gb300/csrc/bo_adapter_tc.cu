@@ -190,7 +190,7 @@ __device__ __forceinline__ bool stage_free(Control* ctl, uint32_t i) {
 // ... and lets the stage's barrier know when what this thread has copied into it is there.  The
 // copying warps never wait for their copies, and the fence between them and the tensor cores is
 // the issuing thread's.  (With both in the copying warps and stages of half the size k_wgrad_tc
-// takes 67.7 us instead of 61.3 over 8191 rows of 4096 + 11008 features, k_low 33.0 instead of 32.0
+// takes 67.7 us instead of 61.3 (59 now) over 8191 rows of 4096 + 11008 features, k_low 33.0 instead of 32.0
 // over 16384 rows of 4096; rank 64.)
 template <uint32_t S>
 __device__ __forceinline__ void stage_issued(Control* ctl, uint32_t i) {
@@ -357,8 +357,8 @@ __global__ void __launch_bounds__(288, 1) k_low(const ApplyArgs P) {
 // while another works; a piece that several blocks share is joined by the one that ends last, in
 // the order of the blocks, from their sums in the workspace.  Four warps carry a piece out while
 // the next one's stages arrive and are multiplied into the other set of sums.  8191 rows of 4
-// adapters, 4096 and 11008 features, rank 64: 61 us for 247 MB, 4.0 TB/s, of which 53 us are the
-// reading and the rest its start and the last piece's join; 2048 rows of 4096 + 4096: 14.5 us.
+// adapters, 4096 and 11008 features, rank 64: 59 us for 247 MB, 4.2 TB/s, of which 53 us are the
+// reading and the rest its start and the last piece's join; 2048 rows of 4096 + 4096: 13.3 us.
 template <int RP>
 struct WgradTc {
   static constexpr uint32_t kThreads = 32 * (kCopyWarps + 1 + 4);
@@ -388,9 +388,7 @@ __global__ void __launch_bounds__(32 * (kCopyWarps + 5), 1) k_wgrad_tc(const Wgr
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   after_previous();
   const uint32_t hs = (P.hidden + kFeat - 1) / kFeat, slices = hs + (P.out + kFeat - 1) / kFeat;
-  Shares sh;
-  sh.all = (uint64_t)P.blocks[P.k] * slices;
-  sh.G = gridDim.x < sh.all ? gridDim.x : (uint32_t)sh.all;
+  const Shares sh((uint64_t)P.blocks[P.k] * slices, gridDim.x);
   if (blockIdx.x >= sh.G) return;
   const uint64_t s_begin = sh.begin(blockIdx.x), s_end = sh.begin(blockIdx.x + 1);
   const uint32_t tmem = begin_block(ctl, S, M::kAlloc);
@@ -504,10 +502,8 @@ __global__ void __launch_bounds__(32 * (kCopyWarps + 5), 1) k_wgrad_tc(const Wgr
       uint32_t* const count = P.counters + (uint64_t)Q.adapter * slices + Q.slice;
       if (!whole) {
         const uint64_t p_last = Q.begin + Q.stages - 1;
-        b0 = (uint32_t)(Q.begin * sh.G / sh.all);
-        while (sh.begin(b0 + 1) <= Q.begin) b0++;
-        b1 = (uint32_t)(p_last * sh.G / sh.all);
-        while (sh.begin(b1 + 1) <= p_last) b1++;
+        if (Q.begin < s_begin) b0 = sh.owner(Q.begin);
+        if (p_last >= s_end) b1 = sh.owner(p_last);
       }
       bool kept = whole;                           // this block's part stays in tensor memory
       auto look = [&]() {                          // whether the other parts are there
@@ -522,7 +518,7 @@ __global__ void __launch_bounds__(32 * (kCopyWarps + 5), 1) k_wgrad_tc(const Wgr
         __threadfence();
         return r;
       };
-      constexpr uint32_t W = RP < 64 ? RP : 64;    // columns joined at once
+      constexpr uint32_t W = RP < 32 ? RP : 32;    // columns joined at once (64 spill: 66 us, not 59)
       auto join = [&](uint32_t wide, uint32_t q, float (&sum)[W]) {   // block q's first piece, or its last
         const float* p =
             P.sums + (2 * (uint64_t)q + (sh.begin(q) < Q.begin)) * (kFeat * RP) + wide * kFeat + fl;
@@ -542,7 +538,7 @@ __global__ void __launch_bounds__(32 * (kCopyWarps + 5), 1) k_wgrad_tc(const Wgr
       const uint32_t from = tmem + b * M::kCols + (quarter << 21);
       bool write = true;
       if (!whole && !early) {
-        kept = look();
+        kept = b0 == blockIdx.x && look();   // (the others are not expected to be last)
         if (!kept) {   // this part to the workspace; the last block to do so joins
           float* const to = P.sums + (2 * (uint64_t)blockIdx.x + (Q.at != s_begin)) * (kFeat * RP) + fl;
 #pragma unroll 1

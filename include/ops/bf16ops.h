@@ -193,7 +193,7 @@ typedef struct bo_adapter_set {
 typedef struct bo_adapter_rows {
   const int32_t* d_perm;     /* rows, grouped */
   const int32_t* d_offsets;  /* adapter a has d_perm[d_offsets[a] .. d_offsets[a + 1]) */
-  const int32_t* d_blocks;   /* blocks of 64 rows (at least one) of the adapters before */
+  const int32_t* d_blocks;   /* blocks of 64 rows (counted as at least four) of the adapters before */
   const void* d_tiles[3];    /* tiles of at most 16, 64 and 128 rows of one adapter */
   const int32_t* d_ntiles;   /* how many of each */
   int32_t* d_status;         /* as given; also BD_ERR_CUDA from a call whose waits ran out */

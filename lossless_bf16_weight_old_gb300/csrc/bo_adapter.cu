@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads) k_rows_place(
     c16 += (c + 15) / 16;
     c64 += (c + 63) / 64;
     c128 += (c + 127) / 128;
-    cb += c > 64 ? (c + 63) / 64 : 1;
+    cb += max((c + 63) / 64, kLeast);
   }
   c0 = block_sum(c0, sh);
   c16 = block_sum(c16, sh);
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) k_rows_place(
     blocks[a] = cb;
     if (a == k - 1) {
       offsets[k] = c0 + mine;
-      blocks[k] = cb + (n64 > 1 ? n64 : 1);
+      blocks[k] = cb + max(n64, kLeast);
       ntiles[0] = c16 + n16;
       ntiles[1] = c64 + n64;
       ntiles[2] = c128 + n128;

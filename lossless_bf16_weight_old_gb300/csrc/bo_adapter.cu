@@ -231,13 +231,16 @@ __device__ __forceinline__ uint4 load8w(const uint16_t* p, int32_t n, bool vec) 
 __device__ __forceinline__ void fill8(uint32_t dst, const uint16_t* p, int32_t n, bool vec) {
   if (vec) {
     cp16n(dst, p, n);
-  } else if (n >= 8 && !(reinterpret_cast<uintptr_t>(p) & 2)) {
-    // rows of even widths: not waited for either (8192 rows of 4094 and 4098, rank 16: forward 110
+  } else if (n > 0 && (n >= 8 || !(n & 1)) && !(reinterpret_cast<uintptr_t>(p) & 2)) {
+    // rows of even widths: not waited for either (8192 rows of 4094 and 4098, rank 16: forward 100
     // us, with loads and stores 128)
 #pragma unroll
-    for (int j = 0; j < 4; j++)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + 4 * j), "l"(p + 2 * j)
+    for (int j = 0; j < 4; j++) {
+      const bool there = 2 * j < n;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 4 * j),
+                   "l"(there ? p + 2 * j : p), "r"(there ? 4 : 0)
                    : "memory");
+    }
   } else {
     sts16(dst, gather8(p, n));
   }
@@ -665,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const Ap
       const bool there = o0 + r + urow < P.N;
       const uint32_t dst = at + swz_dealt<RP>(r + urow, uch);
       if (A.vec_up) cp16n(dst, there && un > 0 ? upp + (uint64_t)(o0 + r) * A.ld_up : A.up, there ? un : 0);
-      else sts16(dst, gather8(upp + (uint64_t)(o0 + r) * A.ld_up, there ? un : 0));
+      else fill8(dst, upp + (uint64_t)(o0 + r) * A.ld_up, there ? un : 0, false);
     }
   };
   // join the sums of the cluster's blocks: each joins some of the rows and hands them to all
@@ -817,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_expand(const App
       const int32_t n = n0 + row < P.N ? rank - (int32_t)ch * 8 : 0;
       const uint16_t* src = n > 0 ? A.up + (uint64_t)(n0 + row) * A.ld_up + ch * 8 : A.up;
       if (A.vec_up) cp16n(bs + L::at(row, ch * 16), src, n);
-      else sts16(bs + L::at(row, ch * 16), gather8(src, n));
+      else fill8(bs + L::at(row, ch * 16), src, n, false);
     }
     cp_commit();   // (waited for below, with the first pieces of y on their way too)
 
@@ -1015,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads) k_transpose(const DevAdapter* __rest
 // while another works; a piece that several blocks share is joined by the one that ends last, in
 // the order of the blocks, from their sums in the workspace.
 // This form, on mma.sync, takes what the other's 16-byte copies cannot: 8192 rows of 4095 and 4097
-// features, rank 64, take 157 us; of 4096, there, 38 us.
+// features, rank 64, take 142 us; of 4096, there, 38 us.
 constexpr uint32_t kWStages = 3;
 template <int RP>
 struct Wgrad {
@@ -1174,18 +1177,40 @@ __global__ void __launch_bounds__(kThreads, 2) k_wgrad(const WgradArgs P) {
       write = sh_last != 0;
       __threadfence();
     }
+    if (write && mine < Q.stages) {   // the blocks' sums, in their order, many at once
+      constexpr uint32_t U = RP >= 64 ? 8 : RP / 8;
+      for (uint32_t e = tid * 4; e < kFeat * RP; e += kThreads * 4 * U) {
+        float4 v[U];
+#pragma unroll
+        for (uint32_t u = 0; u < U; u++) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (uint32_t b = b0; b <= b1; b++) {   // a block's first piece, or its last
+          const float* const from =
+              P.sums + (2 * (uint64_t)b + (sh.begin(b) < Q.begin)) * (kFeat * RP) + e;
+#pragma unroll
+          for (uint32_t u = 0; u < U; u++) {
+            const float4 w = __ldcg(reinterpret_cast<const float4*>(from + u * kThreads * 4));
+            v[u].x += w.x;
+            v[u].y += w.y;
+            v[u].z += w.z;
+            v[u].w += w.w;
+          }
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < U; u++) {
+          const uint32_t at = e + u * kThreads * 4;
+          float2* const d = reinterpret_cast<float2*>(part + at / RP * L::kLd + at % RP);
+          d[0] = make_float2(v[u].x, v[u].y);
+          d[1] = make_float2(v[u].z, v[u].w);
+        }
+      }
+      __syncthreads();
+    }
     if (write) {
       for (uint32_t e = tid; e < kFeat * RP; e += kThreads) {
         // neighbours in memory to neighbouring threads: along the features for dA, the rank for dB
         const uint32_t fl = down ? e % kFeat : e / RP, r = down ? e / kFeat : e % RP;
         if (f0 + fl >= F || r >= A.rank) continue;
-        float v = 0.f;
-        if (mine == Q.stages) {
-          v = part[fl * L::kLd + r];
-        } else {
-          for (uint32_t b = b0; b <= b1; b++)   // a block's first piece, or its last
-            v += __ldcg(P.sums + (2 * (uint64_t)b + (sh.begin(b) < Q.begin)) * (kFeat * RP) + fl * RP + r);
-        }
+        const float v = part[fl * L::kLd + r];
         if (down)
           put_grad(A.gdown, (uint64_t)r * A.ld_gdown + f0 + fl, v, P.grad_f32, P.accumulate);
         else

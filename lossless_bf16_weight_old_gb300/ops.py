@@ -298,7 +298,8 @@ class AdapterSet:
         self.rank = int(self.handle.rank)
         self._ref = ctypes.byref(self.handle)
         self._low_rows = int(lib.bo_adapter_low_rows(self._ref))
-        self._forward = lib.bo_adapter_forward
+        self._forward, self._backward = lib.bo_adapter_forward, lib.bo_adapter_backward
+        self._need = (-1, 0)     # rows, and the bytes that a backward pass of as many needs
         self._keep = (list(downs), list(ups), d_downs, d_ups)
 
 
@@ -349,7 +350,7 @@ def _rows_of(t: torch.Tensor, name: str, shape: tuple, device) -> int:
 
 
 def _low(low: torch.Tensor, adapters: AdapterSet, rows: AdapterRows) -> int:
-    if low.shape != (rows.rows, adapters.rank) or low.dtype != torch.bfloat16 or \
+    if low.shape != (rows.rows, adapters.rank) or low.dtype is not torch.bfloat16 or \
             not low.is_contiguous() or low.device != adapters.device:
         raise ValueError(f"low must be a contiguous bfloat16 tensor of shape "
                          f"({rows.rows}, {adapters.rank}) on {adapters.device}")
@@ -389,16 +390,21 @@ def adapter_backward(x: torch.Tensor, dy: torch.Tensor, low: torch.Tensor,
     ldx = _rows_of(x, "x", (rows.rows, adapters.hidden), dev)
     lddy = _rows_of(dy, "dy", (rows.rows, adapters.out), dev)
     lddx = 0 if dx is None else _rows_of(dx, "dx", (rows.rows, adapters.hidden), dev)
-    lib = _ops_lib.load()
     ws = workspace
     if ws is None:
-        need = int(lib.bo_adapter_backward_workspace_size(adapters._ref, rows.rows))
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        n, need = adapters._need
+        if n != rows.rows:
+            need = max(256, int(_ops_lib.load().bo_adapter_backward_workspace_size(adapters._ref,
+                                                                                   rows.rows)))
+            adapters._need = rows.rows, need
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
         if stream is not None:
             ws.record_stream(stream)   # (the allocator may not hand it out while it is in use)
-    rc = lib.bo_adapter_backward(
+    else:
+        need = ws.numel() * ws.element_size()
+    rc = adapters._backward(
         adapters._ref, rows._ref, x.data_ptr(), ldx, dy.data_ptr(), lddy,
-        _low(low, adapters, rows), None if dx is None else dx.data_ptr(), lddx, int(accumulate),
-        ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream, dev))
+        _low(low, adapters, rows), None if dx is None else dx.data_ptr(), lddx, accumulate,
+        ws.data_ptr(), need, _stream(stream, dev))
     if rc != OK:
         raise OpsError(rc, "bo_adapter_backward")

@@ -198,24 +198,32 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
 }
 
 // Eight values from p, of which the first n exist (n <= 0: none); the others are 0.  Off the
-// 16-byte boundary they come as the 4-byte words that they fill, and the ends.
-__device__ __forceinline__ uint32_t ld4(const uint16_t* p) {
-  return *reinterpret_cast<const uint32_t*>(p);
-}
+// 16-byte boundary they come as the 4-byte words that they fill, and the ends, without a branch:
+// several of them wait for memory together (in branches each waits by itself: 8192 rows, x of 4095
+// columns, rank 16, take 109 us, not 92).
 __device__ __forceinline__ uint4 gather8(const uint16_t* p, int32_t n) {
-  uint32_t w[4] = {0, 0, 0, 0};
-  if (n >= 8) {   // (one way for both: neighbouring rows may differ)
-    const uint32_t odd = (uint32_t)reinterpret_cast<uintptr_t>(p) >> 1 & 1;
-    const uint32_t t[5] = {odd ? (uint32_t)p[0] << 16 : ld4(p), ld4(p + 2 - odd), ld4(p + 4 - odd),
-                           ld4(p + 6 - odd), odd ? p[7] : 0u};
+  const int32_t odd = (int32_t)(reinterpret_cast<uintptr_t>(p) >> 1 & 1);
+  n = min(n, 8);
+  uint32_t t[5];
 #pragma unroll
-    for (int j = 0; j < 4; j++) w[j] = __funnelshift_r(t[j], t[j + 1], 16 * odd);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-      if (j < n) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+  for (int32_t j = 0; j < 5; j++) {   // values 2 j - odd and the next
+    const int32_t e = 2 * j - odd;
+    const bool front = j == 0 && odd;
+    const uint32_t two = !front && e + 1 < n, one = front ? n > 0 : e + 1 == n;
+    asm volatile(
+        "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %2, 0;\n\tsetp.ne.u32 b, %3, 0;\n\t"
+        "mov.b32 %0, 0;\n\t@a ld.global.b32 %0, [%1];\n\t@b ld.global.u16 %0, [%1];\n\t}"
+        : "=&r"(t[j])
+        : "l"(p + (front ? 0 : e)), "r"(two), "r"(one));
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  t[0] <<= 16 * odd;
+  return make_uint4(__funnelshift_r(t[0], t[1], 16 * odd), __funnelshift_r(t[1], t[2], 16 * odd),
+                    __funnelshift_r(t[2], t[3], 16 * odd), __funnelshift_r(t[3], t[4], 16 * odd));
+}
+// How rows of a matrix may be read: 16 bytes at a time, 4 bytes, or 2.
+enum : uint32_t { kWide = 2, kEven = 1, kAny = 0 };
+__device__ __forceinline__ uint32_t row_access(const uint16_t* base, uint64_t ld, bool vec) {
+  return vec ? kWide : ((uint32_t)reinterpret_cast<uintptr_t>(base) | (uint32_t)ld * 2) & 3 ? kAny : kEven;
 }
 __device__ __forceinline__ uint4 load8(const uint16_t* p, int32_t n, bool vec) {
   if (vec) return n > 0 ? ld16(p) : make_uint4(0, 0, 0, 0);   // (n is a multiple of 8)
@@ -227,22 +235,30 @@ __device__ __forceinline__ uint4 load8w(const uint16_t* p, int32_t n, bool vec) 
     return n > 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
   return gather8(p, n);
 }
-// ... into shared memory
-__device__ __forceinline__ void fill8(uint32_t dst, const uint16_t* p, int32_t n, bool vec) {
-  if (vec) {
-    cp16n(dst, p, n);
-  } else if (n > 0 && (n >= 8 || !(n & 1)) && !(reinterpret_cast<uintptr_t>(p) & 2)) {
-    // rows of even widths: not waited for either (8192 rows of 4094 and 4098, rank 16: forward 100
-    // us, with loads and stores 128)
+// ... N of them into shared memory.  Rows of even widths are copied without waiting too (8192 rows
+// of 4094 and 4098, rank 16: forward 100 us, with loads and stores 128).
+template <int N>
+__device__ __forceinline__ void fill8(const uint32_t (&dst)[N], const uint16_t* const (&p)[N],
+                                      const int32_t (&n)[N], const uint16_t* base, uint32_t access) {
+  if (access == kWide) {
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const bool there = 2 * j < n;
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 4 * j),
-                   "l"(there ? p + 2 * j : p), "r"(there ? 4 : 0)
-                   : "memory");
-    }
+    for (int i = 0; i < N; i++) cp16n(dst[i], n[i] > 0 ? p[i] : base, n[i]);
+  } else if (access == kEven) {
+#pragma unroll
+    for (int i = 0; i < N; i++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int32_t bytes = max(0, min(2 * n[i] - 4 * j, 4));
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst[i] + 4 * j),
+                     "l"(bytes > 0 ? p[i] + 2 * j : base), "r"(bytes)
+                     : "memory");
+      }
   } else {
-    sts16(dst, gather8(p, n));
+    uint4 v[N];
+#pragma unroll
+    for (int i = 0; i < N; i++) v[i] = gather8(p[i], n[i]);
+#pragma unroll
+    for (int i = 0; i < N; i++) sts16(dst[i], v[i]);
   }
 }
 __device__ __forceinline__ void store8(uint16_t* p, uint4 v, int32_t n, bool vec) {
@@ -560,6 +576,8 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const Ap
     const uint16_t* const xp0 = P.x + (int64_t)(s0 >= 0 ? s0 : row_a) * P.ldx + xch * 8;
     const uint16_t* const xp1 = P.x + (int64_t)(s1 >= 0 ? s1 : row_a) * P.ldx + xch * 8;
     const uint16_t* const wp = A.down + xch * 8;
+    const uint32_t x_access = row_access(P.x, P.ldx, P.vec_x);
+    const uint32_t w_access = row_access(A.down, A.ld_down, A.vec_down);
     const uint32_t sx = swz(xrow * 128 + xch * 16);   // (32 rows on: the same slot, 4096 bytes on)
     auto load_stage = [&](uint32_t i) {
       const uint32_t k0 = (c + i * C) * kBK, at = ring + (i % kStages) * L::kStage + sx;
@@ -568,18 +586,33 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const Ap
       if (VEC) {
         cp16z(at, xp0 + k, s0 >= 0 && n > 0);
         cp16z(at + 4096, xp1 + k, s1 >= 0 && n > 0);
-      } else {
-        fill8(at, xp0 + k, s0 >= 0 ? n : 0, P.vec_x);
-        fill8(at + 4096, xp1 + k, s1 >= 0 ? n : 0, P.vec_x);
-      }
 #pragma unroll
-      for (uint32_t r = 0; r < RP; r += 32) {
-        const uint32_t row = r + xrow;
-        if (RP < 32 && row >= RP) break;
-        const bool there = (int32_t)row < rank;
-        const uint16_t* src = wp + (there ? (uint64_t)row * A.ld_down : 0) + k;
-        if (VEC) cp16z(at + L::kXBytes + r * 128, src, there && n > 0);
-        else fill8(at + L::kXBytes + r * 128, src, there ? n : 0, A.vec_down);
+        for (uint32_t r = 0; r < RP; r += 32) {
+          const uint32_t row = r + xrow;
+          if (RP < 32 && row >= RP) break;
+          const bool there = (int32_t)row < rank;
+          cp16z(at + L::kXBytes + r * 128, wp + (there ? (uint64_t)row * A.ld_down : 0) + k,
+                there && n > 0);
+        }
+      } else {
+        const uint32_t xd[2] = {at, at + 4096};
+        const uint16_t* const xs[2] = {xp0 + k, xp1 + k};
+        const int32_t xn[2] = {s0 >= 0 ? n : 0, s1 >= 0 ? n : 0};
+        fill8(xd, xs, xn, P.x, x_access);
+        constexpr uint32_t W = (RP + 31) / 32;
+        if (RP < 32 && xrow >= RP) return;
+        uint32_t wd[W];
+        const uint16_t* ws[W];
+        int32_t wn[W];
+#pragma unroll
+        for (uint32_t i = 0; i < W; i++) {
+          const uint32_t row = i * 32 + xrow;
+          const bool there = (int32_t)row < rank;
+          wd[i] = at + L::kXBytes + i * 4096;
+          ws[i] = wp + (there ? (uint64_t)row * A.ld_down : 0) + k;
+          wn[i] = there ? n : 0;
+        }
+        fill8(wd, ws, wn, A.down, w_access);
       }
     };
     constexpr int MR = L::kMR;
@@ -661,15 +694,21 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_apply64(const Ap
   const uint32_t up0 = ring + L::kPart;
   const uint16_t* const upp = A.up + (uint64_t)urow * A.ld_up + uch * 8;
   const int32_t un = rank - (int32_t)uch * 8;
+  const uint32_t up_access = row_access(A.up, A.ld_up, A.vec_up);
   auto load_up = [&](uint32_t i) {
     const uint32_t o0 = (c + i * C) * kBN, at = up0 + i % L::kUps * L::kUp;
+    constexpr uint32_t W = kBN / span;
+    uint32_t ud[W];
+    const uint16_t* us[W];
+    int32_t ns[W];
 #pragma unroll
-    for (uint32_t r = 0; r < kBN; r += span) {
-      const bool there = o0 + r + urow < P.N;
-      const uint32_t dst = at + swz_dealt<RP>(r + urow, uch);
-      if (A.vec_up) cp16n(dst, there && un > 0 ? upp + (uint64_t)(o0 + r) * A.ld_up : A.up, there ? un : 0);
-      else fill8(dst, upp + (uint64_t)(o0 + r) * A.ld_up, there ? un : 0, false);
+    for (uint32_t r = 0; r < W; r++) {
+      const uint32_t o = o0 + r * span;
+      ud[r] = at + swz_dealt<RP>(r * span + urow, uch);
+      us[r] = upp + (uint64_t)o * A.ld_up;
+      ns[r] = o + urow < P.N ? un : 0;
     }
+    fill8(ud, us, ns, A.up, up_access);
   };
   // join the sums of the cluster's blocks: each joins some of the rows and hands them to all
   cluster.sync();
@@ -815,12 +854,26 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) k_expand(const App
     const DevAdapter A = P.table[T.adapter];
     const int32_t rank = (int32_t)A.rank, r_end = Z.start + Z.count;
     __syncthreads();   // every warp is done with the B before
-    for (uint32_t s = tid; s < L::kN * (RP / 8); s += kThreads) {
-      const uint32_t row = s / (RP / 8), ch = s % (RP / 8);
-      const int32_t n = n0 + row < P.N ? rank - (int32_t)ch * 8 : 0;
-      const uint16_t* src = n > 0 ? A.up + (uint64_t)(n0 + row) * A.ld_up + ch * 8 : A.up;
-      if (A.vec_up) cp16n(bs + L::at(row, ch * 16), src, n);
-      else fill8(bs + L::at(row, ch * 16), src, n, false);
+    const uint32_t access = row_access(A.up, A.ld_up, A.vec_up);
+    constexpr uint32_t W = 4;
+    for (uint32_t s0 = tid; s0 < L::kN * (RP / 8); s0 += kThreads * W) {
+      uint32_t dst[W];
+      const uint16_t* src[W];
+      int32_t ns[W];
+#pragma unroll
+      for (uint32_t i = 0; i < W; i++) {
+        const uint32_t s = s0 + i * kThreads, row = s / (RP / 8), ch = s % (RP / 8);
+        if (L::kN * (RP / 8) % (kThreads * W) != 0 && s >= L::kN * (RP / 8)) {
+          dst[i] = dst[0];   // (once more the same)
+          src[i] = src[0];
+          ns[i] = ns[0];
+          continue;
+        }
+        dst[i] = bs + L::at(row, ch * 16);
+        src[i] = A.up + (uint64_t)(n0 + row) * A.ld_up + ch * 8;
+        ns[i] = n0 + row < P.N ? rank - (int32_t)ch * 8 : 0;
+      }
+      fill8(dst, src, ns, A.up, access);
     }
     cp_commit();   // (waited for below, with the first pieces of y on their way too)
 
@@ -1056,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_wgrad(const WgradArgs P) {
     const bool down = Q.slice < hs;
     const uint32_t f0 = (down ? Q.slice : Q.slice - hs) * kFeat, F = down ? P.hidden : P.out;
     const uint64_t lds = down ? P.ldx : P.lddy;
-    const bool vec = down ? P.vec_x : P.vec_dy;
+    const uint32_t access = down ? row_access(P.x, P.ldx, P.vec_x) : row_access(P.dy, P.lddy, P.vec_dy);
     const uint16_t* const pr = down ? P.dlow : P.low;
     const int32_t start = Q.row0 + (int32_t)Q.first * 64, end = Q.row1;
     const int32_t qn = (int32_t)F - (int32_t)(f0 + qch * 8);
@@ -1081,12 +1134,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_wgrad(const WgradArgs P) {
     };
     auto load_stage = [&](uint32_t i) {
       const uint32_t to = ring + (i % kWStages) * L::kStage;
+      uint32_t dst[4];
+      const uint16_t* src[4];
+      int32_t ns[4];
 #pragma unroll
       for (uint32_t j = 0; j < 4; j++) {
-        const uint32_t dst = to + (qch >> 3) * 8192 + swz((qrow + 16 * j) * 128 + (qch & 7) * 16);
-        const uint16_t* p = qsrc + (int64_t)(tq[j] >= 0 ? tq[j] : 0) * lds;
-        fill8(dst, p, tq[j] >= 0 ? qn : 0, vec);
+        dst[j] = to + (qch >> 3) * 8192 + swz((qrow + 16 * j) * 128 + (qch & 7) * 16);
+        src[j] = qsrc + (int64_t)(tq[j] >= 0 ? tq[j] : 0) * lds;
+        ns[j] = tq[j] >= 0 ? qn : 0;
       }
+      fill8(dst, src, ns, qsrc, access);
 #pragma unroll
       for (uint32_t j = 0; j < PN; j++) {
         const uint32_t r = prow + span * j;

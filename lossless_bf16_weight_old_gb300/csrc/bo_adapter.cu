@@ -230,8 +230,9 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p, int32_t n, bool vec) {
   return gather8(p, n);
 }
 // The same for the factors, which other blocks read too (n may be anything).
+template <bool VEC = false>   // (whole words only)
 __device__ __forceinline__ uint4 load8w(const uint16_t* p, int32_t n, bool vec) {
-  if (vec && (n >= 8 || n <= 0))
+  if (VEC || (vec && (n >= 8 || n <= 0)))
     return n > 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
   return gather8(p, n);
 }
@@ -315,15 +316,18 @@ __device__ __forceinline__ uint32_t swz_dealt(uint32_t row, uint32_t chunk) {
 // others.  low enters the second product as two BF16 numbers, its rounding and what that cut
 // off: with few rows the rounding errors of low would not average out in y, and the products
 // cost nothing beside the latency of the loads.  What bounds it is the chain from the row's number
-// to the stores, five trips to memory and one across the cluster: one row of rank 16 takes 4.8 us
-// (4096 x 4096), 64 rows of 48 adapters 8.6 us (4096 x 11008, whose bytes take 3.9 us).
+// to the stores, five trips to memory and one across the cluster: one row of rank 16 takes 4.6 us
+// (4096 x 4096), 64 rows of 48 adapters 7.2 us (4096 x 11008, whose bytes take 3.9 us).
 template <int RP>
 struct Apply16 {
   static constexpr uint32_t kULd = RP + 8;
   static constexpr uint32_t kSmem = 9 * 16 * RP * 4 + 2 * 16 * kULd * 2;
 };
 
-template <int RP>
+// VEC: all rows, of the factors too, are whole 16-byte words; the code for others would be in the
+// way of so short a kernel (one row of rank 16 5.3 us a call with it, 4.6 without; of rank 64 and
+// 4096 x 11008 15.6 and 10.7).
+template <int RP, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_apply16(const ApplyArgs P) {
   using L = Apply16<RP>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -352,12 +356,12 @@ __global__ void __launch_bounds__(kThreads) k_apply16(const ApplyArgs P) {
     const int32_t k = KS == 32 ? ks * 32 + 8 * (int32_t)q : 4 * (int32_t)q;
     const uint16_t* src = A.up + (uint64_t)o * A.ld_up + k;
     const int32_t n = o < P.N ? rank - k : 0;
-    if (KS == 32) return load8w(src, n, A.vec_up);
+    if (KS == 32) return load8w<VEC>(src, n, A.vec_up);
     uint2 t = make_uint2(0, 0);   // rank at most 16: four values a thread make one mma step
-    if (A.vec_up) {
-      if (n >= 4) t = __ldg(reinterpret_cast<const uint2*>(src));
+    if (VEC || A.vec_up) {
+      if (n >= (VEC ? 1 : 4)) t = __ldg(reinterpret_cast<const uint2*>(src));
     }
-    if (!A.vec_up || (n > 0 && n < 4)) {
+    if (!VEC && (!A.vec_up || (n > 0 && n < 4))) {
       const uint4 f = gather8(src, min(n, 4));
       t = make_uint2(f.x, f.y);
     }
@@ -366,8 +370,8 @@ __global__ void __launch_bounds__(kThreads) k_apply16(const ApplyArgs P) {
   auto load_group = [&](uint32_t gc) {
     const uint32_t col = gc * 32 + 8 * q;
     const int32_t n = (int32_t)P.N - (int32_t)col;
-    y0 = load8(P.y + (int64_t)r0 * P.ldy + col, r0 >= 0 ? n : 0, P.vec_y);
-    y1 = load8(P.y + (int64_t)r1 * P.ldy + col, r1 >= 0 ? n : 0, P.vec_y);
+    y0 = load8(P.y + (int64_t)r0 * P.ldy + col, r0 >= 0 ? n : 0, VEC || P.vec_y);
+    y1 = load8(P.y + (int64_t)r1 * P.ldy + col, r1 >= 0 ? n : 0, VEC || P.vec_y);
     if (kAhead) {
 #pragma unroll
       for (int j = 0; j < 4; j++) w[j] = load_w(gc, 0, j);
@@ -383,12 +387,12 @@ __global__ void __launch_bounds__(kThreads) k_apply16(const ApplyArgs P) {
   for (uint32_t kc = first; kc * 32 < P.K; kc += step) {
     const uint32_t k = kc * 32 + 8 * q;
     const int32_t n = (int32_t)P.K - (int32_t)k;
-    const uint4 xa = load8(P.x + (int64_t)r0 * P.ldx + k, r0 >= 0 ? n : 0, P.vec_x);
-    const uint4 xb = load8(P.x + (int64_t)r1 * P.ldx + k, r1 >= 0 ? n : 0, P.vec_x);
+    const uint4 xa = load8(P.x + (int64_t)r0 * P.ldx + k, r0 >= 0 ? n : 0, VEC || P.vec_x);
+    const uint4 xb = load8(P.x + (int64_t)r1 * P.ldx + k, r1 >= 0 ? n : 0, VEC || P.vec_x);
 #pragma unroll
     for (int j = 0; j < RP / 8; j++) {
       const int32_t row = j * 8 + g;
-      const uint4 b = load8w(A.down + (uint64_t)row * A.ld_down + k, row < rank ? n : 0, A.vec_down);
+      const uint4 b = load8w<VEC>(A.down + (uint64_t)row * A.ld_down + k, row < rank ? n : 0, A.vec_down);
       mma16816(acc[j], xa.x, xb.x, xa.y, xb.y, b.x, b.y);
       mma16816(acc[j], xa.z, xb.z, xa.w, xb.w, b.z, b.w);
     }
@@ -472,12 +476,12 @@ __global__ void __launch_bounds__(kThreads) k_apply16(const ApplyArgs P) {
         store8(P.y + (int64_t)r0 * P.ldy + col,
                make_uint4(pack_bf16(d[0][0], d[0][1]), pack_bf16(d[1][0], d[1][1]),
                           pack_bf16(d[2][0], d[2][1]), pack_bf16(d[3][0], d[3][1])),
-               n, P.vec_y);
+               n, VEC || P.vec_y);
       if (r1 >= 0)
         store8(P.y + (int64_t)r1 * P.ldy + col,
                make_uint4(pack_bf16(d[0][2], d[0][3]), pack_bf16(d[1][2], d[1][3]),
                           pack_bf16(d[2][2], d[2][3]), pack_bf16(d[3][2], d[3][3])),
-               n, P.vec_y);
+               n, VEC || P.vec_y);
     }
   }
   cluster.barrier_wait(std::move(token));   // the others may still read `part`
@@ -1282,7 +1286,9 @@ template <int RP>
 cudaError_t launch_apply(bool small, bool vec, uint32_t tiles, uint32_t C, const ApplyArgs& P,
                          cudaStream_t s) {
   if constexpr (RP <= 64) {
-    if (small) return launch(k_apply16<RP>, dim3(tiles * C), kThreads, Apply16<RP>::kSmem, C, s, P);
+    if (small)
+      return launch(vec && P.vec_ups ? k_apply16<RP, true> : k_apply16<RP, false>, dim3(tiles * C),
+                    kThreads, Apply16<RP>::kSmem, C, s, P);
   }
   return launch(vec ? k_apply64<RP, true> : k_apply64<RP, false>, dim3(tiles * C), kThreads,
                 Apply64<RP>::kSmem, C, s, P);
@@ -1446,7 +1452,7 @@ int bo_adapter_set_init(const bo_adapter* h_items, uint32_t k, uint32_t hidden, 
   if (!dev) return BD_ERR_INVALID_ARG;
   const uintptr_t gsize = grad_dtype == BO_FP32 ? 4 : 2;
   uint32_t most = 1;
-  bool grads = true, all_wide = true;
+  bool grads = true, all_wide = true, ups_whole = true;
   for (uint32_t i = 0; i < k; i++) {
     const bo_adapter& a = h_items[i];
     if (!a.d_down || !a.d_up || !aligned(a.d_down, 2) || !aligned(a.d_up, 2) || a.rank < 1 ||
@@ -1475,6 +1481,7 @@ int bo_adapter_set_init(const bo_adapter* h_items, uint32_t k, uint32_t hidden, 
     d.vec_gup = a.d_grad_up && wide(a.d_grad_up, a.ld_grad_up, a.rank);
     d.pad[0] = d.pad[1] = d.pad[2] = 0;
     if (!d.vec_down) all_wide = false;
+    if (!d.vec_up || a.rank % 8 != 0) ups_whole = false;
     if (a.rank > most) most = a.rank;
   }
   const int rc = check(upload(dev.get(), (uint64_t)k * sizeof(DevAdapter), d_set,
@@ -1487,7 +1494,7 @@ int bo_adapter_set_init(const bo_adapter* h_items, uint32_t k, uint32_t hidden, 
   h_out->out = out;
   h_out->grad_dtype = grad_dtype;
   h_out->has_grads = grads;
-  h_out->wide = all_wide;
+  h_out->wide = (all_wide ? 1u : 0u) | (ups_whole ? 2u : 0u);
   return BD_OK;
 }
 
@@ -1558,7 +1565,8 @@ int bo_adapter_forward(const bo_adapter_set* set, const bo_adapter_rows* rows, c
   P.N = set->out;
   P.vec_x = wide(d_x, ldx, set->hidden);
   P.vec_y = wide(d_y, ldy, set->out);
-  P.vec_factors = set->wide;
+  P.vec_factors = set->wide & 1;
+  P.vec_ups = set->wide >> 1;
   return apply(set->rank, rows, P, sms, static_cast<cudaStream_t>(stream));
 }
 
@@ -1614,7 +1622,7 @@ int bo_adapter_backward(const bo_adapter_set* set, const bo_adapter_rows* rows,
     P.N = set->hidden;
     P.vec_x = wide(d_dy, lddy, set->out);
     P.vec_y = d_dx && wide(d_dx, lddx, set->hidden);
-    P.vec_factors = 1;
+    P.vec_factors = P.vec_ups = 1;
     if ((rc = apply(set->rank, rows, P, sms, s))) return rc;
   }
   if (!set->has_grads) return BD_OK;

@@ -63,6 +63,7 @@ struct ApplyArgs {
   uint32_t K, N;
   uint32_t vec_x, vec_y;  // rows may be read 16 bytes at a time
   uint32_t vec_factors;   // ... of every adapter's first factor
+  uint32_t vec_ups;       // ... of every second one, whose rows end with (or are 0 up to) whole words
   int32_t* status;        // BD_ERR_CUDA when a wait inside a kernel ran out; may be NULL
 };
 

@@ -1322,7 +1322,9 @@ uint32_t tile_bound(uint32_t rows, uint32_t k, uint32_t high) {
   return (uint32_t)(b < rows ? b : rows);
 }
 // ... as many as to expect: an adapter's last tile is there in two cases of three.
-uint32_t tile_guess(uint32_t rows, uint32_t k, uint32_t high) { return tile_bound(rows, 2 * k / 3 + 1, high); }
+uint32_t tile_guess(uint32_t rows, uint32_t k, uint32_t high) {
+  return tile_bound(rows, 2 * k / 3 + 1, high);
+}
 
 int apply(uint32_t RP, const bo_adapter_rows* R, ApplyArgs& P, int sms, cudaStream_t s) {
   const uint32_t rows = R->rows, k = R->k;
@@ -1347,14 +1349,19 @@ int apply(uint32_t RP, const bo_adapter_rows* R, ApplyArgs& P, int sms, cudaStre
   }
   // Tiles of 16 rows have the shorter way to a result, tiles of 64 read the factors less often and
   // carry less in registers (us, tiles of 16 / of 64):
-  //   rank 16, 4096 x 4096:   1 row 5.2 / 6.6, 512 rows of 8 adapters 6.6 / 7.6, 1024 of 32 10.5 / 9.8,
-  //                           1024 of 64 11.1 / 17.1, 2048 of 64 25 / 20
-  //   rank 64, 4096 x 11008:  1 row 15.7 / 16.8, 128 of 1 16.0 / 19.1, 64 of 64 47 / 41, 256 of 8 20 / 18
+  //   rank 16, 4096 x 4096:   16 rows of 16 adapters 5.1 / 8.8, 512 of 8 6.1 / 8.0, 1024 of 8 9.3 / 10.6,
+  //                           1024 of 64 9.7 / 15.0, 2048 of 64 19.9 / 18.6
+  //   rank 64, 4096 x 11008:  64 of 1 11.7 / 17.8, 64 of 64 31.6 / 41.4, 256 of 32 22.6 / 26.3,
+  //                           512 of 8 20.5 / 19.3, 1024 of 32 34 / 29
   //   rank 128, 4096 x 4096:  1 row 18.6 / 16.0, 64 of 64 114 / 48
-  const bool small = RP <= 32   ? rows <= 512 || rows / k < 24
-                     : RP == 64 ? tile_guess(rows, k, 16) <= 16
-                                : false;
-  const uint32_t tiles = tile_bound(rows, k, small ? 16 : 64), guess = tile_guess(rows, k, small ? 16 : 64);
+  // and, where rows do not end with whole words, of rank 16 as above up to 512 rows, of rank 64
+  //                           128 of 1 16.0 / 19.1, 64 of 64 47 / 41, 256 of 8 20 / 18.
+  const uint32_t few = RP <= 32 && vec && P.vec_ups ? 1024 : 512;
+  const bool small = RP == 128                        ? false
+                     : RP <= 32 || (vec && P.vec_ups) ? rows <= few || rows / k < 24
+                                                      : tile_guess(rows, k, 16) <= 16;
+  const uint32_t high = small ? 16 : 64;
+  const uint32_t tiles = tile_bound(rows, k, high), guess = tile_guess(rows, k, high);
   P.tiles = static_cast<const Tile*>(R->d_tiles[small ? 0 : 1]);
   P.ntiles = R->d_ntiles + (small ? 0 : 1);
   // Blocks of 64 rows fit twice on an SM (of rank 128 once), of 16 rows three times.  Past that a
@@ -1400,7 +1407,8 @@ bool valid(const bo_adapter_set* s) {
          (s->rank == 16 || s->rank == 32 || s->rank == 64 || s->rank == 128);
 }
 bool valid(const bo_adapter_rows* r) {
-  return r && r->d_perm && r->d_offsets && r->d_blocks && r->d_tiles[0] && r->d_tiles[1] && r->d_tiles[2] && r->d_ntiles;
+  return r && r->d_perm && r->d_offsets && r->d_blocks && r->d_tiles[0] && r->d_tiles[1] &&
+         r->d_tiles[2] && r->d_ntiles;
 }
 bool wide(const void* p, uint64_t ld, uint64_t width) {
   return aligned(p, 16) && ld % 8 == 0 && width % 8 == 0;

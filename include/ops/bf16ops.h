@@ -40,8 +40,9 @@ extern "C" {
  *   c = min(1, max_norm / (norm + 1e-6)) when clipping, else 1;   g' = c g
  *   m = beta1 m + (1 - beta1) g'          v = beta2 v + (1 - beta2) g'^2
  *   p = p (1 - lr wd) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
- * computed in FP32 (the quotient is 0 where m is 0, whatever eps).  norm = sqrt(sum of g^2 over all
- * tensors), summed in a fixed order.
+ * computed in FP32, where v may underflow to 0 under an m that did not: with eps = 0 the quotient is
+ * 0 wherever its denominator is.  norm = sqrt(sum of g^2 over all tensors), summed in a fixed order
+ * (in FP32 too: a gradient above 1.8e19 has an infinite square, and the norm is not finite then).
  *
  * State arenas.  The elements of item i take the blocks of 256 from first_block on (the last
  * one padded); m, v and master of all items lie in one arena each, indexed by

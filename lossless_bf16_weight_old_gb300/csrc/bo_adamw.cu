@@ -151,6 +151,8 @@ __device__ __forceinline__ float nan_of(const float (&p)[N]) {
 }
 
 // ----------------------------------------------------------------------------- the formula
+constexpr float kTinyEps = 0x1p-39f;   // below it the root is taken of denormal numbers too
+
 struct Rates {      // per launch
   float b1, c1, b2, c2;      // beta and 1 - beta
   float inv_bc1, inv_bc2;    // 1 / (1 - beta^t)
@@ -211,11 +213,15 @@ __device__ __forceinline__ void finish_step(const StepParams& P, bool taken) {
   }
 }
 
-// Within 2^-22 or so of the root and the reciprocal; denormal numbers count as 0, which a root
-// beside eps and a ratio of two moments do not notice.
+// Within 2^-22 or so of the root and the reciprocal; denormal numbers count as 0.
 __device__ __forceinline__ float sqrt_fast(float x) {
   float r;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float sqrt_full(float x) {   // ... and the root of denormal numbers
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ float rsqrt_fast(float x) {
@@ -229,16 +235,29 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return r;
 }
 
-// One element: updates m, v and p.  The root and the quotient are the hardware's approximations,
-// a few units in the last place of a term that lr scales down before it meets p.
+// m / (sqrt(v) + eps), v with its bias correction.  The root and the quotient are the hardware's
+// approximations, a few units in the last place of a term that lr scales down before it meets p.
+// TINY: eps is so small that a v below 2^-126 counts (its root is below 2^-63, and beside a larger
+// eps nothing).  The ratio of two small moments is the step then: an element with a gradient of
+// 1e-20 moves as far as one with 1.  Where the denominator is 0, v having underflowed, nothing is
+// known of the ratio, and it counts as 0.  (A denormal denominator, of a denormal eps, counts as
+// 2^-126.)
+template <bool TINY>
+__device__ __forceinline__ float quotient(float m, float v, float eps) {
+  if (!TINY) return m * rcp_fast(sqrt_fast(v) + eps);
+  const float den = sqrt_full(v) + eps, q = m * rcp_fast(fmaxf(den, 0x1p-126f));
+  return den == 0.f ? 0.f : q;
+}
+
+// One element: updates m, v and p.
+template <bool TINY>
 __device__ __forceinline__ void update(const Rates& R, float keep, float g, float& m, float& v,
                                        float& p) {
   g *= R.coef;
   m = fmaf(R.b1, m, R.c1 * g);
   v = fmaf(R.b2, v, R.c2 * g * g);
-  // (a denominator of 0, with eps = 0, counts as the least normal number: 0 / 0 is 0)
-  const float den = fmaxf(sqrt_fast(v * R.inv_bc2) + R.eps, 0x1p-126f);
-  p = fmaf(p, keep, R.rate * (m * rcp_fast(den)));
+  const float vt = v * R.inv_bc2;
+  p = fmaf(p, keep, R.rate * quotient<TINY>(m, vt, R.eps));
 }
 
 // BF16 words of weights p, rounded to nearest or by the random bits
@@ -341,8 +360,13 @@ __global__ void __launch_bounds__(kThreads, 4) k_step32(const StepParams P) {
       if (i + 8 <= c.count) {
         if (!loaded) x.load(P, c, i);
         loaded = false;
+        if (P.eps < kTinyEps) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) update(R, keep, x.g[j], x.m.v[j], x.v.v[j], x.p[j]);
+          for (int j = 0; j < 8; j++) update<true>(R, keep, x.g[j], x.m.v[j], x.v.v[j], x.p[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; j++) update<false>(R, keep, x.g[j], x.m.v[j], x.v.v[j], x.p[j]);
+        }
         st8(am + e, x.m);
         st8(av + e, x.v);
         uint32_t r[8] = {}, w[4] = {};
@@ -359,7 +383,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_step32(const StepParams P) {
           const float g = load1<GF32>(c.g, i + j);
           float m = am[e + j], v = av[e + j];
           float p = WK == BO_WEIGHT_MASTER ? pm[j] : load1<WK == BO_WEIGHT_FP32>(c.w, i + j);
-          update(R, keep, g, m, v, p);
+          if (P.eps < kTinyEps) update<true>(R, keep, g, m, v, p);
+          else update<false>(R, keep, g, m, v, p);
           am[e + j] = m;
           av[e + j] = v;
           store_weight1<WK>(c, i + j, pm + (WK == BO_WEIGHT_MASTER ? j : 0), p, P.stochastic, r[j]);
@@ -433,15 +458,20 @@ __device__ __forceinline__ float2 sum2(float2 a, float2 b) {
   return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
 }
 // Two elements' update (the formula of `update`; the moments as said above).
+template <bool TINY>
 __device__ __forceinline__ void update2(const Rates& R, float keep, float2 g, float2& m, float2& v,
                                         float2& p) {
   g = mul2(g, both(R.coef));
   m = sum2(mul2(m, both(R.b1)), mul2(g, both(R.c1)));
   v = sum2(mul2(v, both(R.b2)), mul2(mul2(g, g), both(R.c2)));
   const float2 t = mul2(v, both(R.inv_bc2));
-  const float2 den = add2(make_float2(sqrt_fast(t.x), sqrt_fast(t.y)), both(R.eps));
-  const float2 q = mul2(m, make_float2(rcp_fast(fmaxf(den.x, 0x1p-126f)),
-                                       rcp_fast(fmaxf(den.y, 0x1p-126f))));
+  float2 q;
+  if (TINY) {
+    q = make_float2(quotient<true>(m.x, t.x, R.eps), quotient<true>(m.y, t.y, R.eps));
+  } else {
+    const float2 den = add2(make_float2(sqrt_fast(t.x), sqrt_fast(t.y)), both(R.eps));
+    q = mul2(m, make_float2(rcp_fast(den.x), rcp_fast(den.y)));
+  }
   p = fma2(p, both(keep), mul2(both(R.rate), q));
 }
 // x / scale, rounded once: the product with the reciprocal, put right by its remainder
@@ -460,8 +490,8 @@ __device__ __forceinline__ float2 m_codes(float2 m, float scale, float inv) {
   return add2(make_float2(copysignf(r.x, m.x), copysignf(r.y, m.y)), both(12582912.f));
 }
 // Of the two codes whose values enclose v / scale, the upper one with the chance that makes the
-// expected value v / scale; never 0 for v > 0 (a root of 0 under a moment that is not 0 would
-// make a step without bound).
+// expected value v / scale; never 0 for v > 0 (a root of 0 under a moment that is not 0 is a
+// step of m / eps).
 __device__ __forceinline__ float2 v_codes(float2 v, float scale, float inv, uint32_t r0, uint32_t r1) {
   const float2 x = ratio2(v, scale, inv);
   // floor of 255 times x's fourth root, by rounding down at 2^23, where the code stays in the low
@@ -542,7 +572,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_step8(const StepParams P) {
         m[j] = mul2(m_values(bytes_s(j < 2 ? cm.x : cm.y, 2 * j & 3)), both(sm));
         v[j] = mul2(v_values(bytes_u(j < 2 ? cv.x : cv.y, 2 * j & 3)), both(sv));
         float2 q = make_float2(p[2 * j], p[2 * j + 1]);
-        update2(R, keep, make_float2(g[2 * j], g[2 * j + 1]), m[j], v[j], q);
+        const float2 gj = make_float2(g[2 * j], g[2 * j + 1]);
+        if (P.eps < kTinyEps) update2<true>(R, keep, gj, m[j], v[j], q);
+        else update2<false>(R, keep, gj, m[j], v[j], q);
         p[2 * j] = q.x;
         p[2 * j + 1] = q.y;
       }

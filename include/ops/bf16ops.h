@@ -159,8 +159,12 @@ BD_API int bo_adamw_moments(const bo_adamw* h, uint32_t dtype, void* d_m, void* 
  * Rows without an adapter are neither read nor written.  Sums are held in FP32; low and dlow
  * are rounded to BF16, the type of the tensor cores' operands, once per row and rank (an error
  * of at most 2^-8 of each term, that of a model that stores its low-rank activations); every output is
- * rounded once.  Results do not depend on which other rows are in the batch's tiles, and the
- * order of every sum is fixed for given sizes.
+ * rounded once.  With few rows the product with low takes it as two BF16 numbers, its rounding and
+ * what that cut off.  An infinity in x, dy, y or dx gives what the formula gives for its row, and a
+ * low beyond BF16's largest number counts as infinity; an infinity in a factor gives infinity or NaN
+ * where it enters.
+ * Results do not depend on which other rows are in the batch's tiles, and the order of every sum
+ * is fixed for given sizes.
  *
  * x, y, dy, dx: rows of BF16 with a row stride in elements; any sizes and strides (16-byte
  * aligned rows, with hidden and out multiples of 8, take wide accesses). */

@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads) k_apply16(const ApplyArgs P) {
     // columns past the rank are 0 whatever x holds (an infinity times a padded 0 is not)
     s = col < rank ? s * A.scale : 0.f;
     const uint32_t hi = pack_bf16(s, 0.f);
-    const float rest = isfinite(s) ? s - bf16_lo(hi) : 0.f;
+    const float rest = isfinite(bf16_lo(hi)) ? s - bf16_lo(hi) : 0.f;   // (s may round to infinity)
     us[row * L::kULd + col] = (uint16_t)hi;
     us[(16 + row) * L::kULd + col] = (uint16_t)pack_bf16(rest, 0.f);
     if (P.low && c == 0 && row < T.count)

@@ -7,6 +7,10 @@
 
 Every computation runs in libbf16ops' CUDA kernels; this module checks and marshals arguments
 and allocates device buffers with PyTorch.  The names are re-exported by the package.
+
+Every call works in the order of the stream that it is given (the current one by default), and so
+do the buffers that it makes for itself.  Tensors of the caller's must be ready in that order, and
+stay allocated until the work is done.
 """
 from __future__ import annotations
 
@@ -49,6 +53,38 @@ def _stream(stream, device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+class _Owner:
+    """An object with device buffers of its own, which are made and filled in the order of the
+    stream that its constructor was given (or the current one).  Its first use on another stream
+    waits until they are filled, and the allocator learns of that stream."""
+
+    def _made(self, buffers: list, device: torch.device) -> None:   # (on the constructor's stream)
+        self._buffers, self.device = buffers, device
+        self._home, self._others = _stream(None, device), set()
+        self._filled = None
+        if not torch.cuda.is_current_stream_capturing():
+            self._filled = torch.cuda.Event()
+            self._filled.record()
+
+    def _on(self, stream) -> int:
+        """The handle of the stream of a call."""
+        raw = _stream(stream, self.device)
+        if raw != self._home and raw not in self._others:
+            self._join(raw, stream)
+        return raw
+
+    def _join(self, raw: int, stream) -> None:
+        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        for t in self._buffers:
+            t.record_stream(s)
+        with torch.cuda.stream(s):
+            # (a capture may not wait for what lies before it, and whoever began it has)
+            if self._filled is None or torch.cuda.is_current_stream_capturing():
+                return
+            s.wait_event(self._filled)
+        self._others.add(raw)
+
+
 def _arena(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int, device) -> torch.Tensor:
     if t.dtype != dtype or t.numel() != numel or not t.is_contiguous() or t.device != device:
         raise ValueError(f"state[{name!r}] must be a contiguous {dtype} tensor of {numel} "
@@ -56,7 +92,7 @@ def _arena(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int, device) -
     return t
 
 
-class AdamWBatch:
+class AdamWBatch(_Owner):
     """One AdamW step over fixed tensors: the tensor table, the state and the step count.
 
     weights       tensors to update: bfloat16, or float32 for 32-bit weights
@@ -139,13 +175,14 @@ class AdamWBatch:
         if set(given) - set(want):
             raise ValueError(f"state has no place for {sorted(set(given) - set(want))}")
         self.state: dict[str, torch.Tensor] = {}
-        for name, dt in want.items():
-            numel = blocks if name.endswith("_scale") else elems
-            self.state[name] = _arena(given[name], name, dt, numel, dev) if name in given else \
-                torch.zeros(numel, dtype=dt, device=dev)
-        if master and "master" not in given:
-            for i, w in enumerate(weights):
-                self.view("master", i).copy_(w)
+        with torch.cuda.stream(stream):
+            for name, dt in want.items():
+                numel = blocks if name.endswith("_scale") else elems
+                self.state[name] = _arena(given[name], name, dt, numel, dev) if name in given else \
+                    torch.zeros(numel, dtype=dt, device=dev)
+            if master and "master" not in given:
+                for i, w in enumerate(weights):
+                    self.view("master", i).copy_(w)
 
         items = (_ops_lib.AdamWItem * k)()
         for i in range(k):
@@ -159,13 +196,15 @@ class AdamWBatch:
         st = _ops_lib.AdamWState(ptr["m"], ptr["v"], ptr.get("m_scale"), ptr.get("v_scale"),
                                  ptr.get("master"), blocks)
         lib = _ops_lib.load()
-        self.plan = torch.empty(int(lib.bo_adamw_plan_size(items, k)), dtype=torch.uint8, device=dev)
         self.handle = _ops_lib.AdamW()
         kind = 2 if wtype == torch.float32 else 0 if master else 1
-        _check(lib.bo_adamw_plan(items, k, ctypes.byref(st), kind, _DTYPES[gtype], state_bits,
-                                 int(bool(stochastic)), int(step), self.plan.data_ptr(),
-                                 self.plan.numel(), ctypes.byref(self.handle), _stream(stream, dev)),
-               "bo_adamw_plan")
+        with torch.cuda.stream(stream):
+            self.plan = torch.empty(int(lib.bo_adamw_plan_size(items, k)), dtype=torch.uint8, device=dev)
+            _check(lib.bo_adamw_plan(items, k, ctypes.byref(st), kind, _DTYPES[gtype], state_bits,
+                                     int(bool(stochastic)), int(step), self.plan.data_ptr(),
+                                     self.plan.numel(), ctypes.byref(self.handle), _stream(None, dev)),
+                   "bo_adamw_plan")
+            self._made([self.plan] + [t for n, t in self.state.items() if n not in given], dev)
         self.steps = self.plan[:8].view(torch.int64)
         self.norm = self.plan[8:12].view(torch.float32)
         self.status = self.plan[16:20].view(torch.int32)
@@ -174,7 +213,6 @@ class AdamWBatch:
                                             int(seed) & _U64)
         self._refs = ctypes.byref(self.handle), ctypes.byref(self._args)
         self._step = lib.bo_adamw_step
-        self._device = dev
         self._keep = (list(weights), list(grads), outs)
 
     def run(self, lr: float | torch.Tensor | None = None, stream=None) -> None:
@@ -189,14 +227,13 @@ class AdamWBatch:
             else:
                 self.lr = float(lr)
                 self._args.lr, self._args.d_lr = self.lr, None
-        rc = self._step(*self._refs, _stream(stream, self._device))
+        rc = self._step(*self._refs, self._on(stream))
         if rc != OK:
             raise OpsError(rc, "bo_adamw_step")
 
     def grad_norm(self, stream=None) -> torch.Tensor:
         """The global norm of the gradients as they are now (`norm`), without a step."""
-        _check(_ops_lib.load().bo_adamw_norm(self._refs[0], self._args.max_norm,
-                                               _stream(stream, self._device)),
+        _check(_ops_lib.load().bo_adamw_norm(self._refs[0], self._args.max_norm, self._on(stream)),
                "bo_adamw_norm")
         return self.norm
 
@@ -212,13 +249,18 @@ class AdamWBatch:
         are the arenas themselves (dtype float32) or copies."""
         if dtype not in _DTYPES:
             raise TypeError("dtype must be bfloat16 or float32")
-        if self.state_bits == 32:
-            return self.state["m"].to(dtype), self.state["v"].to(dtype)
-        m = torch.empty(self.state["m"].numel(), dtype=dtype, device=self.plan.device)
-        v = torch.empty_like(m)
-        _check(_ops_lib.load().bo_adamw_moments(self._refs[0], _DTYPES[dtype], m.data_ptr(),
-                                                v.data_ptr(), _stream(stream, self._device)),
-               "bo_adamw_moments")
+        raw = self._on(stream)
+        with torch.cuda.stream(stream):
+            if self.state_bits == 32:
+                m, v = self.state["m"].to(dtype), self.state["v"].to(dtype)
+            else:
+                m = torch.empty(self.state["m"].numel(), dtype=dtype, device=self.device)
+                v = torch.empty_like(m)
+                _check(_ops_lib.load().bo_adamw_moments(self._refs[0], _DTYPES[dtype], m.data_ptr(),
+                                                        v.data_ptr(), raw), "bo_adamw_moments")
+        if stream is not None:   # (the caller may go on with them on the current one)
+            m.record_stream(torch.cuda.current_stream(self.device))
+            v.record_stream(torch.cuda.current_stream(self.device))
         return m, v
 
 
@@ -240,7 +282,7 @@ def _ld(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-class AdapterSet:
+class AdapterSet(_Owner):
     """The adapters of one projection, read where they lie.
 
     downs, ups   factors: downs[i] is [rank_i, hidden], ups[i] is [out, rank_i], bfloat16, rows
@@ -288,12 +330,14 @@ class AdapterSet:
                 it.d_grad_down, it.ld_grad_down = d_downs[i].data_ptr(), _ld(d_downs[i])
                 it.d_grad_up, it.ld_grad_up = d_ups[i].data_ptr(), _ld(d_ups[i])
         lib = _ops_lib.load()
-        self.table = torch.empty(max(256, int(lib.bo_adapter_set_size(k))), dtype=torch.uint8, device=dev)
         self.handle = _ops_lib.AdapterSet()
-        _check(lib.bo_adapter_set_init(items, k, hidden, out, _DTYPES[gtype], self.table.data_ptr(),
-                                       self.table.numel(), ctypes.byref(self.handle), _stream(stream, dev)),
-               "bo_adapter_set_init")
-        self.k, self.hidden, self.out, self.device = k, hidden, out, dev
+        with torch.cuda.stream(stream):
+            self.table = torch.empty(max(256, int(lib.bo_adapter_set_size(k))), dtype=torch.uint8, device=dev)
+            _check(lib.bo_adapter_set_init(items, k, hidden, out, _DTYPES[gtype], self.table.data_ptr(),
+                                           self.table.numel(), ctypes.byref(self.handle), _stream(None, dev)),
+                   "bo_adapter_set_init")
+            self._made([self.table], dev)
+        self.k, self.hidden, self.out = k, hidden, out
         #: columns of `low`, the activations that the forward pass keeps for the backward
         self.rank = int(self.handle.rank)
         self._ref = ctypes.byref(self.handle)
@@ -303,7 +347,7 @@ class AdapterSet:
         self._keep = (list(downs), list(ups), d_downs, d_ups)
 
 
-class AdapterRows:
+class AdapterRows(_Owner):
     """The rows of a batch grouped by adapter, on the device: index[t] (int32) is the adapter of
     row t, -1 for none.  One grouping serves every projection of a model step; `update` regroups
     for new values of as many rows.  `status` (int32[1]) is ERR_INVALID_ARG when an index lies
@@ -313,30 +357,52 @@ class AdapterRows:
         if index.dtype != torch.int32 or index.dim() != 1 or not index.is_cuda:
             raise ValueError("index must be a 1-dimensional int32 CUDA tensor")
         lib = _ops_lib.load()
-        self.rows, self.k, self.device = index.numel(), int(k), index.device
+        self.rows, self.k = index.numel(), int(k)
         need = int(lib.bo_adapter_rows_size(self.rows, self.k)) if self.k > 0 else 0
         if need == 0:
             raise ValueError("k must lie in 1 .. 65535 and the rows be fewer than 2**30")
-        self.memory = torch.empty(need, dtype=torch.uint8, device=index.device)
-        self.status = torch.zeros(1, dtype=torch.int32, device=index.device)
         self.handle = _ops_lib.AdapterRows()
         self._ref = ctypes.byref(self.handle)
-        self.update(index, stream)
+        with torch.cuda.stream(stream):
+            self.memory = torch.empty(need, dtype=torch.uint8, device=index.device)
+            self.status = torch.zeros(1, dtype=torch.int32, device=index.device)
+            self.device = index.device
+            self._group(index, stream, _stream(None, index.device))
+            self._made([self.memory, self.status], index.device)
 
     def update(self, index: torch.Tensor, stream=None) -> None:
+        self._group(index, stream, self._on(stream))
+
+    def _group(self, index: torch.Tensor, stream, raw: int) -> None:
         if index.dtype != torch.int32 or index.numel() != self.rows or index.device != self.device \
                 or not index.is_contiguous():
             raise ValueError(f"index must be a contiguous int32 tensor of {self.rows} elements on "
                              f"{self.device}")
+        if stream is not None:
+            index.record_stream(stream)   # (it may go before the grouping has read it)
         self.index = index
         _check(_ops_lib.load().bo_adapter_rows_init(
             index.data_ptr(), self.rows, self.k, self.memory.data_ptr(), self.memory.numel(),
-            self._ref, self.status.data_ptr(), _stream(stream, self.device)), "bo_adapter_rows_init")
+            self._ref, self.status.data_ptr(), raw), "bo_adapter_rows_init")
 
 
-def _pair(adapters: AdapterSet, rows: AdapterRows) -> None:
+def _pair(adapters: AdapterSet, rows: AdapterRows, stream) -> int:
+    """Checks that the two go together; returns the handle of the call's stream."""
     if rows.k != adapters.k:
         raise ValueError(f"rows are grouped over {rows.k} adapters, the set has {adapters.k}")
+    raw = adapters._on(stream)
+    if raw != rows._home:
+        rows._on(stream)
+    return raw
+
+
+def _scratch(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """Memory for one call, from the pool of the stream that the call runs on: what used it
+    before, and what will after, is in that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _rows_of(t: torch.Tensor, name: str, shape: tuple, device) -> int:
@@ -363,16 +429,14 @@ def adapter_forward(x: torch.Tensor, y: torch.Tensor, adapters: AdapterSet, rows
     projection's output.  x [rows, hidden] and y [rows, out] are bfloat16 with contiguous rows.
     low (optional, bfloat16 [rows, adapters.rank]) receives what adapter_backward needs.  Rows
     without an adapter are left alone.  Returns y."""
-    _pair(adapters, rows)
+    raw = _pair(adapters, rows, stream)
     dev = adapters.device
     ldx = _rows_of(x, "x", (rows.rows, adapters.hidden), dev)
     ldy = _rows_of(y, "y", (rows.rows, adapters.out), dev)
     if low is None and rows.rows >= adapters._low_rows:   # (workspace, for many rows)
-        low = torch.empty(rows.rows, adapters.rank, dtype=torch.bfloat16, device=dev)
-        if stream is not None:
-            low.record_stream(stream)
+        low = _scratch((rows.rows, adapters.rank), torch.bfloat16, dev, stream)
     rc = adapters._forward(adapters._ref, rows._ref, x.data_ptr(), ldx, y.data_ptr(), ldy,
-                           None if low is None else _low(low, adapters, rows), _stream(stream, dev))
+                           None if low is None else _low(low, adapters, rows), raw)
     if rc != OK:
         raise OpsError(rc, "bo_adapter_forward")
     return y
@@ -385,7 +449,7 @@ def adapter_backward(x: torch.Tensor, dy: torch.Tensor, low: torch.Tensor,
     """The backward pass of adapter_forward: dx[t] += the adapter's part (dx holds the shared
     projection's part; None: not wanted), in place, and the gradients given to the set are
     written, or with accumulate=True added to.  low is the forward pass's."""
-    _pair(adapters, rows)
+    raw = _pair(adapters, rows, stream)
     dev = adapters.device
     ldx = _rows_of(x, "x", (rows.rows, adapters.hidden), dev)
     lddy = _rows_of(dy, "dy", (rows.rows, adapters.out), dev)
@@ -397,14 +461,12 @@ def adapter_backward(x: torch.Tensor, dy: torch.Tensor, low: torch.Tensor,
             need = max(256, int(_ops_lib.load().bo_adapter_backward_workspace_size(adapters._ref,
                                                                                    rows.rows)))
             adapters._need = rows.rows, need
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            ws.record_stream(stream)   # (the allocator may not hand it out while it is in use)
+        ws = _scratch(need, torch.uint8, dev, stream)
     else:
         need = ws.numel() * ws.element_size()
     rc = adapters._backward(
         adapters._ref, rows._ref, x.data_ptr(), ldx, dy.data_ptr(), lddy,
         _low(low, adapters, rows), None if dx is None else dx.data_ptr(), lddx, accumulate,
-        ws.data_ptr(), need, _stream(stream, dev))
+        ws.data_ptr(), need, raw)
     if rc != OK:
         raise OpsError(rc, "bo_adapter_backward")

@@ -16,8 +16,10 @@
  * memory, all owned by the caller; nothing is allocated; calls are asynchronous on `stream` and
  * never wait for the GPU; the return value (a bd_status) reports argument and launch errors
  * only, and nothing has been enqueued when it is BD_ERR_INVALID_ARG.  Every call may be captured
- * in a CUDA graph.  Handles (bo_adamw, bo_adapter_set) are plain structs in host memory: the
- * caller owns them and may copy or drop them; their fields are the library's.
+ * in a CUDA graph.  Handles (bo_adamw, bo_adapter_set, bo_adapter_rows) are plain structs in host
+ * memory: the caller owns them and may copy or drop them; their fields are the library's.  A handle
+ * belongs to the device that was current when it was made; with another one current, calls that
+ * take it return BD_ERR_INVALID_ARG.
  */
 #ifndef BF16OPS_H
 #define BF16OPS_H
@@ -111,6 +113,7 @@ typedef struct bo_adamw {
   double* d_partials;
   uint64_t chunks;
   uint32_t weight_kind, grad_dtype, state_bits, flags;
+  int32_t device;
 } bo_adamw;
 
 /* Arguments of one step. */
@@ -193,6 +196,7 @@ typedef struct bo_adapter_set {
   uint32_t k, hidden, out;
   uint32_t rank;           /* columns of low: the largest rank, as 16, 32, 64 or 128 */
   uint32_t grad_dtype, has_grads, wide;
+  int32_t device;
 } bo_adapter_set;
 
 /* The rows of a batch grouped by adapter, laid out by bo_adapter_rows_init. */
@@ -204,6 +208,7 @@ typedef struct bo_adapter_rows {
   const int32_t* d_ntiles;   /* how many of each */
   int32_t* d_status;         /* as given; also BD_ERR_CUDA from a call whose waits ran out */
   uint32_t rows, k;
+  int32_t device;
 } bo_adapter_rows;
 
 /* Bytes of device memory (256-byte aligned) for a set of k adapters. */

@@ -26,7 +26,7 @@ class AdamWState(ctypes.Structure):
 class AdamW(ctypes.Structure):
     _fields_ = [("state", AdamWState), ("d_control", c_p), ("d_chunks", c_p),
                 ("d_partials", c_p), ("chunks", c_u64), ("weight_kind", c_u32),
-                ("grad_dtype", c_u32), ("state_bits", c_u32), ("flags", c_u32)]
+                ("grad_dtype", c_u32), ("state_bits", c_u32), ("flags", c_u32), ("device", c_int)]
 
 
 class AdamWStepArgs(ctypes.Structure):
@@ -43,13 +43,13 @@ class Adapter(ctypes.Structure):
 class AdapterSet(ctypes.Structure):
     _fields_ = [("d_table", c_p), ("k", c_u32), ("hidden", c_u32), ("out", c_u32),
                 ("rank", c_u32), ("grad_dtype", c_u32), ("has_grads", c_u32),
-                ("wide", c_u32)]
+                ("wide", c_u32), ("device", c_int)]
 
 
 class AdapterRows(ctypes.Structure):
     _fields_ = [("d_perm", c_p), ("d_offsets", c_p), ("d_blocks", c_p), ("d_tiles", c_p * 3), ("d_ntiles", c_p),
                 ("d_status", c_p),
-                ("rows", c_u32), ("k", c_u32)]
+                ("rows", c_u32), ("k", c_u32), ("device", c_int)]
 
 
 # name -> (restype, argtypes); must match include/ops/bf16ops.h

@@ -891,6 +891,7 @@ int bo_adamw_plan(const bo_adamw_item* h_items, uint32_t k, const bo_adamw_state
   h.state_bits = state_bits;
   h.flags = flags;
   int rc;
+  if ((rc = check(cudaGetDevice(&h.device)))) return rc;
   k_init_control<<<1, 1, 0, s>>>(h.d_control, step);
   if ((rc = check(cudaGetLastError()))) return rc;
   if (L.chunks > 0) {
@@ -906,8 +907,8 @@ int bo_adamw_plan(const bo_adamw_item* h_items, uint32_t k, const bo_adamw_state
 
 int bo_adamw_norm(const bo_adamw* h, float max_norm, void* stream) {
   if (!valid(h) || !(max_norm >= 0.f)) return BD_ERR_INVALID_ARG;
-  const int sms = sm_count();
-  if (sms <= 0) return BD_ERR_CUDA;
+  int sms = 0;
+  if (const int rc = sm_count(h->device, sms)) return rc;
   return launch_norm(h, max_norm, sms, static_cast<cudaStream_t>(stream));
 }
 
@@ -917,8 +918,8 @@ int bo_adamw_step(const bo_adamw* h, const bo_adamw_step_args* a, void* stream) 
       !(a->max_norm >= 0.f) || (a->d_lr && !aligned(a->d_lr, 4)) ||
       (!a->d_lr && !std::isfinite(a->lr)))
     return BD_ERR_INVALID_ARG;
-  const int sms = sm_count();
-  if (sms <= 0) return BD_ERR_CUDA;
+  int sms = 0;
+  if (const int rc = sm_count(h->device, sms)) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a->max_norm > 0.f) {
     const int rc = launch_norm(h, a->max_norm, sms, s);
@@ -963,8 +964,8 @@ int bo_adamw_step(const bo_adamw* h, const bo_adamw_step_args* a, void* stream) 
 int bo_adamw_moments(const bo_adamw* h, uint32_t dtype, void* d_m, void* d_v, void* stream) {
   if (!valid(h) || h->state_bits != 8 || dtype > BO_FP32 || !aligned(d_m, 16) || !aligned(d_v, 16))
     return BD_ERR_INVALID_ARG;
-  const int sms = sm_count();
-  if (sms <= 0) return BD_ERR_CUDA;
+  int sms = 0;
+  if (const int rc = sm_count(h->device, sms)) return rc;
   const uint64_t blocks = h->state.blocks;
   if (blocks == 0) return BD_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

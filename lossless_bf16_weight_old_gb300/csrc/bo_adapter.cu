@@ -1492,8 +1492,11 @@ int bo_adapter_set_init(const bo_adapter* h_items, uint32_t k, uint32_t hidden, 
     if (!d.vec_up || a.rank % 8 != 0) ups_whole = false;
     if (a.rank > most) most = a.rank;
   }
-  const int rc = check(upload(dev.get(), (uint64_t)k * sizeof(DevAdapter), d_set,
-                              static_cast<cudaStream_t>(stream)));
+  int device = 0;
+  int rc = check(cudaGetDevice(&device));
+  if (rc) return rc;
+  rc = check(upload(dev.get(), (uint64_t)k * sizeof(DevAdapter), d_set,
+                    static_cast<cudaStream_t>(stream)));
   if (rc) return rc;
   h_out->rank = most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 ? 64 : 128;
   h_out->d_table = d_set;
@@ -1503,6 +1506,7 @@ int bo_adapter_set_init(const bo_adapter* h_items, uint32_t k, uint32_t hidden, 
   h_out->grad_dtype = grad_dtype;
   h_out->has_grads = grads;
   h_out->wide = (all_wide ? 1u : 0u) | (ups_whole ? 2u : 0u);
+  h_out->device = device;
   return BD_OK;
 }
 
@@ -1529,7 +1533,10 @@ int bo_adapter_rows_init(const int32_t* d_index, uint32_t rows, uint32_t k, void
   Tile* t64 = reinterpret_cast<Tile*>(p + L.tiles64);
   Tile* t128 = reinterpret_cast<Tile*>(p + L.tiles128);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int rc = check(launch(k_rows_count, dim3(k), kThreads, 0, 1, s, d_index, rows, k, counts, d_status));
+  int device = 0;
+  int rc = check(cudaGetDevice(&device));
+  if (rc) return rc;
+  rc = check(launch(k_rows_count, dim3(k), kThreads, 0, 1, s, d_index, rows, k, counts, d_status));
   if (rc) return rc;
   rc = check(launch(k_rows_place, dim3(k), kThreads, 0, 1, s, d_index, rows, k, counts, perm, offsets,
                     t16, t64, t128, ntiles, blocks));
@@ -1544,12 +1551,14 @@ int bo_adapter_rows_init(const int32_t* d_index, uint32_t rows, uint32_t k, void
   h_out->d_ntiles = ntiles;
   h_out->rows = rows;
   h_out->k = k;
+  h_out->device = device;
   return BD_OK;
 }
 
 int bo_adapter_forward(const bo_adapter_set* set, const bo_adapter_rows* rows, const uint16_t* d_x,
                        uint64_t ldx, uint16_t* d_y, uint64_t ldy, uint16_t* d_low, void* stream) {
-  if (!valid(set) || !valid(rows) || rows->k != set->k) return BD_ERR_INVALID_ARG;
+  if (!valid(set) || !valid(rows) || rows->k != set->k || rows->device != set->device)
+    return BD_ERR_INVALID_ARG;
   if (rows->rows == 0) return BD_OK;
   if (!d_x || !d_y || !aligned(d_x, 2) || !aligned(d_y, 2) || ldx < set->hidden ||
       ldy < set->out || ldx > (1ull << 40) || ldy > (1ull << 40) || !aligned(d_low, 16) ||
@@ -1560,8 +1569,8 @@ int bo_adapter_forward(const bo_adapter_set* set, const bo_adapter_rows* rows, c
   if (overlaps(d_x, extent(rows->rows, ldx, set->hidden), d_y, yb) || overlaps(d_low, lb, d_y, yb) ||
       overlaps(d_low, lb, d_x, extent(rows->rows, ldx, set->hidden)))
     return BD_ERR_INVALID_ARG;
-  const int sms = sm_count();
-  if (sms <= 0) return BD_ERR_CUDA;
+  int sms = 0;
+  if (const int rc = sm_count(set->device, sms)) return rc;
   ApplyArgs P = {};
   P.table = static_cast<const DevAdapter*>(set->d_table);
   P.x = d_x;
@@ -1586,7 +1595,8 @@ int bo_adapter_backward(const bo_adapter_set* set, const bo_adapter_rows* rows,
                         const uint16_t* d_x, uint64_t ldx, const uint16_t* d_dy, uint64_t lddy,
                         const uint16_t* d_low, uint16_t* d_dx, uint64_t lddx, int32_t accumulate,
                         void* d_ws, uint64_t ws_bytes, void* stream) {
-  if (!valid(set) || !valid(rows) || rows->k != set->k) return BD_ERR_INVALID_ARG;
+  if (!valid(set) || !valid(rows) || rows->k != set->k || rows->device != set->device)
+    return BD_ERR_INVALID_ARG;
   const BackwardLayout L = backward_layout(set, rows->rows);
   if (!d_ws || !aligned(d_ws, 256) || ws_bytes < L.total) return BD_ERR_INVALID_ARG;
   const uint64_t xb = extent(rows->rows, ldx, set->hidden), yb = extent(rows->rows, lddy, set->out);
@@ -1602,8 +1612,8 @@ int bo_adapter_backward(const bo_adapter_set* set, const bo_adapter_rows* rows,
         overlaps(d_dx, db, d_ws, L.total))
       return BD_ERR_INVALID_ARG;
   }
-  const int sms = sm_count();
-  if (sms <= 0) return BD_ERR_CUDA;
+  int sms = 0;
+  if (const int rc = sm_count(set->device, sms)) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(d_ws);
   uint16_t* dlow = reinterpret_cast<uint16_t*>(w + L.dlow);

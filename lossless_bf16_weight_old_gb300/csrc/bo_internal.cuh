@@ -20,11 +20,13 @@ inline bool overlaps(const void* a, uint64_t na, const void* b, uint64_t nb) {
 inline uint64_t up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
 inline int check(cudaError_t e) { return e == cudaSuccess ? BD_OK : BD_ERR_CUDA; }
 
-inline int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return sms;
+// The SMs of the current device, which has to be the one that a handle was made on: its memory and
+// the streams that go with it are not the others'.
+inline int sm_count(int32_t device, int& sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BD_ERR_CUDA;
+  if (dev != device) return BD_ERR_INVALID_ARG;
+  return check(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
 }
 
 // Copies `bytes` (a multiple of 16) of host memory to dst as kernel parameters: the host memory

@@ -46,8 +46,22 @@ def _check(rc: int, what: str) -> None:
         raise OpsError(rc, what)
 
 
+def _here(device: torch.device) -> None:
+    """The library works on the current device, which has to be the tensors'."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _failed(rc: int, what: str, device: torch.device):
+    _here(device)      # (of a handle from another device the library says no more than that it is one)
+    raise OpsError(rc, what)
+
+
 def _stream(stream, device: torch.device) -> int:
     if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
         return stream.cuda_stream
     # (the handle alone: a torch.cuda.Stream object would cost more than the launch)
     return torch._C._cuda_getCurrentRawStream(device.index)
@@ -157,6 +171,8 @@ class AdamWBatch(_Owner):
                 if t.numel() != weights[i].numel():
                     raise ValueError(f"{name}[{i}] has {t.numel()} elements, its weights "
                                      f"{weights[i].numel()}")
+        _here(dev)
+        _stream(stream, dev)
         self.shapes = [w.shape for w in weights]
         self.ns = [w.numel() for w in weights]
         self.first_blocks, blocks = [], 0
@@ -220,8 +236,8 @@ class AdamWBatch(_Owner):
         the step reads when it runs) or the batch's own."""
         if lr is not None:
             if isinstance(lr, torch.Tensor):
-                if lr.dtype != torch.float32 or lr.numel() != 1 or not lr.is_cuda:
-                    raise ValueError("lr must be a number or a float32[1] CUDA tensor")
+                if lr.dtype != torch.float32 or lr.numel() != 1 or lr.device != self.device:
+                    raise ValueError(f"lr must be a number or a float32[1] tensor on {self.device}")
                 self._lr = lr
                 self._args.d_lr = lr.data_ptr()
             else:
@@ -229,7 +245,7 @@ class AdamWBatch(_Owner):
                 self._args.lr, self._args.d_lr = self.lr, None
         rc = self._step(*self._refs, self._on(stream))
         if rc != OK:
-            raise OpsError(rc, "bo_adamw_step")
+            _failed(rc, "bo_adamw_step", self.device)
 
     def grad_norm(self, stream=None) -> torch.Tensor:
         """The global norm of the gradients as they are now (`norm`), without a step."""
@@ -313,6 +329,8 @@ class AdapterSet(_Owner):
             gtype = d_downs[0].dtype
             if gtype not in _DTYPES:
                 raise TypeError(f"gradients must be bfloat16 or float32, got {gtype}")
+        _here(dev)
+        _stream(stream, dev)
         items = (_ops_lib.Adapter * k)()
         for i in range(k):
             r = downs[i].shape[0]
@@ -361,8 +379,10 @@ class AdapterRows(_Owner):
         need = int(lib.bo_adapter_rows_size(self.rows, self.k)) if self.k > 0 else 0
         if need == 0:
             raise ValueError("k must lie in 1 .. 65535 and the rows be fewer than 2**30")
+        _here(index.device)
         self.handle = _ops_lib.AdapterRows()
         self._ref = ctypes.byref(self.handle)
+        _stream(stream, index.device)
         with torch.cuda.stream(stream):
             self.memory = torch.empty(need, dtype=torch.uint8, device=index.device)
             self.status = torch.zeros(1, dtype=torch.int32, device=index.device)
@@ -378,6 +398,7 @@ class AdapterRows(_Owner):
                 or not index.is_contiguous():
             raise ValueError(f"index must be a contiguous int32 tensor of {self.rows} elements on "
                              f"{self.device}")
+        _here(self.device)
         if stream is not None:
             index.record_stream(stream)   # (it may go before the grouping has read it)
         self.index = index
@@ -438,7 +459,7 @@ def adapter_forward(x: torch.Tensor, y: torch.Tensor, adapters: AdapterSet, rows
     rc = adapters._forward(adapters._ref, rows._ref, x.data_ptr(), ldx, y.data_ptr(), ldy,
                            None if low is None else _low(low, adapters, rows), raw)
     if rc != OK:
-        raise OpsError(rc, "bo_adapter_forward")
+        _failed(rc, "bo_adapter_forward", dev)
     return y
 
 
@@ -469,4 +490,4 @@ def adapter_backward(x: torch.Tensor, dy: torch.Tensor, low: torch.Tensor,
         _low(low, adapters, rows), None if dx is None else dx.data_ptr(), lddx, accumulate,
         ws.data_ptr(), need, raw)
     if rc != OK:
-        raise OpsError(rc, "bo_adapter_backward")
+        _failed(rc, "bo_adapter_backward", dev)

@@ -249,15 +249,13 @@ __device__ __forceinline__ float quotient(float m, float v, float eps) {
   return den == 0.f ? 0.f : q;
 }
 
-// One element: updates m, v and p.
-template <bool TINY>
+// One element: updates m, v and p.  (For any eps: HBM bounds the step that this is for.)
 __device__ __forceinline__ void update(const Rates& R, float keep, float g, float& m, float& v,
                                        float& p) {
   g *= R.coef;
   m = fmaf(R.b1, m, R.c1 * g);
   v = fmaf(R.b2, v, R.c2 * g * g);
-  const float vt = v * R.inv_bc2;
-  p = fmaf(p, keep, R.rate * quotient<TINY>(m, vt, R.eps));
+  p = fmaf(p, keep, R.rate * quotient<true>(m, v * R.inv_bc2, R.eps));
 }
 
 // BF16 words of weights p, rounded to nearest or by the random bits
@@ -360,13 +358,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_step32(const StepParams P) {
       if (i + 8 <= c.count) {
         if (!loaded) x.load(P, c, i);
         loaded = false;
-        if (P.eps < kTinyEps) {
 #pragma unroll
-          for (int j = 0; j < 8; j++) update<true>(R, keep, x.g[j], x.m.v[j], x.v.v[j], x.p[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; j++) update<false>(R, keep, x.g[j], x.m.v[j], x.v.v[j], x.p[j]);
-        }
+        for (int j = 0; j < 8; j++) update(R, keep, x.g[j], x.m.v[j], x.v.v[j], x.p[j]);
         st8(am + e, x.m);
         st8(av + e, x.v);
         uint32_t r[8] = {}, w[4] = {};
@@ -383,8 +376,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_step32(const StepParams P) {
           const float g = load1<GF32>(c.g, i + j);
           float m = am[e + j], v = av[e + j];
           float p = WK == BO_WEIGHT_MASTER ? pm[j] : load1<WK == BO_WEIGHT_FP32>(c.w, i + j);
-          if (P.eps < kTinyEps) update<true>(R, keep, g, m, v, p);
-          else update<false>(R, keep, g, m, v, p);
+          update(R, keep, g, m, v, p);
           am[e + j] = m;
           av[e + j] = v;
           store_weight1<WK>(c, i + j, pm + (WK == BO_WEIGHT_MASTER ? j : 0), p, P.stochastic, r[j]);

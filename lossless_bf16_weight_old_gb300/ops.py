@@ -180,7 +180,7 @@ class AdamWBatch(_Owner):
             self.first_blocks.append(blocks)
             blocks += -(-n // BLOCK_ELEMS)
         self.blocks, self.state_bits = blocks, state_bits
-        self.lr, self.betas, self.eps = lr, (float(betas[0]), float(betas[1])), float(eps)
+        self.lr, self.betas, self.eps = float(lr), (float(betas[0]), float(betas[1])), float(eps)
         self.max_norm = max_norm
 
         given, elems = dict(state or {}), blocks * BLOCK_ELEMS
@@ -233,16 +233,17 @@ class AdamWBatch(_Owner):
 
     def run(self, lr: float | torch.Tensor | None = None, stream=None) -> None:
         """Takes one step, with this learning rate (a number, or a float32[1] device tensor that
-        the step reads when it runs) or the batch's own."""
-        if lr is not None:
-            if isinstance(lr, torch.Tensor):
-                if lr.dtype != torch.float32 or lr.numel() != 1 or lr.device != self.device:
-                    raise ValueError(f"lr must be a number or a float32[1] tensor on {self.device}")
-                self._lr = lr
-                self._args.d_lr = lr.data_ptr()
-            else:
-                self.lr = float(lr)
-                self._args.lr, self._args.d_lr = self.lr, None
+        the step reads when it runs) for this step alone, or the batch's own (`lr`)."""
+        args, where = self._args, None
+        if isinstance(lr, torch.Tensor):
+            if lr.dtype != torch.float32 or lr.numel() != 1 or lr.device != self.device:
+                raise ValueError(f"lr must be a number or a float32[1] tensor on {self.device}")
+            if stream is not None:
+                lr.record_stream(stream)
+            self._lr, where, rate = lr, lr.data_ptr(), 0.0
+        else:
+            rate = self.lr if lr is None else float(lr)
+        args.lr, args.d_lr = rate, where
         rc = self._step(*self._refs, self._on(stream))
         if rc != OK:
             _failed(rc, "bo_adamw_step", self.device)

@@ -1601,6 +1601,7 @@ int bo_adapter_backward(const bo_adapter_set* set, const bo_adapter_rows* rows,
   if (!d_ws || !aligned(d_ws, 256) || ws_bytes < L.total) return BD_ERR_INVALID_ARG;
   const uint64_t xb = extent(rows->rows, ldx, set->hidden), yb = extent(rows->rows, lddy, set->out);
   const uint64_t db = d_dx ? extent(rows->rows, lddx, set->hidden) : 0;
+  const uint64_t lb = (uint64_t)rows->rows * set->rank * 2;
   if (rows->rows > 0) {
     if (!d_x || !d_dy || !d_low || !aligned(d_x, 2) || !aligned(d_dy, 2) || !aligned(d_dx, 2) ||
         !aligned(d_low, 16) || ldx < set->hidden || lddy < set->out ||
@@ -1608,8 +1609,9 @@ int bo_adapter_backward(const bo_adapter_set* set, const bo_adapter_rows* rows,
         (d_dx && lddx > (1ull << 40)))
       return BD_ERR_INVALID_ARG;
     if (overlaps(d_dx, db, d_x, xb) || overlaps(d_dx, db, d_dy, yb) ||
-        overlaps(d_dx, db, d_low, (uint64_t)rows->rows * set->rank * 2) ||
-        overlaps(d_dx, db, d_ws, L.total))
+        overlaps(d_dx, db, d_low, lb) || overlaps(d_dx, db, d_ws, L.total) ||
+        overlaps(d_ws, L.total, d_x, xb) || overlaps(d_ws, L.total, d_dy, yb) ||
+        overlaps(d_ws, L.total, d_low, lb))
       return BD_ERR_INVALID_ARG;
   }
   int sms = 0;

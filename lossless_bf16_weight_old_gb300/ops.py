@@ -485,6 +485,8 @@ def adapter_backward(x: torch.Tensor, dy: torch.Tensor, low: torch.Tensor,
             adapters._need = rows.rows, need
         ws = _scratch(need, torch.uint8, dev, stream)
     else:
+        if ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         need = ws.numel() * ws.element_size()
     rc = adapters._backward(
         adapters._ref, rows._ref, x.data_ptr(), ldx, dy.data_ptr(), lddy,

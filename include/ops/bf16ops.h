@@ -132,7 +132,9 @@ BD_API uint64_t bo_adamw_plan_size(const bo_adamw_item* h_items, uint32_t k);
 
 /* Lays the tensor table out in d_plan and fills *h_out.  h_items is read during the call only.
  * step: steps taken so far.  The tensors, the arenas and d_plan must stay where they are while
- * the handle is used.  Arenas of different items may not overlap. */
+ * the handle is used.  What a step writes (outputs, arenas, d_plan) may not overlap anything else of
+ * the plan, but for an output that is its own item's weights, nor may the items' blocks: a tensor that
+ * two items share is refused. */
 BD_API int bo_adamw_plan(const bo_adamw_item* h_items, uint32_t k, const bo_adamw_state* state,
                          uint32_t weight_kind, uint32_t grad_dtype, uint32_t state_bits,
                          uint32_t flags, int64_t step, void* d_plan, uint64_t plan_bytes,

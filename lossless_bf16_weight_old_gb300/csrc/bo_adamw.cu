@@ -836,7 +836,22 @@ int bo_adamw_plan(const bo_adamw_item* h_items, uint32_t k, const bo_adamw_state
   const uint64_t wsize = weight_kind == BO_WEIGHT_FP32 ? 4 : 2, gsize = grad_dtype == BO_FP32 ? 4 : 2;
   const uint64_t elems = state->blocks * BO_BLOCK_ELEMS, msize = state_bits == 8 ? 1 : 4;
   std::unique_ptr<DevItem[]> dev(new (std::nothrow) DevItem[k ? k : 1]);
-  if (!dev) return BD_ERR_INVALID_ARG;
+  std::unique_ptr<Span[]> memory(new (std::nothrow) Span[3 * (size_t)k + 6]);
+  std::unique_ptr<Span[]> arena(new (std::nothrow) Span[(size_t)k + 1]);
+  if (!dev || !memory || !arena) return BD_ERR_INVALID_ARG;
+  size_t spans = 0;
+  auto uses = [&](const void* p, uint64_t bytes, bool write) {
+    const uint64_t at = reinterpret_cast<uintptr_t>(p);
+    memory[spans++] = Span{at, at + bytes, write};
+  };
+  uses(d_plan, L.total, true);
+  uses(state->d_m, elems * msize, true);
+  uses(state->d_v, elems * msize, true);
+  if (state_bits == 8) {
+    uses(state->d_m_scale, state->blocks * 4, true);
+    uses(state->d_v_scale, state->blocks * 4, true);
+  }
+  if (master) uses(state->d_master, elems * 4, true);
   uint64_t chunk0 = 0;
   for (uint32_t i = 0; i < k; i++) {
     const bo_adamw_item& it = h_items[i];
@@ -844,19 +859,14 @@ int bo_adamw_plan(const bo_adamw_item* h_items, uint32_t k, const bo_adamw_state
     if (it.reserved != 0 || it.first_block > state->blocks ||
         blocks > state->blocks - it.first_block)
       return BD_ERR_INVALID_ARG;
+    arena[i] = Span{it.first_block, it.first_block + blocks, true};
     if (it.n > 0) {
       if (!it.d_out || !it.d_grad || !aligned(it.d_out, 16) || !aligned(it.d_grad, 16))
         return BD_ERR_INVALID_ARG;
       if (!master && (!it.d_weight || !aligned(it.d_weight, 16))) return BD_ERR_INVALID_ARG;
-      const uint64_t ob = it.n * wsize;
-      if (!master && it.d_out != it.d_weight && overlaps(it.d_out, ob, it.d_weight, ob))
-        return BD_ERR_INVALID_ARG;
-      if (overlaps(it.d_out, ob, it.d_grad, it.n * gsize) ||
-          overlaps(it.d_out, ob, d_plan, L.total) ||
-          overlaps(it.d_out, ob, state->d_m, elems * msize) ||
-          overlaps(it.d_out, ob, state->d_v, elems * msize) ||
-          (master && overlaps(it.d_out, ob, state->d_master, elems * 4)))
-        return BD_ERR_INVALID_ARG;
+      uses(it.d_out, it.n * wsize, true);
+      uses(it.d_grad, it.n * gsize, false);
+      if (!master && it.d_weight != it.d_out) uses(it.d_weight, it.n * wsize, false);
     }
     DevItem& d = dev[i];
     std::memset(&d, 0, sizeof(d));
@@ -869,6 +879,7 @@ int bo_adamw_plan(const bo_adamw_item* h_items, uint32_t k, const bo_adamw_state
     d.wd = it.weight_decay;
     chunk0 += (it.n + kChunkElems - 1) / kChunkElems;
   }
+  if (!disjoint(memory.get(), spans) || !disjoint(arena.get(), k)) return BD_ERR_INVALID_ARG;
   uint8_t* p = static_cast<uint8_t*>(d_plan);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   bo_adamw h;

@@ -1,6 +1,7 @@
 // bo_internal.cuh -- definitions shared by the kernels of libbf16ops (include/ops/bf16ops.h).
 #pragma once
 
+#include <algorithm>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -16,6 +17,23 @@ inline bool aligned(const void* p, uintptr_t a) {
 inline bool overlaps(const void* a, uint64_t na, const void* b, uint64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+// Memory (or anything numbered) that a call reads or writes.
+struct Span {
+  uint64_t begin, end;
+  bool write;
+};
+// Whether nothing that is written meets anything else.  Sorts them.
+inline bool disjoint(Span* s, size_t n) {
+  std::sort(s, s + n, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  uint64_t reads = 0, writes = 0;   // where those before end
+  for (size_t i = 0; i < n; i++) {
+    if (s[i].begin == s[i].end) continue;
+    if (s[i].begin < writes || (s[i].write && s[i].begin < reads)) return false;
+    uint64_t& most = s[i].write ? writes : reads;
+    most = std::max(most, s[i].end);
+  }
+  return true;
 }
 inline uint64_t up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
 inline int check(cudaError_t e) { return e == cudaSuccess ? BD_OK : BD_ERR_CUDA; }

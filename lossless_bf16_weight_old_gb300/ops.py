@@ -129,7 +129,8 @@ class AdamWBatch(_Owner):
     The arenas in `state` hold the tensors one after the other, each from a new block of 256 on;
     `view(name, i)` is tensor i's part.  Results on the device after `run`: the new weights, the
     state, `norm` (float32[1], with max_norm), `status` (int32[1]: OK or SKIPPED_NONFINITE) and
-    `steps` (int64[1]).  Tensors must stay where they are for the life of the batch."""
+    `steps` (int64[1]).  Tensors must stay where they are for the life of the batch, and each be
+    given once (tied weights: as one tensor, with the sum of their gradients)."""
 
     def __init__(self, weights: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], *,
                  news: Sequence[torch.Tensor] | None = None, master: bool | None = None,

@@ -180,7 +180,7 @@ BD_API int bo_adamw_moments(const bo_adamw* h, uint32_t dtype, void* d_m, void* 
 #define BO_ADAPTER_MAX_ROWS (1u << 30)
 
 /* One adapter.  Row strides in elements: at least hidden for down, at least rank for up.  The
- * gradients may be NULL where no backward pass is made. */
+ * gradients are NULL in all adapters of a set (a backward pass then gives dx alone) or in none. */
 typedef struct bo_adapter {
   const uint16_t* d_down;  /* A: rank x hidden */
   const uint16_t* d_up;    /* B: out x rank */

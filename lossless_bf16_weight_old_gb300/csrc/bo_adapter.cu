@@ -1460,18 +1460,18 @@ int bo_adapter_set_init(const bo_adapter* h_items, uint32_t k, uint32_t hidden, 
   if (!dev) return BD_ERR_INVALID_ARG;
   const uintptr_t gsize = grad_dtype == BO_FP32 ? 4 : 2;
   uint32_t most = 1;
-  bool grads = true, all_wide = true, ups_whole = true;
+  const bool grads = h_items[0].d_grad_down != nullptr;
+  bool all_wide = true, ups_whole = true;
   for (uint32_t i = 0; i < k; i++) {
     const bo_adapter& a = h_items[i];
     if (!a.d_down || !a.d_up || !aligned(a.d_down, 2) || !aligned(a.d_up, 2) || a.rank < 1 ||
         a.rank > BO_ADAPTER_MAX_RANK || a.ld_down < hidden || a.ld_up < a.rank ||
         a.ld_down > (1ull << 40) || a.ld_up > (1ull << 40))
       return BD_ERR_INVALID_ARG;
-    if (!a.d_grad_down != !a.d_grad_up) return BD_ERR_INVALID_ARG;
-    if (!a.d_grad_down) grads = false;
-    else if (!aligned(a.d_grad_down, gsize) || !aligned(a.d_grad_up, gsize) ||
-             a.ld_grad_down < hidden || a.ld_grad_up < a.rank || a.ld_grad_down > (1ull << 40) ||
-             a.ld_grad_up > (1ull << 40))
+    if (!a.d_grad_down == grads || !a.d_grad_up == grads) return BD_ERR_INVALID_ARG;
+    if (grads && (!aligned(a.d_grad_down, gsize) || !aligned(a.d_grad_up, gsize) ||
+                  a.ld_grad_down < hidden || a.ld_grad_up < a.rank || a.ld_grad_down > (1ull << 40) ||
+                  a.ld_grad_up > (1ull << 40)))
       return BD_ERR_INVALID_ARG;
     DevAdapter& d = dev[i];
     d.down = a.d_down;

@@ -1413,9 +1413,22 @@ bool valid(const bo_adapter_rows* r) {
 bool wide(const void* p, uint64_t ld, uint64_t width) {
   return aligned(p, 16) && ld % 8 == 0 && width % 8 == 0;
 }
-// bytes from the first to past the last value of `rows` rows
-uint64_t extent(uint64_t rows, uint64_t ld, uint64_t width) {
-  return rows == 0 ? 0 : 2 * ((rows - 1) * ld + width);
+// Memory of `rows` rows, in bytes.
+struct Region {
+  uint64_t at, ld, width, rows;
+  Region(const void* p, uint64_t n, uint64_t stride, uint64_t columns, uint64_t size = 2)
+      : at(reinterpret_cast<uintptr_t>(p)), ld(stride * size), width(columns * size), rows(p ? n : 0) {}
+  uint64_t end() const { return rows ? at + (rows - 1) * ld + width : at; }
+};
+// Whether two of them have a byte in common.  Rows of the same stride may lie between one another's
+// (columns of one buffer); of different strides they may not.
+bool meet(const Region& a, const Region& b) {
+  if (a.rows == 0 || b.rows == 0 || a.at >= b.end() || b.at >= a.end()) return false;
+  if (a.at > b.at) return meet(b, a);
+  if (a.rows == 1 || (b.rows > 1 && a.ld != b.ld)) return true;
+  // b begins `off` bytes into row `skip` of a, which is not past a's last
+  const uint64_t skip = (b.at - a.at) / a.ld, off = (b.at - a.at) % a.ld;
+  return off < a.width || (skip + 1 < a.rows && off + b.width > a.ld);
 }
 uint64_t up8(uint64_t x) { return (x + 7) / 8 * 8; }
 
@@ -1564,11 +1577,9 @@ int bo_adapter_forward(const bo_adapter_set* set, const bo_adapter_rows* rows, c
       ldy < set->out || ldx > (1ull << 40) || ldy > (1ull << 40) || !aligned(d_low, 16) ||
       (!d_low && rows->rows >= bo_adapter_low_rows(set)))
     return BD_ERR_INVALID_ARG;
-  const uint64_t yb = extent(rows->rows, ldy, set->out);
-  const uint64_t lb = d_low ? (uint64_t)rows->rows * set->rank * 2 : 0;
-  if (overlaps(d_x, extent(rows->rows, ldx, set->hidden), d_y, yb) || overlaps(d_low, lb, d_y, yb) ||
-      overlaps(d_low, lb, d_x, extent(rows->rows, ldx, set->hidden)))
-    return BD_ERR_INVALID_ARG;
+  const Region x(d_x, rows->rows, ldx, set->hidden), y(d_y, rows->rows, ldy, set->out);
+  const Region low(d_low, rows->rows, set->rank, set->rank);
+  if (meet(x, y) || meet(low, y) || meet(low, x)) return BD_ERR_INVALID_ARG;
   int sms = 0;
   if (const int rc = sm_count(set->device, sms)) return rc;
   ApplyArgs P = {};
@@ -1599,19 +1610,17 @@ int bo_adapter_backward(const bo_adapter_set* set, const bo_adapter_rows* rows,
     return BD_ERR_INVALID_ARG;
   const BackwardLayout L = backward_layout(set, rows->rows);
   if (!d_ws || !aligned(d_ws, 256) || ws_bytes < L.total) return BD_ERR_INVALID_ARG;
-  const uint64_t xb = extent(rows->rows, ldx, set->hidden), yb = extent(rows->rows, lddy, set->out);
-  const uint64_t db = d_dx ? extent(rows->rows, lddx, set->hidden) : 0;
-  const uint64_t lb = (uint64_t)rows->rows * set->rank * 2;
   if (rows->rows > 0) {
     if (!d_x || !d_dy || !d_low || !aligned(d_x, 2) || !aligned(d_dy, 2) || !aligned(d_dx, 2) ||
         !aligned(d_low, 16) || ldx < set->hidden || lddy < set->out ||
         (d_dx && lddx < set->hidden) || ldx > (1ull << 40) || lddy > (1ull << 40) ||
         (d_dx && lddx > (1ull << 40)))
       return BD_ERR_INVALID_ARG;
-    if (overlaps(d_dx, db, d_x, xb) || overlaps(d_dx, db, d_dy, yb) ||
-        overlaps(d_dx, db, d_low, lb) || overlaps(d_dx, db, d_ws, L.total) ||
-        overlaps(d_ws, L.total, d_x, xb) || overlaps(d_ws, L.total, d_dy, yb) ||
-        overlaps(d_ws, L.total, d_low, lb))
+    const Region x(d_x, rows->rows, ldx, set->hidden), dy(d_dy, rows->rows, lddy, set->out);
+    const Region low(d_low, rows->rows, set->rank, set->rank), ws(d_ws, 1, L.total, L.total, 1);
+    const Region dx(d_dx, rows->rows, lddx, set->hidden);
+    if (meet(dx, x) || meet(dx, dy) || meet(dx, low) || meet(ws, x) || meet(ws, dy) ||
+        meet(ws, low) || meet(ws, dx))
       return BD_ERR_INVALID_ARG;
   }
   int sms = 0;

@@ -180,7 +180,9 @@ BD_API int bo_adamw_moments(const bo_adamw* h, uint32_t dtype, void* d_m, void* 
 #define BO_ADAPTER_MAX_ROWS (1u << 30)
 
 /* One adapter.  Row strides in elements: at least hidden for down, at least rank for up.  The
- * gradients are NULL in all adapters of a set (a backward pass then gives dx alone) or in none. */
+ * gradients are NULL in all adapters of a set (a backward pass then gives dx alone) or in none.  A
+ * gradient may not overlap another one or a factor of the set (refused), nor anything else of a
+ * backward call.  Adapters may share factors, but not gradients. */
 typedef struct bo_adapter {
   const uint16_t* d_down;  /* A: rank x hidden */
   const uint16_t* d_up;    /* B: out x rank */

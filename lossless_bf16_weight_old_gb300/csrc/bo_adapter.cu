@@ -20,6 +20,7 @@
 // a slice of the first product's long sum, the slices' sums meet through distributed shared
 // memory in a fixed order, and each block then writes a slice of the second product's columns.
 #include <cooperative_groups.h>
+#include <algorithm>
 #include <cstring>
 #include <memory>
 #include <new>
@@ -1416,6 +1417,8 @@ bool wide(const void* p, uint64_t ld, uint64_t width) {
 // Memory of `rows` rows, in bytes.
 struct Region {
   uint64_t at, ld, width, rows;
+  bool write = false;
+  Region() = default;
   Region(const void* p, uint64_t n, uint64_t stride, uint64_t columns, uint64_t size = 2)
       : at(reinterpret_cast<uintptr_t>(p)), ld(stride * size), width(columns * size), rows(p ? n : 0) {}
   uint64_t end() const { return rows ? at + (rows - 1) * ld + width : at; }
@@ -1429,6 +1432,17 @@ bool meet(const Region& a, const Region& b) {
   // b begins `off` bytes into row `skip` of a, which is not past a's last
   const uint64_t skip = (b.at - a.at) / a.ld, off = (b.at - a.at) % a.ld;
   return off < a.width || (skip + 1 < a.rows && off + b.width > a.ld);
+}
+// Whether a set's gradients lie apart from one another and from its factors.  Sorts the regions.  Of
+// matrices that lie between one another's rows every pair is looked at, a few million at most (all
+// of 65535 adapters' factors as columns of one buffer would take a minute).
+bool apart(Region* r, uint64_t n) {
+  std::sort(r, r + n, [](const Region& a, const Region& b) { return a.at < b.at; });
+  uint64_t left = 1u << 24;
+  for (uint64_t i = 0; i < n; i++)
+    for (uint64_t j = i + 1; j < n && r[j].at < r[i].end() && left; j++, left--)
+      if ((r[i].write || r[j].write) && meet(r[i], r[j])) return false;
+  return true;
 }
 uint64_t up8(uint64_t x) { return (x + 7) / 8 * 8; }
 
@@ -1470,7 +1484,9 @@ int bo_adapter_set_init(const bo_adapter* h_items, uint32_t k, uint32_t hidden, 
       out > BO_ADAPTER_MAX_WIDTH)
     return BD_ERR_INVALID_ARG;
   std::unique_ptr<DevAdapter[]> dev(new (std::nothrow) DevAdapter[k]);
-  if (!dev) return BD_ERR_INVALID_ARG;
+  std::unique_ptr<Region[]> memory(new (std::nothrow) Region[4 * (size_t)k]);
+  if (!dev || !memory) return BD_ERR_INVALID_ARG;
+  uint64_t regions = 0;
   const uintptr_t gsize = grad_dtype == BO_FP32 ? 4 : 2;
   uint32_t most = 1;
   const bool grads = h_items[0].d_grad_down != nullptr;
@@ -1486,6 +1502,13 @@ int bo_adapter_set_init(const bo_adapter* h_items, uint32_t k, uint32_t hidden, 
                   a.ld_grad_down < hidden || a.ld_grad_up < a.rank || a.ld_grad_down > (1ull << 40) ||
                   a.ld_grad_up > (1ull << 40)))
       return BD_ERR_INVALID_ARG;
+    if (grads) {
+      memory[regions++] = Region(a.d_down, a.rank, a.ld_down, hidden);
+      memory[regions++] = Region(a.d_up, out, a.ld_up, a.rank);
+      memory[regions++] = Region(a.d_grad_down, a.rank, a.ld_grad_down, hidden, gsize);
+      memory[regions++] = Region(a.d_grad_up, out, a.ld_grad_up, a.rank, gsize);
+      memory[regions - 2].write = memory[regions - 1].write = true;
+    }
     DevAdapter& d = dev[i];
     d.down = a.d_down;
     d.up = a.d_up;
@@ -1505,6 +1528,7 @@ int bo_adapter_set_init(const bo_adapter* h_items, uint32_t k, uint32_t hidden, 
     if (!d.vec_up || a.rank % 8 != 0) ups_whole = false;
     if (a.rank > most) most = a.rank;
   }
+  if (!apart(memory.get(), regions)) return BD_ERR_INVALID_ARG;
   int device = 0;
   int rc = check(cudaGetDevice(&device));
   if (rc) return rc;

@@ -306,7 +306,8 @@ class AdapterSet(_Owner):
     downs, ups   factors: downs[i] is [rank_i, hidden], ups[i] is [out, rank_i], bfloat16, rows
                  contiguous; ranks from 1 to 128 may differ
     scales       one number per adapter (usually alpha / rank), or one for all
-    d_downs, d_ups   (for a backward pass) their gradients, all bfloat16 or all float32
+    d_downs, d_ups   (for a backward pass) their gradients, all bfloat16 or all float32; adapters may
+                 share a factor, but each has gradients of its own
 
     The tensors must stay where they are for the life of the set; their values may change at any
     time (an optimizer step, a delta applied in place)."""

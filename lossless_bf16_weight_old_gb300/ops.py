@@ -163,8 +163,8 @@ class AdamWBatch(_Owner):
             raise ValueError("max_norm must be positive")
         if not (0 <= betas[0] < 1 and 0 <= betas[1] < 1) or not eps >= 0:
             raise ValueError("betas must lie in [0, 1) and eps must not be negative")
-        if step < 0:
-            raise ValueError("step must not be negative")
+        if not 0 <= step < 1 << 62:
+            raise ValueError("step must not be negative (or past 2**62)")
         for name, ts, dt in (("weights", weights, wtype), ("grads", grads, gtype), ("news", outs, wtype)):
             for i, t in enumerate(ts):
                 if t.dtype != dt or not t.is_cuda or t.device != dev or not t.is_contiguous():
@@ -334,6 +334,8 @@ class AdapterSet(_Owner):
                 raise TypeError(f"gradients must be bfloat16 or float32, got {gtype}")
         _here(dev)
         _stream(stream, dev)
+        if not (1 <= hidden <= 1 << 24 and 1 <= out <= 1 << 24):
+            raise ValueError("the factors' widths must lie in 1 .. 2**24")
         items = (_ops_lib.Adapter * k)()
         for i in range(k):
             r = downs[i].shape[0]
@@ -377,11 +379,11 @@ class AdapterRows(_Owner):
     def __init__(self, index: torch.Tensor, k: int, *, stream=None):
         if index.dtype != torch.int32 or index.dim() != 1 or not index.is_cuda:
             raise ValueError("index must be a 1-dimensional int32 CUDA tensor")
-        lib = _ops_lib.load()
         self.rows, self.k = index.numel(), int(k)
-        need = int(lib.bo_adapter_rows_size(self.rows, self.k)) if self.k > 0 else 0
-        if need == 0:
-            raise ValueError("k must lie in 1 .. 65535 and the rows be fewer than 2**30")
+        # (here, because the library's integers have 32 bits)
+        if not 1 <= self.k <= 65535 or self.rows > 1 << 30:
+            raise ValueError("k must lie in 1 .. 65535 and the rows be at most 2**30")
+        need = int(_ops_lib.load().bo_adapter_rows_size(self.rows, self.k))
         _here(index.device)
         self.handle = _ops_lib.AdapterRows()
         self._ref = ctypes.byref(self.handle)

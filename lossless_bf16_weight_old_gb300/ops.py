@@ -26,6 +26,7 @@ SKIPPED_NONFINITE = 16
 BLOCK_ELEMS = 256
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 _U64 = (1 << 64) - 1
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 __all__ = ["AdamWBatch", "AdapterSet", "AdapterRows", "adapter_forward", "adapter_backward", "SKIPPED_NONFINITE", "OpsError", "ops_status_name"]
 
@@ -63,8 +64,7 @@ def _stream(stream, device: torch.device) -> int:
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
         return stream.cuda_stream
-    # (the handle alone: a torch.cuda.Stream object would cost more than the launch)
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return _current_stream(device.index)
 
 
 class _Owner:
@@ -73,7 +73,7 @@ class _Owner:
     waits until they are filled, and the allocator learns of that stream."""
 
     def _made(self, buffers: list, device: torch.device) -> None:   # (on the constructor's stream)
-        self._buffers, self.device = buffers, device
+        self._buffers, self.device, self._index = buffers, device, device.index
         self._home, self._others = _stream(None, device), set()
         self._filled = None
         if not torch.cuda.is_current_stream_capturing():
@@ -82,7 +82,8 @@ class _Owner:
 
     def _on(self, stream) -> int:
         """The handle of the stream of a call."""
-        raw = _stream(stream, self.device)
+        # (the handle alone: a torch.cuda.Stream object would cost more than the launch)
+        raw = _current_stream(self._index) if stream is None else _stream(stream, self.device)
         if raw != self._home and raw not in self._others:
             self._join(raw, stream)
         return raw
@@ -422,6 +423,13 @@ def _pair(adapters: AdapterSet, rows: AdapterRows, stream) -> int:
     return raw
 
 
+def _unrecorded(a: torch.Tensor, b: torch.Tensor) -> None:
+    if (a.requires_grad or b.requires_grad) and torch.is_grad_enabled():
+        raise ValueError("autograd records this call's tensors, and would miss the adapters' part: "
+                         "call under torch.no_grad() or with detached tensors, and adapter_backward "
+                         "for the gradients")
+
+
 def _scratch(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
     """Memory for one call, from the pool of the stream that the call runs on: what used it
     before, and what will after, is in that stream's order."""
@@ -454,8 +462,10 @@ def adapter_forward(x: torch.Tensor, y: torch.Tensor, adapters: AdapterSet, rows
     """y[t] += scale * up @ (down @ x[t]) with the adapter of row t, in place; y is the shared
     projection's output.  x [rows, hidden] and y [rows, out] are bfloat16 with contiguous rows.
     low (optional, bfloat16 [rows, adapters.rank]) receives what adapter_backward needs.  Rows
-    without an adapter are left alone.  Returns y."""
+    without an adapter are left alone.  Returns y.  Autograd does not see the call, which refuses
+    an x or y that it records."""
     raw = _pair(adapters, rows, stream)
+    _unrecorded(x, y)
     dev = adapters.device
     ldx = _rows_of(x, "x", (rows.rows, adapters.hidden), dev)
     ldy = _rows_of(y, "y", (rows.rows, adapters.out), dev)
@@ -476,6 +486,7 @@ def adapter_backward(x: torch.Tensor, dy: torch.Tensor, low: torch.Tensor,
     projection's part; None: not wanted), in place, and the gradients given to the set are
     written, or with accumulate=True added to.  low is the forward pass's."""
     raw = _pair(adapters, rows, stream)
+    _unrecorded(dy, dy if dx is None else dx)
     dev = adapters.device
     ldx = _rows_of(x, "x", (rows.rows, adapters.hidden), dev)
     lddy = _rows_of(dy, "dy", (rows.rows, adapters.out), dev)

@@ -203,6 +203,11 @@ typedef struct bo_adapter_set {
   int32_t device;
 } bo_adapter_set;
 
+/* For tests of the kernels' bounded waits: set in bo_adapter_set.wide, it keeps the first stage of
+ * the forms on the tensor cores' own memory from ever being reported, so that their waits run out (two
+ * seconds each) and the calls set *d_status. */
+#define BO_ADAPTER_DEBUG_STALL 0x80000000u
+
 /* The rows of a batch grouped by adapter, laid out by bo_adapter_rows_init. */
 typedef struct bo_adapter_rows {
   const int32_t* d_perm;     /* rows, grouped */
@@ -210,7 +215,8 @@ typedef struct bo_adapter_rows {
   const int32_t* d_blocks;   /* blocks of 64 rows (counted as at least four) of the adapters before */
   const void* d_tiles[3];    /* tiles of at most 16, 64 and 128 rows of one adapter */
   const int32_t* d_ntiles;   /* how many of each */
-  int32_t* d_status;         /* as given; also BD_ERR_CUDA from a call whose waits ran out */
+  int32_t* d_status;         /* as given; BD_ERR_CUDA from a call whose waits ran out (its outputs
+                                are not to be used), until the rows are grouped again */
   uint32_t rows, k;
   int32_t device;
 } bo_adapter_rows;

@@ -1618,7 +1618,8 @@ int bo_adapter_forward(const bo_adapter_set* set, const bo_adapter_rows* rows, c
   P.vec_x = wide(d_x, ldx, set->hidden);
   P.vec_y = wide(d_y, ldy, set->out);
   P.vec_factors = set->wide & 1;
-  P.vec_ups = set->wide >> 1;
+  P.vec_ups = set->wide >> 1 & 1;
+  P.stall = set->wide & BO_ADAPTER_DEBUG_STALL;
   return apply(set->rank, rows, P, sms, static_cast<cudaStream_t>(stream));
 }
 
@@ -1676,6 +1677,7 @@ int bo_adapter_backward(const bo_adapter_set* set, const bo_adapter_rows* rows,
     P.vec_x = wide(d_dy, lddy, set->out);
     P.vec_y = d_dx && wide(d_dx, lddx, set->hidden);
     P.vec_factors = P.vec_ups = 1;
+    P.stall = set->wide & BO_ADAPTER_DEBUG_STALL;
     if ((rc = apply(set->rank, rows, P, sms, s))) return rc;
   }
   if (!set->has_grads) return BD_OK;
@@ -1702,6 +1704,7 @@ int bo_adapter_backward(const bo_adapter_set* set, const bo_adapter_rows* rows,
   G.k = set->k;
   const bool vec = G.vec_x && G.vec_dy;
   G.status = rows->d_status;
+  G.stall = set->wide & BO_ADAPTER_DEBUG_STALL;
   const uint64_t stages = ((uint64_t)rows->rows / 64 + set->k) * slices;   // at most
   const uint64_t slots = sms < (int)kMaxSms ? sms : (int)kMaxSms;
   if (vec && rows->rows > 0)   // a block an SM

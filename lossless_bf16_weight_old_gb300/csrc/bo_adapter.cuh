@@ -65,6 +65,7 @@ struct ApplyArgs {
   uint32_t vec_factors;   // ... of every adapter's first factor
   uint32_t vec_ups;       // ... of every second one, whose rows end with (or are 0 up to) whole words
   int32_t* status;        // BD_ERR_CUDA when a wait inside a kernel ran out; may be NULL
+  uint32_t stall;         // the first stage is never reported
 };
 
 struct WgradArgs {
@@ -83,6 +84,7 @@ struct WgradArgs {
   uint32_t k, hidden, out, vec_x, vec_dy;
   uint32_t grad_f32, accumulate;
   int32_t* status;
+  uint32_t stall;
 };
 
 constexpr uint32_t kFeat = 128;   // features of a piece of the weight gradients

@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(288, 1) k_low(const ApplyArgs P) {
           cp16z(to + L::kX + j * 128, A.down + (w ? (uint64_t)row * A.ld_down + k + ch * 8 : 0), w);
         }
       }
-      stage_issued<S>(ctl, i);
+      if (!P.stall || i > 0) stage_issued<S>(ctl, i);
     }
     copies_wait();
   } else {
@@ -287,6 +287,8 @@ __global__ void __launch_bounds__(288, 1) k_low(const ApplyArgs P) {
         tc_commit(smem_addr(&ctl->freed[s]));
       }
       tc_commit(smem_addr(&ctl->done[0]));
+      // (given up: the others may have too, and nobody else sees that the block's last arrival is in)
+      if (!ok) bar_wait(smem_addr(&ctl->done[0]), 0);
     }
     __syncwarp();
   }
@@ -440,7 +442,7 @@ __global__ void __launch_bounds__(32 * (kCopyWarps + 5), 1) k_wgrad_tc(const Wgr
                     t >= 0);
           }
         }
-        stage_issued<S>(ctl, i);
+        if (!P.stall || i > 0) stage_issued<S>(ctl, i);
       }
     }
     copies_wait();
@@ -470,6 +472,7 @@ __global__ void __launch_bounds__(32 * (kCopyWarps + 5), 1) k_wgrad_tc(const Wgr
           tc_commit(smem_addr(&ctl->freed[s]));
         }
         tc_commit(smem_addr(&ctl->done[b]));
+        if (!ok) bar_wait(smem_addr(&ctl->done[b]), (piece / 2) & 1);   // (as in k_low)
       }
     }
     __syncwarp();

@@ -375,7 +375,9 @@ class AdapterRows(_Owner):
     """The rows of a batch grouped by adapter, on the device: index[t] (int32) is the adapter of
     row t, -1 for none.  One grouping serves every projection of a model step; `update` regroups
     for new values of as many rows.  `status` (int32[1]) is ERR_INVALID_ARG when an index lies
-    outside -1 .. k - 1 (such rows count as rows without an adapter)."""
+    outside -1 .. k - 1 (such rows count as rows without an adapter), and ERR_CUDA from a call of
+    adapter_forward or adapter_backward on that found a wait inside one of its kernels too long, until
+    the next `update`: that call's outputs are not to be used."""
 
     def __init__(self, index: torch.Tensor, k: int, *, stream=None):
         if index.dtype != torch.int32 or index.dim() != 1 or not index.is_cuda:
@@ -462,8 +464,8 @@ def adapter_forward(x: torch.Tensor, y: torch.Tensor, adapters: AdapterSet, rows
     """y[t] += scale * up @ (down @ x[t]) with the adapter of row t, in place; y is the shared
     projection's output.  x [rows, hidden] and y [rows, out] are bfloat16 with contiguous rows.
     low (optional, bfloat16 [rows, adapters.rank]) receives what adapter_backward needs.  Rows
-    without an adapter are left alone.  Returns y.  Autograd does not see the call, which refuses
-    an x or y that it records."""
+    without an adapter are left alone.  Returns y.  `rows.status` tells of a kernel that gave up.
+    Autograd does not see the call, which refuses an x or y that it records."""
     raw = _pair(adapters, rows, stream)
     _unrecorded(x, y)
     dev = adapters.device
@@ -484,7 +486,8 @@ def adapter_backward(x: torch.Tensor, dy: torch.Tensor, low: torch.Tensor,
                      stream=None) -> None:
     """The backward pass of adapter_forward: dx[t] += the adapter's part (dx holds the shared
     projection's part; None: not wanted), in place, and the gradients given to the set are
-    written, or with accumulate=True added to.  low is the forward pass's."""
+    written, or with accumulate=True added to.  low is the forward pass's; `rows.status` tells of a
+    kernel that gave up."""
     raw = _pair(adapters, rows, stream)
     _unrecorded(dy, dy if dx is None else dx)
     dev = adapters.device

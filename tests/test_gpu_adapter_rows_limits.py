@@ -37,3 +37,39 @@ def test_counts_past_32_bits_are_refused():
             bd.AdamWBatch([small], [small.clone()], step=step)
     del wide, tall
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("k,rows", [(257, 300), (700, 5000), (700, 3), (65535, 4000)])
+def test_more_adapters_than_threads(k, rows):
+    """Adapters of rank 1 whose factors are small whole numbers: every product is exact in FP32, and
+    whole numbers below 256 in BF16, so that the results are equal to the formula's."""
+    rng = np.random.default_rng(k + rows)
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+
+    def whole(*shape):
+        return torch.randint(-2, 3, shape, generator=gen, device="cuda").bfloat16()
+
+    x, y, downs, ups = whole(rows, 16), whole(rows, 8), whole(k, 1, 16), whole(k, 8, 1)
+    x[:, 8:] = 0     # low is at most 32
+    d_downs, d_ups = torch.full((k, 1, 16), 9.0, device="cuda"), torch.full((k, 8, 1), 9.0, device="cuda")
+    s = bd.AdapterSet(list(downs), list(ups), d_downs=list(d_downs), d_ups=list(d_ups))
+    index = torch.from_numpy(rng.integers(-1, k, rows).astype(np.int32)).cuda()
+    index[-1], index[0] = k - 1, 256 if k > 256 else 0
+    plan = bd.AdapterRows(index, k)
+    low = torch.zeros(rows, s.rank, dtype=torch.bfloat16, device="cuda")
+    dy, dx = whole(rows, 8), torch.zeros(rows, 16, dtype=torch.bfloat16, device="cuda")
+    want = y.double()
+    at = index.clamp(min=0).long()
+    has = (index >= 0).double()[:, None]
+    p = (x.double()[:, None, :] * downs[at, 0].double()[:, None, :]).sum(2) * has
+    q = (dy.double() * ups[at, :, 0].double()).sum(1, keepdim=True) * has
+    want += p * ups[at, :, 0].double()
+    bd.adapter_forward(x, y, s, plan, low=low)
+    bd.adapter_backward(x, dy, low, dx, s, plan)
+    assert int(plan.status.item()) == bd.OK
+    assert torch.equal(y.double(), want)
+    assert torch.equal(dx.double(), q * downs[at, 0].double())
+    ga, gb = torch.zeros(k, 16, dtype=torch.double, device="cuda"), torch.zeros(k, 8, dtype=torch.double, device="cuda")
+    ga.index_add_(0, at, q * x.double())
+    gb.index_add_(0, at, p * dy.double())
+    assert torch.equal(d_downs[:, 0].double(), ga) and torch.equal(d_ups[:, :, 0].double(), gb)

@@ -466,7 +466,9 @@ __device__ __forceinline__ void update2(const Rates& R, float keep, float2 g, fl
   }
   p = fma2(p, both(keep), mul2(both(R.rate), q));
 }
-// x / scale, rounded once: the product with the reciprocal, put right by its remainder
+// x / scale, rounded once: the product with the (correctly rounded) reciprocal, put right by its
+// remainder, which one fused operation gives exactly (P. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990; the root in m_codes likewise)
 __device__ __forceinline__ float2 ratio2(float2 x, float scale, float inv) {
   const float2 q = mul2(x, both(inv));
   return fma2(fma2(q, both(-scale), x), both(inv), q);

@@ -168,8 +168,10 @@ BD_API int bo_adamw_moments(const bo_adamw* h, uint32_t dtype, void* d_m, void* 
  * what that cut off.  An infinity in x, dy, y or dx gives what the formula gives for its row, and a
  * low beyond BF16's largest number counts as infinity; an infinity in a factor gives infinity or NaN
  * where it enters.
- * Results do not depend on which other rows are in the batch's tiles, and the order of every sum
- * is fixed for given sizes.
+ * A row's result does not depend on which other rows are in the batch, nor on their order.  It may
+ * depend on the numbers of rows and adapters, which choose the form (low in one BF16 number or in
+ * two) and where its sums are cut: batches of other sizes can differ in the last bits.  Every sum has
+ * one order for given numbers of rows of each adapter, so that the same call repeats its results.
  *
  * x, y, dy, dx: rows of BF16 with a row stride in elements; any sizes and strides (16-byte
  * aligned rows, with hidden and out multiples of 8, take wide accesses). */

@@ -1349,7 +1349,8 @@ int apply(uint32_t RP, const bo_adapter_rows* R, ApplyArgs& P, int sms, cudaStre
     }
   }
   // Tiles of 16 rows have the shorter way to a result, tiles of 64 read the factors less often and
-  // carry less in registers (us, tiles of 16 / of 64):
+  // carry less in registers.  Measured at two widths (us, tiles of 16 / of 64; the bounds are where most
+  // of these change sides, and miss by up to 6% beside them: rank 64, 512 rows of 8):
   //   rank 16, 4096 x 4096:   16 rows of 16 adapters 5.1 / 8.8, 512 of 8 6.1 / 8.0, 1024 of 8 9.3 / 10.6,
   //                           1024 of 64 9.7 / 15.0, 2048 of 64 19.9 / 18.6
   //   rank 64, 4096 x 11008:  64 of 1 11.7 / 17.8, 64 of 64 31.6 / 41.4, 256 of 32 22.6 / 26.3,

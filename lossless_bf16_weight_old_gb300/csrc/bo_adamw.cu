@@ -512,7 +512,7 @@ __device__ __forceinline__ uint32_t low_bytes(float2 a, float2 b) {
 
 // One warp per block of 256: its eight elements a lane stay in registers while the block's
 // maxima are found, so each byte is read and written once.  202M elements (BF16 gradients, FP32
-// master) take 605 us, 5.3 TB/s: 84 instructions an element keep the FP32 pipes busy, and HBM is
+// master) take 605 us, 5.3 TB/s: 85 instructions an element keep the FP32 pipes busy, and HBM is
 // not the bound.  Four blocks an SM at 64 registers: three have room for more and take 775 us.
 // Fetching the next chunk ahead through shared memory does not help either (711 us, of BF16
 // weights 134 us for 40M elements with and without).

@@ -12,11 +12,18 @@
  *   that all requests share.  The factors are read where they lie, so a delta applied to them
  *   (bd_decompress) takes effect with the next call.
  *
+ *   Token log probabilities (bo_logprobs_*): what a worker reports beside its answers and a
+ *   trainer's loss is made of, with the distribution's entropy and its top alternatives, and the
+ *   logits' gradient.
+ *
+ *   Routing to experts (bo_routing_*): the experts of each token of a mixture and their weights,
+ *   per-expert counts and the balance loss, and the gradient of the router's logits.
+ *
  * Conventions are those of bf16delta.h: "d_" pointers are device memory and "h_" pointers host
  * memory, all owned by the caller; nothing is allocated; calls are asynchronous on `stream` and
  * never wait for the GPU; the return value (a bd_status) reports argument and launch errors
  * only, and nothing has been enqueued when it is BD_ERR_INVALID_ARG.  Every call may be captured
- * in a CUDA graph.  Handles (bo_adamw, bo_adapter_set, bo_adapter_rows) are plain structs in host
+ * in a CUDA graph.  Handles (bo_adamw, bo_adapter_set, bo_adapter_rows, bo_logprobs, bo_routing) are plain structs in host
  * memory: the caller owns them and may copy or drop them; their fields are the library's.  A handle
  * belongs to the device that was current when it was made; with another one current, calls that
  * take it return BD_ERR_INVALID_ARG.
@@ -265,6 +272,132 @@ BD_API int bo_adapter_backward(const bo_adapter_set* set, const bo_adapter_rows*
                                uint64_t lddy, const uint16_t* d_low, uint16_t* d_dx,
                                uint64_t lddx, int32_t accumulate, void* d_ws, uint64_t ws_bytes,
                                void* stream);
+
+/* --------------------------------------------------------------- token log probabilities
+ *
+ * Row t holds the logits x_j of `vocab` tokens; v is its given token and T its temperature:
+ *   z_j = x_j / T        lp_j = z_j - ln sum_i e^(z_i)        p_j = e^(lp_j)
+ *   logprob = lp_v       entropy H = -sum_j p_j lp_j
+ *   top: the `top` tokens of greatest x_j in order, of equal ones the lowest first, and their lp_j
+ * and, from the gradients g of logprob and h of the entropy,
+ *   dx_j = (g ([j = v] - p_j) - h p_j (lp_j + H)) / T
+ * computed in FP32 from logits of BF16 or FP32; each output is rounded once.
+ *
+ * A row whose token is negative is left out: it is not read, its logprob, entropy and
+ * top_logprobs are 0, its top tokens -1 and its gradient 0.  A token of `vocab` or more, and a
+ * temperature that is not a positive number, make the row's logprob and gradient NaN.  A logit of
+ * -infinity is a token of probability 0, which adds nothing to the entropy.  A row of nothing else
+ * has no distribution: logprob and top_logprobs are -infinity, entropy and gradient 0.  A NaN or
+ * +infinity in a row makes its logprob, entropy and gradient NaN; NaN counts as the greatest among
+ * the top tokens.  Rows whose g and h are both 0 have the gradient 0 and are not read.
+ *
+ * Sums have one order for given sizes and alignment, so the same call repeats its results. */
+
+#define BO_LOGPROBS_MAX_TOP 32u
+#define BO_LOGPROBS_MAX_VOCAB (1u << 24)
+#define BO_LOGPROBS_MAX_ROWS (1u << 28)
+
+/* Results of up to `rows` rows, and what the backward pass takes from the forward one.  Rows behind
+ * those of a call stay as they were. */
+typedef struct bo_logprobs {
+  float* d_logprobs;      /* rows */
+  float* d_entropy;       /* rows; NULL where it was not asked for */
+  float* d_top_logprobs;  /* rows x top */
+  int32_t* d_top_tokens;  /* rows x top */
+  void* d_saved;          /* the library's */
+  uint32_t rows, vocab, top;
+  int32_t device;
+} bo_logprobs;
+
+/* Bytes of device memory (256-byte aligned) for the results; 0 on bad arguments.  top is at most
+ * vocab and BO_LOGPROBS_MAX_TOP; entropy is 0 or 1. */
+BD_API uint64_t bo_logprobs_size(uint32_t rows, uint32_t vocab, uint32_t top, uint32_t entropy);
+
+/* Lays the results out in d_mem and zeroes them (in the stream's order). */
+BD_API int bo_logprobs_init(uint32_t rows, uint32_t vocab, uint32_t top, uint32_t entropy,
+                            void* d_mem, uint64_t mem_bytes, bo_logprobs* h_out, void* stream);
+
+/* Log probabilities of d_tokens (int32 or int64 by token_bytes, 4 or 8) in the first `rows` rows.
+ * d_logits: rows of `vocab` values with a row stride of ld elements.  Strides of tokens and
+ * temperatures are in elements and may be 0.  d_temperature: one number a row, or NULL for
+ * `temperature` throughout (a positive number). */
+BD_API int bo_logprobs_forward(const bo_logprobs* h, const void* d_logits, uint32_t dtype,
+                               uint64_t ld, uint32_t rows, const void* d_tokens,
+                               uint32_t token_bytes, uint64_t token_stride, float temperature,
+                               const float* d_temperature, uint64_t temperature_stride,
+                               void* stream);
+
+/* The logits' gradient for the forward call before it on this handle, over the same logits and no
+ * more rows than it had: written to d_grad_logits, of the logits' type, with a row stride of ld_grad
+ * elements.  That may be the logits themselves (with the same stride), which the gradient then takes
+ * the place of, but may not overlap anything else of the call.  Of d_grad_logprobs and d_grad_entropy
+ * one may be NULL (0 throughout); strides in elements, 0 for one number for all rows.  d_grad_entropy
+ * needs a handle with entropy. */
+BD_API int bo_logprobs_backward(const bo_logprobs* h, const void* d_logits, uint32_t dtype,
+                                uint64_t ld, uint32_t rows, const float* d_grad_logprobs,
+                                uint64_t grad_logprobs_stride, const float* d_grad_entropy,
+                                uint64_t grad_entropy_stride, void* d_grad_logits,
+                                uint64_t ld_grad, void* stream);
+
+/* -------------------------------------------------------------------- routing to experts
+ *
+ * Token t's router logits x_e over `experts` experts:
+ *   p = softmax(x)       the k experts of greatest x_e in order, of equal ones the lowest first
+ *   weight of the i-th chosen:  w_i = p_i, or normalized  w_i = p_i / (sum over the chosen)
+ *   n_e: tokens that chose e;  N: tokens;  f_e = n_e / (N k);  P_e = (sum over tokens of p_e) / N
+ *   balance loss L = experts * sum_e f_e P_e     (1 when all are alike)
+ * and, from the gradients of the weights and of L (n_e has none, so dL/dp_te = experts f_e / N),
+ * the gradient of x.  Computed in FP32 from logits of BF16 or FP32; each output is rounded once.
+ *
+ * Tokens that the mask leaves out, and tokens whose logits are all -infinity, are not counted: their
+ * experts are -1, their weights and gradients 0.  A single logit of -infinity is an expert of
+ * probability 0, chosen only where fewer than k others are left.  A NaN or +infinity makes the
+ * token's weights and gradient NaN, and with them P and L; NaN counts as the greatest.
+ *
+ * Sums have one order for given sizes, so the same call repeats its results. */
+
+#define BO_ROUTING_MAX_EXPERTS 1024u
+#define BO_ROUTING_MAX_K 32u
+#define BO_ROUTING_MAX_TOKENS (1u << 28)
+
+/* Results of up to `tokens` tokens.  Weights and experts of tokens behind those of a call stay as
+ * they were. */
+typedef struct bo_routing {
+  float* d_weights;       /* tokens x k */
+  int32_t* d_experts;     /* tokens x k */
+  int32_t* d_counts;      /* n: experts */
+  float* d_probs;         /* P: experts */
+  float* d_loss;          /* L */
+  int32_t* d_real;        /* N */
+  void* d_partials;       /* the library's */
+  uint32_t tokens, experts, k, normalize;
+  int32_t device;
+} bo_routing;
+
+/* Bytes of device memory (256-byte aligned) for the results; 0 on bad arguments.  k is at most
+ * experts and BO_ROUTING_MAX_K. */
+BD_API uint64_t bo_routing_size(uint32_t tokens, uint32_t experts, uint32_t k);
+
+/* Lays the results out in d_mem and zeroes them (in the stream's order).  normalize is 0 or 1. */
+BD_API int bo_routing_init(uint32_t tokens, uint32_t experts, uint32_t k, uint32_t normalize,
+                           void* d_mem, uint64_t mem_bytes, bo_routing* h_out, void* stream);
+
+/* Routes the first `tokens` tokens.  d_logits: rows of `experts` values with a row stride of ld
+ * elements.  d_mask: NULL, or a byte per token, 0 to leave it out, with a stride in bytes. */
+BD_API int bo_routing_forward(const bo_routing* h, const void* d_logits, uint32_t dtype,
+                              uint64_t ld, uint32_t tokens, const uint8_t* d_mask,
+                              uint64_t mask_stride, void* stream);
+
+/* The logits' gradient for the forward call before it on this handle, over the same logits and no
+ * more tokens than it had.  d_grad_weights: the weights' gradients (NULL: 0), with strides in
+ * elements of tokens and of choices, which may be 0.  The gradient of L is *d_grad_loss, or
+ * grad_loss where that is NULL.  d_counts: n to take in place of the handle's (NULL), as of several
+ * batches together; f is n over its sum.  d_grad_logits: as in bo_logprobs_backward. */
+BD_API int bo_routing_backward(const bo_routing* h, const void* d_logits, uint32_t dtype,
+                               uint64_t ld, uint32_t tokens, const float* d_grad_weights,
+                               uint64_t grad_stride, uint64_t grad_choice_stride, float grad_loss,
+                               const float* d_grad_loss, const int32_t* d_counts,
+                               void* d_grad_logits, uint64_t ld_grad, void* stream);
 
 /* Library utility: static description of a status, bd_status included. */
 BD_API const char* bo_status_string(int code);

@@ -19,8 +19,8 @@ from typing import Sequence
 import torch
 
 from . import _lib
-from .ops import (AdamWBatch, AdapterRows, AdapterSet, OpsError, SKIPPED_NONFINITE,
-                  adapter_backward, adapter_forward, ops_status_name)
+from .ops import (AdamWBatch, AdapterRows, AdapterSet, ExpertRouting, OpsError, SKIPPED_NONFINITE,
+                  TokenLogprobs, adapter_backward, adapter_forward, ops_status_name)
 
 OK, ERR_INVALID_ARG, ERR_CAPACITY, ERR_FORMAT, ERR_CHECKSUM, ERR_CUDA, ERR_BASE = range(7)
 FORMAT_NAME = "bf16_xor_v1"
@@ -34,7 +34,7 @@ __all__ = [
     "compress_bound", "compress_workspace_size", "decompress_workspace_size", "payload_info",
     "DeltaError", "status_name", "MappedHostBuffer", "StreamedDecompressBatch",
     "AdamWBatch", "AdapterSet", "AdapterRows", "adapter_forward", "adapter_backward",
-    "SKIPPED_NONFINITE", "OpsError", "ops_status_name",
+    "TokenLogprobs", "ExpertRouting", "SKIPPED_NONFINITE", "OpsError", "ops_status_name",
 ]
 
 

@@ -52,6 +52,18 @@ class AdapterRows(ctypes.Structure):
                 ("rows", c_u32), ("k", c_u32), ("device", c_int)]
 
 
+class Logprobs(ctypes.Structure):
+    _fields_ = [("d_logprobs", c_p), ("d_entropy", c_p), ("d_top_logprobs", c_p),
+                ("d_top_tokens", c_p), ("d_saved", c_p), ("rows", c_u32), ("vocab", c_u32),
+                ("top", c_u32), ("device", c_int)]
+
+
+class Routing(ctypes.Structure):
+    _fields_ = [("d_weights", c_p), ("d_experts", c_p), ("d_counts", c_p), ("d_probs", c_p),
+                ("d_loss", c_p), ("d_real", c_p), ("d_partials", c_p), ("tokens", c_u32),
+                ("experts", c_u32), ("k", c_u32), ("normalize", c_u32), ("device", c_int)]
+
+
 # name -> (restype, argtypes); must match include/ops/bf16ops.h
 SIGNATURES = {
     "bo_adamw_plan_size": (c_u64, [c_p, c_u32]),
@@ -69,6 +81,17 @@ SIGNATURES = {
     "bo_adapter_backward_workspace_size": (c_u64, [c_p, c_u32]),
     "bo_adapter_backward": (c_int, [c_p, c_p, c_p, c_u64, c_p, c_u64, c_p, c_p, c_u64, c_int, c_p,
                                     c_u64, c_p]),
+    "bo_logprobs_size": (c_u64, [c_u32, c_u32, c_u32, c_u32]),
+    "bo_logprobs_init": (c_int, [c_u32, c_u32, c_u32, c_u32, c_p, c_u64, c_p, c_p]),
+    "bo_logprobs_forward": (c_int, [c_p, c_p, c_u32, c_u64, c_u32, c_p, c_u32, c_u64, c_f, c_p, c_u64,
+                                    c_p]),
+    "bo_logprobs_backward": (c_int, [c_p, c_p, c_u32, c_u64, c_u32, c_p, c_u64, c_p, c_u64, c_p, c_u64,
+                                     c_p]),
+    "bo_routing_size": (c_u64, [c_u32, c_u32, c_u32]),
+    "bo_routing_init": (c_int, [c_u32, c_u32, c_u32, c_u32, c_p, c_u64, c_p, c_p]),
+    "bo_routing_forward": (c_int, [c_p, c_p, c_u32, c_u64, c_u32, c_p, c_u64, c_p]),
+    "bo_routing_backward": (c_int, [c_p, c_p, c_u32, c_u64, c_u32, c_p, c_u64, c_u64, c_f, c_p, c_p,
+                                    c_p, c_u64, c_p]),
     "bo_status_string": (ctypes.c_char_p, [c_int]),
 }
 

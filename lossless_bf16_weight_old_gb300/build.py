@@ -20,7 +20,7 @@ OPS_LIB = os.path.join(PKG, "libbf16ops.so")
 
 SOURCES = ["bd_api.cu", "bd_encode.cu", "bd_scan.cu", "bd_apply.cu", "bd_checksum.cu",
            "bd_noalloc.cu"]
-OPS_SOURCES = ["bo_adamw.cu", "bo_adapter.cu", "bo_adapter_tc.cu"]
+OPS_SOURCES = ["bo_adamw.cu", "bo_adapter.cu", "bo_adapter_tc.cu", "bo_logprobs.cu", "bo_routing.cu"]
 LIBRARIES = {LIB: SOURCES, OPS_LIB: OPS_SOURCES}
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",

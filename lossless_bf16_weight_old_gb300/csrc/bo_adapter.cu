@@ -1415,25 +1415,6 @@ bool valid(const bo_adapter_rows* r) {
 bool wide(const void* p, uint64_t ld, uint64_t width) {
   return aligned(p, 16) && ld % 8 == 0 && width % 8 == 0;
 }
-// Memory of `rows` rows, in bytes.
-struct Region {
-  uint64_t at, ld, width, rows;
-  bool write = false;
-  Region() = default;
-  Region(const void* p, uint64_t n, uint64_t stride, uint64_t columns, uint64_t size = 2)
-      : at(reinterpret_cast<uintptr_t>(p)), ld(stride * size), width(columns * size), rows(p ? n : 0) {}
-  uint64_t end() const { return rows ? at + (rows - 1) * ld + width : at; }
-};
-// Whether two of them have a byte in common.  Rows of the same stride may lie between one another's
-// (columns of one buffer); of different strides they may not.
-bool meet(const Region& a, const Region& b) {
-  if (a.rows == 0 || b.rows == 0 || a.at >= b.end() || b.at >= a.end()) return false;
-  if (a.at > b.at) return meet(b, a);
-  if (a.rows == 1 || (b.rows > 1 && a.ld != b.ld)) return true;
-  // b begins `off` bytes into row `skip` of a, which is not past a's last
-  const uint64_t skip = (b.at - a.at) / a.ld, off = (b.at - a.at) % a.ld;
-  return off < a.width || (skip + 1 < a.rows && off + b.width > a.ld);
-}
 // Whether a set's gradients lie apart from one another and from its factors.  Sorts the regions.  Of
 // matrices that lie between one another's rows every pair is looked at, a few million at most (all
 // of 65535 adapters' factors as columns of one buffer would take a minute).

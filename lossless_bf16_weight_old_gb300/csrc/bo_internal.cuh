@@ -35,6 +35,25 @@ inline bool disjoint(Span* s, size_t n) {
   }
   return true;
 }
+// Memory of `rows` rows, in bytes.
+struct Region {
+  uint64_t at, ld, width, rows;
+  bool write = false;
+  Region() = default;
+  Region(const void* p, uint64_t n, uint64_t stride, uint64_t columns, uint64_t size = 2)
+      : at(reinterpret_cast<uintptr_t>(p)), ld(stride * size), width(columns * size), rows(p ? n : 0) {}
+  uint64_t end() const { return rows ? at + (rows - 1) * ld + width : at; }
+};
+// Whether two of them have a byte in common.  Rows of the same stride may lie between one another's
+// (columns of one buffer); of different strides they may not.
+inline bool meet(const Region& a, const Region& b) {
+  if (a.rows == 0 || b.rows == 0 || a.at >= b.end() || b.at >= a.end()) return false;
+  if (a.at > b.at) return meet(b, a);
+  if (a.rows == 1 || (b.rows > 1 && a.ld != b.ld)) return true;
+  // b begins `off` bytes into row `skip` of a, which is not past a's last
+  const uint64_t skip = (b.at - a.at) / a.ld, off = (b.at - a.at) % a.ld;
+  return off < a.width || (skip + 1 < a.rows && off + b.width > a.ld);
+}
 inline uint64_t up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
 inline int check(cudaError_t e) { return e == cudaSuccess ? BD_OK : BD_ERR_CUDA; }
 

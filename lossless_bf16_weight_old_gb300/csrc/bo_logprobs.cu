@@ -1,0 +1,656 @@
+// bo_logprobs.cu -- log probabilities of given tokens with entropy and top alternatives, and the
+// logits' gradient (include/ops/bf16ops.h has the formulas).
+//
+// A row is read once, in windows of 64 bytes that are aligned whatever the row's own alignment is:
+// the first and the last may lie partly outside the row, and are read by the element.
+#include <cfloat>
+#include <cmath>
+#include <cooperative_groups.h>
+
+#include "bo_internal.cuh"
+
+namespace bo {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
+constexpr uint32_t kWindow = 64;                 // bytes
+constexpr uint32_t kSegment = kThreads * 32;     // windows whose maxima are kept at once
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+// What the backward pass takes from the forward one, of each row.
+struct alignas(32) Saved {
+  float max;       // of the logits
+  float log2_sum;  // of 2^((x - max) scale)
+  float entropy;
+  float inv_t;     // 1 / T; NaN for a row without a valid token or temperature
+  int32_t token;   // -1: the gradient is 0
+  int32_t pad[3];
+};
+static_assert(sizeof(Saved) == 32, "one sector");
+
+struct ScoreArgs {
+  const uint8_t* x;
+  uint64_t ld;            // bytes
+  const uint8_t* tokens;
+  uint64_t token_stride;  // bytes
+  const float* temps;     // may be NULL
+  uint64_t temp_stride;   // elements
+  float temp;
+  uint32_t token_bytes, rows, vocab, top;
+  float* logprobs;
+  float* entropy;
+  float* top_logprobs;
+  int32_t* top_tokens;
+  Saved* saved;
+};
+
+struct GradArgs {
+  const uint8_t* x;
+  uint64_t ld;            // bytes
+  uint8_t* dx;
+  uint64_t ld_dx;         // bytes
+  const float* g;
+  uint64_t g_stride;
+  const float* h;
+  uint64_t h_stride;
+  uint32_t rows, vocab, pieces;
+  const Saved* saved;
+};
+
+__device__ __forceinline__ float ex2(float x) {   // 2^x, 0 below 2^-126
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void ld32(uint32_t (&w)[8], const void* p) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
+                 "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+template <bool F32>
+__device__ __forceinline__ float element(const uint8_t* p) {
+  return F32 ? *reinterpret_cast<const float*>(p)
+             : __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(p) << 16);
+}
+
+// The windows of a row.
+template <bool F32>
+struct Windows {
+  static constexpr uint32_t kSize = F32 ? 4 : 2, kElems = kWindow / kSize;
+  const uint8_t* row;
+  const uint8_t* base;   // of the first window
+  uint32_t off, count;   // elements of the first window that lie before the row; windows
+  uint32_t vocab;
+  __device__ __forceinline__ Windows(const uint8_t* r, uint32_t v) : row(r), vocab(v) {
+    const uint32_t skip = (uint32_t)(reinterpret_cast<uintptr_t>(r) & (kWindow - 1));
+    base = r - skip;
+    off = skip / kSize;
+    count = (uint32_t)(((uint64_t)off + v + kElems - 1) / kElems);
+  }
+  // the row's element that begins window w (negative or past its end: outside)
+  __device__ __forceinline__ int32_t first(uint32_t w) const { return (int32_t)(w * kElems) - (int32_t)off; }
+  __device__ __forceinline__ bool whole(uint32_t w) const {
+    return first(w) >= 0 && first(w) + kElems <= vocab;
+  }
+  // the window's words; -infinity outside the row
+  __device__ __forceinline__ void load(uint32_t w, uint32_t (&lo)[8], uint32_t (&hi)[8]) const {
+    if (whole(w)) {
+      const uint8_t* p = base + (uint64_t)w * kWindow;
+      ld32(lo, p);
+      ld32(hi, p + 32);
+      return;
+    }
+    const int32_t e0 = first(w);
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      uint32_t v;
+      if (F32) {
+        const int32_t e = e0 + i;
+        v = e >= 0 && e < (int32_t)vocab ? __float_as_uint(element<true>(row + (int64_t)e * 4)) : 0xFF800000u;
+      } else {
+        const int32_t e = e0 + 2 * i;
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+        v = e >= 0 && e < (int32_t)vocab ? p[e] : 0xFF80u;
+        v |= (e + 1 >= 0 && e + 1 < (int32_t)vocab ? (uint32_t)p[e + 1] : 0xFF80u) << 16;
+      }
+      if (i < 8) lo[i] = v; else hi[i - 8] = v;
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------- online softmax
+// Of the values so far: their maximum, the sum of e = 2^d over d = (x - max) scale, and the sum of
+// e d, in four parts each.  The maximum starts at the lowest finite number, so that -infinity has
+// e = 0; d is kept above -200, where e is 0 too, so that e d is 0 and not NaN.
+template <bool ENT>
+struct Sums {
+  float max = -FLT_MAX;
+  float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  float2 t[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+
+  __device__ __forceinline__ void raise(float to, float scale) {
+    if (!(to > max)) return;   // (a NaN raises nothing: its own e is NaN)
+    const float d = fmaxf((max - to) * scale, -200.f), f = ex2(d);
+    max = to;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      if (ENT) t[i] = make_float2(f * fmaf(s[i].x, d, t[i].x), f * fmaf(s[i].y, d, t[i].y));
+      s[i] = make_float2(f * s[i].x, f * s[i].y);
+    }
+  }
+  __device__ __forceinline__ void add(float2 x, float scale, int i) {
+    float2 d = __fmul2_rn(__fadd2_rn(x, make_float2(-max, -max)), make_float2(scale, scale));
+    d = make_float2(max_nan(d.x, -200.f), max_nan(d.y, -200.f));
+    const float2 e = make_float2(ex2(d.x), ex2(d.y));
+    s[i] = __fadd2_rn(s[i], e);
+    if (ENT) t[i] = __ffma2_rn(e, d, t[i]);
+  }
+};
+template <bool F32>
+__device__ __forceinline__ float window_max(const uint32_t (&lo)[8], const uint32_t (&hi)[8]) {
+  if (F32) {
+    float m[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) m[i] = max_nan(__uint_as_float(lo[i]), __uint_as_float(hi[i]));
+#pragma unroll
+    for (int n = 4; n; n >>= 1)
+#pragma unroll
+      for (int i = 0; i < n; i++) m[i] = max_nan(m[i], m[i + n]);
+    return m[0];
+  }
+  uint32_t m[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) m[i] = max_bf16x2(lo[i], hi[i]);
+#pragma unroll
+  for (int n = 4; n; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; i++) m[i] = max_bf16x2(m[i], m[i + n]);
+  return max_nan(bf16_lo(m[0]), bf16_hi(m[0]));
+}
+template <bool F32, bool ENT>
+__device__ __forceinline__ void add_window(Sums<ENT>& a, const uint32_t (&lo)[8], const uint32_t (&hi)[8],
+                                           float scale) {
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    if (F32) {
+      const uint32_t* w = i < 4 ? lo : hi;
+      const int j = 2 * (i & 3);
+      a.add(make_float2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])), scale, i & 1);
+    } else {
+      a.add(make_float2(bf16_lo(lo[i]), bf16_hi(lo[i])), scale, 0);
+      a.add(make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])), scale, 1);
+    }
+  }
+}
+struct Joined {
+  float max, s, t;
+  __device__ __forceinline__ void join(const Joined& o, float scale) {
+    const float m = fmaxf(max, o.max);
+    const float da = fmaxf((max - m) * scale, -200.f), db = fmaxf((o.max - m) * scale, -200.f);
+    const float fa = max == m ? 1.f : ex2(da), fb = o.max == m ? 1.f : ex2(db);
+    t = (max == m ? t : fa * fmaf(s, da, t)) + (o.max == m ? o.t : fb * fmaf(o.s, db, o.t));
+    s = fa * s + fb * o.s;
+    max = m;
+  }
+};
+
+// ------------------------------------------------------------------------------- top tokens
+// A key orders values and, of equal ones, places (the lowest first); 0 is below every key.
+typedef unsigned long long Key;
+__device__ __forceinline__ uint32_t order_of(float x) {
+  if (x != x) return 0xFFFFFFFFu;
+  const uint32_t u = __float_as_uint(x + 0.f);   // (-0 is 0)
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ Key key_of(uint32_t order, uint32_t place) {
+  return (Key)order << 32 | (uint32_t)~place;
+}
+__device__ __forceinline__ uint32_t place_of(Key k) { return ~(uint32_t)k; }
+
+__device__ __forceinline__ Key step(Key v, uint32_t stride, bool keep_max) {
+  const Key o = __shfl_xor_sync(0xffffffffu, v, stride);
+  return (v > o) == keep_max ? v : o;
+}
+// the lanes' keys in descending order
+__device__ __forceinline__ Key sorted(Key v, uint32_t lane) {
+#pragma unroll
+  for (uint32_t size = 2; size <= 32; size *= 2)
+#pragma unroll
+    for (uint32_t stride = size / 2; stride; stride /= 2)
+      v = step(v, stride, ((lane & stride) == 0) == ((lane & size) == 0));
+  return v;
+}
+// the 32 greatest of two descending lists, in descending order; b reversed: lane 31 - i has its i-th
+__device__ __forceinline__ Key merged_reversed(Key a, Key b, uint32_t lane) {
+  Key v = a > b ? a : b;
+#pragma unroll
+  for (uint32_t stride = 16; stride; stride /= 2) v = step(v, stride, (lane & stride) == 0);
+  return v;
+}
+__device__ __forceinline__ Key merged(Key a, Key b, uint32_t lane) {
+  return merged_reversed(a, __shfl_sync(0xffffffffu, b, 31 - lane), lane);
+}
+// The warps' lists joined in lists[0].
+__device__ __forceinline__ void join_lists(Key mine, Key (*lists)[32], uint32_t warp, uint32_t lane) {
+  lists[warp][lane] = mine;
+  __syncthreads();
+  for (uint32_t half = kWarps / 2; half; half /= 2) {
+    if (warp < half) {
+      mine = merged_reversed(mine, lists[warp + half][31 - lane], lane);
+      lists[warp][lane] = mine;
+    }
+    __syncthreads();
+  }
+}
+
+// Of a segment of windows [w0, w1) with the maxima's order in maxima[], its 32 greatest elements in
+// lists[0].  The k greatest elements lie in the k windows with the greatest maxima (each of those
+// that precede an element's window has one that precedes the element), and those windows are among
+// the windows of the k threads with the greatest maxima.  best: this thread's greatest window key.
+template <bool F32>
+__device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top,
+                                            Key best, const uint32_t* maxima, Key (*lists)[32],
+                                            uint32_t warp, uint32_t lane) {
+  join_lists(sorted(best, lane), lists, warp, lane);   // (its barrier: the maxima are there)
+  Key mine = 0;
+  for (uint32_t i = warp; i < top; i += kWarps) {
+    const Key k = lists[0][i];
+    if (!k) break;
+    const uint32_t w = (place_of(k) - w0) % kThreads + lane * kThreads;   // the thread's windows
+    const Key v = w0 + w < w1 ? key_of(maxima[w], w0 + w) : 0;
+    mine = merged(mine, sorted(v, lane), lane);
+  }
+  __syncthreads();
+  join_lists(mine, lists, warp, lane);
+  mine = 0;
+  for (uint32_t i = warp; i < top; i += kWarps) {
+    const Key k = lists[0][i];
+    if (!k) break;
+    Key v = 0;
+    if (lane < Windows<F32>::kElems) {
+      const int32_t e = W.first(place_of(k)) + (int32_t)lane;
+      if (e >= 0 && e < (int32_t)W.vocab)
+        v = key_of(order_of(element<F32>(W.row + (int64_t)e * Windows<F32>::kSize)), (uint32_t)e);
+    }
+    mine = merged(mine, sorted(v, lane), lane);
+  }
+  __syncthreads();
+  join_lists(mine, lists, warp, lane);
+}
+
+// ------------------------------------------------------------------------------ forward pass
+// The blocks of a cluster share a row: each takes its part of the windows, and the first one joins
+// their sums and lists.
+template <bool F32, bool ENT, bool TOP>
+__global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs P) {
+  extern __shared__ uint32_t maxima[];
+  __shared__ Key lists[kWarps + 1][32];   // the last one: of the segments so far
+  __shared__ Joined parts[kWarps];
+  after_previous();
+  const cg::cluster_group cluster = cg::this_cluster();
+  const uint32_t C = cluster.num_blocks(), c = cluster.block_rank();
+  const uint32_t row = blockIdx.x / C, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint8_t* at = P.tokens + row * P.token_stride;
+  const int64_t token = P.token_bytes == 8 ? *reinterpret_cast<const int64_t*>(at)
+                                           : *reinterpret_cast<const int32_t*>(at);
+  if (token < 0) {   // (the whole cluster)
+    if (c == 0) {
+      if (threadIdx.x == 0) {
+        P.logprobs[row] = 0.f;
+        if (P.entropy) P.entropy[row] = 0.f;
+        P.saved[row].token = -1;
+      }
+      if (TOP && threadIdx.x < P.top) {
+        P.top_logprobs[(uint64_t)row * P.top + threadIdx.x] = 0.f;
+        P.top_tokens[(uint64_t)row * P.top + threadIdx.x] = -1;
+      }
+    }
+    return;
+  }
+  const float temp = P.temps ? P.temps[row * P.temp_stride] : P.temp;
+  const float inv_t = temp > 0.f && temp <= FLT_MAX ? 1.f / temp : __int_as_float(0x7FFFFFFF);
+  const float scale = inv_t * kLog2e;
+  const Windows<F32> W(P.x + row * P.ld, P.vocab);
+  const uint32_t begin = (uint32_t)((uint64_t)W.count * c / C), end = (uint32_t)((uint64_t)W.count * (c + 1) / C);
+
+  Sums<ENT> a;
+  if (TOP && warp == 0) lists[kWarps][lane] = 0;
+  for (uint32_t w0 = begin; w0 < end; w0 += kSegment) {
+    const uint32_t w1 = TOP ? min(end, w0 + kSegment) : end;
+    Key best = 0;
+    for (uint32_t w = w0 + threadIdx.x; w < w1; w += kThreads) {
+      uint32_t lo[8], hi[8];
+      W.load(w, lo, hi);
+      const float m = window_max<F32>(lo, hi);
+      if (TOP) {
+        const uint32_t o = order_of(m);
+        maxima[w - w0] = o;
+        const Key k = key_of(o, w);
+        best = best > k ? best : k;
+      }
+      a.raise(m, scale);
+      add_window<F32, ENT>(a, lo, hi, scale);
+    }
+    if (!TOP) break;
+    segment_top<F32>(W, w0, w1, P.top, best, maxima, lists, warp, lane);
+    if (warp == 0) {
+      const Key v = merged(lists[kWarps][lane], lists[0][lane], lane);
+      lists[kWarps][lane] = v;
+    }
+    __syncthreads();
+  }
+
+  Joined j{a.max, (a.s[0].x + a.s[0].y) + (a.s[1].x + a.s[1].y), (a.t[0].x + a.t[0].y) + (a.t[1].x + a.t[1].y)};
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    Joined o{__shfl_xor_sync(0xffffffffu, j.max, d), __shfl_xor_sync(0xffffffffu, j.s, d),
+             __shfl_xor_sync(0xffffffffu, j.t, d)};
+    j.join(o, scale);
+  }
+  if (lane == 0) parts[warp] = j;
+  __syncthreads();
+  if (C > 1) cluster.sync();
+  if (c == 0 && warp == 0) {
+    j = Joined{-FLT_MAX, 0.f, 0.f};
+    Key best = 0;
+    for (uint32_t b = 0; b < C; b++) {
+      const Joined* p = C > 1 ? cluster.map_shared_rank(parts, b) : parts;
+      for (uint32_t i = 0; i < kWarps; i++) j.join(p[i], scale);
+      if (TOP) {
+        const Key* l = C > 1 ? cluster.map_shared_rank(&lists[kWarps][0], b) : lists[kWarps];
+        best = merged(best, l[lane], lane);
+      }
+    }
+    const bool empty = j.s == 0.f;             // nothing but -infinity
+    const float inf = __int_as_float(0x7F800000), nan = __int_as_float(0x7FFFFFFF);
+    const float log_sum = logf(j.s);
+    const float entropy = empty ? 0.f : log_sum - kLn2 * (j.t / j.s);
+    if (lane == 0) {
+      const bool valid = token < (int64_t)P.vocab;
+      float lp = nan;
+      if (valid) {
+        const float x = element<F32>(W.row + token * Windows<F32>::kSize);
+        lp = empty ? -inf * inv_t : (x - j.max) * inv_t - log_sum;
+      }
+      P.logprobs[row] = lp;
+      if (ENT) P.entropy[row] = entropy;
+      Saved sv = {};
+      sv.max = j.max;
+      sv.log2_sum = log2f(j.s);
+      sv.entropy = entropy;
+      sv.inv_t = valid ? inv_t : nan;
+      sv.token = empty && valid && inv_t == inv_t ? -1 : (int32_t)(valid ? token : 0);
+      P.saved[row] = sv;
+    }
+    if (TOP && lane < P.top) {
+      const float x = value_of((uint32_t)(best >> 32));
+      P.top_logprobs[(uint64_t)row * P.top + lane] = empty ? -inf * inv_t : (x - j.max) * inv_t - log_sum;
+      P.top_tokens[(uint64_t)row * P.top + lane] = (int32_t)place_of(best);
+    }
+  }
+  if (C > 1) cluster.sync();   // (the others' memory is read until here)
+}
+
+// ----------------------------------------------------------------------------- backward pass
+struct RowGrad {
+  float max, scale, log2_sum;   // lp_j = ((x_j - max) scale - log2_sum) ln 2
+  float a, b;                   // dx_j = p_j (a + b log2 p_j) + [j = v] at
+  float at;
+  __device__ __forceinline__ float operator()(float x) const {
+    const float l = max_nan((x - max) * scale - log2_sum, -200.f);
+    return ex2(l) * fmaf(b, l, a);
+  }
+};
+template <bool F32>
+__global__ void __launch_bounds__(kThreads) k_grad(const GradArgs P) {
+  after_previous();
+  const uint32_t row = blockIdx.x / P.pieces, piece = blockIdx.x % P.pieces;
+  const Saved sv = P.saved[row];
+  const float g = P.g ? P.g[row * P.g_stride] : 0.f, h = P.h ? P.h[row * P.h_stride] : 0.f;
+  const Windows<F32> W(P.x + row * P.ld, P.vocab);
+  uint8_t* out = P.dx + row * P.ld_dx;
+  const bool zero = sv.token < 0 || (g == 0.f && h == 0.f);
+  RowGrad R;
+  R.max = sv.max;
+  R.scale = sv.inv_t * kLog2e;
+  R.log2_sum = sv.log2_sum;
+  R.a = -(g + h * sv.entropy) * sv.inv_t;
+  R.b = -h * kLn2 * sv.inv_t;
+  R.at = g * sv.inv_t;
+  const uint32_t w = piece * kThreads + threadIdx.x;
+  if (w >= W.count) return;
+  const int32_t e0 = W.first(w);
+  constexpr uint32_t E = Windows<F32>::kElems, S = Windows<F32>::kSize;
+  if (W.whole(w) && (reinterpret_cast<uintptr_t>(out + (int64_t)e0 * S) & 31) == 0) {
+    uint8_t* o = out + (int64_t)e0 * S;
+    uint32_t q[2][8];
+    const uint32_t v = (uint32_t)(sv.token - e0);   // the token's place, when below E
+    float at = 0.f;
+    if (zero) {
+#pragma unroll
+      for (int i = 0; i < 16; i++) q[i / 8][i % 8] = 0;
+    } else {
+      W.load(w, q[0], q[1]);
+      if (v < E) at = R(element<F32>(W.row + (int64_t)sv.token * S)) + R.at;
+#pragma unroll
+      for (int i = 0; i < 16; i++) {
+        uint32_t& u = q[i / 8][i % 8];
+        u = F32 ? __float_as_uint(R(__uint_as_float(u))) : pack_bf16(R(bf16_lo(u)), R(bf16_hi(u)));
+      }
+    }
+    st32(o, q[0]);
+    st32(o + 32, q[1]);
+    if (!zero && v < E) {
+      if (F32) *reinterpret_cast<float*>(o + v * S) = at;
+      else *reinterpret_cast<uint16_t*>(o + v * S) = (uint16_t)pack_bf16(at, 0.f);
+    }
+    return;
+  }
+  for (uint32_t i = 0; i < E; i++) {
+    const int32_t e = e0 + (int32_t)i;
+    if (e < 0 || e >= (int32_t)P.vocab) continue;
+    float v = 0.f;
+    if (!zero) v = R(element<F32>(W.row + (int64_t)e * S)) + (e == sv.token ? R.at : 0.f);
+    if (F32) reinterpret_cast<float*>(out)[e] = v;
+    else reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)pack_bf16(v, 0.f);
+  }
+}
+
+// --------------------------------------------------------------------------------- host side
+struct Layout {
+  uint64_t logprobs, entropy, top_logprobs, top_tokens, saved, total;
+};
+bool layout(uint32_t rows, uint32_t vocab, uint32_t top, uint32_t entropy, Layout& L) {
+  if (rows > BO_LOGPROBS_MAX_ROWS || vocab == 0 || vocab > BO_LOGPROBS_MAX_VOCAB || top > vocab ||
+      top > BO_LOGPROBS_MAX_TOP || entropy > 1)
+    return false;
+  uint64_t off = 0;
+  auto take = [&](uint64_t bytes) {
+    const uint64_t at = off;
+    off = up(off + bytes, 256);
+    return at;
+  };
+  L.logprobs = take((uint64_t)rows * 4);
+  L.entropy = take(entropy ? (uint64_t)rows * 4 : 0);
+  L.top_logprobs = take((uint64_t)rows * top * 4);
+  L.top_tokens = take((uint64_t)rows * top * 4);
+  L.saved = take((uint64_t)rows * sizeof(Saved));
+  L.total = off ? off : 256;
+  return true;
+}
+bool valid(const bo_logprobs* h) {
+  return h && h->d_logprobs && h->d_saved && h->vocab > 0 && h->vocab <= BO_LOGPROBS_MAX_VOCAB &&
+         h->rows <= BO_LOGPROBS_MAX_ROWS && h->top <= BO_LOGPROBS_MAX_TOP && h->top <= h->vocab &&
+         (h->top == 0 || (h->d_top_logprobs && h->d_top_tokens));
+}
+// The results' memory, from the first to the last byte.
+Region results(const bo_logprobs* h) {
+  Layout L;
+  layout(h->rows, h->vocab, h->top, h->d_entropy != nullptr, L);
+  return Region(h->d_logprobs, 1, 0, L.total, 1);
+}
+// Numbers of `size` bytes, one a row, which may all be the same one.
+Region column(const void* p, uint64_t rows, uint64_t stride, uint64_t size) {
+  return Region(p, stride ? rows : std::min<uint64_t>(rows, 1), stride, 1, size);
+}
+bool matrix(const void* p, uint64_t ld, uint64_t rows, uint64_t width, uint64_t size) {
+  return p && aligned(p, size) && ld <= (1ull << 40) && (rows <= 1 || ld >= width);
+}
+bool strided(const void* p, uint64_t stride, uint64_t size) {
+  return aligned(p, size) && stride <= (1ull << 40);
+}
+
+template <bool F32>
+cudaError_t score(const ScoreArgs& P, uint32_t cluster, cudaStream_t s) {
+  const bool ent = P.entropy != nullptr, top = P.top > 0;
+  auto k = ent ? (top ? k_score<F32, true, true> : k_score<F32, true, false>)
+               : (top ? k_score<F32, false, true> : k_score<F32, false, false>);
+  return launch(k, dim3(P.rows * cluster), kThreads, top ? kSegment * 4 : 0, cluster, s, P);
+}
+
+}  // namespace
+}  // namespace bo
+
+using namespace bo;
+
+extern "C" {
+
+uint64_t bo_logprobs_size(uint32_t rows, uint32_t vocab, uint32_t top, uint32_t entropy) {
+  Layout L;
+  return layout(rows, vocab, top, entropy, L) ? L.total : 0;
+}
+
+int bo_logprobs_init(uint32_t rows, uint32_t vocab, uint32_t top, uint32_t entropy, void* d_mem,
+                     uint64_t mem_bytes, bo_logprobs* h_out, void* stream) {
+  Layout L;
+  if (!h_out || !layout(rows, vocab, top, entropy, L) || !d_mem || !aligned(d_mem, 256) ||
+      mem_bytes < L.total)
+    return BD_ERR_INVALID_ARG;
+  uint8_t* p = static_cast<uint8_t*>(d_mem);
+  bo_logprobs h = {};
+  h.d_logprobs = reinterpret_cast<float*>(p + L.logprobs);
+  h.d_entropy = entropy ? reinterpret_cast<float*>(p + L.entropy) : nullptr;
+  h.d_top_logprobs = reinterpret_cast<float*>(p + L.top_logprobs);
+  h.d_top_tokens = reinterpret_cast<int32_t*>(p + L.top_tokens);
+  h.d_saved = p + L.saved;
+  h.rows = rows;
+  h.vocab = vocab;
+  h.top = top;
+  int rc;
+  if ((rc = check(cudaGetDevice(&h.device)))) return rc;
+  if ((rc = check(cudaMemsetAsync(d_mem, 0, L.total, static_cast<cudaStream_t>(stream))))) return rc;
+  *h_out = h;
+  return BD_OK;
+}
+
+int bo_logprobs_forward(const bo_logprobs* h, const void* d_logits, uint32_t dtype, uint64_t ld,
+                        uint32_t rows, const void* d_tokens, uint32_t token_bytes,
+                        uint64_t token_stride, float temperature, const float* d_temperature,
+                        uint64_t temperature_stride, void* stream) {
+  if (!valid(h) || dtype > BO_FP32 || rows > h->rows || (token_bytes != 4 && token_bytes != 8) ||
+      (!d_temperature && !(temperature > 0.f && temperature <= FLT_MAX)))
+    return BD_ERR_INVALID_ARG;
+  const uint64_t size = dtype == BO_FP32 ? 4 : 2;
+  if (rows > 0) {
+    if (!matrix(d_logits, ld, rows, h->vocab, size) || !d_tokens ||
+        !strided(d_tokens, token_stride, token_bytes) || !strided(d_temperature, temperature_stride, 4))
+      return BD_ERR_INVALID_ARG;
+    const Region out = results(h);
+    if (meet(out, Region(d_logits, rows, ld, h->vocab, size)) ||
+        meet(out, column(d_tokens, rows, token_stride, token_bytes)) ||
+        meet(out, column(d_temperature, rows, temperature_stride, 4)))
+      return BD_ERR_INVALID_ARG;
+  }
+  int sms = 0;
+  if (const int rc = sm_count(h->device, sms)) return rc;
+  if (rows == 0) return BD_OK;
+  ScoreArgs P;
+  P.x = static_cast<const uint8_t*>(d_logits);
+  P.ld = ld * size;
+  P.tokens = static_cast<const uint8_t*>(d_tokens);
+  P.token_stride = token_stride * token_bytes;
+  P.temps = d_temperature;
+  P.temp_stride = temperature_stride;
+  P.temp = temperature;
+  P.token_bytes = token_bytes;
+  P.rows = rows;
+  P.vocab = h->vocab;
+  P.top = h->top;
+  P.logprobs = h->d_logprobs;
+  P.entropy = h->d_entropy;
+  P.top_logprobs = h->d_top_logprobs;
+  P.top_tokens = h->d_top_tokens;
+  P.saved = static_cast<Saved*>(h->d_saved);
+  uint32_t cluster = 1;
+  while (cluster < 8 && (uint64_t)rows * cluster * 2 <= (uint64_t)sms * 4 &&
+         (uint64_t)h->vocab * size >= (uint64_t)cluster * 2 * kThreads * kWindow / 2)
+    cluster *= 2;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return check(dtype == BO_FP32 ? score<true>(P, cluster, s) : score<false>(P, cluster, s));
+}
+
+int bo_logprobs_backward(const bo_logprobs* h, const void* d_logits, uint32_t dtype, uint64_t ld,
+                         uint32_t rows, const float* d_grad_logprobs, uint64_t grad_logprobs_stride,
+                         const float* d_grad_entropy, uint64_t grad_entropy_stride,
+                         void* d_grad_logits, uint64_t ld_grad, void* stream) {
+  if (!valid(h) || dtype > BO_FP32 || rows > h->rows || (d_grad_entropy && !h->d_entropy))
+    return BD_ERR_INVALID_ARG;
+  const uint64_t size = dtype == BO_FP32 ? 4 : 2;
+  if (rows > 0) {
+    if (!matrix(d_logits, ld, rows, h->vocab, size) ||
+        !matrix(d_grad_logits, ld_grad, rows, h->vocab, size) || (!d_grad_logprobs && !d_grad_entropy) ||
+        !strided(d_grad_logprobs, grad_logprobs_stride, 4) || !strided(d_grad_entropy, grad_entropy_stride, 4))
+      return BD_ERR_INVALID_ARG;
+    const Region out(d_grad_logits, rows, ld_grad, h->vocab, size);
+    const bool in_place = d_grad_logits == d_logits && (ld == ld_grad || rows == 1);
+    if ((!in_place && meet(out, Region(d_logits, rows, ld, h->vocab, size))) || meet(out, results(h)) ||
+        meet(out, column(d_grad_logprobs, rows, grad_logprobs_stride, 4)) ||
+        meet(out, column(d_grad_entropy, rows, grad_entropy_stride, 4)))
+      return BD_ERR_INVALID_ARG;
+  }
+  int sms = 0;
+  if (const int rc = sm_count(h->device, sms)) return rc;
+  if (rows == 0) return BD_OK;
+  GradArgs P;
+  P.x = static_cast<const uint8_t*>(d_logits);
+  P.ld = ld * size;
+  P.dx = static_cast<uint8_t*>(d_grad_logits);
+  P.ld_dx = ld_grad * size;
+  P.g = d_grad_logprobs;
+  P.g_stride = grad_logprobs_stride;
+  P.h = d_grad_entropy;
+  P.h_stride = grad_entropy_stride;
+  P.rows = rows;
+  P.vocab = h->vocab;
+  // (one window more than a row fills where it begins inside one)
+  P.pieces = (uint32_t)(((uint64_t)h->vocab * size / kWindow + 2 + kThreads - 1) / kThreads);
+  P.saved = static_cast<const Saved*>(h->d_saved);
+  const uint64_t blocks = (uint64_t)rows * P.pieces;
+  if (blocks > 0x7FFFFFFFull) return BD_ERR_INVALID_ARG;
+  return check(launch(dtype == BO_FP32 ? k_grad<true> : k_grad<false>, dim3((uint32_t)blocks), kThreads, 0,
+                      1, static_cast<cudaStream_t>(stream), P));
+}
+
+}  // extern "C"

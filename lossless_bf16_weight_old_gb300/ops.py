@@ -4,6 +4,10 @@
                       the new weights that CompressBatch encodes
     AdapterSet, AdapterRows, adapter_forward, adapter_backward
                       low-rank adapters of many requests beside a shared projection
+    TokenLogprobs     log probabilities of given tokens with entropy and top alternatives, and
+                      the logits' gradient
+    ExpertRouting     the experts of each token and their weights, per-expert counts and the
+                      balance loss, and the gradient of the router's logits
 
 Every computation runs in libbf16ops' CUDA kernels; this module checks and marshals arguments
 and allocates device buffers with PyTorch.  The names are re-exported by the package.
@@ -28,7 +32,7 @@ _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 _U64 = (1 << 64) - 1
 _current_stream = torch._C._cuda_getCurrentRawStream
 
-__all__ = ["AdamWBatch", "AdapterSet", "AdapterRows", "adapter_forward", "adapter_backward", "SKIPPED_NONFINITE", "OpsError", "ops_status_name"]
+__all__ = ["AdamWBatch", "AdapterSet", "AdapterRows", "adapter_forward", "adapter_backward", "TokenLogprobs", "ExpertRouting", "SKIPPED_NONFINITE", "OpsError", "ops_status_name"]
 
 
 class OpsError(RuntimeError):
@@ -512,3 +516,265 @@ def adapter_backward(x: torch.Tensor, dy: torch.Tensor, low: torch.Tensor,
         ws.data_ptr(), need, raw)
     if rc != OK:
         _failed(rc, "bo_adapter_backward", dev)
+
+
+def _device_of(device) -> torch.device:
+    """The current device, which has to be the one that was asked for."""
+    dev = torch.device("cuda" if device is None else device)
+    if dev.type == "cuda" and dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    _here(dev)
+    return dev
+
+
+class _Results(_Owner):
+    """An object whose one buffer holds the results of its calls."""
+
+    def _memory(self, nbytes: int, device: torch.device) -> torch.Tensor:
+        self._at = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return self._at
+
+    def _part(self, pointer: int | None, dtype: torch.dtype, *shape: int) -> torch.Tensor:
+        """The part of the buffer that begins there."""
+        numel = 1
+        for n in shape:
+            numel *= n
+        if numel == 0 or not pointer:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        at = pointer - self._at.data_ptr()
+        return self._at[at:at + numel * dtype.itemsize].view(dtype).view(shape)
+
+
+def _rows_in(t: torch.Tensor, name: str, most: int, width: int, device: torch.device) -> int:
+    """Checks a matrix of at most `most` rows; returns its row stride."""
+    if t.dim() == 2 and t.device == device and t.dtype in _DTYPES and t.shape[1] == width:
+        rows = t.shape[0]
+        ld, one = t.stride()
+        if rows <= most and (one == 1 or width == 1) and (ld >= width or rows <= 1):
+            return ld if rows > 1 else width
+    if t.dim() != 2 or t.dtype not in _DTYPES or t.device != device:
+        raise ValueError(f"{name} must be a 2-dimensional bfloat16 or float32 tensor on {device}")
+    if t.shape[1] != width or t.shape[0] > most:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (up to {most}, {width})")
+    raise ValueError(f"{name}'s rows must be contiguous and may not overlap")
+
+
+def _column(t: torch.Tensor, name: str, rows: int, dtypes, device: torch.device) -> int:
+    """Checks a vector of one number a row; returns its stride."""
+    if t.dim() != 1 or t.shape[0] != rows or t.device != device or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be a 1-dimensional tensor of {rows} elements of type "
+                         f"{' or '.join(str(d) for d in dtypes)} on {device}")
+    return t.stride(0)
+
+
+def _out_for(out: torch.Tensor | None, t: torch.Tensor, ld: int, device: torch.device,
+             stream) -> tuple[torch.Tensor, int]:
+    """Where the gradient of the logits t goes, and its row stride: `out`, or memory of its own whose
+    rows lie as far apart as the logits' (so that they begin alike)."""
+    rows, width = t.shape
+    if out is None:
+        out = _scratch((rows, ld), t.dtype, device, stream)
+        if stream is not None:   # (the caller may go on with it on the current one)
+            out.record_stream(torch.cuda.current_stream(device))
+        return out[:, :width], ld
+    if out.shape != t.shape or out.dtype != t.dtype:
+        raise ValueError(f"out must have the logits' shape {tuple(t.shape)} and type {t.dtype}")
+    return out, _rows_in(out, "out", rows, width, device)
+
+
+def _unrecorded_logits(t: torch.Tensor) -> None:
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError("autograd records these logits, and would miss the call's part: call under "
+                         "torch.no_grad() or with detached logits, and backward() for the gradient")
+
+
+class TokenLogprobs(_Results):
+    """Log probabilities of given tokens, for up to `rows` rows of logits over `vocab` tokens.
+
+    top       how many alternatives each row gets (at most 32)
+    entropy   also the entropy of each row's distribution (and its gradient)
+    device    the current CUDA device (default)
+
+    Results on the device after `run`, of its rows (those behind them stay as they were):
+    `logprobs` (float32[rows]), `entropy` (float32[rows], or None), `top_logprobs`
+    (float32[rows, top]) and `top_tokens` (int32[rows, top]), the greatest first and of equal ones
+    the lowest token first.  Each run overwrites them: calls at the same time, on several streams or
+    in graphs that run side by side, want an object each.
+
+    Rows whose token is negative are left out and not read: their results are 0, their top tokens -1
+    and their gradients 0.  A token of `vocab` or more makes a row's log probability and gradient
+    NaN, which a clipped AdamWBatch skips.  Logits of -inf are tokens of probability 0."""
+
+    def __init__(self, rows: int, vocab: int, *, top: int = 0, entropy: bool = False, device=None,
+                 stream=None):
+        rows, vocab, top = int(rows), int(vocab), int(top)
+        if not 0 <= rows <= 1 << 28 or not 1 <= vocab <= 1 << 24:
+            raise ValueError("rows must lie in 0 .. 2**28 and vocab in 1 .. 2**24")
+        if not 0 <= top <= min(32, vocab):
+            raise ValueError("top must lie in 0 .. 32 and not exceed vocab")
+        dev = _device_of(device)
+        _stream(stream, dev)
+        lib = _ops_lib.load()
+        self.handle = _ops_lib.Logprobs()
+        with torch.cuda.stream(stream):
+            mem = self._memory(int(lib.bo_logprobs_size(rows, vocab, top, int(bool(entropy)))), dev)
+            _check(lib.bo_logprobs_init(rows, vocab, top, int(bool(entropy)), mem.data_ptr(), mem.numel(),
+                                        ctypes.byref(self.handle), _stream(None, dev)), "bo_logprobs_init")
+            self._made([mem], dev)
+        h = self.handle
+        self.rows, self.vocab, self.top, self._ran = rows, vocab, top, 0
+        self.logprobs = self._part(h.d_logprobs, torch.float32, rows)
+        self.entropy = self._part(h.d_entropy, torch.float32, rows) if entropy else None
+        self.top_logprobs = self._part(h.d_top_logprobs, torch.float32, rows, top)
+        self.top_tokens = self._part(h.d_top_tokens, torch.int32, rows, top)
+        self._ref = ctypes.byref(h)
+        self._forward, self._backward = lib.bo_logprobs_forward, lib.bo_logprobs_backward
+
+    def run(self, logits: torch.Tensor, tokens: torch.Tensor,
+            temperature: float | torch.Tensor = 1.0, stream=None) -> None:
+        """Log probabilities of tokens [n] (int32 or int64) under logits [n, vocab] (bfloat16 or
+        float32, contiguous rows) divided by the temperature: one positive number, or float32[n].
+        Autograd does not see the call, which refuses logits that it records."""
+        raw = self._on(stream)
+        _unrecorded_logits(logits)
+        dev = self.device
+        ld = _rows_in(logits, "logits", self.rows, self.vocab, dev)
+        n = logits.shape[0]
+        step = _column(tokens, "tokens", n, (torch.int64, torch.int32), dev)
+        heat, heats, heat_step = 1.0, None, 0
+        if isinstance(temperature, torch.Tensor):
+            heat_step = _column(temperature, "temperature", n, (torch.float32,), dev)
+            heats = temperature.data_ptr() or None
+        else:
+            heat = float(temperature)
+            if not 0.0 < heat < float("inf"):
+                raise ValueError("temperature must be a positive number")
+        rc = self._forward(self._ref, logits.data_ptr(), _DTYPES[logits.dtype], ld, n, tokens.data_ptr(),
+                           tokens.element_size(), step, heat, heats, heat_step, raw)
+        if rc != OK:
+            _failed(rc, "bo_logprobs_forward", dev)
+        self._ran = n
+
+    def backward(self, logits: torch.Tensor, d_logprobs: torch.Tensor | None,
+                 d_entropy: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+        """The gradient of the last run's logits (the same ones, or their first rows) from those of
+        its log probabilities and entropies (float32[n], either may be None).  Goes to `out`, which
+        may be the logits themselves, or to memory of its own; returns it."""
+        raw = self._on(stream)
+        _unrecorded_logits(logits)
+        dev = self.device
+        ld = _rows_in(logits, "logits", self._ran, self.vocab, dev)
+        n = logits.shape[0]
+        if d_logprobs is None and d_entropy is None:
+            raise ValueError("d_logprobs or d_entropy must be given")
+        if d_entropy is not None and self.entropy is None:
+            raise ValueError("d_entropy needs an object with entropy=True")
+        g = h = None
+        g_step = h_step = 0
+        if d_logprobs is not None:
+            g_step, g = _column(d_logprobs, "d_logprobs", n, (torch.float32,), dev), d_logprobs.data_ptr()
+        if d_entropy is not None:
+            h_step, h = _column(d_entropy, "d_entropy", n, (torch.float32,), dev), d_entropy.data_ptr()
+        out, ld_out = _out_for(out, logits, ld, dev, stream)
+        rc = self._backward(self._ref, logits.data_ptr(), _DTYPES[logits.dtype], ld, n, g, g_step, h, h_step,
+                            out.data_ptr(), ld_out, raw)
+        if rc != OK:
+            _failed(rc, "bo_logprobs_backward", dev)
+        return out
+
+
+class ExpertRouting(_Results):
+    """Routing of up to `tokens` tokens to k of `experts` experts each.
+
+    normalize   divide the chosen experts' weights by their sum (default)
+    device      the current CUDA device (default)
+
+    Results on the device after `run`: `experts` (int32[tokens, k], the likeliest first and of
+    equal ones the lowest first) and `weights` (float32[tokens, k]), of the run's tokens (those
+    behind them stay as they were); over the run's tokens `counts` (int32[experts]), `probs`
+    (float32[experts], mean probabilities), `loss` (float32[1], the balance loss
+    experts * sum(counts / counts.sum() * probs), 1 when all experts are alike) and `real`
+    (int32[1], how many tokens counted).  Each run overwrites them: calls at the same time, on
+    several streams or in graphs that run side by side, want an object each.
+
+    Tokens that the mask leaves out have experts -1 and weights and gradients 0, and count
+    nowhere."""
+
+    def __init__(self, tokens: int, experts: int, k: int, *, normalize: bool = True, device=None,
+                 stream=None):
+        tokens, experts, k = int(tokens), int(experts), int(k)
+        if not 0 <= tokens <= 1 << 28 or not 1 <= experts <= 1024:
+            raise ValueError("tokens must lie in 0 .. 2**28 and experts in 1 .. 1024")
+        if not 1 <= k <= min(32, experts):
+            raise ValueError("k must lie in 1 .. 32 and not exceed experts")
+        dev = _device_of(device)
+        _stream(stream, dev)
+        lib = _ops_lib.load()
+        self.handle = _ops_lib.Routing()
+        with torch.cuda.stream(stream):
+            mem = self._memory(int(lib.bo_routing_size(tokens, experts, k)), dev)
+            _check(lib.bo_routing_init(tokens, experts, k, int(bool(normalize)), mem.data_ptr(), mem.numel(),
+                                       ctypes.byref(self.handle), _stream(None, dev)), "bo_routing_init")
+            self._made([mem], dev)
+        h = self.handle
+        self.tokens, self.k, self.normalize, self._ran = tokens, k, bool(normalize), 0
+        self.weights = self._part(h.d_weights, torch.float32, tokens, k)
+        self.experts = self._part(h.d_experts, torch.int32, tokens, k)
+        self.counts = self._part(h.d_counts, torch.int32, experts)
+        self.probs = self._part(h.d_probs, torch.float32, experts)
+        self.loss = self._part(h.d_loss, torch.float32, 1)
+        self.real = self._part(h.d_real, torch.int32, 1)
+        self._width, self._ref = experts, ctypes.byref(h)
+        self._forward, self._backward = lib.bo_routing_forward, lib.bo_routing_backward
+
+    def run(self, logits: torch.Tensor, mask: torch.Tensor | None = None, stream=None) -> None:
+        """Routes by logits [n, experts] (bfloat16 or float32, contiguous rows).  mask (bool or
+        uint8 [n]): tokens that are False or 0 are left out.  Autograd does not see the call, which
+        refuses logits that it records."""
+        raw = self._on(stream)
+        _unrecorded_logits(logits)
+        dev = self.device
+        ld = _rows_in(logits, "logits", self.tokens, self._width, dev)
+        n, at, step = logits.shape[0], None, 0
+        if mask is not None:
+            step, at = _column(mask, "mask", n, (torch.bool, torch.uint8), dev), mask.data_ptr() or None
+        rc = self._forward(self._ref, logits.data_ptr(), _DTYPES[logits.dtype], ld, n, at, step, raw)
+        if rc != OK:
+            _failed(rc, "bo_routing_forward", dev)
+        self._ran = n
+
+    def backward(self, logits: torch.Tensor, d_weights: torch.Tensor | None,
+                 d_loss: float | torch.Tensor = 0.0, out: torch.Tensor | None = None, *,
+                 counts: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """The gradient of the last run's logits (the same ones, or their first rows) from those of
+        its weights (float32[n, k], or None) and of its balance loss (a number or a float32[1]
+        device tensor).  counts (int32[experts]): the experts' counts to take for the balance loss in
+        place of the run's, as of several batches together.  Goes to `out`, which may be the logits
+        themselves, or to memory of its own; returns it."""
+        raw = self._on(stream)
+        _unrecorded_logits(logits)
+        dev = self.device
+        ld = _rows_in(logits, "logits", self._ran, self._width, dev)
+        n = logits.shape[0]
+        gw, steps = None, (0, 0)
+        if d_weights is not None:
+            if d_weights.shape != (n, self.k) or d_weights.dtype != torch.float32 or d_weights.device != dev:
+                raise ValueError(f"d_weights must be a float32 tensor of shape ({n}, {self.k}) on {dev}")
+            gw, steps = d_weights.data_ptr() or None, d_weights.stride()
+        where, rate = None, 0.0
+        if isinstance(d_loss, torch.Tensor):
+            if d_loss.dtype != torch.float32 or d_loss.numel() != 1 or d_loss.device != dev:
+                raise ValueError(f"d_loss must be a number or a float32[1] tensor on {dev}")
+            where = d_loss.data_ptr()
+        else:
+            rate = float(d_loss)
+        if counts is not None and (counts.shape != (self._width,) or counts.dtype != torch.int32 or
+                                   counts.device != dev or not counts.is_contiguous()):
+            raise ValueError(f"counts must be a contiguous int32 tensor of {self._width} elements on {dev}")
+        out, ld_out = _out_for(out, logits, ld, dev, stream)
+        rc = self._backward(self._ref, logits.data_ptr(), _DTYPES[logits.dtype], ld, n, gw, *steps, rate, where,
+                            None if counts is None else counts.data_ptr(), out.data_ptr(), ld_out, raw)
+        if rc != OK:
+            _failed(rc, "bo_routing_backward", dev)
+        return out

@@ -1,16 +1,19 @@
 // bo_routing.cu -- the experts of each token of a mixture, their weights, per-expert counts and the
 // balance loss, and the gradient of the router's logits (include/ops/bf16ops.h has the formulas).
-#include <cfloat>
-#include <cmath>
+#include <cooperative_groups.h>
 
 #include "bo_internal.cuh"
 
 namespace bo {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
-constexpr uint32_t kMaxBlocks = 304;   // of the forward pass (its partial sums)
+constexpr uint32_t kMaxBlocks = 304;     // of the forward pass (its partial sums)
+constexpr uint32_t kFewBlocks = 8;       // that join their sums themselves
 constexpr uint32_t kJoinThreads = 1024;
+constexpr uint32_t kLane = 16;           // experts that a lane holds
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -20,11 +23,18 @@ struct RouteArgs {
   const uint8_t* mask;    // may be NULL
   uint64_t mask_stride;
   uint32_t tokens, experts, k, normalize;
+  uint32_t lanes;         // that share a token (a power of two)
+  uint32_t vec;           // their parts of a row are whole, aligned words of 32 bytes
+  uint32_t joined;        // the grid is one cluster, which writes the results itself
   float* weights;
   int32_t* chosen;
   float* sums;            // of p: one row of `experts` for each block
   int32_t* counts;        // likewise
   int32_t* real;          // one for each block
+  float* out_probs;
+  int32_t* out_counts;
+  float* out_loss;
+  int32_t* out_real;
 };
 struct RouteGradArgs {
   const uint8_t* x;
@@ -36,6 +46,7 @@ struct RouteGradArgs {
   const float* gloss;     // may be NULL
   float loss;
   uint32_t tokens, experts, k, normalize;
+  uint32_t lanes, vec, vec_dx;
   const int32_t* chosen;
   const int32_t* counts;
   const int32_t* real;
@@ -46,18 +57,40 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// A whole number that orders values: NaN above all, -0 as 0; 0 is below every one.
-__device__ __forceinline__ uint32_t order_of(float x) {
-  if (x != x) return 0xFFFFFFFFu;
-  const uint32_t u = __float_as_uint(x + 0.f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
-__device__ __forceinline__ float value_of(uint32_t o) {
-  return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void ld32(uint32_t* w, const void* p) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
+                 "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st32(void* p, const uint32_t* w) {
+  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  return v;
+}
+// among the lanes that share a token
+__device__ __forceinline__ float lanes_sum(float v, uint32_t lanes) {
+  for (uint32_t d = 1; d < lanes; d *= 2) v += __shfl_xor_sync(kAll, v, d);
+  return v;
+}
+__device__ __forceinline__ float lanes_max(float v, uint32_t lanes) {
+  for (uint32_t d = 1; d < lanes; d *= 2) v = max_nan(v, __shfl_xor_sync(kAll, v, d));
   return v;
 }
 template <bool F32>
@@ -66,13 +99,292 @@ __device__ __forceinline__ float element(const uint8_t* row, uint32_t e) {
              : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(row)[e] << 16);
 }
 
-// One warp a token: lane l holds experts l, l + 32, ...
+// N experts' logits from expert e0 on, as they lie in memory; -infinity past the last expert.
+template <bool F32, int N>
+struct Logits {
+  static constexpr int kWords = F32 ? N : N / 2;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void load(const uint8_t* row, uint32_t e0, uint32_t experts, bool vec) {
+    if (vec && e0 < experts) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 8) ld32(w + i, row + (uint64_t)e0 * (F32 ? 4 : 2) + i * 4);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; i++) {
+      if (F32) {
+        w[i] = e0 + i < experts ? reinterpret_cast<const uint32_t*>(row)[e0 + i] : 0xFF800000u;
+      } else {
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+        const uint32_t e = e0 + 2 * i;
+        w[i] = e < experts ? p[e] : 0xFF80u;
+        w[i] |= (e + 1 < experts ? (uint32_t)p[e + 1] : 0xFF80u) << 16;
+      }
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; i++) w[i] = 0;
+  }
+  __device__ __forceinline__ float2 pair(int i) const {   // elements 2 i and 2 i + 1
+    return F32 ? make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]))
+               : make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+  }
+  __device__ __forceinline__ float max() const {
+    if (F32) {
+      float m = __uint_as_float(w[0]);
+#pragma unroll
+      for (int i = 1; i < kWords; i++) m = max_nan(m, __uint_as_float(w[i]));
+      return m;
+    }
+    uint32_t m = w[0];
+#pragma unroll
+    for (int i = 1; i < kWords; i++) m = max_bf16x2(m, w[i]);
+    return max_nan(bf16_lo(m), bf16_hi(m));
+  }
+};
+
+// ------------------------------------------------------------------------------------- keys
+// A whole number that orders logits, and equal ones by their expert, the lowest first: the bits of
+// the logit as a signed number orders them, above the expert's complement.  NaN is above all others
+// and -0 is 0.  32 bits hold a BF16 logit and its expert, 64 an FP32 one.
+template <bool F32>
+struct Keys;
+template <>
+struct Keys<false> {
+  typedef int32_t T;
+  static constexpr T kNone = INT32_MIN;
+  // the words' logits are those of experts e0, e0 + 1, ...; past the last expert: none
+  template <int N>
+  static __device__ __forceinline__ void make(const Logits<false, N>& x, uint32_t e0, uint32_t experts, T* k) {
+#pragma unroll
+    for (int i = 0; i < N / 2; i++) {
+      uint32_t v, sign;
+      asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(x.w[i]), "r"(0u));   // one zero, one NaN
+      asm("prmt.b32 %0, %1, %1, 0xBB99;" : "=r"(sign) : "r"(v));          // all ones where negative
+      v ^= sign & 0x7FFF7FFFu;
+      const uint32_t c = 0xFFFFu - e0 - 2 * i;                            // complements
+      const uint32_t lo = __byte_perm(v, c, 0x1054), hi = (v & 0xFFFF0000u) | (c - 1);
+      k[2 * i] = e0 + 2 * i < experts ? (T)lo : kNone;
+      k[2 * i + 1] = e0 + 2 * i + 1 < experts ? (T)hi : kNone;
+    }
+  }
+  static __device__ __forceinline__ T make1(float x, uint32_t e) {
+    const int32_t s = x != x ? 0x7FFF0000 : __float_as_int(x + 0.f);
+    return (s ^ ((s >> 31) & 0x7FFF0000)) | (int32_t)(0xFFFFu - e);
+  }
+  static __device__ __forceinline__ float value(T k) {
+    const int32_t s = k & (int32_t)0xFFFF0000;
+    return __int_as_float(s ^ ((s >> 31) & 0x7FFF0000));
+  }
+  static __device__ __forceinline__ uint32_t expert(T k) { return 0xFFFFu - (uint32_t)(k & 0xFFFF); }
+  static __device__ __forceinline__ T warp_max(T k) { return __reduce_max_sync(kAll, k); }
+};
+template <>
+struct Keys<true> {
+  typedef long long T;
+  static constexpr T kNone = INT64_MIN;
+  static __device__ __forceinline__ T make1(float x, uint32_t e) {
+    const int32_t s = x != x ? 0x7FFFFFFF : __float_as_int(x + 0.f);
+    return (T)((unsigned long long)(uint32_t)(s ^ ((s >> 31) & 0x7FFFFFFF)) << 32 | (uint32_t)~e);
+  }
+  template <int N>
+  static __device__ __forceinline__ void make(const Logits<true, N>& x, uint32_t e0, uint32_t experts, T* k) {
+#pragma unroll
+    for (int i = 0; i < N; i++)
+      k[i] = e0 + i < experts ? make1(__uint_as_float(x.w[i]), e0 + i) : kNone;
+  }
+  static __device__ __forceinline__ float value(T k) {
+    const int32_t s = (int32_t)(k >> 32);
+    return __int_as_float(s ^ ((s >> 31) & 0x7FFFFFFF));
+  }
+  static __device__ __forceinline__ uint32_t expert(T k) { return ~(uint32_t)k; }
+  static __device__ __forceinline__ T warp_max(T k) {
+    const int32_t hi = __reduce_max_sync(kAll, (int32_t)(k >> 32));
+    const uint32_t lo = __reduce_max_sync(kAll, (int32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+    return (T)((unsigned long long)(uint32_t)hi << 32 | lo);
+  }
+};
+
+// Sorting networks, greatest first.
+template <class T>
+__device__ __forceinline__ void order(T& a, T& b) {
+  const T hi = a > b ? a : b, lo = a > b ? b : a;
+  a = hi;
+  b = lo;
+}
+template <class T>
+__device__ __forceinline__ void sort4(T* k) {
+  order(k[0], k[1]), order(k[2], k[3]), order(k[0], k[2]), order(k[1], k[3]), order(k[1], k[2]);
+}
+template <class T>
+__device__ __forceinline__ void sort8(T* k) {   // (K. Batcher, "Sorting networks and their applications", 1968)
+  sort4(k), sort4(k + 4);
+  order(k[0], k[4]), order(k[1], k[5]), order(k[2], k[6]), order(k[3], k[7]);
+  order(k[2], k[4]), order(k[3], k[5]), order(k[1], k[2]), order(k[3], k[4]), order(k[5], k[6]);
+}
+template <int N, class T>
+__device__ __forceinline__ void clean(T* k) {   // of a bitonic sequence
+#pragma unroll
+  for (int s = N / 2; s; s /= 2)
+#pragma unroll
+    for (int i = 0; i < N; i++)
+      if (!(i & s)) order(k[i], k[i + s]);
+}
+// the N greatest of two sorted lists, in a
+template <int N, class T>
+__device__ __forceinline__ void merge(T* a, const T* b) {
+#pragma unroll
+  for (int i = 0; i < N; i++) a[i] = a[i] > b[N - 1 - i] ? a[i] : b[N - 1 - i];
+  clean<N>(a);
+}
+// the N greatest of 16, in the first places
+template <int N, class T>
+__device__ __forceinline__ void best_of_16(T* k) {
+  if (N <= 4) {
+    sort4(k), sort4(k + 4), sort4(k + 8), sort4(k + 12);
+    merge<4>(k, k + 4), merge<4>(k + 8, k + 12), merge<4>(k, k + 8);
+  } else if (N <= 8) {
+    sort8(k), sort8(k + 8);
+    merge<8>(k, k + 8);
+  } else {
+    sort8(k), sort8(k + 8);
+#pragma unroll
+    for (int i = 0; i < 8; i++) order(k[i], k[15 - i]);
+    clean<8>(k), clean<8>(k + 8);
+  }
+}
+// Two lists of each of two lanes that are `stride` apart joined to one: the lane with that bit of its
+// number clear joins the lists `first`, the other one the lists `second`.
+template <int N, class T>
+__device__ __forceinline__ void exchange(const T* first, T* second, bool upper, uint32_t stride) {
+  T other[N];
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    const T give = upper ? first[i] : second[i];
+    if (!upper) second[i] = first[i];
+    other[i] = __shfl_xor_sync(kAll, give, stride);
+  }
+  merge<N>(second, other);
+}
+
+// ------------------------------------------------------------------- a block's sums and counts
+// In shared memory: counts of each expert, then sums of each warp.  The blocks of a cluster that is
+// the whole grid join them and write the results; else each block leaves its own for k_route_join.
+__device__ __forceinline__ void finish(const RouteArgs& P, const int32_t* counts, float* sums, int32_t* reals,
+                                       double* parts, uint32_t warps) {
+  const uint32_t E = P.experts;
+  __syncthreads();
+  for (uint32_t e = threadIdx.x; e < E; e += blockDim.x) {
+    float s = 0.f;
+    for (uint32_t i = 0; i < warps; i++) s += sums[i * E + e];
+    if (P.joined) {
+      sums[e] = s;   // (the column is this thread's)
+    } else {
+      P.sums[(uint64_t)blockIdx.x * E + e] = s;
+      P.counts[(uint64_t)blockIdx.x * E + e] = counts[e];
+    }
+  }
+  if (threadIdx.x == 0) {
+    int32_t n = 0;
+    for (uint32_t i = 0; i < warps; i++) n += reals[i];
+    if (P.joined) reals[0] = n;
+    else P.real[blockIdx.x] = n;
+  }
+  if (!P.joined) return;
+  const cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  if (blockIdx.x == 0) {
+    int32_t N = 0;
+    for (uint32_t b = 0; b < gridDim.x; b++) N += *cluster.map_shared_rank(reals, b);
+    double share = 0;
+    for (uint32_t e = threadIdx.x; e < E; e += blockDim.x) {
+      float v[kFewBlocks];
+      int32_t c[kFewBlocks], n = 0;
+#pragma unroll
+      for (uint32_t b = 0; b < kFewBlocks; b++) {
+        v[b] = b < gridDim.x ? cluster.map_shared_rank(sums, b)[e] : 0.f;
+        c[b] = b < gridDim.x ? cluster.map_shared_rank(counts, b)[e] : 0;
+      }
+      double s = 0;
+#pragma unroll
+      for (uint32_t b = 0; b < kFewBlocks; b++) s += v[b], n += c[b];
+      const double p = N > 0 ? s / N : 0;
+      P.out_probs[e] = (float)p;
+      P.out_counts[e] = n;
+      share += p * n;
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) share += __shfl_xor_sync(kAll, share, d);
+    if (threadIdx.x % 32 == 0) parts[threadIdx.x / 32] = share;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (uint32_t i = 1; i < warps; i++) share += parts[i];
+      *P.out_loss = N > 0 ? (float)(share * E / ((double)N * P.k)) : 0.f;
+      *P.out_real = N;
+    }
+  }
+  cluster.sync();   // (the others' memory is read until here)
+}
+
+// Joins the blocks' sums and counts: several slices of the blocks at a time, in a fixed order.
+__global__ void __launch_bounds__(kJoinThreads) k_route_join(const RouteArgs P, uint32_t blocks) {
+  __shared__ double sums[kJoinThreads];
+  __shared__ int32_t counts[kJoinThreads];
+  __shared__ double parts[kJoinThreads / 32];
+  __shared__ int32_t reals[kJoinThreads / 32];
+  after_previous();
+  const uint32_t E = P.experts, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  int32_t r = threadIdx.x < blocks ? P.real[threadIdx.x] : 0;
+  r = __reduce_add_sync(kAll, r);
+  if (lane == 0) reals[warp] = r;
+  const uint32_t slices = kJoinThreads / E, slice = threadIdx.x / E, e = threadIdx.x % E;
+  double s = 0;
+  int32_t c = 0;
+  if (slice < slices) {
+#pragma unroll 8
+    for (uint32_t b = slice; b < blocks; b += slices) {
+      s += P.sums[(uint64_t)b * E + e];
+      c += P.counts[(uint64_t)b * E + e];
+    }
+  }
+  sums[threadIdx.x] = s;
+  counts[threadIdx.x] = c;
+  __syncthreads();
+  int32_t N = 0;
+  for (uint32_t i = 0; i < kJoinThreads / 32; i++) N += reals[i];
+  double share = 0;
+  if (threadIdx.x < E) {
+    for (uint32_t i = 1; i < slices; i++) s += sums[i * E + e], c += counts[i * E + e];
+    const double p = N > 0 ? s / N : 0;
+    P.out_probs[e] = (float)p;
+    P.out_counts[e] = c;
+    share = p * c;
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) share += __shfl_xor_sync(kAll, share, d);
+  if (lane == 0) parts[warp] = share;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 1; i < kJoinThreads / 32; i++) share += parts[i];
+    *P.out_loss = N > 0 ? (float)(share * E / ((double)N * P.k)) : 0.f;
+    *P.out_real = N;
+  }
+}
+
+// ------------------------------------------------------------------------------ forward pass
+// One warp a token, for few tokens, or more experts or choices than k_route_many takes: lane l holds
+// experts l, l + 32, ...
 template <bool F32, int NV>
 __global__ void __launch_bounds__(kThreads) k_route(const RouteArgs P) {
-  extern __shared__ uint32_t sh[];   // experts counts, then experts sums of each warp
+  extern __shared__ uint32_t sh[];
   int32_t* counts = reinterpret_cast<int32_t*>(sh);
   float* sums = reinterpret_cast<float*>(sh + P.experts);
   __shared__ int32_t reals[kWarps];
+  __shared__ double parts[kWarps];
+  typedef Keys<F32> K;
+  typedef typename K::T Key;
   after_previous();
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = P.experts;
   for (uint32_t e = threadIdx.x; e < E; e += kThreads) counts[e] = 0;
@@ -84,21 +396,19 @@ __global__ void __launch_bounds__(kThreads) k_route(const RouteArgs P) {
   for (uint64_t t = (uint64_t)blockIdx.x * kWarps + warp; t < P.tokens; t += (uint64_t)gridDim.x * kWarps) {
     const uint8_t* row = P.x + t * P.ld;
     bool use = !P.mask || P.mask[t * P.mask_stride] != 0;
-    uint32_t o[NV];
+    Key key[NV], mine = 0;   // lane i: the i-th choice
     float p[NV], sum = 0.f, w = 0.f;
-    uint32_t mine = 0;       // lane i: the i-th choice
     if (use) {
-      uint32_t top = 0;
+      Key top = K::kNone;
 #pragma unroll
       for (int j = 0; j < NV; j++) {
         const uint32_t e = lane + 32 * j;
-        const float x = e < E ? element<F32>(row, e) : __int_as_float(0xFF800000);
-        p[j] = x;
-        o[j] = e < E ? order_of(x) : 0;
-        top = max(top, o[j]);
+        p[j] = e < E ? element<F32>(row, e) : __int_as_float(0xFF800000);
+        key[j] = e < E ? K::make1(p[j], e) : K::kNone;
+        top = key[j] > top ? key[j] : top;
       }
-      top = __reduce_max_sync(kAll, top);
-      const float max = value_of(top);
+      Key best = K::warp_max(top);
+      const float max = K::value(best);
       use = max != __int_as_float(0xFF800000);
       if (use) {
 #pragma unroll
@@ -110,34 +420,26 @@ __global__ void __launch_bounds__(kThreads) k_route(const RouteArgs P) {
         const float inv = 1.f / sum;
 #pragma unroll
         for (int j = 0; j < NV; j++) total[j] += p[j] * inv;
-        float x_mine = max;
-        for (uint32_t i = 0; i < P.k; i++) {
-          uint32_t best = 0;
+        for (uint32_t i = 0;;) {
+          if (lane == i) mine = best;
+          if (++i == P.k) break;
+          Key next = K::kNone;
 #pragma unroll
-          for (int j = 0; j < NV; j++) best = ::max(best, o[j]);
-          best = __reduce_max_sync(kAll, best);
-          uint32_t at = 0xffffffffu;
-#pragma unroll
-          for (int j = NV - 1; j >= 0; j--)
-            if (o[j] == best) at = lane + 32 * j;
-          at = __reduce_min_sync(kAll, at);
-#pragma unroll
-          for (int j = 0; j < NV; j++)
-            if (at == lane + 32 * j) o[j] = 0;
-          if (lane == i) {
-            mine = at;
-            x_mine = value_of(best);
+          for (int j = 0; j < NV; j++) {
+            if (key[j] == best) key[j] = K::kNone;
+            next = key[j] > next ? key[j] : next;
           }
+          best = K::warp_max(next);
         }
-        w = lane < P.k ? ex2((x_mine - max) * kLog2e) : 0.f;
+        w = lane < P.k ? ex2((K::value(mine) - max) * kLog2e) : 0.f;
         w *= P.normalize ? 1.f / warp_sum(w) : inv;
-        if (lane < P.k) atomicAdd(&counts[mine], 1);
+        if (lane < P.k) atomicAdd(&counts[K::expert(mine)], 1);
         real++;
       }
     }
     if (lane < P.k) {
       P.weights[t * P.k + lane] = use ? w : 0.f;
-      P.chosen[t * P.k + lane] = use ? (int32_t)mine : -1;
+      P.chosen[t * P.k + lane] = use ? (int32_t)K::expert(mine) : -1;
     }
   }
 #pragma unroll
@@ -146,63 +448,172 @@ __global__ void __launch_bounds__(kThreads) k_route(const RouteArgs P) {
     if (e < E) sums[warp * E + e] = total[j];
   }
   if (lane == 0) reals[warp] = real;
-  __syncthreads();
-  for (uint32_t e = threadIdx.x; e < E; e += kThreads) {
-    float s = 0.f;
-    for (uint32_t i = 0; i < kWarps; i++) s += sums[i * E + e];
-    P.sums[(uint64_t)blockIdx.x * E + e] = s;
-    P.counts[(uint64_t)blockIdx.x * E + e] = counts[e];
-  }
-  if (threadIdx.x == 0) {
-    int32_t n = 0;
-    for (uint32_t i = 0; i < kWarps; i++) n += reals[i];
-    P.real[blockIdx.x] = n;
-  }
+  finish(P, counts, sums, reals, parts, kWarps);
 }
 
-// Joins the blocks' sums and counts, in their order.
-__global__ void __launch_bounds__(kJoinThreads) k_route_join(const float* sums, const int32_t* counts,
-                                                             const int32_t* reals, uint32_t blocks,
-                                                             uint32_t E, uint32_t k, float* probs,
-                                                             int32_t* n, float* loss, int32_t* real) {
-  __shared__ double part[kJoinThreads];
-  __shared__ int32_t total;
+// A warp takes 32 tokens at a time.  `lanes` lanes share a token, 16 experts each, so that it takes
+// `lanes` rounds of 32 / lanes tokens; in each, a lane finds the KL greatest of its 16 keys.  Lanes
+// join their lists in pairs as soon as two rounds have one each: one of the two lanes goes on with the
+// first round's token, the other with the second's.  After all rounds each lane has the whole list
+// of one token, the one with the lane's number among the 32: a join costs each list once, and not
+// each lane.
+template <bool F32, int KL>
+__global__ void __launch_bounds__(kThreads, F32 ? 1 : 2) k_route_many(const RouteArgs P) {
+  extern __shared__ uint32_t sh[];
+  int32_t* counts = reinterpret_cast<int32_t*>(sh);
+  float* sums = reinterpret_cast<float*>(sh + P.experts);
+  __shared__ int32_t reals[kWarps];
+  __shared__ double parts[kWarps];
+  typedef Keys<F32> K;
+  typedef typename K::T Key;
   after_previous();
-  if (threadIdx.x == 0) {
-    int32_t r = 0;
-    for (uint32_t b = 0; b < blocks; b++) r += reals[b];
-    total = r;
-    *real = r;
-  }
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = P.experts, G = P.lanes;
+  const uint32_t g = lane % G, q = lane / G, e0 = g * kLane;
+  for (uint32_t e = threadIdx.x; e < E; e += kThreads) counts[e] = 0;
   __syncthreads();
-  const int32_t N = total;
-  double share = 0;
-  for (uint32_t e = threadIdx.x; e < E; e += kJoinThreads) {
-    double s = 0;
-    int32_t c = 0;
-    for (uint32_t b = 0; b < blocks; b++) {
-      s += sums[(uint64_t)b * E + e];
-      c += counts[(uint64_t)b * E + e];
+  const uint32_t units = (P.tokens + 31) / 32, step = gridDim.x * kWarps;
+  float2 total[kLane / 2];
+#pragma unroll
+  for (int j = 0; j < (int)kLane / 2; j++) total[j] = make_float2(0.f, 0.f);
+  int32_t real = 0;
+  Logits<F32, kLane> ahead;
+  bool use_ahead = false;
+  auto fetch = [&](uint32_t unit, uint32_t round) {
+    const uint64_t t = (uint64_t)unit * 32 + q * G + round;
+    use_ahead = t < P.tokens && (!P.mask || P.mask[t * P.mask_stride] != 0);
+    if (use_ahead) ahead.load(P.x + t * P.ld, e0, E, P.vec);
+    else ahead.clear();
+  };
+  uint32_t unit = blockIdx.x * kWarps + warp;
+  if (unit < units) fetch(unit, 0);
+  for (; unit < units; unit += step) {
+    float sum_mine = 0.f;
+    bool use_mine = false;
+    uint32_t round = 0;
+    Key list[kLane], l0[KL], l1[KL], l2[KL], l3[KL];
+    auto take = [&]() {      // one round
+      const Logits<F32, kLane> x = ahead;
+      bool use = use_ahead;
+      if (round + 1 < G) fetch(unit, round + 1);
+      else if (unit + step < units) fetch(unit + step, 0);
+      float max = lanes_max(x.max(), G);
+      if (max == __int_as_float(0xFF800000)) use = false, max = 0.f;
+      float2 e[kLane / 2], s = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < (int)kLane / 2; j++) {
+        const float2 d = __fmul2_rn(__fadd2_rn(x.pair(j), make_float2(-max, -max)), make_float2(kLog2e, kLog2e));
+        e[j] = make_float2(ex2(d.x), ex2(d.y));
+        s = __fadd2_rn(s, e[j]);
+      }
+      const float sum = lanes_sum(s.x + s.y, G);
+      const float inv = use ? 1.f / sum : 0.f;
+#pragma unroll
+      for (int j = 0; j < (int)kLane / 2; j++) total[j] = __ffma2_rn(e[j], make_float2(inv, inv), total[j]);
+      if (round == g) sum_mine = sum, use_mine = use;
+      K::make(x, e0, E, list);
+      best_of_16<KL>(list);
+      round++;
+    };
+    auto keep = [&](Key* to) {
+#pragma unroll
+      for (int i = 0; i < KL; i++) to[i] = list[i];
+    };
+    // (loops of one or two turns: only one copy of a round's code)
+#pragma unroll 1
+    for (uint32_t c = 0;; c++) {
+#pragma unroll 1
+      for (uint32_t b = 0;; b++) {
+#pragma unroll 1
+        for (uint32_t a = 0;; a++) {
+#pragma unroll 1
+          for (uint32_t i = 0;; i++) {
+            take();
+            if (G < 2) break;
+            if (i) {
+              exchange<KL>(l0, list, lane & 1, 1);
+              break;
+            }
+            keep(l0);
+          }
+          if (G < 4) break;
+          if (a) {
+            exchange<KL>(l1, list, lane & 2, 2);
+            break;
+          }
+          keep(l1);
+        }
+        if (G < 8) break;
+        if (b) {
+          exchange<KL>(l2, list, lane & 4, 4);
+          break;
+        }
+        keep(l2);
+      }
+      if (G < 16) break;
+      if (c) {
+        exchange<KL>(l3, list, lane & 8, 8);
+        break;
+      }
+      keep(l3);
     }
-    const double p = N > 0 ? s / N : 0;
-    probs[e] = (float)p;
-    n[e] = c;
-    share += p * c;
+    const uint64_t t = (uint64_t)unit * 32 + lane;
+    if (t >= P.tokens) use_mine = false;
+    real += __popc(__ballot_sync(kAll, use_mine));
+    if (t < P.tokens) {
+      const float max = K::value(list[0]);
+      float w[KL], s[KL];
+#pragma unroll
+      for (int i = 0; i < KL; i++) {
+        w[i] = ex2((K::value(list[i]) - max) * kLog2e);
+        s[i] = i < (int)P.k ? w[i] : 0.f;
+      }
+#pragma unroll
+      for (int n = KL / 2; n; n /= 2)   // (as warp_sum does: a token's weights are k_route's)
+#pragma unroll
+        for (int i = 0; i < n; i++) s[i] += s[i + n];
+      const float inv = 1.f / (P.normalize ? s[0] : sum_mine);
+      float* to = P.weights + t * P.k;
+      int32_t* at = P.chosen + t * P.k;
+      uint32_t wo[KL], eo[KL];
+#pragma unroll
+      for (int i = 0; i < KL; i++) {
+        wo[i] = use_mine ? __float_as_uint(w[i] * inv) : 0u;
+        eo[i] = use_mine ? K::expert(list[i]) : 0xffffffffu;
+        if (use_mine && i < (int)P.k) atomicAdd(&counts[eo[i]], 1);
+      }
+      if (KL == 8 && P.k == 8) {
+        st32(to, wo);
+        st32(at, eo);
+      } else {
+#pragma unroll
+        for (int i = 0; i < KL; i++)
+          if (i < (int)P.k) to[i] = __uint_as_float(wo[i]), at[i] = (int32_t)eo[i];
+      }
+    }
   }
-  part[threadIdx.x] = share;
-  __syncthreads();
-  for (uint32_t d = kJoinThreads / 2; d; d /= 2) {
-    if (threadIdx.x < d) part[threadIdx.x] += part[threadIdx.x + d];
-    __syncthreads();
+#pragma unroll
+  for (int j = 0; j < (int)kLane / 2; j++) {
+    for (uint32_t d = G; d < 32; d *= 2) {
+      total[j].x += __shfl_xor_sync(kAll, total[j].x, d);
+      total[j].y += __shfl_xor_sync(kAll, total[j].y, d);
+    }
+    if (q == 0 && e0 + 2 * j < E) sums[warp * E + e0 + 2 * j] = total[j].x;
+    if (q == 0 && e0 + 2 * j + 1 < E) sums[warp * E + e0 + 2 * j + 1] = total[j].y;
   }
-  if (threadIdx.x == 0) *loss = N > 0 ? (float)(part[0] * E / ((double)N * k)) : 0.f;
+  if (lane == 0) reals[warp] = real;
+  finish(P, counts, sums, reals, parts, kWarps);
 }
 
-template <bool F32, int NV>
+// ----------------------------------------------------------------------------- backward pass
+// `lanes` lanes share a token, N experts each and at most one of its choices each.  The choices'
+// logits get their gradient on top of the others' a second time, from the lanes that hold them.
+template <bool F32, int N>
 __global__ void __launch_bounds__(kThreads) k_route_grad(const RouteGradArgs P) {
+  extern __shared__ float share[];   // dL/dp of each expert
   __shared__ long long parts[kWarps];
   after_previous();
-  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = P.experts;
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = P.experts, G = P.lanes;
+  const uint32_t g = lane % G, q = lane / G, e0 = g * N, per = 32 / G;
   long long sum = 0;
   for (uint32_t e = threadIdx.x; e < E; e += kThreads) sum += P.counts[e];
 #pragma unroll
@@ -211,70 +622,82 @@ __global__ void __launch_bounds__(kThreads) k_route_grad(const RouteGradArgs P) 
   __syncthreads();
   sum = 0;
   for (uint32_t i = 0; i < kWarps; i++) sum += parts[i];
-  const int32_t N = *P.real;
+  const int32_t real = *P.real;
   const float gl = P.gloss ? *P.gloss : P.loss;
-  // dL/dp of expert e is unit * counts[e]
-  const float unit = sum > 0 && N > 0 ? (float)((double)gl * E / ((double)sum * N)) : 0.f;
-  for (uint64_t t = (uint64_t)blockIdx.x * kWarps + warp; t < P.tokens; t += (uint64_t)gridDim.x * kWarps) {
+  const float unit = sum > 0 && real > 0 ? (float)((double)gl * E / ((double)sum * real)) : 0.f;
+  for (uint32_t e = threadIdx.x; e < E; e += kThreads) share[e] = unit * P.counts[e];
+  __syncthreads();
+  float2 c[N / 2];
+#pragma unroll
+  for (int j = 0; j < N / 2; j++)
+    c[j] = make_float2(e0 + 2 * j < E ? share[e0 + 2 * j] : 0.f, e0 + 2 * j + 1 < E ? share[e0 + 2 * j + 1] : 0.f);
+  const uint64_t groups = ((uint64_t)P.tokens + per - 1) / per;
+  for (uint64_t n = (uint64_t)blockIdx.x * kWarps + warp; n < groups; n += (uint64_t)gridDim.x * kWarps) {
+    const uint64_t t = n * per + q;
+    const bool there = t < P.tokens;
+    const bool choose = there && g < P.k;
+    const uint8_t* row = P.x + t * P.ld;
     uint8_t* out = P.dx + t * P.ld_dx;
-    const int32_t mine = lane < P.k ? P.chosen[t * P.k + lane] : 0;
-    const bool use = __shfl_sync(kAll, mine, 0) >= 0;
-    float d[NV];
+    const int32_t mine = choose ? P.chosen[t * P.k + g] : -1;
+    const float gw = choose && P.gw ? P.gw[t * P.gw_stride + g * P.gw_choice] : 0.f;
+    Logits<F32, N> x;
+    if (there) x.load(row, e0, E, P.vec);
+    else x.clear();
+    const float xm = mine >= 0 ? element<F32>(row, (uint32_t)mine) : 0.f;
+    const bool use = __shfl_sync(kAll, mine, q * G) >= 0;
+    const float max = lanes_max(x.max(), G);
+    float2 p[N / 2], s = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < NV; j++) d[j] = 0.f;
-    if (use) {
-      const uint8_t* row = P.x + t * P.ld;
-      float x[NV], max = -FLT_MAX, s = 0.f;
+    for (int j = 0; j < N / 2; j++) {
+      const float2 d = __fmul2_rn(__fadd2_rn(x.pair(j), make_float2(-max, -max)), make_float2(kLog2e, kLog2e));
+      p[j] = make_float2(ex2(d.x), ex2(d.y));
+      s = __fadd2_rn(s, p[j]);
+    }
+    const float inv = 1.f / lanes_sum(s.x + s.y, G);
+    float2 dots = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < NV; j++) {
-        const uint32_t e = lane + 32 * j;
-        x[j] = e < E ? element<F32>(row, e) : __int_as_float(0xFF800000);
-        max = fmaxf(max, x[j]);
+    for (int j = 0; j < N / 2; j++) {
+      p[j] = __fmul2_rn(p[j], make_float2(inv, inv));
+      dots = __ffma2_rn(p[j], c[j], dots);
+    }
+    float dot = dots.x + dots.y;       // of p and dL/dp
+    const float pm = mine >= 0 ? ex2((xm - max) * kLog2e) * inv : 0.f;
+    float add;                         // what the choice adds to its logit
+    if (P.normalize) {
+      const float w = pm / lanes_sum(pm, G);
+      add = w * (gw - lanes_sum(mine >= 0 ? w * gw : 0.f, G));
+    } else {
+      add = pm * gw;
+      dot += mine >= 0 ? add : 0.f;
+    }
+    dot = lanes_sum(dot, G);
+    __syncwarp();   // (the rows are read: their gradients may take their place)
+    if (there) {
+      uint32_t o[Logits<F32, N>::kWords];
+#pragma unroll
+      for (int j = 0; j < N / 2; j++) {
+        float2 d = __fmul2_rn(p[j], __fadd2_rn(c[j], make_float2(-dot, -dot)));
+        if (!use) d = make_float2(0.f, 0.f);
+        if (F32) o[2 * j] = __float_as_uint(d.x), o[2 * j + 1] = __float_as_uint(d.y);
+        else o[j] = pack_bf16(d.x, d.y);
       }
+      if (P.vec_dx && e0 < E) {
 #pragma unroll
-      for (int i = 16; i; i >>= 1) max = fmaxf(max, __shfl_xor_sync(kAll, max, i));
-#pragma unroll
-      for (int j = 0; j < NV; j++) {
-        x[j] = ex2((x[j] - max) * kLog2e);
-        s += x[j];
-      }
-      const float inv = 1.f / warp_sum(s);
-      const float gw = P.gw && lane < P.k ? P.gw[t * P.gw_stride + lane * P.gw_choice] : 0.f;
-      const float pm = lane < P.k ? ex2((element<F32>(row, (uint32_t)mine) - max) * kLog2e) * inv : 0.f;
-      float dot = 0.f;   // sum of p dL/dp
-#pragma unroll
-      for (int j = 0; j < NV; j++) {
-        const uint32_t e = lane + 32 * j;
-        x[j] *= inv;
-        d[j] = e < E ? unit * P.counts[e] : 0.f;
-        dot = fmaf(x[j], d[j], dot);
-      }
-      float add;         // what the choice adds to its logit
-      if (P.normalize) {
-        const float w = pm / warp_sum(pm);
-        add = w * (gw - warp_sum(w * gw));
+        for (int i = 0; i < Logits<F32, N>::kWords; i += 8) st32(out + (uint64_t)e0 * (F32 ? 4 : 2) + i * 4, o + i);
       } else {
-        add = pm * gw;
-        dot += add;
-      }
-      dot = warp_sum(dot);
 #pragma unroll
-      for (int j = 0; j < NV; j++) d[j] = x[j] * (d[j] - dot);
-      for (uint32_t i = 0; i < P.k; i++) {
-        const uint32_t e = (uint32_t)__shfl_sync(kAll, mine, i);
-        const float a = __shfl_sync(kAll, add, i);
-#pragma unroll
-        for (int j = 0; j < NV; j++)
-          if (e == lane + 32 * j) d[j] += a;
+        for (int i = 0; i < N; i++) {
+          if (e0 + i >= E) continue;
+          if (F32) reinterpret_cast<uint32_t*>(out)[e0 + i] = o[i];
+          else reinterpret_cast<uint16_t*>(out)[e0 + i] = (uint16_t)(o[i / 2] >> (16 * (i & 1)));
+        }
       }
     }
-    __syncwarp();   // (the row is read: its gradient may take its place)
-#pragma unroll
-    for (int j = 0; j < NV; j++) {
-      const uint32_t e = lane + 32 * j;
-      if (e >= E) continue;
-      if (F32) reinterpret_cast<float*>(out)[e] = d[j];
-      else reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)pack_bf16(d[j], 0.f);
+    __syncwarp();
+    if (mine >= 0) {
+      const float d = pm * (share[mine] - dot) + add;
+      if (F32) reinterpret_cast<float*>(out)[mine] = d;
+      else reinterpret_cast<uint16_t*>(out)[mine] = (uint16_t)pack_bf16(d, 0.f);
     }
   }
 }
@@ -316,26 +739,51 @@ Region results(const bo_routing* h) {
 bool matrix(const void* p, uint64_t ld, uint64_t rows, uint64_t width, uint64_t size) {
   return p && aligned(p, size) && ld <= (1ull << 40) && (rows <= 1 || ld >= width);
 }
-// the smallest of 1, 2, 4, ... 32 experts a lane
-template <bool F32, class A, class F>
-int by_experts(uint32_t experts, const F& f) {
-  const uint32_t nv = (experts + 31) / 32;
-  return nv <= 1 ? f(std::integral_constant<int, 1>()) : nv <= 2 ? f(std::integral_constant<int, 2>())
-       : nv <= 4 ? f(std::integral_constant<int, 4>()) : nv <= 8 ? f(std::integral_constant<int, 8>())
-       : nv <= 16 ? f(std::integral_constant<int, 16>()) : f(std::integral_constant<int, 32>());
+uint32_t power_of_two(uint32_t n) {   // the least that is not below n
+  uint32_t p = 1;
+  while (p < n) p *= 2;
+  return p;
+}
+// rows whose parts of `each` elements are whole, aligned words of 32 bytes
+bool whole(const void* p, uint64_t ld, uint32_t width, uint32_t each) {   // (ld in bytes)
+  return aligned(p, 32) && ld % 32 == 0 && width % each == 0;
 }
 template <bool F32>
-int route(const RouteArgs& P, uint32_t grid, cudaStream_t s) {
-  return by_experts<F32, RouteArgs>(P.experts, [&](auto nv) {
-    return check(launch(k_route<F32, decltype(nv)::value>, dim3(grid), kThreads,
-                        P.experts * (1 + kWarps) * 4, 1, s, P));
-  });
+int route(RouteArgs& P, uint32_t sms, cudaStream_t s) {
+  const uint32_t smem = P.experts * (1 + kWarps) * 4;
+  const uint32_t nv = (P.experts + 31) / 32;
+  auto one = nv <= 1 ? k_route<F32, 1> : nv <= 2 ? k_route<F32, 2> : nv <= 4 ? k_route<F32, 4>
+           : nv <= 8 ? k_route<F32, 8> : nv <= 16 ? k_route<F32, 16> : k_route<F32, 32>;
+  if (P.tokens <= kFewBlocks * kWarps * 2) {   // one launch
+    const uint32_t grid = P.tokens <= kWarps ? 1 : P.tokens <= 2 * kWarps ? 2 : P.tokens <= 4 * kWarps ? 4 : kFewBlocks;
+    P.joined = 1;
+    return check(launch(one, dim3(grid), kThreads, smem, grid, s, P));
+  }
+  P.joined = 0;
+  uint32_t grid;
+  int rc;
+  if (P.tokens > sms * 2 * kWarps && P.experts <= 16 * kLane && P.k <= 16) {
+    P.lanes = power_of_two((P.experts + kLane - 1) / kLane);
+    P.vec = whole(P.x, P.ld, P.experts, kLane);
+    grid = std::min({((P.tokens + 31) / 32 + kWarps - 1) / kWarps, sms * 2, kMaxBlocks});
+    auto many = P.k <= 4 ? k_route_many<F32, 4> : P.k <= 8 ? k_route_many<F32, 8> : k_route_many<F32, 16>;
+    rc = check(launch(many, dim3(grid), kThreads, smem, 1, s, P));
+  } else {
+    grid = std::min({(P.tokens + kWarps - 1) / kWarps, sms * 2, kMaxBlocks});
+    rc = check(launch(one, dim3(grid), kThreads, smem, 1, s, P));
+  }
+  return rc ? rc : check(launch(k_route_join, dim3(1), kJoinThreads, 0, 1, s, P, grid));
 }
 template <bool F32>
-int route_grad(const RouteGradArgs& P, uint32_t grid, cudaStream_t s) {
-  return by_experts<F32, RouteGradArgs>(P.experts, [&](auto nv) {
-    return check(launch(k_route_grad<F32, decltype(nv)::value>, dim3(grid), kThreads, 0, 1, s, P));
-  });
+int route_grad(RouteGradArgs& P, uint32_t sms, cudaStream_t s) {
+  const uint32_t each = P.experts <= 32 * kLane ? kLane : 2 * kLane;
+  P.lanes = power_of_two(std::max((P.experts + each - 1) / each, P.k));
+  P.vec = whole(P.x, P.ld, P.experts, each);
+  P.vec_dx = whole(P.dx, P.ld_dx, P.experts, each);
+  const uint64_t groups = ((uint64_t)P.tokens * P.lanes + 31) / 32;
+  const uint32_t grid = (uint32_t)std::min<uint64_t>((groups + kWarps - 1) / kWarps, sms * 8);
+  return check(launch(each == kLane ? k_route_grad<F32, kLane> : k_route_grad<F32, 2 * kLane>, dim3(grid), kThreads,
+                      P.experts * 4, 1, s, P));
 }
 
 }  // namespace
@@ -390,7 +838,7 @@ int bo_routing_forward(const bo_routing* h, const void* d_logits, uint32_t dtype
   }
   int sms = 0;
   if (const int rc = sm_count(h->device, sms)) return rc;
-  RouteArgs P;
+  RouteArgs P = {};
   P.x = static_cast<const uint8_t*>(d_logits);
   P.ld = ld * size;
   P.mask = d_mask;
@@ -404,13 +852,12 @@ int bo_routing_forward(const bo_routing* h, const void* d_logits, uint32_t dtype
   P.sums = static_cast<float*>(h->d_partials);
   P.counts = static_cast<int32_t*>(h->d_partials) + (uint64_t)kMaxBlocks * h->experts;
   P.real = P.counts + (uint64_t)kMaxBlocks * h->experts;
-  const uint32_t want = (tokens + kWarps - 1) / kWarps;
-  const uint32_t grid = std::max(1u, std::min({want, (uint32_t)sms * 2, kMaxBlocks}));
+  P.out_probs = h->d_probs;
+  P.out_counts = h->d_counts;
+  P.out_loss = h->d_loss;
+  P.out_real = h->d_real;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (const int rc = dtype == BO_FP32 ? route<true>(P, grid, s) : route<false>(P, grid, s)) return rc;
-  return check(launch(k_route_join, dim3(1), kJoinThreads, 0, 1, s, (const float*)P.sums,
-                      (const int32_t*)P.counts, (const int32_t*)P.real, grid, h->experts, h->k,
-                      h->d_probs, h->d_counts, h->d_loss, h->d_real));
+  return dtype == BO_FP32 ? route<true>(P, (uint32_t)sms, s) : route<false>(P, (uint32_t)sms, s);
 }
 
 int bo_routing_backward(const bo_routing* h, const void* d_logits, uint32_t dtype, uint64_t ld,
@@ -437,7 +884,7 @@ int bo_routing_backward(const bo_routing* h, const void* d_logits, uint32_t dtyp
   int sms = 0;
   if (const int rc = sm_count(h->device, sms)) return rc;
   if (tokens == 0) return BD_OK;
-  RouteGradArgs P;
+  RouteGradArgs P = {};
   P.x = static_cast<const uint8_t*>(d_logits);
   P.ld = ld * size;
   P.dx = static_cast<uint8_t*>(d_grad_logits);
@@ -454,10 +901,8 @@ int bo_routing_backward(const bo_routing* h, const void* d_logits, uint32_t dtyp
   P.chosen = h->d_experts;
   P.counts = d_counts ? d_counts : h->d_counts;
   P.real = h->d_real;
-  const uint32_t want = (tokens + kWarps - 1) / kWarps;
-  const uint32_t grid = std::min(want, (uint32_t)sms * 8);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return dtype == BO_FP32 ? route_grad<true>(P, grid, s) : route_grad<false>(P, grid, s);
+  return dtype == BO_FP32 ? route_grad<true>(P, (uint32_t)sms, s) : route_grad<false>(P, (uint32_t)sms, s);
 }
 
 }  // extern "C"

@@ -9,10 +9,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+
 constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
-constexpr uint32_t kMaxBlocks = 304;     // of the forward pass (its partial sums)
-constexpr uint32_t kFewBlocks = 8;       // that join their sums themselves
-constexpr uint32_t kJoinThreads = 1024;
+constexpr uint32_t kMaxCluster = 8;
+constexpr uint32_t kMaxBlocks = 640;     // of the forward pass (its partial sums)
+constexpr uint32_t kJoinThreads = 1024;   // (at least the experts)
 constexpr uint32_t kLane = 16;           // experts that a lane holds
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -57,6 +58,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float rcp(float x) {   // off by one step at most
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -84,15 +90,30 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
   return v;
 }
-// among the lanes that share a token
-__device__ __forceinline__ float lanes_sum(float v, uint32_t lanes) {
-  for (uint32_t d = 1; d < lanes; d *= 2) v += __shfl_xor_sync(kAll, v, d);
-  return v;
-}
-__device__ __forceinline__ float lanes_max(float v, uint32_t lanes) {
-  for (uint32_t d = 1; d < lanes; d *= 2) v = max_nan(v, __shfl_xor_sync(kAll, v, d));
-  return v;
-}
+// Among the lanes that share a token, at most 2^STEPS; steps past them go to the lane itself, without
+// a branch.
+template <int STEPS>
+struct Lanes {
+  uint32_t with[STEPS];
+  float count[STEPS];
+  __device__ __forceinline__ explicit Lanes(uint32_t lanes) {
+#pragma unroll
+    for (int i = 0; i < STEPS; i++) {
+      with[i] = 1u << i < lanes ? 1u << i : 0;
+      count[i] = with[i] ? 1.f : 0.f;
+    }
+  }
+  __device__ __forceinline__ float sum(float v) const {
+#pragma unroll
+    for (int i = 0; i < STEPS; i++) v = fmaf(__shfl_xor_sync(kAll, v, with[i]), count[i], v);
+    return v;
+  }
+  __device__ __forceinline__ float max(float v) const {
+#pragma unroll
+    for (int i = 0; i < STEPS; i++) v = max_nan(v, __shfl_xor_sync(kAll, v, with[i]));
+    return v;
+  }
+};
 template <bool F32>
 __device__ __forceinline__ float element(const uint8_t* row, uint32_t e) {
   return F32 ? reinterpret_cast<const float*>(row)[e]
@@ -155,22 +176,7 @@ template <>
 struct Keys<false> {
   typedef int32_t T;
   static constexpr T kNone = INT32_MIN;
-  // the words' logits are those of experts e0, e0 + 1, ...; past the last expert: none
-  template <int N>
-  static __device__ __forceinline__ void make(const Logits<false, N>& x, uint32_t e0, uint32_t experts, T* k) {
-#pragma unroll
-    for (int i = 0; i < N / 2; i++) {
-      uint32_t v, sign;
-      asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(x.w[i]), "r"(0u));   // one zero, one NaN
-      asm("prmt.b32 %0, %1, %1, 0xBB99;" : "=r"(sign) : "r"(v));          // all ones where negative
-      v ^= sign & 0x7FFF7FFFu;
-      const uint32_t c = 0xFFFFu - e0 - 2 * i;                            // complements
-      const uint32_t lo = __byte_perm(v, c, 0x1054), hi = (v & 0xFFFF0000u) | (c - 1);
-      k[2 * i] = e0 + 2 * i < experts ? (T)lo : kNone;
-      k[2 * i + 1] = e0 + 2 * i + 1 < experts ? (T)hi : kNone;
-    }
-  }
-  static __device__ __forceinline__ T make1(float x, uint32_t e) {
+  static __device__ __forceinline__ T make(float x, uint32_t e) {
     const int32_t s = x != x ? 0x7FFF0000 : __float_as_int(x + 0.f);
     return (s ^ ((s >> 31) & 0x7FFF0000)) | (int32_t)(0xFFFFu - e);
   }
@@ -185,15 +191,9 @@ template <>
 struct Keys<true> {
   typedef long long T;
   static constexpr T kNone = INT64_MIN;
-  static __device__ __forceinline__ T make1(float x, uint32_t e) {
+  static __device__ __forceinline__ T make(float x, uint32_t e) {
     const int32_t s = x != x ? 0x7FFFFFFF : __float_as_int(x + 0.f);
     return (T)((unsigned long long)(uint32_t)(s ^ ((s >> 31) & 0x7FFFFFFF)) << 32 | (uint32_t)~e);
-  }
-  template <int N>
-  static __device__ __forceinline__ void make(const Logits<true, N>& x, uint32_t e0, uint32_t experts, T* k) {
-#pragma unroll
-    for (int i = 0; i < N; i++)
-      k[i] = e0 + i < experts ? make1(__uint_as_float(x.w[i]), e0 + i) : kNone;
   }
   static __device__ __forceinline__ float value(T k) {
     const int32_t s = (int32_t)(k >> 32);
@@ -206,11 +206,62 @@ struct Keys<true> {
     return (T)((unsigned long long)(uint32_t)hi << 32 | lo);
   }
 };
+// The warp's k greatest of NV keys a lane; lane i gets the i-th.  first: the greatest.
+template <bool F32, int NV>
+__device__ __forceinline__ typename Keys<F32>::T choose(typename Keys<F32>::T (&key)[NV],
+                                                        typename Keys<F32>::T first, uint32_t k, uint32_t lane) {
+  typename Keys<F32>::T best = first, mine = 0;
+  for (uint32_t i = 0;;) {
+    if (lane == i) mine = best;
+    if (++i == k) return mine;
+    typename Keys<F32>::T next = Keys<F32>::kNone;
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+      if (key[j] == best) key[j] = Keys<F32>::kNone;
+      next = ::max(key[j], next);
+    }
+    best = Keys<F32>::warp_max(next);
+  }
+}
+
+// k_route_many's keys: 32 bits in which the expert (at most 256) takes the lowest 8.  Of an FP32 logit
+// the lowest 8 bits have to go: keys that differ there alone say nothing about the order.
+template <bool F32>
+struct Short {
+  static constexpr uint32_t kExpertBits = 0xFFu;
+  // of a lane's logits, from expert e0 on.  (What stands in place of experts past the last one,
+  // -infinity, is below every expert's key, and k are chosen of at least as many.)
+  static __device__ __forceinline__ void make(const Logits<F32, kLane>& x, int32_t* k) {
+    if (F32) {
+#pragma unroll
+      for (int i = 0; i < (int)kLane; i++) {
+        const float v = __uint_as_float(x.w[i]);
+        int32_t s = __float_as_int(v + 0.f);
+        s = v != v ? 0x7FFFFFFF : s ^ (int32_t)((uint32_t)(s >> 31) >> 1);
+        k[i] = (s & ~0xFF) | (15 - i);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < (int)kLane / 2; i++) {
+        uint32_t v, sign;
+        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(x.w[i]), "r"(0u));   // one zero, one NaN
+        asm("prmt.b32 %0, %1, %1, 0xBB99;" : "=r"(sign) : "r"(v));          // all ones where negative
+        v ^= sign & 0x7FFF7FFFu;
+        k[2 * i] = (int32_t)__byte_perm(v, 15 - 2 * i, 0x1054);
+        k[2 * i + 1] = (int32_t)__byte_perm(v, 14 - 2 * i, 0x3254);
+      }
+    }
+  }
+  // what is to be added to a lane's keys for its first expert e0
+  static __device__ __forceinline__ int32_t base(uint32_t e0) { return (int32_t)(240 - e0); }
+  static __device__ __forceinline__ uint32_t expert(int32_t k) { return 255 - ((uint32_t)k & 0xFF); }
+  static __device__ __forceinline__ float value(int32_t k) { return Keys<false>::value(k); }   // BF16 alone
+};
 
 // Sorting networks, greatest first.
 template <class T>
 __device__ __forceinline__ void order(T& a, T& b) {
-  const T hi = a > b ? a : b, lo = a > b ? b : a;
+  const T hi = ::max(a, b), lo = ::min(a, b);
   a = hi;
   b = lo;
 }
@@ -236,17 +287,31 @@ __device__ __forceinline__ void clean(T* k) {   // of a bitonic sequence
 template <int N, class T>
 __device__ __forceinline__ void merge(T* a, const T* b) {
 #pragma unroll
-  for (int i = 0; i < N; i++) a[i] = a[i] > b[N - 1 - i] ? a[i] : b[N - 1 - i];
+  for (int i = 0; i < N; i++) a[i] = ::max(a[i], b[N - 1 - i]);
   clean<N>(a);
 }
-// the N greatest of 16, in the first places
-template <int N, class T>
-__device__ __forceinline__ void best_of_16(T* k) {
+// The largest of what merge<N>(a, b) leaves out.
+template <int N>
+__device__ __forceinline__ int32_t left_out(const int32_t* a, const int32_t* b) {
+  int32_t m = INT32_MIN;
+#pragma unroll
+  for (int i = 0; i < N; i++) m = ::max(m, ::min(a[i], b[N - 1 - i]));
+  return m;
+}
+
+// The N greatest of 16, in the first places; with LAST, the greatest of the others is returned.
+template <bool LAST, int N>
+__device__ __forceinline__ int32_t best_of_16(int32_t* k) {
+  int32_t last = INT32_MIN;
   if (N <= 4) {
     sort4(k), sort4(k + 4), sort4(k + 8), sort4(k + 12);
-    merge<4>(k, k + 4), merge<4>(k + 8, k + 12), merge<4>(k, k + 8);
+    if (LAST) last = ::max(left_out<4>(k, k + 4), left_out<4>(k + 8, k + 12));
+    merge<4>(k, k + 4), merge<4>(k + 8, k + 12);
+    if (LAST) last = ::max(last, left_out<4>(k, k + 8));
+    merge<4>(k, k + 8);
   } else if (N <= 8) {
     sort8(k), sort8(k + 8);
+    if (LAST) last = left_out<8>(k, k + 8);
     merge<8>(k, k + 8);
   } else {
     sort8(k), sort8(k + 8);
@@ -254,33 +319,22 @@ __device__ __forceinline__ void best_of_16(T* k) {
     for (int i = 0; i < 8; i++) order(k[i], k[15 - i]);
     clean<8>(k), clean<8>(k + 8);
   }
-}
-// Two lists of each of two lanes that are `stride` apart joined to one: the lane with that bit of its
-// number clear joins the lists `first`, the other one the lists `second`.
-template <int N, class T>
-__device__ __forceinline__ void exchange(const T* first, T* second, bool upper, uint32_t stride) {
-  T other[N];
-#pragma unroll
-  for (int i = 0; i < N; i++) {
-    const T give = upper ? first[i] : second[i];
-    if (!upper) second[i] = first[i];
-    other[i] = __shfl_xor_sync(kAll, give, stride);
-  }
-  merge<N>(second, other);
+  return last;
 }
 
 // ------------------------------------------------------------------- a block's sums and counts
-// In shared memory: counts of each expert, then sums of each warp.  The blocks of a cluster that is
-// the whole grid join them and write the results; else each block leaves its own for k_route_join.
+// In shared memory: counts of each expert, then sums of each warp.  A grid that is one cluster joins its
+// blocks' and writes the results; else each block leaves its own for k_route_join.
 __device__ __forceinline__ void finish(const RouteArgs& P, const int32_t* counts, float* sums, int32_t* reals,
-                                       double* parts, uint32_t warps) {
+                                       float* parts) {
   const uint32_t E = P.experts;
   __syncthreads();
-  for (uint32_t e = threadIdx.x; e < E; e += blockDim.x) {
+  for (uint32_t e = threadIdx.x; e < E; e += kThreads) {   // (the column is this thread's)
     float s = 0.f;
-    for (uint32_t i = 0; i < warps; i++) s += sums[i * E + e];
+#pragma unroll
+    for (uint32_t i = 0; i < kWarps; i++) s += sums[i * E + e];
     if (P.joined) {
-      sums[e] = s;   // (the column is this thread's)
+      sums[e] = s;
     } else {
       P.sums[(uint64_t)blockIdx.x * E + e] = s;
       P.counts[(uint64_t)blockIdx.x * E + e] = counts[e];
@@ -288,7 +342,7 @@ __device__ __forceinline__ void finish(const RouteArgs& P, const int32_t* counts
   }
   if (threadIdx.x == 0) {
     int32_t n = 0;
-    for (uint32_t i = 0; i < warps; i++) n += reals[i];
+    for (uint32_t i = 0; i < kWarps; i++) n += reals[i];
     if (P.joined) reals[0] = n;
     else P.real[blockIdx.x] = n;
   }
@@ -296,81 +350,96 @@ __device__ __forceinline__ void finish(const RouteArgs& P, const int32_t* counts
   const cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
   if (blockIdx.x == 0) {
+    const uint32_t C = gridDim.x;
     int32_t N = 0;
-    for (uint32_t b = 0; b < gridDim.x; b++) N += *cluster.map_shared_rank(reals, b);
-    double share = 0;
-    for (uint32_t e = threadIdx.x; e < E; e += blockDim.x) {
-      float v[kFewBlocks];
-      int32_t c[kFewBlocks], n = 0;
+    for (uint32_t b = 0; b < C; b++) N += *cluster.map_shared_rank(reals, b);
+    float share = 0.f;
+    for (uint32_t e = threadIdx.x; e < E; e += kThreads) {
+      float v[kMaxCluster], s = 0.f;
+      int32_t m[kMaxCluster], n = 0;
 #pragma unroll
-      for (uint32_t b = 0; b < kFewBlocks; b++) {
-        v[b] = b < gridDim.x ? cluster.map_shared_rank(sums, b)[e] : 0.f;
-        c[b] = b < gridDim.x ? cluster.map_shared_rank(counts, b)[e] : 0;
+      for (uint32_t b = 0; b < kMaxCluster; b++) {
+        v[b] = b < C ? cluster.map_shared_rank(sums, b)[e] : 0.f;
+        m[b] = b < C ? cluster.map_shared_rank(counts, b)[e] : 0;
       }
-      double s = 0;
 #pragma unroll
-      for (uint32_t b = 0; b < kFewBlocks; b++) s += v[b], n += c[b];
-      const double p = N > 0 ? s / N : 0;
-      P.out_probs[e] = (float)p;
+      for (uint32_t b = 0; b < kMaxCluster; b++) s += v[b], n += m[b];
+      const float p = N > 0 ? s / (float)N : 0.f;
+      P.out_probs[e] = p;
       P.out_counts[e] = n;
-      share += p * n;
+      share += p * (float)n;
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) share += __shfl_xor_sync(kAll, share, d);
+    share = warp_sum(share);
     if (threadIdx.x % 32 == 0) parts[threadIdx.x / 32] = share;
     __syncthreads();
     if (threadIdx.x == 0) {
-      for (uint32_t i = 1; i < warps; i++) share += parts[i];
-      *P.out_loss = N > 0 ? (float)(share * E / ((double)N * P.k)) : 0.f;
+      for (uint32_t i = 1; i < kWarps; i++) share += parts[i];
+      *P.out_loss = N > 0 ? share / (float)N * ((float)E / (float)P.k) : 0.f;
       *P.out_real = N;
     }
   }
   cluster.sync();   // (the others' memory is read until here)
 }
 
-// Joins the blocks' sums and counts: several slices of the blocks at a time, in a fixed order.
+// Joins the blocks' sums and counts.  Each block of the one cluster takes a part of the experts; its
+// threads read as many slices of the blocks' rows at a time as there is room for, and a warp joins the
+// slices of an expert.  Every sum has a fixed order.  (In FP32: with FP64, of which an SM does a few
+// operations a cycle, 304 rows of 128 experts took 32 us.)
 __global__ void __launch_bounds__(kJoinThreads) k_route_join(const RouteArgs P, uint32_t blocks) {
-  __shared__ double sums[kJoinThreads];
-  __shared__ int32_t counts[kJoinThreads];
-  __shared__ double parts[kJoinThreads / 32];
+  __shared__ float sums[2 * kJoinThreads];
+  __shared__ int32_t counts[2 * kJoinThreads];
+  __shared__ float parts[kJoinThreads / 32], shares[1];
   __shared__ int32_t reals[kJoinThreads / 32];
   after_previous();
+  const cg::cluster_group cluster = cg::this_cluster();
   const uint32_t E = P.experts, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  int32_t r = threadIdx.x < blocks ? P.real[threadIdx.x] : 0;
-  r = __reduce_add_sync(kAll, r);
-  if (lane == 0) reals[warp] = r;
-  const uint32_t slices = kJoinThreads / E, slice = threadIdx.x / E, e = threadIdx.x % E;
-  double s = 0;
-  int32_t c = 0;
-  if (slice < slices) {
+  const uint32_t C = gridDim.x, width = (E + C - 1) / C, first = blockIdx.x * width;
+  const uint32_t slices = kJoinThreads / width, slice = threadIdx.x / width, col = threadIdx.x % width;
+  float s = 0.f;
+  int32_t c = 0, r = 0;
+  if (slice < slices && first + col < E) {
 #pragma unroll 8
     for (uint32_t b = slice; b < blocks; b += slices) {
-      s += P.sums[(uint64_t)b * E + e];
-      c += P.counts[(uint64_t)b * E + e];
+      s += P.sums[(uint64_t)b * E + first + col];
+      c += P.counts[(uint64_t)b * E + first + col];
     }
   }
-  sums[threadIdx.x] = s;
-  counts[threadIdx.x] = c;
-  __syncthreads();
-  int32_t N = 0;
-  for (uint32_t i = 0; i < kJoinThreads / 32; i++) N += reals[i];
-  double share = 0;
-  if (threadIdx.x < E) {
-    for (uint32_t i = 1; i < slices; i++) s += sums[i * E + e], c += counts[i * E + e];
-    const double p = N > 0 ? s / N : 0;
-    P.out_probs[e] = (float)p;
-    P.out_counts[e] = c;
-    share = p * c;
+  for (uint32_t b = threadIdx.x; b < blocks; b += kJoinThreads) r += P.real[b];
+  if (slice < slices) {
+    sums[slice * (width + 1) + col] = s;   // (a column's entries fall into different banks)
+    counts[slice * (width + 1) + col] = c;
   }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) share += __shfl_xor_sync(kAll, share, d);
+  r = __reduce_add_sync(kAll, r);
+  if (lane == 0) reals[warp] = r;
+  __syncthreads();
+  const int32_t N = __reduce_add_sync(kAll, reals[lane]);
+  float share = 0.f;
+  for (uint32_t i = warp; i < width && first + i < E; i += kJoinThreads / 32) {
+    s = 0.f;
+    c = 0;
+    for (uint32_t j = lane; j < slices; j += 32) s += sums[j * (width + 1) + i], c += counts[j * (width + 1) + i];
+    s = warp_sum(s);
+    c = __reduce_add_sync(kAll, c);
+    const float p = N > 0 ? s / (float)N : 0.f;
+    if (lane == 0) {
+      P.out_probs[first + i] = p;
+      P.out_counts[first + i] = c;
+    }
+    share += p * (float)c;
+  }
   if (lane == 0) parts[warp] = share;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (uint32_t i = 1; i < kJoinThreads / 32; i++) share += parts[i];
-    *P.out_loss = N > 0 ? (float)(share * E / ((double)N * P.k)) : 0.f;
+  if (warp == 0) {
+    share = warp_sum(parts[lane]);
+    shares[0] = share;
+  }
+  cluster.sync();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    for (uint32_t b = 1; b < C; b++) share += *cluster.map_shared_rank(shares, b);
+    *P.out_loss = N > 0 ? share / (float)N * ((float)E / (float)P.k) : 0.f;
     *P.out_real = N;
   }
+  cluster.sync();   // (the others' memory is read until here)
 }
 
 // ------------------------------------------------------------------------------ forward pass
@@ -382,7 +451,7 @@ __global__ void __launch_bounds__(kThreads) k_route(const RouteArgs P) {
   int32_t* counts = reinterpret_cast<int32_t*>(sh);
   float* sums = reinterpret_cast<float*>(sh + P.experts);
   __shared__ int32_t reals[kWarps];
-  __shared__ double parts[kWarps];
+  __shared__ float parts[kWarps];
   typedef Keys<F32> K;
   typedef typename K::T Key;
   after_previous();
@@ -393,7 +462,7 @@ __global__ void __launch_bounds__(kThreads) k_route(const RouteArgs P) {
 #pragma unroll
   for (int j = 0; j < NV; j++) total[j] = 0.f;
   int32_t real = 0;
-  for (uint64_t t = (uint64_t)blockIdx.x * kWarps + warp; t < P.tokens; t += (uint64_t)gridDim.x * kWarps) {
+  for (uint64_t t = (uint64_t)warp * gridDim.x + blockIdx.x; t < P.tokens; t += (uint64_t)gridDim.x * kWarps) {
     const uint8_t* row = P.x + t * P.ld;
     bool use = !P.mask || P.mask[t * P.mask_stride] != 0;
     Key key[NV], mine = 0;   // lane i: the i-th choice
@@ -404,10 +473,10 @@ __global__ void __launch_bounds__(kThreads) k_route(const RouteArgs P) {
       for (int j = 0; j < NV; j++) {
         const uint32_t e = lane + 32 * j;
         p[j] = e < E ? element<F32>(row, e) : __int_as_float(0xFF800000);
-        key[j] = e < E ? K::make1(p[j], e) : K::kNone;
-        top = key[j] > top ? key[j] : top;
+        key[j] = e < E ? K::make(p[j], e) : K::kNone;
+        top = ::max(key[j], top);
       }
-      Key best = K::warp_max(top);
+      const Key best = K::warp_max(top);
       const float max = K::value(best);
       use = max != __int_as_float(0xFF800000);
       if (use) {
@@ -420,17 +489,7 @@ __global__ void __launch_bounds__(kThreads) k_route(const RouteArgs P) {
         const float inv = 1.f / sum;
 #pragma unroll
         for (int j = 0; j < NV; j++) total[j] += p[j] * inv;
-        for (uint32_t i = 0;;) {
-          if (lane == i) mine = best;
-          if (++i == P.k) break;
-          Key next = K::kNone;
-#pragma unroll
-          for (int j = 0; j < NV; j++) {
-            if (key[j] == best) key[j] = K::kNone;
-            next = key[j] > next ? key[j] : next;
-          }
-          best = K::warp_max(next);
-        }
+        mine = choose<F32, NV>(key, best, P.k, lane);
         w = lane < P.k ? ex2((K::value(mine) - max) * kLog2e) : 0.f;
         w *= P.normalize ? 1.f / warp_sum(w) : inv;
         if (lane < P.k) atomicAdd(&counts[K::expert(mine)], 1);
@@ -448,7 +507,7 @@ __global__ void __launch_bounds__(kThreads) k_route(const RouteArgs P) {
     if (e < E) sums[warp * E + e] = total[j];
   }
   if (lane == 0) reals[warp] = real;
-  finish(P, counts, sums, reals, parts, kWarps);
+  finish(P, counts, sums, reals, parts);
 }
 
 // A warp takes 32 tokens at a time.  `lanes` lanes share a token, 16 experts each, so that it takes
@@ -456,19 +515,47 @@ __global__ void __launch_bounds__(kThreads) k_route(const RouteArgs P) {
 // join their lists in pairs as soon as two rounds have one each: one of the two lanes goes on with the
 // first round's token, the other with the second's.  After all rounds each lane has the whole list
 // of one token, the one with the lane's number among the 32: a join costs each list once, and not
-// each lane.
+// each lane.  Lists that wait lie in shared memory.
 template <bool F32, int KL>
-__global__ void __launch_bounds__(kThreads, F32 ? 1 : 2) k_route_many(const RouteArgs P) {
-  extern __shared__ uint32_t sh[];
-  int32_t* counts = reinterpret_cast<int32_t*>(sh);
-  float* sums = reinterpret_cast<float*>(sh + P.experts);
+struct Lists {
+  int4 key[KL / 4][32];
+  int32_t out[F32 ? 32 : 1];   // the greatest key that is not in the list
+};
+template <bool F32, int KL>
+__device__ __forceinline__ void put(Lists<F32, KL>& l, uint32_t lane, const int32_t* k, int32_t out) {
+#pragma unroll
+  for (int i = 0; i < KL / 4; i++) l.key[i][lane] = make_int4(k[4 * i], k[4 * i + 1], k[4 * i + 2], k[4 * i + 3]);
+  if (F32) l.out[lane] = out;
+}
+template <bool F32, int KL>
+__device__ __forceinline__ int32_t get(const Lists<F32, KL>& l, uint32_t lane, int32_t* k) {
+#pragma unroll
+  for (int i = 0; i < KL / 4; i++) {
+    const int4 v = l.key[i][lane];
+    k[4 * i] = v.x, k[4 * i + 1] = v.y, k[4 * i + 2] = v.z, k[4 * i + 3] = v.w;
+  }
+  return F32 ? l.out[lane] : 0;
+}
+constexpr uint32_t kLevels = 4;   // 16 lanes a token at most: 256 experts
+template <bool F32, int KL>
+struct Waiting {
+  static constexpr uint32_t kBytes = kWarps * (kLevels + 1) * (uint32_t)sizeof(Lists<F32, KL>);
+};
+
+template <bool F32, int KL>
+__global__ void __launch_bounds__(kThreads, 2) k_route_many(const RouteArgs P) {
+  extern __shared__ int4 sh4[];
+  typedef Lists<F32, KL> L;
+  typedef Short<F32> S;
+  int32_t* counts = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(sh4) + Waiting<F32, KL>::kBytes);
+  float* sums = reinterpret_cast<float*>(counts + P.experts);
   __shared__ int32_t reals[kWarps];
-  __shared__ double parts[kWarps];
-  typedef Keys<F32> K;
-  typedef typename K::T Key;
+  __shared__ float parts[kWarps];
   after_previous();
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = P.experts, G = P.lanes;
   const uint32_t g = lane % G, q = lane / G, e0 = g * kLane;
+  const Lanes<kLevels> lanes(G);
+  L* const wait = reinterpret_cast<L*>(sh4) + warp * (kLevels + 1);
   for (uint32_t e = threadIdx.x; e < E; e += kThreads) counts[e] = 0;
   __syncthreads();
   const uint32_t units = (P.tokens + 31) / 32, step = gridDim.x * kWarps;
@@ -484,19 +571,19 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : 2) k_route_many(const Rout
     if (use_ahead) ahead.load(P.x + t * P.ld, e0, E, P.vec);
     else ahead.clear();
   };
-  uint32_t unit = blockIdx.x * kWarps + warp;
+  uint32_t unit = warp * gridDim.x + blockIdx.x;
   if (unit < units) fetch(unit, 0);
   for (; unit < units; unit += step) {
-    float sum_mine = 0.f;
+    float sum_mine = 0.f, max_mine = 0.f;
     bool use_mine = false;
-    uint32_t round = 0;
-    Key list[kLane], l0[KL], l1[KL], l2[KL], l3[KL];
-    auto take = [&]() {      // one round
+    int32_t list[kLane], out = INT32_MIN;
+#pragma unroll 1
+    for (uint32_t round = 0; round < G; round++) {
       const Logits<F32, kLane> x = ahead;
       bool use = use_ahead;
       if (round + 1 < G) fetch(unit, round + 1);
       else if (unit + step < units) fetch(unit + step, 0);
-      float max = lanes_max(x.max(), G);
+      float max = lanes.max(x.max());
       if (max == __int_as_float(0xFF800000)) use = false, max = 0.f;
       float2 e[kLane / 2], s = make_float2(0.f, 0.f);
 #pragma unroll
@@ -505,66 +592,81 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : 2) k_route_many(const Rout
         e[j] = make_float2(ex2(d.x), ex2(d.y));
         s = __fadd2_rn(s, e[j]);
       }
-      const float sum = lanes_sum(s.x + s.y, G);
-      const float inv = use ? 1.f / sum : 0.f;
+      const float sum = lanes.sum(s.x + s.y);
+      const float inv = use ? rcp(sum) : 0.f;
 #pragma unroll
       for (int j = 0; j < (int)kLane / 2; j++) total[j] = __ffma2_rn(e[j], make_float2(inv, inv), total[j]);
-      if (round == g) sum_mine = sum, use_mine = use;
-      K::make(x, e0, E, list);
-      best_of_16<KL>(list);
-      round++;
-    };
-    auto keep = [&](Key* to) {
+      if (round == g) sum_mine = sum, max_mine = max, use_mine = use;
+      S::make(x, list);
+      out = best_of_16<F32, KL>(list);
 #pragma unroll
-      for (int i = 0; i < KL; i++) to[i] = list[i];
-    };
-    // (loops of one or two turns: only one copy of a round's code)
+      for (int i = 0; i < KL; i++) list[i] += S::base(e0);
+      if (F32) out += S::base(e0);
+      // join as many times as the round's number ends in ones, then wait
+      uint32_t level = 0;
 #pragma unroll 1
-    for (uint32_t c = 0;; c++) {
-#pragma unroll 1
-      for (uint32_t b = 0;; b++) {
-#pragma unroll 1
-        for (uint32_t a = 0;; a++) {
-#pragma unroll 1
-          for (uint32_t i = 0;; i++) {
-            take();
-            if (G < 2) break;
-            if (i) {
-              exchange<KL>(l0, list, lane & 1, 1);
-              break;
-            }
-            keep(l0);
-          }
-          if (G < 4) break;
-          if (a) {
-            exchange<KL>(l1, list, lane & 2, 2);
-            break;
-          }
-          keep(l1);
-        }
-        if (G < 8) break;
-        if (b) {
-          exchange<KL>(l2, list, lane & 4, 4);
-          break;
-        }
-        keep(l2);
+      for (; (round >> level & 1) != 0; level++) {
+        put(wait[kLevels], lane, list, out);
+        __syncwarp();
+        const L& from = lane >> level & 1 ? wait[kLevels] : wait[level];
+        int32_t other[KL];
+        const int32_t out1 = get(from, lane, list), out2 = get(from, lane ^ (1u << level), other);
+        if (F32) out = ::max(::max(out1, out2), left_out<KL>(list, other));
+        merge<KL>(list, other);
+        __syncwarp();
       }
-      if (G < 16) break;
-      if (c) {
-        exchange<KL>(l3, list, lane & 8, 8);
-        break;
-      }
-      keep(l3);
+      if (round + 1 < G) put(wait[level], lane, list, out);
     }
     const uint64_t t = (uint64_t)unit * 32 + lane;
     if (t >= P.tokens) use_mine = false;
     real += __popc(__ballot_sync(kAll, use_mine));
+    uint32_t expert[KL];
+    float x[KL];
+#pragma unroll
+    for (int i = 0; i < KL; i++) {
+      expert[i] = S::expert(list[i]);
+      x[i] = F32 ? 0.f : S::value(list[i]);
+    }
+    if (F32) {
+      const float* row = reinterpret_cast<const float*>(P.x + t * P.ld);
+      bool unsure = false;
+      if (use_mine) {
+#pragma unroll
+        for (int i = 0; i < KL; i++)
+          if (i < (int)P.k) x[i] = row[expert[i]];
+        // keys that are alike but for the expert: in order by the whole logits, or to be done again
+#pragma unroll
+        for (int i = 0; i < KL; i++) {
+          const int32_t next = i + 1 < KL ? list[i + 1 < KL ? i + 1 : i] : out;
+          if (i < (int)P.k && ((uint32_t)list[i] ^ (uint32_t)next) <= S::kExpertBits)
+            if (i + 1 >= (int)P.k || !(x[i] >= x[i + 1 < KL ? i + 1 : i])) unsure = true;
+        }
+      }
+      for (uint32_t who = __ballot_sync(kAll, unsure); who; who &= who - 1) {
+        const uint32_t src = __ffs(who) - 1;
+        const uint8_t* again = P.x + ((uint64_t)unit * 32 + src) * P.ld;
+        typedef Keys<F32> K;
+        typename K::T key[kLane / 2], top = K::kNone;
+#pragma unroll
+        for (int j = 0; j < (int)kLane / 2; j++) {
+          const uint32_t e = lane + 32 * j;
+          key[j] = e < E ? K::make(element<F32>(again, e), e) : K::kNone;
+          top = ::max(top, key[j]);
+        }
+        const typename K::T mine = choose<F32, (int)kLane / 2>(key, K::warp_max(top), P.k, lane);
+#pragma unroll
+        for (int i = 0; i < KL; i++) {
+          const uint32_t ei = __shfl_sync(kAll, K::expert(mine), i);
+          const float xi = __shfl_sync(kAll, K::value(mine), i);
+          if (lane == src && i < (int)P.k) expert[i] = ei, x[i] = xi;
+        }
+      }
+    }
     if (t < P.tokens) {
-      const float max = K::value(list[0]);
       float w[KL], s[KL];
 #pragma unroll
       for (int i = 0; i < KL; i++) {
-        w[i] = ex2((K::value(list[i]) - max) * kLog2e);
+        w[i] = ex2((x[i] - max_mine) * kLog2e);
         s[i] = i < (int)P.k ? w[i] : 0.f;
       }
 #pragma unroll
@@ -574,20 +676,20 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : 2) k_route_many(const Rout
       const float inv = 1.f / (P.normalize ? s[0] : sum_mine);
       float* to = P.weights + t * P.k;
       int32_t* at = P.chosen + t * P.k;
-      uint32_t wo[KL], eo[KL];
+      uint32_t wo[KL];
 #pragma unroll
       for (int i = 0; i < KL; i++) {
         wo[i] = use_mine ? __float_as_uint(w[i] * inv) : 0u;
-        eo[i] = use_mine ? K::expert(list[i]) : 0xffffffffu;
-        if (use_mine && i < (int)P.k) atomicAdd(&counts[eo[i]], 1);
+        if (use_mine && i < (int)P.k) atomicAdd(&counts[expert[i]], 1);
+        if (!use_mine) expert[i] = 0xffffffffu;
       }
       if (KL == 8 && P.k == 8) {
         st32(to, wo);
-        st32(at, eo);
+        st32(at, expert);
       } else {
 #pragma unroll
         for (int i = 0; i < KL; i++)
-          if (i < (int)P.k) to[i] = __uint_as_float(wo[i]), at[i] = (int32_t)eo[i];
+          if (i < (int)P.k) to[i] = __uint_as_float(wo[i]), at[i] = (int32_t)expert[i];
       }
     }
   }
@@ -601,51 +703,63 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : 2) k_route_many(const Rout
     if (q == 0 && e0 + 2 * j + 1 < E) sums[warp * E + e0 + 2 * j + 1] = total[j].y;
   }
   if (lane == 0) reals[warp] = real;
-  finish(P, counts, sums, reals, parts, kWarps);
+  finish(P, counts, sums, reals, parts);
 }
 
 // ----------------------------------------------------------------------------- backward pass
 // `lanes` lanes share a token, N experts each and at most one of its choices each.  The choices'
 // logits get their gradient on top of the others' a second time, from the lanes that hold them.
 template <bool F32, int N>
-__global__ void __launch_bounds__(kThreads) k_route_grad(const RouteGradArgs P) {
-  extern __shared__ float share[];   // dL/dp of each expert
+__global__ void __launch_bounds__(kThreads, 2) k_route_grad(const RouteGradArgs P) {
+  extern __shared__ float share[];   // how often each expert was chosen
   __shared__ long long parts[kWarps];
   after_previous();
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = P.experts, G = P.lanes;
   const uint32_t g = lane % G, q = lane / G, e0 = g * N, per = 32 / G;
+  const Lanes<5> lanes(G);
+  const uint64_t groups = ((uint64_t)P.tokens + per - 1) / per, step = (uint64_t)gridDim.x * kWarps;
+  uint64_t n = (uint64_t)warp * gridDim.x + blockIdx.x;
+  Logits<F32, N> x;
+  int32_t mine;
+  float gw;
+  auto fetch = [&]() {
+    const uint64_t t = n * per + q;
+    const bool choose = t < P.tokens && g < P.k;
+    mine = choose ? P.chosen[t * P.k + g] : -1;
+    gw = choose && P.gw ? P.gw[t * P.gw_stride + g * P.gw_choice] : 0.f;
+    if (t < P.tokens) x.load(P.x + t * P.ld, e0, E, P.vec);
+    else x.clear();
+  };
+  if (n < groups) fetch();   // (under way while the experts' shares are worked out)
   long long sum = 0;
-  for (uint32_t e = threadIdx.x; e < E; e += kThreads) sum += P.counts[e];
+  for (uint32_t e = threadIdx.x; e < E; e += kThreads) {
+    const int32_t m = P.counts[e];
+    share[e] = (float)m;
+    sum += m;
+  }
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
   if (lane == 0) parts[warp] = sum;
   __syncthreads();
   sum = 0;
+#pragma unroll
   for (uint32_t i = 0; i < kWarps; i++) sum += parts[i];
   const int32_t real = *P.real;
   const float gl = P.gloss ? *P.gloss : P.loss;
-  const float unit = sum > 0 && real > 0 ? (float)((double)gl * E / ((double)sum * real)) : 0.f;
-  for (uint32_t e = threadIdx.x; e < E; e += kThreads) share[e] = unit * P.counts[e];
-  __syncthreads();
+  const float unit = sum > 0 && real > 0 ? gl * ((float)E / (float)real) / (float)sum : 0.f;
   float2 c[N / 2];
 #pragma unroll
   for (int j = 0; j < N / 2; j++)
-    c[j] = make_float2(e0 + 2 * j < E ? share[e0 + 2 * j] : 0.f, e0 + 2 * j + 1 < E ? share[e0 + 2 * j + 1] : 0.f);
-  const uint64_t groups = ((uint64_t)P.tokens + per - 1) / per;
-  for (uint64_t n = (uint64_t)blockIdx.x * kWarps + warp; n < groups; n += (uint64_t)gridDim.x * kWarps) {
+    c[j] = make_float2(e0 + 2 * j < E ? unit * share[e0 + 2 * j] : 0.f, e0 + 2 * j + 1 < E ? unit * share[e0 + 2 * j + 1] : 0.f);
+  for (; n < groups; n += step) {
     const uint64_t t = n * per + q;
     const bool there = t < P.tokens;
-    const bool choose = there && g < P.k;
     const uint8_t* row = P.x + t * P.ld;
     uint8_t* out = P.dx + t * P.ld_dx;
-    const int32_t mine = choose ? P.chosen[t * P.k + g] : -1;
-    const float gw = choose && P.gw ? P.gw[t * P.gw_stride + g * P.gw_choice] : 0.f;
-    Logits<F32, N> x;
-    if (there) x.load(row, e0, E, P.vec);
-    else x.clear();
+    if (step <= n) fetch();
     const float xm = mine >= 0 ? element<F32>(row, (uint32_t)mine) : 0.f;
     const bool use = __shfl_sync(kAll, mine, q * G) >= 0;
-    const float max = lanes_max(x.max(), G);
+    const float max = lanes.max(x.max());
     float2 p[N / 2], s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < N / 2; j++) {
@@ -653,7 +767,7 @@ __global__ void __launch_bounds__(kThreads) k_route_grad(const RouteGradArgs P) 
       p[j] = make_float2(ex2(d.x), ex2(d.y));
       s = __fadd2_rn(s, p[j]);
     }
-    const float inv = 1.f / lanes_sum(s.x + s.y, G);
+    const float inv = rcp(lanes.sum(s.x + s.y));
     float2 dots = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < N / 2; j++) {
@@ -664,13 +778,13 @@ __global__ void __launch_bounds__(kThreads) k_route_grad(const RouteGradArgs P) 
     const float pm = mine >= 0 ? ex2((xm - max) * kLog2e) * inv : 0.f;
     float add;                         // what the choice adds to its logit
     if (P.normalize) {
-      const float w = pm / lanes_sum(pm, G);
-      add = w * (gw - lanes_sum(mine >= 0 ? w * gw : 0.f, G));
+      const float w = pm * rcp(lanes.sum(pm));
+      add = w * (gw - lanes.sum(mine >= 0 ? w * gw : 0.f));
     } else {
       add = pm * gw;
       dot += mine >= 0 ? add : 0.f;
     }
-    dot = lanes_sum(dot, G);
+    dot = lanes.sum(dot);
     __syncwarp();   // (the rows are read: their gradients may take their place)
     if (there) {
       uint32_t o[Logits<F32, N>::kWords];
@@ -695,7 +809,7 @@ __global__ void __launch_bounds__(kThreads) k_route_grad(const RouteGradArgs P) 
     }
     __syncwarp();
     if (mine >= 0) {
-      const float d = pm * (share[mine] - dot) + add;
+      const float d = pm * (unit * share[mine] - dot) + add;
       if (F32) reinterpret_cast<float*>(out)[mine] = d;
       else reinterpret_cast<uint16_t*>(out)[mine] = (uint16_t)pack_bf16(d, 0.f);
     }
@@ -754,25 +868,31 @@ int route(RouteArgs& P, uint32_t sms, cudaStream_t s) {
   const uint32_t nv = (P.experts + 31) / 32;
   auto one = nv <= 1 ? k_route<F32, 1> : nv <= 2 ? k_route<F32, 2> : nv <= 4 ? k_route<F32, 4>
            : nv <= 8 ? k_route<F32, 8> : nv <= 16 ? k_route<F32, 16> : k_route<F32, 32>;
-  if (P.tokens <= kFewBlocks * kWarps * 2) {   // one launch
-    const uint32_t grid = P.tokens <= kWarps ? 1 : P.tokens <= 2 * kWarps ? 2 : P.tokens <= 4 * kWarps ? 4 : kFewBlocks;
+  if (P.tokens <= kMaxCluster * kWarps * 2) {   // one launch
+    const uint32_t grid = P.tokens <= kWarps ? 1 : P.tokens <= 2 * kWarps ? 2 : P.tokens <= 4 * kWarps ? 4 : kMaxCluster;
     P.joined = 1;
     return check(launch(one, dim3(grid), kThreads, smem, grid, s, P));
   }
   P.joined = 0;
+  const uint32_t lanes = power_of_two((P.experts + kLane - 1) / kLane);
   uint32_t grid;
   int rc;
-  if (P.tokens > sms * 2 * kWarps && P.experts <= 16 * kLane && P.k <= 16) {
-    P.lanes = power_of_two((P.experts + kLane - 1) / kLane);
+  // (Where a warp a token and 32 tokens a warp meet: 8 experts at 7000 tokens, 64 at 10000, 128 at
+  // 15000, 256 at 19000.)
+  if (P.tokens > 5000 + 1000 * lanes && lanes <= 1u << kLevels && P.k <= 16) {
+    P.lanes = lanes;
     P.vec = whole(P.x, P.ld, P.experts, kLane);
-    grid = std::min({((P.tokens + 31) / 32 + kWarps - 1) / kWarps, sms * 2, kMaxBlocks});
-    auto many = P.k <= 4 ? k_route_many<F32, 4> : P.k <= 8 ? k_route_many<F32, 8> : k_route_many<F32, 16>;
-    rc = check(launch(many, dim3(grid), kThreads, smem, 1, s, P));
+    grid = std::min({(P.tokens + 31) / 32, sms * 2, kMaxBlocks});
+    rc = P.k <= 4   ? check(launch(k_route_many<F32, 4>, dim3(grid), kThreads, smem + Waiting<F32, 4>::kBytes, 1, s, P))
+         : P.k <= 8 ? check(launch(k_route_many<F32, 8>, dim3(grid), kThreads, smem + Waiting<F32, 8>::kBytes, 1, s, P))
+                    : check(launch(k_route_many<F32, 16>, dim3(grid), kThreads, smem + Waiting<F32, 16>::kBytes, 1, s, P));
   } else {
-    grid = std::min({(P.tokens + kWarps - 1) / kWarps, sms * 2, kMaxBlocks});
+    grid = std::min({(P.tokens + kWarps - 1) / kWarps, sms * 3, kMaxBlocks});
     rc = check(launch(one, dim3(grid), kThreads, smem, 1, s, P));
   }
-  return rc ? rc : check(launch(k_route_join, dim3(1), kJoinThreads, 0, 1, s, P, grid));
+  if (rc) return rc;
+  const uint32_t C = std::min(power_of_two((P.experts + 7) / 8), kMaxCluster);
+  return check(launch(k_route_join, dim3(C), kJoinThreads, 0, C, s, P, grid));
 }
 template <bool F32>
 int route_grad(RouteGradArgs& P, uint32_t sms, cudaStream_t s) {
@@ -781,7 +901,7 @@ int route_grad(RouteGradArgs& P, uint32_t sms, cudaStream_t s) {
   P.vec = whole(P.x, P.ld, P.experts, each);
   P.vec_dx = whole(P.dx, P.ld_dx, P.experts, each);
   const uint64_t groups = ((uint64_t)P.tokens * P.lanes + 31) / 32;
-  const uint32_t grid = (uint32_t)std::min<uint64_t>((groups + kWarps - 1) / kWarps, sms * 8);
+  const uint32_t grid = (uint32_t)std::min<uint64_t>((groups + kWarps - 1) / kWarps, sms * 2);
   return check(launch(each == kLane ? k_route_grad<F32, kLane> : k_route_grad<F32, 2 * kLane>, dim3(grid), kThreads,
                       P.experts * 4, 1, s, P));
 }

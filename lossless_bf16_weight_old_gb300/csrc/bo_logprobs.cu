@@ -5,6 +5,7 @@
 // the first and the last may lie partly outside the row, and are read by the element.
 #include <cfloat>
 #include <cmath>
+#include <cstdlib>
 #include <cooperative_groups.h>
 
 #include "bo_internal.cuh"
@@ -13,8 +14,13 @@ namespace bo {
 namespace {
 
 namespace cg = cooperative_groups;
+#ifndef LB
+#define LB 4
+#endif
+
 
 constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
+constexpr uint32_t kMaxCluster = 8;
 constexpr uint32_t kWindow = 64;                 // bytes
 constexpr uint32_t kSegment = kThreads * 32;     // windows whose maxima are kept at once
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
@@ -92,6 +98,22 @@ __device__ __forceinline__ float element(const uint8_t* p) {
              : __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(p) << 16);
 }
 
+// A key orders values and, of equal ones, places (the lowest first); 0 is below every key.
+typedef unsigned long long Key;
+__device__ __forceinline__ uint32_t order_of(float x) {
+  if (x != x) return 0xFFFFFFFFu;
+  const uint32_t u = __float_as_uint(x + 0.f);   // (-0 is 0)
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ Key key_of(uint32_t order, uint32_t place) {
+  return (Key)order << 32 | (uint32_t)~place;
+}
+__device__ __forceinline__ uint32_t place_of(Key k) { return ~(uint32_t)k; }
+
+
 // The windows of a row.
 template <bool F32>
 struct Windows {
@@ -110,6 +132,12 @@ struct Windows {
   __device__ __forceinline__ int32_t first(uint32_t w) const { return (int32_t)(w * kElems) - (int32_t)off; }
   __device__ __forceinline__ bool whole(uint32_t w) const {
     return first(w) >= 0 && first(w) + kElems <= vocab;
+  }
+  // the key of the lane's element of a window; 0 outside the row
+  __device__ __forceinline__ Key key(uint32_t w, uint32_t lane) const {
+    const int32_t e = first(w) + (int32_t)lane;
+    if (lane >= kElems || e < 0 || e >= (int32_t)vocab) return 0;
+    return key_of(order_of(element<F32>(row + (int64_t)e * kSize)), (uint32_t)e);
   }
   // the window's words; -infinity outside the row
   __device__ __forceinline__ void load(uint32_t w, uint32_t (&lo)[8], uint32_t (&hi)[8]) const {
@@ -203,6 +231,10 @@ __device__ __forceinline__ void add_window(Sums<ENT>& a, const uint32_t (&lo)[8]
 }
 struct Joined {
   float max, s, t;
+  __device__ __forceinline__ Joined from(int d) const {   // another lane's
+    return Joined{__shfl_xor_sync(0xffffffffu, max, d), __shfl_xor_sync(0xffffffffu, s, d),
+                  __shfl_xor_sync(0xffffffffu, t, d)};
+  }
   __device__ __forceinline__ void join(const Joined& o, float scale) {
     const float m = fmaxf(max, o.max);
     const float da = fmaxf((max - m) * scale, -200.f), db = fmaxf((o.max - m) * scale, -200.f);
@@ -214,21 +246,6 @@ struct Joined {
 };
 
 // ------------------------------------------------------------------------------- top tokens
-// A key orders values and, of equal ones, places (the lowest first); 0 is below every key.
-typedef unsigned long long Key;
-__device__ __forceinline__ uint32_t order_of(float x) {
-  if (x != x) return 0xFFFFFFFFu;
-  const uint32_t u = __float_as_uint(x + 0.f);   // (-0 is 0)
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-__device__ __forceinline__ float value_of(uint32_t o) {
-  return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
-}
-__device__ __forceinline__ Key key_of(uint32_t order, uint32_t place) {
-  return (Key)order << 32 | (uint32_t)~place;
-}
-__device__ __forceinline__ uint32_t place_of(Key k) { return ~(uint32_t)k; }
-
 __device__ __forceinline__ Key step(Key v, uint32_t stride, bool keep_max) {
   const Key o = __shfl_xor_sync(0xffffffffu, v, stride);
   return (v > o) == keep_max ? v : o;
@@ -264,50 +281,124 @@ __device__ __forceinline__ void join_lists(Key mine, Key (*lists)[32], uint32_t 
     __syncthreads();
   }
 }
+// the same of the numbers that order values alone
+__device__ __forceinline__ uint32_t step(uint32_t v, uint32_t stride, bool keep_max) {
+  const uint32_t o = __shfl_xor_sync(0xffffffffu, v, stride);
+  return keep_max ? max(v, o) : min(v, o);
+}
+__device__ __forceinline__ uint32_t sorted(uint32_t v, uint32_t lane) {
+#pragma unroll
+  for (uint32_t size = 2; size <= 32; size *= 2)
+#pragma unroll
+    for (uint32_t stride = size / 2; stride; stride /= 2)
+      v = step(v, stride, ((lane & stride) == 0) == ((lane & size) == 0));
+  return v;
+}
+
+// Shared memory of the search for top tokens.
+constexpr uint32_t kCandidates = kThreads;
+struct TopSearch {
+  Key lists[kWarps + 1][32];     // the last one: of the segments so far
+  uint32_t values[kWarps][32];
+  uint32_t windows[kCandidates];
+  Key keys[kCandidates];
+  uint32_t nwindows, nkeys;
+};
 
 // Of a segment of windows [w0, w1) with the maxima's order in maxima[], its 32 greatest elements in
-// lists[0].  The k greatest elements lie in the k windows with the greatest maxima (each of those
-// that precede an element's window has one that precedes the element), and those windows are among
-// the windows of the k threads with the greatest maxima.  best: this thread's greatest window key.
+// T.lists[0], whatever values are alike.  The k greatest elements lie in the k windows with the greatest
+// maxima (each of those that precede an element's window has one that precedes the element), and those
+// windows are among the windows of the k threads with the greatest maxima.  best: this thread's.
 template <bool F32>
-__device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top,
-                                            Key best, const uint32_t* maxima, Key (*lists)[32],
-                                            uint32_t warp, uint32_t lane) {
-  join_lists(sorted(best, lane), lists, warp, lane);   // (its barrier: the maxima are there)
+__device__ void segment_top_of_alike(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top, Key best,
+                                     const uint32_t* maxima, TopSearch& T, uint32_t warp, uint32_t lane) {
+  join_lists(sorted(best, lane), T.lists, warp, lane);
   Key mine = 0;
   for (uint32_t i = warp; i < top; i += kWarps) {
-    const Key k = lists[0][i];
+    const Key k = T.lists[0][i];
     if (!k) break;
     const uint32_t w = (place_of(k) - w0) % kThreads + lane * kThreads;   // the thread's windows
     const Key v = w0 + w < w1 ? key_of(maxima[w], w0 + w) : 0;
     mine = merged(mine, sorted(v, lane), lane);
   }
   __syncthreads();
-  join_lists(mine, lists, warp, lane);
+  join_lists(mine, T.lists, warp, lane);
   mine = 0;
   for (uint32_t i = warp; i < top; i += kWarps) {
-    const Key k = lists[0][i];
+    const Key k = T.lists[0][i];
     if (!k) break;
-    Key v = 0;
-    if (lane < Windows<F32>::kElems) {
-      const int32_t e = W.first(place_of(k)) + (int32_t)lane;
-      if (e >= 0 && e < (int32_t)W.vocab)
-        v = key_of(order_of(element<F32>(W.row + (int64_t)e * Windows<F32>::kSize)), (uint32_t)e);
-    }
-    mine = merged(mine, sorted(v, lane), lane);
+    mine = merged(mine, sorted(W.key(place_of(k), lane), lane), lane);
   }
   __syncthreads();
-  join_lists(mine, lists, warp, lane);
+  join_lists(mine, T.lists, warp, lane);
+}
+// The same, much sooner where few values are alike.  At least `top` elements are as great as the thread's
+// maximum that is the top-th of all threads' (the floor), so the others do not count; the windows with
+// such elements are listed, then the elements, and these are sorted.
+template <bool F32>
+__device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top,
+                                            uint32_t best, uint32_t best_at, const uint32_t* maxima, TopSearch& T,
+                                            uint32_t warp, uint32_t lane) {
+  uint32_t v = sorted(best, lane);
+  T.values[warp][lane] = v;
+  if (threadIdx.x == 0) T.nwindows = T.nkeys = 0;
+  __syncthreads();   // (the maxima are there, too)
+  for (uint32_t half = kWarps / 2; half; half /= 2) {
+    if (warp < half) {
+      v = max(v, T.values[warp + half][31 - lane]);
+#pragma unroll
+      for (uint32_t stride = 16; stride; stride /= 2) v = step(v, stride, (lane & stride) == 0);
+      T.values[warp][lane] = v;
+    }
+    __syncthreads();
+  }
+  const uint32_t floor = T.values[0][top - 1];
+  if (best >= floor && best > 0)
+    for (uint32_t w = w0 + threadIdx.x; w < w1; w += kThreads)
+      if (maxima[w - w0] >= floor) {
+        const uint32_t i = atomicAdd(&T.nwindows, 1u);
+        if (i < kCandidates) T.windows[i] = w;
+      }
+  __syncthreads();
+  const uint32_t nw = T.nwindows;
+  if (nw <= kCandidates) {
+    for (uint32_t i = warp; i < nw; i += kWarps) {
+      const Key k = W.key(T.windows[i], lane);
+      const bool in = k && (uint32_t)(k >> 32) >= floor;
+      const uint32_t who = __ballot_sync(0xffffffffu, in);
+      uint32_t at = 0;
+      if (lane == 0) at = atomicAdd(&T.nkeys, (uint32_t)__popc(who));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
+      if (in && at < kCandidates) T.keys[at] = k;
+    }
+    __syncthreads();
+    const uint32_t n = T.nkeys;
+    if (n <= kCandidates) {
+      const uint32_t i = threadIdx.x;
+      Key mine = 0;
+      if (warp * 32 < n) mine = sorted(i < n ? T.keys[i] : 0, lane);
+      if (n > 32) {
+        join_lists(mine, T.lists, warp, lane);
+      } else {
+        if (warp == 0) T.lists[0][lane] = mine;
+        __syncthreads();
+      }
+      return;
+    }
+  }
+  __syncthreads();
+  segment_top_of_alike(W, w0, w1, top, best ? key_of(best, best_at) : 0, maxima, T, warp, lane);
 }
 
 // ------------------------------------------------------------------------------ forward pass
 // The blocks of a cluster share a row: each takes its part of the windows, and the first one joins
 // their sums and lists.
 template <bool F32, bool ENT, bool TOP>
-__global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs P) {
+__global__ void __launch_bounds__(kThreads, LB) k_score(const ScoreArgs P) {
   extern __shared__ uint32_t maxima[];
-  __shared__ Key lists[kWarps + 1][32];   // the last one: of the segments so far
-  __shared__ Joined parts[kWarps];
+  __shared__ TopSearch tops[1];
+  __shared__ Joined parts[kWarps], whole;
+  TopSearch& T = tops[0];
   after_previous();
   const cg::cluster_group cluster = cg::this_cluster();
   const uint32_t C = cluster.num_blocks(), c = cluster.block_rank();
@@ -315,6 +406,7 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs P) {
   const uint8_t* at = P.tokens + row * P.token_stride;
   const int64_t token = P.token_bytes == 8 ? *reinterpret_cast<const int64_t*>(at)
                                            : *reinterpret_cast<const int32_t*>(at);
+  const float temp = P.temps ? P.temps[row * P.temp_stride] : P.temp;
   if (token < 0) {   // (the whole cluster)
     if (c == 0) {
       if (threadIdx.x == 0) {
@@ -329,17 +421,19 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs P) {
     }
     return;
   }
-  const float temp = P.temps ? P.temps[row * P.temp_stride] : P.temp;
   const float inv_t = temp > 0.f && temp <= FLT_MAX ? 1.f / temp : __int_as_float(0x7FFFFFFF);
   const float scale = inv_t * kLog2e;
   const Windows<F32> W(P.x + row * P.ld, P.vocab);
   const uint32_t begin = (uint32_t)((uint64_t)W.count * c / C), end = (uint32_t)((uint64_t)W.count * (c + 1) / C);
+  const bool valid = token < (int64_t)P.vocab;
+  float given = 0.f;   // the token's logit, under way while the row is read
+  if (c == 0 && threadIdx.x == 0 && valid) given = element<F32>(W.row + token * Windows<F32>::kSize);
 
   Sums<ENT> a;
-  if (TOP && warp == 0) lists[kWarps][lane] = 0;
+  if (TOP && warp == 0) T.lists[kWarps][lane] = 0;
   for (uint32_t w0 = begin; w0 < end; w0 += kSegment) {
     const uint32_t w1 = TOP ? min(end, w0 + kSegment) : end;
-    Key best = 0;
+    uint32_t best = 0, best_at = 0;
     for (uint32_t w = w0 + threadIdx.x; w < w1; w += kThreads) {
       uint32_t lo[8], hi[8];
       W.load(w, lo, hi);
@@ -347,54 +441,50 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs P) {
       if (TOP) {
         const uint32_t o = order_of(m);
         maxima[w - w0] = o;
-        const Key k = key_of(o, w);
-        best = best > k ? best : k;
+        if (o > best) best = o, best_at = w;
       }
       a.raise(m, scale);
       add_window<F32, ENT>(a, lo, hi, scale);
     }
     if (!TOP) break;
-    segment_top<F32>(W, w0, w1, P.top, best, maxima, lists, warp, lane);
-    if (warp == 0) {
-      const Key v = merged(lists[kWarps][lane], lists[0][lane], lane);
-      lists[kWarps][lane] = v;
-    }
+    segment_top<F32>(W, w0, w1, P.top, best, best_at, maxima, T, warp, lane);
+    if (warp == 0) T.lists[kWarps][lane] = w0 == begin ? T.lists[0][lane] : merged(T.lists[kWarps][lane], T.lists[0][lane], lane);
     __syncthreads();
   }
 
   Joined j{a.max, (a.s[0].x + a.s[0].y) + (a.s[1].x + a.s[1].y), (a.t[0].x + a.t[0].y) + (a.t[1].x + a.t[1].y)};
 #pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    Joined o{__shfl_xor_sync(0xffffffffu, j.max, d), __shfl_xor_sync(0xffffffffu, j.s, d),
-             __shfl_xor_sync(0xffffffffu, j.t, d)};
-    j.join(o, scale);
-  }
+  for (int d = 16; d; d >>= 1) j.join(j.from(d), scale);
   if (lane == 0) parts[warp] = j;
   __syncthreads();
-  if (C > 1) cluster.sync();
-  if (c == 0 && warp == 0) {
-    j = Joined{-FLT_MAX, 0.f, 0.f};
-    Key best = 0;
-    for (uint32_t b = 0; b < C; b++) {
-      const Joined* p = C > 1 ? cluster.map_shared_rank(parts, b) : parts;
-      for (uint32_t i = 0; i < kWarps; i++) j.join(p[i], scale);
-      if (TOP) {
-        const Key* l = C > 1 ? cluster.map_shared_rank(&lists[kWarps][0], b) : lists[kWarps];
-        best = merged(best, l[lane], lane);
+  if (warp == 0) {
+    j = lane < kWarps ? parts[lane] : Joined{-FLT_MAX, 0.f, 0.f};
+#pragma unroll
+    for (int d = kWarps / 2; d; d >>= 1) j.join(j.from(d), scale);
+    if (lane == 0) whole = j;
+  }
+  if (C > 1) {
+    cluster.sync();
+    if (c == 0) {
+      if (warp == 0) {
+        j = lane < C ? *cluster.map_shared_rank(&whole, lane) : Joined{-FLT_MAX, 0.f, 0.f};
+#pragma unroll
+        for (int d = kMaxCluster / 2; d; d >>= 1) j.join(j.from(d), scale);
+      }
+      if (TOP) {   // (a warp a block: their lists lie sorted)
+        static_assert(kMaxCluster <= kWarps, "a list a warp");
+        join_lists(warp < C ? cluster.map_shared_rank(&T.lists[kWarps][0], warp)[lane] : 0, T.lists, warp, lane);
       }
     }
+  }
+  if (c == 0 && warp == 0) {
+    j = Joined{__shfl_sync(0xffffffffu, j.max, 0), __shfl_sync(0xffffffffu, j.s, 0), __shfl_sync(0xffffffffu, j.t, 0)};
     const bool empty = j.s == 0.f;             // nothing but -infinity
     const float inf = __int_as_float(0x7F800000), nan = __int_as_float(0x7FFFFFFF);
     const float log_sum = logf(j.s);
-    const float entropy = empty ? 0.f : log_sum - kLn2 * (j.t / j.s);
     if (lane == 0) {
-      const bool valid = token < (int64_t)P.vocab;
-      float lp = nan;
-      if (valid) {
-        const float x = element<F32>(W.row + token * Windows<F32>::kSize);
-        lp = empty ? -inf * inv_t : (x - j.max) * inv_t - log_sum;
-      }
-      P.logprobs[row] = lp;
+      const float entropy = empty ? 0.f : log_sum - kLn2 * (j.t / j.s);
+      P.logprobs[row] = !valid ? nan : empty ? -inf * inv_t : (given - j.max) * inv_t - log_sum;
       if (ENT) P.entropy[row] = entropy;
       Saved sv = {};
       sv.max = j.max;
@@ -405,9 +495,10 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs P) {
       P.saved[row] = sv;
     }
     if (TOP && lane < P.top) {
-      const float x = value_of((uint32_t)(best >> 32));
+      const Key k = T.lists[C > 1 ? 0 : kWarps][lane];
+      const float x = value_of((uint32_t)(k >> 32));
       P.top_logprobs[(uint64_t)row * P.top + lane] = empty ? -inf * inv_t : (x - j.max) * inv_t - log_sum;
-      P.top_tokens[(uint64_t)row * P.top + lane] = (int32_t)place_of(best);
+      P.top_tokens[(uint64_t)row * P.top + lane] = (int32_t)place_of(k);
     }
   }
   if (C > 1) cluster.sync();   // (the others' memory is read until here)
@@ -603,10 +694,11 @@ int bo_logprobs_forward(const bo_logprobs* h, const void* d_logits, uint32_t dty
   P.top_logprobs = h->d_top_logprobs;
   P.top_tokens = h->d_top_tokens;
   P.saved = static_cast<Saved*>(h->d_saved);
+  static const uint32_t kCt = getenv("CT") ? atoi(getenv("CT")) : 16;
+  static const uint32_t kCw = getenv("CW") ? atoi(getenv("CW")) : 1024;
+  const uint64_t windows = (uint64_t)h->vocab * size / kWindow;
   uint32_t cluster = 1;
-  while (cluster < 8 && (uint64_t)rows * cluster * 2 <= (uint64_t)sms * 4 &&
-         (uint64_t)h->vocab * size >= (uint64_t)cluster * 2 * kThreads * kWindow / 2)
-    cluster *= 2;
+  while (cluster < kMaxCluster && (uint64_t)rows * cluster < (uint64_t)sms * kCt && windows >= 2 * cluster * kCw) cluster *= 2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return check(dtype == BO_FP32 ? score<true>(P, cluster, s) : score<false>(P, cluster, s));
 }

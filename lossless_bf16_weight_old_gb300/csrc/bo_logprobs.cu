@@ -15,14 +15,15 @@ namespace {
 
 namespace cg = cooperative_groups;
 #ifndef LB
-#define LB 4
+#define LB 6
+#define LBT 4
 #endif
 
 
 constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
 constexpr uint32_t kMaxCluster = 8;
 constexpr uint32_t kWindow = 64;                 // bytes
-constexpr uint32_t kSegment = kThreads * 32;     // windows whose maxima are kept at once
+constexpr uint32_t kSegment = 8192;              // windows whose maxima are kept at once
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 // What the backward pass takes from the forward one, of each row.
@@ -270,10 +271,11 @@ __device__ __forceinline__ Key merged(Key a, Key b, uint32_t lane) {
   return merged_reversed(a, __shfl_sync(0xffffffffu, b, 31 - lane), lane);
 }
 // The warps' lists joined in lists[0].
+template <uint32_t TH>
 __device__ __forceinline__ void join_lists(Key mine, Key (*lists)[32], uint32_t warp, uint32_t lane) {
   lists[warp][lane] = mine;
   __syncthreads();
-  for (uint32_t half = kWarps / 2; half; half /= 2) {
+  for (uint32_t half = (TH / 32) / 2; half; half /= 2) {
     if (warp < half) {
       mine = merged_reversed(mine, lists[warp + half][31 - lane], lane);
       lists[warp][lane] = mine;
@@ -296,10 +298,11 @@ __device__ __forceinline__ uint32_t sorted(uint32_t v, uint32_t lane) {
 }
 
 // Shared memory of the search for top tokens.
-constexpr uint32_t kCandidates = kThreads;
+template <uint32_t TH>
 struct TopSearch {
-  Key lists[kWarps + 1][32];     // the last one: of the segments so far
-  uint32_t values[kWarps][32];
+  static constexpr uint32_t kCandidates = TH;
+  Key lists[(TH / 32) + 1][32];     // the last one: of the segments so far
+  uint32_t values[(TH / 32)][32];
   uint32_t windows[kCandidates];
   Key keys[kCandidates];
   uint32_t nwindows, nkeys;
@@ -309,41 +312,40 @@ struct TopSearch {
 // T.lists[0], whatever values are alike.  The k greatest elements lie in the k windows with the greatest
 // maxima (each of those that precede an element's window has one that precedes the element), and those
 // windows are among the windows of the k threads with the greatest maxima.  best: this thread's.
-template <bool F32>
-__device__ void segment_top_of_alike(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top, Key best,
-                                     const uint32_t* maxima, TopSearch& T, uint32_t warp, uint32_t lane) {
-  join_lists(sorted(best, lane), T.lists, warp, lane);
+template <uint32_t TH, bool F32>
+__device__ __noinline__ void segment_top_of_alike(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top, Key best,
+                                     const uint32_t* maxima, TopSearch<TH>& T, uint32_t warp, uint32_t lane) {
+  join_lists<TH>(sorted(best, lane), T.lists, warp, lane);
   Key mine = 0;
-  for (uint32_t i = warp; i < top; i += kWarps) {
+  for (uint32_t i = warp; i < top; i += (TH / 32)) {
     const Key k = T.lists[0][i];
     if (!k) break;
-    const uint32_t w = (place_of(k) - w0) % kThreads + lane * kThreads;   // the thread's windows
-    const Key v = w0 + w < w1 ? key_of(maxima[w], w0 + w) : 0;
-    mine = merged(mine, sorted(v, lane), lane);
+    for (uint32_t w = w0 + (place_of(k) - w0) % TH + lane * TH, n = 0; n < kSegment; n += 32 * TH, w += 32 * TH)
+      mine = merged(mine, sorted(w < w1 ? key_of(maxima[w - w0], w) : 0, lane), lane);   // the thread's windows
   }
   __syncthreads();
-  join_lists(mine, T.lists, warp, lane);
+  join_lists<TH>(mine, T.lists, warp, lane);
   mine = 0;
-  for (uint32_t i = warp; i < top; i += kWarps) {
+  for (uint32_t i = warp; i < top; i += (TH / 32)) {
     const Key k = T.lists[0][i];
     if (!k) break;
     mine = merged(mine, sorted(W.key(place_of(k), lane), lane), lane);
   }
   __syncthreads();
-  join_lists(mine, T.lists, warp, lane);
+  join_lists<TH>(mine, T.lists, warp, lane);
 }
 // The same, much sooner where few values are alike.  At least `top` elements are as great as the thread's
 // maximum that is the top-th of all threads' (the floor), so the others do not count; the windows with
 // such elements are listed, then the elements, and these are sorted.
-template <bool F32>
+template <uint32_t TH, bool F32>
 __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top,
-                                            uint32_t best, uint32_t best_at, const uint32_t* maxima, TopSearch& T,
+                                            uint32_t best, uint32_t best_at, const uint32_t* maxima, TopSearch<TH>& T,
                                             uint32_t warp, uint32_t lane) {
   uint32_t v = sorted(best, lane);
   T.values[warp][lane] = v;
   if (threadIdx.x == 0) T.nwindows = T.nkeys = 0;
   __syncthreads();   // (the maxima are there, too)
-  for (uint32_t half = kWarps / 2; half; half /= 2) {
+  for (uint32_t half = (TH / 32) / 2; half; half /= 2) {
     if (warp < half) {
       v = max(v, T.values[warp + half][31 - lane]);
 #pragma unroll
@@ -354,31 +356,31 @@ __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, 
   }
   const uint32_t floor = T.values[0][top - 1];
   if (best >= floor && best > 0)
-    for (uint32_t w = w0 + threadIdx.x; w < w1; w += kThreads)
+    for (uint32_t w = w0 + threadIdx.x; w < w1; w += TH)
       if (maxima[w - w0] >= floor) {
         const uint32_t i = atomicAdd(&T.nwindows, 1u);
-        if (i < kCandidates) T.windows[i] = w;
+        if (i < TopSearch<TH>::kCandidates) T.windows[i] = w;
       }
   __syncthreads();
   const uint32_t nw = T.nwindows;
-  if (nw <= kCandidates) {
-    for (uint32_t i = warp; i < nw; i += kWarps) {
+  if (nw <= TopSearch<TH>::kCandidates) {
+    for (uint32_t i = warp; i < nw; i += (TH / 32)) {
       const Key k = W.key(T.windows[i], lane);
       const bool in = k && (uint32_t)(k >> 32) >= floor;
       const uint32_t who = __ballot_sync(0xffffffffu, in);
       uint32_t at = 0;
       if (lane == 0) at = atomicAdd(&T.nkeys, (uint32_t)__popc(who));
       at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
-      if (in && at < kCandidates) T.keys[at] = k;
+      if (in && at < TopSearch<TH>::kCandidates) T.keys[at] = k;
     }
     __syncthreads();
     const uint32_t n = T.nkeys;
-    if (n <= kCandidates) {
+    if (n <= TopSearch<TH>::kCandidates) {
       const uint32_t i = threadIdx.x;
       Key mine = 0;
       if (warp * 32 < n) mine = sorted(i < n ? T.keys[i] : 0, lane);
       if (n > 32) {
-        join_lists(mine, T.lists, warp, lane);
+        join_lists<TH>(mine, T.lists, warp, lane);
       } else {
         if (warp == 0) T.lists[0][lane] = mine;
         __syncthreads();
@@ -393,12 +395,12 @@ __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, 
 // ------------------------------------------------------------------------------ forward pass
 // The blocks of a cluster share a row: each takes its part of the windows, and the first one joins
 // their sums and lists.
-template <bool F32, bool ENT, bool TOP>
-__global__ void __launch_bounds__(kThreads, LB) k_score(const ScoreArgs P) {
+template <uint32_t TH, bool F32, bool ENT, bool TOP>
+__global__ void __launch_bounds__(TH, (TOP ? LBT : LB) * 256 / TH) k_score(const ScoreArgs P) {
   extern __shared__ uint32_t maxima[];
-  __shared__ TopSearch tops[1];
-  __shared__ Joined parts[kWarps], whole;
-  TopSearch& T = tops[0];
+  __shared__ TopSearch<TH> tops[1];
+  __shared__ Joined parts[(TH / 32)], whole;
+  TopSearch<TH>& T = tops[0];
   after_previous();
   const cg::cluster_group cluster = cg::this_cluster();
   const uint32_t C = cluster.num_blocks(), c = cluster.block_rank();
@@ -430,11 +432,11 @@ __global__ void __launch_bounds__(kThreads, LB) k_score(const ScoreArgs P) {
   if (c == 0 && threadIdx.x == 0 && valid) given = element<F32>(W.row + token * Windows<F32>::kSize);
 
   Sums<ENT> a;
-  if (TOP && warp == 0) T.lists[kWarps][lane] = 0;
+  if (TOP && warp == 0) T.lists[(TH / 32)][lane] = 0;
   for (uint32_t w0 = begin; w0 < end; w0 += kSegment) {
     const uint32_t w1 = TOP ? min(end, w0 + kSegment) : end;
     uint32_t best = 0, best_at = 0;
-    for (uint32_t w = w0 + threadIdx.x; w < w1; w += kThreads) {
+    for (uint32_t w = w0 + threadIdx.x; w < w1; w += TH) {
       uint32_t lo[8], hi[8];
       W.load(w, lo, hi);
       const float m = window_max<F32>(lo, hi);
@@ -447,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, LB) k_score(const ScoreArgs P) {
       add_window<F32, ENT>(a, lo, hi, scale);
     }
     if (!TOP) break;
-    segment_top<F32>(W, w0, w1, P.top, best, best_at, maxima, T, warp, lane);
-    if (warp == 0) T.lists[kWarps][lane] = w0 == begin ? T.lists[0][lane] : merged(T.lists[kWarps][lane], T.lists[0][lane], lane);
+    segment_top<TH, F32>(W, w0, w1, P.top, best, best_at, maxima, T, warp, lane);
+    if (warp == 0) T.lists[(TH / 32)][lane] = w0 == begin ? T.lists[0][lane] : merged(T.lists[(TH / 32)][lane], T.lists[0][lane], lane);
     __syncthreads();
   }
 
@@ -458,9 +460,9 @@ __global__ void __launch_bounds__(kThreads, LB) k_score(const ScoreArgs P) {
   if (lane == 0) parts[warp] = j;
   __syncthreads();
   if (warp == 0) {
-    j = lane < kWarps ? parts[lane] : Joined{-FLT_MAX, 0.f, 0.f};
+    j = lane < TH / 32 ? parts[lane] : Joined{-FLT_MAX, 0.f, 0.f};
 #pragma unroll
-    for (int d = kWarps / 2; d; d >>= 1) j.join(j.from(d), scale);
+    for (int d = (TH / 32) / 2; d; d >>= 1) j.join(j.from(d), scale);
     if (lane == 0) whole = j;
   }
   if (C > 1) {
@@ -472,8 +474,12 @@ __global__ void __launch_bounds__(kThreads, LB) k_score(const ScoreArgs P) {
         for (int d = kMaxCluster / 2; d; d >>= 1) j.join(j.from(d), scale);
       }
       if (TOP) {   // (a warp a block: their lists lie sorted)
-        static_assert(kMaxCluster <= kWarps, "a list a warp");
-        join_lists(warp < C ? cluster.map_shared_rank(&T.lists[kWarps][0], warp)[lane] : 0, T.lists, warp, lane);
+        Key mine = 0;
+        for (uint32_t b = warp; b < C; b += TH / 32) {
+          const Key k = cluster.map_shared_rank(&T.lists[TH / 32][0], b)[lane];
+          mine = b == warp ? k : merged(mine, k, lane);
+        }
+        join_lists<TH>(mine, T.lists, warp, lane);
       }
     }
   }
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, LB) k_score(const ScoreArgs P) {
       P.saved[row] = sv;
     }
     if (TOP && lane < P.top) {
-      const Key k = T.lists[C > 1 ? 0 : kWarps][lane];
+      const Key k = T.lists[C > 1 ? 0 : (TH / 32)][lane];
       const float x = value_of((uint32_t)(k >> 32));
       P.top_logprobs[(uint64_t)row * P.top + lane] = empty ? -inf * inv_t : (x - j.max) * inv_t - log_sum;
       P.top_tokens[(uint64_t)row * P.top + lane] = (int32_t)place_of(k);
@@ -613,12 +619,15 @@ bool strided(const void* p, uint64_t stride, uint64_t size) {
   return aligned(p, size) && stride <= (1ull << 40);
 }
 
-template <bool F32>
+template <uint32_t TH, bool F32>
 cudaError_t score(const ScoreArgs& P, uint32_t cluster, cudaStream_t s) {
   const bool ent = P.entropy != nullptr, top = P.top > 0;
-  auto k = ent ? (top ? k_score<F32, true, true> : k_score<F32, true, false>)
-               : (top ? k_score<F32, false, true> : k_score<F32, false, false>);
-  return launch(k, dim3(P.rows * cluster), kThreads, top ? kSegment * 4 : 0, cluster, s, P);
+  auto k = ent ? (top ? k_score<TH, F32, true, true> : k_score<TH, F32, true, false>)
+               : (top ? k_score<TH, F32, false, true> : k_score<TH, F32, false, false>);
+  // (a window more than a row fills where it begins inside one, and than its part of a cluster's)
+  const uint64_t windows = ((uint64_t)P.vocab * (F32 ? 4 : 2) / kWindow + 2) / cluster + 1;
+  const uint32_t smem = top ? (uint32_t)std::min<uint64_t>(kSegment, windows) * 4 : 0;
+  return launch(k, dim3(P.rows * cluster), TH, smem, cluster, s, P);
 }
 
 }  // namespace
@@ -694,13 +703,15 @@ int bo_logprobs_forward(const bo_logprobs* h, const void* d_logits, uint32_t dty
   P.top_logprobs = h->d_top_logprobs;
   P.top_tokens = h->d_top_tokens;
   P.saved = static_cast<Saved*>(h->d_saved);
-  static const uint32_t kCt = getenv("CT") ? atoi(getenv("CT")) : 16;
+  static const uint32_t kCt = getenv("CT") ? atoi(getenv("CT")) : 4;
   static const uint32_t kCw = getenv("CW") ? atoi(getenv("CW")) : 1024;
   const uint64_t windows = (uint64_t)h->vocab * size / kWindow;
   uint32_t cluster = 1;
   while (cluster < kMaxCluster && (uint64_t)rows * cluster < (uint64_t)sms * kCt && windows >= 2 * cluster * kCw) cluster *= 2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return check(dtype == BO_FP32 ? score<true>(P, cluster, s) : score<false>(P, cluster, s));
+  static const uint32_t kTt = getenv("TT") ? atoi(getenv("TT")) : 256;
+  return check(kTt == 128 ? (dtype == BO_FP32 ? score<128, true>(P, cluster, s) : score<128, false>(P, cluster, s)) : 
+    (dtype == BO_FP32 ? score<256, true>(P, cluster, s) : score<256, false>(P, cluster, s)));
 }
 
 int bo_logprobs_backward(const bo_logprobs* h, const void* d_logits, uint32_t dtype, uint64_t ld,

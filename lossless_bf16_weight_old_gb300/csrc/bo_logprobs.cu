@@ -20,7 +20,7 @@ namespace cg = cooperative_groups;
 #endif
 
 
-constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
+constexpr uint32_t kThreads = 256;
 constexpr uint32_t kMaxCluster = 8;
 constexpr uint32_t kWindow = 64;                 // bytes
 constexpr uint32_t kSegment = 8192;              // windows whose maxima are kept at once
@@ -28,12 +28,14 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 
 // What the backward pass takes from the forward one, of each row.
 struct alignas(32) Saved {
-  float max;       // of the logits
-  float log2_sum;  // of 2^((x - max) scale)
+  float shift;      // p_j = 2^(x_j scale - shift) / sum, or, with `careful`, 2^((x_j - shift) scale) / sum
+  float sum;
+  float log2_sum;
   float entropy;
-  float inv_t;     // 1 / T; NaN for a row without a valid token or temperature
-  int32_t token;   // -1: the gradient is 0
-  int32_t pad[3];
+  float inv_t;      // 1 / T; NaN for a row without a valid token or temperature
+  int32_t token;    // -1: the gradient is 0
+  int32_t careful;
+  int32_t pad;
 };
 static_assert(sizeof(Saved) == 32, "one sector");
 
@@ -74,6 +76,11 @@ __device__ __forceinline__ float ex2(float x) {   // 2^x, 0 below 2^-126
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
@@ -140,14 +147,8 @@ struct Windows {
     if (lane >= kElems || e < 0 || e >= (int32_t)vocab) return 0;
     return key_of(order_of(element<F32>(row + (int64_t)e * kSize)), (uint32_t)e);
   }
-  // the window's words; -infinity outside the row
-  __device__ __forceinline__ void load(uint32_t w, uint32_t (&lo)[8], uint32_t (&hi)[8]) const {
-    if (whole(w)) {
-      const uint8_t* p = base + (uint64_t)w * kWindow;
-      ld32(lo, p);
-      ld32(hi, p + 32);
-      return;
-    }
+  // the words of a window that is not whole; -infinity outside the row
+  __device__ __forceinline__ void load_edge(uint32_t w, uint32_t (&lo)[8], uint32_t (&hi)[8]) const {
     const int32_t e0 = first(w);
 #pragma unroll
     for (int i = 0; i < 16; i++) {
@@ -167,19 +168,49 @@ struct Windows {
 };
 
 // ---------------------------------------------------------------------------- online softmax
-// Of the values so far: their maximum, the sum of e = 2^d over d = (x - max) scale, and the sum of
-// e d, in four parts each.  The maximum starts at the lowest finite number, so that -infinity has
-// e = 0; d is kept above -200, where e is 0 too, so that e d is 0 and not NaN.
+// Of the values so far: their maximum; the whole number `shift` above its product with the scale; the sum
+// of e = 2^d over d = x scale - shift, and the sum of e d, in four parts each.  Because the shift is a
+// whole number, d is one fused operation with one rounding, and sums for another shift differ by an exact
+// power of two.  That holds while the product stays between -2^21 and 2^22 (kLeast, kMost): the rows whose
+// maximum does not are read again (careful_sums).  The shift starts below all of them, so that -infinity
+// has e = 0; its d is kept finite, so that e d is 0 and not NaN.
+constexpr float kLeast = -2097152.f, kMost = 4194304.f;
+constexpr uint32_t kFloorBf16 = 0xF149F149u;   // -1e30, twice
+constexpr float kFloor = -1e30f, kLeastScale = 1e-23f;
+
+__device__ __forceinline__ float two_to(float whole) {   // of a whole number that is not positive
+  return whole < -126.f ? 0.f : __int_as_float(((int)whole + 127) << 23);
+}
+struct Joined {
+  float max, shift, s, t;
+  __device__ __forceinline__ Joined from(int d) const {   // another lane's
+    return Joined{__shfl_xor_sync(0xffffffffu, max, d), __shfl_xor_sync(0xffffffffu, shift, d),
+                  __shfl_xor_sync(0xffffffffu, s, d), __shfl_xor_sync(0xffffffffu, t, d)};
+  }
+  __device__ __forceinline__ void join(const Joined& o) {
+    const float to = fmaxf(shift, o.shift), da = shift - to, db = o.shift - to;
+    const float fa = two_to(da), fb = two_to(db);
+    t = fa * fmaf(s, da, t) + fb * fmaf(o.s, db, o.t);
+    s = fa * s + fb * o.s;
+    shift = to;
+    max = fmaxf(max, o.max);
+  }
+};
+__device__ __forceinline__ Joined nothing() {
+  return Joined{-INFINITY, -kMost, 0.f, 0.f};
+}
 template <bool ENT>
 struct Sums {
-  float max = -FLT_MAX;
+  float max = -INFINITY, shift = -kMost;
   float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   float2 t[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 
-  __device__ __forceinline__ void raise(float to, float scale) {
-    if (!(to > max)) return;   // (a NaN raises nothing: its own e is NaN)
-    const float d = fmaxf((max - to) * scale, -200.f), f = ex2(d);
+  __device__ __forceinline__ void raise(float to, float scale) {   // (not called for a NaN)
     max = to;
+    const float up = fminf(ceilf(to * scale), kMost);
+    if (!(up > shift)) return;
+    const float d = shift - up, f = two_to(d);
+    shift = up;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
       if (ENT) t[i] = make_float2(f * fmaf(s[i].x, d, t[i].x), f * fmaf(s[i].y, d, t[i].y));
@@ -187,16 +218,18 @@ struct Sums {
     }
   }
   __device__ __forceinline__ void add(float2 x, float scale, int i) {
-    float2 d = __fmul2_rn(__fadd2_rn(x, make_float2(-max, -max)), make_float2(scale, scale));
-    d = make_float2(max_nan(d.x, -200.f), max_nan(d.y, -200.f));
+    const float2 d = __ffma2_rn(x, make_float2(scale, scale), make_float2(-shift, -shift));
     const float2 e = make_float2(ex2(d.x), ex2(d.y));
     s[i] = __fadd2_rn(s[i], e);
     if (ENT) t[i] = __ffma2_rn(e, d, t[i]);
   }
+  __device__ __forceinline__ Joined joined() const {
+    return Joined{max, shift, (s[0].x + s[0].y) + (s[1].x + s[1].y), (t[0].x + t[0].y) + (t[1].x + t[1].y)};
+  }
 };
 template <bool F32>
 __device__ __forceinline__ float window_max(const uint32_t (&lo)[8], const uint32_t (&hi)[8]) {
-  if (F32) {
+  if constexpr (F32) {
     float m[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) m[i] = max_nan(__uint_as_float(lo[i]), __uint_as_float(hi[i]));
@@ -205,15 +238,16 @@ __device__ __forceinline__ float window_max(const uint32_t (&lo)[8], const uint3
 #pragma unroll
       for (int i = 0; i < n; i++) m[i] = max_nan(m[i], m[i + n]);
     return m[0];
+  } else {
+    uint32_t m[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) m[i] = max_bf16x2(lo[i], hi[i]);
+#pragma unroll
+    for (int n = 4; n; n >>= 1)
+#pragma unroll
+      for (int i = 0; i < n; i++) m[i] = max_bf16x2(m[i], m[i + n]);
+    return max_nan(bf16_lo(m[0]), bf16_hi(m[0]));
   }
-  uint32_t m[8];
-#pragma unroll
-  for (int i = 0; i < 8; i++) m[i] = max_bf16x2(lo[i], hi[i]);
-#pragma unroll
-  for (int n = 4; n; n >>= 1)
-#pragma unroll
-    for (int i = 0; i < n; i++) m[i] = max_bf16x2(m[i], m[i + n]);
-  return max_nan(bf16_lo(m[0]), bf16_hi(m[0]));
 }
 template <bool F32, bool ENT>
 __device__ __forceinline__ void add_window(Sums<ENT>& a, const uint32_t (&lo)[8], const uint32_t (&hi)[8],
@@ -223,28 +257,47 @@ __device__ __forceinline__ void add_window(Sums<ENT>& a, const uint32_t (&lo)[8]
     if (F32) {
       const uint32_t* w = i < 4 ? lo : hi;
       const int j = 2 * (i & 3);
-      a.add(make_float2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])), scale, i & 1);
+      float2 x = make_float2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
+      if (ENT) x = make_float2(max_nan(x.x, kFloor), max_nan(x.y, kFloor));
+      a.add(x, scale, i & 1);
     } else {
-      a.add(make_float2(bf16_lo(lo[i]), bf16_hi(lo[i])), scale, 0);
-      a.add(make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])), scale, 1);
+      const uint32_t u = ENT ? max_bf16x2(lo[i], kFloorBf16) : lo[i], v = ENT ? max_bf16x2(hi[i], kFloorBf16) : hi[i];
+      a.add(make_float2(bf16_lo(u), bf16_hi(u)), scale, 0);
+      a.add(make_float2(bf16_lo(v), bf16_hi(v)), scale, 1);
     }
   }
 }
-struct Joined {
-  float max, s, t;
-  __device__ __forceinline__ Joined from(int d) const {   // another lane's
-    return Joined{__shfl_xor_sync(0xffffffffu, max, d), __shfl_xor_sync(0xffffffffu, s, d),
-                  __shfl_xor_sync(0xffffffffu, t, d)};
+
+// The sums of a whole row for any values: d = (x - max) scale with the row's own maximum, kept above
+// -200, where e is 0, so that e d is 0 and not NaN.  The maximum is taken as the lowest finite number
+// at least: a row of -infinity has the sum 0.  For a block; every thread of warp 0 has the result.
+template <uint32_t TH, bool F32>
+__device__ __noinline__ Joined careful_sums(const Windows<F32>& W, float max, float scale, Joined* parts) {
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  max = fmaxf(max, -FLT_MAX);
+  float s = 0.f, t = 0.f;
+  for (uint32_t e = threadIdx.x; e < W.vocab; e += TH) {
+    const float x = element<F32>(W.row + (uint64_t)e * Windows<F32>::kSize);
+    const float d = max_nan((x - max) * scale, -200.f), p = ex2(d);
+    s += p;
+    t = fmaf(p, d, t);
   }
-  __device__ __forceinline__ void join(const Joined& o, float scale) {
-    const float m = fmaxf(max, o.max);
-    const float da = fmaxf((max - m) * scale, -200.f), db = fmaxf((o.max - m) * scale, -200.f);
-    const float fa = max == m ? 1.f : ex2(da), fb = o.max == m ? 1.f : ex2(db);
-    t = (max == m ? t : fa * fmaf(s, da, t)) + (o.max == m ? o.t : fb * fmaf(o.s, db, o.t));
-    s = fa * s + fb * o.s;
-    max = m;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, d);
+    t += __shfl_xor_sync(0xffffffffu, t, d);
   }
-};
+  if (lane == 0) parts[warp] = Joined{max, max, s, t};
+  __syncthreads();
+  s = lane < TH / 32 ? parts[lane].s : 0.f;
+  t = lane < TH / 32 ? parts[lane].t : 0.f;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, d);
+    t += __shfl_xor_sync(0xffffffffu, t, d);
+  }
+  return Joined{max, max, s, t};
+}
 
 // ------------------------------------------------------------------------------- top tokens
 __device__ __forceinline__ Key step(Key v, uint32_t stride, bool keep_max) {
@@ -429,51 +482,68 @@ __global__ void __launch_bounds__(TH, (TOP ? LBT : LB) * 256 / TH) k_score(const
   const uint32_t begin = (uint32_t)((uint64_t)W.count * c / C), end = (uint32_t)((uint64_t)W.count * (c + 1) / C);
   const bool valid = token < (int64_t)P.vocab;
   float given = 0.f;   // the token's logit, under way while the row is read
-  if (c == 0 && threadIdx.x == 0 && valid) given = element<F32>(W.row + token * Windows<F32>::kSize);
+  if (c == 0 && warp == 0 && valid) given = element<F32>(W.row + token * Windows<F32>::kSize);
 
   Sums<ENT> a;
-  if (TOP && warp == 0) T.lists[(TH / 32)][lane] = 0;
+  if (TOP && warp == 0) T.lists[TH / 32][lane] = 0;
+  // windows [begin, end) but for the first and last ones of the row, where they are not whole
+  const uint32_t edge0 = W.whole(0) ? 0 : 1, edge1 = W.count > 1 && !W.whole(W.count - 1) ? W.count - 1 : W.count;
   for (uint32_t w0 = begin; w0 < end; w0 += kSegment) {
     const uint32_t w1 = TOP ? min(end, w0 + kSegment) : end;
     uint32_t best = 0, best_at = 0;
-    for (uint32_t w = w0 + threadIdx.x; w < w1; w += TH) {
-      uint32_t lo[8], hi[8];
-      W.load(w, lo, hi);
+    auto take = [&](uint32_t w, const uint32_t (&lo)[8], const uint32_t (&hi)[8]) {
       const float m = window_max<F32>(lo, hi);
       if (TOP) {
         const uint32_t o = order_of(m);
         maxima[w - w0] = o;
-        if (o > best) best = o, best_at = w;
+        if (o > best || (o == best && w < best_at)) best = o, best_at = w;   // (the last window comes first)
       }
-      a.raise(m, scale);
+      if (m > a.max) a.raise(m, scale);
       add_window<F32, ENT>(a, lo, hi, scale);
+    };
+    // thread i takes the segment's windows i, i + TH, ...
+#pragma unroll 1
+    for (uint32_t i = 0; i < 2; i++) {
+      const uint32_t edge = i ? edge1 : 0;
+      if ((i ? edge < W.count : edge0 > 0) && edge >= w0 && edge < w1 && (edge - w0) % TH == threadIdx.x) {
+        uint32_t lo[8], hi[8];
+        W.load_edge(edge, lo, hi);
+        take(edge, lo, hi);
+      }
+    }
+    uint32_t w = w0 + threadIdx.x;
+    if (w < edge0) w += TH;
+    const uint32_t stop = min(w1, edge1);
+#pragma unroll 1
+    for (const uint8_t* p = W.base + (uint64_t)w * kWindow; w < stop; w += TH, p += TH * kWindow) {
+      uint32_t lo[8], hi[8];
+      ld32(lo, p);
+      ld32(hi, p + 32);
+      take(w, lo, hi);
     }
     if (!TOP) break;
     segment_top<TH, F32>(W, w0, w1, P.top, best, best_at, maxima, T, warp, lane);
-    if (warp == 0) T.lists[(TH / 32)][lane] = w0 == begin ? T.lists[0][lane] : merged(T.lists[(TH / 32)][lane], T.lists[0][lane], lane);
+    if (warp == 0) T.lists[TH / 32][lane] = w0 == begin ? T.lists[0][lane] : merged(T.lists[TH / 32][lane], T.lists[0][lane], lane);
     __syncthreads();
   }
 
-  Joined j{a.max, (a.s[0].x + a.s[0].y) + (a.s[1].x + a.s[1].y), (a.t[0].x + a.t[0].y) + (a.t[1].x + a.t[1].y)};
+  Joined j = a.joined();
 #pragma unroll
-  for (int d = 16; d; d >>= 1) j.join(j.from(d), scale);
+  for (int d = 16; d; d >>= 1) j.join(j.from(d));
   if (lane == 0) parts[warp] = j;
   __syncthreads();
-  if (warp == 0) {
-    j = lane < TH / 32 ? parts[lane] : Joined{-FLT_MAX, 0.f, 0.f};
+  // (every warp has the block's sums, and of the first block the cluster's)
+  j = lane < TH / 32 ? parts[lane] : nothing();
 #pragma unroll
-    for (int d = (TH / 32) / 2; d; d >>= 1) j.join(j.from(d), scale);
-    if (lane == 0) whole = j;
-  }
+  for (int d = TH / 64; d; d >>= 1) j.join(j.from(d));
   if (C > 1) {
+    if (threadIdx.x == 0) whole = j;
     cluster.sync();
     if (c == 0) {
-      if (warp == 0) {
-        j = lane < C ? *cluster.map_shared_rank(&whole, lane) : Joined{-FLT_MAX, 0.f, 0.f};
+      j = lane < C ? *cluster.map_shared_rank(&whole, lane) : nothing();
 #pragma unroll
-        for (int d = kMaxCluster / 2; d; d >>= 1) j.join(j.from(d), scale);
-      }
-      if (TOP) {   // (a warp a block: their lists lie sorted)
+      for (int d = kMaxCluster / 2; d; d >>= 1) j.join(j.from(d));
+      if (TOP) {   // (their lists lie sorted)
         Key mine = 0;
         for (uint32_t b = warp; b < C; b += TH / 32) {
           const Key k = cluster.map_shared_rank(&T.lists[TH / 32][0], b)[lane];
@@ -483,43 +553,91 @@ __global__ void __launch_bounds__(TH, (TOP ? LBT : LB) * 256 / TH) k_score(const
       }
     }
   }
-  if (c == 0 && warp == 0) {
-    j = Joined{__shfl_sync(0xffffffffu, j.max, 0), __shfl_sync(0xffffffffu, j.s, 0), __shfl_sync(0xffffffffu, j.t, 0)};
-    const bool empty = j.s == 0.f;             // nothing but -infinity
-    const float inf = __int_as_float(0x7F800000), nan = __int_as_float(0x7FFFFFFF);
-    const float log_sum = logf(j.s);
-    if (lane == 0) {
-      const float entropy = empty ? 0.f : log_sum - kLn2 * (j.t / j.s);
-      P.logprobs[row] = !valid ? nan : empty ? -inf * inv_t : (given - j.max) * inv_t - log_sum;
-      if (ENT) P.entropy[row] = entropy;
-      Saved sv = {};
-      sv.max = j.max;
-      sv.log2_sum = log2f(j.s);
-      sv.entropy = entropy;
-      sv.inv_t = valid ? inv_t : nan;
-      sv.token = empty && valid && inv_t == inv_t ? -1 : (int32_t)(valid ? token : 0);
-      P.saved[row] = sv;
+  if (c == 0) {
+    j = Joined{__shfl_sync(0xffffffffu, j.max, 0), __shfl_sync(0xffffffffu, j.shift, 0),
+               __shfl_sync(0xffffffffu, j.s, 0), __shfl_sync(0xffffffffu, j.t, 0)};
+    const float far = j.max * scale;
+    const bool careful = !(far >= kLeast && far <= kMost) || (ENT && !(scale >= kLeastScale));
+    if (careful) {
+      __syncthreads();   // (parts is read)
+      j = careful_sums<TH, F32>(W, j.max, scale, parts);
     }
-    if (TOP && lane < P.top) {
-      const Key k = T.lists[C > 1 ? 0 : (TH / 32)][lane];
-      const float x = value_of((uint32_t)(k >> 32));
-      P.top_logprobs[(uint64_t)row * P.top + lane] = empty ? -inf * inv_t : (x - j.max) * inv_t - log_sum;
-      P.top_tokens[(uint64_t)row * P.top + lane] = (int32_t)place_of(k);
+    if (warp == 0) {
+      const bool empty = careful && j.s == 0.f;             // nothing but -infinity
+      const float inf = __int_as_float(0x7F800000), nan = __int_as_float(0x7FFFFFFF);
+      const float log2_sum = log2f(j.s);
+      auto log_p = [&](float x) {
+        if (empty) return -inf * inv_t;
+        if (careful) return min_nan((x - j.shift) * inv_t - log2_sum * kLn2, 0.f);
+        const float d = fmaf(x, scale, -j.shift) - log2_sum;
+        // (far below, where base 2 could pass the range that the base e does not)
+        return d < -1048576.f ? x * inv_t - (j.shift + log2_sum) * kLn2 : min_nan(d * kLn2, 0.f);
+      };
+      if (lane == 0) {
+        const float entropy = empty ? 0.f : max_nan(kLn2 * (log2_sum - j.t / j.s), 0.f);
+        P.logprobs[row] = valid ? log_p(given) : nan;
+        if (ENT) P.entropy[row] = entropy;
+        Saved sv = {};
+        sv.shift = j.shift;
+        sv.sum = j.s;
+        sv.log2_sum = log2_sum;
+        sv.entropy = entropy;
+        sv.inv_t = valid ? inv_t : nan;
+        sv.token = empty && valid && inv_t == inv_t ? -1 : (int32_t)(valid ? token : 0);
+        sv.careful = careful;
+        P.saved[row] = sv;
+      }
+      if (TOP && lane < P.top) {
+        const Key k = T.lists[C > 1 ? 0 : TH / 32][lane];
+        P.top_logprobs[(uint64_t)row * P.top + lane] = log_p(value_of((uint32_t)(k >> 32)));
+        P.top_tokens[(uint64_t)row * P.top + lane] = (int32_t)place_of(k);
+      }
     }
   }
   if (C > 1) cluster.sync();   // (the others' memory is read until here)
 }
 
 // ----------------------------------------------------------------------------- backward pass
+// dx_j = p_j (a + b log2 p_j) + [j = v] at, with p_j = 2^d / sum:  2^d (A + B d).
 struct RowGrad {
-  float max, scale, log2_sum;   // lp_j = ((x_j - max) scale - log2_sum) ln 2
-  float a, b;                   // dx_j = p_j (a + b log2 p_j) + [j = v] at
-  float at;
-  __device__ __forceinline__ float operator()(float x) const {
-    const float l = max_nan((x - max) * scale - log2_sum, -200.f);
-    return ex2(l) * fmaf(b, l, a);
+  float scale, shift, A, B, at;
+  bool careful, plain;   // plain: B is 0
+  __device__ __forceinline__ RowGrad(const Saved& sv, float g, float h) {
+    const float a = -(g + h * sv.entropy) * sv.inv_t, b = -h * kLn2 * sv.inv_t, inv = 1.f / sv.sum;
+    scale = sv.inv_t * kLog2e;
+    shift = sv.shift;
+    A = inv * (a - b * sv.log2_sum);
+    B = inv * b;
+    at = g * sv.inv_t;
+    careful = sv.careful;
+    plain = h == 0.f;
+  }
+  __device__ __forceinline__ float operator()(float x) const {   // any row
+    const float d = max_nan(careful ? (x - shift) * scale : fmaf(x, scale, -shift), -200.f);
+    return ex2(d) * fmaf(B, d, A);
+  }
+  template <bool PLAIN>
+  __device__ __forceinline__ float2 two(float2 x) const {        // a row that is not `careful`
+    float2 d = __ffma2_rn(x, make_float2(scale, scale), make_float2(-shift, -shift));
+    if (PLAIN) return __fmul2_rn(make_float2(ex2(d.x), ex2(d.y)), make_float2(A, A));
+    d = make_float2(max_nan(d.x, -200.f), max_nan(d.y, -200.f));
+    return __fmul2_rn(make_float2(ex2(d.x), ex2(d.y)), __ffma2_rn(d, make_float2(B, B), make_float2(A, A)));
   }
 };
+template <bool F32, bool PLAIN>
+__device__ __forceinline__ void grad_words(const RowGrad& R, uint32_t (&q)[8]) {
+#pragma unroll
+  for (int i = 0; i < (F32 ? 4 : 8); i++) {
+    if (F32) {
+      const float2 v = R.two<PLAIN>(make_float2(__uint_as_float(q[2 * i]), __uint_as_float(q[2 * i + 1])));
+      q[2 * i] = __float_as_uint(v.x);
+      q[2 * i + 1] = __float_as_uint(v.y);
+    } else {
+      const float2 v = R.two<PLAIN>(make_float2(bf16_lo(q[i]), bf16_hi(q[i])));
+      q[i] = pack_bf16(v.x, v.y);
+    }
+  }
+}
 template <bool F32>
 __global__ void __launch_bounds__(kThreads) k_grad(const GradArgs P) {
   after_previous();
@@ -529,36 +647,29 @@ __global__ void __launch_bounds__(kThreads) k_grad(const GradArgs P) {
   const Windows<F32> W(P.x + row * P.ld, P.vocab);
   uint8_t* out = P.dx + row * P.ld_dx;
   const bool zero = sv.token < 0 || (g == 0.f && h == 0.f);
-  RowGrad R;
-  R.max = sv.max;
-  R.scale = sv.inv_t * kLog2e;
-  R.log2_sum = sv.log2_sum;
-  R.a = -(g + h * sv.entropy) * sv.inv_t;
-  R.b = -h * kLn2 * sv.inv_t;
-  R.at = g * sv.inv_t;
+  const RowGrad R(sv, g, h);
   const uint32_t w = piece * kThreads + threadIdx.x;
   if (w >= W.count) return;
   const int32_t e0 = W.first(w);
   constexpr uint32_t E = Windows<F32>::kElems, S = Windows<F32>::kSize;
-  if (W.whole(w) && (reinterpret_cast<uintptr_t>(out + (int64_t)e0 * S) & 31) == 0) {
-    uint8_t* o = out + (int64_t)e0 * S;
-    uint32_t q[2][8];
+  uint8_t* o = out + (int64_t)e0 * S;
+  if (W.whole(w) && (reinterpret_cast<uintptr_t>(o) & 31) == 0 && (zero || !R.careful)) {
+    uint32_t lo[8], hi[8];
     const uint32_t v = (uint32_t)(sv.token - e0);   // the token's place, when below E
     float at = 0.f;
     if (zero) {
 #pragma unroll
-      for (int i = 0; i < 16; i++) q[i / 8][i % 8] = 0;
+      for (int i = 0; i < 8; i++) lo[i] = hi[i] = 0;
     } else {
-      W.load(w, q[0], q[1]);
+      const uint8_t* p = W.base + (uint64_t)w * kWindow;
+      ld32(lo, p);
+      ld32(hi, p + 32);
       if (v < E) at = R(element<F32>(W.row + (int64_t)sv.token * S)) + R.at;
-#pragma unroll
-      for (int i = 0; i < 16; i++) {
-        uint32_t& u = q[i / 8][i % 8];
-        u = F32 ? __float_as_uint(R(__uint_as_float(u))) : pack_bf16(R(bf16_lo(u)), R(bf16_hi(u)));
-      }
+      if (R.plain) grad_words<F32, true>(R, lo), grad_words<F32, true>(R, hi);
+      else grad_words<F32, false>(R, lo), grad_words<F32, false>(R, hi);
     }
-    st32(o, q[0]);
-    st32(o + 32, q[1]);
+    st32(o, lo);
+    st32(o + 32, hi);
     if (!zero && v < E) {
       if (F32) *reinterpret_cast<float*>(o + v * S) = at;
       else *reinterpret_cast<uint16_t*>(o + v * S) = (uint16_t)pack_bf16(at, 0.f);

@@ -6,6 +6,7 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdlib>
+#include <type_traits>
 #include <cooperative_groups.h>
 
 #include "bo_internal.cuh"
@@ -17,11 +18,12 @@ namespace cg = cooperative_groups;
 #ifndef LB
 #define LB 6
 #define LBT 4
+#define NOIN __noinline__
 #endif
 
 
 constexpr uint32_t kThreads = 256;
-constexpr uint32_t kMaxCluster = 8;
+constexpr uint32_t kMaxLogCluster = 3;
 constexpr uint32_t kWindow = 64;                 // bytes
 constexpr uint32_t kSegment = 8192;              // windows whose maxima are kept at once
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
@@ -47,7 +49,7 @@ struct ScoreArgs {
   const float* temps;     // may be NULL
   uint64_t temp_stride;   // elements
   float temp;
-  uint32_t token_bytes, rows, vocab, top;
+  uint32_t token_bytes, rows, vocab, top, log_cluster;
   float* logprobs;
   float* entropy;
   float* top_logprobs;
@@ -183,17 +185,18 @@ __device__ __forceinline__ float two_to(float whole) {   // of a whole number th
 }
 struct Joined {
   float max, shift, s, t;
-  __device__ __forceinline__ Joined from(int d) const {   // another lane's
-    return Joined{__shfl_xor_sync(0xffffffffu, max, d), __shfl_xor_sync(0xffffffffu, shift, d),
-                  __shfl_xor_sync(0xffffffffu, s, d), __shfl_xor_sync(0xffffffffu, t, d)};
-  }
-  __device__ __forceinline__ void join(const Joined& o) {
-    const float to = fmaxf(shift, o.shift), da = shift - to, db = o.shift - to;
-    const float fa = two_to(da), fb = two_to(db);
-    t = fa * fmaf(s, da, t) + fb * fmaf(o.s, db, o.t);
-    s = fa * s + fb * o.s;
+  // Those of all lanes: the greatest shift, then sums of the same scale.
+  __device__ __forceinline__ void join_warp() {
+    asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(max));
+    const float to = (float)__reduce_max_sync(0xffffffffu, (int)shift), d = shift - to, f = two_to(d);
+    t = f * fmaf(s, d, t);
+    s = f * s;
     shift = to;
-    max = fmaxf(max, o.max);
+#pragma unroll
+    for (int i = 16; i; i >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, i);
+      t += __shfl_xor_sync(0xffffffffu, t, i);
+    }
   }
 };
 __device__ __forceinline__ Joined nothing() {
@@ -350,36 +353,46 @@ __device__ __forceinline__ uint32_t sorted(uint32_t v, uint32_t lane) {
   return v;
 }
 
+// A window's maximum as it is kept: as the logits are.
+template <bool F32>
+using Max = typename std::conditional<F32, float, uint16_t>::type;
+__device__ __forceinline__ void put_max(float* to, float m) { *to = m; }
+__device__ __forceinline__ void put_max(uint16_t* to, float m) { *to = (uint16_t)(__float_as_uint(m) >> 16); }
+__device__ __forceinline__ float max_value(float m) { return m; }
+__device__ __forceinline__ float max_value(uint16_t m) { return __uint_as_float((uint32_t)m << 16); }
+
 // Shared memory of the search for top tokens.
 template <uint32_t TH>
 struct TopSearch {
-  static constexpr uint32_t kCandidates = TH;
   Key lists[(TH / 32) + 1][32];     // the last one: of the segments so far
   uint32_t values[(TH / 32)][32];
-  uint32_t windows[kCandidates];
-  Key keys[kCandidates];
+  uint32_t windows[TH];
+  Key keys[TH];
   uint32_t nwindows, nkeys;
 };
 
-// Of a segment of windows [w0, w1) with the maxima's order in maxima[], its 32 greatest elements in
-// T.lists[0], whatever values are alike.  The k greatest elements lie in the k windows with the greatest
-// maxima (each of those that precede an element's window has one that precedes the element), and those
-// windows are among the windows of the k threads with the greatest maxima.  best: this thread's.
+// Of a segment of windows [w0, w1) with their maxima in maxima[], its 32 greatest elements in T.lists[0],
+// whatever values are alike.  The k greatest elements lie in the k windows with the greatest maxima (each
+// of those that precede an element's window has one that precedes the element), and those windows are
+// among the windows of the k threads with the greatest maxima.
 template <uint32_t TH, bool F32>
-__device__ __noinline__ void segment_top_of_alike(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top, Key best,
-                                     const uint32_t* maxima, TopSearch<TH>& T, uint32_t warp, uint32_t lane) {
+__device__ __noinline__ void segment_top_of_alike(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top,
+                                                  const Max<F32>* maxima, TopSearch<TH>& T) {
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  Key best = 0, mine = 0;
+  for (uint32_t w = w0 + threadIdx.x; w < w1; w += TH) best = max(best, key_of(order_of(max_value(maxima[w - w0])), w));
   join_lists<TH>(sorted(best, lane), T.lists, warp, lane);
-  Key mine = 0;
-  for (uint32_t i = warp; i < top; i += (TH / 32)) {
+  for (uint32_t i = warp; i < top; i += TH / 32) {
     const Key k = T.lists[0][i];
     if (!k) break;
-    for (uint32_t w = w0 + (place_of(k) - w0) % TH + lane * TH, n = 0; n < kSegment; n += 32 * TH, w += 32 * TH)
-      mine = merged(mine, sorted(w < w1 ? key_of(maxima[w - w0], w) : 0, lane), lane);   // the thread's windows
+    uint32_t w = w0 + (place_of(k) - w0) % TH + lane * TH;   // the thread's windows
+    for (uint32_t n = 0; n < kSegment; n += 32 * TH, w += 32 * TH)
+      mine = merged(mine, sorted(w < w1 ? key_of(order_of(max_value(maxima[w - w0])), w) : 0, lane), lane);
   }
   __syncthreads();
   join_lists<TH>(mine, T.lists, warp, lane);
   mine = 0;
-  for (uint32_t i = warp; i < top; i += (TH / 32)) {
+  for (uint32_t i = warp; i < top; i += TH / 32) {
     const Key k = T.lists[0][i];
     if (!k) break;
     mine = merged(mine, sorted(W.key(place_of(k), lane), lane), lane);
@@ -387,18 +400,21 @@ __device__ __noinline__ void segment_top_of_alike(const Windows<F32>& W, uint32_
   __syncthreads();
   join_lists<TH>(mine, T.lists, warp, lane);
 }
-// The same, much sooner where few values are alike.  At least `top` elements are as great as the thread's
-// maximum that is the top-th of all threads' (the floor), so the others do not count; the windows with
-// such elements are listed, then the elements, and these are sorted.
+// The same, much sooner where few values are alike.  best: the greatest maximum of this thread's windows.
+// At least `top` elements are as great as the one of these that is the top-th of all threads' (the floor),
+// so lesser ones do not count; the windows with such elements are listed, then the elements, and each
+// goes to the place that the number of greater ones is.
 template <uint32_t TH, bool F32>
-__device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top,
-                                            uint32_t best, uint32_t best_at, const uint32_t* maxima, TopSearch<TH>& T,
-                                            uint32_t warp, uint32_t lane) {
-  uint32_t v = sorted(best, lane);
+__device__ NOIN void segment_top(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top, float best,
+                                         const Max<F32>* maxima, TopSearch<TH>& T) {
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t best_order = threadIdx.x < w1 - w0 ? order_of(best) : 0;
+  uint32_t v = sorted(best_order, lane);
   T.values[warp][lane] = v;
+  if (warp == 0) T.lists[0][lane] = 0;
   if (threadIdx.x == 0) T.nwindows = T.nkeys = 0;
   __syncthreads();   // (the maxima are there, too)
-  for (uint32_t half = (TH / 32) / 2; half; half /= 2) {
+  for (uint32_t half = TH / 64; half; half /= 2) {
     if (warp < half) {
       v = max(v, T.values[warp + half][31 - lane]);
 #pragma unroll
@@ -408,41 +424,53 @@ __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, 
     __syncthreads();
   }
   const uint32_t floor = T.values[0][top - 1];
-  if (best >= floor && best > 0)
+  if (best_order >= floor && best_order > 0)
     for (uint32_t w = w0 + threadIdx.x; w < w1; w += TH)
-      if (maxima[w - w0] >= floor) {
+      if (order_of(max_value(maxima[w - w0])) >= floor) {
         const uint32_t i = atomicAdd(&T.nwindows, 1u);
-        if (i < TopSearch<TH>::kCandidates) T.windows[i] = w;
+        if (i < TH) T.windows[i] = w;
       }
   __syncthreads();
   const uint32_t nw = T.nwindows;
-  if (nw <= TopSearch<TH>::kCandidates) {
-    for (uint32_t i = warp; i < nw; i += (TH / 32)) {
-      const Key k = W.key(T.windows[i], lane);
-      const bool in = k && (uint32_t)(k >> 32) >= floor;
-      const uint32_t who = __ballot_sync(0xffffffffu, in);
+  if (nw <= TH) {
+    constexpr int kAtOnce = 8;   // windows of a warp that are read at once
+    for (uint32_t i0 = warp; i0 < nw; i0 += kAtOnce * (TH / 32)) {
+      Key k[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; j++) {
+        const uint32_t i = i0 + j * (TH / 32);
+        k[j] = i < nw ? W.key(T.windows[i], lane) : 0;
+      }
+      uint32_t n = 0, before[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; j++) {
+        const uint32_t who = __ballot_sync(0xffffffffu, k[j] && (uint32_t)(k[j] >> 32) >= floor);
+        before[j] = who >> lane & 1 ? n + __popc(who & ((1u << lane) - 1)) : TH;
+        n += __popc(who);
+      }
       uint32_t at = 0;
-      if (lane == 0) at = atomicAdd(&T.nkeys, (uint32_t)__popc(who));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
-      if (in && at < TopSearch<TH>::kCandidates) T.keys[at] = k;
+      if (lane == 0) at = atomicAdd(&T.nkeys, n);
+      at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; j++)
+        if (at + before[j] < TH) T.keys[at + before[j]] = k[j];
     }
     __syncthreads();
     const uint32_t n = T.nkeys;
-    if (n <= TopSearch<TH>::kCandidates) {
-      const uint32_t i = threadIdx.x;
-      Key mine = 0;
-      if (warp * 32 < n) mine = sorted(i < n ? T.keys[i] : 0, lane);
-      if (n > 32) {
-        join_lists<TH>(mine, T.lists, warp, lane);
-      } else {
-        if (warp == 0) T.lists[0][lane] = mine;
-        __syncthreads();
+    if (n <= TH) {
+      if (threadIdx.x < n) {
+        const Key mine = T.keys[threadIdx.x];
+        uint32_t greater = 0;
+#pragma unroll 8
+        for (uint32_t i = 0; i < n; i++) greater += T.keys[i] > mine;
+        if (greater < 32) T.lists[0][greater] = mine;
       }
+      __syncthreads();
       return;
     }
   }
   __syncthreads();
-  segment_top_of_alike(W, w0, w1, top, best ? key_of(best, best_at) : 0, maxima, T, warp, lane);
+  segment_top_of_alike<TH, F32>(W, w0, w1, top, maxima, T);
 }
 
 // ------------------------------------------------------------------------------ forward pass
@@ -450,14 +478,15 @@ __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, 
 // their sums and lists.
 template <uint32_t TH, bool F32, bool ENT, bool TOP>
 __global__ void __launch_bounds__(TH, (TOP ? LBT : LB) * 256 / TH) k_score(const ScoreArgs P) {
-  extern __shared__ uint32_t maxima[];
+  extern __shared__ float dynamic[];
+  Max<F32>* const maxima = reinterpret_cast<Max<F32>*>(dynamic);
   __shared__ TopSearch<TH> tops[1];
   __shared__ Joined parts[(TH / 32)], whole;
   TopSearch<TH>& T = tops[0];
   after_previous();
   const cg::cluster_group cluster = cg::this_cluster();
-  const uint32_t C = cluster.num_blocks(), c = cluster.block_rank();
-  const uint32_t row = blockIdx.x / C, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t log_c = P.log_cluster, C = 1u << log_c, c = blockIdx.x & (C - 1);
+  const uint32_t row = blockIdx.x >> log_c, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint8_t* at = P.tokens + row * P.token_stride;
   const int64_t token = P.token_bytes == 8 ? *reinterpret_cast<const int64_t*>(at)
                                            : *reinterpret_cast<const int32_t*>(at);
@@ -479,7 +508,7 @@ __global__ void __launch_bounds__(TH, (TOP ? LBT : LB) * 256 / TH) k_score(const
   const float inv_t = temp > 0.f && temp <= FLT_MAX ? 1.f / temp : __int_as_float(0x7FFFFFFF);
   const float scale = inv_t * kLog2e;
   const Windows<F32> W(P.x + row * P.ld, P.vocab);
-  const uint32_t begin = (uint32_t)((uint64_t)W.count * c / C), end = (uint32_t)((uint64_t)W.count * (c + 1) / C);
+  const uint32_t begin = W.count * c >> log_c, end = W.count * (c + 1) >> log_c;   // (2^20 windows at most)
   const bool valid = token < (int64_t)P.vocab;
   float given = 0.f;   // the token's logit, under way while the row is read
   if (c == 0 && warp == 0 && valid) given = element<F32>(W.row + token * Windows<F32>::kSize);
@@ -490,13 +519,12 @@ __global__ void __launch_bounds__(TH, (TOP ? LBT : LB) * 256 / TH) k_score(const
   const uint32_t edge0 = W.whole(0) ? 0 : 1, edge1 = W.count > 1 && !W.whole(W.count - 1) ? W.count - 1 : W.count;
   for (uint32_t w0 = begin; w0 < end; w0 += kSegment) {
     const uint32_t w1 = TOP ? min(end, w0 + kSegment) : end;
-    uint32_t best = 0, best_at = 0;
+    float best = -INFINITY;
     auto take = [&](uint32_t w, const uint32_t (&lo)[8], const uint32_t (&hi)[8]) {
       const float m = window_max<F32>(lo, hi);
       if (TOP) {
-        const uint32_t o = order_of(m);
-        maxima[w - w0] = o;
-        if (o > best || (o == best && w < best_at)) best = o, best_at = w;   // (the last window comes first)
+        put_max(maxima + (w - w0), m);
+        best = max_nan(best, m);
       }
       if (m > a.max) a.raise(m, scale);
       add_window<F32, ENT>(a, lo, hi, scale);
@@ -522,27 +550,24 @@ __global__ void __launch_bounds__(TH, (TOP ? LBT : LB) * 256 / TH) k_score(const
       take(w, lo, hi);
     }
     if (!TOP) break;
-    segment_top<TH, F32>(W, w0, w1, P.top, best, best_at, maxima, T, warp, lane);
+    segment_top<TH, F32>(W, w0, w1, P.top, best, maxima, T);
     if (warp == 0) T.lists[TH / 32][lane] = w0 == begin ? T.lists[0][lane] : merged(T.lists[TH / 32][lane], T.lists[0][lane], lane);
     __syncthreads();
   }
 
   Joined j = a.joined();
-#pragma unroll
-  for (int d = 16; d; d >>= 1) j.join(j.from(d));
+  j.join_warp();
   if (lane == 0) parts[warp] = j;
   __syncthreads();
   // (every warp has the block's sums, and of the first block the cluster's)
   j = lane < TH / 32 ? parts[lane] : nothing();
-#pragma unroll
-  for (int d = TH / 64; d; d >>= 1) j.join(j.from(d));
+  j.join_warp();
   if (C > 1) {
     if (threadIdx.x == 0) whole = j;
     cluster.sync();
     if (c == 0) {
       j = lane < C ? *cluster.map_shared_rank(&whole, lane) : nothing();
-#pragma unroll
-      for (int d = kMaxCluster / 2; d; d >>= 1) j.join(j.from(d));
+      j.join_warp();
       if (TOP) {   // (their lists lie sorted)
         Key mine = 0;
         for (uint32_t b = warp; b < C; b += TH / 32) {
@@ -554,8 +579,6 @@ __global__ void __launch_bounds__(TH, (TOP ? LBT : LB) * 256 / TH) k_score(const
     }
   }
   if (c == 0) {
-    j = Joined{__shfl_sync(0xffffffffu, j.max, 0), __shfl_sync(0xffffffffu, j.shift, 0),
-               __shfl_sync(0xffffffffu, j.s, 0), __shfl_sync(0xffffffffu, j.t, 0)};
     const float far = j.max * scale;
     const bool careful = !(far >= kLeast && far <= kMost) || (ENT && !(scale >= kLeastScale));
     if (careful) {
@@ -731,13 +754,14 @@ bool strided(const void* p, uint64_t stride, uint64_t size) {
 }
 
 template <uint32_t TH, bool F32>
-cudaError_t score(const ScoreArgs& P, uint32_t cluster, cudaStream_t s) {
+cudaError_t score(const ScoreArgs& P, cudaStream_t s) {
+  const uint32_t cluster = 1u << P.log_cluster;
   const bool ent = P.entropy != nullptr, top = P.top > 0;
   auto k = ent ? (top ? k_score<TH, F32, true, true> : k_score<TH, F32, true, false>)
                : (top ? k_score<TH, F32, false, true> : k_score<TH, F32, false, false>);
   // (a window more than a row fills where it begins inside one, and than its part of a cluster's)
   const uint64_t windows = ((uint64_t)P.vocab * (F32 ? 4 : 2) / kWindow + 2) / cluster + 1;
-  const uint32_t smem = top ? (uint32_t)std::min<uint64_t>(kSegment, windows) * 4 : 0;
+  const uint32_t smem = top ? (uint32_t)std::min<uint64_t>(kSegment, windows) * sizeof(Max<F32>) : 0;
   return launch(k, dim3(P.rows * cluster), TH, smem, cluster, s, P);
 }
 
@@ -817,12 +841,12 @@ int bo_logprobs_forward(const bo_logprobs* h, const void* d_logits, uint32_t dty
   static const uint32_t kCt = getenv("CT") ? atoi(getenv("CT")) : 4;
   static const uint32_t kCw = getenv("CW") ? atoi(getenv("CW")) : 1024;
   const uint64_t windows = (uint64_t)h->vocab * size / kWindow;
-  uint32_t cluster = 1;
-  while (cluster < kMaxCluster && (uint64_t)rows * cluster < (uint64_t)sms * kCt && windows >= 2 * cluster * kCw) cluster *= 2;
+  P.log_cluster = 0;
+  while (P.log_cluster < kMaxLogCluster && (uint64_t)rows << P.log_cluster < (uint64_t)sms * kCt && windows >> P.log_cluster >= 2 * kCw) P.log_cluster++;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   static const uint32_t kTt = getenv("TT") ? atoi(getenv("TT")) : 256;
-  return check(kTt == 128 ? (dtype == BO_FP32 ? score<128, true>(P, cluster, s) : score<128, false>(P, cluster, s)) : 
-    (dtype == BO_FP32 ? score<256, true>(P, cluster, s) : score<256, false>(P, cluster, s)));
+  return check(kTt == 128 ? (dtype == BO_FP32 ? score<128, true>(P, s) : score<128, false>(P, s)) : 
+    (dtype == BO_FP32 ? score<256, true>(P, s) : score<256, false>(P, s)));
 }
 
 int bo_logprobs_backward(const bo_logprobs* h, const void* d_logits, uint32_t dtype, uint64_t ld,

@@ -5,7 +5,6 @@
 // the first and the last may lie partly outside the row, and are read by the element.
 #include <cfloat>
 #include <cmath>
-#include <cstdlib>
 #include <type_traits>
 #include <cooperative_groups.h>
 
@@ -15,11 +14,6 @@ namespace bo {
 namespace {
 
 namespace cg = cooperative_groups;
-#ifndef LB
-#define LB 6
-#define LBT 4
-#define NOIN __noinline__
-#endif
 
 
 constexpr uint32_t kThreads = 256;
@@ -365,7 +359,7 @@ __device__ __forceinline__ float max_value(uint16_t m) { return __uint_as_float(
 template <uint32_t TH>
 struct TopSearch {
   Key lists[(TH / 32) + 1][32];     // the last one: of the segments so far
-  uint32_t values[(TH / 32)][32];
+  uint32_t values[TH / 32][32];
   uint32_t windows[TH];
   Key keys[TH];
   uint32_t nwindows, nkeys;
@@ -403,10 +397,11 @@ __device__ __noinline__ void segment_top_of_alike(const Windows<F32>& W, uint32_
 // The same, much sooner where few values are alike.  best: the greatest maximum of this thread's windows.
 // At least `top` elements are as great as the one of these that is the top-th of all threads' (the floor),
 // so lesser ones do not count; the windows with such elements are listed, then the elements, and each
-// goes to the place that the number of greater ones is.
+// goes to the place that the number of greater ones is.  (A floor from each warp by itself takes a third
+// of the steps and lets through so many more that one row takes 9.3 us instead of 8.0.)
 template <uint32_t TH, bool F32>
-__device__ NOIN void segment_top(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top, float best,
-                                         const Max<F32>* maxima, TopSearch<TH>& T) {
+__device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top, float best,
+                                            const Max<F32>* maxima, TopSearch<TH>& T) {
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t best_order = threadIdx.x < w1 - w0 ? order_of(best) : 0;
   uint32_t v = sorted(best_order, lane);
@@ -477,7 +472,7 @@ __device__ NOIN void segment_top(const Windows<F32>& W, uint32_t w0, uint32_t w1
 // The blocks of a cluster share a row: each takes its part of the windows, and the first one joins
 // their sums and lists.
 template <uint32_t TH, bool F32, bool ENT, bool TOP>
-__global__ void __launch_bounds__(TH, (TOP ? LBT : LB) * 256 / TH) k_score(const ScoreArgs P) {
+__global__ void __launch_bounds__(TH, (TOP || TH == 128 ? 1024 : 1536) / TH) k_score(const ScoreArgs P) {
   extern __shared__ float dynamic[];
   Max<F32>* const maxima = reinterpret_cast<Max<F32>*>(dynamic);
   __shared__ TopSearch<TH> tops[1];
@@ -568,13 +563,23 @@ __global__ void __launch_bounds__(TH, (TOP ? LBT : LB) * 256 / TH) k_score(const
     if (c == 0) {
       j = lane < C ? *cluster.map_shared_rank(&whole, lane) : nothing();
       j.join_warp();
-      if (TOP) {   // (their lists lie sorted)
-        Key mine = 0;
-        for (uint32_t b = warp; b < C; b += TH / 32) {
-          const Key k = cluster.map_shared_rank(&T.lists[TH / 32][0], b)[lane];
-          mine = b == warp ? k : merged(mine, k, lane);
+      if (TOP) {   // each of their keys goes to the place that the number of greater ones is
+        // (a list a warp: clusters have blocks of 256 threads)
+        if (warp < C) T.lists[warp][lane] = cluster.map_shared_rank(&T.lists[TH / 32][0], warp)[lane];
+        if (warp == 0) T.keys[lane] = 0;
+        __syncthreads();
+        if (warp < C) {
+          const Key mine = T.lists[warp][lane];
+          uint32_t greater = 0;
+          for (uint32_t b = 0; b < C; b++) {   // (the lists are in order)
+            uint32_t n = 0;
+#pragma unroll
+            for (uint32_t step = 16; step; step /= 2) n += T.lists[b][n + step - 1] > mine ? step : 0;
+            greater += n + (T.lists[b][n] > mine);
+          }
+          if (mine && greater < 32) T.keys[greater] = mine;
         }
-        join_lists<TH>(mine, T.lists, warp, lane);
+        __syncthreads();
       }
     }
   }
@@ -611,7 +616,7 @@ __global__ void __launch_bounds__(TH, (TOP ? LBT : LB) * 256 / TH) k_score(const
         P.saved[row] = sv;
       }
       if (TOP && lane < P.top) {
-        const Key k = T.lists[C > 1 ? 0 : TH / 32][lane];
+        const Key k = C > 1 ? T.keys[lane] : T.lists[TH / 32][lane];
         P.top_logprobs[(uint64_t)row * P.top + lane] = log_p(value_of((uint32_t)(k >> 32)));
         P.top_tokens[(uint64_t)row * P.top + lane] = (int32_t)place_of(k);
       }
@@ -671,12 +676,27 @@ __global__ void __launch_bounds__(kThreads) k_grad(const GradArgs P) {
   uint8_t* out = P.dx + row * P.ld_dx;
   const bool zero = sv.token < 0 || (g == 0.f && h == 0.f);
   const RowGrad R(sv, g, h);
-  const uint32_t w = piece * kThreads + threadIdx.x;
-  if (w >= W.count) return;
-  const int32_t e0 = W.first(w);
   constexpr uint32_t E = Windows<F32>::kElems, S = Windows<F32>::kSize;
-  uint8_t* o = out + (int64_t)e0 * S;
-  if (W.whole(w) && (reinterpret_cast<uintptr_t>(o) & 31) == 0 && (zero || !R.careful)) {
+  auto one = [&](int32_t e) {   // an element by itself
+    if (e < 0 || e >= (int32_t)P.vocab) return;
+    float v = 0.f;
+    if (!zero) v = R(element<F32>(W.row + (int64_t)e * S)) + (e == sv.token ? R.at : 0.f);
+    if (F32) reinterpret_cast<float*>(out)[e] = v;
+    else reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)pack_bf16(v, 0.f);
+  };
+  // Where the two rows begin differently within 32 bytes, or the row has to be worked out carefully:
+  // elements side by side.
+  const int32_t off = (int32_t)W.off * (int32_t)S;
+  if ((reinterpret_cast<uintptr_t>(out - off) & 31) != 0 || (R.careful && !zero)) {
+    const int32_t first = W.first(piece * kThreads) + (int32_t)threadIdx.x;
+#pragma unroll 4
+    for (uint32_t i = 0; i < E; i++) one(first + (int32_t)(i * kThreads));
+    return;
+  }
+  const uint32_t w = piece * kThreads + threadIdx.x, last = W.count - 1;
+  if (w <= last && W.whole(w)) {
+    const int32_t e0 = W.first(w);
+    uint8_t* o = out + (int64_t)e0 * S;
     uint32_t lo[8], hi[8];
     const uint32_t v = (uint32_t)(sv.token - e0);   // the token's place, when below E
     float at = 0.f;
@@ -697,15 +717,12 @@ __global__ void __launch_bounds__(kThreads) k_grad(const GradArgs P) {
       if (F32) *reinterpret_cast<float*>(o + v * S) = at;
       else *reinterpret_cast<uint16_t*>(o + v * S) = (uint16_t)pack_bf16(at, 0.f);
     }
-    return;
   }
-  for (uint32_t i = 0; i < E; i++) {
-    const int32_t e = e0 + (int32_t)i;
-    if (e < 0 || e >= (int32_t)P.vocab) continue;
-    float v = 0.f;
-    if (!zero) v = R(element<F32>(W.row + (int64_t)e * S)) + (e == sv.token ? R.at : 0.f);
-    if (F32) reinterpret_cast<float*>(out)[e] = v;
-    else reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)pack_bf16(v, 0.f);
+  // the windows that are not whole: a warp each
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (lane < E) {
+    if (warp == 0 && piece == 0 && !W.whole(0)) one(W.first(0) + (int32_t)lane);
+    if (warp == 1 && piece == last / kThreads && last > 0 && !W.whole(last)) one(W.first(last) + (int32_t)lane);
   }
 }
 
@@ -821,7 +838,7 @@ int bo_logprobs_forward(const bo_logprobs* h, const void* d_logits, uint32_t dty
   int sms = 0;
   if (const int rc = sm_count(h->device, sms)) return rc;
   if (rows == 0) return BD_OK;
-  ScoreArgs P;
+  ScoreArgs P = {};
   P.x = static_cast<const uint8_t*>(d_logits);
   P.ld = ld * size;
   P.tokens = static_cast<const uint8_t*>(d_tokens);
@@ -838,15 +855,25 @@ int bo_logprobs_forward(const bo_logprobs* h, const void* d_logits, uint32_t dty
   P.top_logprobs = h->d_top_logprobs;
   P.top_tokens = h->d_top_tokens;
   P.saved = static_cast<Saved*>(h->d_saved);
-  static const uint32_t kCt = getenv("CT") ? atoi(getenv("CT")) : 4;
-  static const uint32_t kCw = getenv("CW") ? atoi(getenv("CW")) : 1024;
+  // Where rows are fewer than SMs, several blocks share one: up to eight, with a window a thread at least
+  // (64 rows of 151936: four blocks 6.7 us, one 20).  From there on the largest blocks that the SMs
+  // hold at once (300 rows of 151936: 512 threads 18.8 us, 256 22.8, 128 33), and where no size
+  // does, the smallest (1000 rows: 50 us, with 256 53 to 67).  Rows of up to 2048 windows (65536 BF16 logits)
+  // are too short for 512 (300 rows of 32000: 5.6 us, with 256 5.0).
   const uint64_t windows = (uint64_t)h->vocab * size / kWindow;
-  P.log_cluster = 0;
-  while (P.log_cluster < kMaxLogCluster && (uint64_t)rows << P.log_cluster < (uint64_t)sms * kCt && windows >> P.log_cluster >= 2 * kCw) P.log_cluster++;
+  while (P.log_cluster < kMaxLogCluster && (uint64_t)rows << P.log_cluster < (uint64_t)sms * 3 / 2 &&
+         windows >> P.log_cluster >= 2 * 256)
+    P.log_cluster++;
+  const uint32_t held = sms * (h->top ? 1024 : 1536);   // threads at once
+  const uint32_t threads = P.log_cluster > 0                                        ? 256
+                           : (uint64_t)rows * 512 <= held && windows > 2048 ? 512
+                           : (uint64_t)rows * 256 <= held                   ? 256
+                                                                            : 128;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  static const uint32_t kTt = getenv("TT") ? atoi(getenv("TT")) : 256;
-  return check(kTt == 128 ? (dtype == BO_FP32 ? score<128, true>(P, s) : score<128, false>(P, s)) : 
-    (dtype == BO_FP32 ? score<256, true>(P, s) : score<256, false>(P, s)));
+  const bool f32 = dtype == BO_FP32;
+  return check(threads == 512   ? (f32 ? score<512, true>(P, s) : score<512, false>(P, s))
+               : threads == 256 ? (f32 ? score<256, true>(P, s) : score<256, false>(P, s))
+                                : (f32 ? score<128, true>(P, s) : score<128, false>(P, s)));
 }
 
 int bo_logprobs_backward(const bo_logprobs* h, const void* d_logits, uint32_t dtype, uint64_t ld,
@@ -871,7 +898,7 @@ int bo_logprobs_backward(const bo_logprobs* h, const void* d_logits, uint32_t dt
   int sms = 0;
   if (const int rc = sm_count(h->device, sms)) return rc;
   if (rows == 0) return BD_OK;
-  GradArgs P;
+  GradArgs P = {};
   P.x = static_cast<const uint8_t*>(d_logits);
   P.ld = ld * size;
   P.dx = static_cast<uint8_t*>(d_grad_logits);

@@ -594,9 +594,14 @@ __global__ void __launch_bounds__(TH, (TOP || TH == 128 ? 1024 : 1536) / TH) k_s
       const bool empty = careful && j.s == 0.f;             // nothing but -infinity
       const float inf = __int_as_float(0x7F800000), nan = __int_as_float(0x7FFFFFFF);
       const float log2_sum = log2f(j.s);
+      // l = ln sum e^z
+      const float lse = j.max / temp + kLn2 * (log2_sum + fmaf(-j.max, scale, j.shift));
       auto log_p = [&](float x) {
         if (empty) return -inf * inv_t;
         if (careful) return min_nan((x - j.shift) * inv_t - log2_sum * kLn2, 0.f);
+        // The difference of two FP32 numbers, z and l, as a trainer has it that keeps l: the same token
+        // has the same log probability on both sides.  Past 128 the rounding of l would begin to show.
+        if (fabsf(lse) <= 128.f) return min_nan(x / temp - lse, 0.f);
         const float d = fmaf(x, scale, -j.shift) - log2_sum;
         // (far below, where base 2 could pass the range that the base e does not)
         return d < -1048576.f ? x * inv_t - (j.shift + log2_sum) * kLn2 : min_nan(d * kLn2, 0.f);

@@ -164,25 +164,24 @@ struct Windows {
 };
 
 // ---------------------------------------------------------------------------- online softmax
-// Of the values so far: their maximum; the whole number `shift` above its product with the scale; the sum
-// of e = 2^d over d = x scale - shift, and the sum of e d, in four parts each.  Because the shift is a
-// whole number, d is one fused operation with one rounding, and sums for another shift differ by an exact
-// power of two.  That holds while the product stays between -2^21 and 2^22 (kLeast, kMost): the rows whose
-// maximum does not are read again (careful_sums).  The shift starts below all of them, so that -infinity
-// has e = 0; its d is kept finite, so that e d is 0 and not NaN.
+// Of the values so far: their maximum; `shift`, its product with the scale; the sum of e = 2^d over
+// d = x scale - shift, and the sum of e d, in four parts each.  So d is one fused operation with one
+// rounding, whose d of the maximum is the rounding of the shift.  That holds while the shift stays between
+// -2^21 and 2^22 (kLeast, kMost): the rows whose maximum does not are read again (careful_sums).  The
+// shift starts below all of them, so that -infinity has e = 0; its d is kept finite, so that e d is 0 and
+// not NaN.
 constexpr float kLeast = -2097152.f, kMost = 4194304.f;
 constexpr uint32_t kFloorBf16 = 0xF149F149u;   // -1e30, twice
 constexpr float kFloor = -1e30f, kLeastScale = 1e-23f;
 
-__device__ __forceinline__ float two_to(float whole) {   // of a whole number that is not positive
-  return whole < -126.f ? 0.f : __int_as_float(((int)whole + 127) << 23);
-}
 struct Joined {
   float max, shift, s, t;
   // Those of all lanes: the greatest shift, then sums of the same scale.
   __device__ __forceinline__ void join_warp() {
+    float to = shift;
     asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(max));
-    const float to = (float)__reduce_max_sync(0xffffffffu, (int)shift), d = shift - to, f = two_to(d);
+    asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(to));
+    const float d = shift - to, f = d == 0.f ? 1.f : ex2(d);
     t = f * fmaf(s, d, t);
     s = f * s;
     shift = to;
@@ -204,9 +203,9 @@ struct Sums {
 
   __device__ __forceinline__ void raise(float to, float scale) {   // (not called for a NaN)
     max = to;
-    const float up = fminf(ceilf(to * scale), kMost);
+    const float up = fminf(to * scale, kMost);
     if (!(up > shift)) return;
-    const float d = shift - up, f = two_to(d);
+    const float d = shift - up, f = ex2(d);
     shift = up;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
@@ -594,8 +593,11 @@ __global__ void __launch_bounds__(TH, (TOP || TH == 128 ? 1024 : 1536) / TH) k_s
       const bool empty = careful && j.s == 0.f;             // nothing but -infinity
       const float inf = __int_as_float(0x7F800000), nan = __int_as_float(0x7FFFFFFF);
       const float log2_sum = log2f(j.s);
-      // l = ln sum e^z
-      const float lse = j.max / temp + kLn2 * (log2_sum + fmaf(-j.max, scale, j.shift));
+      // The sum over the greatest term of it, whose own error then cancels: near 1 for a row with one
+      // likely token, whose entropy and -lp are small.  l = ln sum e^z.
+      const float top_d = careful ? 0.f : fmaf(j.max, scale, -j.shift);
+      const float log_sum = logf(j.s / (careful ? 1.f : ex2(top_d)));
+      const float lse = j.max / temp + log_sum;
       auto log_p = [&](float x) {
         if (empty) return -inf * inv_t;
         if (careful) return min_nan((x - j.shift) * inv_t - log2_sum * kLn2, 0.f);
@@ -607,7 +609,7 @@ __global__ void __launch_bounds__(TH, (TOP || TH == 128 ? 1024 : 1536) / TH) k_s
         return d < -1048576.f ? x * inv_t - (j.shift + log2_sum) * kLn2 : min_nan(d * kLn2, 0.f);
       };
       if (lane == 0) {
-        const float entropy = empty ? 0.f : max_nan(kLn2 * (log2_sum - j.t / j.s), 0.f);
+        const float entropy = empty ? 0.f : max_nan(log_sum - kLn2 * (j.t / j.s - top_d), 0.f);
         P.logprobs[row] = valid ? log_p(given) : nan;
         if (ENT) P.entropy[row] = entropy;
         Saved sv = {};

@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_route_grad(const RouteGradArgs 
     const float pm = mine >= 0 ? ex2((xm - max) * kLog2e) * inv : 0.f;
     float add;                         // what the choice adds to its logit
     if (P.normalize) {
-      const float w = pm * rcp(lanes.sum(pm));
+      const float w = pm / lanes.sum(pm);   // (1 of a single choice, whose gradient cancels)
       add = w * (gw - lanes.sum(mine >= 0 ? w * gw : 0.f));
     } else {
       add = pm * gw;

@@ -327,12 +327,11 @@ __device__ __forceinline__ int32_t best_of_16(int32_t* k) {
 // blocks' and writes the results; else each block leaves its own for k_route_join.
 __device__ __forceinline__ void finish(const RouteArgs& P, const int32_t* counts, float* sums, int32_t* reals,
                                        float* parts) {
-  const uint32_t E = P.experts;
+  const uint32_t E = P.experts, threads = blockDim.x, warps = threads / 32;
   __syncthreads();
-  for (uint32_t e = threadIdx.x; e < E; e += kThreads) {   // (the column is this thread's)
+  for (uint32_t e = threadIdx.x; e < E; e += threads) {   // (the column is this thread's)
     float s = 0.f;
-#pragma unroll
-    for (uint32_t i = 0; i < kWarps; i++) s += sums[i * E + e];
+    for (uint32_t i = 0; i < warps; i++) s += sums[i * E + e];
     if (P.joined) {
       sums[e] = s;
     } else {
@@ -342,7 +341,7 @@ __device__ __forceinline__ void finish(const RouteArgs& P, const int32_t* counts
   }
   if (threadIdx.x == 0) {
     int32_t n = 0;
-    for (uint32_t i = 0; i < kWarps; i++) n += reals[i];
+    for (uint32_t i = 0; i < warps; i++) n += reals[i];
     if (P.joined) reals[0] = n;
     else P.real[blockIdx.x] = n;
   }
@@ -354,7 +353,7 @@ __device__ __forceinline__ void finish(const RouteArgs& P, const int32_t* counts
     int32_t N = 0;
     for (uint32_t b = 0; b < C; b++) N += *cluster.map_shared_rank(reals, b);
     float share = 0.f;
-    for (uint32_t e = threadIdx.x; e < E; e += kThreads) {
+    for (uint32_t e = threadIdx.x; e < E; e += threads) {
       float v[kMaxCluster], s = 0.f;
       int32_t m[kMaxCluster], n = 0;
 #pragma unroll
@@ -373,7 +372,7 @@ __device__ __forceinline__ void finish(const RouteArgs& P, const int32_t* counts
     if (threadIdx.x % 32 == 0) parts[threadIdx.x / 32] = share;
     __syncthreads();
     if (threadIdx.x == 0) {
-      for (uint32_t i = 1; i < kWarps; i++) share += parts[i];
+      for (uint32_t i = 1; i < warps; i++) share += parts[i];
       *P.out_loss = N > 0 ? share / (float)N * ((float)E / (float)P.k) : 0.f;
       *P.out_real = N;
     }
@@ -538,27 +537,28 @@ __device__ __forceinline__ int32_t get(const Lists<F32, KL>& l, uint32_t lane, i
 }
 constexpr uint32_t kLevels = 4;   // 16 lanes a token at most: 256 experts
 template <bool F32, int KL>
-struct Waiting {
-  static constexpr uint32_t kBytes = kWarps * (kLevels + 1) * (uint32_t)sizeof(Lists<F32, KL>);
+struct Many {
+  static constexpr uint32_t kMostWarps = !F32 && KL <= 8 ? 9 : 8;   // two blocks of them an SM, by registers
+  static constexpr uint32_t kWarpBytes = (kLevels + 1) * (uint32_t)sizeof(Lists<F32, KL>);
 };
 
 template <bool F32, int KL>
-__global__ void __launch_bounds__(kThreads, 2) k_route_many(const RouteArgs P) {
+__global__ void __launch_bounds__((Many<F32, KL>::kMostWarps * 32), 2) k_route_many(const RouteArgs P) {
   extern __shared__ int4 sh4[];
   typedef Lists<F32, KL> L;
   typedef Short<F32> S;
-  int32_t* counts = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(sh4) + Waiting<F32, KL>::kBytes);
+  int32_t* counts = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(sh4) + blockDim.x / 32 * Many<F32, KL>::kWarpBytes);
   float* sums = reinterpret_cast<float*>(counts + P.experts);
-  __shared__ int32_t reals[kWarps];
-  __shared__ float parts[kWarps];
+  __shared__ int32_t reals[Many<F32, KL>::kMostWarps];
+  __shared__ float parts[Many<F32, KL>::kMostWarps];
   after_previous();
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = P.experts, G = P.lanes;
   const uint32_t g = lane % G, q = lane / G, e0 = g * kLane;
   const Lanes<kLevels> lanes(G);
   L* const wait = reinterpret_cast<L*>(sh4) + warp * (kLevels + 1);
-  for (uint32_t e = threadIdx.x; e < E; e += kThreads) counts[e] = 0;
+  for (uint32_t e = threadIdx.x; e < E; e += blockDim.x) counts[e] = 0;
   __syncthreads();
-  const uint32_t units = (P.tokens + 31) / 32, step = gridDim.x * kWarps;
+  const uint32_t units = (P.tokens + 31) / 32, step = gridDim.x * (blockDim.x / 32);
   float2 total[kLane / 2];
 #pragma unroll
   for (int j = 0; j < (int)kLane / 2; j++) total[j] = make_float2(0.f, 0.f);
@@ -862,6 +862,19 @@ uint32_t power_of_two(uint32_t n) {   // the least that is not below n
 bool whole(const void* p, uint64_t ld, uint32_t width, uint32_t each) {   // (ld in bytes)
   return aligned(p, 32) && ld % 32 == 0 && width % each == 0;
 }
+template <bool F32, int KL>
+int route_many(const RouteArgs& P, uint32_t grid, cudaStream_t s) {
+  // Of the numbers of warps a block, the one that leaves the fewest without work in the last turn: 262144
+  // tokens are 27 turns of 304 blocks' warps, 3 of 9 (T9 us) and not 4 of 8 (T8).
+  const uint32_t turns = ((P.tokens + 31) / 32 + grid - 1) / grid;   // of a block with one warp
+  uint32_t warps = Many<F32, KL>::kMostWarps, least = ~0u;
+  for (uint32_t w = warps; w >= 4; w--) {
+    const uint32_t all = (turns + w - 1) / w * w;
+    if (all < least) least = all, warps = w;
+  }
+  return check(launch(k_route_many<F32, KL>, dim3(grid), warps * 32,
+                      warps * Many<F32, KL>::kWarpBytes + P.experts * (1 + warps) * 4, 1, s, P));
+}
 template <bool F32>
 int route(RouteArgs& P, uint32_t sms, cudaStream_t s) {
   const uint32_t smem = P.experts * (1 + kWarps) * 4;
@@ -883,9 +896,7 @@ int route(RouteArgs& P, uint32_t sms, cudaStream_t s) {
     P.lanes = lanes;
     P.vec = whole(P.x, P.ld, P.experts, kLane);
     grid = std::min({(P.tokens + 31) / 32, sms * 2, kMaxBlocks});
-    rc = P.k <= 4   ? check(launch(k_route_many<F32, 4>, dim3(grid), kThreads, smem + Waiting<F32, 4>::kBytes, 1, s, P))
-         : P.k <= 8 ? check(launch(k_route_many<F32, 8>, dim3(grid), kThreads, smem + Waiting<F32, 8>::kBytes, 1, s, P))
-                    : check(launch(k_route_many<F32, 16>, dim3(grid), kThreads, smem + Waiting<F32, 16>::kBytes, 1, s, P));
+    rc = P.k <= 4 ? route_many<F32, 4>(P, grid, s) : P.k <= 8 ? route_many<F32, 8>(P, grid, s) : route_many<F32, 16>(P, grid, s);
   } else {
     grid = std::min({(P.tokens + kWarps - 1) / kWarps, sms * 3, kMaxBlocks});
     rc = check(launch(one, dim3(grid), kThreads, smem, 1, s, P));

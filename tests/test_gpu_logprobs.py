@@ -112,6 +112,8 @@ CASES = [  # rows, vocab, dtype, ld, offset, top, entropy
     (40, 32000, BF16, None, 0, 20, True), (1000, 32000, BF16, None, 0, 0, True),
     (1, 151936, BF16, None, 0, 20, True), (1, 151936, FP32, None, 0, 20, True),
     (70, 151936, BF16, None, 0, 1, False), (5, 151937, FP32, 151940, 1, 32, True),
+    (240, 140001, BF16, 140004, 3, 0, True), (240, 140001, BF16, None, 0, 20, True), (250, 70001, FP32, None, 1, 0, False),
+    (250, 70001, FP32, None, 0, 20, True), (130, 32000, FP32, None, 0, 5, True), (180, 151936, BF16, None, 0, 0, True),
     (2, 600001, BF16, None, 0, 32, True), (700, 300001, BF16, None, 0, 3, True), (650, 140001, FP32, None, 0, 3, True),
 ]
 
@@ -296,6 +298,46 @@ def test_large_values(dtype):
         dx = lp.backward(x, torch.ones(3, device="cuda"), torch.ones(3, device="cuda"))
         want = torch.tensor([[0.5, 0, 0, -0.5], [-1 / 3, 2 / 3, -1 / 3, 0], [0.5, -0.5, 0, 0]], device="cuda").double() / heat
         _near(dx, want, want.abs() * (2.0 ** -8 if dtype == BF16 else 128 * U), "gradient")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("rows,vocab", [(3, 50000), (240, 140000), (1000, 3001)])
+@pytest.mark.parametrize("heat", [1e-7, 1e6])
+def test_far_from_ordinary_temperatures(dtype, rows, vocab, heat):
+    """So cold that a row's shift passes its bound, and so hot that all tokens are alike."""
+    x, tokens = _logits(rows, vocab, dtype)
+    tokens[::9] = -1
+    lp = bd.TokenLogprobs(rows, vocab, top=6, entropy=True)
+    lp.run(x, tokens, heat)
+    g, h = torch.randn(rows, device="cuda"), torch.randn(rows, device="cuda")
+    dx = lp.backward(x, g, h)
+    step = max(1, (1 << 25) // vocab)
+    for a in range(0, rows, step):
+        part = _View(lp, a, min(rows, a + step))
+        r = _check_forward(part, x[a:a + step], tokens[a:a + step], heat, part.rows)
+        _check_grad(dx[a:a + step], r, tokens[a:a + step], heat, g[a:a + step], h[a:a + step], dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_one_likely_token(dtype):
+    """-lp and the entropy are small, and as right as the sum and l are."""
+    rows, vocab = 64, 32000
+    x, tokens = _logits(rows, vocab, dtype, scale=0.5)
+    at = torch.arange(rows, device="cuda")
+    x[at, tokens] = (12.0 + at / 4).to(dtype)
+    lp = bd.TokenLogprobs(rows, vocab, entropy=True)
+    lp.run(x, tokens)
+    r = _reference(x, tokens, 1.0)
+    # Each of the others' terms is off by (8 + 4 |d|) u.  The greatest term is the sum's size, and each
+    # addition that it goes through rounds by u of it, however small the others are: _adds(vocab) u in
+    # the sum over the greatest term, and as much in its logarithm.
+    rest = 1 - r["p"].amax(1)
+    size = rest * U * (8 + 8 * 30) * 30 + U * _adds(vocab)
+    _near(lp.entropy, r["entropy"], size + 4 * U * r["entropy"], "entropy")
+    # and z, l and ln S each by u of their size
+    z = x.double()[at, tokens].abs()
+    _near(lp.logprobs, r["logprob"], size + 2 * U * (z + 1), "logprobs")
+    assert (lp.logprobs <= 0).all() and (lp.entropy >= 0).all()
 
 
 def test_gradient_against_differences():

@@ -25,6 +25,7 @@ struct RouteArgs {
   uint64_t mask_stride;
   uint32_t tokens, experts, k, normalize;
   uint32_t lanes;         // that share a token (a power of two)
+  uint32_t rounds;        // of a warp's tokens: a power of two, at most `lanes`
   uint32_t vec;           // their parts of a row are whole, aligned words of 32 bytes
   uint32_t joined;        // the grid is one cluster, which writes the results itself
   float* weights;
@@ -509,12 +510,17 @@ __global__ void __launch_bounds__(kThreads) k_route(const RouteArgs P) {
   finish(P, counts, sums, reals, parts);
 }
 
-// A warp takes 32 tokens at a time.  `lanes` lanes share a token, 16 experts each, so that it takes
-// `lanes` rounds of 32 / lanes tokens; in each, a lane finds the KL greatest of its 16 keys.  Lanes
-// join their lists in pairs as soon as two rounds have one each: one of the two lanes goes on with the
-// first round's token, the other with the second's.  After all rounds each lane has the whole list
-// of one token, the one with the lane's number among the 32: a join costs each list once, and not
-// each lane.  Lists that wait lie in shared memory.
+// A warp takes up to 32 tokens at a time.  `lanes` lanes share a token, 16 experts each, and it takes
+// rounds of 32 / lanes tokens; in each, a lane finds the KL greatest of its 16 keys.  Lanes join their
+// lists in pairs as soon as two rounds have one each: one of the two lanes goes on with the first
+// round's token, the other with the second's.  After `lanes` rounds each lane has the whole list of one
+// token: a join costs each list once, and not each lane.  Lists that wait lie in shared memory.  With
+// fewer rounds, where there are too few tokens for all warps, lanes that no round brought together join
+// their lists twice, once in each.
+//
+// The ALU pipe bounds it (71% of its rate; 1000000 tokens of 128 experts in 144 us): 60 of a token's 105
+// instructions are minima, maxima, selections and permutations, 34 of them the sorting networks'.  HBM
+// is at a third.  A third block an SM does not help (51 us for 262144 tokens, with two 50).
 template <bool F32, int KL>
 struct Lists {
   int4 key[KL / 4][32];
@@ -552,13 +558,13 @@ __global__ void __launch_bounds__((Many<F32, KL>::kMostWarps * 32), 2) k_route_m
   __shared__ int32_t reals[Many<F32, KL>::kMostWarps];
   __shared__ float parts[Many<F32, KL>::kMostWarps];
   after_previous();
-  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = P.experts, G = P.lanes;
-  const uint32_t g = lane % G, q = lane / G, e0 = g * kLane;
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = P.experts, G = P.lanes, R = P.rounds;
+  const uint32_t g = lane % G, q = lane / G, e0 = g * kLane, own = g % R, per = 32 / G * R;
   const Lanes<kLevels> lanes(G);
   L* const wait = reinterpret_cast<L*>(sh4) + warp * (kLevels + 1);
   for (uint32_t e = threadIdx.x; e < E; e += blockDim.x) counts[e] = 0;
   __syncthreads();
-  const uint32_t units = (P.tokens + 31) / 32, step = gridDim.x * (blockDim.x / 32);
+  const uint32_t units = (P.tokens + per - 1) / per, step = gridDim.x * (blockDim.x / 32);
   float2 total[kLane / 2];
 #pragma unroll
   for (int j = 0; j < (int)kLane / 2; j++) total[j] = make_float2(0.f, 0.f);
@@ -566,7 +572,7 @@ __global__ void __launch_bounds__((Many<F32, KL>::kMostWarps * 32), 2) k_route_m
   Logits<F32, kLane> ahead;
   bool use_ahead = false;
   auto fetch = [&](uint32_t unit, uint32_t round) {
-    const uint64_t t = (uint64_t)unit * 32 + q * G + round;
+    const uint64_t t = (uint64_t)unit * per + q * R + round;
     use_ahead = t < P.tokens && (!P.mask || P.mask[t * P.mask_stride] != 0);
     if (use_ahead) ahead.load(P.x + t * P.ld, e0, E, P.vec);
     else ahead.clear();
@@ -578,10 +584,10 @@ __global__ void __launch_bounds__((Many<F32, KL>::kMostWarps * 32), 2) k_route_m
     bool use_mine = false;
     int32_t list[kLane], out = INT32_MIN;
 #pragma unroll 1
-    for (uint32_t round = 0; round < G; round++) {
+    for (uint32_t round = 0; round < R; round++) {
       const Logits<F32, kLane> x = ahead;
       bool use = use_ahead;
-      if (round + 1 < G) fetch(unit, round + 1);
+      if (round + 1 < R) fetch(unit, round + 1);
       else if (unit + step < units) fetch(unit + step, 0);
       float max = lanes.max(x.max());
       if (max == __int_as_float(0xFF800000)) use = false, max = 0.f;
@@ -596,7 +602,7 @@ __global__ void __launch_bounds__((Many<F32, KL>::kMostWarps * 32), 2) k_route_m
       const float inv = use ? rcp(sum) : 0.f;
 #pragma unroll
       for (int j = 0; j < (int)kLane / 2; j++) total[j] = __ffma2_rn(e[j], make_float2(inv, inv), total[j]);
-      if (round == g) sum_mine = sum, max_mine = max, use_mine = use;
+      if (round == own) sum_mine = sum, max_mine = max, use_mine = use;
       S::make(x, list);
       out = best_of_16<F32, KL>(list);
 #pragma unroll
@@ -615,10 +621,20 @@ __global__ void __launch_bounds__((Many<F32, KL>::kMostWarps * 32), 2) k_route_m
         merge<KL>(list, other);
         __syncwarp();
       }
-      if (round + 1 < G) put(wait[level], lane, list, out);
+      if (round + 1 < R) put(wait[level], lane, list, out);
     }
-    const uint64_t t = (uint64_t)unit * 32 + lane;
-    if (t >= P.tokens) use_mine = false;
+    // lanes whose parts no round brought together: each of two joins both lists
+#pragma unroll 1
+    for (uint32_t d = R; d < G; d *= 2) {
+      int32_t other[KL];
+#pragma unroll
+      for (int i = 0; i < KL; i++) other[i] = __shfl_xor_sync(kAll, list[i], d);
+      if (F32) out = ::max(::max(out, __shfl_xor_sync(kAll, out, d)), left_out<KL>(list, other));
+      merge<KL>(list, other);
+    }
+    const uint64_t t = (uint64_t)unit * per + q * R + own;
+    const bool mine = g < R && t < P.tokens;   // (the token is this lane's to write)
+    if (!mine) use_mine = false;
     real += __popc(__ballot_sync(kAll, use_mine));
     uint32_t expert[KL];
     float x[KL];
@@ -644,7 +660,7 @@ __global__ void __launch_bounds__((Many<F32, KL>::kMostWarps * 32), 2) k_route_m
       }
       for (uint32_t who = __ballot_sync(kAll, unsure); who; who &= who - 1) {
         const uint32_t src = __ffs(who) - 1;
-        const uint8_t* again = P.x + ((uint64_t)unit * 32 + src) * P.ld;
+        const uint8_t* again = P.x + __shfl_sync(kAll, t, src) * P.ld;
         typedef Keys<F32> K;
         typename K::T key[kLane / 2], top = K::kNone;
 #pragma unroll
@@ -653,16 +669,16 @@ __global__ void __launch_bounds__((Many<F32, KL>::kMostWarps * 32), 2) k_route_m
           key[j] = e < E ? K::make(element<F32>(again, e), e) : K::kNone;
           top = ::max(top, key[j]);
         }
-        const typename K::T mine = choose<F32, (int)kLane / 2>(key, K::warp_max(top), P.k, lane);
+        const typename K::T best = choose<F32, (int)kLane / 2>(key, K::warp_max(top), P.k, lane);
 #pragma unroll
         for (int i = 0; i < KL; i++) {
-          const uint32_t ei = __shfl_sync(kAll, K::expert(mine), i);
-          const float xi = __shfl_sync(kAll, K::value(mine), i);
+          const uint32_t ei = __shfl_sync(kAll, K::expert(best), i);
+          const float xi = __shfl_sync(kAll, K::value(best), i);
           if (lane == src && i < (int)P.k) expert[i] = ei, x[i] = xi;
         }
       }
     }
-    if (t < P.tokens) {
+    if (mine) {
       float w[KL], s[KL];
 #pragma unroll
       for (int i = 0; i < KL; i++) {
@@ -865,8 +881,8 @@ bool whole(const void* p, uint64_t ld, uint32_t width, uint32_t each) {   // (ld
 template <bool F32, int KL>
 int route_many(const RouteArgs& P, uint32_t grid, cudaStream_t s) {
   // Of the numbers of warps a block, the one that leaves the fewest without work in the last turn: 262144
-  // tokens are 27 turns of 304 blocks' warps, 3 of 9 (T9 us) and not 4 of 8 (T8).
-  const uint32_t turns = ((P.tokens + 31) / 32 + grid - 1) / grid;   // of a block with one warp
+  // tokens are 27 turns of 304 blocks' warps, 3 of 9 (47.8 us) and not 4 of 8 (48.7).
+  const uint32_t per = 32 / P.lanes * P.rounds, turns = ((P.tokens + per - 1) / per + grid - 1) / grid;   // of a block with one warp
   uint32_t warps = Many<F32, KL>::kMostWarps, least = ~0u;
   for (uint32_t w = warps; w >= 4; w--) {
     const uint32_t all = (turns + w - 1) / w * w;
@@ -890,12 +906,16 @@ int route(RouteArgs& P, uint32_t sms, cudaStream_t s) {
   const uint32_t lanes = power_of_two((P.experts + kLane - 1) / kLane);
   uint32_t grid;
   int rc;
-  // (Where a warp a token and 32 tokens a warp meet: 8 experts at 7000 tokens, 64 at 10000, 128 at
-  // 15000, 256 at 19000.)
-  if (P.tokens > 5000 + 1000 * lanes && lanes <= 1u << kLevels && P.k <= 16) {
+  // (Where the two forms meet: 16 experts at 6000 tokens, 8.1 us, 128 at 5000, 9.7 us, 256 at 3000, 11.3 us.)
+  if (P.tokens > 6000 && lanes <= 1u << kLevels && P.k <= 16) {
     P.lanes = lanes;
     P.vec = whole(P.x, P.ld, P.experts, kLane);
-    grid = std::min({(P.tokens + 31) / 32, sms * 2, kMaxBlocks});
+    // As many rounds as leave most warps some (128 experts: 20000 tokens take 12.5 us with 2 rounds
+    // and 14.6 with 8, 262144 tokens 58 and 48).
+    P.rounds = lanes;
+    while (P.rounds > 1 && P.tokens / (32 / lanes * P.rounds) < sms * 12) P.rounds /= 2;
+    const uint32_t per = 32 / lanes * P.rounds;
+    grid = std::min({(P.tokens + per - 1) / per, sms * 2, kMaxBlocks});
     rc = P.k <= 4 ? route_many<F32, 4>(P, grid, s) : P.k <= 8 ? route_many<F32, 8>(P, grid, s) : route_many<F32, 16>(P, grid, s);
   } else {
     grid = std::min({(P.tokens + kWarps - 1) / kWarps, sms * 3, kMaxBlocks});

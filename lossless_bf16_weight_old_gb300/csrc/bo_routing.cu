@@ -1,5 +1,9 @@
 // bo_routing.cu -- the experts of each token of a mixture, their weights, per-expert counts and the
 // balance loss, and the gradient of the router's logits (include/ops/bf16ops.h has the formulas).
+//
+// Selection orders whole numbers that no two experts share (keys), so it needs no rule for equal logits.
+// A token's logits are a few hundred bytes: few tokens are bounded by latency, many by the selection's
+// arithmetic, and only the gradient of many by HBM.
 #include <cooperative_groups.h>
 
 #include "bo_internal.cuh"
@@ -444,7 +448,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_route_join(const RouteArgs P, 
 
 // ------------------------------------------------------------------------------ forward pass
 // One warp a token, for few tokens, or more experts or choices than k_route_many takes: lane l holds
-// experts l, l + 32, ...
+// experts l, l + 32, ...; a choice is a maximum over the warp, which the hardware finds in one
+// instruction (FP32 keys: two).  64 tokens of 128 experts take 3.9 us, launch to end, in one cluster of
+// eight blocks that also writes the counts and the loss; 2000 tokens 7.5 us, 3.5 of them k_route_join.
 template <bool F32, int NV>
 __global__ void __launch_bounds__(kThreads) k_route(const RouteArgs P) {
   extern __shared__ uint32_t sh[];
@@ -724,7 +730,9 @@ __global__ void __launch_bounds__((Many<F32, KL>::kMostWarps * 32), 2) k_route_m
 
 // ----------------------------------------------------------------------------- backward pass
 // `lanes` lanes share a token, N experts each and at most one of its choices each.  The choices'
-// logits get their gradient on top of the others' a second time, from the lanes that hold them.
+// logits get their gradient on top of the others' a second time, from the lanes that hold them: the
+// other way, handing each choice to the lane that holds its expert, costs an instruction for each of
+// a lane's experts and choices.  1000000 tokens of 128 FP32 logits take 206 us, 5.3 TB/s (HBM); 32768 8 us.
 template <bool F32, int N>
 __global__ void __launch_bounds__(kThreads, 2) k_route_grad(const RouteGradArgs P) {
   extern __shared__ float share[];   // how often each expert was chosen

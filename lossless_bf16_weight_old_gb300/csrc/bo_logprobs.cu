@@ -138,11 +138,15 @@ struct Windows {
   __device__ __forceinline__ bool whole(uint32_t w) const {
     return first(w) >= 0 && first(w) + kElems <= vocab;
   }
-  // the key of the lane's element of a window; 0 outside the row
-  __device__ __forceinline__ Key key(uint32_t w, uint32_t lane) const {
+  // The lane's element of a window (any of the row's where it lies outside), without a branch, so that
+  // several are under way at once; and its key, 0 outside the row.
+  __device__ __forceinline__ float lane_value(uint32_t w, uint32_t lane) const {
+    const int32_t e = min(max(first(w) + (int32_t)lane, 0), (int32_t)vocab - 1);
+    return element<F32>(row + (int64_t)e * kSize);
+  }
+  __device__ __forceinline__ Key lane_key(float x, uint32_t w, uint32_t lane) const {
     const int32_t e = first(w) + (int32_t)lane;
-    if (lane >= kElems || e < 0 || e >= (int32_t)vocab) return 0;
-    return key_of(order_of(element<F32>(row + (int64_t)e * kSize)), (uint32_t)e);
+    return lane < kElems && e >= 0 && e < (int32_t)vocab ? key_of(order_of(x), (uint32_t)e) : 0;
   }
   // the words of a window that is not whole; -infinity outside the row
   __device__ __forceinline__ void load_edge(uint32_t w, uint32_t (&lo)[8], uint32_t (&hi)[8]) const {
@@ -163,6 +167,17 @@ struct Windows {
     }
   }
 };
+
+// has the L2 fetch whole windows of [begin, end)
+template <bool F32>
+__device__ __forceinline__ void ahead(const Windows<F32>& W, uint32_t begin, uint32_t end) {
+  if (begin < end && !W.whole(begin)) begin++;
+  if (begin < end && !W.whole(end - 1)) end--;
+  if (begin < end)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(W.base + (uint64_t)begin * kWindow),
+                 "r"((end - begin) * kWindow)
+                 : "memory");
+}
 
 // ---------------------------------------------------------------------------- online softmax
 // Of the values so far: their maximum; `shift`, its product with the scale; the sum of e = 2^d over
@@ -356,15 +371,15 @@ __device__ __forceinline__ float max_value(float m) { return m; }
 __device__ __forceinline__ float max_value(uint16_t m) { return __uint_as_float((uint32_t)m << 16); }
 
 // Shared memory of the search for top tokens.
+constexpr uint32_t kWarpWindows = 32;   // that a warp lists at most
 template <uint32_t TH>
 struct TopSearch {
-  Key lists[(TH / 32) + 1][32];     // the last one: of the segments so far
+  Key lists[TH / 32 + 1][32];     // the last one: of the segments so far
   uint32_t values[TH / 32][32];
-  uint32_t windows[TH];
+  uint32_t windows[TH / 32][kWarpWindows];
   Key keys[TH];
-  uint32_t nwindows, nkeys;
+  uint32_t nkeys;
 };
-
 // Of a segment of windows [w0, w1) with their maxima in maxima[], its 32 greatest elements in T.lists[0],
 // whatever values are alike.  The k greatest elements lie in the k windows with the greatest maxima (each
 // of those that precede an element's window has one that precedes the element), and those windows are
@@ -389,16 +404,16 @@ __device__ __noinline__ void segment_top_of_alike(const Windows<F32>& W, uint32_
   for (uint32_t i = warp; i < top; i += TH / 32) {
     const Key k = T.lists[0][i];
     if (!k) break;
-    mine = merged(mine, sorted(W.key(place_of(k), lane), lane), lane);
+    mine = merged(mine, sorted(W.lane_key(W.lane_value(place_of(k), lane), place_of(k), lane), lane), lane);
   }
   __syncthreads();
   join_lists<TH>(mine, T.lists, warp, lane);
 }
 // The same, much sooner where few values are alike.  best: the greatest maximum of this thread's windows.
 // At least `top` elements are as great as the one of these that is the top-th of all threads' (the floor),
-// so lesser ones do not count; the windows with such elements are listed, then the elements, and each
-// goes to the place that the number of greater ones is.  (A floor from each warp by itself takes a third
-// of the steps and lets through so many more that one row takes 9.3 us instead of 8.0.)
+// so lesser ones do not count.  Each warp lists its windows with such elements, then their elements, and
+// each of those goes to the place that the number of greater ones is.  (A floor from each warp by itself
+// takes fewer steps and lets through so many more that one row takes 9.3 us instead of 8.0.)
 template <uint32_t TH, bool F32>
 __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top, float best,
                                             const Max<F32>* maxima, TopSearch<TH>& T) {
@@ -407,7 +422,7 @@ __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, 
   uint32_t v = sorted(best_order, lane);
   T.values[warp][lane] = v;
   if (warp == 0) T.lists[0][lane] = 0;
-  if (threadIdx.x == 0) T.nwindows = T.nkeys = 0;
+  if (threadIdx.x == 0) T.nkeys = 0;
   __syncthreads();   // (the maxima are there, too)
   for (uint32_t half = TH / 64; half; half /= 2) {
     if (warp < half) {
@@ -419,50 +434,54 @@ __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, 
     __syncthreads();
   }
   const uint32_t floor = T.values[0][top - 1];
-  if (best_order >= floor && best_order > 0)
-    for (uint32_t w = w0 + threadIdx.x; w < w1; w += TH)
-      if (order_of(max_value(maxima[w - w0])) >= floor) {
-        const uint32_t i = atomicAdd(&T.nwindows, 1u);
-        if (i < TH) T.windows[i] = w;
-      }
-  __syncthreads();
-  const uint32_t nw = T.nwindows;
-  if (nw <= TH) {
-    constexpr int kAtOnce = 8;   // windows of a warp that are read at once
-    for (uint32_t i0 = warp; i0 < nw; i0 += kAtOnce * (TH / 32)) {
+  uint32_t nw = 0;
+  if (__any_sync(0xffffffffu, best_order >= floor && best_order > 0)) {
+    for (uint32_t w = w0 + threadIdx.x; w - lane < w1; w += TH) {
+      const bool in = w < w1 && order_of(max_value(maxima[w - w0])) >= floor;
+      const uint32_t who = __ballot_sync(0xffffffffu, in);
+      const uint32_t at = nw + __popc(who & ((1u << lane) - 1));
+      if (in && at < kWarpWindows) T.windows[warp][at] = w;
+      nw += __popc(who);
+    }
+    __syncwarp();
+    constexpr uint32_t kAtOnce = 8;   // windows that are read at once
+    const uint32_t listed = min(nw, kWarpWindows);
+    for (uint32_t i0 = 0; i0 < listed; i0 += kAtOnce) {
+      float x[kAtOnce];
+#pragma unroll
+      for (uint32_t j = 0; j < kAtOnce; j++) x[j] = W.lane_value(T.windows[warp][min(i0 + j, listed - 1)], lane);
+      uint32_t n = 0, at = 0;
       Key k[kAtOnce];
 #pragma unroll
-      for (int j = 0; j < kAtOnce; j++) {
-        const uint32_t i = i0 + j * (TH / 32);
-        k[j] = i < nw ? W.key(T.windows[i], lane) : 0;
+      for (uint32_t j = 0; j < kAtOnce; j++) {
+        k[j] = i0 + j < listed ? W.lane_key(x[j], T.windows[warp][min(i0 + j, listed - 1)], lane) : 0;
+        if ((uint32_t)(k[j] >> 32) < floor) k[j] = 0;
+        n += k[j] != 0;
       }
-      uint32_t n = 0, before[kAtOnce];
+      // (each lane's to places of its own)
+      if (__any_sync(0xffffffffu, n > 0)) {
+        if (n) at = atomicAdd(&T.nkeys, n);
 #pragma unroll
-      for (int j = 0; j < kAtOnce; j++) {
-        const uint32_t who = __ballot_sync(0xffffffffu, k[j] && (uint32_t)(k[j] >> 32) >= floor);
-        before[j] = who >> lane & 1 ? n + __popc(who & ((1u << lane) - 1)) : TH;
-        n += __popc(who);
+        for (uint32_t j = 0; j < kAtOnce; j++)
+          if (k[j]) {
+            if (at < TH) T.keys[at] = k[j];
+            at++;
+          }
       }
-      uint32_t at = 0;
-      if (lane == 0) at = atomicAdd(&T.nkeys, n);
-      at = __shfl_sync(0xffffffffu, at, 0);
-#pragma unroll
-      for (int j = 0; j < kAtOnce; j++)
-        if (at + before[j] < TH) T.keys[at + before[j]] = k[j];
+    }
+  }
+  const bool fits = __syncthreads_and(nw <= kWarpWindows);
+  const uint32_t n = T.nkeys;
+  if (fits && n <= TH) {
+    if (threadIdx.x < n) {
+      const Key k = T.keys[threadIdx.x];
+      uint32_t greater = 0;
+#pragma unroll 8
+      for (uint32_t i = 0; i < n; i++) greater += T.keys[i] > k;
+      if (greater < 32) T.lists[0][greater] = k;
     }
     __syncthreads();
-    const uint32_t n = T.nkeys;
-    if (n <= TH) {
-      if (threadIdx.x < n) {
-        const Key mine = T.keys[threadIdx.x];
-        uint32_t greater = 0;
-#pragma unroll 8
-        for (uint32_t i = 0; i < n; i++) greater += T.keys[i] > mine;
-        if (greater < 32) T.lists[0][greater] = mine;
-      }
-      __syncthreads();
-      return;
-    }
+    return;
   }
   __syncthreads();
   segment_top_of_alike<TH, F32>(W, w0, w1, top, maxima, T);
@@ -491,6 +510,10 @@ __global__ void __launch_bounds__(TH, (TOP || TH == 128 ? 1024 : 1536) / TH) k_s
   const cg::cluster_group cluster = cg::this_cluster();
   const uint32_t log_c = P.log_cluster, C = 1u << log_c, c = blockIdx.x & (C - 1);
   const uint32_t row = blockIdx.x >> log_c, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const Windows<F32> W(P.x + row * P.ld, P.vocab);
+  const uint32_t begin = W.count * c >> log_c, end = W.count * (c + 1) >> log_c;   // (2^20 windows at most)
+  // (few rows: the L2 may as well have the block's part on its way while the token is looked up)
+  if (C > 1 && threadIdx.x == 0) ahead(W, begin, end);
   const uint8_t* at = P.tokens + row * P.token_stride;
   const int64_t token = P.token_bytes == 8 ? *reinterpret_cast<const int64_t*>(at)
                                            : *reinterpret_cast<const int32_t*>(at);
@@ -511,8 +534,6 @@ __global__ void __launch_bounds__(TH, (TOP || TH == 128 ? 1024 : 1536) / TH) k_s
   }
   const float inv_t = temp > 0.f && temp <= FLT_MAX ? 1.f / temp : __int_as_float(0x7FFFFFFF);
   const float scale = inv_t * kLog2e;
-  const Windows<F32> W(P.x + row * P.ld, P.vocab);
-  const uint32_t begin = W.count * c >> log_c, end = W.count * (c + 1) >> log_c;   // (2^20 windows at most)
   const bool valid = token < (int64_t)P.vocab;
   float given = 0.f;   // the token's logit, under way while the row is read
   if (c == 0 && warp == 0 && valid) given = element<F32>(W.row + token * Windows<F32>::kSize);
@@ -572,25 +593,10 @@ __global__ void __launch_bounds__(TH, (TOP || TH == 128 ? 1024 : 1536) / TH) k_s
     if (c == 0) {
       j = lane < C ? *cluster.map_shared_rank(&whole, lane) : nothing();
       j.join_warp();
-      if (TOP) {   // each of their keys goes to the place that the number of greater ones is
-        // (a list a warp: clusters have blocks of 256 threads)
-        if (warp < C) T.lists[warp][lane] = cluster.map_shared_rank(&T.lists[TH / 32][0], warp)[lane];
-        if (warp == 0) T.keys[lane] = 0;
-        __syncthreads();
-        if (warp < C) {
-          const Key mine = T.lists[warp][lane];
-          uint32_t greater = 0;
-          for (uint32_t b = 0; b < C; b++) {   // (the lists are in order)
-            uint32_t n = 0;
-#pragma unroll
-            for (uint32_t step = 16; step; step /= 2) n += T.lists[b][n + step - 1] > mine ? step : 0;
-            greater += n + (T.lists[b][n] > mine);
-          }
-          if (mine && greater < 32) T.keys[greater] = mine;
-        }
-        __syncthreads();
-      }
+      if (TOP)   // (their lists lie sorted; a list a warp: clusters have blocks of 256 threads)
+        join_lists<TH>(warp < C ? cluster.map_shared_rank(&T.lists[TH / 32][0], warp)[lane] : 0, T.lists, warp, lane);
     }
+    cluster.barrier_arrive();   // (the others' memory is read)
   }
   if (c == 0) {
     const float far = j.max * scale;
@@ -633,13 +639,13 @@ __global__ void __launch_bounds__(TH, (TOP || TH == 128 ? 1024 : 1536) / TH) k_s
         P.saved[row] = sv;
       }
       if (TOP && lane < P.top) {
-        const Key k = C > 1 ? T.keys[lane] : T.lists[TH / 32][lane];
+        const Key k = T.lists[C > 1 ? 0 : TH / 32][lane];
         P.top_logprobs[(uint64_t)row * P.top + lane] = log_p(value_of((uint32_t)(k >> 32)));
         P.top_tokens[(uint64_t)row * P.top + lane] = (int32_t)place_of(k);
       }
     }
   }
-  if (C > 1) cluster.sync();   // (the others' memory is read until here)
+  if (C > 1) cluster.barrier_wait();
 }
 
 // ----------------------------------------------------------------------------- backward pass

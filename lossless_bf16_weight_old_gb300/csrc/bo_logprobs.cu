@@ -504,7 +504,9 @@ __global__ void __launch_bounds__(TH, (TOP || TH == 128 ? 1024 : 1536) / TH) k_s
   extern __shared__ float dynamic[];
   Max<F32>* const maxima = reinterpret_cast<Max<F32>*>(dynamic);
   __shared__ TopSearch<TH> tops[1];
-  __shared__ Joined parts[(TH / 32)], whole;
+  constexpr uint32_t kBlocks = TH == 256 ? 1u << kMaxLogCluster : 1;   // of a cluster (of blocks of 256 threads)
+  __shared__ Joined parts[TH / 32], sums[kBlocks];
+  __shared__ Key keys[TOP ? kBlocks : 1][32];
   TopSearch<TH>& T = tops[0];
   after_previous();
   const cg::cluster_group cluster = cg::this_cluster();
@@ -512,6 +514,7 @@ __global__ void __launch_bounds__(TH, (TOP || TH == 128 ? 1024 : 1536) / TH) k_s
   const uint32_t row = blockIdx.x >> log_c, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const Windows<F32> W(P.x + row * P.ld, P.vocab);
   const uint32_t begin = W.count * c >> log_c, end = W.count * (c + 1) >> log_c;   // (2^20 windows at most)
+  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");   // (before another block's memory is written)
   // (few rows: the L2 may as well have the block's part on its way while the token is looked up)
   if (C > 1 && threadIdx.x == 0) ahead(W, begin, end);
   const uint8_t* at = P.tokens + row * P.token_stride;
@@ -519,6 +522,7 @@ __global__ void __launch_bounds__(TH, (TOP || TH == 128 ? 1024 : 1536) / TH) k_s
                                            : *reinterpret_cast<const int32_t*>(at);
   const float temp = P.temps ? P.temps[row * P.temp_stride] : P.temp;
   if (token < 0) {   // (the whole cluster)
+    if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (c == 0) {
       if (threadIdx.x == 0) {
         P.logprobs[row] = 0.f;
@@ -587,16 +591,16 @@ __global__ void __launch_bounds__(TH, (TOP || TH == 128 ? 1024 : 1536) / TH) k_s
   // (every warp has the block's sums, and of the first block the cluster's)
   j = lane < TH / 32 ? parts[lane] : nothing();
   j.join_warp();
-  if (C > 1) {
-    if (threadIdx.x == 0) whole = j;
+  if (C > 1) {   // each block leaves its sums and its list with the first one
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (threadIdx.x == 0) *cluster.map_shared_rank(&sums[kBlocks > 1 ? c : 0], 0) = j;
+    if (TOP && warp == 0) cluster.map_shared_rank(&keys[kBlocks > 1 ? c : 0][0], 0)[lane] = T.lists[TH / 32][lane];
     cluster.sync();
     if (c == 0) {
-      j = lane < C ? *cluster.map_shared_rank(&whole, lane) : nothing();
+      j = lane < C ? sums[lane] : nothing();
       j.join_warp();
-      if (TOP)   // (their lists lie sorted; a list a warp: clusters have blocks of 256 threads)
-        join_lists<TH>(warp < C ? cluster.map_shared_rank(&T.lists[TH / 32][0], warp)[lane] : 0, T.lists, warp, lane);
+      if (TOP) join_lists<TH>(warp < C ? keys[warp][lane] : 0, T.lists, warp, lane);
     }
-    cluster.barrier_arrive();   // (the others' memory is read)
   }
   if (c == 0) {
     const float far = j.max * scale;
@@ -645,7 +649,6 @@ __global__ void __launch_bounds__(TH, (TOP || TH == 128 ? 1024 : 1536) / TH) k_s
       }
     }
   }
-  if (C > 1) cluster.barrier_wait();
 }
 
 // ----------------------------------------------------------------------------- backward pass

@@ -436,8 +436,10 @@ __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, 
   const uint32_t floor = T.values[0][top - 1];
   uint32_t nw = 0;
   if (__any_sync(0xffffffffu, best_order >= floor && best_order > 0)) {
+    const float least = value_of(floor);   // (NaN, which is only NaN's floor: then all are listed)
+#pragma unroll 4
     for (uint32_t w = w0 + threadIdx.x; w - lane < w1; w += TH) {
-      const bool in = w < w1 && order_of(max_value(maxima[w - w0])) >= floor;
+      const bool in = w < w1 && !(max_value(maxima[min(w, w1 - 1) - w0]) < least);
       const uint32_t who = __ballot_sync(0xffffffffu, in);
       const uint32_t at = nw + __popc(who & ((1u << lane) - 1));
       if (in && at < kWarpWindows) T.windows[warp][at] = w;

@@ -413,7 +413,7 @@ __device__ __noinline__ void segment_top_of_alike(const Windows<F32>& W, uint32_
 // At least `top` elements are as great as the one of these that is the top-th of all threads' (the floor),
 // so lesser ones do not count.  Each warp lists its windows with such elements, then their elements, and
 // each of those goes to the place that the number of greater ones is.  (A floor from each warp by itself
-// takes fewer steps and lets through so many more that one row takes 9.3 us instead of 8.0.)
+// takes fewer steps and lets so many more through that one row took 1.3 us longer.)
 template <uint32_t TH, bool F32>
 __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top, float best,
                                             const Max<F32>* maxima, TopSearch<TH>& T) {
@@ -493,14 +493,14 @@ __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, 
 // The blocks of a cluster share a row: each takes its part of the windows, and the first one joins
 // their sums and lists.
 //
-// 8192 rows of 151936 BF16 logits with entropy take 359 us, 6.9 TB/s, at 4 instructions a logit (half of
+// 8192 rows of 151936 BF16 logits with entropy take 354 us, 7.0 TB/s, at 4 instructions a logit (half of
 // what the SMs issue).  Fetching windows ahead gains nothing, as other blocks read while one waits: by the
 // L2 388 us against 365, into registers (and so with fewer blocks) 1639 rows of 32000 in 22.8 us against
 // 21.8.  Those rows' 105 MB, at 4.6 TB/s, are as much as a launch of 23 us reads: PyTorch's maximum over as
 // many bytes takes 25.
-// The search for top tokens adds to each row some 2 us in which its block reads little: 4000 rows of
-// 32000 take 46 us without, 68 with 20.  One row of 151936 with 20 takes 8.1 us: launch, token, logits,
-// search, the cluster's meeting and the results are trips one after the other.
+// The search for top tokens adds to each row some 2.5 us in which its block reads little: 4000 rows of
+// 32000 take 46 us without, 64 with 20.  One row of 151936 with 20 takes 7.2 us (4.2 without): launch,
+// token, logits, search, the cluster's meeting and the results are trips one after the other.
 template <uint32_t TH, bool F32, bool ENT, bool TOP>
 __global__ void __launch_bounds__(TH, (TOP || TH == 128 ? 1024 : 1536) / TH) k_score(const ScoreArgs P) {
   extern __shared__ float dynamic[];
@@ -888,10 +888,10 @@ int bo_logprobs_forward(const bo_logprobs* h, const void* d_logits, uint32_t dty
   P.top_tokens = h->d_top_tokens;
   P.saved = static_cast<Saved*>(h->d_saved);
   // Where rows are fewer than SMs, several blocks share one: up to eight, with a window a thread at least
-  // (64 rows of 151936: four blocks 6.7 us, one 20).  From there on the largest blocks that the SMs
-  // hold at once (300 rows of 151936: 512 threads 18.8 us, 256 22.8, 128 33), and where no size
+  // (64 rows of 151936: four blocks 6.4 us, one 20).  From there on the largest blocks that the SMs
+  // hold at once (300 rows of 151936: 512 threads 18.2 us, 256 22.8, 128 33), and where no size
   // does, the smallest (1000 rows: 50 us, with 256 53 to 67).  Rows of up to 2048 windows (65536 BF16 logits)
-  // are too short for 512 (300 rows of 32000: 5.6 us, with 256 5.0).
+  // are too short for 512 (300 rows of 32000: 5.6 us, with 256 4.9).
   const uint64_t windows = (uint64_t)h->vocab * size / kWindow;
   while (P.log_cluster < kMaxLogCluster && (uint64_t)rows << P.log_cluster < (uint64_t)sms * 3 / 2 &&
          windows >> P.log_cluster >= 2 * 256)

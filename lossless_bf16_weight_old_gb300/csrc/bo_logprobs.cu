@@ -168,11 +168,12 @@ struct Windows {
   }
 };
 
-// has the L2 fetch whole windows of [begin, end)
+// has the L2 fetch whole windows of [begin, end), 256 KB of them at most
 template <bool F32>
 __device__ __forceinline__ void ahead(const Windows<F32>& W, uint32_t begin, uint32_t end) {
   if (begin < end && !W.whole(begin)) begin++;
   if (begin < end && !W.whole(end - 1)) end--;
+  end = min(end, begin + 4096);
   if (begin < end)
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(W.base + (uint64_t)begin * kWindow),
                  "r"((end - begin) * kWindow)
@@ -371,13 +372,14 @@ __device__ __forceinline__ float max_value(float m) { return m; }
 __device__ __forceinline__ float max_value(uint16_t m) { return __uint_as_float((uint32_t)m << 16); }
 
 // Shared memory of the search for top tokens.
-constexpr uint32_t kWarpWindows = 32;   // that a warp lists at most
 template <uint32_t TH>
 struct TopSearch {
+  static constexpr uint32_t kKeys = TH < 128 ? 128 : TH;          // that are sorted by their places at most
+  static constexpr uint32_t kWindows = TH < 128 ? 4096 / TH : 32; // that a warp lists at most
   Key lists[TH / 32 + 1][32];     // the last one: of the segments so far
   uint32_t values[TH / 32][32];
-  uint32_t windows[TH / 32][kWarpWindows];
-  Key keys[TH];
+  uint32_t windows[TH / 32][kWindows];
+  Key keys[kKeys];
   uint32_t nkeys;
 };
 // Of a segment of windows [w0, w1) with their maxima in maxima[], its 32 greatest elements in T.lists[0],
@@ -417,6 +419,7 @@ __device__ __noinline__ void segment_top_of_alike(const Windows<F32>& W, uint32_
 template <uint32_t TH, bool F32>
 __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, uint32_t w1, uint32_t top, float best,
                                             const Max<F32>* maxima, TopSearch<TH>& T) {
+  constexpr uint32_t kKeys = TopSearch<TH>::kKeys, kWindows = TopSearch<TH>::kWindows;
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t best_order = threadIdx.x < w1 - w0 ? order_of(best) : 0;
   uint32_t v = sorted(best_order, lane);
@@ -442,12 +445,12 @@ __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, 
       const bool in = w < w1 && !(max_value(maxima[min(w, w1 - 1) - w0]) < least);
       const uint32_t who = __ballot_sync(0xffffffffu, in);
       const uint32_t at = nw + __popc(who & ((1u << lane) - 1));
-      if (in && at < kWarpWindows) T.windows[warp][at] = w;
+      if (in && at < kWindows) T.windows[warp][at] = w;
       nw += __popc(who);
     }
     __syncwarp();
     constexpr uint32_t kAtOnce = 8;   // windows that are read at once
-    const uint32_t listed = min(nw, kWarpWindows);
+    const uint32_t listed = min(nw, kWindows);
     for (uint32_t i0 = 0; i0 < listed; i0 += kAtOnce) {
       float x[kAtOnce];
 #pragma unroll
@@ -466,17 +469,17 @@ __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, 
 #pragma unroll
         for (uint32_t j = 0; j < kAtOnce; j++)
           if (k[j]) {
-            if (at < TH) T.keys[at] = k[j];
+            if (at < kKeys) T.keys[at] = k[j];
             at++;
           }
       }
     }
   }
-  const bool fits = __syncthreads_and(nw <= kWarpWindows);
+  const bool fits = __syncthreads_and(nw <= kWindows);
   const uint32_t n = T.nkeys;
-  if (fits && n <= TH) {
-    if (threadIdx.x < n) {
-      const Key k = T.keys[threadIdx.x];
+  if (fits && n <= kKeys) {
+    for (uint32_t j = threadIdx.x; j < n; j += TH) {
+      const Key k = T.keys[j];
       uint32_t greater = 0;
 #pragma unroll 8
       for (uint32_t i = 0; i < n; i++) greater += T.keys[i] > k;
@@ -502,7 +505,7 @@ __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, 
 // 32000 take 46 us without, 64 with 20.  One row of 151936 with 20 takes 7.2 us (4.2 without): launch,
 // token, logits, search, the cluster's meeting and the results are trips one after the other.
 template <uint32_t TH, bool F32, bool ENT, bool TOP>
-__global__ void __launch_bounds__(TH, (TOP || TH == 128 ? 1024 : 1536) / TH) k_score(const ScoreArgs P) {
+__global__ void __launch_bounds__(TH, (TOP || TH <= 128 ? 1024 : 1536) / TH) k_score(const ScoreArgs P) {
   extern __shared__ float dynamic[];
   Max<F32>* const maxima = reinterpret_cast<Max<F32>*>(dynamic);
   __shared__ TopSearch<TH> tops[1];
@@ -889,23 +892,33 @@ int bo_logprobs_forward(const bo_logprobs* h, const void* d_logits, uint32_t dty
   P.saved = static_cast<Saved*>(h->d_saved);
   // Where rows are fewer than SMs, several blocks share one: up to eight, with a window a thread at least
   // (64 rows of 151936: four blocks 6.4 us, one 20).  From there on the largest blocks that the SMs
-  // hold at once (300 rows of 151936: 512 threads 18.2 us, 256 22.8, 128 33), and where no size
-  // does, the smallest (1000 rows: 50 us, with 256 53 to 67).  Rows of up to 2048 windows (65536 BF16 logits)
-  // are too short for 512 (300 rows of 32000: 5.6 us, with 256 4.9).
+  // hold at once (300 rows of 151936: 512 threads 18.2 us, 256 22.8, 128 33; 1500 rows of 32000: 64
+  // threads 19.4, 128 22.2).  Rows of up to 2048 windows (65536 BF16 logits) are too short for 512 (300 rows of
+  // 32000: 5.6 us, with 256 4.9), and where there are more rows than that, 256 windows and fewer take 32
+  // threads (20000 rows of 8000: 57.7 us, with 64 61.5, with 128 70.8), longer ones 64 (20000 rows of 32000:
+  // 193 us, with 128 195), the longest 128 (8192 rows of 151936: 354 us, with 64 380).  With top tokens, whose
+  // search takes shared memory, 128 begin at 1024 windows (1125 rows of 2001: 30 us, with 64 37).
   const uint64_t windows = (uint64_t)h->vocab * size / kWindow;
   while (P.log_cluster < kMaxLogCluster && (uint64_t)rows << P.log_cluster < (uint64_t)sms * 3 / 2 &&
          windows >> P.log_cluster >= 2 * 256)
     P.log_cluster++;
-  const uint32_t held = sms * (h->top ? 1024 : 1536);   // threads at once
-  const uint32_t threads = P.log_cluster > 0                                        ? 256
-                           : (uint64_t)rows * 512 <= held && windows > 2048 ? 512
-                           : (uint64_t)rows * 256 <= held                   ? 256
-                                                                            : 128;
+  const uint64_t held = (uint64_t)sms * (h->top ? 1024 : 1536), held_small = (uint64_t)sms * 1024;   // threads at once
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool f32 = dtype == BO_FP32;
-  return check(threads == 512   ? (f32 ? score<512, true>(P, s) : score<512, false>(P, s))
-               : threads == 256 ? (f32 ? score<256, true>(P, s) : score<256, false>(P, s))
-                                : (f32 ? score<128, true>(P, s) : score<128, false>(P, s)));
+  cudaError_t e;
+  if (P.log_cluster == 0 && (uint64_t)rows * 512 <= held && windows > 2048)
+    e = f32 ? score<512, true>(P, s) : score<512, false>(P, s);
+  else if (P.log_cluster > 0 || (uint64_t)rows * 256 <= held)
+    e = f32 ? score<256, true>(P, s) : score<256, false>(P, s);
+  else if ((uint64_t)rows * 128 <= held_small)
+    e = f32 ? score<128, true>(P, s) : score<128, false>(P, s);
+  else if (windows <= 256)
+    e = f32 ? score<32, true>(P, s) : score<32, false>(P, s);
+  else if (windows <= (h->top ? 1024 : 2048) || (!h->top && (uint64_t)rows * 64 <= held_small))
+    e = f32 ? score<64, true>(P, s) : score<64, false>(P, s);
+  else
+    e = f32 ? score<128, true>(P, s) : score<128, false>(P, s);
+  return check(e);
 }
 
 int bo_logprobs_backward(const bo_logprobs* h, const void* d_logits, uint32_t dtype, uint64_t ld,

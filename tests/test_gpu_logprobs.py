@@ -114,6 +114,8 @@ CASES = [  # rows, vocab, dtype, ld, offset, top, entropy
     (70, 151936, BF16, None, 0, 1, False), (5, 151937, FP32, 151940, 1, 32, True),
     (240, 140001, BF16, 140004, 3, 0, True), (240, 140001, BF16, None, 0, 20, True), (250, 70001, FP32, None, 1, 0, False),
     (250, 70001, FP32, None, 0, 20, True), (130, 32000, FP32, None, 0, 5, True), (180, 151936, BF16, None, 0, 0, True),
+    (3000, 1000, BF16, None, 0, 5, True), (3000, 777, FP32, 779, 1, 32, True), (5000, 4099, FP32, None, 0, 0, True),
+    (1300, 32001, BF16, None, 0, 20, True), (1300, 16001, FP32, None, 0, 32, True), (2500, 60001, BF16, None, 1, 0, True),
     (2, 600001, BF16, None, 0, 32, True), (700, 300001, BF16, None, 0, 3, True), (650, 140001, FP32, None, 0, 3, True),
 ]
 
@@ -267,7 +269,7 @@ def test_values_that_are_not_finite_and_tokens_that_do_not_exist(dtype, vocab):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
-@pytest.mark.parametrize("rows,vocab", [(3, 64), (2, 5001), (1, 151936), (700, 33333), (2, 524288)])
+@pytest.mark.parametrize("rows,vocab", [(3, 64), (2, 5001), (1, 151936), (700, 33333), (2, 524288), (1300, 3000), (1300, 20000)])
 def test_top_tokens_of_equal_values(dtype, rows, vocab):
     """Constant rows, few distinct values, zeros of both signs, ascending and descending rows."""
     for kind in range(5):
@@ -301,7 +303,7 @@ def test_large_values(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
-@pytest.mark.parametrize("rows,vocab", [(3, 50000), (240, 140000), (1000, 3001)])
+@pytest.mark.parametrize("rows,vocab", [(3, 50000), (240, 140000), (1000, 3001), (3000, 3001), (1300, 20001)])
 @pytest.mark.parametrize("heat", [1e-7, 1e6])
 def test_far_from_ordinary_temperatures(dtype, rows, vocab, heat):
     """So cold that a row's shift passes its bound, and so hot that all tokens are alike."""

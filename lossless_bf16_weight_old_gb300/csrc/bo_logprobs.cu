@@ -502,7 +502,7 @@ __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, 
 // 21.8.  Those rows' 105 MB, at 4.6 TB/s, are as much as a launch of 23 us reads: PyTorch's maximum over as
 // many bytes takes 25.
 // The search for top tokens adds to each row some 2.5 us in which its block reads little: 4000 rows of
-// 32000 take 46 us without, 64 with 20.  One row of 151936 with 20 takes 7.2 us (4.2 without): launch,
+// 32000 take 45 us without, 61 with 20.  One row of 151936 with 20 takes 7.2 us (4.2 without): launch,
 // token, logits, search, the cluster's meeting and the results are trips one after the other.
 template <uint32_t TH, bool F32, bool ENT, bool TOP>
 __global__ void __launch_bounds__(TH, (TOP || TH <= 128 ? 1024 : 1536) / TH) k_score(const ScoreArgs P) {

@@ -19,6 +19,7 @@ stay allocated until the work is done.
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import Sequence
 
 import torch
@@ -527,6 +528,9 @@ def _device_of(device) -> torch.device:
     return dev
 
 
+_TOKENS, _FLOAT, _MASKS = (torch.int64, torch.int32), (torch.float32,), (torch.bool, torch.uint8)
+
+
 class _Results(_Owner):
     """An object whose one buffer holds the results of its calls."""
 
@@ -545,41 +549,41 @@ class _Results(_Owner):
         return self._at[at:at + numel * dtype.itemsize].view(dtype).view(shape)
 
 
-def _rows_in(t: torch.Tensor, name: str, most: int, width: int, device: torch.device) -> int:
-    """Checks a matrix of at most `most` rows; returns its row stride."""
-    if t.dim() == 2 and t.device == device and t.dtype in _DTYPES and t.shape[1] == width:
-        rows = t.shape[0]
+def _rows_in(t: torch.Tensor, name: str, most: int, width: int, device: torch.device) -> tuple[int, int]:
+    """Checks a matrix of at most `most` rows; returns how many it has, and its row stride."""
+    if t.dim() == 2 and t.dtype in _DTYPES and t.get_device() == device.index:
+        rows, cols = t.shape
         ld, one = t.stride()
-        if rows <= most and (one == 1 or width == 1) and (ld >= width or rows <= 1):
-            return ld if rows > 1 else width
-    if t.dim() != 2 or t.dtype not in _DTYPES or t.device != device:
-        raise ValueError(f"{name} must be a 2-dimensional bfloat16 or float32 tensor on {device}")
-    if t.shape[1] != width or t.shape[0] > most:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (up to {most}, {width})")
-    raise ValueError(f"{name}'s rows must be contiguous and may not overlap")
+        if cols == width and rows <= most and (one == 1 or width == 1) and (ld >= width or rows <= 1):
+            return rows, ld if rows > 1 else width
+        if cols != width or rows > most:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (up to {most}, {width})")
+        raise ValueError(f"{name}'s rows must be contiguous and may not overlap")
+    raise ValueError(f"{name} must be a 2-dimensional bfloat16 or float32 tensor on {device}")
 
 
 def _column(t: torch.Tensor, name: str, rows: int, dtypes, device: torch.device) -> int:
     """Checks a vector of one number a row; returns its stride."""
-    if t.dim() != 1 or t.shape[0] != rows or t.device != device or t.dtype not in dtypes:
+    if t.dim() != 1 or t.numel() != rows or t.get_device() != device.index or t.dtype not in dtypes:
         raise ValueError(f"{name} must be a 1-dimensional tensor of {rows} elements of type "
                          f"{' or '.join(str(d) for d in dtypes)} on {device}")
     return t.stride(0)
 
 
-def _out_for(out: torch.Tensor | None, t: torch.Tensor, ld: int, device: torch.device,
+def _out_for(out: torch.Tensor | None, t: torch.Tensor, rows: int, width: int, ld: int, device: torch.device,
              stream) -> tuple[torch.Tensor, int]:
     """Where the gradient of the logits t goes, and its row stride: `out`, or memory of its own whose
     rows lie as far apart as the logits' (so that they begin alike)."""
-    rows, width = t.shape
     if out is None:
         out = _scratch((rows, ld), t.dtype, device, stream)
         if stream is not None:   # (the caller may go on with it on the current one)
             out.record_stream(torch.cuda.current_stream(device))
         return out[:, :width], ld
-    if out.shape != t.shape or out.dtype != t.dtype:
-        raise ValueError(f"out must have the logits' shape {tuple(t.shape)} and type {t.dtype}")
-    return out, _rows_in(out, "out", rows, width, device)
+    if out.dtype is t.dtype:
+        n, ld = _rows_in(out, "out", rows, width, device)
+        if n == rows:
+            return out, ld
+    raise ValueError(f"out must have the logits' shape {tuple(t.shape)} and type {t.dtype}")
 
 
 def _unrecorded_logits(t: torch.Tensor) -> None:
@@ -638,19 +642,19 @@ class TokenLogprobs(_Results):
         raw = self._on(stream)
         _unrecorded_logits(logits)
         dev = self.device
-        ld = _rows_in(logits, "logits", self.rows, self.vocab, dev)
-        n = logits.shape[0]
-        step = _column(tokens, "tokens", n, (torch.int64, torch.int32), dev)
-        heat, heats, heat_step = 1.0, None, 0
-        if isinstance(temperature, torch.Tensor):
-            heat_step = _column(temperature, "temperature", n, (torch.float32,), dev)
-            heats = temperature.data_ptr() or None
-        else:
-            heat = float(temperature)
-            if not 0.0 < heat < float("inf"):
-                raise ValueError("temperature must be a positive number")
+        n, ld = _rows_in(logits, "logits", self.rows, self.vocab, dev)
+        step = _column(tokens, "tokens", n, _TOKENS, dev)
+        heat, heats, heat_step = temperature, None, 0
+        if type(heat) is not float:   # (which is quicker to ask than whether it is a tensor)
+            if isinstance(temperature, torch.Tensor):
+                heat_step = _column(temperature, "temperature", n, _FLOAT, dev)
+                heat, heats = 1.0, temperature.data_ptr() or None
+            else:
+                heat = float(temperature)
+        if not 0.0 < heat < math.inf:
+            raise ValueError("temperature must be a positive number")
         rc = self._forward(self._ref, logits.data_ptr(), _DTYPES[logits.dtype], ld, n, tokens.data_ptr(),
-                           tokens.element_size(), step, heat, heats, heat_step, raw)
+                           8 if tokens.dtype is torch.int64 else 4, step, heat, heats, heat_step, raw)
         if rc != OK:
             _failed(rc, "bo_logprobs_forward", dev)
         self._ran = n
@@ -664,8 +668,7 @@ class TokenLogprobs(_Results):
         raw = self._on(stream)
         _unrecorded_logits(logits)
         dev = self.device
-        ld = _rows_in(logits, "logits", self._ran, self.vocab, dev)
-        n = logits.shape[0]
+        n, ld = _rows_in(logits, "logits", self._ran, self.vocab, dev)
         if d_logprobs is None and d_entropy is None:
             raise ValueError("d_logprobs or d_entropy must be given")
         if d_entropy is not None and self.entropy is None:
@@ -673,10 +676,10 @@ class TokenLogprobs(_Results):
         g = h = None
         g_step = h_step = 0
         if d_logprobs is not None:
-            g_step, g = _column(d_logprobs, "d_logprobs", n, (torch.float32,), dev), d_logprobs.data_ptr()
+            g_step, g = _column(d_logprobs, "d_logprobs", n, _FLOAT, dev), d_logprobs.data_ptr()
         if d_entropy is not None:
-            h_step, h = _column(d_entropy, "d_entropy", n, (torch.float32,), dev), d_entropy.data_ptr()
-        out, ld_out = _out_for(out, logits, ld, dev, stream)
+            h_step, h = _column(d_entropy, "d_entropy", n, _FLOAT, dev), d_entropy.data_ptr()
+        out, ld_out = _out_for(out, logits, n, self.vocab, ld, dev, stream)
         rc = self._backward(self._ref, logits.data_ptr(), _DTYPES[logits.dtype], ld, n, g, g_step, h, h_step,
                             out.data_ptr(), ld_out, raw)
         if rc != OK:
@@ -735,10 +738,10 @@ class ExpertRouting(_Results):
         raw = self._on(stream)
         _unrecorded_logits(logits)
         dev = self.device
-        ld = _rows_in(logits, "logits", self.tokens, self._width, dev)
-        n, at, step = logits.shape[0], None, 0
+        n, ld = _rows_in(logits, "logits", self.tokens, self._width, dev)
+        at, step = None, 0
         if mask is not None:
-            step, at = _column(mask, "mask", n, (torch.bool, torch.uint8), dev), mask.data_ptr() or None
+            step, at = _column(mask, "mask", n, _MASKS, dev), mask.data_ptr() or None
         rc = self._forward(self._ref, logits.data_ptr(), _DTYPES[logits.dtype], ld, n, at, step, raw)
         if rc != OK:
             _failed(rc, "bo_routing_forward", dev)
@@ -755,24 +758,25 @@ class ExpertRouting(_Results):
         raw = self._on(stream)
         _unrecorded_logits(logits)
         dev = self.device
-        ld = _rows_in(logits, "logits", self._ran, self._width, dev)
-        n = logits.shape[0]
+        n, ld = _rows_in(logits, "logits", self._ran, self._width, dev)
         gw, steps = None, (0, 0)
         if d_weights is not None:
-            if d_weights.shape != (n, self.k) or d_weights.dtype != torch.float32 or d_weights.device != dev:
+            if d_weights.shape != (n, self.k) or d_weights.dtype is not torch.float32 or \
+                    d_weights.get_device() != dev.index:
                 raise ValueError(f"d_weights must be a float32 tensor of shape ({n}, {self.k}) on {dev}")
             gw, steps = d_weights.data_ptr() or None, d_weights.stride()
-        where, rate = None, 0.0
-        if isinstance(d_loss, torch.Tensor):
-            if d_loss.dtype != torch.float32 or d_loss.numel() != 1 or d_loss.device != dev:
-                raise ValueError(f"d_loss must be a number or a float32[1] tensor on {dev}")
-            where = d_loss.data_ptr()
-        else:
-            rate = float(d_loss)
+        where, rate = None, d_loss
+        if type(rate) is not float:
+            if isinstance(d_loss, torch.Tensor):
+                if d_loss.dtype != torch.float32 or d_loss.numel() != 1 or d_loss.device != dev:
+                    raise ValueError(f"d_loss must be a number or a float32[1] tensor on {dev}")
+                where, rate = d_loss.data_ptr(), 0.0
+            else:
+                rate = float(d_loss)
         if counts is not None and (counts.shape != (self._width,) or counts.dtype != torch.int32 or
                                    counts.device != dev or not counts.is_contiguous()):
             raise ValueError(f"counts must be a contiguous int32 tensor of {self._width} elements on {dev}")
-        out, ld_out = _out_for(out, logits, ld, dev, stream)
+        out, ld_out = _out_for(out, logits, n, self._width, ld, dev, stream)
         rc = self._backward(self._ref, logits.data_ptr(), _DTYPES[logits.dtype], ld, n, gw, *steps, rate, where,
                             None if counts is None else counts.data_ptr(), out.data_ptr(), ld_out, raw)
         if rc != OK:

@@ -328,61 +328,62 @@ __device__ __forceinline__ int32_t best_of_16(int32_t* k) {
 }
 
 // ------------------------------------------------------------------- a block's sums and counts
-// In shared memory: counts of each expert, then sums of each warp.  A grid that is one cluster joins its
-// blocks' and writes the results; else each block leaves its own for k_route_join.
+// In shared memory: counts of each expert, then sums of each warp, and in a grid that is one cluster, a
+// place for each of its blocks' sums and counts.  There each block leaves its own with the first one, which
+// writes the results; else for k_route_join.
 __device__ __forceinline__ void finish(const RouteArgs& P, const int32_t* counts, float* sums, int32_t* reals,
                                        float* parts) {
-  const uint32_t E = P.experts, threads = blockDim.x, warps = threads / 32;
+  const uint32_t E = P.experts, threads = blockDim.x, warps = threads / 32, C = gridDim.x, c = blockIdx.x;
+  const cg::cluster_group cluster = cg::this_cluster();
+  float* all_sums = sums + warps * E;                                    // C x E, then as many counts
+  int32_t* all_counts = reinterpret_cast<int32_t*>(all_sums + C * E);    // (if P.joined)
+  __shared__ int32_t all_reals[kMaxCluster];
   __syncthreads();
-  for (uint32_t e = threadIdx.x; e < E; e += threads) {   // (the column is this thread's)
+  if (P.joined) {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // (the first block is there)
+    all_sums = cluster.map_shared_rank(all_sums + c * E, 0);
+    all_counts = cluster.map_shared_rank(all_counts + c * E, 0);
+  }
+  for (uint32_t e = threadIdx.x; e < E; e += threads) {
     float s = 0.f;
     for (uint32_t i = 0; i < warps; i++) s += sums[i * E + e];
     if (P.joined) {
-      sums[e] = s;
+      all_sums[e] = s;
+      all_counts[e] = counts[e];
     } else {
-      P.sums[(uint64_t)blockIdx.x * E + e] = s;
-      P.counts[(uint64_t)blockIdx.x * E + e] = counts[e];
+      P.sums[(uint64_t)c * E + e] = s;
+      P.counts[(uint64_t)c * E + e] = counts[e];
     }
   }
   if (threadIdx.x == 0) {
     int32_t n = 0;
     for (uint32_t i = 0; i < warps; i++) n += reals[i];
-    if (P.joined) reals[0] = n;
-    else P.real[blockIdx.x] = n;
+    if (P.joined) *cluster.map_shared_rank(&all_reals[c % kMaxCluster], 0) = n;
+    else P.real[c] = n;
   }
   if (!P.joined) return;
-  const cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
-  if (blockIdx.x == 0) {
-    const uint32_t C = gridDim.x;
-    int32_t N = 0;
-    for (uint32_t b = 0; b < C; b++) N += *cluster.map_shared_rank(reals, b);
-    float share = 0.f;
-    for (uint32_t e = threadIdx.x; e < E; e += threads) {
-      float v[kMaxCluster], s = 0.f;
-      int32_t m[kMaxCluster], n = 0;
-#pragma unroll
-      for (uint32_t b = 0; b < kMaxCluster; b++) {
-        v[b] = b < C ? cluster.map_shared_rank(sums, b)[e] : 0.f;
-        m[b] = b < C ? cluster.map_shared_rank(counts, b)[e] : 0;
-      }
-#pragma unroll
-      for (uint32_t b = 0; b < kMaxCluster; b++) s += v[b], n += m[b];
-      const float p = N > 0 ? s / (float)N : 0.f;
-      P.out_probs[e] = p;
-      P.out_counts[e] = n;
-      share += p * (float)n;
-    }
-    share = warp_sum(share);
-    if (threadIdx.x % 32 == 0) parts[threadIdx.x / 32] = share;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (uint32_t i = 1; i < warps; i++) share += parts[i];
-      *P.out_loss = N > 0 ? share / (float)N * ((float)E / (float)P.k) : 0.f;
-      *P.out_real = N;
-    }
+  if (c != 0) return;
+  int32_t N = 0;
+  for (uint32_t b = 0; b < C; b++) N += all_reals[b];
+  float share = 0.f;
+  for (uint32_t e = threadIdx.x; e < E; e += threads) {
+    float s = 0.f;
+    int32_t n = 0;
+    for (uint32_t b = 0; b < C; b++) s += all_sums[b * E + e], n += all_counts[b * E + e];
+    const float p = N > 0 ? s / (float)N : 0.f;
+    P.out_probs[e] = p;
+    P.out_counts[e] = n;
+    share += p * (float)n;
   }
-  cluster.sync();   // (the others' memory is read until here)
+  share = warp_sum(share);
+  if (threadIdx.x % 32 == 0) parts[threadIdx.x / 32] = share;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 1; i < warps; i++) share += parts[i];
+    *P.out_loss = N > 0 ? share / (float)N * ((float)E / (float)P.k) : 0.f;
+    *P.out_real = N;
+  }
 }
 
 // Joins the blocks' sums and counts.  Each block of the one cluster takes a part of the experts; its
@@ -392,9 +393,10 @@ __device__ __forceinline__ void finish(const RouteArgs& P, const int32_t* counts
 __global__ void __launch_bounds__(kJoinThreads) k_route_join(const RouteArgs P, uint32_t blocks) {
   __shared__ float sums[2 * kJoinThreads];
   __shared__ int32_t counts[2 * kJoinThreads];
-  __shared__ float parts[kJoinThreads / 32], shares[1];
+  __shared__ float parts[kJoinThreads / 32], shares[kMaxCluster];
   __shared__ int32_t reals[kJoinThreads / 32];
   after_previous();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;");   // (before another block's memory is written)
   const cg::cluster_group cluster = cg::this_cluster();
   const uint32_t E = P.experts, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t C = gridDim.x, width = (E + C - 1) / C, first = blockIdx.x * width;
@@ -433,17 +435,18 @@ __global__ void __launch_bounds__(kJoinThreads) k_route_join(const RouteArgs P, 
   }
   if (lane == 0) parts[warp] = share;
   __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (warp == 0) {
     share = warp_sum(parts[lane]);
-    shares[0] = share;
+    if (lane == 0) *cluster.map_shared_rank(&shares[blockIdx.x], 0) = share;
   }
   cluster.sync();
   if (blockIdx.x == 0 && threadIdx.x == 0) {
-    for (uint32_t b = 1; b < C; b++) share += *cluster.map_shared_rank(shares, b);
+    share = shares[0];
+    for (uint32_t b = 1; b < C; b++) share += shares[b];
     *P.out_loss = N > 0 ? share / (float)N * ((float)E / (float)P.k) : 0.f;
     *P.out_real = N;
   }
-  cluster.sync();   // (the others' memory is read until here)
 }
 
 // ------------------------------------------------------------------------------ forward pass
@@ -461,6 +464,7 @@ __global__ void __launch_bounds__(kThreads) k_route(const RouteArgs P) {
   typedef Keys<F32> K;
   typedef typename K::T Key;
   after_previous();
+  if (P.joined) asm volatile("barrier.cluster.arrive.relaxed.aligned;");   // (waited for in `finish`)
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = P.experts;
   for (uint32_t e = threadIdx.x; e < E; e += kThreads) counts[e] = 0;
   __syncthreads();
@@ -908,7 +912,7 @@ int route(RouteArgs& P, uint32_t sms, cudaStream_t s) {
   if (P.tokens <= kMaxCluster * kWarps * 2) {   // one launch
     const uint32_t grid = P.tokens <= kWarps ? 1 : P.tokens <= 2 * kWarps ? 2 : P.tokens <= 4 * kWarps ? 4 : kMaxCluster;
     P.joined = 1;
-    return check(launch(one, dim3(grid), kThreads, smem, grid, s, P));
+    return check(launch(one, dim3(grid), kThreads, smem + grid * P.experts * 8, grid, s, P));
   }
   P.joined = 0;
   const uint32_t lanes = power_of_two((P.experts + kLane - 1) / kLane);

@@ -452,8 +452,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_route_join(const RouteArgs P, 
 // ------------------------------------------------------------------------------ forward pass
 // One warp a token, for few tokens, or more experts or choices than k_route_many takes: lane l holds
 // experts l, l + 32, ...; a choice is a maximum over the warp, which the hardware finds in one
-// instruction (FP32 keys: two).  64 tokens of 128 experts take 3.9 us, launch to end, in one cluster of
-// eight blocks that also writes the counts and the loss; 2000 tokens 7.5 us, 3.5 of them k_route_join.
+// instruction (FP32 keys: two).  64 tokens of 128 experts take 3.4 us, launch to end, in one cluster of
+// eight blocks that also writes the counts and the loss; 2000 tokens 6.8 us, 3 of them k_route_join.
 template <bool F32, int NV>
 __global__ void __launch_bounds__(kThreads) k_route(const RouteArgs P) {
   extern __shared__ uint32_t sh[];
@@ -893,7 +893,7 @@ bool whole(const void* p, uint64_t ld, uint32_t width, uint32_t each) {   // (ld
 template <bool F32, int KL>
 int route_many(const RouteArgs& P, uint32_t grid, cudaStream_t s) {
   // Of the numbers of warps a block, the one that leaves the fewest without work in the last turn: 262144
-  // tokens are 27 turns of 304 blocks' warps, 3 of 9 (47.8 us) and not 4 of 8 (48.7).
+  // tokens are 27 turns of 304 blocks' warps, 3 of 9 (0.9 us less) and not 4 of 8.
   const uint32_t per = 32 / P.lanes * P.rounds, turns = ((P.tokens + per - 1) / per + grid - 1) / grid;   // of a block with one warp
   uint32_t warps = Many<F32, KL>::kMostWarps, least = ~0u;
   for (uint32_t w = warps; w >= 4; w--) {
@@ -918,7 +918,7 @@ int route(RouteArgs& P, uint32_t sms, cudaStream_t s) {
   const uint32_t lanes = power_of_two((P.experts + kLane - 1) / kLane);
   uint32_t grid;
   int rc;
-  // (Where the two forms meet: 16 experts at 6000 tokens, 8.1 us, 128 at 5000, 9.7 us, 256 at 3000, 11.3 us.)
+  // (Where the two forms meet: 16 experts at 6000 tokens, 128 at 5000, 256 at 3000; 7 to 10 us.)
   if (P.tokens > 6000 && lanes <= 1u << kLevels && P.k <= 16) {
     P.lanes = lanes;
     P.vec = whole(P.x, P.ld, P.experts, kLane);

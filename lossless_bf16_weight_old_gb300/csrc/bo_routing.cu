@@ -240,10 +240,8 @@ struct Short {
     if (F32) {
 #pragma unroll
       for (int i = 0; i < (int)kLane; i++) {
-        const float v = __uint_as_float(x.w[i]);
-        int32_t s = __float_as_int(v + 0.f);
-        s = v != v ? 0x7FFFFFFF : s ^ (int32_t)((uint32_t)(s >> 31) >> 1);
-        k[i] = (s & ~0xFF) | (15 - i);
+        const int32_t s = __float_as_int(__fadd_rn(__uint_as_float(x.w[i]), 0.f));   // one zero, one NaN
+        k[i] = ((s ^ ((s >> 31) & 0x7FFFFFFF)) & ~0xFF) | (15 - i);
       }
     } else {
 #pragma unroll

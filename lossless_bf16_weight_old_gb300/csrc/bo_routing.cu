@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kThreads) k_route(const RouteArgs P) {
 // fewer rounds, where there are too few tokens for all warps, lanes that no round brought together join
 // their lists twice, once in each.
 //
-// The ALU pipe bounds it (71% of its rate; 1000000 tokens of 128 experts in 144 us): 60 of a token's 105
+// The ALU pipe bounds it (73% of its rate; 1000000 tokens of 128 experts in 144 us): 62 of a token's 105
 // instructions are minima, maxima, selections and permutations, 34 of them the sorting networks'.  HBM
 // is at a third.  A third block an SM does not help (51 us for 262144 tokens, with two 50).
 template <bool F32, int KL>

@@ -438,15 +438,24 @@ __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, 
   }
   const uint32_t floor = T.values[0][top - 1];
   uint32_t nw = 0;
-  if (__any_sync(0xffffffffu, best_order >= floor && best_order > 0)) {
+  const uint32_t threads = __ballot_sync(0xffffffffu, best_order >= floor && best_order > 0);
+  if (threads) {
     const float least = value_of(floor);   // (NaN, which is only NaN's floor: then all are listed)
-#pragma unroll 4
-    for (uint32_t w = w0 + threadIdx.x; w - lane < w1; w += TH) {
+    auto look = [&](uint32_t w) {
       const bool in = w < w1 && !(max_value(maxima[min(w, w1 - 1) - w0]) < least);
       const uint32_t who = __ballot_sync(0xffffffffu, in);
       const uint32_t at = nw + __popc(who & ((1u << lane) - 1));
       if (in && at < kWindows) T.windows[warp][at] = w;
       nw += __popc(who);
+    };
+    // a step for each of the threads' windows, or for each such thread (1000 rows of 151936, top 5: 58 and 54
+    // us; one row, top 20: 7.1 and 7.9)
+    if (2 * __popc(threads) >= (w1 - w0) / TH) {
+#pragma unroll 4
+      for (uint32_t w = w0 + threadIdx.x; w - lane < w1; w += TH) look(w);
+    } else {
+      for (uint32_t left = threads; left; left &= left - 1)
+        for (uint32_t first = w0 + warp * 32 + __ffs(left) - 1; first < w1; first += 32 * TH) look(first + lane * TH);
     }
     __syncwarp();
     constexpr uint32_t kAtOnce = 8;   // windows that are read at once

@@ -906,7 +906,7 @@ int bo_logprobs_forward(const bo_logprobs* h, const void* d_logits, uint32_t dty
   // 32000: 5.6 us, with 256 4.9), and where there are more rows than that, 256 windows and fewer take 32
   // threads (20000 rows of 8000: 57.7 us, with 64 61.5, with 128 70.8), longer ones 64 (20000 rows of 32000:
   // 193 us, with 128 195), the longest 128 (8192 rows of 151936: 354 us, with 64 380).  With top tokens, whose
-  // search takes shared memory, 128 begin at 1024 windows (1125 rows of 2001: 30 us, with 64 37).
+  // search takes shared memory, 128 begin at 1024 windows (1125 rows of 2001: 29 us, with 64 36).
   const uint64_t windows = (uint64_t)h->vocab * size / kWindow;
   while (P.log_cluster < kMaxLogCluster && (uint64_t)rows << P.log_cluster < (uint64_t)sms * 3 / 2 &&
          windows >> P.log_cluster >= 2 * 256)

@@ -402,6 +402,29 @@ def test_offsets_past_32_bits():
     assert x0.shape == dx[at].shape and not dx[1:14200].any() and not dx[14201:-1].any()
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_the_largest_vocabulary(dtype):
+    rows, vocab = 2, 1 << 24
+    x, tokens = _logits(rows, vocab, dtype)
+    x[1, -1], tokens[1] = 30.0, vocab - 1
+    lp = bd.TokenLogprobs(rows, vocab, top=32, entropy=True)
+    lp.run(x, tokens)
+    g, h = torch.randn(rows, device="cuda"), torch.randn(rows, device="cuda")
+    dx = lp.backward(x, g, h)
+    for i in range(rows):
+        part = _View(lp, i, i + 1)
+        r = _check_forward(part, x[i:i + 1], tokens[i:i + 1], 1.0, 1)
+        _check_grad(dx[i:i + 1], r, tokens[i:i + 1], 1.0, g[i:i + 1], h[i:i + 1], dtype)
+
+
+def test_the_gradient_of_the_first_rows():
+    x, tokens = _logits(50, 3000, BF16)
+    lp = bd.TokenLogprobs(50, 3000, entropy=True)
+    lp.run(x, tokens)
+    g = torch.randn(50, device="cuda")
+    assert torch.equal(lp.backward(x[:20], g[:20], g[:20]), lp.backward(x, g, g)[:20])
+
+
 def test_no_rows():
     lp = bd.TokenLogprobs(4, 10, top=2)
     x = torch.empty(0, 10, dtype=BF16, device="cuda")

@@ -261,6 +261,15 @@ def test_calls_repeat_and_a_token_is_as_by_itself():
     assert torch.equal(a.weights[1:], first[0][1:])
 
 
+def test_the_gradient_of_the_first_tokens():
+    """Their share of the balance loss is that among all of the run's."""
+    x = _logits(300, 64, FP32)
+    a = bd.ExpertRouting(400, 64, 4)
+    a.run(x)
+    gw = torch.randn(300, 4, device="cuda")
+    assert torch.equal(a.backward(x[:77], gw[:77], 3.0), a.backward(x, gw, 3.0)[:77])
+
+
 def test_columns_of_one_buffer():
     both = torch.randn(500, 256, device="cuda").bfloat16()
     x, out = both[:, :128], both[:, 128:]

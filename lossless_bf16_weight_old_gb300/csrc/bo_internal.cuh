@@ -70,6 +70,13 @@ inline int sm_count(int32_t device, int& sms) {
 // may go as soon as the call returns, and the call works during stream capture.
 cudaError_t upload(const void* host, uint64_t bytes, void* dst, cudaStream_t s);
 
+// Shared memory of a block: what the kernel declares itself and what its launch adds are together at most
+// kDefaultSmem, unless the kernel was allowed more, and kMaxSmem then.  The allowance is the kernel's in
+// the whole process, and the last one counts: every launch that may need it asks for all that there is, so
+// that none takes away what a call on another thread is about to use.  Kernels that are launched with more
+// than kDefaultSmem - kOwnSmem declare at most kOwnSmem.
+constexpr uint32_t kDefaultSmem = 48 * 1024, kMaxSmem = 227 * 1024, kOwnSmem = 1024;
+
 // Launches a kernel with programmatic stream serialization: it may be set up while the kernel
 // before it on the stream ends (one row's adapter: 8.1 us a call without, 5.0 us with).  Every
 // kernel launched this way first waits (after_previous) until all work before it is done and
@@ -79,9 +86,9 @@ cudaError_t upload(const void* host, uint64_t bytes, void* dst, cudaStream_t s);
 template <class... P, class... A>
 cudaError_t launch(void (*kernel)(P...), dim3 grid, uint32_t threads, uint32_t smem,
                    uint32_t cluster, cudaStream_t s, const A&... args) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > kDefaultSmem - kOwnSmem) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)std::max(smem, kMaxSmem - kOwnSmem));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

@@ -521,6 +521,8 @@ __global__ void __launch_bounds__(TH, (TOP || TH <= 128 ? 1024 : 1536) / TH) k_s
   constexpr uint32_t kBlocks = TH == 256 ? 1u << kMaxLogCluster : 1;   // of a cluster (of blocks of 256 threads)
   __shared__ Joined parts[TH / 32], sums[kBlocks];
   __shared__ Key keys[TOP ? kBlocks : 1][32];
+  static_assert(sizeof(tops) + sizeof(parts) + sizeof(sums) + sizeof(keys) + kSegment * sizeof(float) <= kDefaultSmem,
+                "no allowance");
   TopSearch<TH>& T = tops[0];
   after_previous();
   const cg::cluster_group cluster = cg::this_cluster();

@@ -186,10 +186,12 @@ __device__ __forceinline__ void ahead(const Windows<F32>& W, uint32_t begin, uin
 // rounding, whose d of the maximum is the rounding of the shift.  That holds while the shift stays between
 // -2^21 and 2^22 (kLeast, kMost): the rows whose maximum does not are read again (careful_sums).  The
 // shift starts below all of them, so that -infinity has e = 0; its d is kept finite, so that e d is 0 and
-// not NaN.
+// not NaN.  The floor that does so has to be far below the maximum at any scale and its product with the
+// scale finite: rows of scales outside kLeastScale (with entropy, which alone has the floor) and kMostScale
+// are read again too.
 constexpr float kLeast = -2097152.f, kMost = 4194304.f;
 constexpr uint32_t kFloorBf16 = 0xF149F149u;   // -1e30, twice
-constexpr float kFloor = -1e30f, kLeastScale = 1e-23f;
+constexpr float kFloor = -1e30f, kLeastScale = 1e-23f, kMostScale = 1e8f;
 
 struct Joined {
   float max, shift, s, t;
@@ -620,7 +622,7 @@ __global__ void __launch_bounds__(TH, (TOP || TH <= 128 ? 1024 : 1536) / TH) k_s
   }
   if (c == 0) {
     const float far = j.max * scale;
-    const bool careful = !(far >= kLeast && far <= kMost) || (ENT && !(scale >= kLeastScale));
+    const bool careful = !(far >= kLeast && far <= kMost && scale <= kMostScale) || (ENT && !(scale >= kLeastScale));
     if (careful) {
       __syncthreads();   // (parts is read)
       j = careful_sums<TH, F32>(W, j.max, scale, parts);
@@ -673,7 +675,7 @@ struct RowGrad {
   float scale, shift, A, B, at;
   bool careful, plain;   // plain: B is 0
   __device__ __forceinline__ RowGrad(const Saved& sv, float g, float h) {
-    const float a = -(g + h * sv.entropy) * sv.inv_t, b = -h * kLn2 * sv.inv_t, inv = 1.f / sv.sum;
+    const float a = -(h == 0.f ? g : g + h * sv.entropy) * sv.inv_t, b = -h * kLn2 * sv.inv_t, inv = 1.f / sv.sum;
     scale = sv.inv_t * kLog2e;
     shift = sv.shift;
     A = inv * (a - b * sv.log2_sum);

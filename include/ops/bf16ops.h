@@ -281,9 +281,8 @@ BD_API int bo_adapter_backward(const bo_adapter_set* set, const bo_adapter_rows*
  *   top: the `top` tokens of greatest x_j in order, of equal ones the lowest first, and their lp_j
  * and, from the gradients g of logprob and h of the entropy,
  *   dx_j = (g ([j = v] - p_j) - h p_j (lp_j + H)) / T
- * computed in FP32 from logits of BF16 or FP32.  Where l = ln sum_i e^(z_i) is at most 128 in size, z and
- * l are rounded to FP32 before their difference is taken, as by whoever keeps l (an error of at most
- * 2^-18); past that the difference is taken before it is rounded.
+ * computed in FP32 from logits of BF16 or FP32, by differences from the row's greatest logit: lp_j =
+ * (x_j - max) / T - ln sum_i e^((x_i - max) / T), whose error does not depend on where the row lies.
  *
  * A row whose token is negative is left out: it is not read, its logprob, entropy and
  * top_logprobs are 0, its top tokens -1 and its gradient 0.  A token of `vocab` or more, and a

@@ -25,14 +25,14 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 
 // What the backward pass takes from the forward one, of each row.
 struct alignas(32) Saved {
-  float shift;      // p_j = 2^(x_j scale - shift) / sum, or, with `careful`, 2^((x_j - shift) scale) / sum
+  float shift;      // p_j = 2^(x_j scale - shift) / sum, or, with `careful`, 2^((x_j - shift) / T log2 e) / sum
   float sum;
   float log2_sum;
   float entropy;
   float inv_t;      // 1 / T; NaN for a row without a valid token or temperature
   int32_t token;    // -1: the gradient is 0
   int32_t careful;
-  int32_t pad;
+  float temp;       // T; NaN as inv_t is
 };
 static_assert(sizeof(Saved) == 32, "one sector");
 
@@ -97,11 +97,21 @@ __device__ __forceinline__ void st32(void* p, const uint32_t (&w)[8]) {
                "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
-// (x - max) / T, also where the difference by itself passes FP32's range
-__device__ __forceinline__ float over_t(float x, float max, float t) {
-  const float d = x - max;
-  return d >= -FLT_MAX || max < 0.f ? d / t : x / t - max / t;
-}
+// (x - max) / T for any of them, as two products: (x - max) 2^n by one fused operation, and with 1 / (T 2^n).
+// The power keeps both in FP32's range: T may be so small that 1 / T is not, or a difference so large that it
+// is not by itself.  (A small T needs none where max is 2^60 or more: there x is max, or so far below it that
+// the product with FP32's greatest number is far enough.)
+struct OverT {
+  float pow, from, inv;
+  __device__ __forceinline__ OverT(float max, float t) {
+    pow = t > 0x1p64f ? 0x1p-64f : t < 0x1p-64f && fabsf(max) < 0x1p60f ? 0x1p64f : 1.f;
+    from = max * pow;
+    inv = 1.f / (t * pow);
+    if (inv > FLT_MAX) inv = FLT_MAX;
+  }
+  __device__ __forceinline__ float far(float x) const { return fmaf(x, pow, -from); }
+  __device__ __forceinline__ float operator()(float x) const { return far(x) * inv; }
+};
 template <bool F32>
 __device__ __forceinline__ float element(const uint8_t* p) {
   return F32 ? *reinterpret_cast<const float*>(p)
@@ -288,17 +298,19 @@ __device__ __forceinline__ void add_window(Sums<ENT>& a, const uint32_t (&lo)[8]
   }
 }
 
-// The sums of a whole row for any values: d = (x - max) scale with the row's own maximum, kept above
-// -200, where e is 0, so that e d is 0 and not NaN.  The maximum is taken as the lowest finite number
-// at least: a row of -infinity has the sum 0.  For a block; every thread of warp 0 has the result.
+// The sums of a whole row for any values and temperatures: d = (x - max) / T log2 e with the row's own maximum
+// (OverT), kept above -200, where e is 0, so that e d is 0 and not NaN.  The maximum is taken as the lowest finite number at least: a row of -infinity has the sum 0.  For a
+// block; every thread of warp 0 has the result.
 template <uint32_t TH, bool F32>
-__device__ __noinline__ Joined careful_sums(const Windows<F32>& W, float max, float scale, Joined* parts) {
+__device__ __noinline__ Joined careful_sums(const Windows<F32>& W, float max, float temp, Joined* parts) {
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   max = fmaxf(max, -FLT_MAX);
+  const OverT by(max, temp);
+  const float scale = by.inv * kLog2e;
   float s = 0.f, t = 0.f;
   for (uint32_t e = threadIdx.x; e < W.vocab; e += TH) {
     const float x = element<F32>(W.row + (uint64_t)e * Windows<F32>::kSize);
-    const float d = max_nan((x - max) * scale, -200.f), p = ex2(d);
+    const float d = max_nan(by.far(x) * scale, -200.f), p = ex2(d);
     s += p;
     t = fmaf(p, d, t);
   }
@@ -559,7 +571,7 @@ __global__ void __launch_bounds__(TH, (TOP || TH <= 128 ? 1024 : 1536) / TH) k_s
     }
     return;
   }
-  const float inv_t = temp > 0.f && temp <= FLT_MAX ? 1.f / temp : __int_as_float(0x7FFFFFFF);
+  const float inv_t = temp > 0.f && temp <= FLT_MAX ? 1.f / temp : __int_as_float(0x7FFFFFFF);   // (infinite below 2^-128)
   const float scale = inv_t * kLog2e;
   const bool valid = token < (int64_t)P.vocab;
   float given = 0.f;   // the token's logit, under way while the row is read
@@ -631,7 +643,7 @@ __global__ void __launch_bounds__(TH, (TOP || TH <= 128 ? 1024 : 1536) / TH) k_s
                          (ENT && !(scale >= kLeastScale));
     if (careful) {
       __syncthreads();   // (parts is read)
-      j = careful_sums<TH, F32>(W, j.max, scale, parts);
+      j = careful_sums<TH, F32>(W, j.max, inv_t == inv_t ? temp : inv_t, parts);
     }
     if (warp == 0) {
       const bool empty = careful && j.s == 0.f;             // nothing but -infinity
@@ -641,10 +653,11 @@ __global__ void __launch_bounds__(TH, (TOP || TH <= 128 ? 1024 : 1536) / TH) k_s
       const float top_d = careful ? 0.f : fmaf(j.max, scale, -j.shift);
       const float log_sum = logf(j.s / (careful ? 1.f : ex2(top_d)));
       // (x - max) / T - ln sum e^((x - max) / T): no part is larger than the result, wherever the row lies.
-      // (By 1 / T, with two roundings for the quotient's one: divided, one row took 7.5 us, so 7.26.)
+      // (Multiplied by 1 / T: divided by T, which is half a step better, one row took 7.5 us, so 7.2.)
       auto log_p = [&](float x) {
-        if (empty) return -inf * inv_t;
-        return min_nan((careful ? over_t(x, j.max, temp) : (x - j.max) * inv_t) - log_sum, 0.f);
+        if (empty) return -inf * inv_t;   // (NaN for a temperature that is none)
+        if (careful) return min_nan(OverT(j.max, inv_t == inv_t ? temp : inv_t)(x) - log_sum, 0.f);
+        return min_nan((x - j.max) * inv_t - log_sum, 0.f);
       };
       if (lane == 0) {
         const float entropy = empty ? 0.f : max_nan(log_sum - kLn2 * (j.t / j.s - top_d), 0.f);
@@ -658,6 +671,7 @@ __global__ void __launch_bounds__(TH, (TOP || TH <= 128 ? 1024 : 1536) / TH) k_s
         sv.inv_t = valid ? inv_t : nan;
         sv.token = empty && valid && inv_t == inv_t ? -1 : (int32_t)(valid ? token : 0);
         sv.careful = careful;
+        sv.temp = valid && inv_t == inv_t ? temp : nan;
         P.saved[row] = sv;
       }
       if (TOP && lane < P.top) {
@@ -675,18 +689,20 @@ struct RowGrad {
   float scale, shift, A, B, at;
   bool careful, plain;   // plain: B is 0
   __device__ __forceinline__ RowGrad(const Saved& sv, float g, float h) {
-    const float a = -(h == 0.f ? g : g + h * sv.entropy) * sv.inv_t, b = -h * kLn2 * sv.inv_t, inv = 1.f / sv.sum;
+    const float unit = sv.careful ? 1.f : sv.inv_t;   // (CarefulGrad divides by T at the end)
+    const float a = -(h == 0.f ? g : g + h * sv.entropy) * unit, b = -h * kLn2 * unit, inv = 1.f / sv.sum;
     scale = sv.inv_t * kLog2e;
     shift = sv.shift;
     A = inv * (a - b * sv.log2_sum);
     B = inv * b;
-    at = g * sv.inv_t;
+    at = g * unit;
     careful = sv.careful;
     plain = h == 0.f;
   }
-  __device__ __forceinline__ float operator()(float x) const {   // any row
-    const float d = max_nan(careful ? (x - shift) * scale : fmaf(x, scale, -shift), -200.f);
-    return ex2(d) * fmaf(B, d, A);
+  // an element, and whether it is the given token, of a row that is not `careful`
+  __device__ __forceinline__ float operator()(float x, bool given) const {
+    const float d = max_nan(fmaf(x, scale, -shift), -200.f);
+    return ex2(d) * fmaf(B, d, A) + (given ? at : 0.f);
   }
   template <bool PLAIN>
   __device__ __forceinline__ float2 two(float2 x) const {        // a row that is not `careful`
@@ -694,6 +710,17 @@ struct RowGrad {
     if (PLAIN) return __fmul2_rn(make_float2(ex2(d.x), ex2(d.y)), make_float2(A, A));
     d = make_float2(max_nan(d.x, -200.f), max_nan(d.y, -200.f));
     return __fmul2_rn(make_float2(ex2(d.x), ex2(d.y)), __ffma2_rn(d, make_float2(B, B), make_float2(A, A)));
+  }
+};
+// The same of a careful row.  1 / T is the last factor, in two products: by the least of T, parts of the sum
+// would be infinite where it is 0.
+struct CarefulGrad {
+  const RowGrad& R;
+  OverT by;
+  __device__ __forceinline__ CarefulGrad(const RowGrad& r, float temp) : R(r), by(r.shift, temp) {}
+  __device__ __forceinline__ float operator()(float x, bool given) const {
+    const float d = max_nan(by.far(x) * (by.inv * kLog2e), -200.f);
+    return (ex2(d) * fmaf(R.B, d, R.A) + (given ? R.at : 0.f)) * by.inv * by.pow;
   }
 };
 template <bool F32, bool PLAIN>
@@ -725,10 +752,9 @@ __global__ void __launch_bounds__(kThreads) k_grad(const GradArgs P) {
   const bool zero = sv.token < 0 || (g == 0.f && h == 0.f);
   const RowGrad R(sv, g, h);
   constexpr uint32_t E = Windows<F32>::kElems, S = Windows<F32>::kSize;
-  auto one = [&](int32_t e) {   // an element by itself
+  auto one = [&](int32_t e, const auto& value) {   // an element by itself
     if (e < 0 || e >= (int32_t)P.vocab) return;
-    float v = 0.f;
-    if (!zero) v = R(element<F32>(W.row + (int64_t)e * S)) + (e == sv.token ? R.at : 0.f);
+    const float v = zero ? 0.f : value(element<F32>(W.row + (int64_t)e * S), e == sv.token);
     if (F32) reinterpret_cast<float*>(out)[e] = v;
     else reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)pack_bf16(v, 0.f);
   };
@@ -737,8 +763,14 @@ __global__ void __launch_bounds__(kThreads) k_grad(const GradArgs P) {
   const int32_t off = (int32_t)W.off * (int32_t)S;
   if ((reinterpret_cast<uintptr_t>(out - off) & 31) != 0 || (R.careful && !zero)) {
     const int32_t first = W.first(piece * kThreads) + (int32_t)threadIdx.x;
+    if (R.careful) {
+      const CarefulGrad careful(R, sv.temp);
 #pragma unroll 4
-    for (uint32_t i = 0; i < E; i++) one(first + (int32_t)(i * kThreads));
+      for (uint32_t i = 0; i < E; i++) one(first + (int32_t)(i * kThreads), careful);
+    } else {
+#pragma unroll 4
+      for (uint32_t i = 0; i < E; i++) one(first + (int32_t)(i * kThreads), R);
+    }
     return;
   }
   const uint32_t w = piece * kThreads + threadIdx.x, last = W.count - 1;
@@ -755,7 +787,7 @@ __global__ void __launch_bounds__(kThreads) k_grad(const GradArgs P) {
       const uint8_t* p = W.base + (uint64_t)w * kWindow;
       ld32(lo, p);
       ld32(hi, p + 32);
-      if (v < E) at = R(element<F32>(W.row + (int64_t)sv.token * S)) + R.at;
+      if (v < E) at = R(element<F32>(W.row + (int64_t)sv.token * S), true);
       if (R.plain) grad_words<F32, true>(R, lo), grad_words<F32, true>(R, hi);
       else grad_words<F32, false>(R, lo), grad_words<F32, false>(R, hi);
     }
@@ -769,8 +801,8 @@ __global__ void __launch_bounds__(kThreads) k_grad(const GradArgs P) {
   // the windows that are not whole: a warp each
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (lane < E) {
-    if (warp == 0 && piece == 0 && !W.whole(0)) one(W.first(0) + (int32_t)lane);
-    if (warp == 1 && piece == last / kThreads && last > 0 && !W.whole(last)) one(W.first(last) + (int32_t)lane);
+    if (warp == 0 && piece == 0 && !W.whole(0)) one(W.first(0) + (int32_t)lane, R);
+    if (warp == 1 && piece == last / kThreads && last > 0 && !W.whole(last)) one(W.first(last) + (int32_t)lane, R);
   }
 }
 

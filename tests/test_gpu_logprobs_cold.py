@@ -66,7 +66,7 @@ def _check(lp, x, tokens, heat, has_entropy):
     adds = v / 32 + 36
     tol = U * (8 + 4 * r["D"] + adds)
     far = torch.isinf(r["logprob"])
-    big = r["logprob"].abs() > 3e38                # FP32 has no such number
+    big = r["logprob"].abs() > torch.finfo(FP32).max
     got = lp.logprobs
     assert (got[far | big] == -INF).all()
     some = ~(far | big)
@@ -79,7 +79,7 @@ def _check(lp, x, tokens, heat, has_entropy):
     return r
 
 
-def _check_gradient(dx, r, tokens, heat, g, h, dtype):
+def _check_gradient(dx, r, tokens, heat, g, h, dtype, least=0.0):
     """Where the type has the gradient, and 0 where nothing is to be learned."""
     heats = heat.double()[:, None] if isinstance(heat, torch.Tensor) else heat
     g, h = g.double()[:, None], (torch.zeros_like(g) if h is None else h).double()[:, None]
@@ -93,7 +93,7 @@ def _check_gradient(dx, r, tokens, heat, g, h, dtype):
     assert not dx[(r["p"] == 0) & (one == 0)].any()
     each = (g.abs() + h.abs() * (lp.abs() + entropy + 1)) / heats
     sums = U * (8 + 4 * r["D"] + dx.shape[1] / 32 + 36)[:, None]
-    tol = r["p"] * each * (U * (24 + 8 * r["d"].abs()) + 2 * sums) + 2.0 ** -126 * each
+    tol = r["p"] * each * (U * (24 + 8 * r["d"].abs()) + 2 * sums) + 2.0 ** -126 * each + least / heats
     tol = tol + one * g.abs() / heats * 8 * U + want.abs() * (2.0 ** -8 if dtype == BF16 else 4 * U)
     fine = (each < most / 4).expand_as(dx)
     _near(dx[fine], want[fine], tol[fine], "gradient")

@@ -572,9 +572,10 @@ def _column(t: torch.Tensor, name: str, rows: int, dtypes, device: torch.device)
 
 def _out_for(out: torch.Tensor | None, t: torch.Tensor, rows: int, width: int, ld: int, device: torch.device,
              stream) -> tuple[torch.Tensor, int]:
-    """Where the gradient of the logits t goes, and its row stride: `out`, or memory of its own whose
-    rows lie as far apart as the logits' (so that they begin alike)."""
+    """Where the gradient of the logits t goes, and its row stride: `out`, or memory of its own whose rows are
+    as far apart as the logits', but for whole words of 32 bytes (in which the kernels read and write)."""
     if out is None:
+        ld = width + (ld - width) % (32 // t.dtype.itemsize)
         out = _scratch((rows, ld), t.dtype, device, stream)
         if stream is not None:   # (the caller may go on with it on the current one)
             out.record_stream(torch.cuda.current_stream(device))

@@ -580,6 +580,7 @@ def _out_for(out: torch.Tensor | None, t: torch.Tensor, rows: int, width: int, l
         if stream is not None:   # (the caller may go on with it on the current one)
             out.record_stream(torch.cuda.current_stream(device))
         return out[:, :width], ld
+    _unrecorded_tensor(out, "out")
     if out.dtype is t.dtype:
         n, ld = _rows_in(out, "out", rows, width, device)
         if n == rows:
@@ -591,6 +592,12 @@ def _unrecorded_logits(t: torch.Tensor) -> None:
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError("autograd records these logits, and would miss the call's part: call under "
                          "torch.no_grad() or with detached logits, and backward() for the gradient")
+
+
+def _unrecorded_tensor(t: torch.Tensor, name: str) -> None:
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"autograd records {name}, and would miss the call's part: call under "
+                         "torch.no_grad() or with a detached tensor")
 
 
 class TokenLogprobs(_Results):
@@ -639,7 +646,7 @@ class TokenLogprobs(_Results):
             temperature: float | torch.Tensor = 1.0, stream=None) -> None:
         """Log probabilities of tokens [n] (int32 or int64) under logits [n, vocab] (bfloat16 or
         float32, contiguous rows) divided by the temperature: one positive number, or float32[n].
-        Autograd does not see the call, which refuses logits that it records."""
+        Autograd does not see the call, which refuses logits and temperatures that it records."""
         raw = self._on(stream)
         _unrecorded_logits(logits)
         dev = self.device
@@ -648,6 +655,7 @@ class TokenLogprobs(_Results):
         heat, heats, heat_step = temperature, None, 0
         if type(heat) is not float:   # (which is quicker to ask than whether it is a tensor)
             if isinstance(temperature, torch.Tensor):
+                _unrecorded_tensor(temperature, "the temperature")
                 heat_step = _column(temperature, "temperature", n, _FLOAT, dev)
                 heat, heats = 1.0, temperature.data_ptr() or None
             else:
@@ -665,7 +673,8 @@ class TokenLogprobs(_Results):
                  stream=None) -> torch.Tensor:
         """The gradient of the last run's logits (the same ones, or their first rows) from those of
         its log probabilities and entropies (float32[n], either may be None).  Goes to `out`, which
-        may be the logits themselves, or to memory of its own; returns it."""
+        may be the logits themselves, or to memory of its own; returns it.  Tensors that autograd
+        records are refused: it could not go on through the call."""
         raw = self._on(stream)
         _unrecorded_logits(logits)
         dev = self.device
@@ -677,8 +686,10 @@ class TokenLogprobs(_Results):
         g = h = None
         g_step = h_step = 0
         if d_logprobs is not None:
+            _unrecorded_tensor(d_logprobs, "d_logprobs")
             g_step, g = _column(d_logprobs, "d_logprobs", n, _FLOAT, dev), d_logprobs.data_ptr()
         if d_entropy is not None:
+            _unrecorded_tensor(d_entropy, "d_entropy")
             h_step, h = _column(d_entropy, "d_entropy", n, _FLOAT, dev), d_entropy.data_ptr()
         out, ld_out = _out_for(out, logits, n, self.vocab, ld, dev, stream)
         rc = self._backward(self._ref, logits.data_ptr(), _DTYPES[logits.dtype], ld, n, g, g_step, h, h_step,
@@ -755,7 +766,8 @@ class ExpertRouting(_Results):
         its weights (float32[n, k], or None) and of its balance loss (a number or a float32[1]
         device tensor).  counts (int32[experts]): the experts' counts to take for the balance loss in
         place of the run's, as of several batches together.  Goes to `out`, which may be the logits
-        themselves, or to memory of its own; returns it."""
+        themselves, or to memory of its own; returns it.  Tensors that autograd records are refused: it
+        could not go on through the call."""
         raw = self._on(stream)
         _unrecorded_logits(logits)
         dev = self.device
@@ -765,12 +777,14 @@ class ExpertRouting(_Results):
             if d_weights.shape != (n, self.k) or d_weights.dtype is not torch.float32 or \
                     d_weights.get_device() != dev.index:
                 raise ValueError(f"d_weights must be a float32 tensor of shape ({n}, {self.k}) on {dev}")
+            _unrecorded_tensor(d_weights, "d_weights")
             gw, steps = d_weights.data_ptr() or None, d_weights.stride()
         where, rate = None, d_loss
         if type(rate) is not float:
             if isinstance(d_loss, torch.Tensor):
                 if d_loss.dtype != torch.float32 or d_loss.numel() != 1 or d_loss.device != dev:
                     raise ValueError(f"d_loss must be a number or a float32[1] tensor on {dev}")
+                _unrecorded_tensor(d_loss, "d_loss")
                 where, rate = d_loss.data_ptr(), 0.0
             else:
                 rate = float(d_loss)

@@ -355,7 +355,10 @@ BD_API int bo_logprobs_backward(const bo_logprobs* h, const void* d_logits, uint
  * probability 0, chosen only where fewer than k others are left.  A NaN or +infinity makes the
  * token's weights and gradient NaN, and with them P and L; NaN counts as the greatest.
  *
- * Sums have one order for given sizes, so the same call repeats its results. */
+ * Sums have one order for given sizes, so the same call repeats its results.  A token's experts and
+ * normalized weights do not depend on the call's other tokens; weights that are not normalized are divided
+ * by a sum over all experts, whose order, and so the weights' last bits, may change with the number of
+ * tokens. */
 
 #define BO_ROUTING_MAX_EXPERTS 1024u
 #define BO_ROUTING_MAX_K 32u

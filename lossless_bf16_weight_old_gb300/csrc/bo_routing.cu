@@ -694,7 +694,7 @@ __global__ void __launch_bounds__((Many<F32, KL>::kMostWarps * 32), 2) k_route_m
         s[i] = i < (int)P.k ? w[i] : 0.f;
       }
 #pragma unroll
-      for (int n = KL / 2; n; n /= 2)   // (as warp_sum does: a token's weights are k_route's)
+      for (int n = KL / 2; n; n /= 2)   // (as warp_sum does: a token's normalized weights are k_route's)
 #pragma unroll
         for (int i = 0; i < n; i++) s[i] += s[i + n];
       const float inv = 1.f / (P.normalize ? s[0] : sum_mine);

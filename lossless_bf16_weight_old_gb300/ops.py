@@ -714,7 +714,8 @@ class ExpertRouting(_Results):
     several streams or in graphs that run side by side, want an object each.
 
     Tokens that the mask leaves out have experts -1 and weights and gradients 0, and count
-    nowhere."""
+    nowhere.  A token's experts and normalized weights do not depend on how many others there are; the
+    last bits of weights that are not normalized may."""
 
     def __init__(self, tokens: int, experts: int, k: int, *, normalize: bool = True, device=None,
                  stream=None):

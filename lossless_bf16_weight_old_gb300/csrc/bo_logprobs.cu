@@ -525,13 +525,13 @@ __device__ __forceinline__ void segment_top(const Windows<F32>& W, uint32_t w0, 
 // The blocks of a cluster share a row: each takes its part of the windows, and the first one joins
 // their sums and lists.
 //
-// 8192 rows of 151936 BF16 logits with entropy take 354 us, 7.0 TB/s, at 4 instructions a logit (half of
+// 8192 rows of 151936 BF16 logits with entropy take 354 to 360 us, 7.0 TB/s, at 4 instructions a logit (half of
 // what the SMs issue).  Fetching windows ahead gains nothing, as other blocks read while one waits: by the
 // L2 388 us against 365, into registers (and so with fewer blocks) 1639 rows of 32000 in 22.8 us against
 // 21.8.  Those rows' 105 MB, at 4.6 TB/s, are as much as a launch of 23 us reads: PyTorch's maximum over as
 // many bytes takes 25.
 // The search for top tokens adds to each row some 2.5 us in which its block reads little: 4000 rows of
-// 32000 take 45 us without, 61 with 20.  One row of 151936 with 20 takes 7.2 us (4.2 without): launch,
+// 32000 take 45 us without, 61 with 20.  One row of 151936 with 20 takes 7.2 us (4.8 without): launch,
 // token, logits, search, the cluster's meeting and the results are trips one after the other.
 template <uint32_t TH, bool F32, bool ENT, bool TOP>
 __global__ void __launch_bounds__(TH, (TOP || TH <= 128 ? 1024 : 1536) / TH) k_score(const ScoreArgs P) {

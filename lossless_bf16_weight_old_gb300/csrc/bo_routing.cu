@@ -552,7 +552,7 @@ __device__ __forceinline__ int32_t get(const Lists<F32, KL>& l, uint32_t lane, i
 constexpr uint32_t kLevels = 4;   // 16 lanes a token at most: 256 experts
 template <bool F32, int KL>
 struct Many {
-  static constexpr uint32_t kMostWarps = !F32 && KL <= 8 ? 9 : 8;   // two blocks of them an SM, by registers
+  static constexpr uint32_t kMostWarps = !F32 && KL <= 8 ? 9 : 8;   // two blocks of them an SM (10 would fit: 262144 tokens 47.1 us, with 9 46.7)
   static constexpr uint32_t kWarpBytes = (kLevels + 1) * (uint32_t)sizeof(Lists<F32, KL>);
 };
 
@@ -916,7 +916,9 @@ int route(RouteArgs& P, uint32_t sms, cudaStream_t s) {
   const uint32_t lanes = power_of_two((P.experts + kLane - 1) / kLane);
   uint32_t grid;
   int rc;
-  // (Where the two forms meet: 16 experts at 6000 tokens, 128 at 5000, 256 at 3000; 7 to 10 us.)
+  // One bound for all numbers of experts, near where the two forms meet: 6000 tokens in the first one and 6001
+  // in the second take 7.4 and 7.5 us of 16 experts (FP32 7.3 and 8.2), 9.9 and 9.3 of 128 (12.0 and 10.6), 13.2
+  // and 12.7 of 256 (17.2 and 15.3).  With 256 experts they meet at 3000 already.
   if (P.tokens > 6000 && lanes <= 1u << kLevels && P.k <= 16) {
     P.lanes = lanes;
     P.vec = whole(P.x, P.ld, P.experts, kLane);

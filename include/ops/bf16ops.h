@@ -393,7 +393,8 @@ BD_API int bo_routing_forward(const bo_routing* h, const void* d_logits, uint32_
                               uint64_t mask_stride, void* stream);
 
 /* The logits' gradient for the forward call before it on this handle, over the same logits and no
- * more tokens than it had.  d_grad_weights: the weights' gradients (NULL: 0), with strides in
+ * more tokens than it had, with the experts and counts as they are in its results (a number there that is
+ * no expert's counts as none).  d_grad_weights: the weights' gradients (NULL: 0), with strides in
  * elements of tokens and of choices, which may be 0.  The gradient of L is *d_grad_loss, or
  * grad_loss where that is NULL.  d_counts: n to take in place of the handle's (NULL), as of several
  * batches together; f is n over its sum.  d_grad_logits: as in bo_logprobs_backward. */

@@ -783,6 +783,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_route_grad(const RouteGradArgs 
     const uint8_t* row = P.x + t * P.ld;
     uint8_t* out = P.dx + t * P.ld_dx;
     if (step <= n) fetch();
+    if ((uint32_t)mine >= E) mine = -1;   // (the caller may have written there)
     const float xm = mine >= 0 ? element<F32>(row, (uint32_t)mine) : 0.f;
     const bool use = __shfl_sync(kAll, mine, q * G) >= 0;
     const float max = lanes.max(x.max());

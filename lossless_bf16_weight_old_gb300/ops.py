@@ -763,8 +763,8 @@ class ExpertRouting(_Results):
     def backward(self, logits: torch.Tensor, d_weights: torch.Tensor | None,
                  d_loss: float | torch.Tensor = 0.0, out: torch.Tensor | None = None, *,
                  counts: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-        """The gradient of the last run's logits (the same ones, or their first rows) from those of
-        its weights (float32[n, k], or None) and of its balance loss (a number or a float32[1]
+        """The gradient of the last run's logits (the same ones, or their first rows; `experts` and `real`
+        as it left them) from those of its weights (float32[n, k], or None) and of its balance loss (a number or a float32[1]
         device tensor).  counts (int32[experts]): the experts' counts to take for the balance loss in
         place of the run's, as of several batches together.  Goes to `out`, which may be the logits
         themselves, or to memory of its own; returns it.  Tensors that autograd records are refused: it

@@ -99,8 +99,8 @@ __device__ __forceinline__ void st32(void* p, const uint32_t (&w)[8]) {
 }
 // (x - max) / T for any of them, as two products: (x - max) 2^n by one fused operation, and with 1 / (T 2^n).
 // The power keeps both in FP32's range: T may be so small that 1 / T is not, or a difference so large that it
-// is not by itself.  (A small T needs none where max is 2^60 or more: there x is max, or so far below it that
-// the product with FP32's greatest number is far enough.)
+// is not by itself.  (A small T gets none where max is 2^60 or more, and a 1 / T of 1e38 at most, whose product
+// with log2 e is finite: there x is max, or 2^37 and more below it.)
 struct OverT {
   float pow, from, inv;
   __device__ __forceinline__ OverT(float p, float f, float i) : pow(p), from(f), inv(i) {}
@@ -108,7 +108,7 @@ struct OverT {
     pow = t > 0x1p64f ? 0x1p-64f : t < 0x1p-64f && fabsf(max) < 0x1p60f ? 0x1p64f : 1.f;
     from = max * pow;
     inv = 1.f / (t * pow);
-    if (inv > FLT_MAX) inv = FLT_MAX;
+    if (inv > 1e38f) inv = 1e38f;
   }
   __device__ __forceinline__ float far(float x) const { return fmaf(x, pow, -from); }
   __device__ __forceinline__ float operator()(float x) const { return far(x) * inv; }
@@ -300,8 +300,8 @@ __device__ __forceinline__ void add_window(Sums<ENT>& a, const uint32_t (&lo)[8]
 }
 
 // The sums of a whole row for any values and temperatures: d = (x - max) / T log2 e with the row's own maximum
-// (OverT), kept above -200, where e is 0, so that e d is 0 and not NaN.  The maximum is taken as the lowest finite number at least: a row of -infinity has the sum 0.  For a
-// block; every thread of warp 0 has the result.
+// (OverT), kept above -200, where e is 0, so that e d is 0 and not NaN.  The maximum is taken as the lowest
+// finite number at least: a row of -infinity has the sum 0.  For a block; every thread of warp 0 has the result.
 template <uint32_t TH, bool F32>
 __device__ __noinline__ Joined careful_sums(const Windows<F32>& W, float max, float temp, Joined* parts) {
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -720,11 +720,11 @@ struct RowGrad {
 // would be infinite where it is 0.
 struct CarefulGrad {
   const RowGrad& R;
-  OverT by;
-  __device__ __forceinline__ CarefulGrad(const RowGrad& r, float temp) : R(r), by(r.shift, temp) {}
+  OverT by, end;
+  __device__ __forceinline__ CarefulGrad(const RowGrad& r, float temp) : R(r), by(r.shift, temp), end(0.f, temp) {}
   __device__ __forceinline__ float operator()(float x, bool given) const {
     const float d = max_nan(by.far(x) * (by.inv * kLog2e), -200.f);
-    return (ex2(d) * fmaf(R.B, d, R.A) + (given ? R.at : 0.f)) * by.inv * by.pow;
+    return (ex2(d) * fmaf(R.B, d, R.A) + (given ? R.at : 0.f)) * end.inv * end.pow;
   }
 };
 template <bool F32, bool PLAIN>

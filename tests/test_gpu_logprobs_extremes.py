@@ -73,3 +73,29 @@ def test_differences_past_the_range(dtype, vocab, heat):
         _check_gradient(lp.backward(x, g), r, tokens, heat, g, None, dtype, least)
         if entropy:
             _check_gradient(lp.backward(x, g, h), r, tokens, heat, g, h, dtype, least)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("vocab", [4, 1003, 40000])
+@pytest.mark.parametrize("heat", [1e-5, 1e-18, 1e-25, 1e-37, 4e-39, 2e-39, 1e-40, 2.0 ** -149])
+def test_large_logits_at_low_temperatures(dtype, vocab, heat):
+    """Maxima so large that their next neighbours are infinitely far below them."""
+    heat = _number(heat)
+    rows = 8
+    x = torch.zeros(rows, vocab, device="cuda")
+    for i, most in enumerate((1e20, -1e20, 2.0 ** 60, 2.0 ** 59, 1e38, -3e38, torch.finfo(dtype).max, -1e10)):
+        x[i] = most - abs(most) / 64 if i != 6 else -most
+        x[i, 1] = x[i, vocab - 1] = most
+    x[1, 0] = x[5, 0] = -float("inf")
+    x = x.to(dtype)
+    tokens = torch.tensor([1, 1, 0, 1, 2, 1, 1, 1], device="cuda")
+    g, h = torch.randn(rows, device="cuda"), torch.randn(rows, device="cuda")
+    small = min(1.0, heat * 1e35)
+    for entropy in (True, False):
+        lp = bd.TokenLogprobs(rows, vocab, top=3, entropy=entropy)
+        lp.run(x, tokens, heat)
+        r = _check(lp, x, tokens, heat, entropy)
+        for of in (1.0, small):
+            _check_gradient(lp.backward(x, g * of), r, tokens, heat, g * of, None, dtype, 2.0 ** -148)
+            if entropy:
+                _check_gradient(lp.backward(x, g * of, h * of), r, tokens, heat, g * of, h * of, dtype, 2.0 ** -148)
